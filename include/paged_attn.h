@@ -250,8 +250,9 @@ pa_status pa_verify_fp8(void* out, const void* q, const void* k_cache, const voi
                         float scale, int partition_size, void* workspace,
                         size_t workspace_bytes, pa_stream_t stream);
 
-/* KV page formats for pa_attention. */
-enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 };
+/* KV page formats.  pa_attention and the graph runner take the first two; 4-bit pages
+ * have pa_attention_int4, and pa_accumulate_weights and pa_evict_tokens take all three. */
+enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT4 = 2 };
 
 /*
  * pa_attention — the general per-sequence call; pa_decode, pa_verify,
@@ -322,6 +323,168 @@ pa_status pa_decode_append(void* out, const void* q, const void* new_key, const 
                            int num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
                            int block_size, float scale, int partition_size, void* workspace,
                            size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * INT4 pages — the cache at 4.25 bits a value: a quarter of what decode loads from bf16
+ * pages ("ranksignal" post, Quantifier : des nombres plus petits, carried one step on
+ * from FP8).  Codes are 4-bit integers with one E4M3 scale for every 32 head dims
+ * of a token, and, as for FP8 pages, one float32 scale per kv head that the
+ * caller chooses (k_scale, v_scale: device float32 [num_kv_heads]):
+ *   value = (code - 8) * e4m3_value(scale) * head_scale
+ * Layout (uint8; each (block, kv head) page contiguous, K and V pages alike, separate
+ * pools [num_blocks, num_kv_heads, page], page = 16 * (head_dim/2 + head_dim/32) bytes):
+ *   codes   [16 tokens][head_dim / 2]    dim d in byte d/2, even d in the low nibble
+ *   scales  [16 tokens][head_dim / 32]   E4M3, one for dims 32 i .. 32 i + 31
+ * A written token's scale is e4m3(max|x| / (7 head_scale)) over the 32 dims (the product
+ * 7 head_scale and the quotient in IEEE float32; nearest, ties to even, saturating at
+ * 448), its codes are the integers nearest to x / (scale * head_scale), ties to
+ * even, limited to -7 .. 7, plus 8.  Code 0 is never written.  E4M3 scales span 17
+ * octaves, so a head scale need only be of the order of the head's largest
+ * magnitude / 1000 (between its largest magnitude / 3136, below which values saturate,
+ * and a few thousandths of it); it lies in [2^-100, 2^100].  A NaN makes its 32 dims
+ * NaN; infinities saturate.
+ */
+
+/*
+ * pa_reshape_and_cache_int4 — pa_reshape_and_cache into INT4 pages.  key / value are
+ * bf16 [num_tokens, num_kv_heads, head_dim].  head_dim 64 or 128; otherwise
+ * requirements and errors as pa_reshape_and_cache, plus k_scale and v_scale non-NULL.
+ * Two tokens naming the same slot leave its contents unspecified.
+ */
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, void* k_cache,
+                                    void* v_cache, const int64_t* slot_mapping,
+                                    const float* k_scale, const float* v_scale, int num_tokens,
+                                    int num_blocks, int num_kv_heads, int head_dim,
+                                    int block_size, pa_stream_t stream);
+
+/*
+ * pa_gather_cache_int4 — the reverse: the values held in `num_tokens` slots, rounded to
+ * bf16, into key / value bf16 [num_tokens, num_kv_heads, head_dim] (for a prefill that
+ * attends to cached tokens, or to check what a cache holds).  Rows with a negative slot
+ * are zero; so are rows whose slot lies outside the pool, which sets PA_ERR_BOUNDS on
+ * the device.  Requirements as pa_reshape_and_cache_int4.
+ */
+pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, const void* v_cache,
+                               const int64_t* slot_mapping, const float* k_scale,
+                               const float* v_scale, int num_tokens, int num_blocks,
+                               int num_kv_heads, int head_dim, int block_size,
+                               pa_stream_t stream);
+
+/* Bytes of scratch pa_attention_int4 needs with these sizes (0 if no sequence can need
+ * more than one partition); partition_size 0 = the library default. */
+size_t pa_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                              int num_query_tokens, int max_context_len, int head_dim,
+                              int block_size, int partition_size, int window_size);
+
+/*
+ * pa_attention_int4 — pa_attention over INT4 pages: 1 to 64 query rows per kv head (T
+ * query tokens times the GQA group), an optional sliding window, and optionally the
+ * query tokens' K/V (new_key / new_value, both or neither) quantised as
+ * pa_reshape_and_cache_int4 does and stored at positions context_lens[b] - T .. - 1
+ * before they are read.  k_cache / v_cache are written only then.
+ *
+ * The products run on f16 operands with fp32 accumulation: query rows are scaled by a
+ * power of two (any bf16 magnitude is taken), softmax weights are rounded to f16,
+ * multiplied by the E4M3 scales and rounded to f16 again, and the codes are exact.
+ * Workspace as pa_decode, sized by pa_int4_workspace_size; with partition_size = 0 and
+ * workspace == NULL every sequence is processed whole.  Other arguments,
+ * requirements and errors as pa_attention.
+ */
+pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const void* new_value,
+                            void* k_cache, void* v_cache, const float* k_scale,
+                            const float* v_scale, int window_size, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* context_lens,
+                            int max_context_len, int num_seqs, int num_query_tokens,
+                            int num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, float scale, int partition_size, void* workspace,
+                            size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * Bounded caches — attention sums to one over the context, and over many steps a few
+ * entries collect most of it.  pa_accumulate_weights keeps, for every cache entry, the
+ * running sum of the attention weights it received; pa_evict_tokens drops the
+ * entries with the smallest sums and closes the gaps, so that a sequence decodes
+ * in a fixed number of blocks.  Each kv head chooses its own entries; all heads keep
+ * the same number.  The pages that eviction rewrites must belong to one sequence only
+ * (reference count 1, see pa_bm_ref_count): a block shared copy-on-write is copied first.
+ *
+ *   weights    [num_seqs, num_kv_heads, max_entries] float32   sum of entry j
+ *   positions  [num_seqs, num_kv_heads, max_entries] int32     position in its sequence
+ *              of the token that entry j holds (which entries are the newest)
+ * Row b belongs to the sequence in row b of block_tables; entry j is cache position
+ * j.  The caller starts them at zero and 0, 1, 2, ... for a prompt.
+ *
+ * After an eviction the entries of a sequence are no longer in token order (the
+ * newest tokens are appended behind them as before): a sliding window over such a cache
+ * has no meaning.
+ */
+
+/* Bytes of scratch pa_accumulate_weights needs (0 for sizes it does not take). */
+size_t pa_accumulate_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                    int num_query_tokens, int max_context_len);
+
+/*
+ * pa_accumulate_weights — after an attention call, add its softmax weights: with
+ * L = context_lens[b], T = num_query_tokens and p the softmax weights (scale
+ * q . K_j, query token t seeing entries j <= L - T + t) of the T query tokens and
+ * the query heads h of kv head g,
+ *   weights_out[b, g, j] = decay * weights[b, g, j] + sum_{t, h} p[t, h, j]    j < L - T
+ *   weights_out[b, g, j] = sum_{t, h} p[t, h, j]                       L - T <= j < L
+ *   positions[b, g, j]   = seq_lens[b] - L + j                         L - T <= j < L
+ * The T newest entries start afresh whatever the arrays held; entries from L on are
+ * left as they were.  weights_out may be weights itself, and otherwise does not overlap
+ * it.  positions may be NULL (not written); seq_lens[b], the number of tokens the
+ * sequence has seen (NULL: L, nothing evicted so far), gives them.  Only K pages are
+ * read: kv_format PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_INT4, k_scale ignored for bf16.
+ * q is bf16 [num_seqs, T, num_q_heads, head_dim].
+ * Requirements: head_dim 64 or 128, block_size 16, num_q_heads a multiple of
+ * num_kv_heads, (num_q_heads/num_kv_heads) * T <= 64, num_seqs * num_kv_heads <= 65535,
+ * max_context_len <= max_entries and <= max_blocks_per_seq * 16, q / k_cache 16-byte
+ * aligned, a 256-byte aligned workspace of pa_accumulate_workspace_size bytes (calls in
+ * flight at once do not share it; its contents carry nothing from call to call).
+ * A context length above max_context_len or below T, or a block id outside
+ * the pool, sets PA_ERR_BOUNDS on the device; the sequence, or the block's
+ * entries, are skipped.  The result does not depend on scheduling.
+ */
+pa_status pa_accumulate_weights(const float* weights, float* weights_out, int32_t* positions,
+                                int max_entries, const void* q, const void* k_cache,
+                                const float* k_scale, int kv_format, const int32_t* block_tables,
+                                int max_blocks_per_seq, const int32_t* context_lens,
+                                const int32_t* seq_lens, int max_context_len, int num_seqs,
+                                int num_query_tokens, int num_blocks, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, float scale,
+                                float decay, void* workspace, size_t workspace_bytes,
+                                pa_stream_t stream);
+
+/* Bytes of scratch pa_evict_tokens needs. */
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len, int budget);
+
+/*
+ * pa_evict_tokens — cut every sequence with more than `budget` entries down to it.  Of
+ * the L = context_lens[b] entries of (sequence b, kv head g) those stay that come
+ * first in this order: the newest (position > the largest position - num_recent) before
+ * the others, then the larger weight (NaN below every number), then the lower
+ * index.  The entries that stay and lie below `budget` do not move; the i-th entry
+ * that stays and lies at or above it moves, with its K and V rows, weight and
+ * position, into the i-th gap below it.  new_lens[b] = min(L, budget); entries from
+ * there on are left as they were.  context_lens is not written (new_lens must not
+ * overlap it); the host passes min(L, budget) to pa_bm_truncate and both carry on with
+ * the new length.
+ * Requirements: 1 <= budget, 0 <= num_recent <= budget, head_dim 64 or 128, block_size
+ * 16, num_seqs * num_kv_heads <= 65535, max_context_len <= max_entries and <=
+ * max_blocks_per_seq * 16, pools 16-byte aligned, a 256-byte aligned workspace of
+ * pa_evict_workspace_size bytes (calls in flight at once do not share it).  Pools by
+ * kv_format as for pa_attention / pa_attention_int4.  A context length outside
+ * 0 .. max_context_len, or a block id outside the pool among the sequence's blocks, sets
+ * PA_ERR_BOUNDS on the device and leaves that sequence as it is (new_lens[b] = L).
+ */
+pa_status pa_evict_tokens(int32_t* new_lens, void* k_cache, void* v_cache, int kv_format,
+                          const int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* context_lens, int max_context_len, float* weights,
+                          int32_t* positions, int max_entries, int budget, int num_recent,
+                          int num_seqs, int num_blocks, int num_kv_heads, int head_dim,
+                          int block_size, void* workspace, size_t workspace_bytes,
+                          pa_stream_t stream);
 
 /*
  * pa_decode_shared_prefix — pa_decode for batches where groups of sequences
@@ -573,6 +736,11 @@ pa_status pa_bm_fork(pa_block_manager* bm, int parent_id, int child_id);
  * manager unchanged. */
 pa_status pa_bm_append_slot(pa_block_manager* bm, int seq_id, int64_t* slot, int32_t* copy_src,
                             int32_t* copy_dst);
+
+/* Shorten a sequence to its first num_tokens tokens (after pa_evict_tokens, or to take
+ * back rejected drafts): the blocks behind them are dropped as by
+ * pa_bm_free_sequence.  PA_ERR_INVALID_ARG if it is unknown or holds fewer tokens. */
+pa_status pa_bm_truncate(pa_block_manager* bm, int seq_id, int num_tokens);
 
 /* Drop a sequence; blocks whose reference count reaches 0 become free. */
 pa_status pa_bm_free_sequence(pa_block_manager* bm, int seq_id);

@@ -20,6 +20,17 @@ FP8 (E4M3) pages (``reshape_and_cache_fp8``, ``decode_fp8``, ``verify_fp8``):
     v_cache       [num_blocks, num_kv_heads, head_dim, block_size] uint8 codes
     k_scale,
     v_scale       [num_kv_heads] float32 (value = code value * scale)
+
+INT4 pages (``reshape_and_cache_int4``, ``gather_cache_int4``, ``attention_int4``):
+    k_cache,
+    v_cache       [num_blocks, num_kv_heads, int4_page_bytes(head_dim)] uint8: 16 rows of
+                  head_dim/2 code bytes, then 16 rows of head_dim/32 E4M3 scales
+    k_scale,
+    v_scale       [num_kv_heads] float32 (value = (code - 8) * scale * head scale)
+
+Bounded caches (``accumulate_weights``, ``evict_tokens``; bf16, FP8 and INT4 pages):
+    weights       [num_seqs, num_kv_heads, max_entries] float32
+    positions     [num_seqs, num_kv_heads, max_entries] int32
 """
 from __future__ import annotations
 
@@ -36,7 +47,10 @@ from ._lib import PagedAttnError, STATUS_NAMES
 __all__ = ["reshape_and_cache", "decode", "verify", "decode_shared_prefix", "workspace_size",
            "default_partition_size", "get_device_error", "selftest_wait_timeout", "library",
            "copy_blocks", "BlockManager", "reshape_and_cache_fp8", "decode_fp8", "verify_fp8",
-           "attention", "spec_accept", "GraphRunner",
+           "attention", "spec_accept", "GraphRunner", "reshape_and_cache_int4",
+           "gather_cache_int4", "attention_int4", "int4_workspace_size", "int4_page_bytes",
+           "accumulate_weights", "accumulate_workspace_size", "evict_tokens",
+           "evict_workspace_size",
            "PagedAttnError", "STATUS_NAMES"]
 
 
@@ -409,6 +423,283 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     return o4.squeeze(1) if squeeze else o4
 
 
+def int4_page_bytes(head_dim: int) -> int:
+    """Bytes of one INT4 page (16 tokens of one kv head)."""
+    return 16 * (head_dim // 2 + head_dim // 32)
+
+
+_KV_BF16, _KV_FP8, _KV_INT4 = 0, 1, 2
+
+
+def _int4_pools(k_cache, v_cache, k_scale, v_scale):
+    _need("k_cache", k_cache, torch.uint8, 3)
+    dev = k_cache.device
+    _need("v_cache", v_cache, torch.uint8, 3, dev)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("inconsistent shapes")
+    NB, Hkv, page = k_cache.shape
+    D = {int4_page_bytes(d): d for d in (64, 128)}.get(page)
+    if D is None:
+        raise ValueError("INT4 pools are [num_blocks, num_kv_heads, int4_page_bytes(head_dim)] "
+                         f"with head_dim 64 or 128, got pages of {page} bytes")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(name, t, torch.float32, 1, dev)
+        if t.shape[0] != Hkv:
+            raise ValueError(f"{name} must have num_kv_heads entries")
+    return dev, NB, Hkv, D
+
+
+def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                           k_scale: torch.Tensor, v_scale: torch.Tensor) -> None:
+    """Quantise new bf16 K/V rows [N, Hkv, D] into INT4 pages at their slots (negative slots
+    are skipped)."""
+    dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
+    _need("key", key, torch.bfloat16, 3, dev)
+    _need("value", value, torch.bfloat16, 3, dev)
+    _need("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    N = key.shape[0]
+    if key.shape != (N, Hkv, D) or value.shape != key.shape or slot_mapping.shape[0] != N:
+        raise ValueError("inconsistent shapes")
+    with torch.cuda.device(dev):
+        st = library().pa_reshape_and_cache_int4(_vp(key), _vp(value), _vp(k_cache), _vp(v_cache),
+                                                 _vp(slot_mapping), _vp(k_scale), _vp(v_scale), N,
+                                                 NB, Hkv, D, 16, _stream(dev))
+    _lib.check("pa_reshape_and_cache_int4", st)
+
+
+def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                      k_scale: torch.Tensor, v_scale: torch.Tensor):
+    """The values held in INT4 slots as bf16: (key, value), each [N, Hkv, D]; rows with a
+    negative slot are zero."""
+    dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
+    _need("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    N = slot_mapping.shape[0]
+    key = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=dev)
+    value = torch.empty_like(key)
+    with torch.cuda.device(dev):
+        st = library().pa_gather_cache_int4(_vp(key), _vp(value), _vp(k_cache), _vp(v_cache),
+                                            _vp(slot_mapping), _vp(k_scale), _vp(v_scale), N, NB,
+                                            Hkv, D, 16, _stream(dev))
+    _lib.check("pa_gather_cache_int4", st)
+    return key, value
+
+
+def int4_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                        num_query_tokens: int, max_context_len: int, head_dim: int,
+                        partition_size: int = 0, window_size: int = 0) -> int:
+    """Scratch bytes ``attention_int4`` needs with these sizes (0 if none)."""
+    return int(library().pa_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                num_query_tokens, max_context_len, head_dim, 16,
+                                                partition_size, window_size))
+
+
+def _max_len(max_context_len, context_lens, least):
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if context_lens.numel() else least
+    return int(max_context_len)
+
+
+def attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                   context_lens: torch.Tensor, max_context_len: Optional[int] = None,
+                   scale: Optional[float] = None, partition_size: int = 0,
+                   workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   new_key: Optional[torch.Tensor] = None,
+                   new_value: Optional[torch.Tensor] = None,
+                   window_size: int = 0) -> torch.Tensor:
+    """Attention over INT4 pages: q [B, T, Hq, D] or, for one query token, [B, Hq, D] (out has
+    q's shape).
+
+    With ``new_key`` / ``new_value`` ([B*T, Hkv, D] or [B, T, Hkv, D] bf16) the query tokens'
+    K/V are quantised and stored at positions L-T .. L-1 first; ``window_size`` > 0 limits each
+    query token to its last ``window_size`` positions.
+    """
+    squeeze = isinstance(q, torch.Tensor) and q.dim() == 3
+    q4 = q.unsqueeze(1) if squeeze else q
+    o4 = out.unsqueeze(1) if squeeze and out is not None else out
+    dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
+    _need("q", q4, torch.bfloat16, 4, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("context_lens", context_lens, torch.int32, 1, dev)
+    B, T, Hq, Dq = q4.shape
+    if Dq != D or block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("inconsistent shapes")
+    mcl = _max_len(max_context_len, context_lens, T)
+    if o4 is None:
+        o4 = torch.empty_like(q4)
+    else:
+        _need("out", o4, torch.bfloat16, 4, dev)
+        if o4.shape != q4.shape:
+            raise ValueError("out must have q's shape")
+    if (new_key is None) != (new_value is None):
+        raise ValueError("new_key and new_value go together")
+    if new_key is not None:
+        for name, t in (("new_key", new_key), ("new_value", new_value)):
+            _need(name, t, torch.bfloat16, t.dim(), dev)
+            if t.numel() != B * T * Hkv * D:
+                raise ValueError(f"{name} must hold [B, T, Hkv, D] values")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    need = int4_workspace_size(B, Hq, Hkv, T, mcl, D, partition_size, window_size) if B else 0
+    ws, wsb = _workspace(dev, workspace, need)
+    with torch.cuda.device(dev):
+        st = library().pa_attention_int4(
+            _vp(o4), _vp(q4), _vp(new_key), _vp(new_value), _vp(k_cache), _vp(v_cache),
+            _vp(k_scale), _vp(v_scale), int(window_size), _vp(block_tables),
+            block_tables.shape[1], _vp(context_lens), mcl, B, T, NB, Hq, Hkv, D, 16, scale,
+            partition_size, _vp(ws), wsb, _stream(dev))
+    _lib.check("pa_attention_int4", st)
+    return o4.squeeze(1) if squeeze else o4
+
+
+def _stat(name, t, dtype, dev, B, Hkv, mcl):
+    _need(name, t, dtype, 3, dev)
+    if tuple(t.shape[:2]) != (B, Hkv) or t.shape[2] < mcl:
+        raise ValueError(f"{name} must be [num_seqs, num_kv_heads, max_entries >= "
+                         f"max_context_len], got {tuple(t.shape)}")
+
+
+def accumulate_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                              num_query_tokens: int, max_context_len: int) -> int:
+    """Scratch bytes ``accumulate_weights`` needs with these sizes."""
+    return int(library().pa_accumulate_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                      num_query_tokens, max_context_len))
+
+
+def accumulate_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, weights: torch.Tensor,
+                       positions: Optional[torch.Tensor] = None,
+                       seq_lens: Optional[torch.Tensor] = None,
+                       max_context_len: Optional[int] = None, scale: Optional[float] = None,
+                       decay: float = 1.0, k_scale: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Add the softmax weights of q [B, T, Hq, D] (or [B, Hq, D]) to each cache entry's sum.
+
+    ``weights`` [B, Hkv, max_entries] float32 becomes ``decay * weights`` plus the weights
+    each entry receives, in place or in ``out``; the T newest entries start afresh, and their
+    ``positions`` are set from ``seq_lens`` (tokens seen by each sequence; default
+    ``context_lens``).  The K pool may hold bf16, FP8 (with ``k_scale``) or INT4 pages (3-dim,
+    with ``k_scale``)."""
+    squeeze = isinstance(q, torch.Tensor) and q.dim() == 3
+    q4 = q.unsqueeze(1) if squeeze else q
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    if k_cache.dtype == torch.bfloat16:
+        fmt = _KV_BF16
+        _need("k_cache", k_cache, torch.bfloat16, 4)
+    elif k_cache.dim() == 3:
+        fmt = _KV_INT4
+        _need("k_cache", k_cache, torch.uint8, 3)
+    else:
+        fmt = _KV_FP8
+        _need("k_cache", k_cache, torch.uint8, 4)
+    dev = k_cache.device
+    NB, Hkv = k_cache.shape[:2]
+    _need("q", q4, torch.bfloat16, 4, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("context_lens", context_lens, torch.int32, 1, dev)
+    B, T, Hq, D = q4.shape
+    page = (NB, Hkv, int4_page_bytes(D)) if fmt == _KV_INT4 else (NB, Hkv, 16, D)
+    if tuple(k_cache.shape) != page or block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("inconsistent shapes")
+    if fmt == _KV_BF16:
+        if k_scale is not None:
+            raise ValueError("bf16 pages take no k_scale")
+    else:
+        _need("k_scale", k_scale, torch.float32, 1, dev)
+        if k_scale.shape[0] != Hkv:
+            raise ValueError("k_scale must have num_kv_heads entries")
+    mcl = _max_len(max_context_len, context_lens, T)
+    _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
+    if out is None:
+        out = weights
+    else:
+        _stat("out", out, torch.float32, dev, B, Hkv, mcl)
+        if out.shape != weights.shape:
+            raise ValueError("out must have the shape of weights")
+    if positions is not None:
+        _stat("positions", positions, torch.int32, dev, B, Hkv, mcl)
+        if positions.shape != weights.shape:
+            raise ValueError("positions must have the shape of weights")
+    if seq_lens is not None:
+        _need("seq_lens", seq_lens, torch.int32, 1, dev)
+        if seq_lens.shape[0] != B:
+            raise ValueError("inconsistent shapes")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    need = accumulate_workspace_size(B, Hq, Hkv, T, mcl) if B else 0
+    ws, wsb = _workspace(dev, workspace, need)
+    with torch.cuda.device(dev):
+        st = library().pa_accumulate_weights(
+            _vp(weights), _vp(out), _vp(positions), weights.shape[2], _vp(q4), _vp(k_cache),
+            _vp(k_scale), fmt, _vp(block_tables), block_tables.shape[1], _vp(context_lens),
+            _vp(seq_lens), mcl, B, T, NB, Hq, Hkv, D, 16, scale, float(decay), _vp(ws), wsb,
+            _stream(dev))
+    _lib.check("pa_accumulate_weights", st)
+    return out
+
+
+def evict_workspace_size(num_seqs: int, num_kv_heads: int, max_context_len: int,
+                         budget: int) -> int:
+    """Scratch bytes ``evict_tokens`` needs with these sizes."""
+    return int(library().pa_evict_workspace_size(num_seqs, num_kv_heads, max_context_len, budget))
+
+
+def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, weights: torch.Tensor, positions: torch.Tensor,
+                 budget: int, num_recent: int, max_context_len: Optional[int] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Cut every sequence with more than ``budget`` entries down to it, in place.
+
+    Of each (sequence, kv head) the ``num_recent`` newest entries stay, and of the others
+    those with the largest ``weights`` (ties: the lowest index); kept entries from ``budget``
+    on move into the gaps below it, with their ``weights`` and ``positions``.  Returns the new
+    context lengths (int32 [B], min(L, budget)).  Pools: bf16, FP8 or INT4 pages, owned by
+    these sequences alone (no shared copy-on-write blocks)."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    if k_cache.dtype == torch.bfloat16:
+        fmt = _KV_BF16
+        _need("k_cache", k_cache, torch.bfloat16, 4)
+    elif k_cache.dim() == 3:
+        fmt = _KV_INT4
+        _need("k_cache", k_cache, torch.uint8, 3)
+    else:
+        fmt = _KV_FP8
+        _need("k_cache", k_cache, torch.uint8, 4)
+    dev = k_cache.device
+    _need("v_cache", v_cache, k_cache.dtype, k_cache.dim(), dev)
+    NB, Hkv = k_cache.shape[:2]
+    if fmt == _KV_INT4:
+        BS, D = 16, {int4_page_bytes(d): d for d in (64, 128)}.get(k_cache.shape[2], 0)
+        good = D > 0 and v_cache.shape == k_cache.shape
+    else:
+        BS, D = k_cache.shape[2:]
+        good = tuple(v_cache.shape) == ((NB, Hkv, D, BS) if fmt == _KV_FP8 else
+                                        (NB, Hkv, BS, D))
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("context_lens", context_lens, torch.int32, 1, dev)
+    B = context_lens.shape[0]
+    if not good or block_tables.shape[0] != B:
+        raise ValueError("inconsistent shapes")
+    mcl = max(1, _max_len(max_context_len, context_lens, 1))
+    _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
+    _stat("positions", positions, torch.int32, dev, B, Hkv, mcl)
+    if positions.shape != weights.shape:
+        raise ValueError("positions must have the shape of weights")
+    new_lens = torch.empty_like(context_lens)
+    need = evict_workspace_size(B, Hkv, mcl, budget) if B else 0
+    ws, wsb = _workspace(dev, workspace, need)
+    with torch.cuda.device(dev):
+        st = library().pa_evict_tokens(
+            _vp(new_lens), _vp(k_cache), _vp(v_cache), fmt, _vp(block_tables),
+            block_tables.shape[1], _vp(context_lens), mcl, _vp(weights), _vp(positions),
+            weights.shape[2], int(budget), int(num_recent), B, NB, Hkv, D, BS, _vp(ws), wsb,
+            _stream(dev))
+    _lib.check("pa_evict_tokens", st)
+    return new_lens
+
+
 def get_device_error(device=None) -> int:
     """Synchronise the current stream and return (and clear) the device error status."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else \
@@ -650,6 +941,11 @@ class BlockManager:
         _lib.check("pa_bm_append_slot", self._lib.pa_bm_append_slot(
             self._h, seq_id, ctypes.byref(slot), ctypes.byref(src), ctypes.byref(dst)))
         return slot.value, (None if src.value < 0 else (src.value, dst.value))
+
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """Shorten a sequence to its first ``num_tokens`` tokens and drop the blocks behind them
+        (after ``evict_tokens``, or to take back rejected drafts)."""
+        _lib.check("pa_bm_truncate", self._lib.pa_bm_truncate(self._h, seq_id, num_tokens))
 
     def free_sequence(self, seq_id: int) -> None:
         _lib.check("pa_bm_free_sequence", self._lib.pa_bm_free_sequence(self._h, seq_id))

@@ -73,6 +73,19 @@ SIGNATURES = {
                           _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "pa_decode_append_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i,
                                   _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "pa_reshape_and_cache_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                       _vp]),
+    "pa_gather_cache_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "pa_int4_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "pa_attention_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i,
+                               _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "pa_accumulate_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "pa_accumulate_weights": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i,
+                                   _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _sz, _vp]),
+    "pa_evict_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "pa_evict_tokens": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
+                             _i, _i, _i, _vp, _sz, _vp]),
+    "pa_bm_truncate": (_i, [_vp, _i, _i]),
     "pa_bm_create": (_i, [_i, _i, ctypes.POINTER(_vp)]),
     "pa_bm_destroy": (None, [_vp]),
     "pa_bm_add_sequence": (_i, [_vp, _i, _i]),

@@ -366,6 +366,64 @@ pa_status run_attention(const AttnArgs& a) {
   return PA_OK;
 }
 
+// ---------------------------------------------------------------- 4-bit pages
+bool int4_geometry(int head_dim, int block_size) {
+  return (head_dim == 64 || head_dim == 128) && block_size == kBlockSize;
+}
+
+// One thread per 8 dims, 256 a CTA: the grid's x extent.
+bool int4_store_fits(long long tokens, int hkv, int head_dim) {
+  return tokens * hkv * (head_dim / 8) < (1ll << 31) * 256;
+}
+
+// Entries a sequence's query tokens can see, rounded up to where blocks begin.
+int int4_span(int max_context_len, int T, int window) {
+  if (window == 0) return max_context_len;
+  return static_cast<int>(std::min<long long>(
+      max_context_len, (static_cast<long long>(window) + T - 1 + 2 * kBlockSize - 1) /
+                           kBlockSize * kBlockSize));
+}
+
+int int4_partition_tokens(int span, int num_seqs, int num_kv_heads) {
+  return default_partition_tokens(span, num_seqs, num_kv_heads, true);
+}
+
+// ---------------------------------------------------------------- accumulated weights
+// Scratch: [(m, l) per chunk and row][scores], 256-byte aligned.
+struct ObservePlan {
+  int ppb, max_chunks, row_stride;
+  size_t off_scores, bytes;
+};
+
+ObservePlan observe_plan(int num_seqs, int hq, int hkv, int T, int max_ctx) {
+  ObservePlan pl;
+  const int rows = hq / hkv * T;
+  const int max_blocks = ceil_div(max_ctx, kBlockSize);
+  pl.ppb = 64;
+  pl.max_chunks = ceil_div(max_blocks, pl.ppb);
+  pl.row_stride = (rows + 1) & ~1;
+  const size_t pairs = static_cast<size_t>(num_seqs) * hkv;
+  pl.off_scores = round256(pairs * pl.max_chunks * rows * 8);
+  pl.bytes = pl.off_scores + round256(pairs * max_ctx * pl.row_stride * 4);
+  return pl;
+}
+
+// ---------------------------------------------------------------- eviction
+// Scratch: [move counts][moves], 256-byte aligned.
+struct EvictPlan {
+  int max_moves;
+  size_t off_moves, bytes;
+};
+
+EvictPlan evict_plan(int num_seqs, int hkv, int max_ctx, int budget) {
+  EvictPlan pl;
+  pl.max_moves = std::max(1, std::min(budget, max_ctx - budget));
+  const size_t pairs = static_cast<size_t>(num_seqs) * hkv;
+  pl.off_moves = round256(pairs * 4);
+  pl.bytes = pl.off_moves + round256(pairs * pl.max_moves * 8);
+  return pl;
+}
+
 }  // namespace
 
 namespace pa {
@@ -652,6 +710,285 @@ pa_status pa_decode_shared_prefix_fp8(
   return run_attention(a);
 }
 
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, void* k_cache,
+                                    void* v_cache, const int64_t* slot_mapping,
+                                    const float* k_scale, const float* v_scale, int num_tokens,
+                                    int num_blocks, int num_kv_heads, int head_dim,
+                                    int block_size, pa_stream_t stream) {
+  if (num_tokens < 0 || num_blocks < 1 || num_kv_heads < 1) return PA_ERR_INVALID_ARG;
+  if (!int4_geometry(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  if (!int4_store_fits(num_tokens, num_kv_heads, head_dim)) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping || !k_scale || !v_scale)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID_ARG;
+  return launch_store_int4(key, value, k_cache, v_cache, slot_mapping, nullptr, nullptr, 1, 0, 0,
+                           k_scale, v_scale, num_tokens, num_blocks, num_kv_heads, head_dim,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, const void* v_cache,
+                               const int64_t* slot_mapping, const float* k_scale,
+                               const float* v_scale, int num_tokens, int num_blocks,
+                               int num_kv_heads, int head_dim, int block_size,
+                               pa_stream_t stream) {
+  if (num_tokens < 0 || num_blocks < 1 || num_kv_heads < 1) return PA_ERR_INVALID_ARG;
+  if (!int4_geometry(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  if (!int4_store_fits(num_tokens, num_kv_heads, head_dim)) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping || !k_scale || !v_scale)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID_ARG;
+  return launch_gather_int4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                            num_tokens, num_blocks, num_kv_heads, head_dim,
+                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+size_t pa_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                              int num_query_tokens, int max_context_len, int head_dim,
+                              int block_size, int partition_size, int window_size) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_query_tokens <= 0 ||
+      max_context_len <= 0 || head_dim <= 0 || block_size != kBlockSize || partition_size < 0 ||
+      window_size < 0)
+    return 0;
+  const int span = int4_span(max_context_len, num_query_tokens, window_size);
+  const int psize = partition_size > 0 ? partition_size
+                                       : int4_partition_tokens(span, num_seqs, num_kv_heads);
+  return make_plan(num_seqs, num_q_heads, num_query_tokens, span, head_dim, psize, 0).ws_bytes;
+}
+
+pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const void* new_value,
+                            void* k_cache, void* v_cache, const float* k_scale,
+                            const float* v_scale, int window_size, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* context_lens,
+                            int max_context_len, int num_seqs, int num_query_tokens,
+                            int num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, float scale, int partition_size, void* workspace,
+                            size_t workspace_bytes, pa_stream_t stream) {
+  const int T = num_query_tokens;
+  if (num_seqs < 0 || T < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 1 || partition_size < 0 || window_size < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !k_scale || !v_scale)
+    return PA_ERR_INVALID_ARG;
+  if ((new_key == nullptr) != (new_value == nullptr)) return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(new_key) || !aligned16(new_value))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (!int4_geometry(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  const int G = num_q_heads / num_kv_heads;
+  if (static_cast<long long>(G) * T > kMaxRows) return PA_ERR_UNSUPPORTED;
+  if (max_context_len < T || static_cast<long long>(max_context_len) >
+                                 static_cast<long long>(max_blocks_per_seq) * kBlockSize)
+    return PA_ERR_INVALID_ARG;
+  if (partition_size % kBlockSize != 0) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+
+  // the entries one sequence may read: all of them, or those under its queries' windows
+  const int span = int4_span(max_context_len, T, window_size);
+  int psize = partition_size;
+  if (psize == 0) {
+    psize = int4_partition_tokens(span, num_seqs, num_kv_heads);
+    if (workspace == nullptr) psize = ceil_div(span, kBlockSize) * kBlockSize;   // whole sequences
+  }
+  const Plan plan = make_plan(num_seqs, num_q_heads, T, span, head_dim, psize, 0);
+  if (plan.max_parts > kMaxPartitions) return PA_ERR_UNSUPPORTED;
+  if (plan.ws_bytes > 0) {
+    if (!workspace || workspace_bytes < plan.ws_bytes) return PA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  }
+  const long long units =
+      static_cast<long long>(plan.max_parts) * num_kv_heads * num_seqs;
+  if (units >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (new_key != nullptr &&
+      !int4_store_fits(static_cast<long long>(num_seqs) * T, num_kv_heads, head_dim))
+    return PA_ERR_UNSUPPORTED;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (new_key != nullptr &&
+      launch_store_int4(new_key, new_value, k_cache, v_cache, nullptr, block_tables, context_lens,
+                        T, max_blocks_per_seq, max_context_len, k_scale, v_scale, num_seqs * T,
+                        num_blocks, num_kv_heads, head_dim, s) != cudaSuccess)
+    return PA_ERR_CUDA;
+  AttnParams p{};
+  p.q = q;
+  p.out = out;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.k_pool = k_cache;
+  p.v_pool = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  if (plan.ws_bytes > 0) {
+    char* ws = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+    p.stream_ctl = ws + plan.off_counter + 16;   // the merge leaves it as after any call
+  }
+  p.mbs = max_blocks_per_seq;
+  p.max_ctx = max_context_len;
+  p.num_seqs = num_seqs;
+  p.T = T;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.G = G;
+  p.num_blocks = num_blocks;
+  p.ppb = plan.ppb;
+  p.max_parts = plan.max_parts;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = window_size;
+  p.wcap = window_size > 0 ? static_cast<unsigned>(window_size) : 0x80000000u;
+  p.wspan = window_size > 0 ? window_size : (1 << 30);
+  const int rows = G * T;
+  const unsigned n = static_cast<unsigned>(units);
+  cudaError_t e = head_dim == 64 ? launch_attn4_d64(p, rows, n, s) : launch_attn4_d128(p, rows, n, s);
+  if (e == cudaSuccess && plan.ws_bytes > 0) e = launch_reduce(p, head_dim, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_accumulate_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                    int num_query_tokens, int max_context_len) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_query_tokens <= 0 ||
+      max_context_len <= 0 || num_q_heads % num_kv_heads != 0)
+    return 0;
+  return observe_plan(num_seqs, num_q_heads, num_kv_heads, num_query_tokens, max_context_len).bytes;
+}
+
+pa_status pa_accumulate_weights(const float* weights, float* weights_out, int32_t* positions,
+                                int max_entries, const void* q, const void* k_cache,
+                                const float* k_scale, int kv_format, const int32_t* block_tables,
+                                int max_blocks_per_seq, const int32_t* context_lens,
+                                const int32_t* seq_lens, int max_context_len, int num_seqs,
+                                int num_query_tokens, int num_blocks, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, float scale,
+                                float decay, void* workspace, size_t workspace_bytes,
+                                pa_stream_t stream) {
+  const int T = num_query_tokens;
+  if (num_seqs < 0 || T < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 1 || kv_format < PA_KV_BF16 || kv_format > PA_KV_INT4)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!weights || !weights_out || !q || !k_cache || !block_tables || !context_lens)
+    return PA_ERR_INVALID_ARG;
+  if (kv_format != PA_KV_BF16 && !k_scale) return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache)) return PA_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+  const int G = num_q_heads / num_kv_heads;
+  if (static_cast<long long>(G) * T > kMaxRows) return PA_ERR_UNSUPPORTED;
+  if (max_context_len < T ||
+      static_cast<long long>(max_context_len) >
+          static_cast<long long>(max_blocks_per_seq) * kBlockSize ||
+      max_context_len > max_entries)
+    return PA_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_seqs) * num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const ObservePlan plan = observe_plan(num_seqs, num_q_heads, num_kv_heads, T, max_context_len);
+  if (!workspace || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  const long long units = static_cast<long long>(plan.max_chunks) * num_kv_heads * num_seqs;
+  if (units >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+
+  ObserveParams p{};
+  p.q = q;
+  p.k_pool = k_cache;
+  p.k_scale = k_scale;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.seq_lens = seq_lens;
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.positions = positions;
+  p.ml = static_cast<float2*>(workspace);
+  p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.off_scores);
+  p.mbs = max_blocks_per_seq;
+  p.max_ctx = max_context_len;
+  p.num_seqs = num_seqs;
+  p.T = T;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.G = G;
+  p.num_blocks = num_blocks;
+  p.ppb = plan.ppb;
+  p.max_chunks = plan.max_chunks;
+  p.max_entries = max_context_len;
+  p.row_stride = plan.row_stride;
+  p.weight_entries = max_entries;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.decay = decay;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rows = G * T;
+  const unsigned n = static_cast<unsigned>(units);
+  cudaError_t e = kv_format == PA_KV_BF16  ? launch_observe_bf16(p, head_dim, rows, n, s)
+                  : kv_format == PA_KV_INT4 ? launch_observe_int4(p, head_dim, rows, n, s)
+                                            : launch_observe_fp8(p, head_dim, rows, n, s);
+  if (e == cudaSuccess) e = launch_observe_sum(p, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len, int budget) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len <= 0 || budget <= 0) return 0;
+  return evict_plan(num_seqs, num_kv_heads, max_context_len, budget).bytes;
+}
+
+pa_status pa_evict_tokens(int32_t* new_lens, void* k_cache, void* v_cache, int kv_format,
+                          const int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* context_lens, int max_context_len, float* weights,
+                          int32_t* positions, int max_entries, int budget, int num_recent,
+                          int num_seqs, int num_blocks, int num_kv_heads, int head_dim,
+                          int block_size, void* workspace, size_t workspace_bytes,
+                          pa_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads < 1 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      max_context_len < 1 || budget < 1 || num_recent < 0 || num_recent > budget ||
+      kv_format < PA_KV_BF16 || kv_format > PA_KV_INT4)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!new_lens || !k_cache || !v_cache || !block_tables || !context_lens || !weights ||
+      !positions || new_lens == context_lens)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_context_len) >
+          static_cast<long long>(max_blocks_per_seq) * kBlockSize ||
+      max_context_len > max_entries)
+    return PA_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_seqs) * num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  const EvictPlan plan = evict_plan(num_seqs, num_kv_heads, max_context_len, budget);
+  if (!workspace || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  EvictParams p{};
+  p.k_pool = k_cache;
+  p.v_pool = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.new_lens = new_lens;
+  p.weights = weights;
+  p.positions = positions;
+  p.counts = static_cast<int32_t*>(workspace);
+  p.moves = reinterpret_cast<int2*>(static_cast<char*>(workspace) + plan.off_moves);
+  p.mbs = max_blocks_per_seq;
+  p.max_ctx = max_context_len;
+  p.num_seqs = num_seqs;
+  p.Hkv = num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.weight_entries = max_entries;
+  p.budget = budget;
+  p.num_recent = num_recent;
+  p.max_moves = plan.max_moves;
+  return launch_evict(p, kv_format, head_dim, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 pa_status pa_get_device_error(pa_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PA_ERR_CUDA;
@@ -662,7 +999,11 @@ pa_status pa_get_device_error(pa_stream_t stream) {
       take_error_attn8_d128(&bits) != cudaSuccess || take_error_group8_d64(&bits) != cudaSuccess ||
       take_error_group8_d128(&bits) != cudaSuccess || take_error_spec(&bits) != cudaSuccess ||
       take_error_attn_tc_d128(&bits) != cudaSuccess || take_error_stream_d64(&bits) != cudaSuccess ||
-      take_error_stream_d128(&bits) != cudaSuccess || take_error_misc(&bits) != cudaSuccess)
+      take_error_stream_d128(&bits) != cudaSuccess || take_error_misc(&bits) != cudaSuccess ||
+      take_error_attn4_d64(&bits) != cudaSuccess || take_error_attn4_d128(&bits) != cudaSuccess ||
+      take_error_cache4(&bits) != cudaSuccess || take_error_observe_bf16(&bits) != cudaSuccess ||
+      take_error_observe_fp8(&bits) != cudaSuccess ||
+      take_error_observe_int4(&bits) != cudaSuccess || take_error_evict(&bits) != cudaSuccess)
     return PA_ERR_CUDA;
   if (bits & kErrTimeout) return PA_ERR_TIMEOUT;
   if (bits & kErrBounds) return PA_ERR_BOUNDS;

@@ -107,6 +107,20 @@ pa_status pa_bm_append_slot(pa_block_manager* bm, int seq_id, int64_t* slot, int
   return PA_OK;
 }
 
+pa_status pa_bm_truncate(pa_block_manager* bm, int seq_id, int num_tokens) {
+  if (!bm || num_tokens < 0) return PA_ERR_INVALID_ARG;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end() || num_tokens > it->second.num_tokens) return PA_ERR_INVALID_ARG;
+  pa_block_manager::Seq& s = it->second;
+  const size_t keep = (static_cast<size_t>(num_tokens) + bm->block_size - 1) / bm->block_size;
+  while (s.blocks.size() > keep) {
+    bm->release(s.blocks.back());
+    s.blocks.pop_back();
+  }
+  s.num_tokens = num_tokens;
+  return PA_OK;
+}
+
 pa_status pa_bm_free_sequence(pa_block_manager* bm, int seq_id) {
   if (!bm) return PA_ERR_INVALID_ARG;
   auto it = bm->seqs.find(seq_id);

@@ -1,0 +1,150 @@
+// 4-bit pages: quantising writes by slot (pa_reshape_and_cache_int4) or by block table
+// (the new tokens of pa_attention_int4), and reads by slot (pa_gather_cache_int4).
+#include "pa_pages.cuh"
+
+namespace pa {
+
+// One thread per 8 head dims of one (token, kv head), K and V; four threads make a
+// group of 32 dims.  APPEND: token i = b * T + t goes to position context_lens[b] - T + t
+// of sequence b; otherwise to slots[i].
+template <int D, bool APPEND>
+__global__ void __launch_bounds__(256)
+    store_int4_kernel(const uint4* __restrict__ key, const uint4* __restrict__ value,
+                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
+                      const int64_t* __restrict__ slots, const int32_t* __restrict__ tables,
+                      const int32_t* __restrict__ lens, int T, int mbs, int max_ctx,
+                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+                      int num_tokens, int num_blocks, int hkv) {
+  using P = Page<kPageInt4, D>;
+  constexpr int VEC = D / 8;
+  const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long total = static_cast<long long>(num_tokens) * hkv * VEC;
+  const long long at = min(idx, total - 1);    // every lane takes part in the shuffles
+  const int v = static_cast<int>(at % VEC);
+  const long long th = at / VEC;
+  const int h = static_cast<int>(th % hkv);
+  const int i = static_cast<int>(th / hkv);
+  long long s = -1;
+  bool bad = false;
+  if constexpr (APPEND) {
+    const int b = i / T, L = lens[b];
+    // a length out of range is reported by the attention kernel, which skips the sequence
+    if (L >= T && L <= max_ctx) {
+      const int pos = L - T + i % T;
+      const int phys = tables[static_cast<size_t>(b) * mbs + pos / kBlockSize];
+      s = static_cast<long long>(phys) * kBlockSize + pos % kBlockSize;
+      bad = static_cast<unsigned>(phys) >= static_cast<unsigned>(num_blocks);
+    }
+  } else {
+    s = slots[i];
+    bad = s >= static_cast<long long>(num_blocks) * kBlockSize;
+  }
+  const uint4 kx = key[at], vx = value[at];
+  uint32_t ks, vs;
+  const uint32_t kc = quantize_int4_8(kx, k_scale[h], ks);
+  const uint32_t vc = quantize_int4_8(vx, v_scale[h], vs);
+  if (idx >= total) return;
+  if (bad) {
+    if (v == 0) atomicOr(&g_pa_err, kErrBounds);
+    return;
+  }
+  if (s < 0) return;                           // padding token
+  const size_t page = (static_cast<size_t>(s / kBlockSize) * hkv + h) * P::kBytes;
+  const int t = static_cast<int>(s % kBlockSize);
+  *reinterpret_cast<uint32_t*>(k_cache + page + t * P::kRow + 4 * v) = kc;
+  *reinterpret_cast<uint32_t*>(v_cache + page + t * P::kRow + 4 * v) = vc;
+  if ((v & 3) == 0) {
+    k_cache[page + P::kCodes + t * P::kGroups + v / 4] = static_cast<uint8_t>(ks);
+    v_cache[page + P::kCodes + t * P::kGroups + v / 4] = static_cast<uint8_t>(vs);
+  }
+}
+
+// One thread per 8 head dims of one (slot, kv head): bf16((u - 8) * (scale * head_scale)).
+template <int D>
+__global__ void __launch_bounds__(256)
+    gather_int4_kernel(uint4* __restrict__ key, uint4* __restrict__ value,
+                       const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
+                       const int64_t* __restrict__ slots, const float* __restrict__ k_scale,
+                       const float* __restrict__ v_scale, int num_tokens, int num_blocks,
+                       int hkv) {
+  using P = Page<kPageInt4, D>;
+  constexpr int VEC = D / 8;
+  const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (idx >= static_cast<long long>(num_tokens) * hkv * VEC) return;
+  const int v = static_cast<int>(idx % VEC);
+  const long long th = idx / VEC;
+  const int h = static_cast<int>(th % hkv);
+  const long long s = slots[th / hkv];
+  uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (s >= static_cast<long long>(num_blocks) * kBlockSize) {
+    if (v == 0) atomicOr(&g_pa_err, kErrBounds);
+  } else if (s >= 0) {
+    const size_t page = (static_cast<size_t>(s / kBlockSize) * hkv + h) * P::kBytes;
+    const int t = static_cast<int>(s % kBlockSize);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint8_t* pool = kv ? v_cache : k_cache;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(pool + page + t * P::kRow + 4 * v);
+      const uint32_t sb = pool[page + P::kCodes + t * P::kGroups + v / 4];
+      const uint32_t sh = e4m3x2_to_f16x2(sb);
+      const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffffu))) *
+                         (kv ? v_scale[h] : k_scale[h]);
+      uint32_t r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = static_cast<float>(static_cast<int>((w >> (8 * e)) & 15u) - 8) * step;
+        const float c = static_cast<float>(static_cast<int>((w >> (8 * e + 4)) & 15u) - 8) * step;
+        r[e] = bf162_bits(__floats2bfloat162_rn(a, c));
+      }
+      out[kv] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+  key[idx] = out[0];
+  value[idx] = out[1];
+}
+
+namespace {
+
+unsigned blocks_for(long long threads) { return static_cast<unsigned>((threads + 255) / 256); }
+
+}  // namespace
+
+cudaError_t launch_store_int4(const void* key, const void* value, void* k_cache, void* v_cache,
+                              const int64_t* slots, const int32_t* tables, const int32_t* lens,
+                              int T, int mbs, int max_ctx, const float* k_scale,
+                              const float* v_scale, int num_tokens, int num_blocks, int hkv,
+                              int head_dim, cudaStream_t s) {
+  if (num_tokens == 0) return cudaSuccess;
+  const unsigned grid = blocks_for(static_cast<long long>(num_tokens) * hkv * (head_dim / 8));
+  auto go = [&](auto fn) {
+    fn<<<grid, 256, 0, s>>>(static_cast<const uint4*>(key), static_cast<const uint4*>(value),
+                            static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), slots,
+                            tables, lens, T, mbs, max_ctx, k_scale, v_scale, num_tokens,
+                            num_blocks, hkv);
+  };
+  if (slots != nullptr)
+    head_dim == 64 ? go(store_int4_kernel<64, false>) : go(store_int4_kernel<128, false>);
+  else
+    head_dim == 64 ? go(store_int4_kernel<64, true>) : go(store_int4_kernel<128, true>);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_int4(void* key, void* value, const void* k_cache, const void* v_cache,
+                               const int64_t* slots, const float* k_scale, const float* v_scale,
+                               int num_tokens, int num_blocks, int hkv, int head_dim,
+                               cudaStream_t s) {
+  if (num_tokens == 0) return cudaSuccess;
+  const unsigned grid = blocks_for(static_cast<long long>(num_tokens) * hkv * (head_dim / 8));
+  auto go = [&](auto fn) {
+    fn<<<grid, 256, 0, s>>>(static_cast<uint4*>(key), static_cast<uint4*>(value),
+                            static_cast<const uint8_t*>(k_cache),
+                            static_cast<const uint8_t*>(v_cache), slots, k_scale, v_scale,
+                            num_tokens, num_blocks, hkv);
+  };
+  head_dim == 64 ? go(gather_int4_kernel<64>) : go(gather_int4_kernel<128>);
+  return cudaGetLastError();
+}
+
+cudaError_t take_error_cache4(unsigned* bits) { return read_error_word(bits); }
+
+}  // namespace pa

@@ -70,6 +70,40 @@ struct StreamCtl {
 };
 constexpr unsigned long long kStreamTag = 0x70615F7374726D31ull;
 
+// Accumulated attention weights: the first launch writes scores and the chunks' (m, l),
+// the second adds the weights up.
+struct ObserveParams {
+  const void* q;                  // bf16 [B, T, Hq, D]
+  const void* k_pool;
+  const float* k_scale;           // [Hkv], FP8 and INT4 pages
+  const int32_t* block_tables;    // [B, mbs]
+  const int32_t* context_lens;    // [B]
+  const int32_t* seq_lens;        // [B] or nullptr (= context_lens)
+  const float* weights;           // [B, Hkv, weight_entries]
+  float* weights_out;             // may be `weights`
+  int32_t* positions;             // [B, Hkv, weight_entries] or nullptr
+  float* scores;                  // scratch [B, Hkv, max_entries, row_stride]
+  float2* ml;                     // scratch [B, Hkv, max_chunks, G * T]
+  int mbs, max_ctx, num_seqs, T, Hq, Hkv, G, num_blocks;
+  int ppb;                        // pages per chunk
+  int max_chunks, max_entries, row_stride, weight_entries;
+  float scale_log2, decay;
+};
+
+// Eviction: the first launch selects and pairs movers with gaps, the second moves.
+struct EvictParams {
+  void* k_pool;
+  void* v_pool;
+  const int32_t* block_tables;    // [B, mbs]
+  const int32_t* context_lens;    // [B]
+  int32_t* new_lens;              // [B]
+  float* weights;                 // [B, Hkv, weight_entries]
+  int32_t* positions;             // [B, Hkv, weight_entries]
+  int2* moves;                    // scratch [B, Hkv, max_moves] (from, to)
+  int32_t* counts;                // scratch [B, Hkv]
+  int mbs, max_ctx, num_seqs, Hkv, num_blocks, weight_entries, budget, num_recent, max_moves;
+};
+
 // The partition size (tokens) a per-sequence call with partition_size 0 uses:
 // the library default for this batch, with the FP8-page rule when fp8_pages.
 int default_partition_for(int max_context_len, int num_seqs, int num_kv_heads, bool fp8_pages);
@@ -131,6 +165,27 @@ cudaError_t launch_pad_rows(int32_t* block_tables, int32_t* context_lens, int fr
 // Graph runner staging: `bytes` (a multiple of 16; both addresses 16-byte aligned and
 // device-addressable) copied by a kernel.
 cudaError_t launch_stage_copy(void* dst, const void* src, size_t bytes, cudaStream_t s);
+// 4-bit pages: attention (k_pool / v_pool hold the pools), writes by slot or, with slots ==
+// nullptr, by block table, and reads by slot.
+cudaError_t launch_attn4_d64(const AttnParams& p, int rows, unsigned units, cudaStream_t s);
+cudaError_t launch_attn4_d128(const AttnParams& p, int rows, unsigned units, cudaStream_t s);
+cudaError_t launch_store_int4(const void* key, const void* value, void* k_cache, void* v_cache,
+                              const int64_t* slots, const int32_t* tables, const int32_t* lens,
+                              int T, int mbs, int max_ctx, const float* k_scale,
+                              const float* v_scale, int num_tokens, int num_blocks, int hkv,
+                              int head_dim, cudaStream_t s);
+cudaError_t launch_gather_int4(void* key, void* value, const void* k_cache, const void* v_cache,
+                               const int64_t* slots, const float* k_scale, const float* v_scale,
+                               int num_tokens, int num_blocks, int hkv, int head_dim,
+                               cudaStream_t s);
+cudaError_t launch_observe_bf16(const ObserveParams& p, int head_dim, int rows, unsigned units,
+                                cudaStream_t s);
+cudaError_t launch_observe_fp8(const ObserveParams& p, int head_dim, int rows, unsigned units,
+                               cudaStream_t s);
+cudaError_t launch_observe_int4(const ObserveParams& p, int head_dim, int rows, unsigned units,
+                                cudaStream_t s);
+cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s);
+cudaError_t launch_evict(const EvictParams& p, int format, int head_dim, cudaStream_t s);
 cudaError_t launch_reduce(const AttnParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_reshape(const void* key, const void* value, void* k_cache, void* v_cache,
                            const int64_t* slots, int num_tokens, int num_blocks, int hkv,
@@ -154,5 +209,12 @@ cudaError_t take_error_attn_tc_d128(unsigned* bits);
 cudaError_t take_error_stream_d64(unsigned* bits);
 cudaError_t take_error_stream_d128(unsigned* bits);
 cudaError_t take_error_misc(unsigned* bits);
+cudaError_t take_error_attn4_d64(unsigned* bits);
+cudaError_t take_error_attn4_d128(unsigned* bits);
+cudaError_t take_error_cache4(unsigned* bits);
+cudaError_t take_error_observe_bf16(unsigned* bits);
+cudaError_t take_error_observe_fp8(unsigned* bits);
+cudaError_t take_error_observe_int4(unsigned* bits);
+cudaError_t take_error_evict(unsigned* bits);
 
 }  // namespace pa
