@@ -384,8 +384,47 @@ int int4_span(int max_context_len, int T, int window) {
                            kBlockSize * kBlockSize));
 }
 
-int int4_partition_tokens(int span, int num_seqs, int num_kv_heads) {
-  return default_partition_tokens(span, num_seqs, num_kv_heads, true);
+// How a call over 4-bit pages splits its work.  An explicit partition size, no scratch, or
+// contexts too short to be worth splitting: units of fixed size (a merge only if a
+// sequence has several).  Otherwise balanced runs over the resident warps.
+constexpr int kInt4WholePages = 16;     // contexts up to this stay whole
+constexpr int kInt4MinShare = 8;        // list entries (pages) a warp takes at least
+constexpr int kInt4FlatSeqs = 1024;     // every warp reads all lengths: not for larger batches
+
+struct Int4Plan {
+  bool flat = false;
+  Plan units;
+  int workers = 1;
+  size_t off_ml = 0, bytes = 0;
+};
+
+Int4Plan int4_plan(int num_seqs, int hq, int hkv, int T, int span, int head_dim,
+                   int partition_size, bool scratch) {
+  Int4Plan pl;
+  const int pages = ceil_div(span, kBlockSize);
+  const int rows = hq / hkv * T;
+  const Attn4Tile tile = attn4_tile(rows);
+  const long long jobs = static_cast<long long>(num_seqs) * hkv * tile.ntw;
+  const long long all = jobs * pages;
+  pl.flat = partition_size == 0 && scratch && pages > kInt4WholePages &&
+            num_seqs <= kInt4FlatSeqs && all < (1ll << 31);
+  if (pl.flat) {
+    pl.workers = static_cast<int>(std::min<long long>(kAttn4Sms * tile.ctas * 4,
+                                                      (all + kInt4MinShare - 1) / kInt4MinShare));
+    const size_t slot_rows = static_cast<size_t>(pl.workers) * 2 * 8 * tile.nt;
+    pl.off_ml = round256(slot_rows * head_dim * sizeof(float));
+    pl.bytes = pl.off_ml + round256(slot_rows * sizeof(float2));
+    return pl;
+  }
+  int psize = partition_size;
+  if (psize == 0)
+    psize = scratch && pages > kInt4WholePages ? default_partition_tokens(span, num_seqs, hkv, true)
+                                               : pages * kBlockSize;
+  pl.units = make_plan(num_seqs, hq, T, span, head_dim, psize, 0);
+  pl.off_ml = pl.units.off_ml;
+  pl.bytes = pl.units.ws_bytes;
+  pl.workers = static_cast<int>(std::min<long long>(jobs * pl.units.max_parts, 1 << 30));
+  return pl;
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -757,10 +796,11 @@ size_t pa_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
       max_context_len <= 0 || head_dim <= 0 || block_size != kBlockSize || partition_size < 0 ||
       window_size < 0)
     return 0;
-  const int span = int4_span(max_context_len, num_query_tokens, window_size);
-  const int psize = partition_size > 0 ? partition_size
-                                       : int4_partition_tokens(span, num_seqs, num_kv_heads);
-  return make_plan(num_seqs, num_q_heads, num_query_tokens, span, head_dim, psize, 0).ws_bytes;
+  if (num_q_heads % num_kv_heads != 0) return 0;
+  return int4_plan(num_seqs, num_q_heads, num_kv_heads, num_query_tokens,
+                   int4_span(max_context_len, num_query_tokens, window_size), head_dim,
+                   partition_size, true)
+      .bytes;
 }
 
 pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const void* new_value,
@@ -794,20 +834,16 @@ pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const
 
   // the entries one sequence may read: all of them, or those under its queries' windows
   const int span = int4_span(max_context_len, T, window_size);
-  int psize = partition_size;
-  if (psize == 0) {
-    psize = int4_partition_tokens(span, num_seqs, num_kv_heads);
-    if (workspace == nullptr) psize = ceil_div(span, kBlockSize) * kBlockSize;   // whole sequences
-  }
-  const Plan plan = make_plan(num_seqs, num_q_heads, T, span, head_dim, psize, 0);
-  if (plan.max_parts > kMaxPartitions) return PA_ERR_UNSUPPORTED;
-  if (plan.ws_bytes > 0) {
-    if (!workspace || workspace_bytes < plan.ws_bytes) return PA_ERR_WORKSPACE;
+  const Int4Plan plan = int4_plan(num_seqs, num_q_heads, num_kv_heads, T, span, head_dim,
+                                  partition_size, workspace != nullptr);
+  if (!plan.flat && plan.units.max_parts > kMaxPartitions) return PA_ERR_UNSUPPORTED;
+  if (plan.bytes > 0) {
+    if (!workspace || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
   }
-  const long long units =
-      static_cast<long long>(plan.max_parts) * num_kv_heads * num_seqs;
-  if (units >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  // one CTA per (sequence, kv head, row) merges balanced runs
+  if (static_cast<long long>(num_seqs) * num_kv_heads * 64 >= (1ll << 31))
+    return PA_ERR_UNSUPPORTED;
   if (new_key != nullptr &&
       !int4_store_fits(static_cast<long long>(num_seqs) * T, num_kv_heads, head_dim))
     return PA_ERR_UNSUPPORTED;
@@ -818,7 +854,7 @@ pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const
                         T, max_blocks_per_seq, max_context_len, k_scale, v_scale, num_seqs * T,
                         num_blocks, num_kv_heads, head_dim, s) != cudaSuccess)
     return PA_ERR_CUDA;
-  AttnParams p{};
+  Attn4Params p{};
   p.q = q;
   p.out = out;
   p.block_tables = block_tables;
@@ -827,12 +863,17 @@ pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const
   p.v_pool = v_cache;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
-  if (plan.ws_bytes > 0) {
+  if (plan.bytes > 0) {
     char* ws = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-    p.stream_ctl = ws + plan.off_counter + 16;   // the merge leaves it as after any call
+    // the split-KV merge waits for the attention kernel in one CTA at least when it has this
+    // state to leave as after any call
+    if (!plan.flat) p.stream_ctl = ws + plan.units.off_counter + 16;
   }
+  p.flat = plan.flat;
+  p.workers = plan.workers;
+  p.min_share = kInt4MinShare;
   p.mbs = max_blocks_per_seq;
   p.max_ctx = max_context_len;
   p.num_seqs = num_seqs;
@@ -841,16 +882,15 @@ pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const
   p.Hkv = num_kv_heads;
   p.G = G;
   p.num_blocks = num_blocks;
-  p.ppb = plan.ppb;
-  p.max_parts = plan.max_parts;
+  p.ppb = plan.units.ppb;
+  p.max_parts = plan.units.max_parts;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window_size;
   p.wcap = window_size > 0 ? static_cast<unsigned>(window_size) : 0x80000000u;
   p.wspan = window_size > 0 ? window_size : (1 << 30);
   const int rows = G * T;
-  const unsigned n = static_cast<unsigned>(units);
-  cudaError_t e = head_dim == 64 ? launch_attn4_d64(p, rows, n, s) : launch_attn4_d128(p, rows, n, s);
-  if (e == cudaSuccess && plan.ws_bytes > 0) e = launch_reduce(p, head_dim, s);
+  cudaError_t e = head_dim == 64 ? launch_attn4_d64(p, rows, s) : launch_attn4_d128(p, rows, s);
+  if (e == cudaSuccess && plan.units.ws_bytes > 0) e = launch_reduce(p, head_dim, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -70,6 +70,27 @@ struct StreamCtl {
 };
 constexpr unsigned long long kStreamTag = 0x70615F7374726D31ull;
 
+// 4-bit pages.  flat: balanced runs, two partial slots of a tile's rows per worker in part_o /
+// part_ml; otherwise units of ppb pages and the split-KV layout.
+struct Attn4Params : AttnParams {
+  bool flat;
+  int workers;                    // warps that take part
+  int min_share;                  // balanced mode: smallest run in list entries
+};
+// Tile of a warp for `rows` query rows per kv head: n-tiles of 8 rows, row columns, and the
+// CTAs of four warps that an SM holds.
+struct Attn4Tile {
+  int nt, ntw, ctas;
+};
+constexpr Attn4Tile attn4_tile(int rows) {
+  return rows <= 8    ? Attn4Tile{1, 1, 4}
+         : rows <= 16 ? Attn4Tile{2, 1, 2}
+         : rows <= 24 ? Attn4Tile{3, 1, 2}
+         : rows <= 32 ? Attn4Tile{4, 1, 2}
+                      : Attn4Tile{4, 2, 2};
+}
+constexpr int kAttn4Sms = 152;    // SMs the balanced mode fills
+
 // Accumulated attention weights: the first launch writes scores and the chunks' (m, l),
 // the second adds the weights up.
 struct ObserveParams {
@@ -167,8 +188,8 @@ cudaError_t launch_pad_rows(int32_t* block_tables, int32_t* context_lens, int fr
 cudaError_t launch_stage_copy(void* dst, const void* src, size_t bytes, cudaStream_t s);
 // 4-bit pages: attention (k_pool / v_pool hold the pools), writes by slot or, with slots ==
 // nullptr, by block table, and reads by slot.
-cudaError_t launch_attn4_d64(const AttnParams& p, int rows, unsigned units, cudaStream_t s);
-cudaError_t launch_attn4_d128(const AttnParams& p, int rows, unsigned units, cudaStream_t s);
+cudaError_t launch_attn4_d64(const Attn4Params& p, int rows, cudaStream_t s);
+cudaError_t launch_attn4_d128(const Attn4Params& p, int rows, cudaStream_t s);
 cudaError_t launch_store_int4(const void* key, const void* value, void* k_cache, void* v_cache,
                               const int64_t* slots, const int32_t* tables, const int32_t* lens,
                               int T, int mbs, int max_ctx, const float* k_scale,

@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) observe_scores_kernel(co
   for (int i = 0; i < S - 1; ++i) issue(i);
 
   uint8_t* qt = smem + Sm::kQOff;
-  load_q_tile<F, D, C::kRows>(qt, p.q, b, g, T, G, p.Hq, nrows, p.scale_log2,
-                              F == kPageBf16 ? 1.f : p.k_scale[g], warp, lane, C::kWarps);
+  load_q_tile<F, D, C::kRows, 2>(qt, p.q, b, g, T, G, p.Hq, 0, nrows, p.scale_log2,
+                                 F == kPageBf16 ? 1.f : p.k_scale[g], lane, warp, C::kWarps);
   __syncthreads();
   QOperand<F, D, NT, C::kQRegs> qo;
   qo.template load<C::kRows>(qt, col * NT, lane);
@@ -107,6 +107,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) observe_scores_kernel(co
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int j0 = tok0 + gid, j1 = j0 + 8;
+      t[j][0] *= qo.rs0[j];
+      t[j][1] *= qo.rs1[j];
+      t[j][2] *= qo.rs0[j];
+      t[j][3] *= qo.rs1[j];
       if (!ok || j0 > lim0[j]) t[j][0] = -CUDART_INF_F;
       if (!ok || j0 > lim1[j]) t[j][1] = -CUDART_INF_F;
       if (!ok || j1 > lim0[j]) t[j][2] = -CUDART_INF_F;

@@ -14,8 +14,8 @@
 // both are exact, and mma.sync multiplies subnormal f16 operands exactly.  A 32-bit word
 // of eight nibbles therefore gives its four operand registers with one shift and
 // four masks; the factors 2^24 and 16 are powers of two folded elsewhere (the even
-// and odd dims of Q, the output), and the offset 8 leaves the contraction as
-// 8 * (sum of the other operand).  E2M1 codes would need a conversion for
+// and odd dims of Q, the output), and the offset 8 leaves the contraction as 8 * (sum
+// over the group of scale * the other operand), one more small tile.  E2M1 codes would need a conversion for
 // every pair of values, and have a larger error on normally distributed values.
 #pragma once
 
@@ -86,15 +86,28 @@ __device__ __forceinline__ uint32_t ldsm_offset(int lane) {
   return page_swizzle<F, D>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
 }
 
-// Four E4M3 codes of a word as floats.
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&s)[4]) {
-  const uint32_t a = e4m3x2_to_f16x2(w), b = e4m3x2_to_f16x2(w >> 16);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+// Four E4M3 codes of a word as two f16x2 (codes 0, 1 and 2, 3).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ void f16x4_to_f32(const uint32_t (&h)[2], float (&s)[4]) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
   s[0] = x.x;
   s[1] = x.y;
   s[2] = y.x;
   s[3] = y.y;
+}
+
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+  return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&b)));
 }
 
 constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
@@ -102,8 +115,12 @@ constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
 // Query rows in shared memory, as B operands of the score tiles.
 //   frag  [n-tile][16-dim k step][lane] two registers: row 8 n-tile + lane/4, the
 //         dims that the K format puts into lane%4's A registers
-//   qsum  [row][group] INT4: -8 * 2^-24 * (sum of the group's operands)
-//   rs    [row] factor from a score accumulator to the log2-domain score
+//   off   [n-tile][lane] INT4: two registers of a k step over the groups that takes the
+//         codes' offset back, with the token's scales as the A operand: row n's
+//         x_g = -8 * 2^-24 * (sum of group g's operands) as f16 high part (k = g) and
+//         2^11 times the f16 residual (k = g + 8; A is 2^-11 times the scale there)
+//   rs    [row] positive factor from a score accumulator to the log2-domain score (the
+//         sign of the softmax scale goes into the operands)
 // bf16 pages take Q as it is.  FP8 and INT4 pages take it in f16: each row is
 // scaled by a power of two so that its largest magnitude lies in [2^13, 2^14),
 // which keeps every value within 2^-24 of the row's largest exact (the odd dims of
@@ -111,9 +128,9 @@ constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
 template <int F, int D, int ROWS>
 struct QTile {
   static constexpr int kFragBytes = (ROWS / 8) * (D / 16) * 32 * 8;
-  static constexpr int kSumOff = kFragBytes;
-  static constexpr int kSumBytes = F == kPageInt4 ? ROWS * (D / kGroupDims) * 4 : 0;
-  static constexpr int kRsOff = kSumOff + kSumBytes;
+  static constexpr int kOffOff = kFragBytes;
+  static constexpr int kOffBytes = F == kPageInt4 ? ROWS / 8 * 32 * 8 : 0;
+  static constexpr int kRsOff = kOffOff + kOffBytes;
   static constexpr int kBytes = kRsOff + ROWS * 4;
 };
 
@@ -142,59 +159,101 @@ __device__ __forceinline__ int q_frag_pos(int n, int d) {
   return ((((n >> 3) * (D / 16) + step) * 32) + (n & 7) * 4 + lane4) * 4 + e;
 }
 
-// All threads of the CTA: write the query rows of (sequence b, kv head g) as operands.
-// Row n = t * G + hl; rows past nrows are zero.  Needs a CTA barrier afterwards.
-template <int F, int D, int ROWS>
+// Query rows row0 .. row0 + ROWS - 1 of (sequence b, kv head g) as operands; row n = t * G +
+// hl, rows past nrows are zero.  Warp `part` of `parts` writes every parts-th run of RC
+// rows (all its loads in flight at once); a barrier among the warps follows.
+template <int F, int D, int ROWS, int RC>
 __device__ __forceinline__ void load_q_tile(uint8_t* qt, const void* q, int b, int g, int T, int G,
-                                            int Hq, int nrows, float scale_log2, float k_scale,
-                                            int warp, int lane, int nwarps) {
+                                            int Hq, int row0, int nrows, float scale_log2,
+                                            float k_scale, int lane, int part, int parts) {
   using Q = QTile<F, D, ROWS>;
-  constexpr int DL = D / 32;                 // dims per lane: lane + 32 k
+  constexpr int DL = D / 32;                 // consecutive dims per lane
+  static_assert(ROWS % RC == 0, "whole runs");
   uint16_t* frag = reinterpret_cast<uint16_t*>(qt);
-  float* qsum = reinterpret_cast<float*>(qt + Q::kSumOff);
+  uint16_t* off = reinterpret_cast<uint16_t*>(qt + Q::kOffOff);
   float* rs = reinterpret_cast<float*>(qt + Q::kRsOff);
-  for (int n = warp; n < ROWS; n += nwarps) {
-    float x[DL];
+  const float sign = scale_log2 * k_scale < 0.f ? -1.f : 1.f;
+  const float size = fabsf(scale_log2 * k_scale);
+  const int d0 = lane * DL;
+  for (int n0 = RC * part; n0 < ROWS; n0 += RC * parts) {
+    uint32_t raw[RC][DL / 2];
 #pragma unroll
-    for (int k = 0; k < DL; ++k) x[k] = 0.f;
-    if (n < nrows) {
-      const size_t row = (static_cast<size_t>(b) * T + n / G) * Hq + g * G + n % G;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(q) + row * D;
+    for (int r = 0; r < RC; ++r) {
+      const int n = row0 + n0 + r;
 #pragma unroll
-      for (int k = 0; k < DL; ++k) x[k] = __bfloat162float(src[lane + 32 * k]);
-    }
-    if constexpr (F == kPageBf16) {
-#pragma unroll
-      for (int k = 0; k < DL; ++k)
-        frag[q_frag_pos<F, D>(n, lane + 32 * k)] = __bfloat16_as_ushort(__float2bfloat16_rn(x[k]));
-      if (lane == 0) rs[n] = scale_log2;
-      continue;
-    }
-    float mx = 0.f;
-#pragma unroll
-    for (int k = 0; k < DL; ++k) mx = fmaxf(mx, fabsf(x[k]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // exponent of the row's largest magnitude, kept where 2^(13 - e) and its inverse are normal
-    int e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-    e = max(-100, min(e, 100));
-    const float up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-    const float down = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-#pragma unroll
-    for (int k = 0; k < DL; ++k) {
-      const int d = lane + 32 * k;
-      float y = x[k] * up;
-      if (F == kPageInt4 && (d & 1)) y *= 0.0625f;
-      const __half h = __float2half_rn(y);
-      frag[q_frag_pos<F, D>(n, d)] = __half_as_ushort(h);
-      if constexpr (F == kPageInt4) {
-        float s = __half2float(h) * ((d & 1) ? 16.f : 1.f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) qsum[n * DL + k] = s * (-8.f / 16777216.f);
+      for (int k = 0; k < DL / 2; ++k) raw[r][k] = 0u;
+      if (n < nrows) {
+        const size_t row = (static_cast<size_t>(b) * T + n / G) * Hq + g * G + n % G;
+        const uint32_t* src =
+            reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(q) + row * D + d0);
+        if constexpr (DL == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src);
+          raw[r][0] = v.x;
+          raw[r][1] = v.y;
+        } else {
+          raw[r][0] = *src;
+        }
       }
     }
-    if (lane == 0) rs[n] = scale_log2 * k_scale * down * (F == kPageInt4 ? 16777216.f : 1.f);
+#pragma unroll
+    for (int r = 0; r < RC; ++r) {
+      const int n = n0 + r;
+      float x[DL];
+#pragma unroll
+      for (int k = 0; k < DL; ++k)
+        x[k] = sign * ((k & 1) ? bf16_hi(raw[r][k / 2]) : bf16_lo(raw[r][k / 2]));
+      if constexpr (F == kPageBf16) {
+#pragma unroll
+        for (int k = 0; k < DL; ++k)
+          frag[q_frag_pos<F, D>(n, d0 + k)] = __bfloat16_as_ushort(__float2bfloat16_rn(x[k]));
+        if (lane == 0) rs[n] = fmaxf(size, 1e-36f);
+      } else {
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < DL; ++k) mx = fmaxf(mx, fabsf(x[k]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // exponent of the row's largest magnitude, kept where 2^(13 - e) and its inverse are
+        // normal
+        int e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127;
+        e = max(-100, min(e, 100));
+        const float up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < DL; ++k) {
+          float y = x[k] * up;
+          if (F == kPageInt4 && (k & 1)) y *= 0.0625f;
+          const __half h = __float2half_rn(y);
+          frag[q_frag_pos<F, D>(n, d0 + k)] = __half_as_ushort(h);
+          sum += __half2float(h) * ((k & 1) ? 16.f : 1.f);
+        }
+        if constexpr (F == kPageInt4) {
+          constexpr int GL = kGroupDims / DL;    // lanes of a group
+#pragma unroll
+          for (int o = GL / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float v = sum * (-8.f / 16777216.f);
+          const __half vh = __float2half_rn(v);
+          const __half vl = __float2half_rn((v - __half2float(vh)) * 2048.f);
+          uint16_t* to = off + (n >> 3) * 128 + (n & 7) * 16;   // [lane % 4][4 halves]
+          if (lane % GL == 0) {
+            const int g2 = lane / GL;
+            to[(g2 >> 1) * 4 + (g2 & 1)] = __half_as_ushort(vh);
+            to[(g2 >> 1) * 4 + (g2 & 1) + 2] = __half_as_ushort(vl);
+          } else if (lane % GL == 1 && lane / GL < 4) {
+            // the k steps' other lanes: zero
+            constexpr int kUsed = D / kGroupDims / 2;
+            if (lane / GL >= kUsed)
+              *reinterpret_cast<uint2*>(to + (lane / GL) * 4) = make_uint2(0u, 0u);
+          }
+          if constexpr (D / kGroupDims == 2) {
+            if (lane == 2 || lane == 3) *reinterpret_cast<uint2*>(to + lane * 4) = make_uint2(0u, 0u);
+          }
+        }
+        if (lane == 0)
+          rs[n] = fmaxf(size * down * (F == kPageInt4 ? 16777216.f : 1.f), 1e-36f);
+      }
+    }
   }
 }
 
@@ -203,28 +262,23 @@ __device__ __forceinline__ void load_q_tile(uint8_t* qt, const void* q, int b, i
 template <int F, int D, int NT, bool kRegs>
 struct QOperand {
   uint2 f[kRegs ? NT : 1][kRegs ? D / 16 : 1];
-  float c0[NT][F == kPageInt4 ? D / kGroupDims : 1], c1[NT][F == kPageInt4 ? D / kGroupDims : 1];
+  uint2 o[kRegs ? NT : 1];
   float rs0[NT], rs1[NT];
   const uint2* base;
+  const uint2* obase;
 
   template <int ROWS>
   __device__ __forceinline__ void load(const uint8_t* qt, int tile0, int lane) {
     using Q = QTile<F, D, ROWS>;
     base = reinterpret_cast<const uint2*>(qt) + static_cast<size_t>(tile0) * (D / 16) * 32 + lane;
-    const float* qsum = reinterpret_cast<const float*>(qt + Q::kSumOff);
+    obase = reinterpret_cast<const uint2*>(qt + Q::kOffOff) + tile0 * 32 + lane;
     const float* rs = reinterpret_cast<const float*>(qt + Q::kRsOff);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r0 = 8 * (tile0 + j) + 2 * (lane & 3);
       rs0[j] = rs[r0];
       rs1[j] = rs[r0 + 1];
-      if constexpr (F == kPageInt4) {
-#pragma unroll
-        for (int g = 0; g < D / kGroupDims; ++g) {
-          c0[j][g] = qsum[r0 * (D / kGroupDims) + g];
-          c1[j][g] = qsum[(r0 + 1) * (D / kGroupDims) + g];
-        }
-      }
+      if constexpr (kRegs && F == kPageInt4) o[j] = obase[j * 32];
       if constexpr (kRegs) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) f[j][k] = base[(j * (D / 16) + k) * 32];
@@ -237,30 +291,57 @@ struct QOperand {
     else
       return base[(j * (D / 16) + k) * 32];
   }
+  __device__ __forceinline__ uint2 offset(int j) const {
+    if constexpr (kRegs)
+      return o[j];
+    else
+      return obase[j * 32];
+  }
 };
 
-__device__ __forceinline__ void mma_f16_16816_c(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                                float c0, float c1, float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+// D = A * B + C and D += A * B on f16 operands; without side effects, so that the compiler
+// may move them.
+__device__ __forceinline__ void mma_f16_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1, float c0,
+                                          float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
-// Log2-domain scores of a staged K page: lane (gid = lane/4, q = lane%4) gets
+// Scores of a staged K page, to be multiplied by the rows' rs: lane (gid = lane/4, q = lane%4) gets
 // t[j] = S^T[gid][2q], [gid][2q+1], [gid+8][2q], [gid+8][2q+1] of n-tile j.
 template <int F, int D, int NT, bool kRegs>
 __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, uint32_t koff,
                                             const QOperand<F, D, NT, kRegs>& q, int lane) {
   if constexpr (F == kPageInt4) {
     using P = Page<F, D>;
-    // scales of tokens gid and gid + 8
+    // scales of tokens gid and gid + 8, and the codes' offset taken back:
+    // t = sum_g scale_g x_g
     float s0[4], s1[4];
     {
       const uint32_t a = page + P::kCodes + (lane >> 2) * P::kGroups;
-      uint32_t w0, w1;
+      uint32_t w0, w1, h0[2], h1[2];
       if constexpr (P::kGroups == 4) {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(a));
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"(a + 8 * P::kGroups));
@@ -268,13 +349,19 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
         asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w0) : "r"(a));
         asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w1) : "r"(a + 8 * P::kGroups));
       }
-      e4m3x4_to_f32(w0, s0);
-      e4m3x4_to_f32(w1, s1);
+      e4m3x4_to_f16x4(w0, h0[0], h0[1]);
+      e4m3x4_to_f16x4(w1, h1[0], h1[1]);
+      const bool odd = P::kGroups == 4 && (lane & 1);
+      const uint32_t a0 = odd ? h0[1] : h0[0], a1 = odd ? h1[1] : h1[0];
+      const uint32_t a2 = f16x2_mul(a0, 0x10001000u), a3 = f16x2_mul(a1, 0x10001000u);   // 2^-11
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const uint2 b = q.offset(j);
+        mma_f16_c(t[j], a0, a1, a2, a3, b.x, b.y, 0.f, 0.f, 0.f, 0.f);
+      }
+      f16x4_to_f32(h0, s0);
+      f16x4_to_f32(h1, s1);
     }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[j][e] = 0.f;
 #pragma unroll
     for (int g2 = 0; g2 < P::kGroups; g2 += 2) {
       uint32_t w[4];
@@ -288,9 +375,9 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
         for (int j = 0; j < NT; ++j) {
           float d[4];
           const uint2 b0 = q.get(j, 2 * g), b1 = q.get(j, 2 * g + 1);
-          mma_f16_16816_c(d, x0 & kNibLo, x1 & kNibLo, y0 & kNibLo, y1 & kNibLo, b0.x, b0.y,
-                          q.c0[j][g], q.c1[j][g], q.c0[j][g], q.c1[j][g]);
-          mma_f16_16816(d, x0 & kNibHi, x1 & kNibHi, y0 & kNibHi, y1 & kNibHi, b1.x, b1.y);
+          mma_f16_c(d, x0 & kNibLo, x1 & kNibLo, y0 & kNibLo, y1 & kNibLo, b0.x, b0.y, 0.f, 0.f,
+                    0.f, 0.f);
+          mma_f16(d, x0 & kNibHi, x1 & kNibHi, y0 & kNibHi, y1 & kNibHi, b1.x, b1.y);
           t[j][0] = fmaf(d[0], s0[g], t[j][0]);
           t[j][1] = fmaf(d[1], s0[g], t[j][1]);
           t[j][2] = fmaf(d[2], s1[g], t[j][2]);
@@ -313,7 +400,7 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const uint2 b = q.get(j, k);
-          mma_bf16_16816(k & 1 ? u[j] : t[j], a0, a1, a2, a3, b.x, b.y);
+          mma_bf16(k & 1 ? u[j] : t[j], a0, a1, a2, a3, b.x, b.y);
         }
       }
     } else {
@@ -329,7 +416,7 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             const uint2 b = q.get(j, k + h);
-            mma_f16_16816(h ? u[j] : t[j], a0, a1, a2, a3, b.x, b.y);
+            mma_f16(h ? u[j] : t[j], a0, a1, a2, a3, b.x, b.y);
           }
         }
       }
@@ -338,13 +425,6 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[j][e] += u[j][e];
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    t[j][0] *= q.rs0[j];
-    t[j][1] *= q.rs1[j];
-    t[j][2] *= q.rs0[j];
-    t[j][3] *= q.rs1[j];
   }
 }
 

@@ -77,7 +77,9 @@ def test_attention_arguments(lib):
 
 def test_workspace_sizes(lib):
     size = lib.pa_int4_workspace_size
-    assert size(64, 32, 8, 1, 512, 128, 16, 0, 0) == 0                # whole sequences
+    assert size(64, 32, 8, 1, 256, 128, 16, 0, 0) == 0                # whole sequences
+    assert size(64, 32, 8, 1, 512, 128, 16, 512, 0) == 0
+    assert size(64, 30, 8, 1, 4096, 128, 16, 0, 0) == 0               # heads do not divide
     assert size(0, 32, 8, 1, 512, 128, 16, 0, 0) == 0
     assert size(4, 32, 8, 1, 16384, 128, 16, 0, 0) > 0
     # a window needs no more than the entries it spans

@@ -42,17 +42,25 @@ class Dev:
                                  self.lens, scale=self.c.scale, **new, **kw)
 
 
-def bound(c, k, v, ref, mag):
+def bound(c, k, v, ref, mag, window):
     """Largest error the roundings allow.  Output: half a bf16 step, 2^-8 of it.  A weight is
-    rounded to f16 (2^-11), times an E4M3 scale rounded again (2^-11); scores err by fp32
-    accumulation, at most 2^-20 of sum |q k|, and so does a weight (exp).  Below 2^-14 of a
-    row's reference weight (the largest weight is at least 1) a rounding is 2^-25 absolute,
-    before the scale and after it, times codes up to 7 and the head scale."""
+    rounded to f16 (2^-11), times an E4M3 scale rounded again (2^-11); the codes enter as u = value
+    / (scale head_scale) + 8 and the 8 is taken back with the weight times the scale unrounded,
+    so the second rounding also counts for 8 scale head_scale: 2^-11 * 8 * sum_j p_j s_j.  The
+    weights' sum is that of the rounded weights.  Scores err by fp32 accumulation, at most
+    2^-20 of sum |q k|, and so does a weight (exp).  Below 2^-14 of a row's reference weight (the
+    largest weight is at least 1) a rounding is 2^-25 absolute, before the scale and after it,
+    times codes up to 15 and the head scale."""
     keys = [[c.rows(k, b, g, int(n), "k") for g in range(c.Hkv)] for b, n in enumerate(c.lens)]
     score = 2.0 ** -20 * c.score_size(keys)
-    s_max = np.nanmax(F.decode(Q4.unpack(v, c.D)[1]))
-    small = int(c.lens.max()) * 2.0 ** -25 * 7 * (s_max + 1) * float(c.v_scale.max())
-    return 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 2.0 ** -16 + score) * mag + small
+    sc = Q4.unpack(v, c.D)[1]
+    s_max = np.nanmax(F.decode(sc))
+    small = int(c.lens.max()) * 2.0 ** -25 * 15 * (s_max + 1) * float(c.v_scale.max())
+    # sum_j p_j s_j: attention over the values of code 9 (value = scale)
+    nine = Q4.pack(np.full((*sc.shape[:-1], c.D), 9, dtype=np.uint8), sc)
+    step, _ = Q4.attention(c.q, k, nine, c.k_scale, c.v_scale, c.tables, c.lens, c.scale, window)
+    return (2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 2.0 ** -16 + score) * mag +
+            2.0 ** -11 * 8 * step + small)
 
 
 def check(out, c, k=None, v=None, window=0):
@@ -60,7 +68,7 @@ def check(out, c, k=None, v=None, window=0):
     ref, mag = Q4.attention(c.q, k, v, c.k_scale, c.v_scale, c.tables, c.lens, c.scale, window)
     got = out.float().cpu().double().numpy()
     assert np.isfinite(got).all()
-    over = np.abs(got - ref) - bound(c, k, v, ref, mag)
+    over = np.abs(got - ref) - bound(c, k, v, ref, mag, window)
     assert over.max() <= 0, f"error exceeds its bound by {over.max():.3e}"
     return got, ref
 
