@@ -405,9 +405,9 @@ Int4Plan int4_plan(int num_seqs, int hq, int hkv, int T, int span, int head_dim,
   const int rows = hq / hkv * T;
   const Attn4Tile tile = attn4_tile(rows);
   const long long jobs = static_cast<long long>(num_seqs) * hkv * tile.ntw;
-  const long long all = jobs * pages;
+  const long long all = jobs * (pages + 3);      // list entries at most
   pl.flat = partition_size == 0 && scratch && pages > kInt4WholePages &&
-            num_seqs <= kInt4FlatSeqs && all < (1ll << 31);
+            num_seqs <= kInt4FlatSeqs && all < (1ll << 30);
   if (pl.flat) {
     pl.workers = static_cast<int>(std::min<long long>(kAttn4Sms * tile.ctas * 4,
                                                       (all + kInt4MinShare - 1) / kInt4MinShare));

@@ -36,14 +36,11 @@ struct Cfg4 {
 template <int D, class C>
 struct Smem4 {
   using P = Page<kPageInt4, D>;
-  using Q = QTile<kPageInt4, D, C::kRows>;
   static constexpr int kPairBytes = 2 * P::kBytes;          // a K page, then its V page
   static constexpr int kStageBytes = C::TP * kPairBytes;
-  // Query operands that go to registers before the ring's last stage is first filled lie there.
-  static constexpr bool kQInRing = C::kQRegs && Q::kBytes <= kStageBytes;
   static constexpr int kRingBytes = C::STAGES * kStageBytes;
-  static constexpr int kQOff = kQInRing ? kRingBytes - kStageBytes : kRingBytes;
-  static constexpr int kWarpBytes = kRingBytes + (kQInRing ? 0 : (Q::kBytes + 15) / 16 * 16);
+  static constexpr int kQBytes = C::kQRegs ? 0 : C::NT * QTileSmem<kPageInt4, D>::kBytes;
+  static constexpr int kWarpBytes = kRingBytes + kQBytes;
   static constexpr int kBytes = C::kWarps * kWarpBytes;
   static_assert(kStageBytes % 16 == 0 && kWarpBytes % 16 == 0, "16-byte copies");
 };
@@ -63,23 +60,34 @@ constexpr int kSetup = 3;
 // List entries of a pair with nb pages: its setup, then its pages.
 __device__ __forceinline__ int pair_entries(int nb) { return nb > 0 ? nb + kSetup : 0; }
 
-// List entries of all sequences together (one head), over a warp.
-__device__ __forceinline__ int all_entries(const AttnParams& p, int lane, bool report) {
-  int sum = 0;
-  bool bad = false;
-  for (int b = lane; b < p.num_seqs; b += 32) {
-    int first;
-    const int L = p.context_lens[b];
-    sum += pair_entries(visible_pages(p, L, &first));
-    bad |= L < p.T || L > p.max_ctx;
+// The list over all sequences (one head): the entries of all, and of those before sequence
+// `upto`.  A warp; kKeep chunks of 32 lengths are in flight at once.
+constexpr int kKeep = 8;
+__device__ __forceinline__ void count_entries(const AttnParams& p, int lane, int upto, int& all,
+                                              int& before) {
+  all = before = 0;
+  for (int base = 0; base < p.num_seqs; base += 32 * kKeep) {
+    int L[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+      const int b = base + 32 * k + lane;
+      L[k] = b < p.num_seqs ? p.context_lens[b] : p.T - 1;   // no pages
+    }
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+      int first;
+      const int n = pair_entries(visible_pages(p, L[k], &first));
+      all += n;
+      if (base + 32 * k + lane < upto) before += n;
+    }
   }
-  if (report && bad) atomicOr(&g_pa_err, kErrBounds);
-  return __reduce_add_sync(0xffffffffu, sum);
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
 }
 
 // Entries per run: everything split evenly over the workers, but at least min_share.
-__device__ __forceinline__ int run_entries(const Attn4Params& p, long long total) {
-  return max(p.min_share, static_cast<int>((total + p.workers - 1) / p.workers));
+__device__ __forceinline__ int run_entries(const Attn4Params& p, int total) {
+  return max(p.min_share, (total + p.workers - 1) / p.workers);
 }
 
 // base + page * stride in one wide multiply-add.
@@ -118,42 +126,63 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   // Flat: entries [f, f_end) of the list; b is found by adding up the sequences before it,
   // `entry` counts from the pair's first entry.
   // Units: u, u + workers, ...
-  long long f = 0, f_end = 0, f0 = 0;
+  int f = 0, f_end = 0, f0 = 0;
   int b = 0, job = 0, entry = 0, nb = 0, first = 0, L = 0;
   if constexpr (kFlat) {
-    const long long total = static_cast<long long>(all_entries(p, lane, worker == 0)) * heads;
+    // The first 32 * kKeep lengths stay in registers between the sum and the search.
+    int len[kKeep], sum = 0;
+    bool invalid = false;
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      len[k] = 32 * k + lane < p.num_seqs ? p.context_lens[32 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+      int skip;
+      sum += pair_entries(visible_pages(p, len[k], &skip));
+      invalid |= 32 * k + lane < p.num_seqs && (len[k] < T || len[k] > p.max_ctx);
+    }
+    for (int i = 32 * kKeep + lane; i < p.num_seqs; i += 32) {
+      int skip;
+      const int x = p.context_lens[i];
+      sum += pair_entries(visible_pages(p, x, &skip));
+      invalid |= x < T || x > p.max_ctx;
+    }
+    if (invalid && worker == 0) atomicOr(&g_pa_err, kErrBounds);
+    const int total = __reduce_add_sync(0xffffffffu, sum) * heads;
     const int share = run_entries(p, total);
-    f = f0 = static_cast<long long>(worker) * share;
+    if (static_cast<long long>(worker) * share >= total) return;
+    f = f0 = worker * share;
     f_end = min(total, f + share);
-    if (f >= f_end) return;
-    long long before = 0;                    // entries of the sequences before b, all heads
-    for (int base = 0;; base += 32) {
-      int fl = 0, Ll = 0;
-      if (base + lane < p.num_seqs) Ll = p.context_lens[base + lane];
-      const int mine = base + lane < p.num_seqs ? visible_pages(p, Ll, &fl) : 0;
-      int sum = pair_entries(mine);
+    int before = 0;                          // entries of the sequences before b, all heads
+    bool found = false;
+    auto search = [&](int base, int Ll) {
+      int fl, mine = visible_pages(p, Ll, &fl);
+      int run = pair_entries(mine);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
+        const int y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
       }
-      const long long upto = before + static_cast<long long>(sum) * heads;
+      const int upto = before + run * heads;
       const unsigned past = __ballot_sync(0xffffffffu, upto > f);
-      if (past != 0) {                       // total > f: some chunk ends past it
-        const int at = __ffs(past) - 1;
-        b = base + at;
-        nb = __shfl_sync(0xffffffffu, mine, at);
-        first = __shfl_sync(0xffffffffu, fl, at);
-        L = __shfl_sync(0xffffffffu, Ll, at);
-        const int ne = pair_entries(nb);
-        const long long start =
-            __shfl_sync(0xffffffffu, upto, at) - static_cast<long long>(ne) * heads;
-        job = static_cast<int>((f - start) / ne);
-        entry = static_cast<int>((f - start) % ne);
-        break;
-      }
       before = __shfl_sync(0xffffffffu, upto, 31);
-    }
+      if (past == 0) return;
+      found = true;
+      const int at = __ffs(past) - 1;
+      b = base + at;
+      nb = __shfl_sync(0xffffffffu, mine, at);
+      first = __shfl_sync(0xffffffffu, fl, at);
+      L = __shfl_sync(0xffffffffu, Ll, at);
+      const int ne = pair_entries(nb);
+      const int from = f - (__shfl_sync(0xffffffffu, upto, at) - ne * heads);
+      job = from / ne;
+      entry = from % ne;
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (!found && 32 * k < p.num_seqs) search(32 * k, len[k]);
+    for (int base = 32 * kKeep; !found; base += 32)   // f < total: some chunk ends past it
+      search(base, base + lane < p.num_seqs ? p.context_lens[base + lane] : -1);
   }
   long long u = worker;
 
@@ -162,7 +191,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     int taken = 0;                           // list entries of this segment
     bool direct;
     if constexpr (kFlat) {
-      taken = static_cast<int>(min(static_cast<long long>(pair_entries(nb) - entry), f_end - f));
+      taken = min(pair_entries(nb) - entry, f_end - f);
       page = max(0, entry - kSetup);
       n = max(0, entry + taken - kSetup) - page;
       direct = n == nb;
@@ -185,6 +214,12 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     if (n > 0) {
     const int g = job / NTW, row0 = (job % NTW) * C::kRows;
     const int pg0 = first + page;
+
+    // the query rows, on their way while the block ids are fetched
+    QTileRaw<kPageInt4, D> raw[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      load_q_raw(raw[j], p.q, b, g, T, G, p.Hq, row0 + 8 * j, nrows, lane);
 
     // -------------------------------------------------------------- page stream
     const size_t head_off = static_cast<size_t>(g) * P::kBytes;
@@ -236,12 +271,26 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue();
 
-    uint8_t* qt = smem + Sm::kQOff;
-    load_q_tile<kPageInt4, D, C::kRows, 8>(qt, p.q, b, g, T, G, p.Hq, row0, nrows, p.scale_log2,
-                                           p.k_scale[g], lane, 0, 1);
-    __syncwarp();
     QOperand<kPageInt4, D, NT, C::kQRegs> qo;
-    qo.template load<C::kRows>(qt, 0, lane);
+    {
+      const float k_scale = p.k_scale[g];
+      uint8_t* qt = smem + Sm::kRingBytes;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (C::kQRegs) {
+          make_q_tile(qo.tile[j], raw[j], p.scale_log2, k_scale, lane);
+          qo.rs0[j] = qo.tile[j].rs0;
+          qo.rs1[j] = qo.tile[j].rs1;
+        } else {
+          QTile<kPageInt4, D> tile;
+          make_q_tile(tile, raw[j], p.scale_log2, k_scale, lane);
+          put_q_tile(qt + j * QTileSmem<kPageInt4, D>::kBytes, tile, lane);
+          qo.rs0[j] = tile.rs0;
+          qo.rs1[j] = tile.rs1;
+        }
+      }
+      if constexpr (!C::kQRegs) qo.base = qt + lane * 8;   // each lane reads what it wrote
+    }
 
     // Softmax state of rows 2q4, 2q4 + 1 of each n-tile: minus the reference m (log2
     // domain) and, in units of the raw scores, the value a score must pass to move m
@@ -511,24 +560,19 @@ __global__ void __launch_bounds__(32 * W) attn4_merge_kernel(const Attn4Params p
   const int job = static_cast<int>(blockIdx.x / live % heads);
   const int b = static_cast<int>(blockIdx.x / live / heads);
   const int row = job % ntw * tile_rows + r;
-  int first, before = 0, all = 0;
-  for (int i = lane; i < p.num_seqs; i += 32) {
-    const int n = pair_entries(visible_pages(p, p.context_lens[i], &first));
-    all += n;
-    if (i < b) before += n;
-  }
-  all = __reduce_add_sync(0xffffffffu, all);
-  before = __reduce_add_sync(0xffffffffu, before);
-  const int nb = visible_pages(p, p.context_lens[b], &first);
-  const int share = run_entries(p, static_cast<long long>(all) * heads);
+  int first, before, all;
+  const int mine = p.context_lens[b];
+  count_entries(p, lane, b, all, before);
+  const int nb = visible_pages(p, mine, &first);
+  const int share = run_entries(p, all * heads);
   const int ne = pair_entries(nb);
-  const long long f0 = static_cast<long long>(before) * heads + static_cast<long long>(job) * ne;
+  const int f0 = before * heads + job * ne;
   // the workers of its first and its last page
-  const long long w0 = (f0 + kSetup) / share, w1 = (f0 + ne - 1) / share;
+  const int w0 = (f0 + kSetup) / share, w1 = (f0 + ne - 1) / share;
   // every CTA waits, so that this grid does not complete before the one it follows
   grid_dependency_wait();
   if (nb == 0 || w0 == w1 || row >= p.G * p.T) return;
-  const int parts = static_cast<int>(w1 - w0) + 1;
+  const int parts = w1 - w0 + 1;
   auto slot = [&](int i) {
     const bool second = i == 0 && f0 > w0 * share;       // the run's last pair, not its first
     return (static_cast<size_t>(w0 + i) * 2 + (second ? 1 : 0)) * tile_rows + r;

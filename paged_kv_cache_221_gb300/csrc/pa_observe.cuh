@@ -23,7 +23,7 @@ template <int F, int D, class C>
 struct ObserveSmem {
   using P = Page<F, D>;
   static constexpr int kQOff = C::kWarps * C::STAGES * P::kBytes;
-  static constexpr int kMlOff = kQOff + QTile<F, D, C::kRows>::kBytes;
+  static constexpr int kMlOff = kQOff + C::kRows / 8 * QTileSmem<F, D>::kBytes;
   static constexpr int kBytes = kMlOff + C::kWarps * 8 * C::NT * 8;
 };
 
@@ -75,11 +75,16 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) observe_scores_kernel(co
   for (int i = 0; i < S - 1; ++i) issue(i);
 
   uint8_t* qt = smem + Sm::kQOff;
-  load_q_tile<F, D, C::kRows, 2>(qt, p.q, b, g, T, G, p.Hq, 0, nrows, p.scale_log2,
-                                 F == kPageBf16 ? 1.f : p.k_scale[g], lane, warp, C::kWarps);
+  for (int j = warp; j < NT * NTW; j += C::kWarps) {
+    QTileRaw<F, D> raw;
+    QTile<F, D> tile;
+    load_q_raw(raw, p.q, b, g, T, G, p.Hq, 8 * j, nrows, lane);
+    make_q_tile(tile, raw, p.scale_log2, F == kPageBf16 ? 1.f : p.k_scale[g], lane);
+    put_q_tile(qt + j * QTileSmem<F, D>::kBytes, tile, lane);
+  }
   __syncthreads();
   QOperand<F, D, NT, C::kQRegs> qo;
-  qo.template load<C::kRows>(qt, col * NT, lane);
+  qo.load(qt + col * NT * QTileSmem<F, D>::kBytes, lane);
 
   int lim0[NT], lim1[NT];
   float m0[NT], m1[NT], l0[NT], l1[NT];

@@ -112,190 +112,201 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
 
 constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
 
-// Query rows in shared memory, as B operands of the score tiles.
-//   frag  [n-tile][16-dim k step][lane] two registers: row 8 n-tile + lane/4, the
-//         dims that the K format puts into lane%4's A registers
-//   off   [n-tile][lane] INT4: two registers of a k step over the groups that takes the
-//         codes' offset back, with the token's scales as the A operand: row n's
-//         x_g = -8 * 2^-24 * (sum of group g's operands) as f16 high part (k = g) and
-//         2^11 times the f16 residual (k = g + 8; A is 2^-11 times the scale there)
-//   rs    [row] positive factor from a score accumulator to the log2-domain score (the
-//         sign of the softmax scale goes into the operands)
+// Query rows as B operands of the score tiles.  Lane (gid = lane/4, q = lane%4) of a warp
+// holds, for row gid of an n-tile of 8 rows, the head dims that the K format puts
+// into lane q's A registers, so a warp loads a tile straight into operand order:
+//   bf16  16-dim k step k: dims 16k + 2q, +1 and 16k + 2q + 8, +9
+//   FP8   16-dim k step k: dims 16k + 4q .. + 3
+//   INT4  group g: dims 32g + 8q .. + 7 (nibbles 0 .. 7 of the lane's word): the even
+//         nibbles in k step 2g, the odd ones in 2g + 1; a register pairs nibbles i, i + 4
 // bf16 pages take Q as it is.  FP8 and INT4 pages take it in f16: each row is
 // scaled by a power of two so that its largest magnitude lies in [2^13, 2^14),
 // which keeps every value within 2^-24 of the row's largest exact (the odd dims of
 // INT4 pages, divided by 16, within 2^-20).
-template <int F, int D, int ROWS>
-struct QTile {
-  static constexpr int kFragBytes = (ROWS / 8) * (D / 16) * 32 * 8;
-  static constexpr int kOffOff = kFragBytes;
-  static constexpr int kOffBytes = F == kPageInt4 ? ROWS / 8 * 32 * 8 : 0;
-  static constexpr int kRsOff = kOffOff + kOffBytes;
-  static constexpr int kBytes = kRsOff + ROWS * 4;
+//   rs0, rs1  positive factors from the score accumulators of rows 2q, 2q + 1 to log2-domain
+//             scores (the sign of the softmax scale goes into the operands)
+//   off       INT4: operand of a k step over the groups that takes the codes' offset back,
+//             with the token's scales as the A operand: x_g = -8 * 2^-24 * (sum of group g's
+//             operands) as f16 high part (k = g) and 2^11 times the f16 residual (k = g +
+//             8; A is 2^-11 times the scale there)
+template <int F, int D>
+struct QTileRaw {
+  uint32_t w[D / 8];                         // the lane's D / 4 values
 };
 
-// Position, in halves, of head dim d of row n within the frag array.
 template <int F, int D>
-__device__ __forceinline__ int q_frag_pos(int n, int d) {
-  int step, lane4, e;                        // k step, lane % 4, element 0..3 of the two registers
+struct QTile {
+  uint2 f[D / 16];
+  uint2 off;
+  float rs0, rs1;
+};
+
+// Bytes of one n-tile's operands in shared memory: [k step][lane], off, then rs.
+template <int F, int D>
+struct QTileSmem {
+  static constexpr int kOff = (D / 16) * 32 * 8;
+  static constexpr int kRs = kOff + (F == kPageInt4 ? 32 * 8 : 0);
+  static constexpr int kBytes = kRs + 32 * 8;
+};
+
+// Row n = t * G + hl of (sequence b, kv head g); rows from nrows on are zero.
+template <int F, int D>
+__device__ __forceinline__ void load_q_raw(QTileRaw<F, D>& raw, const void* q, int b, int g, int T,
+                                           int G, int Hq, int row0, int nrows, int lane) {
+  const int n = row0 + (lane >> 2), q4 = lane & 3;
+  const bool live = n < nrows;
+  const size_t row = (static_cast<size_t>(b) * T + (live ? n / G : 0)) * Hq + g * G +
+                     (live ? n % G : 0);
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(q) + row * D;
+#pragma unroll
+  for (int k = 0; k < D / 8; ++k) raw.w[k] = 0u;
+  if (!live) return;
   if constexpr (F == kPageBf16) {
-    step = d >> 4;
-    const int x = d & 15;
-    lane4 = (x & 7) >> 1;
-    e = (x & 1) + 2 * (x >> 3);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      raw.w[2 * k] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q4);
+      raw.w[2 * k + 1] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q4 + 8);
+    }
   } else if constexpr (F == kPageFp8) {
-    step = d >> 4;
-    lane4 = (d & 15) >> 2;
-    e = d & 3;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint2 v = *reinterpret_cast<const uint2*>(src + 16 * k + 4 * q4);
+      raw.w[2 * k] = v.x;
+      raw.w[2 * k + 1] = v.y;
+    }
   } else {
-    // word lane4 of the group's 16-byte chunk: nibble i; even nibbles in the first
-    // of the group's two k steps, odd ones in the second; a register pairs nibbles
-    // i and i + 4
-    const int i = d & 7;
-    step = 2 * (d >> 5) + (i & 1);
-    lane4 = (d & 31) >> 3;
-    e = (i & 2) + (i >> 2);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 32 * k + 8 * q4);
+      raw.w[4 * k] = v.x;
+      raw.w[4 * k + 1] = v.y;
+      raw.w[4 * k + 2] = v.z;
+      raw.w[4 * k + 3] = v.w;
+    }
   }
-  return ((((n >> 3) * (D / 16) + step) * 32) + (n & 7) * 4 + lane4) * 4 + e;
 }
 
-// Query rows row0 .. row0 + ROWS - 1 of (sequence b, kv head g) as operands; row n = t * G +
-// hl, rows past nrows are zero.  Warp `part` of `parts` writes every parts-th run of RC
-// rows (all its loads in flight at once); a barrier among the warps follows.
-template <int F, int D, int ROWS, int RC>
-__device__ __forceinline__ void load_q_tile(uint8_t* qt, const void* q, int b, int g, int T, int G,
-                                            int Hq, int row0, int nrows, float scale_log2,
-                                            float k_scale, int lane, int part, int parts) {
-  using Q = QTile<F, D, ROWS>;
-  constexpr int DL = D / 32;                 // consecutive dims per lane
-  static_assert(ROWS % RC == 0, "whole runs");
-  uint16_t* frag = reinterpret_cast<uint16_t*>(qt);
-  uint16_t* off = reinterpret_cast<uint16_t*>(qt + Q::kOffOff);
-  float* rs = reinterpret_cast<float*>(qt + Q::kRsOff);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  return half2_bits(__floats2half2_rn(lo, hi));
+}
+
+template <int F, int D>
+__device__ __forceinline__ void make_q_tile(QTile<F, D>& t, const QTileRaw<F, D>& raw,
+                                            float scale_log2, float k_scale, int lane) {
   const float sign = scale_log2 * k_scale < 0.f ? -1.f : 1.f;
-  const float size = fabsf(scale_log2 * k_scale);
-  const int d0 = lane * DL;
-  for (int n0 = RC * part; n0 < ROWS; n0 += RC * parts) {
-    uint32_t raw[RC][DL / 2];
+  float rs = fabsf(scale_log2 * k_scale);
+  t.off = make_uint2(0u, 0u);
+  if constexpr (F == kPageBf16) {
+    const uint32_t flip = sign < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-    for (int r = 0; r < RC; ++r) {
-      const int n = row0 + n0 + r;
+    for (int k = 0; k < D / 16; ++k)
+      t.f[k] = make_uint2(raw.w[2 * k] ^ flip, raw.w[2 * k + 1] ^ flip);
+  } else {
+    uint32_t mb = 0;                         // largest magnitude of the row, as bf16 bits
 #pragma unroll
-      for (int k = 0; k < DL / 2; ++k) raw[r][k] = 0u;
-      if (n < nrows) {
-        const size_t row = (static_cast<size_t>(b) * T + n / G) * Hq + g * G + n % G;
-        const uint32_t* src =
-            reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(q) + row * D + d0);
-        if constexpr (DL == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(src);
-          raw[r][0] = v.x;
-          raw[r][1] = v.y;
-        } else {
-          raw[r][0] = *src;
+    for (int k = 0; k < D / 8; ++k)
+      mb = max(mb, max(raw.w[k] & 0x7fffu, (raw.w[k] >> 16) & 0x7fffu));
+    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+    // its exponent, kept where 2^(13 - e) and its inverse are normal
+    int e = static_cast<int>(mb >> 7) - 127;
+    e = max(-100, min(e, 100));
+    const float up = sign * __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+    rs *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+    if constexpr (F == kPageFp8) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        t.f[k] = make_uint2(pack_f16(bf16_lo(raw.w[2 * k]) * up, bf16_hi(raw.w[2 * k]) * up),
+                            pack_f16(bf16_lo(raw.w[2 * k + 1]) * up, bf16_hi(raw.w[2 * k + 1]) * up));
+    } else {
+      constexpr int NG = D / kGroupDims;
+      const float odd = up * 0.0625f;
+      float sum[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t* w = raw.w + 4 * g;   // nibbles 0,1 | 2,3 | 4,5 | 6,7
+        t.f[2 * g] = make_uint2(pack_f16(bf16_lo(w[0]) * up, bf16_lo(w[2]) * up),
+                                pack_f16(bf16_lo(w[1]) * up, bf16_lo(w[3]) * up));
+        t.f[2 * g + 1] = make_uint2(pack_f16(bf16_hi(w[0]) * odd, bf16_hi(w[2]) * odd),
+                                    pack_f16(bf16_hi(w[1]) * odd, bf16_hi(w[3]) * odd));
+        const uint32_t u[4] = {t.f[2 * g].x, t.f[2 * g].y, t.f[2 * g + 1].x, t.f[2 * g + 1].y};
+        float part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+          part[i] = x.x + x.y;
         }
+        sum[g] = (part[0] + part[1]) + 16.f * (part[2] + part[3]);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
       }
-    }
-#pragma unroll
-    for (int r = 0; r < RC; ++r) {
-      const int n = n0 + r;
-      float x[DL];
-#pragma unroll
-      for (int k = 0; k < DL; ++k)
-        x[k] = sign * ((k & 1) ? bf16_hi(raw[r][k / 2]) : bf16_lo(raw[r][k / 2]));
-      if constexpr (F == kPageBf16) {
-#pragma unroll
-        for (int k = 0; k < DL; ++k)
-          frag[q_frag_pos<F, D>(n, d0 + k)] = __bfloat16_as_ushort(__float2bfloat16_rn(x[k]));
-        if (lane == 0) rs[n] = fmaxf(size, 1e-36f);
-      } else {
-        float mx = 0.f;
-#pragma unroll
-        for (int k = 0; k < DL; ++k) mx = fmaxf(mx, fabsf(x[k]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // exponent of the row's largest magnitude, kept where 2^(13 - e) and its inverse are
-        // normal
-        int e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-        e = max(-100, min(e, 100));
-        const float up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < DL; ++k) {
-          float y = x[k] * up;
-          if (F == kPageInt4 && (k & 1)) y *= 0.0625f;
-          const __half h = __float2half_rn(y);
-          frag[q_frag_pos<F, D>(n, d0 + k)] = __half_as_ushort(h);
-          sum += __half2float(h) * ((k & 1) ? 16.f : 1.f);
-        }
-        if constexpr (F == kPageInt4) {
-          constexpr int GL = kGroupDims / DL;    // lanes of a group
-#pragma unroll
-          for (int o = GL / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float v = sum * (-8.f / 16777216.f);
-          const __half vh = __float2half_rn(v);
-          const __half vl = __float2half_rn((v - __half2float(vh)) * 2048.f);
-          uint16_t* to = off + (n >> 3) * 128 + (n & 7) * 16;   // [lane % 4][4 halves]
-          if (lane % GL == 0) {
-            const int g2 = lane / GL;
-            to[(g2 >> 1) * 4 + (g2 & 1)] = __half_as_ushort(vh);
-            to[(g2 >> 1) * 4 + (g2 & 1) + 2] = __half_as_ushort(vl);
-          } else if (lane % GL == 1 && lane / GL < 4) {
-            // the k steps' other lanes: zero
-            constexpr int kUsed = D / kGroupDims / 2;
-            if (lane / GL >= kUsed)
-              *reinterpret_cast<uint2*>(to + (lane / GL) * 4) = make_uint2(0u, 0u);
-          }
-          if constexpr (D / kGroupDims == 2) {
-            if (lane == 2 || lane == 3) *reinterpret_cast<uint2*>(to + lane * 4) = make_uint2(0u, 0u);
-          }
-        }
-        if (lane == 0)
-          rs[n] = fmaxf(size * down * (F == kPageInt4 ? 16777216.f : 1.f), 1e-36f);
+      const int q4 = lane & 3;
+      float a = sum[0], c = sum[1];
+      if constexpr (NG == 4) {
+        a = q4 == 1 ? sum[2] : a;
+        c = q4 == 1 ? sum[3] : c;
       }
+      if (q4 < NG / 2) {
+        a *= -8.f / 16777216.f;
+        c *= -8.f / 16777216.f;
+        const float ah = __half2float(__float2half_rn(a)), ch = __half2float(__float2half_rn(c));
+        t.off = make_uint2(pack_f16(ah, ch), pack_f16((a - ah) * 2048.f, (c - ch) * 2048.f));
+      }
+      rs *= 16777216.f;
     }
   }
+  rs = fmaxf(rs, 1e-36f);
+  t.rs0 = __shfl_sync(0xffffffffu, rs, (lane & 3) * 8);        // from lanes of rows 2q, 2q + 1
+  t.rs1 = __shfl_sync(0xffffffffu, rs, (lane & 3) * 8 + 4);
+}
+
+template <int F, int D>
+__device__ __forceinline__ void put_q_tile(uint8_t* to, const QTile<F, D>& t, int lane) {
+  using S = QTileSmem<F, D>;
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) reinterpret_cast<uint2*>(to)[k * 32 + lane] = t.f[k];
+  if constexpr (F == kPageInt4) reinterpret_cast<uint2*>(to + S::kOff)[lane] = t.off;
+  reinterpret_cast<float2*>(to + S::kRs)[lane] = make_float2(t.rs0, t.rs1);
 }
 
 // The query operands one warp needs for its n-tiles, in registers or (kRegs = false)
-// read from shared memory at every page.
+// read from shared memory (consecutive QTileSmem tiles) at every page.
 template <int F, int D, int NT, bool kRegs>
 struct QOperand {
-  uint2 f[kRegs ? NT : 1][kRegs ? D / 16 : 1];
-  uint2 o[kRegs ? NT : 1];
+  QTile<F, D> tile[kRegs ? NT : 1];
   float rs0[NT], rs1[NT];
-  const uint2* base;
-  const uint2* obase;
+  const uint8_t* base;
 
-  template <int ROWS>
-  __device__ __forceinline__ void load(const uint8_t* qt, int tile0, int lane) {
-    using Q = QTile<F, D, ROWS>;
-    base = reinterpret_cast<const uint2*>(qt) + static_cast<size_t>(tile0) * (D / 16) * 32 + lane;
-    obase = reinterpret_cast<const uint2*>(qt + Q::kOffOff) + tile0 * 32 + lane;
-    const float* rs = reinterpret_cast<const float*>(qt + Q::kRsOff);
+  // From shared memory that put_q_tile filled.
+  __device__ __forceinline__ void load(const uint8_t* qt, int lane) {
+    using S = QTileSmem<F, D>;
+    base = qt + lane * 8;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int r0 = 8 * (tile0 + j) + 2 * (lane & 3);
-      rs0[j] = rs[r0];
-      rs1[j] = rs[r0 + 1];
-      if constexpr (kRegs && F == kPageInt4) o[j] = obase[j * 32];
+      const float2 r = *reinterpret_cast<const float2*>(base + j * S::kBytes + S::kRs);
+      rs0[j] = r.x;
+      rs1[j] = r.y;
       if constexpr (kRegs) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) f[j][k] = base[(j * (D / 16) + k) * 32];
+        for (int k = 0; k < D / 16; ++k)
+          tile[j].f[k] = *reinterpret_cast<const uint2*>(base + j * S::kBytes + k * 256);
+        if constexpr (F == kPageInt4)
+          tile[j].off = *reinterpret_cast<const uint2*>(base + j * S::kBytes + S::kOff);
       }
     }
   }
   __device__ __forceinline__ uint2 get(int j, int k) const {
     if constexpr (kRegs)
-      return f[j][k];
+      return tile[j].f[k];
     else
-      return base[(j * (D / 16) + k) * 32];
+      return *reinterpret_cast<const uint2*>(base + j * QTileSmem<F, D>::kBytes + k * 256);
   }
   __device__ __forceinline__ uint2 offset(int j) const {
     if constexpr (kRegs)
-      return o[j];
+      return tile[j].off;
     else
-      return obase[j * 32];
+      return *reinterpret_cast<const uint2*>(base + j * QTileSmem<F, D>::kBytes +
+                                             QTileSmem<F, D>::kOff);
   }
 };
 
