@@ -428,22 +428,41 @@ Int4Plan int4_plan(int num_seqs, int hq, int hkv, int T, int span, int head_dim,
 }
 
 // ---------------------------------------------------------------- accumulated weights
-// Scratch: [(m, l) per chunk and row][scores], 256-byte aligned.
+// Scratch: [(m, l) of every piece and row][scores], 256-byte aligned.  Balanced runs, except
+// for batches so large that every warp reading all lengths would show.
+constexpr int kObserveUnitPages = 64;
+
 struct ObservePlan {
-  int ppb, max_chunks, row_stride;
+  bool flat;
+  int workers, ppb, max_parts, max_entries, tile_rows, ntw;
   size_t off_scores, bytes;
 };
 
 ObservePlan observe_plan(int num_seqs, int hq, int hkv, int T, int max_ctx) {
-  ObservePlan pl;
+  ObservePlan pl{};
   const int rows = hq / hkv * T;
-  const int max_blocks = ceil_div(max_ctx, kBlockSize);
-  pl.ppb = 64;
-  pl.max_chunks = ceil_div(max_blocks, pl.ppb);
-  pl.row_stride = (rows + 1) & ~1;
-  const size_t pairs = static_cast<size_t>(num_seqs) * hkv;
-  pl.off_scores = round256(pairs * pl.max_chunks * rows * 8);
-  pl.bytes = pl.off_scores + round256(pairs * max_ctx * pl.row_stride * 4);
+  const int pages = ceil_div(max_ctx, kBlockSize);
+  const Attn4Tile tile = observe_tile(rows);
+  const long long jobs = static_cast<long long>(num_seqs) * hkv * tile.ntw;
+  const long long all = jobs * (pages + 3);
+  pl.tile_rows = 8 * tile.nt;
+  pl.ntw = tile.ntw;
+  pl.max_entries = pages * kBlockSize;
+  pl.flat = num_seqs <= kInt4FlatSeqs && all < (1ll << 30);
+  pl.ppb = kObserveUnitPages;
+  pl.max_parts = ceil_div(pages, pl.ppb);
+  size_t slots;
+  if (pl.flat) {
+    pl.workers = static_cast<int>(std::min<long long>(kAttn4Sms * tile.ctas * 4,
+                                                      (all + kInt4MinShare - 1) / kInt4MinShare));
+    slots = static_cast<size_t>(pl.workers) * 2;
+  } else {
+    pl.workers = static_cast<int>(std::min<long long>(jobs * pl.max_parts, 1 << 30));
+    slots = static_cast<size_t>(jobs) * pl.max_parts;
+  }
+  pl.off_scores = round256(slots * pl.tile_rows * sizeof(float2));
+  pl.bytes = pl.off_scores + round256(static_cast<size_t>(num_seqs) * hkv * rows * pl.max_entries *
+                                      sizeof(float));
   return pl;
 }
 
@@ -934,8 +953,6 @@ pa_status pa_accumulate_weights(const float* weights, float* weights_out, int32_
   const ObservePlan plan = observe_plan(num_seqs, num_q_heads, num_kv_heads, T, max_context_len);
   if (!workspace || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
-  const long long units = static_cast<long long>(plan.max_chunks) * num_kv_heads * num_seqs;
-  if (units >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
 
   ObserveParams p{};
   p.q = q;
@@ -957,19 +974,22 @@ pa_status pa_accumulate_weights(const float* weights, float* weights_out, int32_
   p.Hkv = num_kv_heads;
   p.G = G;
   p.num_blocks = num_blocks;
+  p.flat = plan.flat;
+  p.workers = plan.workers;
+  p.min_share = kInt4MinShare;
   p.ppb = plan.ppb;
-  p.max_chunks = plan.max_chunks;
-  p.max_entries = max_context_len;
-  p.row_stride = plan.row_stride;
+  p.max_parts = plan.max_parts;
+  p.tile_rows = plan.tile_rows;
+  p.ntw = plan.ntw;
+  p.max_entries = plan.max_entries;
   p.weight_entries = max_entries;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.decay = decay;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rows = G * T;
-  const unsigned n = static_cast<unsigned>(units);
-  cudaError_t e = kv_format == PA_KV_BF16  ? launch_observe_bf16(p, head_dim, rows, n, s)
-                  : kv_format == PA_KV_INT4 ? launch_observe_int4(p, head_dim, rows, n, s)
-                                            : launch_observe_fp8(p, head_dim, rows, n, s);
+  cudaError_t e = kv_format == PA_KV_BF16  ? launch_observe_bf16(p, head_dim, rows, s)
+                  : kv_format == PA_KV_INT4 ? launch_observe_int4(p, head_dim, rows, s)
+                                            : launch_observe_fp8(p, head_dim, rows, s);
   if (e == cudaSuccess) e = launch_observe_sum(p, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -8,18 +8,13 @@
 // (pa_pages.cuh), scales multiply score accumulators and softmax weights, and
 // everything that only an edge page needs is behind one branch.
 //
-// Balanced mode (kFlat): the pages of all (sequence, kv head) pairs form one list, cut
-// into equal runs, one for each worker that is resident at once, so that ragged
-// contexts neither leave a tail nor a second wave.  Each pair counts kSetup pages more
-// than it has, for what starting on it costs.  A pair that lies in one run is
-// written out directly; the others leave (m, l, O) partials, at most two per worker
-// (the run's first and last pair), which attn4_merge_kernel joins.
-// Unit mode: a worker takes whole (partition, sequence, kv head) units of a fixed size;
-// the split-KV merge joins the partitions.  The result of a sequence then does not
-// depend on the batch it is in.
+// Balanced mode (kFlat): runs of pa_runs.cuh.  A job that lies in one run is written out
+// directly; the others leave (m, l, O) partials, which attn4_merge_kernel joins.
+// Unit mode: units of a fixed size; the split-KV merge joins the partitions.  The result of a
+// sequence then does not depend on the batch it is in.
 #pragma once
 
-#include "pa_pages.cuh"
+#include "pa_runs.cuh"
 
 namespace pa {
 
@@ -45,57 +40,9 @@ struct Smem4 {
   static_assert(kStageBytes % 16 == 0 && kWarpBytes % 16 == 0, "16-byte copies");
 };
 
-// Pages that sequence b's query tokens can see (0 if its length is out of range).
-__device__ __forceinline__ int visible_pages(const AttnParams& p, int L, int* first) {
-  *first = 0;
-  if (L < p.T || L > p.max_ctx) return 0;
-  if (p.window > 0) *first = max(0, L - p.T - p.window + 1) / kBlockSize;
-  return (L + kBlockSize - 1) / kBlockSize - *first;
-}
-
-// What starting on a pair costs, in pages: block ids, query rows and the first pages are
-// fetched one after the other.
-constexpr int kSetup = 3;
-
-// List entries of a pair with nb pages: its setup, then its pages.
-__device__ __forceinline__ int pair_entries(int nb) { return nb > 0 ? nb + kSetup : 0; }
-
-// The list over all sequences (one head): the entries of all, and of those before sequence
-// `upto`.  A warp; kKeep chunks of 32 lengths are in flight at once.
-constexpr int kKeep = 8;
-__device__ __forceinline__ void count_entries(const AttnParams& p, int lane, int upto, int& all,
-                                              int& before) {
-  all = before = 0;
-  for (int base = 0; base < p.num_seqs; base += 32 * kKeep) {
-    int L[kKeep];
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k) {
-      const int b = base + 32 * k + lane;
-      L[k] = b < p.num_seqs ? p.context_lens[b] : p.T - 1;   // no pages
-    }
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k) {
-      int first;
-      const int n = pair_entries(visible_pages(p, L[k], &first));
-      all += n;
-      if (base + 32 * k + lane < upto) before += n;
-    }
-  }
-  all = __reduce_add_sync(0xffffffffu, all);
-  before = __reduce_add_sync(0xffffffffu, before);
-}
-
-// Entries per run: everything split evenly over the workers, but at least min_share.
-__device__ __forceinline__ int run_entries(const Attn4Params& p, int total) {
-  return max(p.min_share, (total + p.workers - 1) / p.workers);
-}
-
-// base + page * stride in one wide multiply-add.
-__device__ __forceinline__ const uint8_t* at_page(const uint8_t* base, uint32_t page,
-                                                  uint32_t stride) {
-  const uint8_t* r;
-  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(page), "r"(stride), "l"(base));
-  return r;
+__device__ __forceinline__ RunList run_list(const Attn4Params& p, int ntw) {
+  return RunList{p.context_lens, p.num_seqs, p.T,         p.max_ctx, p.window,
+                 p.Hkv * ntw,    p.workers,  p.min_share, p.ppb,     p.max_parts};
 }
 
 template <int D, class C, bool kFlat>
@@ -110,7 +57,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   const int gid = lane >> 2, q4 = lane & 3;
   uint8_t* smem = smem_all + warp * Sm::kWarpBytes;
   const int G = p.G, T = p.T, nrows = G * T;
-  const int heads = p.Hkv * NTW;             // jobs per sequence
+  const RunList list = run_list(p, NTW);
   const int worker = blockIdx.x * C::kWarps + warp;
 
   // Per lane: its chunks within a page (chunk `lane` of K and of V, and one of the scale
@@ -122,98 +69,17 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   const uint32_t sdst = P::kCodes + 16 * (lane % SC) + (lane < SC ? 0 : P::kBytes);
   const uint32_t koff = ldsm_offset<kPageInt4, D>(lane);
 
-  // ---------------------------------------------------------------- this worker's work
-  // Flat: entries [f, f_end) of the list; b is found by adding up the sequences before it,
-  // `entry` counts from the pair's first entry.
-  // Units: u, u + workers, ...
-  int f = 0, f_end = 0, f0 = 0;
-  int b = 0, job = 0, entry = 0, nb = 0, first = 0, L = 0;
-  if constexpr (kFlat) {
-    // The first 32 * kKeep lengths stay in registers between the sum and the search.
-    int len[kKeep], sum = 0;
-    bool invalid = false;
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      len[k] = 32 * k + lane < p.num_seqs ? p.context_lens[32 * k + lane] : -1;
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k) {
-      int skip;
-      sum += pair_entries(visible_pages(p, len[k], &skip));
-      invalid |= 32 * k + lane < p.num_seqs && (len[k] < T || len[k] > p.max_ctx);
-    }
-    for (int i = 32 * kKeep + lane; i < p.num_seqs; i += 32) {
-      int skip;
-      const int x = p.context_lens[i];
-      sum += pair_entries(visible_pages(p, x, &skip));
-      invalid |= x < T || x > p.max_ctx;
-    }
-    if (invalid && worker == 0) atomicOr(&g_pa_err, kErrBounds);
-    const int total = __reduce_add_sync(0xffffffffu, sum) * heads;
-    const int share = run_entries(p, total);
-    if (static_cast<long long>(worker) * share >= total) return;
-    f = f0 = worker * share;
-    f_end = min(total, f + share);
-    int before = 0;                          // entries of the sequences before b, all heads
-    bool found = false;
-    auto search = [&](int base, int Ll) {
-      int fl, mine = visible_pages(p, Ll, &fl);
-      int run = pair_entries(mine);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += y;
-      }
-      const int upto = before + run * heads;
-      const unsigned past = __ballot_sync(0xffffffffu, upto > f);
-      before = __shfl_sync(0xffffffffu, upto, 31);
-      if (past == 0) return;
-      found = true;
-      const int at = __ffs(past) - 1;
-      b = base + at;
-      nb = __shfl_sync(0xffffffffu, mine, at);
-      first = __shfl_sync(0xffffffffu, fl, at);
-      L = __shfl_sync(0xffffffffu, Ll, at);
-      const int ne = pair_entries(nb);
-      const int from = f - (__shfl_sync(0xffffffffu, upto, at) - ne * heads);
-      job = from / ne;
-      entry = from % ne;
-    };
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (!found && 32 * k < p.num_seqs) search(32 * k, len[k]);
-    for (int base = 32 * kKeep; !found; base += 32)   // f < total: some chunk ends past it
-      search(base, base + lane < p.num_seqs ? p.context_lens[base + lane] : -1);
-  }
-  long long u = worker;
+  Cursor<kFlat> cur;
+  Segment seg;
+  bool invalid = false;
+  const bool any = cur.start(list, worker, lane, invalid);
+  if (kFlat && worker == 0 && invalid) atomicOr(&g_pa_err, kErrBounds);
+  if (!any) return;
 
-  while (true) {
-    int page, n, part = 0;                   // pages of this segment; its partition
-    int taken = 0;                           // list entries of this segment
-    bool direct;
-    if constexpr (kFlat) {
-      taken = min(pair_entries(nb) - entry, f_end - f);
-      page = max(0, entry - kSetup);
-      n = max(0, entry + taken - kSetup) - page;
-      direct = n == nb;
-    } else {
-      const long long units = static_cast<long long>(p.max_parts) * heads * p.num_seqs;
-      if (u >= units) return;
-      // partition-major: every sequence's first partition, then every second one, ...
-      part = static_cast<int>(u / (heads * p.num_seqs));
-      b = static_cast<int>(u / heads % p.num_seqs);
-      job = static_cast<int>(u % heads);
-      u += p.workers;
-      L = p.context_lens[b];
-      nb = visible_pages(p, L, &first);
-      if (nb == 0 && part == 0 && lane == 0) atomicOr(&g_pa_err, kErrBounds);
-      page = part * p.ppb;
-      n = min(p.ppb, nb - page);
-      if (n <= 0) continue;
-      direct = nb <= p.ppb;
-    }
-    if (n > 0) {
-    const int g = job / NTW, row0 = (job % NTW) * C::kRows;
-    const int pg0 = first + page;
+  while (cur.next(list, seg, invalid)) {
+    const int b = seg.b, L = seg.L, n = seg.n;
+    const int g = seg.job / NTW, row0 = (seg.job % NTW) * C::kRows;
+    const int pg0 = seg.first + seg.page;
 
     // the query rows, on their way while the block ids are fetched
     QTileRaw<kPageInt4, D> raw[NT];
@@ -272,25 +138,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     for (int i = 0; i < S - 1; ++i) issue();
 
     QOperand<kPageInt4, D, NT, C::kQRegs> qo;
-    {
-      const float k_scale = p.k_scale[g];
-      uint8_t* qt = smem + Sm::kRingBytes;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if constexpr (C::kQRegs) {
-          make_q_tile(qo.tile[j], raw[j], p.scale_log2, k_scale, lane);
-          qo.rs0[j] = qo.tile[j].rs0;
-          qo.rs1[j] = qo.tile[j].rs1;
-        } else {
-          QTile<kPageInt4, D> tile;
-          make_q_tile(tile, raw[j], p.scale_log2, k_scale, lane);
-          put_q_tile(qt + j * QTileSmem<kPageInt4, D>::kBytes, tile, lane);
-          qo.rs0[j] = tile.rs0;
-          qo.rs1[j] = tile.rs1;
-        }
-      }
-      if constexpr (!C::kQRegs) qo.base = qt + lane * 8;   // each lane reads what it wrote
-    }
+    make_q_operand(qo, raw, smem + Sm::kRingBytes, p.scale_log2, p.k_scale[g], lane);
 
     // Softmax state of rows 2q4, 2q4 + 1 of each n-tile: minus the reference m (log2
     // domain) and, in units of the raw scores, the value a score must pass to move m
@@ -486,7 +334,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
 
     // -------------------------------------------------------------- result
     const float out_scale = p.v_scale[g];
-    const size_t slot = kFlat ? static_cast<size_t>(worker) * 2 + (f == f0 ? 0 : 1) : 0;
+    const size_t slot = kFlat ? static_cast<size_t>(worker) * 2 + seg.second : 0;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float zz[2][NG];
@@ -504,8 +352,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
         const float inv = l > 0.f ? out_scale / l : 0.f;
         const size_t orow = (static_cast<size_t>(b) * T + r / G) * p.Hq + g * G + r % G;
         float* po = nullptr;
-        if (!direct) {
-          const size_t at = kFlat ? slot * C::kRows + (r - row0) : orow * p.max_parts + part;
+        if (!seg.whole) {
+          const size_t at = kFlat ? slot * C::kRows + (r - row0) : orow * p.max_parts + seg.part;
           po = p.part_o + at * D;
           if (gid == 0)
             p.part_ml[at] = make_float2(none ? -CUDART_INF_F : -(h ? nm1[j] : nm0[j]), l);
@@ -519,7 +367,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           const float4 o = make_float4(fmaf(a[0], A, -z8) * inv, fmaf(c[0], B, -z8) * inv,
                                        fmaf(a[2], A, -z8) * inv, fmaf(c[2], B, -z8) * inv);
           const int d = 32 * gr + 4 * gid;
-          if (direct)
+          if (seg.whole)
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + d) =
                 make_uint2(bf162_bits(__floats2bfloat162_rn(o.x, o.y)),
                            bf162_bits(__floats2bfloat162_rn(o.z, o.w)));
@@ -529,54 +377,39 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
       }
     }
 
-    }                                        // n > 0
-    if constexpr (kFlat) {
-      f += taken;
-      if (f >= f_end) return;
-      entry = 0;                             // the run goes on with the next pair
-      if (++job == heads) {
-        job = 0;
-        do {
-          L = p.context_lens[++b];
-          nb = visible_pages(p, L, &first);
-        } while (nb == 0);                   // f < total: a later sequence has pages
-      }
-    }
   }
+  if (!kFlat && invalid && lane == 0) atomicOr(&g_pa_err, kErrBounds);
 }
 
 // ---------------------------------------------------------------- merge of the runs
-// One CTA of W warps per (job, query row).  Partial i of the job comes from worker w0 + i;
-// warp k takes partials k, k + W, ...
+// W warps per (job, query row), 4 / W rows per CTA of four warps (W = 1) or one row per CTA.
+// Warp k of a row takes pieces k, k + W, ...
 template <int D, int W>
-__global__ void __launch_bounds__(32 * W) attn4_merge_kernel(const Attn4Params p, int ntw,
-                                                             int tile_rows, int live) {
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
+    attn4_merge_kernel(const Attn4Params p, int ntw, int tile_rows, int live) {
   constexpr int DL = D / 32;
   __shared__ float s_acc[W][D];
   __shared__ float s_ml[W][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = p.Hkv * ntw;
-  const int r = static_cast<int>(blockIdx.x % live);
-  const int job = static_cast<int>(blockIdx.x / live % heads);
-  const int b = static_cast<int>(blockIdx.x / live / heads);
+  const RunList list = run_list(p, ntw);
+  const int lane = threadIdx.x & 31;
+  const int warp = W == 1 ? 0 : threadIdx.x >> 5;
+  const int id = W == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int r = id % live;
+  const int job = id / live % list.heads;
+  const int b = id / live / list.heads;
   const int row = job % ntw * tile_rows + r;
-  int first, before, all;
-  const int mine = p.context_lens[b];
-  count_entries(p, lane, b, all, before);
-  const int nb = visible_pages(p, mine, &first);
-  const int share = run_entries(p, all * heads);
-  const int ne = pair_entries(nb);
-  const int f0 = before * heads + job * ne;
-  // the workers of its first and its last page
-  const int w0 = (f0 + kSetup) / share, w1 = (f0 + ne - 1) / share;
   // every CTA waits, so that this grid does not complete before the one it follows
+  if (b >= p.num_seqs) {
+    grid_dependency_wait();
+    return;
+  }
+  int first;
+  const int nb = visible_pages(list, p.context_lens[b], first);
+  const Pieces pc = find_pieces(list, b, job, nb, lane);
   grid_dependency_wait();
-  if (nb == 0 || w0 == w1 || row >= p.G * p.T) return;
-  const int parts = w1 - w0 + 1;
-  auto slot = [&](int i) {
-    const bool second = i == 0 && f0 > w0 * share;       // the run's last pair, not its first
-    return (static_cast<size_t>(w0 + i) * 2 + (second ? 1 : 0)) * tile_rows + r;
-  };
+  if (nb == 0 || pc.count == 1 || row >= p.G * p.T) return;
+  const int parts = pc.count;
+  auto slot = [&](int i) { return pc.slot(i) * tile_rows + r; };
   float M = -CUDART_INF_F, S = 0.f, acc[DL];
 #pragma unroll
   for (int k = 0; k < DL; ++k) acc[k] = 0.f;
@@ -584,7 +417,7 @@ __global__ void __launch_bounds__(32 * W) attn4_merge_kernel(const Attn4Params p
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float u = M == -CUDART_INF_F ? 0.f : M;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = warp; i < parts; i += W) {
     const size_t at = slot(i);
     const float2 ml = p.part_ml[at];
@@ -650,20 +483,22 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
   // the merge starts during the attention kernel's last wave
   cudaLaunchConfig_t cfg = {};
   const int live = std::min(C::kRows, p.G * p.T);   // rows of a tile that are used
-  cfg.gridDim = dim3(static_cast<unsigned>(jobs * live), 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  auto go = [&](auto fn, int warps, unsigned ctas) {
+    cfg.blockDim = dim3(32 * warps, 1, 1);
+    cfg.gridDim = dim3(ctas, 1, 1);
+    return cudaLaunchKernelEx(&cfg, fn, p, C::NTW, C::kRows, live);
+  };
   // more warps per row when a job has many runs
-  if (p.workers >= 16 * jobs) {
-    cfg.blockDim = dim3(256, 1, 1);
-    return cudaLaunchKernelEx(&cfg, attn4_merge_kernel<D, 8>, p, C::NTW, C::kRows, live);
-  }
-  cfg.blockDim = dim3(32, 1, 1);
-  return cudaLaunchKernelEx(&cfg, attn4_merge_kernel<D, 1>, p, C::NTW, C::kRows, live);
+  const unsigned rows = static_cast<unsigned>(jobs * live);
+  if (p.workers >= 64 * jobs) return go(attn4_merge_kernel<D, 32>, 32, rows);
+  if (p.workers >= 12 * jobs) return go(attn4_merge_kernel<D, 8>, 8, rows);
+  return go(attn4_merge_kernel<D, 1>, 4, (rows + 3) / 4);
 }
 
 template <int D>

@@ -2,55 +2,99 @@
 // of pa_accumulate_weights.
 #include <algorithm>
 
-#include "pa_pages.cuh"
+#include "pa_runs.cuh"
 
 namespace pa {
 
 // ---------------------------------------------------------------- weights
-// A CTA takes 256 entries of one (sequence, kv head): the rows' final (m, l) from the
-// chunks, then one entry per thread.
-constexpr int kSumThreads = 256;
+// A CTA takes 1024 entries of one (sequence, kv head), four per thread: first every row's
+// final (m, l) from the pieces of its job (a warp per row), then the sum over the rows, 16
+// bytes of every row's scores per load.
+constexpr int kSumThreads = 256, kSumEntries = 4 * kSumThreads;
 
 __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveParams p) {
   __shared__ float s_m[kMaxRows], s_f[kMaxRows];
   const int b = blockIdx.y / p.Hkv, g = blockIdx.y % p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RunList list = observe_list(p, p.ntw);
   const int L = p.context_lens[b], T = p.T, nrows = p.G * p.T;
-  if (L < T || L > p.max_ctx) return;
-  const int e0 = blockIdx.x * kSumThreads;
-  if (e0 >= L) return;
-  grid_dependency_wait();
-  const int chunks = ((L + kBlockSize - 1) / kBlockSize + p.ppb - 1) / p.ppb;
-  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
-  for (int r = threadIdx.x; r < nrows; r += kSumThreads) {
-    const float2* ml = p.ml + bg * p.max_chunks * nrows + r;
-    float M = -CUDART_INF_F, l = 0.f;
-    for (int c = 0; c < chunks; ++c) M = fmaxf(M, ml[static_cast<size_t>(c) * nrows].x);
-    const float u = M == -CUDART_INF_F ? 0.f : M;
-    for (int c = 0; c < chunks; ++c) {
-      const float2 x = ml[static_cast<size_t>(c) * nrows];
-      l += x.y * exp2f(x.x - u);
+  const int e0 = blockIdx.x * kSumEntries;
+  int first;
+  const int nb = visible_pages(list, L, first);
+  const bool work = nb > 0 && e0 < L;
+  Pieces pc[2];                              // of the row columns
+  if (work) {
+    for (int c = 0; c < p.ntw; ++c) {
+      if (p.flat)
+        pc[c] = find_pieces(list, b, g * p.ntw + c, nb, lane);
+      else
+        pc[c] = Pieces{0, (nb + p.ppb - 1) / p.ppb, false};
     }
-    s_m[r] = u;
-    s_f[r] = l > 0.f ? 1.f / l : 0.f;
+  }
+  grid_dependency_wait();
+  if (!work) return;
+  for (int r = warp; r < nrows; r += kSumThreads / 32) {
+    const int c = r / p.tile_rows, rl = r % p.tile_rows;
+    const Pieces& x = c == 0 ? pc[0] : pc[1];
+    const size_t unit0 = (static_cast<size_t>(b) * list.heads + g * p.ntw + c) * p.max_parts;
+    float M = -CUDART_INF_F, l = 0.f;
+    for (int i = lane; i < x.count; i += 32) {
+      const float2 ml = p.ml[(p.flat ? x.slot(i) : unit0 + i) * p.tile_rows + rl];
+      const float m = fmaxf(M, ml.x), u = m == -CUDART_INF_F ? 0.f : m;
+      l = l * hw_exp2(M - u) + ml.y * hw_exp2(ml.x - u);
+      M = m;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float a = __shfl_xor_sync(0xffffffffu, M, o), y = __shfl_xor_sync(0xffffffffu, l, o);
+      const float m = fmaxf(M, a), u = m == -CUDART_INF_F ? 0.f : m;
+      l = l * hw_exp2(M - u) + y * hw_exp2(a - u);
+      M = m;
+    }
+    if (lane == 0) {
+      s_m[r] = M == -CUDART_INF_F ? 0.f : M;
+      s_f[r] = l > 0.f ? 1.f / l : 0.f;
+    }
   }
   __syncthreads();
-  const int j = e0 + threadIdx.x;
-  if (j >= L) return;
-  const float* t = p.scores + (bg * p.max_entries + j) * p.row_stride;
-  float w = 0.f;
-  for (int r = 0; r < nrows; ++r) w += exp2f(t[r] - s_m[r]) * s_f[r];
-  const size_t at = bg * p.weight_entries + j;
-  const bool fresh = j >= L - T;
-  p.weights_out[at] = fresh ? w : fmaf(p.decay, p.weights[at], w);
-  if (fresh && p.positions != nullptr)
-    p.positions[at] = (p.seq_lens != nullptr ? p.seq_lens[b] : L) - L + j;
+  const int j0 = e0 + 4 * threadIdx.x;
+  if (j0 >= L) return;
+  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
+  const float* t = p.scores + bg * nrows * p.max_entries + j0;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int r = 0; r < nrows; ++r) {
+    const float4 x = *reinterpret_cast<const float4*>(t + static_cast<size_t>(r) * p.max_entries);
+    const float m = s_m[r], f = s_f[r];
+    w[0] = fmaf(hw_exp2(x.x - m), f, w[0]);
+    w[1] = fmaf(hw_exp2(x.y - m), f, w[1]);
+    w[2] = fmaf(hw_exp2(x.z - m), f, w[2]);
+    w[3] = fmaf(hw_exp2(x.w - m), f, w[3]);
+  }
+  const size_t at = bg * p.weight_entries + j0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int j = j0 + e;
+    if (j >= L) break;
+    const bool fresh = j >= L - T;
+    p.weights_out[at + e] = fresh ? w[e] : fmaf(p.decay, p.weights[at + e], w[e]);
+    if (fresh && p.positions != nullptr)
+      p.positions[at + e] = (p.seq_lens != nullptr ? p.seq_lens[b] : L) - L + j;
+  }
 }
 
 cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
-  dim3 grid(static_cast<unsigned>((p.max_ctx + kSumThreads - 1) / kSumThreads),
-            static_cast<unsigned>(p.num_seqs * p.Hkv));
-  observe_sum_kernel<<<grid, kSumThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.max_ctx + kSumEntries - 1) / kSumEntries),
+                     static_cast<unsigned>(p.num_seqs * p.Hkv), 1);
+  cfg.blockDim = dim3(kSumThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, observe_sum_kernel, p);
 }
 
 // ---------------------------------------------------------------- selection

@@ -89,6 +89,13 @@ constexpr Attn4Tile attn4_tile(int rows) {
          : rows <= 32 ? Attn4Tile{4, 1, 2}
                       : Attn4Tile{4, 2, 2};
 }
+constexpr Attn4Tile observe_tile(int rows) {
+  return rows <= 8    ? Attn4Tile{1, 1, 4}
+         : rows <= 16 ? Attn4Tile{2, 1, 3}
+         : rows <= 24 ? Attn4Tile{3, 1, 3}
+         : rows <= 32 ? Attn4Tile{4, 1, 2}
+                      : Attn4Tile{4, 2, 2};
+}
 constexpr int kAttn4Sms = 152;    // SMs the balanced mode fills
 
 // Accumulated attention weights: the first launch writes scores and the chunks' (m, l),
@@ -103,11 +110,14 @@ struct ObserveParams {
   const float* weights;           // [B, Hkv, weight_entries]
   float* weights_out;             // may be `weights`
   int32_t* positions;             // [B, Hkv, weight_entries] or nullptr
-  float* scores;                  // scratch [B, Hkv, max_entries, row_stride]
-  float2* ml;                     // scratch [B, Hkv, max_chunks, G * T]
+  float* scores;                  // scratch [B, Hkv, G * T, max_entries]
+  float2* ml;                     // scratch [slot][rows of a tile]: (m, l) of every piece
   int mbs, max_ctx, num_seqs, T, Hq, Hkv, G, num_blocks;
-  int ppb;                        // pages per chunk
-  int max_chunks, max_entries, row_stride, weight_entries;
+  int max_entries;                // max_ctx in whole blocks
+  int weight_entries;
+  bool flat;                      // balanced runs, or units of ppb pages
+  int workers, min_share, ppb, max_parts;
+  int tile_rows, ntw;             // rows of a tile, row columns
   float scale_log2, decay;
 };
 
@@ -199,12 +209,9 @@ cudaError_t launch_gather_int4(void* key, void* value, const void* k_cache, cons
                                const int64_t* slots, const float* k_scale, const float* v_scale,
                                int num_tokens, int num_blocks, int hkv, int head_dim,
                                cudaStream_t s);
-cudaError_t launch_observe_bf16(const ObserveParams& p, int head_dim, int rows, unsigned units,
-                                cudaStream_t s);
-cudaError_t launch_observe_fp8(const ObserveParams& p, int head_dim, int rows, unsigned units,
-                               cudaStream_t s);
-cudaError_t launch_observe_int4(const ObserveParams& p, int head_dim, int rows, unsigned units,
-                                cudaStream_t s);
+cudaError_t launch_observe_bf16(const ObserveParams& p, int head_dim, int rows, cudaStream_t s);
+cudaError_t launch_observe_fp8(const ObserveParams& p, int head_dim, int rows, cudaStream_t s);
+cudaError_t launch_observe_int4(const ObserveParams& p, int head_dim, int rows, cudaStream_t s);
 cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, int format, int head_dim, cudaStream_t s);
 cudaError_t launch_reduce(const AttnParams& p, int head_dim, cudaStream_t s);

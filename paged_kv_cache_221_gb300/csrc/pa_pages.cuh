@@ -54,28 +54,27 @@ __device__ __forceinline__ uint32_t page_swizzle(int row, int ch) {
     return row * P::kRow + ((ch ^ ((row >> 2) & 1)) << 4);
 }
 
+// Chunk `lane + 32 c` of a page lies at (lane's offset ^ swizzle_step(c)) + 512 c.
+template <int F, int D>
+__device__ __forceinline__ constexpr uint32_t swizzle_step(int c) {
+  constexpr int kRows = 32 / Page<F, D>::kChunks;   // rows per 32 chunks
+  return Page<F, D>::kChunks >= 8 ? ((kRows * c) & 7) << 4 : 0;
+}
+
+// base + page * stride in one wide multiply-add.
+__device__ __forceinline__ const uint8_t* at_page(const uint8_t* base, uint32_t page,
+                                                  uint32_t stride) {
+  const uint8_t* r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(page), "r"(stride), "l"(base));
+  return r;
+}
+
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// One warp copies a page to shared memory (asynchronously); ok = false zero-fills it.
-template <int F, int D>
-__device__ __forceinline__ void stage_page(uint32_t dst, const uint8_t* src, int lane, bool ok) {
-  using P = Page<F, D>;
-  const uint32_t n = ok ? 16u : 0u;
-#pragma unroll
-  for (int c0 = 0; c0 < P::kCodes / 16; c0 += 32) {
-    const int c = c0 + lane;
-    cp_async_16(dst + page_swizzle<F, D>(c / P::kChunks, c % P::kChunks), src + 16 * c, n);
-  }
-  if constexpr (P::kScales > 0) {
-    if (lane < P::kScales / 16)
-      cp_async_16(dst + P::kCodes + 16 * lane, src + P::kCodes + 16 * lane, n);
-  }
 }
 
 // This lane's ldmatrix row address within a staged page: tile i of an x4 load
@@ -141,12 +140,11 @@ struct QTile {
   float rs0, rs1;
 };
 
-// Bytes of one n-tile's operands in shared memory: [k step][lane], off, then rs.
+// Bytes of one n-tile's operands in shared memory: [k step][lane], then off.
 template <int F, int D>
 struct QTileSmem {
   static constexpr int kOff = (D / 16) * 32 * 8;
-  static constexpr int kRs = kOff + (F == kPageInt4 ? 32 * 8 : 0);
-  static constexpr int kBytes = kRs + 32 * 8;
+  static constexpr int kBytes = kOff + (F == kPageInt4 ? 32 * 8 : 0);
 };
 
 // Row n = t * G + hl of (sequence b, kv head g); rows from nrows on are zero.
@@ -266,7 +264,6 @@ __device__ __forceinline__ void put_q_tile(uint8_t* to, const QTile<F, D>& t, in
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) reinterpret_cast<uint2*>(to)[k * 32 + lane] = t.f[k];
   if constexpr (F == kPageInt4) reinterpret_cast<uint2*>(to + S::kOff)[lane] = t.off;
-  reinterpret_cast<float2*>(to + S::kRs)[lane] = make_float2(t.rs0, t.rs1);
 }
 
 // The query operands one warp needs for its n-tiles, in registers or (kRegs = false)
@@ -277,24 +274,6 @@ struct QOperand {
   float rs0[NT], rs1[NT];
   const uint8_t* base;
 
-  // From shared memory that put_q_tile filled.
-  __device__ __forceinline__ void load(const uint8_t* qt, int lane) {
-    using S = QTileSmem<F, D>;
-    base = qt + lane * 8;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const float2 r = *reinterpret_cast<const float2*>(base + j * S::kBytes + S::kRs);
-      rs0[j] = r.x;
-      rs1[j] = r.y;
-      if constexpr (kRegs) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tile[j].f[k] = *reinterpret_cast<const uint2*>(base + j * S::kBytes + k * 256);
-        if constexpr (F == kPageInt4)
-          tile[j].off = *reinterpret_cast<const uint2*>(base + j * S::kBytes + S::kOff);
-      }
-    }
-  }
   __device__ __forceinline__ uint2 get(int j, int k) const {
     if constexpr (kRegs)
       return tile[j].f[k];
@@ -309,6 +288,29 @@ struct QOperand {
                                              QTileSmem<F, D>::kOff);
   }
 };
+
+// A warp's operands for NT n-tiles; those kept in shared memory are read back by the lane that
+// wrote them.
+template <int F, int D, int NT, bool kRegs>
+__device__ __forceinline__ void make_q_operand(QOperand<F, D, NT, kRegs>& qo,
+                                               const QTileRaw<F, D> (&raw)[NT], uint8_t* qt,
+                                               float scale_log2, float k_scale, int lane) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if constexpr (kRegs) {
+      make_q_tile(qo.tile[j], raw[j], scale_log2, k_scale, lane);
+      qo.rs0[j] = qo.tile[j].rs0;
+      qo.rs1[j] = qo.tile[j].rs1;
+    } else {
+      QTile<F, D> tile;
+      make_q_tile(tile, raw[j], scale_log2, k_scale, lane);
+      put_q_tile(qt + j * QTileSmem<F, D>::kBytes, tile, lane);
+      qo.rs0[j] = tile.rs0;
+      qo.rs1[j] = tile.rs1;
+    }
+  }
+  if constexpr (!kRegs) qo.base = qt + lane * 8;
+}
 
 // D = A * B + C and D += A * B on f16 operands; without side effects, so that the compiler
 // may move them.
