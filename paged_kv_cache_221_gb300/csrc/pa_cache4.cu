@@ -4,9 +4,10 @@
 
 namespace pa {
 
-// One thread per 8 head dims of one (token, kv head), K and V; four threads make a
-// group of 32 dims.  APPEND: token i = b * T + t goes to position context_lens[b] - T + t
-// of sequence b; otherwise to slots[i].
+// One thread per group of 32 head dims of one (token, kv head) of K or of V: no value is
+// exchanged between threads, and a group's maximum, scale and reciprocal are worked out once.
+// APPEND: token i = b * T + t goes to position context_lens[b] - T + t of sequence b; otherwise
+// to slots[i].
 template <int D, bool APPEND>
 __global__ void __launch_bounds__(256)
     store_int4_kernel(const uint4* __restrict__ key, const uint4* __restrict__ value,
@@ -16,14 +17,17 @@ __global__ void __launch_bounds__(256)
                       const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                       int num_tokens, int num_blocks, int hkv) {
   using P = Page<kPageInt4, D>;
-  constexpr int VEC = D / 8;
   const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long total = static_cast<long long>(num_tokens) * hkv * VEC;
-  const long long at = min(idx, total - 1);    // every lane takes part in the shuffles
-  const int v = static_cast<int>(at % VEC);
-  const long long th = at / VEC;
+  const long long half = static_cast<long long>(num_tokens) * hkv * P::kGroups;
+  if (idx >= 2 * half) return;
+  const bool is_v = idx >= half;
+  const long long at = is_v ? idx - half : idx;
+  const int gr = static_cast<int>(at % P::kGroups);
+  const long long th = at / P::kGroups;
   const int h = static_cast<int>(th % hkv);
   const int i = static_cast<int>(th / hkv);
+  const uint4* src = (is_v ? value : key) + at * 4;
+  const uint4 x[4] = {src[0], src[1], src[2], src[3]};
   long long s = -1;
   bool bad = false;
   if constexpr (APPEND) {
@@ -39,24 +43,21 @@ __global__ void __launch_bounds__(256)
     s = slots[i];
     bad = s >= static_cast<long long>(num_blocks) * kBlockSize;
   }
-  const uint4 kx = key[at], vx = value[at];
-  uint32_t ks, vs;
-  const uint32_t kc = quantize_int4_8(kx, k_scale[h], ks);
-  const uint32_t vc = quantize_int4_8(vx, v_scale[h], vs);
-  if (idx >= total) return;
   if (bad) {
-    if (v == 0) atomicOr(&g_pa_err, kErrBounds);
+    if (gr == 0) atomicOr(&g_pa_err, kErrBounds);
     return;
   }
   if (s < 0) return;                           // padding token
-  const size_t page = (static_cast<size_t>(s / kBlockSize) * hkv + h) * P::kBytes;
+  const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
+                          x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
+  uint32_t codes[4], scale;
+  quantize_int4_32(w, (is_v ? v_scale : k_scale)[h], codes, scale);
+  uint8_t* page = (is_v ? v_cache : k_cache) +
+                  (static_cast<size_t>(s / kBlockSize) * hkv + h) * P::kBytes;
   const int t = static_cast<int>(s % kBlockSize);
-  *reinterpret_cast<uint32_t*>(k_cache + page + t * P::kRow + 4 * v) = kc;
-  *reinterpret_cast<uint32_t*>(v_cache + page + t * P::kRow + 4 * v) = vc;
-  if ((v & 3) == 0) {
-    k_cache[page + P::kCodes + t * P::kGroups + v / 4] = static_cast<uint8_t>(ks);
-    v_cache[page + P::kCodes + t * P::kGroups + v / 4] = static_cast<uint8_t>(vs);
-  }
+  *reinterpret_cast<uint4*>(page + t * P::kRow + 16 * gr) =
+      make_uint4(codes[0], codes[1], codes[2], codes[3]);
+  page[P::kCodes + t * P::kGroups + gr] = static_cast<uint8_t>(scale);
 }
 
 // One thread per 8 head dims of one (slot, kv head): bf16((u - 8) * (scale * head_scale)).
@@ -115,7 +116,7 @@ cudaError_t launch_store_int4(const void* key, const void* value, void* k_cache,
                               const float* v_scale, int num_tokens, int num_blocks, int hkv,
                               int head_dim, cudaStream_t s) {
   if (num_tokens == 0) return cudaSuccess;
-  const unsigned grid = blocks_for(static_cast<long long>(num_tokens) * hkv * (head_dim / 8));
+  const unsigned grid = blocks_for(2ll * num_tokens * hkv * (head_dim / kGroupDims));
   auto go = [&](auto fn) {
     fn<<<grid, 256, 0, s>>>(static_cast<const uint4*>(key), static_cast<const uint4*>(value),
                             static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), slots,

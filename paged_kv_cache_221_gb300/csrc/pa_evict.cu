@@ -102,11 +102,12 @@ cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
 // order (newest num_recent first, larger weight, lower index).  Either all protected
 // (newest) entries stay and the threshold lies among the others, or it lies among the
 // protected ones; a radix selection over the weights' order-preserving bits finds it
-// in four passes, and a scan in index order settles ties, numbers the dropped
-// entries below `budget` (the gaps) and the kept ones from `budget` on (the movers),
-// and writes pair i = (i-th mover, i-th gap).
-constexpr int kSelThreads = 512;
-
+// in four passes.  Weights and positions are read once: keys and the protected bits
+// stay in shared memory (contexts too long for it are read again at every pass).  Each
+// warp then owns a run of consecutive entries: a ballot per 32 of them and one exchange
+// between the warps settle which ties stay (the lowest indices), a second exchange numbers
+// the dropped entries below `budget` (the gaps) and the kept ones from `budget` on
+// (the movers), and pair i becomes (i-th mover, i-th gap).
 // Larger for larger weights; -0 equals +0; NaN is below every number.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -114,49 +115,39 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sums of up to three small counts over the CTA, with the totals.
-struct Count3 {
-  int a, b, c;
-};
-__device__ __forceinline__ Count3 scan3(Count3 x, Count3& total, int3* sh) {
+// Exclusive prefix over the CTA's warps of two counts each warp holds, and the totals.
+template <int W>
+__device__ __forceinline__ int2 over_warps(int2 mine, int2& total, int2* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Count3 v = x;
+  if (lane == 0) sh[warp] = mine;
+  __syncthreads();
+  int2 v = lane < W ? sh[lane] : make_int2(0, 0);
+  const int2 own = v;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o);
-    const int c = __shfl_up_sync(0xffffffffu, v.c, o);
+  for (int o = 1; o < W; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, v.x, o), c = __shfl_up_sync(0xffffffffu, v.y, o);
     if (lane >= o) {
-      v.a += a;
-      v.b += b;
-      v.c += c;
+      v.x += a;
+      v.y += c;
     }
   }
-  if (lane == 31) sh[warp] = make_int3(v.a, v.b, v.c);
+  total = make_int2(__shfl_sync(0xffffffffu, v.x, W - 1), __shfl_sync(0xffffffffu, v.y, W - 1));
+  const int x = __shfl_sync(0xffffffffu, v.x - own.x, warp);
+  const int y = __shfl_sync(0xffffffffu, v.y - own.y, warp);
   __syncthreads();
-  Count3 before{0, 0, 0};
-  total = Count3{0, 0, 0};
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    const int3 y = sh[w];
-    if (w < warp) {
-      before.a += y.x;
-      before.b += y.y;
-      before.c += y.z;
-    }
-    total.a += y.x;
-    total.b += y.y;
-    total.c += y.z;
-  }
-  __syncthreads();
-  return Count3{before.a + v.a - x.a, before.b + v.b - x.b, before.c + v.c - x.c};
+  return make_int2(x, y);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+template <int W, bool kStaged>
+__global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams p) {
+  constexpr int kThreads = 32 * W;
+  extern __shared__ uint32_t s_dyn[];        // staged: protected bits, then keys
   __shared__ int s_hist[256];
-  __shared__ int3 s_scan[kSelThreads / 32];
+  __shared__ int2 s_warp[W];
   __shared__ int s_newest, s_protected, s_bad, s_digit, s_left;
   grid_launch_dependents();
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = p.context_lens[b];
   int* count = p.counts + blockIdx.x;
   if (L < 0 || L > p.max_ctx) {
@@ -179,6 +170,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * p.weight_entries;
   const float* w = p.weights + row;
   const int* pos = p.positions + row;
+  const int words = (L + 31) / 32;
+  uint32_t* s_prot = s_dyn;
+  uint32_t* s_key = s_dyn + (p.max_ctx + 31) / 32;
   if (tid == 0) {
     s_newest = -0x7fffffff - 1;
     s_protected = 0;
@@ -187,14 +181,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   __syncthreads();
   // a block outside the pool: the sequence is left as it is (every head sees the same table)
   const int nblk = (L + kBlockSize - 1) / kBlockSize;
-  for (int i = tid; i < nblk; i += kSelThreads)
+  for (int i = tid; i < nblk; i += kThreads)
     if (static_cast<unsigned>(p.block_tables[static_cast<size_t>(b) * p.mbs + i]) >=
         static_cast<unsigned>(p.num_blocks))
       s_bad = 1;
   int newest = -0x7fffffff - 1;
-  for (int j = tid; j < L; j += kSelThreads) newest = max(newest, pos[j]);
+#pragma unroll 4
+  for (int j = tid; j < L; j += kThreads) {
+    newest = max(newest, pos[j]);
+    if constexpr (kStaged) s_key[j] = weight_key(w[j]);
+  }
   newest = __reduce_max_sync(0xffffffffu, newest);
-  if ((tid & 31) == 0) atomicMax(&s_newest, newest);
+  if (lane == 0) atomicMax(&s_newest, newest);
   __syncthreads();
   if (s_bad) {
     if (tid == 0) {
@@ -208,140 +206,249 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   }
   const long long bar = static_cast<long long>(s_newest) - p.num_recent;   // protected: pos > bar
   int mine = 0;
-  for (int j = tid; j < L; j += kSelThreads) mine += pos[j] > bar ? 1 : 0;
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if ((tid & 31) == 0) atomicAdd(&s_protected, mine);
+#pragma unroll 4
+  for (int i = warp; i < words; i += W) {
+    const int j = 32 * i + lane;
+    const uint32_t bits = __ballot_sync(0xffffffffu, j < L && pos[j] > bar);
+    if constexpr (kStaged) {
+      if (lane == 0) s_prot[i] = bits;
+    }
+    mine += __popc(bits);
+  }
+  if (lane == 0 && mine > 0) atomicAdd(&s_protected, mine);
   __syncthreads();
   const bool among = s_protected >= p.budget;      // the threshold lies among the protected
   int k = among ? p.budget : p.budget - s_protected;   // entries of that class to keep
+  const bool none = k == 0;
+  auto is_protected = [&](int j) {
+    if constexpr (kStaged) return ((s_prot[j >> 5] >> (j & 31)) & 1u) != 0u;
+    return pos[j] > bar;
+  };
+  auto key_of = [&](int j) {
+    if constexpr (kStaged) return s_key[j];
+    return weight_key(w[j]);
+  };
 
   // k-th largest key of the class, a byte at a time
   uint32_t prefix = 0, mask = 0;
-  for (int shift = 24; shift >= 0 && k > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
+  for (int shift = 24; shift >= 0 && !none; shift -= 8) {
+    for (int i = tid; i < 256; i += kThreads) s_hist[i] = 0;
     __syncthreads();
-    for (int j = tid; j < L; j += kSelThreads) {
-      if ((pos[j] > bar) != among) continue;
-      const uint32_t key = weight_key(w[j]);
-      if ((key & mask) == prefix) atomicAdd(&s_hist[(key >> shift) & 255], 1);
+    for (int i = warp; i < words; i += W) {
+      const int j = 32 * i + lane;
+      int bin = 256;                         // not counted
+      if (j < L && is_protected(j) == among) {
+        const uint32_t key = key_of(j);
+        if ((key & mask) == prefix) bin = (key >> shift) & 255;
+      }
+      // one addition per bin and warp: the first byte of most weights is the same
+      const unsigned peers = __match_any_sync(0xffffffffu, bin);
+      if (bin < 256 && __ffs(peers) - 1 == lane) atomicAdd(&s_hist[bin], __popc(peers));
     }
     __syncthreads();
-    if (tid == 0) {
-      int left = k, d = 255;
-      while (d > 0 && s_hist[d] < left) left -= s_hist[d--];
-      s_digit = d;
-      s_left = left;
+    if (warp == 0) {
+      // bins 255 - 8 lane .. 248 - 8 lane: find where the count from the top passes k
+      int h[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = s_hist[255 - 8 * lane - i];
+        sum += h[i];
+      }
+      int above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, above, o);
+        if (lane >= o) above += a;
+      }
+      above -= sum;
+      if (above < k && above + sum >= k) {
+        int left = k - above, i = 0;
+        while (h[i] < left) left -= h[i++];
+        s_digit = 255 - 8 * lane - i;
+        s_left = left;
+      }
     }
     __syncthreads();
     k = s_left;
     prefix |= static_cast<uint32_t>(s_digit) << shift;
     mask |= 255u << shift;
-    __syncthreads();
   }
-  // of the class: every key above `prefix` stays, and the first k that equal it (k = 0: none)
-  const bool none = (among ? p.budget : p.budget - s_protected) == 0;
-
-  int2* moves = p.moves + static_cast<size_t>(blockIdx.x) * p.max_moves;
-  int ties = 0, gaps = 0, movers = 0;
-  for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    bool keep = false, tie = false;
-    if (j < L) {
-      const bool prot = pos[j] > bar;
-      if (prot != among) {
-        keep = prot;                         // protected, or below a class that fills the budget
-      } else if (!none) {
-        const uint32_t key = weight_key(w[j]);
-        keep = key > prefix;
-        tie = key == prefix;
-      }
+  // of the class: every key above `prefix` stays, and the first k that equal it
+  const int per_warp = (words + W - 1) / W;
+  const int i0 = min(words, warp * per_warp), i1 = min(words, i0 + per_warp);
+  auto look = [&](int i, bool& keep, bool& tie) {
+    const int j = 32 * i + lane;
+    keep = tie = false;
+    if (j >= L) return;
+    const bool prot = is_protected(j);
+    if (prot != among) {
+      keep = prot;                           // protected, or below a class that fills the budget
+    } else if (!none) {
+      const uint32_t key = key_of(j);
+      keep = key > prefix;
+      tie = key == prefix;
     }
-    Count3 total;
-    const Count3 at = scan3(Count3{tie ? 1 : 0, 0, 0}, total, s_scan);
-    if (tie && ties + at.a < k) keep = true;
-    ties += total.a;
-    const bool gap = j < L && !keep && j < p.budget, mover = keep && j >= p.budget;
-    const Count3 to = scan3(Count3{0, gap ? 1 : 0, mover ? 1 : 0}, total, s_scan);
-    if (gap) moves[gaps + to.b].y = j;
-    if (mover) moves[movers + to.c].x = j;
-    gaps += total.b;
-    movers += total.c;
+  };
+  int ties = 0;
+  for (int i = i0; i < i1; ++i) {
+    bool keep, tie;
+    look(i, keep, tie);
+    ties += __popc(__ballot_sync(0xffffffffu, tie));
+  }
+  int2 total;
+  const int ties_before = over_warps<W>(make_int2(ties, 0), total, s_warp).x;
+  const unsigned below = (1u << lane) - 1u;
+  int2* moves = p.moves + static_cast<size_t>(blockIdx.x) * p.max_moves;
+  int2 at = make_int2(0, 0);                 // gaps and movers before this warp's run
+  for (int pass = 0; pass < 2; ++pass) {
+    int seen = ties_before, gaps = 0, movers = 0;
+    for (int i = i0; i < i1; ++i) {
+      const int j = 32 * i + lane;
+      bool keep, tie;
+      look(i, keep, tie);
+      const unsigned tb = __ballot_sync(0xffffffffu, tie);
+      if (tie && seen + __popc(tb & below) < k) keep = true;
+      seen += __popc(tb);
+      const bool gap = j < L && !keep && j < p.budget, mover = keep && j >= p.budget;
+      const unsigned gb = __ballot_sync(0xffffffffu, gap), mb = __ballot_sync(0xffffffffu, mover);
+      if (pass == 1) {
+        if (gap) moves[at.x + gaps + __popc(gb & below)].y = j;
+        if (mover) moves[at.y + movers + __popc(mb & below)].x = j;
+      }
+      gaps += __popc(gb);
+      movers += __popc(mb);
+    }
+    if (pass == 0) at = over_warps<W>(make_int2(gaps, movers), total, s_warp);
   }
   if (tid == 0) {
-    *count = movers;
+    *count = total.y;
     if (g == 0) p.new_lens[b] = p.budget;
   }
 }
 
 // ---------------------------------------------------------------- moves
-// A warp copies one entry at a time: its K and V rows, weight and position.  Gaps lie
-// below `budget` and movers at or above it, so no copy reads what another writes.
-constexpr int kMoveThreads = 256;
+// A warp copies kBatch entries at a time, all loads of a batch in flight before its first
+// store: their K and V rows, weights and positions.  Gaps lie below `budget` and movers at or
+// above it, so no copy reads what another writes.
+constexpr int kMoveThreads = 256, kBatch = 4;
 
 template <int F, int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
   using P = Page<F, D>;
+  // 16-byte chunks of a K and a V row; for FP8 the K row and, a byte per dim, the V row
+  constexpr int kVec = F == kPageFp8 ? P::kChunks : 2 * P::kChunks;
+  static_assert(kVec <= 32, "one chunk per lane");
+  constexpr int kBytes = F == kPageFp8 ? D : (F == kPageInt4 ? 2 * P::kGroups : 0);
+  constexpr int kB = (kBytes + 31) / 32;     // single bytes per lane
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   const int bg = blockIdx.y;
   const int b = bg / p.Hkv, g = bg % p.Hkv;
   const int n = p.counts[bg];
-  const int stride = gridDim.x * (kMoveThreads / 32);
+  const int stride = gridDim.x * (kMoveThreads / 32) * kBatch;
   const int32_t* trow = p.block_tables + static_cast<size_t>(b) * p.mbs;
   uint8_t* kp = static_cast<uint8_t*>(p.k_pool);
   uint8_t* vp = static_cast<uint8_t*>(p.v_pool);
-  for (int i = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); i < n; i += stride) {
-    const int2 mv = p.moves[static_cast<size_t>(bg) * p.max_moves + i];
-    const size_t sp = (static_cast<size_t>(trow[mv.x / kBlockSize]) * p.Hkv + g) * P::kBytes;
-    const size_t dp = (static_cast<size_t>(trow[mv.y / kBlockSize]) * p.Hkv + g) * P::kBytes;
-    const int ts = mv.x % kBlockSize, td = mv.y % kBlockSize;
-    if constexpr (F == kPageFp8) {
-      for (int c = lane; c < P::kChunks; c += 32)
-        reinterpret_cast<uint4*>(kp + dp + td * P::kRow)[c] =
-            reinterpret_cast<const uint4*>(kp + sp + ts * P::kRow)[c];
-      for (int d = lane; d < D; d += 32)     // V pages are transposed: a byte per dim
-        vp[dp + d * kBlockSize + td] = vp[sp + d * kBlockSize + ts];
-    } else {
-      for (int c = lane; c < 2 * P::kChunks; c += 32) {
-        uint8_t* pool = c < P::kChunks ? kp : vp;
-        const int cc = c < P::kChunks ? c : c - P::kChunks;
-        reinterpret_cast<uint4*>(pool + dp + td * P::kRow)[cc] =
-            reinterpret_cast<const uint4*>(pool + sp + ts * P::kRow)[cc];
-      }
-      if constexpr (F == kPageInt4) {
-        if (lane >= 32 - 2 * P::kGroups) {
-          const int c = lane - (32 - 2 * P::kGroups);
-          uint8_t* pool = c < P::kGroups ? kp : vp;
-          const int cc = c < P::kGroups ? c : c - P::kGroups;
-          pool[dp + P::kCodes + td * P::kGroups + cc] = pool[sp + P::kCodes + ts * P::kGroups + cc];
-        }
-      }
+  const size_t row = static_cast<size_t>(bg) * p.weight_entries;
+  uint8_t* vpool = F != kPageFp8 && lane >= P::kChunks ? vp : kp;   // of this lane's chunk
+  const int vchunk = 16 * (lane % P::kChunks);
+  // byte i of an entry at token t of a page
+  auto byte_at = [&](int i, size_t page, int t) -> uint8_t* {
+    if constexpr (F == kPageFp8)
+      return vp + page + i * kBlockSize + t;  // V pages are transposed
+    else
+      return (i < P::kGroups ? kp : vp) + page + P::kCodes + t * P::kGroups + i % P::kGroups;
+  };
+  for (int i = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * kBatch; i < n;
+       i += stride) {
+    size_t sp[kBatch], dp[kBatch];
+    int2 mv[kBatch];
+    uint4 v[kBatch];
+    uint8_t x[kBatch][kB > 0 ? kB : 1];
+    float w[kBatch];
+    int32_t ps[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      mv[e] = p.moves[static_cast<size_t>(bg) * p.max_moves + min(i + e, n - 1)];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      sp[e] = (static_cast<size_t>(trow[mv[e].x / kBlockSize]) * p.Hkv + g) * P::kBytes;
+      dp[e] = (static_cast<size_t>(trow[mv[e].y / kBlockSize]) * p.Hkv + g) * P::kBytes;
     }
-    if (lane == 0) {
-      const size_t row = static_cast<size_t>(bg) * p.weight_entries;
-      p.weights[row + mv.y] = p.weights[row + mv.x];
-      p.positions[row + mv.y] = p.positions[row + mv.x];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int t = mv[e].x % kBlockSize;
+      if (lane < kVec) v[e] = *reinterpret_cast<const uint4*>(vpool + sp[e] + t * P::kRow + vchunk);
+#pragma unroll
+      for (int c = 0; c < kB; ++c)
+        if (lane + 32 * c < kBytes) x[e][c] = *byte_at(lane + 32 * c, sp[e], t);
+      w[e] = p.weights[row + mv[e].x];
+      ps[e] = p.positions[row + mv[e].x];
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (i + e >= n) break;
+      const int t = mv[e].y % kBlockSize;
+      if (lane < kVec) *reinterpret_cast<uint4*>(vpool + dp[e] + t * P::kRow + vchunk) = v[e];
+#pragma unroll
+      for (int c = 0; c < kB; ++c)
+        if (lane + 32 * c < kBytes) *byte_at(lane + 32 * c, dp[e], t) = x[e][c];
+      if (lane == 0) {
+        p.weights[row + mv[e].y] = w[e];
+        p.positions[row + mv[e].y] = ps[e];
+      }
     }
   }
 }
 
+namespace {
+
+template <int W>
+cudaError_t launch_select(const EvictParams& p, cudaStream_t s) {
+  // keys and protected bits of the longest context, if they fit
+  const size_t bytes = (static_cast<size_t>(p.max_ctx) + (p.max_ctx + 31) / 32) * 4;
+  const unsigned grid = static_cast<unsigned>(p.num_seqs * p.Hkv);
+  if (bytes <= 200 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<W, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               200 * 1024);
+    if (e != cudaSuccess) return e;
+    evict_select_kernel<W, true><<<grid, 32 * W, bytes, s>>>(p);
+  } else {
+    evict_select_kernel<W, false><<<grid, 32 * W, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_evict(const EvictParams& p, int format, int head_dim, cudaStream_t s) {
   const int pairs = p.num_seqs * p.Hkv;
-  evict_select_kernel<<<pairs, kSelThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // few entries per (sequence, kv head): smaller CTAs, more of them at once
+  cudaError_t e = p.max_ctx <= 4096 ? launch_select<8>(p, s) : launch_select<32>(p, s);
   if (e != cudaSuccess) return e;
-  // about 8 CTAs per SM in all, at most one warp per move
+  // about 8 CTAs per SM in all, at most one batch per warp
   const int want = std::max(1, 8 * 152 / pairs);
-  const int most = (p.max_moves + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
-  dim3 grid(static_cast<unsigned>(std::min(want, most)), static_cast<unsigned>(pairs));
-  auto go = [&](auto fn) { fn<<<grid, kMoveThreads, 0, s>>>(p); };
+  const int per_cta = kMoveThreads / 32 * kBatch;
+  const int most = (p.max_moves + per_cta - 1) / per_cta;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(want, most)), static_cast<unsigned>(pairs), 1);
+  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto go = [&](auto fn) { return cudaLaunchKernelEx(&cfg, fn, p); };
   if (format == kPageBf16)
-    head_dim == 64 ? go(evict_move_kernel<kPageBf16, 64>) : go(evict_move_kernel<kPageBf16, 128>);
-  else if (format == kPageFp8)
-    head_dim == 64 ? go(evict_move_kernel<kPageFp8, 64>) : go(evict_move_kernel<kPageFp8, 128>);
-  else
-    head_dim == 64 ? go(evict_move_kernel<kPageInt4, 64>) : go(evict_move_kernel<kPageInt4, 128>);
-  return cudaGetLastError();
+    return head_dim == 64 ? go(evict_move_kernel<kPageBf16, 64>)
+                          : go(evict_move_kernel<kPageBf16, 128>);
+  if (format == kPageFp8)
+    return head_dim == 64 ? go(evict_move_kernel<kPageFp8, 64>)
+                          : go(evict_move_kernel<kPageFp8, 128>);
+  return head_dim == 64 ? go(evict_move_kernel<kPageInt4, 64>)
+                        : go(evict_move_kernel<kPageInt4, 128>);
 }
 
 cudaError_t take_error_evict(unsigned* bits) { return read_error_word(bits); }

@@ -442,40 +442,45 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
 }
 
 // ---------------------------------------------------------------- INT4 quantisation
-// Four lanes hold the 32 dims of a group, eight each (bf16 pairs in w).  Returns the
-// lane's eight codes (dim i in bits 4i .. 4i+3) and the group's scale byte:
+// A thread's group of 32 dims (bf16 pairs in w): its codes (dim i in bits 4 (i % 8) of word
+// i / 8) and scale byte:
 //   scale = e4m3(max|x| / (7 head_scale))      (IEEE float32 division; saturates at 448)
 //   code  = the integer nearest to x / (scale head_scale), ties to even, in -7 .. 7, + 8
 // A zero scale gives the codes of zero; a NaN in the group gives a NaN scale.
-__device__ __forceinline__ uint32_t quantize_int4_8(const uint4& v, float head_scale,
-                                                    uint32_t& scale_byte) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t mb = 0;                            // largest magnitude as bf16 bits (NaN on top)
+// The quotient is x * (1 / step) with one correction by its residual, which makes
+// ties come out exact; it is rounded by adding 1.5 * 2^23 + 8 (to nearest even), whose
+// low bits then are the code, and the codes of a word are strung together by multiply-adds
+// on the whole bit patterns, whose constant parts are taken off at the end.
+__device__ __forceinline__ void quantize_int4_32(const uint32_t (&w)[16], float head_scale,
+                                                 uint32_t (&codes)[4], uint32_t& scale_byte) {
+  uint32_t mb = 0;                            // largest magnitudes as bf16 bits (NaN on top)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) mb = max(mb, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-  mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-  mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+  for (int i = 0; i < 16; ++i) mb = __vmaxu2(mb, w[i] & 0x7fff7fffu);
+  mb = max(mb & 0xffffu, mb >> 16);
   const float amax = __uint_as_float(mb << 16);
   scale_byte = f32x2_to_e4m3x2(__fdiv_rn(amax, __fmul_rn(7.f, head_scale)), 0.f) & 0xffu;
   const uint32_t sh = e4m3x2_to_f16x2(scale_byte);
   const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffffu))) *
                      head_scale;
-  const float inv = step > 0.f ? __fdividef(1.f, step) : 0.f;
-  uint32_t codes = 0;
+  const bool good = step > 0.f;               // not zero, not NaN
+  const float inv = good ? __frcp_rn(step) : 0.f;
+  const float lim = 7.25f * step;             // beyond it the code is +-7
+  constexpr float kMagic = 12582912.f + 8.f;
+  constexpr uint32_t kBase = 0x4B400000u;     // bits of 12582912.f
+  constexpr uint32_t kBases = kBase * 0x11111111u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-    // f + 1/2 is a midpoint next to x / step (x * inv may err by a few ulp, not by half
-    // a step); the sign of x - (f + 1/2) step decides, its zero is a tie
-    const float y = fminf(fmaxf(x * inv, -8.f), 8.f);
-    const float f = floorf(y);
-    const float r = fmaf(-(f + 0.5f), step, x);
-    int c = static_cast<int>(f);
-    c += (r > 0.f || (r == 0.f && (c & 1))) ? 1 : 0;
-    c = step > 0.f ? max(-7, min(7, c)) : 0;
-    codes |= static_cast<uint32_t>(c + 8) << (4 * i);
+  for (int v = 0; v < 4; ++v) {
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const uint32_t pair = w[4 * v + (i >> 1)];
+      const float x = fminf(fmaxf((i & 1) ? bf16_hi(pair) : bf16_lo(pair), -lim), lim);
+      const float y = x * inv;
+      const float q = fmaf(fmaf(-y, step, x), inv, y);
+      c = c * 16u + __float_as_uint(q + kMagic);
+    }
+    codes[v] = good ? c - kBases : 0x88888888u;
   }
-  return codes;
 }
 
 // Read and clear this translation unit's error word.
