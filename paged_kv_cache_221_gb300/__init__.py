@@ -35,6 +35,7 @@ Bounded caches (``accumulate_weights``, ``evict_tokens``; bf16, FP8 and INT4 pag
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -431,20 +432,68 @@ def int4_page_bytes(head_dim: int) -> int:
 _KV_BF16, _KV_FP8, _KV_INT4 = 0, 1, 2
 
 
+# The calls below are made once per layer and token, so their host time counts: arguments are
+# checked with a few attribute reads each (``_need`` words the error), sizes of workspaces are
+# computed once per shape, and pointers go to ctypes as plain integers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _is(t, dtype, ndim, index):
+    return (t.__class__ is torch.Tensor and t.dtype is dtype and t.dim() == ndim
+            and t.get_device() == index and t.is_contiguous())
+
+
+def _want(name, t, dtype, ndim, dev):
+    if not _is(t, dtype, ndim, dev.index):
+        _need(name, t, dtype, ndim, dev)
+
+
+def _call(name, dev, *args):
+    """library().name(*args, stream) with dev current, on its current stream."""
+    index = dev.index
+    fn = getattr(_lib.load(), name)
+    stream = _raw_stream(index) if _raw_stream is not None else \
+        torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
+    if st != _lib.PA_OK:
+        _lib.check(name, st)
+
+
+def _scratch(dev, workspace, need):
+    """(pointer, bytes, tensor to keep until the call is made)."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+_INT4_DIMS = {int4_page_bytes(d): d for d in (64, 128)}
+
+
 def _int4_pools(k_cache, v_cache, k_scale, v_scale):
-    _need("k_cache", k_cache, torch.uint8, 3)
+    if not (isinstance(k_cache, torch.Tensor) and _is(k_cache, torch.uint8, 3, k_cache.get_device())
+            and k_cache.is_cuda):
+        _need("k_cache", k_cache, torch.uint8, 3)
     dev = k_cache.device
-    _need("v_cache", v_cache, torch.uint8, 3, dev)
-    if v_cache.shape != k_cache.shape:
+    _want("v_cache", v_cache, torch.uint8, 3, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("inconsistent shapes")
-    NB, Hkv, page = k_cache.shape
-    D = {int4_page_bytes(d): d for d in (64, 128)}.get(page)
+    NB, Hkv, page = shape
+    D = _INT4_DIMS.get(page)
     if D is None:
         raise ValueError("INT4 pools are [num_blocks, num_kv_heads, int4_page_bytes(head_dim)] "
                          f"with head_dim 64 or 128, got pages of {page} bytes")
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(name, t, torch.float32, 1, dev)
-        if t.shape[0] != Hkv:
+        _want(name, t, torch.float32, 1, dev)
+        if t.numel() != Hkv:
             raise ValueError(f"{name} must have num_kv_heads entries")
     return dev, NB, Hkv, D
 
@@ -455,17 +504,16 @@ def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torc
     """Quantise new bf16 K/V rows [N, Hkv, D] into INT4 pages at their slots (negative slots
     are skipped)."""
     dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
-    _need("key", key, torch.bfloat16, 3, dev)
-    _need("value", value, torch.bfloat16, 3, dev)
-    _need("slot_mapping", slot_mapping, torch.int64, 1, dev)
-    N = key.shape[0]
-    if key.shape != (N, Hkv, D) or value.shape != key.shape or slot_mapping.shape[0] != N:
+    _want("key", key, torch.bfloat16, 3, dev)
+    _want("value", value, torch.bfloat16, 3, dev)
+    _want("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    shape = key.shape
+    N = shape[0]
+    if shape != (N, Hkv, D) or value.shape != shape or slot_mapping.numel() != N:
         raise ValueError("inconsistent shapes")
-    with torch.cuda.device(dev):
-        st = library().pa_reshape_and_cache_int4(_vp(key), _vp(value), _vp(k_cache), _vp(v_cache),
-                                                 _vp(slot_mapping), _vp(k_scale), _vp(v_scale), N,
-                                                 NB, Hkv, D, 16, _stream(dev))
-    _lib.check("pa_reshape_and_cache_int4", st)
+    _call("pa_reshape_and_cache_int4", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), slot_mapping.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), N,
+          NB, Hkv, D, 16)
 
 
 def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
@@ -473,18 +521,17 @@ def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping
     """The values held in INT4 slots as bf16: (key, value), each [N, Hkv, D]; rows with a
     negative slot are zero."""
     dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
-    _need("slot_mapping", slot_mapping, torch.int64, 1, dev)
-    N = slot_mapping.shape[0]
+    _want("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    N = slot_mapping.numel()
     key = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=dev)
     value = torch.empty_like(key)
-    with torch.cuda.device(dev):
-        st = library().pa_gather_cache_int4(_vp(key), _vp(value), _vp(k_cache), _vp(v_cache),
-                                            _vp(slot_mapping), _vp(k_scale), _vp(v_scale), N, NB,
-                                            Hkv, D, 16, _stream(dev))
-    _lib.check("pa_gather_cache_int4", st)
+    _call("pa_gather_cache_int4", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), slot_mapping.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), N,
+          NB, Hkv, D, 16)
     return key, value
 
 
+@functools.lru_cache(maxsize=1024)
 def int4_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                         num_query_tokens: int, max_context_len: int, head_dim: int,
                         partition_size: int = 0, window_size: int = 0) -> int:
@@ -496,7 +543,7 @@ def int4_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
 
 def _max_len(max_context_len, context_lens, least):
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if context_lens.numel() else least
+        max_context_len = context_lens.max().item() if context_lens.numel() else least  # host sync
     return int(max_context_len)
 
 
@@ -515,50 +562,67 @@ def attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     K/V are quantised and stored at positions L-T .. L-1 first; ``window_size`` > 0 limits each
     query token to its last ``window_size`` positions.
     """
-    squeeze = isinstance(q, torch.Tensor) and q.dim() == 3
-    q4 = q.unsqueeze(1) if squeeze else q
-    o4 = out.unsqueeze(1) if squeeze and out is not None else out
     dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
-    _need("q", q4, torch.bfloat16, 4, dev)
-    _need("block_tables", block_tables, torch.int32, 2, dev)
-    _need("context_lens", context_lens, torch.int32, 1, dev)
-    B, T, Hq, Dq = q4.shape
-    if Dq != D or block_tables.shape[0] != B or context_lens.shape[0] != B:
+    ndim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+    _want("q", q, torch.bfloat16, ndim, dev)
+    _want("block_tables", block_tables, torch.int32, 2, dev)
+    _want("context_lens", context_lens, torch.int32, 1, dev)
+    shape = q.shape
+    B, Hq, Dq = shape[0], shape[-2], shape[-1]
+    T = 1 if ndim == 3 else shape[1]
+    rows, mbs = block_tables.shape
+    if Dq != D or rows != B or context_lens.numel() != B:
         raise ValueError("inconsistent shapes")
     mcl = _max_len(max_context_len, context_lens, T)
-    if o4 is None:
-        o4 = torch.empty_like(q4)
+    if out is None:
+        out = torch.empty_like(q)
     else:
-        _need("out", o4, torch.bfloat16, 4, dev)
-        if o4.shape != q4.shape:
+        _want("out", out, torch.bfloat16, ndim, dev)
+        if out.shape != shape:
             raise ValueError("out must have q's shape")
-    if (new_key is None) != (new_value is None):
-        raise ValueError("new_key and new_value go together")
-    if new_key is not None:
+    nk = nv = None
+    if new_key is not None or new_value is not None:
+        if new_key is None or new_value is None:
+            raise ValueError("new_key and new_value go together")
         for name, t in (("new_key", new_key), ("new_value", new_value)):
-            _need(name, t, torch.bfloat16, t.dim(), dev)
+            _want(name, t, torch.bfloat16, t.dim() if isinstance(t, torch.Tensor) else 3, dev)
             if t.numel() != B * T * Hkv * D:
                 raise ValueError(f"{name} must hold [B, T, Hkv, D] values")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    need = int4_workspace_size(B, Hq, Hkv, T, mcl, D, partition_size, window_size) if B else 0
-    ws, wsb = _workspace(dev, workspace, need)
-    with torch.cuda.device(dev):
-        st = library().pa_attention_int4(
-            _vp(o4), _vp(q4), _vp(new_key), _vp(new_value), _vp(k_cache), _vp(v_cache),
-            _vp(k_scale), _vp(v_scale), int(window_size), _vp(block_tables),
-            block_tables.shape[1], _vp(context_lens), mcl, B, T, NB, Hq, Hkv, D, 16, scale,
-            partition_size, _vp(ws), wsb, _stream(dev))
-    _lib.check("pa_attention_int4", st)
-    return o4.squeeze(1) if squeeze else o4
+        nk, nv = new_key.data_ptr(), new_value.data_ptr()
+    need = int4_workspace_size(B, Hq, Hkv, T, mcl, D, partition_size, window_size)
+    ws, wsb, keep = _scratch(dev, workspace, need)
+    _call("pa_attention_int4", dev, out.data_ptr(), q.data_ptr(), nk, nv, k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), int(window_size),
+          block_tables.data_ptr(), mbs, context_lens.data_ptr(), mcl, B, T, NB, Hq, Hkv, D, 16,
+          D ** -0.5 if scale is None else float(scale), partition_size, ws, wsb)
+    return out
 
 
 def _stat(name, t, dtype, dev, B, Hkv, mcl):
-    _need(name, t, dtype, 3, dev)
-    if tuple(t.shape[:2]) != (B, Hkv) or t.shape[2] < mcl:
+    _want(name, t, dtype, 3, dev)
+    shape = t.shape
+    if shape[0] != B or shape[1] != Hkv or shape[2] < mcl:
         raise ValueError(f"{name} must be [num_seqs, num_kv_heads, max_entries >= "
-                         f"max_context_len], got {tuple(t.shape)}")
+                         f"max_context_len], got {tuple(shape)}")
+    return shape
 
 
+def _kv_format(k_cache):
+    """(format, dtype, dims) of a K pool by its type and shape."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    if k_cache.dtype is torch.bfloat16:
+        fmt = _KV_BF16, torch.bfloat16, 4
+    elif k_cache.dim() == 3:
+        fmt = _KV_INT4, torch.uint8, 3
+    else:
+        fmt = _KV_FP8, torch.uint8, 4
+    if not (k_cache.is_cuda and _is(k_cache, fmt[1], fmt[2], k_cache.get_device())):
+        _need("k_cache", k_cache, fmt[1], fmt[2])
+    return fmt
+
+
+@functools.lru_cache(maxsize=1024)
 def accumulate_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                               num_query_tokens: int, max_context_len: int) -> int:
     """Scratch bytes ``accumulate_weights`` needs with these sizes."""
@@ -581,64 +645,53 @@ def accumulate_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: tor
     ``positions`` are set from ``seq_lens`` (tokens seen by each sequence; default
     ``context_lens``).  The K pool may hold bf16, FP8 (with ``k_scale``) or INT4 pages (3-dim,
     with ``k_scale``)."""
-    squeeze = isinstance(q, torch.Tensor) and q.dim() == 3
-    q4 = q.unsqueeze(1) if squeeze else q
-    if not isinstance(k_cache, torch.Tensor):
-        raise TypeError("k_cache must be a torch.Tensor")
-    if k_cache.dtype == torch.bfloat16:
-        fmt = _KV_BF16
-        _need("k_cache", k_cache, torch.bfloat16, 4)
-    elif k_cache.dim() == 3:
-        fmt = _KV_INT4
-        _need("k_cache", k_cache, torch.uint8, 3)
-    else:
-        fmt = _KV_FP8
-        _need("k_cache", k_cache, torch.uint8, 4)
+    fmt = _kv_format(k_cache)[0]
     dev = k_cache.device
-    NB, Hkv = k_cache.shape[:2]
-    _need("q", q4, torch.bfloat16, 4, dev)
-    _need("block_tables", block_tables, torch.int32, 2, dev)
-    _need("context_lens", context_lens, torch.int32, 1, dev)
-    B, T, Hq, D = q4.shape
+    pool = k_cache.shape
+    NB, Hkv = pool[0], pool[1]
+    ndim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+    _want("q", q, torch.bfloat16, ndim, dev)
+    _want("block_tables", block_tables, torch.int32, 2, dev)
+    _want("context_lens", context_lens, torch.int32, 1, dev)
+    shape = q.shape
+    B, Hq, D = shape[0], shape[-2], shape[-1]
+    T = 1 if ndim == 3 else shape[1]
+    rows, mbs = block_tables.shape
     page = (NB, Hkv, int4_page_bytes(D)) if fmt == _KV_INT4 else (NB, Hkv, 16, D)
-    if tuple(k_cache.shape) != page or block_tables.shape[0] != B or context_lens.shape[0] != B:
+    if pool != page or rows != B or context_lens.numel() != B:
         raise ValueError("inconsistent shapes")
     if fmt == _KV_BF16:
         if k_scale is not None:
             raise ValueError("bf16 pages take no k_scale")
     else:
-        _need("k_scale", k_scale, torch.float32, 1, dev)
-        if k_scale.shape[0] != Hkv:
+        _want("k_scale", k_scale, torch.float32, 1, dev)
+        if k_scale.numel() != Hkv:
             raise ValueError("k_scale must have num_kv_heads entries")
     mcl = _max_len(max_context_len, context_lens, T)
-    _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
+    entries = _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
     if out is None:
         out = weights
-    else:
-        _stat("out", out, torch.float32, dev, B, Hkv, mcl)
-        if out.shape != weights.shape:
-            raise ValueError("out must have the shape of weights")
-    if positions is not None:
-        _stat("positions", positions, torch.int32, dev, B, Hkv, mcl)
-        if positions.shape != weights.shape:
-            raise ValueError("positions must have the shape of weights")
+    elif _stat("out", out, torch.float32, dev, B, Hkv, mcl) != entries:
+        raise ValueError("out must have the shape of weights")
+    if positions is not None and \
+            _stat("positions", positions, torch.int32, dev, B, Hkv, mcl) != entries:
+        raise ValueError("positions must have the shape of weights")
     if seq_lens is not None:
-        _need("seq_lens", seq_lens, torch.int32, 1, dev)
-        if seq_lens.shape[0] != B:
+        _want("seq_lens", seq_lens, torch.int32, 1, dev)
+        if seq_lens.numel() != B:
             raise ValueError("inconsistent shapes")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    need = accumulate_workspace_size(B, Hq, Hkv, T, mcl) if B else 0
-    ws, wsb = _workspace(dev, workspace, need)
-    with torch.cuda.device(dev):
-        st = library().pa_accumulate_weights(
-            _vp(weights), _vp(out), _vp(positions), weights.shape[2], _vp(q4), _vp(k_cache),
-            _vp(k_scale), fmt, _vp(block_tables), block_tables.shape[1], _vp(context_lens),
-            _vp(seq_lens), mcl, B, T, NB, Hq, Hkv, D, 16, scale, float(decay), _vp(ws), wsb,
-            _stream(dev))
-    _lib.check("pa_accumulate_weights", st)
+    need = accumulate_workspace_size(B, Hq, Hkv, T, mcl)
+    ws, wsb, keep = _scratch(dev, workspace, need)
+    _call("pa_accumulate_weights", dev, weights.data_ptr(), out.data_ptr(),
+          None if positions is None else positions.data_ptr(), entries[2], q.data_ptr(),
+          k_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(), fmt,
+          block_tables.data_ptr(), mbs, context_lens.data_ptr(),
+          None if seq_lens is None else seq_lens.data_ptr(), mcl, B, T, NB, Hq, Hkv, D, 16,
+          D ** -0.5 if scale is None else float(scale), float(decay), ws, wsb)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def evict_workspace_size(num_seqs: int, num_kv_heads: int, max_context_len: int,
                          budget: int) -> int:
     """Scratch bytes ``evict_tokens`` needs with these sizes."""
@@ -656,47 +709,34 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
     on move into the gaps below it, with their ``weights`` and ``positions``.  Returns the new
     context lengths (int32 [B], min(L, budget)).  Pools: bf16, FP8 or INT4 pages, owned by
     these sequences alone (no shared copy-on-write blocks)."""
-    if not isinstance(k_cache, torch.Tensor):
-        raise TypeError("k_cache must be a torch.Tensor")
-    if k_cache.dtype == torch.bfloat16:
-        fmt = _KV_BF16
-        _need("k_cache", k_cache, torch.bfloat16, 4)
-    elif k_cache.dim() == 3:
-        fmt = _KV_INT4
-        _need("k_cache", k_cache, torch.uint8, 3)
-    else:
-        fmt = _KV_FP8
-        _need("k_cache", k_cache, torch.uint8, 4)
+    fmt, dtype, ndim = _kv_format(k_cache)
     dev = k_cache.device
-    _need("v_cache", v_cache, k_cache.dtype, k_cache.dim(), dev)
-    NB, Hkv = k_cache.shape[:2]
+    _want("v_cache", v_cache, dtype, ndim, dev)
+    pool = k_cache.shape
+    NB, Hkv = pool[0], pool[1]
     if fmt == _KV_INT4:
-        BS, D = 16, {int4_page_bytes(d): d for d in (64, 128)}.get(k_cache.shape[2], 0)
-        good = D > 0 and v_cache.shape == k_cache.shape
+        BS, D = 16, _INT4_DIMS.get(pool[2], 0)
+        good = D > 0 and v_cache.shape == pool
     else:
-        BS, D = k_cache.shape[2:]
-        good = tuple(v_cache.shape) == ((NB, Hkv, D, BS) if fmt == _KV_FP8 else
-                                        (NB, Hkv, BS, D))
-    _need("block_tables", block_tables, torch.int32, 2, dev)
-    _need("context_lens", context_lens, torch.int32, 1, dev)
-    B = context_lens.shape[0]
-    if not good or block_tables.shape[0] != B:
+        BS, D = pool[2], pool[3]
+        good = v_cache.shape == ((NB, Hkv, D, BS) if fmt == _KV_FP8 else pool)
+    _want("block_tables", block_tables, torch.int32, 2, dev)
+    _want("context_lens", context_lens, torch.int32, 1, dev)
+    B = context_lens.numel()
+    rows, mbs = block_tables.shape
+    if not good or rows != B:
         raise ValueError("inconsistent shapes")
     mcl = max(1, _max_len(max_context_len, context_lens, 1))
-    _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
-    _stat("positions", positions, torch.int32, dev, B, Hkv, mcl)
-    if positions.shape != weights.shape:
+    entries = _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
+    if _stat("positions", positions, torch.int32, dev, B, Hkv, mcl) != entries:
         raise ValueError("positions must have the shape of weights")
     new_lens = torch.empty_like(context_lens)
-    need = evict_workspace_size(B, Hkv, mcl, budget) if B else 0
-    ws, wsb = _workspace(dev, workspace, need)
-    with torch.cuda.device(dev):
-        st = library().pa_evict_tokens(
-            _vp(new_lens), _vp(k_cache), _vp(v_cache), fmt, _vp(block_tables),
-            block_tables.shape[1], _vp(context_lens), mcl, _vp(weights), _vp(positions),
-            weights.shape[2], int(budget), int(num_recent), B, NB, Hkv, D, BS, _vp(ws), wsb,
-            _stream(dev))
-    _lib.check("pa_evict_tokens", st)
+    need = evict_workspace_size(B, Hkv, mcl, budget)
+    ws, wsb, keep = _scratch(dev, workspace, need)
+    _call("pa_evict_tokens", dev, new_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), fmt,
+          block_tables.data_ptr(), mbs, context_lens.data_ptr(), mcl, weights.data_ptr(),
+          positions.data_ptr(), entries[2], int(budget), int(num_recent), B, NB, Hkv, D, BS, ws,
+          wsb)
     return new_lens
 
 

@@ -473,8 +473,8 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
   static_assert(tile.nt == C::NT && tile.ntw == C::NTW && tile.ctas == C::MINB, "the host's tile");
   const long long jobs = static_cast<long long>(p.num_seqs) * p.Hkv * C::NTW;
   auto fn = p.flat ? paged_attn4_kernel<D, C, true> : paged_attn4_kernel<D, C, false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = p.flat ? allow_smem<paged_attn4_kernel<D, C, true>>(bytes)
+                               : allow_smem<paged_attn4_kernel<D, C, false>>(bytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>((p.workers + C::kWarps - 1) / C::kWarps);
   fn<<<grid, C::kThreads, bytes, s>>>(p);

@@ -31,24 +31,40 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
         pc[c] = Pieces{0, (nb + p.ppb - 1) / p.ppb, false};
     }
   }
+  const int j0 = e0 + 4 * threadIdx.x;
+  const bool mine = work && j0 < L;
+  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
+  const float* t = p.scores + bg * nrows * p.max_entries + j0;
+  const size_t at = bg * p.weight_entries + j0;
+  float old[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) old[e] = mine && j0 + e < L - T ? p.weights[at + e] : 0.f;
   grid_dependency_wait();
   if (!work) return;
+  // the first rows' scores, on their way while the (m, l) are joined
+  constexpr int kAhead = 4;
+  float4 x[kAhead];
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r)
+    x[r] = mine && r < nrows
+               ? *reinterpret_cast<const float4*>(t + static_cast<size_t>(r) * p.max_entries)
+               : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int r = warp; r < nrows; r += kSumThreads / 32) {
     const int c = r / p.tile_rows, rl = r % p.tile_rows;
-    const Pieces& x = c == 0 ? pc[0] : pc[1];
+    const Pieces& y = c == 0 ? pc[0] : pc[1];
     const size_t unit0 = (static_cast<size_t>(b) * list.heads + g * p.ntw + c) * p.max_parts;
     float M = -CUDART_INF_F, l = 0.f;
-    for (int i = lane; i < x.count; i += 32) {
-      const float2 ml = p.ml[(p.flat ? x.slot(i) : unit0 + i) * p.tile_rows + rl];
+    for (int i = lane; i < y.count; i += 32) {
+      const float2 ml = p.ml[(p.flat ? y.slot(i) : unit0 + i) * p.tile_rows + rl];
       const float m = fmaxf(M, ml.x), u = m == -CUDART_INF_F ? 0.f : m;
       l = l * hw_exp2(M - u) + ml.y * hw_exp2(ml.x - u);
       M = m;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const float a = __shfl_xor_sync(0xffffffffu, M, o), y = __shfl_xor_sync(0xffffffffu, l, o);
+      const float a = __shfl_xor_sync(0xffffffffu, M, o), z = __shfl_xor_sync(0xffffffffu, l, o);
       const float m = fmaxf(M, a), u = m == -CUDART_INF_F ? 0.f : m;
-      l = l * hw_exp2(M - u) + y * hw_exp2(a - u);
+      l = l * hw_exp2(M - u) + z * hw_exp2(a - u);
       M = m;
     }
     if (lane == 0) {
@@ -57,27 +73,33 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
     }
   }
   __syncthreads();
-  const int j0 = e0 + 4 * threadIdx.x;
-  if (j0 >= L) return;
-  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
-  const float* t = p.scores + bg * nrows * p.max_entries + j0;
+  if (!mine) return;
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int r = 0; r < nrows; ++r) {
-    const float4 x = *reinterpret_cast<const float4*>(t + static_cast<size_t>(r) * p.max_entries);
-    const float m = s_m[r], f = s_f[r];
-    w[0] = fmaf(hw_exp2(x.x - m), f, w[0]);
-    w[1] = fmaf(hw_exp2(x.y - m), f, w[1]);
-    w[2] = fmaf(hw_exp2(x.z - m), f, w[2]);
-    w[3] = fmaf(hw_exp2(x.w - m), f, w[3]);
+  for (int r0 = 0; r0 < nrows; r0 += kAhead) {
+    float4 next[kAhead];
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      const int n = r0 + kAhead + r;
+      if (n < nrows)
+        next[r] = *reinterpret_cast<const float4*>(t + static_cast<size_t>(n) * p.max_entries);
+    }
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      if (r0 + r >= nrows) break;
+      const float m = s_m[r0 + r], f = s_f[r0 + r];
+      w[0] = fmaf(hw_exp2(x[r].x - m), f, w[0]);
+      w[1] = fmaf(hw_exp2(x[r].y - m), f, w[1]);
+      w[2] = fmaf(hw_exp2(x[r].z - m), f, w[2]);
+      w[3] = fmaf(hw_exp2(x[r].w - m), f, w[3]);
+      x[r] = next[r];
+    }
   }
-  const size_t at = bg * p.weight_entries + j0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int j = j0 + e;
     if (j >= L) break;
     const bool fresh = j >= L - T;
-    p.weights_out[at + e] = fresh ? w[e] : fmaf(p.decay, p.weights[at + e], w[e]);
+    p.weights_out[at + e] = fresh ? w[e] : fmaf(p.decay, old[e], w[e]);
     if (fresh && p.positions != nullptr)
       p.positions[at + e] = (p.seq_lens != nullptr ? p.seq_lens[b] : L) - L + j;
   }
@@ -234,16 +256,11 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   for (int shift = 24; shift >= 0 && !none; shift -= 8) {
     for (int i = tid; i < 256; i += kThreads) s_hist[i] = 0;
     __syncthreads();
-    for (int i = warp; i < words; i += W) {
-      const int j = 32 * i + lane;
-      int bin = 256;                         // not counted
-      if (j < L && is_protected(j) == among) {
-        const uint32_t key = key_of(j);
-        if ((key & mask) == prefix) bin = (key >> shift) & 255;
-      }
-      // one addition per bin and warp: the first byte of most weights is the same
-      const unsigned peers = __match_any_sync(0xffffffffu, bin);
-      if (bin < 256 && __ffs(peers) - 1 == lane) atomicAdd(&s_hist[bin], __popc(peers));
+#pragma unroll 4
+    for (int j = tid; j < L; j += kThreads) {
+      const uint32_t key = key_of(j);
+      if (is_protected(j) == among && (key & mask) == prefix)
+        atomicAdd(&s_hist[(key >> shift) & 255], 1);
     }
     __syncthreads();
     if (warp == 0) {
@@ -290,6 +307,7 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
     }
   };
   int ties = 0;
+#pragma unroll 4
   for (int i = i0; i < i1; ++i) {
     bool keep, tie;
     look(i, keep, tie);
@@ -302,6 +320,7 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   int2 at = make_int2(0, 0);                 // gaps and movers before this warp's run
   for (int pass = 0; pass < 2; ++pass) {
     int seen = ties_before, gaps = 0, movers = 0;
+#pragma unroll 4
     for (int i = i0; i < i1; ++i) {
       const int j = 32 * i + lane;
       bool keep, tie;
@@ -409,9 +428,7 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t s) {
   const size_t bytes = (static_cast<size_t>(p.max_ctx) + (p.max_ctx + 31) / 32) * 4;
   const unsigned grid = static_cast<unsigned>(p.num_seqs * p.Hkv);
   if (bytes <= 200 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<W, true>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               200 * 1024);
+    const cudaError_t e = allow_smem<evict_select_kernel<W, true>>(200 * 1024);
     if (e != cudaSuccess) return e;
     evict_select_kernel<W, true><<<grid, 32 * W, bytes, s>>>(p);
   } else {
@@ -425,7 +442,7 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t s) {
 cudaError_t launch_evict(const EvictParams& p, int format, int head_dim, cudaStream_t s) {
   const int pairs = p.num_seqs * p.Hkv;
   // few entries per (sequence, kv head): smaller CTAs, more of them at once
-  cudaError_t e = p.max_ctx <= 4096 ? launch_select<8>(p, s) : launch_select<32>(p, s);
+  cudaError_t e = p.max_ctx <= 4096 ? launch_select<16>(p, s) : launch_select<32>(p, s);
   if (e != cudaSuccess) return e;
   // about 8 CTAs per SM in all, at most one batch per warp
   const int want = std::max(1, 8 * 152 / pairs);

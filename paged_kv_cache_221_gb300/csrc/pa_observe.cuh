@@ -250,8 +250,8 @@ cudaError_t launch_observe_cfg(const ObserveParams& p, cudaStream_t s) {
   constexpr Attn4Tile tile = observe_tile(C::kRows * C::NTW);
   static_assert(tile.nt == C::NT && tile.ntw == C::NTW && tile.ctas == C::MINB, "the host's tile");
   auto fn = p.flat ? observe_scores_kernel<F, D, C, true> : observe_scores_kernel<F, D, C, false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = p.flat ? allow_smem<observe_scores_kernel<F, D, C, true>>(bytes)
+                               : allow_smem<observe_scores_kernel<F, D, C, false>>(bytes);
   if (e != cudaSuccess) return e;
   fn<<<(p.workers + C::kWarps - 1) / C::kWarps, C::kThreads, bytes, s>>>(p);
   return cudaGetLastError();

@@ -22,6 +22,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "pa_ptx.cuh"
 
 namespace pa {
@@ -481,6 +483,20 @@ __device__ __forceinline__ void quantize_int4_32(const uint32_t (&w)[16], float 
     }
     codes[v] = good ? c - kBases : 0x88888888u;
   }
+}
+
+// Let a kernel use `bytes` of dynamic shared memory: asked of the driver once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0ull};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
 }
 
 // Read and clear this translation unit's error word.
