@@ -141,15 +141,14 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     make_q_operand(qo, raw, smem + Sm::kRingBytes, p.scale_log2, p.k_scale[g], lane);
 
     // Softmax state of rows 2q4, 2q4 + 1 of each n-tile: minus the reference m (log2
-    // domain) and, in units of the raw scores, the value a score must pass to move m
-    // (minus infinity until a score was seen).
+    // domain; kUnseen until a score was seen).
     // z: rows 0 .. NG - 1 hold the groups' sums of weight * scale (what the codes' offset
     // adds to the output), rows 8 .. 15 the sum of the weights.
-    float acc[NT][D / 16][4], z[NT][4], nm0[NT], nm1[NT], thr0[NT], thr1[NT];
+    constexpr float kUnseen = 1e30f;
+    float acc[NT][D / 16][4], z[NT][4], nm0[NT], nm1[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      nm0[j] = nm1[j] = 0.f;
-      thr0[j] = thr1[j] = -CUDART_INF_F;
+      nm0[j] = nm1[j] = kUnseen;
 #pragma unroll
       for (int e = 0; e < 4; ++e) z[j][e] = 0.f;
 #pragma unroll
@@ -207,38 +206,41 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
       // Online softmax: the reference m of a row moves only when a score passes it by
       // 7, so a weight is at most 2^7 and, times a V scale (at most 448), an f16 value.
       bool over = false;
-      float x0[NT], x1[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        x0[j] = fmaxf(t[0][j][0], t[0][j][2]);
-        x1[j] = fmaxf(t[0][j][1], t[0][j][3]);
+        float x = -CUDART_INF_F;
 #pragma unroll
-        for (int k = 1; k < TP; ++k) {
-          x0[j] = fmaxf(x0[j], fmaxf(t[k][j][0], t[k][j][2]));
-          x1[j] = fmaxf(x1[j], fmaxf(t[k][j][1], t[k][j][3]));
+        for (int k = 0; k < TP; ++k) {
+          const float* y = t[k][j];
+          x = fmaxf(x, fmaxf(fmaxf(fmaf(y[0], qo.rs0[j], nm0[j]), fmaf(y[2], qo.rs0[j], nm0[j])),
+                             fmaxf(fmaf(y[1], qo.rs1[j], nm1[j]), fmaf(y[3], qo.rs1[j], nm1[j]))));
         }
-        over |= x0[j] > thr0[j] || x1[j] > thr1[j];
+        over |= x > 7.f;
       }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
+#pragma unroll
+          for (int k = 0; k < TP; ++k) {
+            x0 = fmaxf(x0, fmaxf(t[k][j][0], t[k][j][2]));
+            x1 = fmaxf(x1, fmaxf(t[k][j][1], t[k][j][3]));
+          }
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
-            x0[j] = fmaxf(x0[j], __shfl_xor_sync(0xffffffffu, x0[j], o));
-            x1[j] = fmaxf(x1[j], __shfl_xor_sync(0xffffffffu, x1[j], o));
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
           }
           float f0 = 1.f, f1 = 1.f;
-          if (x0[j] > thr0[j]) {
-            const float nm = -x0[j] * qo.rs0[j];
-            f0 = thr0[j] == -CUDART_INF_F ? 0.f : hw_exp2(nm - nm0[j]);
+          if (fmaf(x0, qo.rs0[j], nm0[j]) > 7.f) {
+            const float nm = -x0 * qo.rs0[j];
+            f0 = nm0[j] == kUnseen ? 0.f : hw_exp2(nm - nm0[j]);
             nm0[j] = nm;
-            thr0[j] = x0[j] + 7.f / qo.rs0[j];
           }
-          if (x1[j] > thr1[j]) {
-            const float nm = -x1[j] * qo.rs1[j];
-            f1 = thr1[j] == -CUDART_INF_F ? 0.f : hw_exp2(nm - nm1[j]);
+          if (fmaf(x1, qo.rs1[j], nm1[j]) > 7.f) {
+            const float nm = -x1 * qo.rs1[j];
+            f1 = nm1[j] == kUnseen ? 0.f : hw_exp2(nm - nm1[j]);
             nm1[j] = nm;
-            thr1[j] = x1[j] + 7.f / qo.rs1[j];
           }
           z[j][0] *= f0;
           z[j][1] *= f1;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
         const int r = row0 + 8 * j + 2 * q4 + h;
         if (r >= nrows) continue;
         const float l = z[j][2 + h];
-        const bool none = (h ? thr1[j] : thr0[j]) == -CUDART_INF_F;
+        const bool none = (h ? nm1[j] : nm0[j]) == kUnseen;
         const float inv = l > 0.f ? out_scale / l : 0.f;
         const size_t orow = (static_cast<size_t>(b) * T + r / G) * p.Hq + g * G + r % G;
         float* po = nullptr;
@@ -503,9 +505,9 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_attn4(const Attn4Params& p, int rows, cudaStream_t s) {
-  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 2, 3, 4>>(p, s);
+  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 1, 6, 3>>(p, s);
   if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 1, 6, 2>>(p, s);
-  if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 1, 6, 2>>(p, s);
+  if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 2, 3, 2>>(p, s);
   if (rows <= 32) return launch_cfg4<D, Cfg4<4, 1, 1, 6, 2>>(p, s);
   return launch_cfg4<D, Cfg4<4, 2, 1, 6, 2>>(p, s);
 }

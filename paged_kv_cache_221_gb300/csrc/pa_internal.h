@@ -83,7 +83,7 @@ struct Attn4Tile {
   int nt, ntw, ctas;
 };
 constexpr Attn4Tile attn4_tile(int rows) {
-  return rows <= 8    ? Attn4Tile{1, 1, 4}
+  return rows <= 8    ? Attn4Tile{1, 1, 3}
          : rows <= 16 ? Attn4Tile{2, 1, 2}
          : rows <= 24 ? Attn4Tile{3, 1, 2}
          : rows <= 32 ? Attn4Tile{4, 1, 2}
