@@ -893,6 +893,7 @@ pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const
   p.flat = plan.flat;
   p.workers = plan.workers;
   p.min_share = kInt4MinShare;
+  p.after_store = new_key != nullptr;
   p.mbs = max_blocks_per_seq;
   p.max_ctx = max_context_len;
   p.num_seqs = num_seqs;

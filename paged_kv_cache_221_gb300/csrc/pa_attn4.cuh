@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   bool invalid = false;
   const bool any = cur.start(list, worker, lane, invalid);
   if (kFlat && worker == 0 && invalid) atomicOr(&g_pa_err, kErrBounds);
+  // new tokens are stored by the launch before, which this one may overlap up to here
+  grid_dependency_wait();
   if (!any) return;
 
   while (cur.next(list, seg, invalid)) {
@@ -479,17 +481,21 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
                                : allow_smem<paged_attn4_kernel<D, C, false>>(bytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>((p.workers + C::kWarps - 1) / C::kWarps);
-  fn<<<grid, C::kThreads, bytes, s>>>(p);
-  cudaError_t r = cudaGetLastError();
-  if (r != cudaSuccess || !p.flat) return r;
-  // the merge starts during the attention kernel's last wave
   cudaLaunchConfig_t cfg = {};
-  const int live = std::min(C::kRows, p.G * p.T);   // rows of a tile that are used
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.numAttrs = p.after_store ? 1 : 0;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, fn, p);
+  if (r != cudaSuccess || !p.flat) return r;
+  // the merge starts during the attention kernel's last wave
+  const int live = std::min(C::kRows, p.G * p.T);   // rows of a tile that are used
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   auto go = [&](auto fn, int warps, unsigned ctas) {
     cfg.blockDim = dim3(32 * warps, 1, 1);

@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(256)
                       const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                       int num_tokens, int num_blocks, int hkv) {
   using P = Page<kPageInt4, D>;
+  grid_launch_dependents();                    // the attention launch that follows an append
   const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long half = static_cast<long long>(num_tokens) * hkv * P::kGroups;
   if (idx >= 2 * half) return;

@@ -76,6 +76,7 @@ struct Attn4Params : AttnParams {
   bool flat;
   int workers;                    // warps that take part
   int min_share;                  // balanced mode: smallest run in list entries
+  bool after_store;               // follows the launch that stores the call's new tokens
 };
 // Tile of a warp for `rows` query rows per kv head: n-tiles of 8 rows, row columns, and the
 // CTAs of four warps that an SM holds.
