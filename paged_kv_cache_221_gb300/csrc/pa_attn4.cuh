@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   bool invalid = false;
   const bool any = cur.start(list, worker, lane, invalid);
   if (kFlat && worker == 0 && invalid) atomicOr(&g_pa_err, kErrBounds);
-  // new tokens are stored by the launch before, which this one may overlap up to here
+  // With an append the launch before is the one that stores the new tokens: it started only
+  // when the lengths were final, so this one may find its work alongside it.
   grid_dependency_wait();
   if (!any) return;
 
@@ -481,32 +482,19 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
                                : allow_smem<paged_attn4_kernel<D, C, false>>(bytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>((p.workers + C::kWarps - 1) / C::kWarps);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(C::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.numAttrs = p.after_store ? 1 : 0;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, fn, p);
+  const cudaError_t r = launch_behind(fn, dim3(grid), C::kThreads, bytes, s, p.after_store, p);
   if (r != cudaSuccess || !p.flat) return r;
-  // the merge starts during the attention kernel's last wave
   const int live = std::min(C::kRows, p.G * p.T);   // rows of a tile that are used
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  auto go = [&](auto fn, int warps, unsigned ctas) {
-    cfg.blockDim = dim3(32 * warps, 1, 1);
-    cfg.gridDim = dim3(ctas, 1, 1);
-    return cudaLaunchKernelEx(&cfg, fn, p, C::NTW, C::kRows, live);
-  };
-  // more warps per row when a job has many runs
   const unsigned rows = static_cast<unsigned>(jobs * live);
-  if (p.workers >= 64 * jobs) return go(attn4_merge_kernel<D, 32>, 32, rows);
-  if (p.workers >= 12 * jobs) return go(attn4_merge_kernel<D, 8>, 8, rows);
-  return go(attn4_merge_kernel<D, 1>, 4, (rows + 3) / 4);
+  // more warps per row when a job has many runs
+  if (p.workers >= 64 * jobs)
+    return launch_behind(attn4_merge_kernel<D, 32>, dim3(rows), 1024, 0, s, true, p, C::NTW, C::kRows,
+                         live);
+  if (p.workers >= 12 * jobs)
+    return launch_behind(attn4_merge_kernel<D, 8>, dim3(rows), 256, 0, s, true, p, C::NTW, C::kRows,
+                         live);
+  return launch_behind(attn4_merge_kernel<D, 1>, dim3((rows + 3) / 4), 128, 0, s, true, p, C::NTW,
+                       C::kRows, live);
 }
 
 template <int D>

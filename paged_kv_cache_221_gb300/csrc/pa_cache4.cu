@@ -61,7 +61,10 @@ __global__ void __launch_bounds__(256)
   page[P::kCodes + t * P::kGroups + gr] = static_cast<uint8_t>(scale);
 }
 
-// One thread per 8 head dims of one (slot, kv head): bf16((u - 8) * (scale * head_scale)).
+// One thread per 8 head dims of kTokens (slot, kv head) rows a stride apart, K and V, all their
+// loads in flight at once: bf16((u - 8) * (scale * head_scale)).
+constexpr int kTokens = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256)
     gather_int4_kernel(uint4* __restrict__ key, uint4* __restrict__ value,
@@ -71,38 +74,56 @@ __global__ void __launch_bounds__(256)
                        int hkv) {
   using P = Page<kPageInt4, D>;
   constexpr int VEC = D / 8;
+  const int per_token = hkv * VEC;
+  const int step = (num_tokens + kTokens - 1) / kTokens;   // tokens i, i + step, ...
   const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (idx >= static_cast<long long>(num_tokens) * hkv * VEC) return;
-  const int v = static_cast<int>(idx % VEC);
-  const long long th = idx / VEC;
-  const int h = static_cast<int>(th % hkv);
-  const long long s = slots[th / hkv];
-  uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (s >= static_cast<long long>(num_blocks) * kBlockSize) {
-    if (v == 0) atomicOr(&g_pa_err, kErrBounds);
-  } else if (s >= 0) {
-    const size_t page = (static_cast<size_t>(s / kBlockSize) * hkv + h) * P::kBytes;
-    const int t = static_cast<int>(s % kBlockSize);
+  if (idx >= static_cast<long long>(step) * per_token) return;
+  const int i0 = static_cast<int>(idx / per_token);
+  const int hv = static_cast<int>(idx % per_token);
+  const int v = hv % VEC, h = hv / VEC;
+  long long s[kTokens];
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) s[k] = i0 + k * step < num_tokens ? slots[i0 + k * step] : -1;
+  const long long limit = static_cast<long long>(num_blocks) * kBlockSize;
+  uint32_t w[kTokens][2], sb[kTokens][2];
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) {
+    w[k][0] = w[k][1] = 0x88888888u;           // zero, for rows without a slot
+    sb[k][0] = sb[k][1] = 0u;
+    if (s[k] >= limit) {
+      if (v == 0) atomicOr(&g_pa_err, kErrBounds);
+    } else if (s[k] >= 0) {
+      const size_t page = (static_cast<size_t>(s[k] / kBlockSize) * hkv + h) * P::kBytes;
+      const int t = static_cast<int>(s[k] % kBlockSize);
+      const size_t code = page + t * P::kRow + 4 * v;
+      const size_t scale = page + P::kCodes + t * P::kGroups + v / 4;
+      w[k][0] = *reinterpret_cast<const uint32_t*>(k_cache + code);
+      w[k][1] = *reinterpret_cast<const uint32_t*>(v_cache + code);
+      sb[k][0] = k_cache[scale];
+      sb[k][1] = v_cache[scale];
+    }
+  }
+  const float hs[2] = {k_scale[h], v_scale[h]};
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) {
+    if (i0 + k * step >= num_tokens) break;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* pool = kv ? v_cache : k_cache;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(pool + page + t * P::kRow + 4 * v);
-      const uint32_t sb = pool[page + P::kCodes + t * P::kGroups + v / 4];
-      const uint32_t sh = e4m3x2_to_f16x2(sb);
-      const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffffu))) *
-                         (kv ? v_scale[h] : k_scale[h]);
+      const uint32_t sh = e4m3x2_to_f16x2(sb[k][kv]);
+      const float unit =
+          __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffffu))) * hs[kv];
       uint32_t r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float a = static_cast<float>(static_cast<int>((w >> (8 * e)) & 15u) - 8) * step;
-        const float c = static_cast<float>(static_cast<int>((w >> (8 * e + 4)) & 15u) - 8) * step;
-        r[e] = bf162_bits(__floats2bfloat162_rn(a, c));
+        const uint32_t x = w[k][kv] >> (8 * e);
+        r[e] = bf162_bits(
+            __floats2bfloat162_rn(static_cast<float>(static_cast<int>(x & 15u) - 8) * unit,
+                                  static_cast<float>(static_cast<int>(x >> 4 & 15u) - 8) * unit));
       }
-      out[kv] = make_uint4(r[0], r[1], r[2], r[3]);
+      (kv ? value : key)[(static_cast<long long>(i0) + k * step) * per_token + hv] =
+          make_uint4(r[0], r[1], r[2], r[3]);
     }
   }
-  key[idx] = out[0];
-  value[idx] = out[1];
 }
 
 namespace {
@@ -136,15 +157,15 @@ cudaError_t launch_gather_int4(void* key, void* value, const void* k_cache, cons
                                int num_tokens, int num_blocks, int hkv, int head_dim,
                                cudaStream_t s) {
   if (num_tokens == 0) return cudaSuccess;
-  const unsigned grid = blocks_for(static_cast<long long>(num_tokens) * hkv * (head_dim / 8));
+  const long long runs = (static_cast<long long>(num_tokens) + kTokens - 1) / kTokens;
+  const dim3 grid(blocks_for(runs * hkv * (head_dim / 8)));
   auto go = [&](auto fn) {
-    fn<<<grid, 256, 0, s>>>(static_cast<uint4*>(key), static_cast<uint4*>(value),
-                            static_cast<const uint8_t*>(k_cache),
-                            static_cast<const uint8_t*>(v_cache), slots, k_scale, v_scale,
-                            num_tokens, num_blocks, hkv);
+    return launch_behind(fn, grid, 256, 0, s, false, static_cast<uint4*>(key),
+                         static_cast<uint4*>(value), static_cast<const uint8_t*>(k_cache),
+                         static_cast<const uint8_t*>(v_cache), slots, k_scale, v_scale, num_tokens,
+                         num_blocks, hkv);
   };
-  head_dim == 64 ? go(gather_int4_kernel<64>) : go(gather_int4_kernel<128>);
-  return cudaGetLastError();
+  return head_dim == 64 ? go(gather_int4_kernel<64>) : go(gather_int4_kernel<128>);
 }
 
 cudaError_t take_error_cache4(unsigned* bits) { return read_error_word(bits); }

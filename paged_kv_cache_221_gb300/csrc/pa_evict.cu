@@ -106,17 +106,9 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
 }
 
 cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.max_ctx + kSumEntries - 1) / kSumEntries),
-                     static_cast<unsigned>(p.num_seqs * p.Hkv), 1);
-  cfg.blockDim = dim3(kSumThreads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, observe_sum_kernel, p);
+  const dim3 grid(static_cast<unsigned>((p.max_ctx + kSumEntries - 1) / kSumEntries),
+                  static_cast<unsigned>(p.num_seqs * p.Hkv));
+  return launch_behind(observe_sum_kernel, grid, kSumThreads, 0, s, true, p);
 }
 
 // ---------------------------------------------------------------- selection
@@ -430,11 +422,9 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t s) {
   if (bytes <= 200 * 1024) {
     const cudaError_t e = allow_smem<evict_select_kernel<W, true>>(200 * 1024);
     if (e != cudaSuccess) return e;
-    evict_select_kernel<W, true><<<grid, 32 * W, bytes, s>>>(p);
-  } else {
-    evict_select_kernel<W, false><<<grid, 32 * W, 0, s>>>(p);
+    return launch_behind(evict_select_kernel<W, true>, dim3(grid), 32 * W, bytes, s, false, p);
   }
-  return cudaGetLastError();
+  return launch_behind(evict_select_kernel<W, false>, dim3(grid), 32 * W, 0, s, false, p);
 }
 
 }  // namespace
@@ -448,16 +438,8 @@ cudaError_t launch_evict(const EvictParams& p, int format, int head_dim, cudaStr
   const int want = std::max(1, 8 * 152 / pairs);
   const int per_cta = kMoveThreads / 32 * kBatch;
   const int most = (p.max_moves + per_cta - 1) / per_cta;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(want, most)), static_cast<unsigned>(pairs), 1);
-  cfg.blockDim = dim3(kMoveThreads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  auto go = [&](auto fn) { return cudaLaunchKernelEx(&cfg, fn, p); };
+  const dim3 grid(static_cast<unsigned>(std::min(want, most)), static_cast<unsigned>(pairs));
+  auto go = [&](auto fn) { return launch_behind(fn, grid, kMoveThreads, 0, s, true, p); };
   if (format == kPageBf16)
     return head_dim == 64 ? go(evict_move_kernel<kPageBf16, 64>)
                           : go(evict_move_kernel<kPageBf16, 128>);

@@ -253,8 +253,8 @@ cudaError_t launch_observe_cfg(const ObserveParams& p, cudaStream_t s) {
   const cudaError_t e = p.flat ? allow_smem<observe_scores_kernel<F, D, C, true>>(bytes)
                                : allow_smem<observe_scores_kernel<F, D, C, false>>(bytes);
   if (e != cudaSuccess) return e;
-  fn<<<(p.workers + C::kWarps - 1) / C::kWarps, C::kThreads, bytes, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(fn, dim3((p.workers + C::kWarps - 1) / C::kWarps), C::kThreads, bytes, s,
+                       false, p);
 }
 
 template <int F, int D>

@@ -485,6 +485,26 @@ __device__ __forceinline__ void quantize_int4_32(const uint32_t (&w)[16], float 
   }
 }
 
+// Launch a kernel that, with `behind`, may become resident while the one before it in the
+// stream drains (programmatic stream serialisation): the later launches of a call.  It calls grid_dependency_wait() before it reads
+// what earlier work wrote and before it writes; every CTA waits, so that it does not
+// complete before the kernel it follows.
+template <class... Params, class... Args>
+cudaError_t launch_behind(void (*fn)(Params...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t s, bool behind, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 // Let a kernel use `bytes` of dynamic shared memory: asked of the driver once per device.
 template <auto kKernel>
 cudaError_t allow_smem(int bytes) {
