@@ -161,6 +161,31 @@ def test_bad_blocks_and_lengths_are_reported():
     assert torch.allclose(gain, torch.full_like(gain, 2.0), atol=1e-3)
 
 
+@pytest.mark.parametrize("B,hi,T", [(1, 9000, 1), (257, 60, 1), (300, 40, 3), (1030, 33, 1)])
+def test_weights_of_many_sequences(B, hi, T):
+    """Batches around the chunks of lengths a warp holds and past the size up to which runs are
+    balanced, and one sequence over all workers: rows sum to their number."""
+    gen = torch.Generator("cuda").manual_seed(B)
+    lens = torch.randint(T, hi + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    lens[0], lens[-1] = T, hi
+    M = -(-hi // 16)
+    tables = torch.randperm(B * M, generator=gen, device="cuda").int().view(B, M)
+    k = torch.randn((B * M, 2, 16, 64), generator=gen, device="cuda").bfloat16()
+    q = torch.randn((B, T, 6, 64), generator=gen, device="cuda").bfloat16()
+    w = torch.full((B, 2, hi), 3.0, device="cuda")
+    pa.accumulate_weights(q, k, tables, lens, w, max_context_len=hi, decay=0.0)
+    live = torch.arange(hi, device="cuda") < lens[:, None, None]
+    assert (w[~live.expand_as(w)] == 3).all()
+    gained = torch.where(live, w, torch.zeros_like(w)).double()
+    keys = k[tables.long()].transpose(1, 2).flatten(2, 3)[:, :, :hi].double()
+    s = torch.einsum("bthgd,bhjd->bhtgj", q.double().view(B, T, 2, 3, 64), keys) / 8
+    last = lens[:, None] - T + torch.arange(T, device="cuda")
+    see = torch.arange(hi, device="cuda") <= last[..., None]
+    ref = torch.softmax(s.masked_fill(~see[:, None, :, None], -float("inf")), -1).sum((2, 3))
+    # scores err by 2^-20 of sum |q k| (at most 40 here, in units of log2), sums by 2^-19
+    assert ((gained - ref).abs() <= (40 * 2.0 ** -20 + 2.0 ** -19) * ref + 1e-37).all()
+
+
 # ------------------------------------------------------------------------------- eviction
 def evict(c, d, w0, p0, budget, recent, mcl=None):
     """One call, checked entry by entry and page by page against the oracle."""
@@ -233,6 +258,31 @@ def test_evict_long(kind, budget, recent):
     c = Case(8, [3000, 701, 1501], 2, 2, 64, T=0, fmt="int4")
     w0, p0 = stats(np.random.default_rng(budget), c.lens, 2, 3008, kind)
     evict(c, Dev(c), w0, p0, budget, recent)
+
+
+def test_evict_context_past_shared_memory():
+    """A row whose keys do not fit in shared memory: read again at every pass."""
+    n, budget = 60000, 20000
+    gen = torch.Generator("cuda").manual_seed(0)
+    k = torch.randn((n // 16, 1, 16, 64), generator=gen, device="cuda").bfloat16()
+    v = torch.randn((n // 16, 1, 16, 64), generator=gen, device="cuda").bfloat16()
+    tables = torch.randperm(n // 16, generator=gen, device="cuda").int()[None]
+    w = torch.randint(0, 5000, (1, 1, n), generator=gen, device="cuda").float()
+    pos = torch.randperm(n, generator=gen, device="cuda").int().view(1, 1, n)
+    w0, p0 = w.clone(), pos.clone()
+    old = k[tables[0].long()][:, 0].flatten(0, 1).clone()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    new = pa.evict_tokens(k, v, tables, lens, w, pos, budget, 1000, n)
+    assert new.item() == budget
+    ref = BD.select(w0[0, 0].cpu().numpy(), p0[0, 0].cpu().numpy(), budget, 1000)
+    at = torch.arange(n, device="cuda")
+    src, dst = (torch.tensor(x, device="cuda") for x in zip(*ref))
+    at[dst] = src
+    assert torch.equal(pos[0, 0, :budget], p0[0, 0][at[:budget]])
+    assert torch.equal(w[0, 0, :budget], w0[0, 0][at[:budget]])
+    got = k[tables[0].long()][:, 0].flatten(0, 1)
+    assert torch.equal(got[:budget], old[at[:budget]])
+    assert torch.equal(got[budget:], old[budget:])
 
 
 def test_evict_in_order_keeps_the_tail():

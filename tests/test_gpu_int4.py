@@ -284,6 +284,137 @@ def test_outputs_of_one_call_do_not_depend_on_the_batch():
         assert torch.equal(one[0], out[b])
 
 
+def reference(q, k, v, ks, vs, tables, lens, scale, window=0):
+    """fp64 attention on the device, sequence by sequence, for sizes the host oracle is slow at:
+    (out, bound) with the bound's terms as in bound()."""
+    B, T, Hq, D = q.shape
+    Hkv, J = k.shape[1], tables.shape[1] * 16
+    table = torch.tensor(F.DECODE_TABLE, device=q.device)
+
+    def rows(pool, s, ids, n):
+        page = pool[ids.long()]                                     # [M, Hkv, bytes]
+        code = page[..., :8 * D].unflatten(-1, (16, D // 2)).long()
+        code = torch.stack([code & 15, code >> 4], -1).flatten(-2).double() - 8
+        unit = table[page[..., 8 * D:].long()].unflatten(-1, (16, D // 32))
+        unit = (unit * s.double()[:, None, None]).repeat_interleave(32, -1)
+        x, u = ((y.transpose(0, 1).flatten(1, 2)[:, :n]) for y in (code * unit, unit))
+        return x, u                                                 # [Hkv, n, D]
+
+    out, tol = torch.zeros(q.shape, dtype=torch.float64, device=q.device), None
+    tol = torch.zeros_like(out)
+    for b in range(B):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        K, _ = rows(k, ks, tables[b, :-(-n // 16)], n)
+        V, U = rows(v, vs, tables[b, :-(-n // 16)], n)
+        qq = q[b].double().view(T, Hkv, Hq // Hkv, D).permute(1, 0, 2, 3)
+        s = torch.einsum("htgd,hjd->htgj", qq, K) * scale
+        size = torch.einsum("htgd,hjd->htgj", qq.abs(), K.abs()).max() * scale * 1.4427
+        j, last = torch.arange(n, device=q.device), n - T + torch.arange(T, device=q.device)
+        see = j <= last[:, None]
+        if window:
+            see &= j > last[:, None] - window
+        s = s.masked_fill(~see[None, :, None], -float("inf"))
+        p = torch.softmax(s, -1)
+        put = lambda x: x.permute(1, 0, 2, 3).reshape(T, Hq, D)     # noqa: E731
+        out[b] = put(torch.einsum("htgj,hjd->htgd", p, V))
+        mag = put(torch.einsum("htgj,hjd->htgd", p, V.abs()))
+        step = put(torch.einsum("htgj,hjd->htgd", p, U))
+        small = n * 2.0 ** -25 * 15 * float(U.max() + vs.max())
+        tol[b] = (2.0 ** -8 * out[b].abs() + (2.0 ** -10 + 2.0 ** -16 + 2.0 ** -20 * size) * mag +
+                  2.0 ** -11 * 8 * step + small)
+    return out, tol
+
+
+def random_cache(gen, B, lens, Hkv, D):
+    need = [-(-n // 16) for n in lens]
+    NB = sum(need) + 2
+    ids = torch.randperm(NB, generator=gen, device="cuda").int()
+    tables = torch.zeros((B, max(max(need), 1)), dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        tables[b, :n] = ids[at:at + n]
+        at += n
+    scales = [torch.rand(Hkv, generator=gen, device="cuda") * 0.2 + 0.02 for _ in range(2)]
+    pools = [torch.zeros((NB, Hkv, pa.int4_page_bytes(D)), dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    slots = torch.arange(NB * 16, device="cuda")
+    x = [torch.randn((NB * 16, Hkv, D), generator=gen, device="cuda").bfloat16()
+         for _ in range(2)]
+    pa.reshape_and_cache_int4(*x, *pools, slots, *scales)
+    return pools, scales, tables, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def against_reference(gen, lens, Hq, Hkv, D, T=1, window=0, **kw):
+    B = len(lens)
+    (k, v), (ks, vs), tables, dl = random_cache(gen, B, lens, Hkv, D)
+    q = torch.randn((B, T, Hq, D), generator=gen, device="cuda").bfloat16()
+    out = torch.full_like(q, 7.0)
+    pa.attention_int4(q, k, v, ks, vs, tables, dl, max(max(lens), T), out=out, window_size=window,
+                      **kw)
+    ok = dl >= T
+    ref, tol = reference(q, k, v, ks, vs, tables, torch.where(ok, dl, 0), D ** -0.5, window)
+    over = (out.double() - ref).abs()[ok] - tol[ok]
+    assert torch.isfinite(out.float()).all() and over.max() <= 0, f"by {over.max():.3e}"
+    assert (out[~ok] == 7).all()                  # sequences out of range are left alone
+    return out
+
+
+@pytest.mark.parametrize("B,lo,hi", [(1, 20000, 20000), (2, 1, 9000), (33, 1, 400),
+                                     (257, 1, 700), (300, 250, 300), (1030, 1, 300)])
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(8, 2, 128, 1), (6, 2, 64, 1), (8, 1, 128, 3)])
+def test_balanced_runs(B, lo, hi, Hq, Hkv, D, T):
+    """Batches around the chunks of lengths a warp holds, past the size up to which runs are
+    balanced, one long sequence over all workers, and one long among short ones."""
+    gen = torch.Generator("cuda").manual_seed(B + hi)
+    lens = torch.randint(lo, hi + 1, (B,), generator=gen, device="cuda").tolist()
+    lens[0], lens[-1] = max(T, lo), hi
+    if B == 33:
+        lens[17] = 12345
+    lens = [max(T, n) for n in lens]
+    against_reference(gen, lens, Hq, Hkv, D, T)
+
+
+@pytest.mark.parametrize("window", [100, 700])
+def test_balanced_window(window):
+    gen = torch.Generator("cuda").manual_seed(window)
+    against_reference(gen, [5, 90, 3000, 5000, 17, 2049], 8, 2, 128, T=2, window=window)
+
+
+def test_balanced_runs_skip_sequences_out_of_range():
+    """Lengths below the query tokens (an idle row of a batch) take no part."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    against_reference(gen, [0, 900, 1, 0, 2, 400, 0], 8, 2, 64, T=2)
+    assert pa.get_device_error() == 5
+    # nothing at all to do
+    against_reference(gen, [0, 1, 0, 300], 8, 2, 64, T=2)
+    assert pa.get_device_error() == 5
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each: overlapping calls do not disturb one another."""
+    gen = torch.Generator("cuda").manual_seed(6)
+    lens = torch.randint(300, 3000, (16,), generator=gen, device="cuda").tolist()
+    (k, v), (ks, vs), tables, dl = random_cache(gen, 16, lens, 4, 128)
+    qs = [torch.randn((16, 1, 16, 128), generator=gen, device="cuda").bfloat16()
+          for _ in range(2)]
+    mcl = max(lens)
+    want = [pa.attention_int4(q, k, v, ks, vs, tables, dl, mcl) for q in qs]
+    need = pa.int4_workspace_size(16, 16, 4, 1, mcl, 128)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.empty_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                pa.attention_int4(qs[i], k, v, ks, vs, tables, dl, mcl, workspace=ws[i],
+                                  out=outs[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
 def test_three_dim_query_and_out():
     c = Case(17, [9, 50], 4, 2, 64)
     d = Dev(c)
