@@ -7,21 +7,26 @@
 namespace pa {
 
 // ---------------------------------------------------------------- weights
-// A CTA takes 1024 entries of one (sequence, kv head), four per thread: first every row's
-// final (m, l) from the pieces of its job (a warp per row), then the sum over the rows, 16
-// bytes of every row's scores per load.
-constexpr int kSumThreads = 256, kSumEntries = 4 * kSumThreads;
+// A CTA joins the (m, l) of one (sequence, kv head)'s rows from the pieces of its job (a warp
+// per row) and then takes every gridDim.x-th tile of 512 entries, four per thread: each
+// thread copies its 16 bytes of every row's scores to shared memory, all rows in flight at
+// once, and sums over them.  As many CTAs as are resident at once, so that what they do
+// before the first tile is not repeated.  Bound by the scores' bytes: 189 MB of 20 rows (32
+// sequences of 2048-16384 tokens) take 46 us, past what L2 still holds of them; a second
+// buffer per CTA (half the CTAs) took 54.
+constexpr int kSumThreads = 128, kSumEntries = 4 * kSumThreads;
+constexpr int kSumRowBytes = kSumEntries * 4;
 
 __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveParams p) {
   __shared__ float s_m[kMaxRows], s_f[kMaxRows];
+  extern __shared__ __align__(16) float s_scores[];   // [row][thread][4]
   const int b = blockIdx.y / p.Hkv, g = blockIdx.y % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RunList list = observe_list(p, p.ntw);
   const int L = p.context_lens[b], T = p.T, nrows = p.G * p.T;
-  const int e0 = blockIdx.x * kSumEntries;
   int first;
   const int nb = visible_pages(list, L, first);
-  const bool work = nb > 0 && e0 < L;
+  const bool work = nb > 0 && static_cast<int>(blockIdx.x) * kSumEntries < L;
   Pieces pc[2];                              // of the row columns
   if (work) {
     for (int c = 0; c < p.ntw; ++c) {
@@ -31,24 +36,22 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
         pc[c] = Pieces{0, (nb + p.ppb - 1) / p.ppb, false};
     }
   }
-  const int j0 = e0 + 4 * threadIdx.x;
-  const bool mine = work && j0 < L;
-  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
-  const float* t = p.scores + bg * nrows * p.max_entries + j0;
-  const size_t at = bg * p.weight_entries + j0;
-  float old[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) old[e] = mine && j0 + e < L - T ? p.weights[at + e] : 0.f;
   grid_dependency_wait();
   if (!work) return;
-  // the first rows' scores, on their way while the (m, l) are joined
-  constexpr int kAhead = 4;
-  float4 x[kAhead];
-#pragma unroll
-  for (int r = 0; r < kAhead; ++r)
-    x[r] = mine && r < nrows
-               ? *reinterpret_cast<const float4*>(t + static_cast<size_t>(r) * p.max_entries)
-               : make_float4(0.f, 0.f, 0.f, 0.f);
+  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
+  const float* scores = p.scores + bg * nrows * p.max_entries + 4 * threadIdx.x;
+  const uint32_t mine_at = smem_u32(s_scores) + 16 * threadIdx.x;
+  const int stride = gridDim.x * kSumEntries;
+  auto fetch = [&](int e0) {
+    const bool mine = e0 + 4 * static_cast<int>(threadIdx.x) < L;
+    for (int r = 0; r < nrows; ++r)
+      cp_async_16(mine_at + r * kSumRowBytes,
+                  mine ? scores + static_cast<size_t>(r) * p.max_entries + e0 : p.scores,
+                  mine ? 16u : 0u);
+    cp_async_commit();
+  };
+  int e0 = blockIdx.x * kSumEntries;
+  fetch(e0);
   for (int r = warp; r < nrows; r += kSumThreads / 32) {
     const int c = r / p.tile_rows, rl = r % p.tile_rows;
     const Pieces& y = c == 0 ? pc[0] : pc[1];
@@ -73,42 +76,48 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
     }
   }
   __syncthreads();
-  if (!mine) return;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int r0 = 0; r0 < nrows; r0 += kAhead) {
-    float4 next[kAhead];
+  for (; e0 < L; e0 += stride) {
+    const int j0 = e0 + 4 * threadIdx.x;
+    const size_t at = bg * p.weight_entries + j0;
+    float old[4];
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r) {
-      const int n = r0 + kAhead + r;
-      if (n < nrows)
-        next[r] = *reinterpret_cast<const float4*>(t + static_cast<size_t>(n) * p.max_entries);
+    for (int e = 0; e < 4; ++e) old[e] = j0 + e < L - T ? p.weights[at + e] : 0.f;
+    cp_async_wait<0>();
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    const float4* x4 = reinterpret_cast<const float4*>(s_scores);   // this thread's own copies
+#pragma unroll 4
+    for (int r = 0; r < nrows; ++r) {
+      const float4 x = x4[r * kSumThreads + threadIdx.x];
+      const float m = s_m[r], f = s_f[r];
+      w[0] = fmaf(hw_exp2(x.x - m), f, w[0]);
+      w[1] = fmaf(hw_exp2(x.y - m), f, w[1]);
+      w[2] = fmaf(hw_exp2(x.z - m), f, w[2]);
+      w[3] = fmaf(hw_exp2(x.w - m), f, w[3]);
     }
+    if (e0 + stride < L) fetch(e0 + stride);
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r) {
-      if (r0 + r >= nrows) break;
-      const float m = s_m[r0 + r], f = s_f[r0 + r];
-      w[0] = fmaf(hw_exp2(x[r].x - m), f, w[0]);
-      w[1] = fmaf(hw_exp2(x[r].y - m), f, w[1]);
-      w[2] = fmaf(hw_exp2(x[r].z - m), f, w[2]);
-      w[3] = fmaf(hw_exp2(x[r].w - m), f, w[3]);
-      x[r] = next[r];
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + e;
+      if (j >= L) break;
+      const bool fresh = j >= L - T;
+      p.weights_out[at + e] = fresh ? w[e] : fmaf(p.decay, old[e], w[e]);
+      if (fresh && p.positions != nullptr)
+        p.positions[at + e] = (p.seq_lens != nullptr ? p.seq_lens[b] : L) - L + j;
     }
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int j = j0 + e;
-    if (j >= L) break;
-    const bool fresh = j >= L - T;
-    p.weights_out[at + e] = fresh ? w[e] : fmaf(p.decay, old[e], w[e]);
-    if (fresh && p.positions != nullptr)
-      p.positions[at + e] = (p.seq_lens != nullptr ? p.seq_lens[b] : L) - L + j;
   }
 }
 
 cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.max_ctx + kSumEntries - 1) / kSumEntries),
-                  static_cast<unsigned>(p.num_seqs * p.Hkv));
-  return launch_behind(observe_sum_kernel, grid, kSumThreads, 0, s, true, p);
+  constexpr int kMost = kMaxRows * kSumRowBytes;
+  const int pairs = p.num_seqs * p.Hkv, bytes = p.G * p.T * kSumRowBytes;
+  const int resident = std::min(2048 / kSumThreads, 200 * 1024 / bytes);
+  const int tiles = (p.max_ctx + kSumEntries - 1) / kSumEntries;
+  const int wanted = (kAttn4Sms * resident + pairs - 1) / pairs;
+  const cudaError_t e = allow_smem<observe_sum_kernel>(kMost);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(std::max(1, std::min(tiles, wanted))),
+                  static_cast<unsigned>(pairs));
+  return launch_behind(observe_sum_kernel, grid, kSumThreads, bytes, s, true, p);
 }
 
 // ---------------------------------------------------------------- selection

@@ -381,24 +381,36 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
     for (int g2 = 0; g2 < P::kGroups; g2 += 2) {
       uint32_t w[4];
       ldsm_x4(w[0], w[1], w[2], w[3], page + (koff ^ (g2 << 4)));
+      // the first k steps of both groups, then the second ones: no tile waits for its own
+      float d[2][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int g = g2 + h;
-        const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1];
-        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+        const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1], y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float d[4];
-          const uint2 b0 = q.get(j, 2 * g), b1 = q.get(j, 2 * g + 1);
-          mma_f16_c(d, x0 & kNibLo, x1 & kNibLo, y0 & kNibLo, y1 & kNibLo, b0.x, b0.y, 0.f, 0.f,
-                    0.f, 0.f);
-          mma_f16(d, x0 & kNibHi, x1 & kNibHi, y0 & kNibHi, y1 & kNibHi, b1.x, b1.y);
-          t[j][0] = fmaf(d[0], s0[g], t[j][0]);
-          t[j][1] = fmaf(d[1], s0[g], t[j][1]);
-          t[j][2] = fmaf(d[2], s1[g], t[j][2]);
-          t[j][3] = fmaf(d[3], s1[g], t[j][3]);
+          const uint2 b0 = q.get(j, 2 * (g2 + h));
+          mma_f16_c(d[h][j], x0 & kNibLo, x1 & kNibLo, y0 & kNibLo, y1 & kNibLo, b0.x, b0.y, 0.f,
+                    0.f, 0.f, 0.f);
         }
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint2 b1 = q.get(j, 2 * (g2 + h) + 1);
+          mma_f16(d[h][j], x0 & kNibHi, x1 & kNibHi, y0 & kNibHi, y1 & kNibHi, b1.x, b1.y);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          t[j][0] = fmaf(d[h][j][0], s0[g2 + h], t[j][0]);
+          t[j][1] = fmaf(d[h][j][1], s0[g2 + h], t[j][1]);
+          t[j][2] = fmaf(d[h][j][2], s1[g2 + h], t[j][2]);
+          t[j][3] = fmaf(d[h][j][3], s1[g2 + h], t[j][3]);
+        }
     }
   } else {
     // two accumulator chains per n-tile
