@@ -405,7 +405,7 @@ Int4Plan int4_plan(int num_seqs, int hq, int hkv, int T, int span, int head_dim,
   const int rows = hq / hkv * T;
   const Attn4Tile tile = attn4_tile(rows);
   const long long jobs = static_cast<long long>(num_seqs) * hkv * tile.ntw;
-  const long long all = jobs * (pages + 3);      // list entries at most
+  const long long all = jobs * (pages + kRunSetup);      // list entries at most
   pl.flat = partition_size == 0 && scratch && pages > kInt4WholePages &&
             num_seqs <= kInt4FlatSeqs && all < (1ll << 30);
   if (pl.flat) {
@@ -444,7 +444,7 @@ ObservePlan observe_plan(int num_seqs, int hq, int hkv, int T, int max_ctx) {
   const int pages = ceil_div(max_ctx, kBlockSize);
   const Attn4Tile tile = observe_tile(rows);
   const long long jobs = static_cast<long long>(num_seqs) * hkv * tile.ntw;
-  const long long all = jobs * (pages + 3);
+  const long long all = jobs * (pages + kRunSetup);
   pl.tile_rows = 8 * tile.nt;
   pl.ntw = tile.ntw;
   pl.max_entries = pages * kBlockSize;

@@ -499,11 +499,18 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_attn4(const Attn4Params& p, int rows, cudaStream_t s) {
-  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 1, 6, 3>>(p, s);
-  if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 1, 6, 2>>(p, s);
-  if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 2, 3, 2>>(p, s);
-  if (rows <= 32) return launch_cfg4<D, Cfg4<4, 1, 1, 6, 2>>(p, s);
-  return launch_cfg4<D, Cfg4<4, 2, 1, 6, 2>>(p, s);
+  // Pages in flight per warp: with more (a ring of 6 or 8 single pages) the queues in front of
+  // memory grow and every dependent fetch at a job's start waits longer.  64 sequences of
+  // 512-4096 tokens, 4 rows: 41.0 us with rings of 3 double pages, 40.9 / 41.1 / 43.2 / 45.1
+  // with 3 / 4 / 6 / 8 single ones; 256 of 128-8192 tokens, 8 rows: 115.1 and 116.0 / 115.7
+  // / 118.4 / 121.3.  16 warps per SM instead of 12 (128 registers): 43.9 and 123.
+  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 2, 3, 3>>(p, s);
+  if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 1, 4, 2>>(p, s);
+  // 20 rows, 32 sequences of 2048-16384 tokens: 120 us, 125 with double pages, 182 with 12 warps
+  // (168 registers: the output tile spills)
+  if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 1, 3, 2>>(p, s);
+  if (rows <= 32) return launch_cfg4<D, Cfg4<4, 1, 1, 3, 2>>(p, s);
+  return launch_cfg4<D, Cfg4<4, 2, 1, 3, 2>>(p, s);
 }
 
 }  // namespace pa

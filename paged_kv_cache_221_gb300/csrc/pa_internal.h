@@ -98,6 +98,7 @@ constexpr Attn4Tile observe_tile(int rows) {
                       : Attn4Tile{4, 2, 2};
 }
 constexpr int kAttn4Sms = 152;    // SMs the balanced mode fills
+constexpr int kRunSetup = 5;      // list entries a job counts besides its pages (pa_runs.cuh)
 
 // Accumulated attention weights: the first launch writes scores and the chunks' (m, l),
 // the second adds the weights up.
