@@ -27,14 +27,11 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
   int first;
   const int nb = visible_pages(list, L, first);
   const bool work = nb > 0 && static_cast<int>(blockIdx.x) * kSumEntries < L;
-  Pieces pc[2];                              // of the row columns
-  if (work) {
-    for (int c = 0; c < p.ntw; ++c) {
-      if (p.flat)
-        pc[c] = find_pieces(list, b, g * p.ntw + c, nb, lane);
-      else
-        pc[c] = Pieces{0, (nb + p.ppb - 1) / p.ppb, false};
-    }
+  __shared__ Pieces pc[2];                   // of the row columns, a warp each
+  if (work && warp < p.ntw) {
+    Pieces x{0, (nb + p.ppb - 1) / p.ppb, false};
+    if (p.flat) x = find_pieces(list, b, g * p.ntw + warp, nb, lane);
+    if (lane == 0) pc[warp] = x;
   }
   grid_dependency_wait();
   if (!work) return;
@@ -52,9 +49,10 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
   };
   int e0 = blockIdx.x * kSumEntries;
   fetch(e0);
+  __syncthreads();
   for (int r = warp; r < nrows; r += kSumThreads / 32) {
     const int c = r / p.tile_rows, rl = r % p.tile_rows;
-    const Pieces& y = c == 0 ? pc[0] : pc[1];
+    const Pieces y = pc[c];
     const size_t unit0 = (static_cast<size_t>(b) * list.heads + g * p.ntw + c) * p.max_parts;
     float M = -CUDART_INF_F, l = 0.f;
     for (int i = lane; i < y.count; i += 32) {

@@ -69,6 +69,7 @@ struct Cursor {
       len[k] = 32 * k + lane < r.num_seqs ? r.lens[32 * k + lane] : -1;
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
+      if (32 * k >= r.num_seqs) break;
       int skip;
       sum += pair_entries(visible_pages(r, len[k], skip));
       invalid |= 32 * k + lane < r.num_seqs && (len[k] < r.T || len[k] > r.max_ctx);
@@ -182,6 +183,7 @@ __device__ __forceinline__ Pieces find_pieces(const RunList& r, int b, int job, 
       len[k] = base + 32 * k + lane < r.num_seqs ? r.lens[base + 32 * k + lane] : -1;
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
+      if (base + 32 * k >= r.num_seqs) break;
       int first;
       const int n = pair_entries(visible_pages(r, len[k], first));
       all += n;

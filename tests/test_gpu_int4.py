@@ -125,6 +125,24 @@ def test_store_is_exact_and_leaves_the_rest(D, Hkv, n):
                 np.testing.assert_allclose(got[i, h], ref, rtol=2.0 ** -8 + 2.0 ** -22, atol=0)
 
 
+def test_many_tokens_round_trip():
+    """Enough tokens for the form that reads several per thread, not a multiple of them."""
+    n, Hkv, D = 2503, 8, 128
+    gen = torch.Generator("cuda").manual_seed(0)
+    x = torch.randint(-7, 8, (2, n, Hkv, D), generator=gen, device="cuda").bfloat16()
+    x[..., ::32] = 7                                        # every group reaches 7: scale 1
+    NB = n // 16 + 2
+    pools = [torch.zeros((NB, Hkv, pa.int4_page_bytes(D)), dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    one = torch.ones(Hkv, device="cuda")
+    slots = torch.randperm(NB * 16, generator=gen, device="cuda")[:n]
+    slots[::11] = -1
+    pa.reshape_and_cache_int4(x[0], x[1], *pools, slots, one, one)
+    live = (slots >= 0)[:, None, None]
+    for got, want in zip(pa.gather_cache_int4(*pools, slots, one, one), x):
+        assert torch.equal(got, torch.where(live, want, torch.zeros_like(want)))
+
+
 def test_empty_calls():
     c = Case(0, [5], 2, 2, 64)
     d = Dev(c)
