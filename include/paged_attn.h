@@ -349,7 +349,7 @@ pa_status pa_decode_append(void* out, const void* q, const void* new_key, const 
  * pa_reshape_and_cache_int4 — pa_reshape_and_cache into INT4 pages.  key / value are
  * bf16 [num_tokens, num_kv_heads, head_dim].  head_dim 64 or 128; otherwise
  * requirements and errors as pa_reshape_and_cache, plus k_scale and v_scale non-NULL.
- * Two tokens naming the same slot leave its contents unspecified.
+ * Two tokens naming the same slot leave its contents unspecified.  At most 2^30 tokens.
  */
 pa_status pa_reshape_and_cache_int4(const void* key, const void* value, void* k_cache,
                                     void* v_cache, const int64_t* slot_mapping,
@@ -370,8 +370,9 @@ pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, cons
                                int num_kv_heads, int head_dim, int block_size,
                                pa_stream_t stream);
 
-/* Bytes of scratch pa_attention_int4 needs with these sizes (0 if no sequence can need
- * more than one partition); partition_size 0 = the library default. */
+/* Bytes of scratch pa_attention_int4 needs with these sizes (0 if every sequence is processed
+ * whole); partition_size 0 = the library default.  It does not grow with the batch
+ * then: the partial results of the warps that are resident at once. */
 size_t pa_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                               int num_query_tokens, int max_context_len, int head_dim,
                               int block_size, int partition_size, int window_size);
@@ -384,11 +385,22 @@ size_t pa_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
  * before they are read.  k_cache / v_cache are written only then.
  *
  * The products run on f16 operands with fp32 accumulation: query rows are scaled by a
- * power of two (any bf16 magnitude is taken), softmax weights are rounded to f16,
- * multiplied by the E4M3 scales and rounded to f16 again, and the codes are exact.
- * Workspace as pa_decode, sized by pa_int4_workspace_size; with partition_size = 0 and
- * workspace == NULL every sequence is processed whole.  Other arguments,
- * requirements and errors as pa_attention.
+ * power of two, softmax weights are rounded to f16, multiplied by the E4M3 scales and
+ * rounded to f16 again, and the codes are exact.  Scores scale * q . K stay below 10^29 in
+ * magnitude.
+ *
+ * Work: with partition_size = 0 and a workspace of pa_int4_workspace_size bytes, the pages
+ * of all sequences are split into equal runs over the GPU's warps (contexts above 256
+ * tokens, at most 1024 sequences; otherwise as below); the last bits of a sequence's result
+ * then depend on the other sequences of the batch, not on scheduling.  With an explicit
+ * partition_size (a multiple of 16) each partition is one warp's work, and a sequence's
+ * result does not depend on the batch.  With partition_size = 0 and workspace == NULL every
+ * sequence is processed whole.  The workspace needs no initialisation, is 256-byte
+ * aligned, and calls in flight at once do not share it.
+ *
+ * Other arguments, requirements and errors as pa_attention; a sequence whose context length
+ * is out of range is skipped (its output rows are left as they were, its new tokens
+ * not stored).
  */
 pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const void* new_value,
                             void* k_cache, void* v_cache, const float* k_scale,
@@ -419,7 +431,8 @@ pa_status pa_attention_int4(void* out, const void* q, const void* new_key, const
  * has no meaning.
  */
 
-/* Bytes of scratch pa_accumulate_weights needs (0 for sizes it does not take). */
+/* Bytes of scratch pa_accumulate_weights needs (0 for sizes it does not take): about 4 bytes
+ * for every query row and entry up to max_context_len. */
 size_t pa_accumulate_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                     int num_query_tokens, int max_context_len);
 

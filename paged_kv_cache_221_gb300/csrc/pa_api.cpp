@@ -371,9 +371,9 @@ bool int4_geometry(int head_dim, int block_size) {
   return (head_dim == 64 || head_dim == 128) && block_size == kBlockSize;
 }
 
-// One thread per 8 dims, 256 a CTA: the grid's x extent.
+// At most one thread per 8 dims, 256 a CTA (the grid's x extent); token numbers stay below 2^30.
 bool int4_store_fits(long long tokens, int hkv, int head_dim) {
-  return tokens * hkv * (head_dim / 8) < (1ll << 31) * 256;
+  return tokens <= (1ll << 30) && tokens * hkv * (head_dim / 8) < (1ll << 31) * 256;
 }
 
 // Entries a sequence's query tokens can see, rounded up to where blocks begin.

@@ -8,6 +8,21 @@
 // (pa_pages.cuh), scales multiply score accumulators and softmax weights, and
 // everything that only an edge page needs is behind one branch.
 //
+// The tiles are those of the other attention kernels: S^T[16 tokens x 8 rows] = K . Q^T and
+// O^T[D x 8] += V^T . P^T, so that a page is one step.  Scores: two k steps per group of
+// 32 dims, times the tokens' scales in fp32.  P.V: the weights, f16, are transposed by
+// movmatrix, multiplied by the group's scales of their tokens, and meet V codes that
+// ldmatrix.trans delivers as (token 2q, token 2q + 1) pairs of four dims each.
+//
+// Measured (GPU time of a call, bytes of every page once, against a copy's 6780 GB/s): 64
+// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 40.5 us, 161 MB (0.59; the kernel
+// alone 36 us, 0.66); 256 of 128-8192, 64/8 heads, 114 us, 551 MB (0.71); one of 131071 37 us
+// (0.57); five drafts over 32 of 2048-16384 120 us, 324 MB (0.40).  What bounds it: for up to
+// 8 rows memory from the first page to the last (0.68 us per page and warp on 12 warps per
+// SM), 3.5 us to find the work and the first block ids, an uneven end of 5 us and the merge,
+// 5 us; for 24 rows the latency of dependent tensor-core and FP32 steps with the 8 warps
+// per SM that 255 registers allow (tensor pipe 49 %, issue slots 45 %).
+//
 // Balanced mode (kFlat): runs of pa_runs.cuh.  A job that lies in one run is written out
 // directly; the others leave (m, l, O) partials, which attn4_merge_kernel joins.
 // Unit mode: units of a fixed size; the split-KV merge joins the partitions.  The result of a
@@ -289,12 +304,14 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
             w3 = y >> 16;
           }
         }
-        if (edge) {                            // rows past the context may hold any scale, even NaN
+        if (edge) {
+          // entries that no query token sees may hold any scale, even NaN
           const int nv = end_of(k) - (tok0 + k * kBlockSize);
-          w0 = 2 * q4 < nv ? w0 : 0u;
-          w1 = 2 * q4 + 1 < nv ? w1 : 0u;
-          w2 = 2 * q4 + 8 < nv ? w2 : 0u;
-          w3 = 2 * q4 + 9 < nv ? w3 : 0u;
+          const int from = p.window > 0 ? L - T - p.window + 1 - (tok0 + k * kBlockSize) : 0;
+          w0 = 2 * q4 < nv && 2 * q4 >= from ? w0 : 0u;
+          w1 = 2 * q4 + 1 < nv && 2 * q4 + 1 >= from ? w1 : 0u;
+          w2 = 2 * q4 + 8 < nv && 2 * q4 + 8 >= from ? w2 : 0u;
+          w3 = 2 * q4 + 9 < nv && 2 * q4 + 9 >= from ? w3 : 0u;
         }
         {
           uint32_t za, zb, none;

