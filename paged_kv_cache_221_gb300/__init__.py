@@ -435,12 +435,14 @@ _KV_BF16, _KV_FP8, _KV_INT4 = 0, 1, 2
 # The calls below are made once per layer and token, so their host time counts: arguments are
 # checked with a few attribute reads each (``_need`` words the error), sizes of workspaces are
 # computed once per shape, and pointers go to ctypes as plain integers.
+_Tensor, _u8, _bf16, _f32, _i32, _i64 = (torch.Tensor, torch.uint8, torch.bfloat16, torch.float32,
+                                         torch.int32, torch.int64)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _is(t, dtype, ndim, index):
-    return (t.__class__ is torch.Tensor and t.dtype is dtype and t.dim() == ndim
-            and t.get_device() == index and t.is_contiguous())
+    return (t.__class__ is _Tensor and t.dtype is dtype and t.get_device() == index
+            and t.dim() == ndim and t.is_contiguous())
 
 
 def _want(name, t, dtype, ndim, dev):
@@ -448,18 +450,22 @@ def _want(name, t, dtype, ndim, dev):
         _need(name, t, dtype, ndim, dev)
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    return getattr(_lib.load(), name)
+
+
 def _call(name, dev, *args):
     """library().name(*args, stream) with dev current, on its current stream."""
     index = dev.index
-    fn = getattr(_lib.load(), name)
     stream = _raw_stream(index) if _raw_stream is not None else \
         torch.cuda.current_stream(dev).cuda_stream
     if torch.cuda.current_device() == index:
-        st = fn(*args, stream)
+        st = _entry(name)(*args, stream)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, stream)
-    if st != _lib.PA_OK:
+            st = _entry(name)(*args, stream)
+    if st:
         _lib.check(name, st)
 
 
@@ -478,23 +484,25 @@ _INT4_DIMS = {int4_page_bytes(d): d for d in (64, 128)}
 
 
 def _int4_pools(k_cache, v_cache, k_scale, v_scale):
-    if not (isinstance(k_cache, torch.Tensor) and _is(k_cache, torch.uint8, 3, k_cache.get_device())
-            and k_cache.is_cuda):
-        _need("k_cache", k_cache, torch.uint8, 3)
+    if not isinstance(k_cache, _Tensor) or not k_cache.is_cuda:
+        _need("k_cache", k_cache, _u8, 3)
     dev = k_cache.device
-    _want("v_cache", v_cache, torch.uint8, 3, dev)
+    index = dev.index
+    if not (_is(k_cache, _u8, 3, index) and _is(v_cache, _u8, 3, index) and
+            _is(k_scale, _f32, 1, index) and _is(v_scale, _f32, 1, index)):
+        for name, t, dtype, ndim in (("k_cache", k_cache, _u8, 3), ("v_cache", v_cache, _u8, 3),
+                                     ("k_scale", k_scale, _f32, 1), ("v_scale", v_scale, _f32, 1)):
+            _need(name, t, dtype, ndim, dev)
     shape = k_cache.shape
-    if v_cache.shape != shape:
-        raise ValueError("inconsistent shapes")
     NB, Hkv, page = shape
     D = _INT4_DIMS.get(page)
     if D is None:
         raise ValueError("INT4 pools are [num_blocks, num_kv_heads, int4_page_bytes(head_dim)] "
                          f"with head_dim 64 or 128, got pages of {page} bytes")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _want(name, t, torch.float32, 1, dev)
-        if t.numel() != Hkv:
-            raise ValueError(f"{name} must have num_kv_heads entries")
+    if v_cache.shape != shape:
+        raise ValueError("inconsistent shapes")
+    if k_scale.numel() != Hkv or v_scale.numel() != Hkv:
+        raise ValueError("k_scale and v_scale must have num_kv_heads entries")
     return dev, NB, Hkv, D
 
 
@@ -504,9 +512,9 @@ def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torc
     """Quantise new bf16 K/V rows [N, Hkv, D] into INT4 pages at their slots (negative slots
     are skipped)."""
     dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
-    _want("key", key, torch.bfloat16, 3, dev)
-    _want("value", value, torch.bfloat16, 3, dev)
-    _want("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    _want("key", key, _bf16, 3, dev)
+    _want("value", value, _bf16, 3, dev)
+    _want("slot_mapping", slot_mapping, _i64, 1, dev)
     shape = key.shape
     N = shape[0]
     if shape != (N, Hkv, D) or value.shape != shape or slot_mapping.numel() != N:
@@ -521,9 +529,9 @@ def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping
     """The values held in INT4 slots as bf16: (key, value), each [N, Hkv, D]; rows with a
     negative slot are zero."""
     dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
-    _want("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    _want("slot_mapping", slot_mapping, _i64, 1, dev)
     N = slot_mapping.numel()
-    key = torch.empty((N, Hkv, D), dtype=torch.bfloat16, device=dev)
+    key = torch.empty((N, Hkv, D), dtype=_bf16, device=dev)
     value = torch.empty_like(key)
     _call("pa_gather_cache_int4", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), slot_mapping.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), N,
@@ -563,13 +571,18 @@ def attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     query token to its last ``window_size`` positions.
     """
     dev, NB, Hkv, D = _int4_pools(k_cache, v_cache, k_scale, v_scale)
-    ndim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
-    _want("q", q, torch.bfloat16, ndim, dev)
-    _want("block_tables", block_tables, torch.int32, 2, dev)
-    _want("context_lens", context_lens, torch.int32, 1, dev)
+    index = dev.index
+    ndim = 3 if isinstance(q, _Tensor) and q.dim() == 3 else 4
+    if not (_is(q, _bf16, ndim, index) and _is(block_tables, _i32, 2, index) and
+            _is(context_lens, _i32, 1, index)):
+        _need("q", q, _bf16, ndim, dev)
+        _need("block_tables", block_tables, _i32, 2, dev)
+        _need("context_lens", context_lens, _i32, 1, dev)
     shape = q.shape
-    B, Hq, Dq = shape[0], shape[-2], shape[-1]
-    T = 1 if ndim == 3 else shape[1]
+    if ndim == 4:
+        B, T, Hq, Dq = shape
+    else:
+        (B, Hq, Dq), T = shape, 1
     rows, mbs = block_tables.shape
     if Dq != D or rows != B or context_lens.numel() != B:
         raise ValueError("inconsistent shapes")
@@ -577,7 +590,7 @@ def attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if out is None:
         out = torch.empty_like(q)
     else:
-        _want("out", out, torch.bfloat16, ndim, dev)
+        _want("out", out, _bf16, ndim, dev)
         if out.shape != shape:
             raise ValueError("out must have q's shape")
     nk = nv = None
@@ -585,7 +598,7 @@ def attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         if new_key is None or new_value is None:
             raise ValueError("new_key and new_value go together")
         for name, t in (("new_key", new_key), ("new_value", new_value)):
-            _want(name, t, torch.bfloat16, t.dim() if isinstance(t, torch.Tensor) else 3, dev)
+            _want(name, t, _bf16, t.dim() if isinstance(t, _Tensor) else 3, dev)
             if t.numel() != B * T * Hkv * D:
                 raise ValueError(f"{name} must hold [B, T, Hkv, D] values")
         nk, nv = new_key.data_ptr(), new_value.data_ptr()
@@ -609,14 +622,14 @@ def _stat(name, t, dtype, dev, B, Hkv, mcl):
 
 def _kv_format(k_cache):
     """(format, dtype, dims) of a K pool by its type and shape."""
-    if not isinstance(k_cache, torch.Tensor):
+    if not isinstance(k_cache, _Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
-    if k_cache.dtype is torch.bfloat16:
-        fmt = _KV_BF16, torch.bfloat16, 4
+    if k_cache.dtype is _bf16:
+        fmt = _KV_BF16, _bf16, 4
     elif k_cache.dim() == 3:
-        fmt = _KV_INT4, torch.uint8, 3
+        fmt = _KV_INT4, _u8, 3
     else:
-        fmt = _KV_FP8, torch.uint8, 4
+        fmt = _KV_FP8, _u8, 4
     if not (k_cache.is_cuda and _is(k_cache, fmt[1], fmt[2], k_cache.get_device())):
         _need("k_cache", k_cache, fmt[1], fmt[2])
     return fmt
@@ -649,13 +662,18 @@ def accumulate_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: tor
     dev = k_cache.device
     pool = k_cache.shape
     NB, Hkv = pool[0], pool[1]
-    ndim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
-    _want("q", q, torch.bfloat16, ndim, dev)
-    _want("block_tables", block_tables, torch.int32, 2, dev)
-    _want("context_lens", context_lens, torch.int32, 1, dev)
+    index = dev.index
+    ndim = 3 if isinstance(q, _Tensor) and q.dim() == 3 else 4
+    if not (_is(q, _bf16, ndim, index) and _is(block_tables, _i32, 2, index) and
+            _is(context_lens, _i32, 1, index)):
+        _need("q", q, _bf16, ndim, dev)
+        _need("block_tables", block_tables, _i32, 2, dev)
+        _need("context_lens", context_lens, _i32, 1, dev)
     shape = q.shape
-    B, Hq, D = shape[0], shape[-2], shape[-1]
-    T = 1 if ndim == 3 else shape[1]
+    if ndim == 4:
+        B, T, Hq, D = shape
+    else:
+        (B, Hq, D), T = shape, 1
     rows, mbs = block_tables.shape
     page = (NB, Hkv, int4_page_bytes(D)) if fmt == _KV_INT4 else (NB, Hkv, 16, D)
     if pool != page or rows != B or context_lens.numel() != B:
@@ -664,20 +682,20 @@ def accumulate_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: tor
         if k_scale is not None:
             raise ValueError("bf16 pages take no k_scale")
     else:
-        _want("k_scale", k_scale, torch.float32, 1, dev)
+        _want("k_scale", k_scale, _f32, 1, dev)
         if k_scale.numel() != Hkv:
             raise ValueError("k_scale must have num_kv_heads entries")
     mcl = _max_len(max_context_len, context_lens, T)
-    entries = _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
+    entries = _stat("weights", weights, _f32, dev, B, Hkv, mcl)
     if out is None:
         out = weights
-    elif _stat("out", out, torch.float32, dev, B, Hkv, mcl) != entries:
+    elif _stat("out", out, _f32, dev, B, Hkv, mcl) != entries:
         raise ValueError("out must have the shape of weights")
     if positions is not None and \
-            _stat("positions", positions, torch.int32, dev, B, Hkv, mcl) != entries:
+            _stat("positions", positions, _i32, dev, B, Hkv, mcl) != entries:
         raise ValueError("positions must have the shape of weights")
     if seq_lens is not None:
-        _want("seq_lens", seq_lens, torch.int32, 1, dev)
+        _want("seq_lens", seq_lens, _i32, 1, dev)
         if seq_lens.numel() != B:
             raise ValueError("inconsistent shapes")
     need = accumulate_workspace_size(B, Hq, Hkv, T, mcl)
@@ -720,15 +738,15 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
     else:
         BS, D = pool[2], pool[3]
         good = v_cache.shape == ((NB, Hkv, D, BS) if fmt == _KV_FP8 else pool)
-    _want("block_tables", block_tables, torch.int32, 2, dev)
-    _want("context_lens", context_lens, torch.int32, 1, dev)
+    _want("block_tables", block_tables, _i32, 2, dev)
+    _want("context_lens", context_lens, _i32, 1, dev)
     B = context_lens.numel()
     rows, mbs = block_tables.shape
     if not good or rows != B:
         raise ValueError("inconsistent shapes")
     mcl = max(1, _max_len(max_context_len, context_lens, 1))
-    entries = _stat("weights", weights, torch.float32, dev, B, Hkv, mcl)
-    if _stat("positions", positions, torch.int32, dev, B, Hkv, mcl) != entries:
+    entries = _stat("weights", weights, _f32, dev, B, Hkv, mcl)
+    if _stat("positions", positions, _i32, dev, B, Hkv, mcl) != entries:
         raise ValueError("positions must have the shape of weights")
     new_lens = torch.empty_like(context_lens)
     need = evict_workspace_size(B, Hkv, mcl, budget)
