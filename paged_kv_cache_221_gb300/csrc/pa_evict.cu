@@ -10,10 +10,12 @@ namespace pa {
 // A CTA joins the (m, l) of one (sequence, kv head)'s rows from the pieces of its job (a warp
 // per row) and then takes every gridDim.x-th tile of 512 entries, four per thread: each
 // thread copies its 16 bytes of every row's scores to shared memory, all rows in flight at
-// once, and sums over them.  As many CTAs as are resident at once, so that what they do
-// before the first tile is not repeated.  Bound by the scores' bytes: 189 MB of 20 rows (32
-// sequences of 2048-16384 tokens) take 46 us, past what L2 still holds of them; a second
-// buffer per CTA (half the CTAs) took 54.
+// once, and sums over them.  Twice as many CTAs as are resident at once: the jobs' lengths
+// differ, and what a CTA does before its first tile costs (a call with 1 / 2 / 4 times as many:
+// 121.6 / 118.4 / 123.1 us; equal runs of tiles per CTA: 121.1).  Bound by the scores' bytes on
+// their way out of L2 and back: 189 MB of 20 rows (32 sequences of 2048-16384 tokens) take 43
+// us; a second buffer per CTA (half the CTAs) took 8 us more, refilling each quarter of the
+// rows as it is read 6.
 constexpr int kSumThreads = 128, kSumEntries = 4 * kSumThreads;
 constexpr int kSumRowBytes = kSumEntries * 4;
 
@@ -110,7 +112,7 @@ cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
   const int pairs = p.num_seqs * p.Hkv, bytes = p.G * p.T * kSumRowBytes;
   const int resident = std::min(2048 / kSumThreads, 200 * 1024 / bytes);
   const int tiles = (p.max_ctx + kSumEntries - 1) / kSumEntries;
-  const int wanted = (kAttn4Sms * resident + pairs - 1) / pairs;
+  const int wanted = (2 * kAttn4Sms * resident + pairs - 1) / pairs;
   const cudaError_t e = allow_smem<observe_sum_kernel>(kMost);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(std::max(1, std::min(tiles, wanted))),

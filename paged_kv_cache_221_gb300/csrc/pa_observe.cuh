@@ -10,10 +10,11 @@
 // and repeats the part that binds the first launch.
 //
 // Measured (GPU time of a call): 64 sequences of 512-4096 tokens, 32/8 heads of 128 dims, bf16
-// pages, 62 us (302 MB of K; the first launch alone 53 us, 5.7 TB/s: bound by memory); five
-// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 121 us: 76 us of scores (160
-// MB of K, 189 MB written; 69 us with the stores left out: bound by the score tiles), 46
-// us of sums.
+// pages, 59 us (302 MB of K; the first launch alone 53 us, 5.7 TB/s: bound by memory); five
+// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 119 us: 76 us of scores (160
+// MB of K, 189 MB written; 69 us with the stores left out: bound by the score tiles), 43
+// us of sums.  The sequences in 2, 3 or 4 parts through one smaller scratch, so that the scores
+// stay in L2: 130, 146, 160 us.
 #pragma once
 
 #include "pa_runs.cuh"
@@ -58,6 +59,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB)
   const uint32_t swz = page_swizzle<F, D>(lane / P::kChunks, lane % P::kChunks);
   const uint32_t koff = ldsm_offset<F, D>(lane);
 
+  // The scores are read again by the second launch.  Where they are the smaller stream, and one
+  // column reads the pages, those leave the L2 cache first (64 sequences of 512-4096 tokens,
+  // bf16: 61.8 -> 58.8 us); where they are the larger one that loses (121.8 -> 124.4 us).
+  const uint64_t policy = read_policy(NTW == 1 && 4 * nrows * kBlockSize < P::kBytes);
   Cursor<kFlat> cur;
   Segment seg;
   bool invalid = false;
@@ -102,9 +107,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB)
           const uint32_t to = st_in + k * P::kBytes;
 #pragma unroll
           for (int c = 0; c < P::kCodes / 512; ++c)
-            cp_async_16(to + (swz ^ swizzle_step<F, D>(c)) + 512 * c, kp + 512 * c, 16);
+            cp_async_16_hint(to + (swz ^ swizzle_step<F, D>(c)) + 512 * c, kp + 512 * c, policy);
           if constexpr (P::kScales > 0) {
-            if (lane < P::kScales / 16) cp_async_16(to + P::kCodes + 16 * lane, kp + P::kCodes, 16);
+            if (lane < P::kScales / 16)
+              cp_async_16_hint(to + P::kCodes + 16 * lane, kp + P::kCodes, policy);
           }
         }
         it += TP;
