@@ -134,6 +134,12 @@ cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
 // newest position, 1 us more to the protected bits, 5 us for the four passes and 5 us for the two
 // exchanges, for 8192 entries with 1024 threads as for 2049 with 512.
 
+// Up to this many dropped entries are found one after the other (a decode step drops one per new
+// token).  64 x 8 rows of 2048 + n entries, the whole call: n = 1 / 4 / 8 / 12: 11.1 / 15.2 /
+// 19.7 / 24.2 us, 23.4 / 24.6 / 24.9 / 25.3 by the radix passes; 6000 + n entries: 21.4 / 31.6 /
+// 43.5 / 55.1 and 53.1 / 55.2 / 55.8 / 55.8.
+constexpr int kFewDropped = 8;
+
 // Larger for larger weights; -0 equals +0; NaN is below every number.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -170,6 +176,7 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   extern __shared__ uint32_t s_dyn[];        // staged: protected bits, then keys
   __shared__ int s_hist[256];
   __shared__ int2 s_warp[W];
+  __shared__ long long s_low[2][W];
   __shared__ int s_newest, s_protected, s_bad, s_digit, s_left;
   grid_launch_dependents();
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
@@ -243,9 +250,6 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   }
   if (lane == 0 && mine > 0) atomicAdd(&s_protected, mine);
   __syncthreads();
-  const bool among = s_protected >= p.budget;      // the threshold lies among the protected
-  int k = among ? p.budget : p.budget - s_protected;   // entries of that class to keep
-  const bool none = k == 0;
   auto is_protected = [&](int j) {
     if constexpr (kStaged) return ((s_prot[j >> 5] >> (j & 31)) & 1u) != 0u;
     return pos[j] > bar;
@@ -254,7 +258,64 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
     if constexpr (kStaged) return s_key[j];
     return weight_key(w[j]);
   };
+  int2* moves = p.moves + static_cast<size_t>(blockIdx.x) * p.max_moves;
 
+  const int drop = L - p.budget;
+  if (drop <= kFewDropped && L < (1 << 30)) {
+    // entry j as a number: the smallest ones go, an unprotected one before a protected one, then
+    // the smaller weight, then the higher index
+    constexpr long long kNone = 0x7fffffffffffffffll;
+    long long low = kNone, last = -1;        // this thread's smallest one above `last`
+    auto scan = [&]() {
+      low = kNone;
+#pragma unroll 4
+      for (int j = tid; j < L; j += kThreads) {
+        const long long x = static_cast<long long>(
+            (is_protected(j) ? 1ull << 62 : 0ull) |
+            (static_cast<unsigned long long>(key_of(j)) << 30) |
+            static_cast<unsigned>(0x3fffffff - j));
+        if (x > last) low = min(low, x);
+      }
+    };
+    int gone = -1;                           // lane i: the i-th dropped entry
+    scan();
+    for (int i = 0; i < drop; ++i) {
+      long long all = low;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all = min(all, __shfl_xor_sync(0xffffffffu, all, o));
+      if (lane == 0) s_low[i & 1][warp] = all;
+      __syncthreads();
+      all = s_low[i & 1][lane % W];
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) all = min(all, __shfl_xor_sync(0xffffffffu, all, o));
+      last = all;
+      if (low == last) scan();
+      if (lane == i) gone = 0x3fffffff - static_cast<int>(last & 0x3fffffff);
+    }
+    if (warp != 0) return;
+    // the dropped ones below `budget` are the gaps, the kept ones from it on the movers; both
+    // in rising order
+    const bool gap = gone >= 0 && gone < p.budget;
+    bool mover = lane < drop;
+    int before = 0;
+    for (int i = 0; i < drop; ++i) {
+      const int x = __shfl_sync(0xffffffffu, gone, i);
+      before += x < gone;                    // all dropped entries below a gap are gaps
+      if (x == p.budget + lane) mover = false;
+    }
+    const unsigned mb = __ballot_sync(0xffffffffu, mover);
+    if (gap) moves[before].y = gone;
+    if (mover) moves[__popc(mb & ((1u << lane) - 1u))].x = p.budget + lane;
+    if (lane == 0) {
+      *count = __popc(mb);
+      if (g == 0) p.new_lens[b] = p.budget;
+    }
+    return;
+  }
+
+  const bool among = s_protected >= p.budget;      // the threshold lies among the protected
+  int k = among ? p.budget : p.budget - s_protected;   // entries of that class to keep
+  const bool none = k == 0;
   // k-th largest key of the class, a byte at a time
   uint32_t prefix = 0, mask = 0;
   for (int shift = 24; shift >= 0 && !none; shift -= 8) {
@@ -320,7 +381,6 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   int2 total;
   const int ties_before = over_warps<W>(make_int2(ties, 0), total, s_warp).x;
   const unsigned below = (1u << lane) - 1u;
-  int2* moves = p.moves + static_cast<size_t>(blockIdx.x) * p.max_moves;
   int2 at = make_int2(0, 0);                 // gaps and movers before this warp's run
   for (int pass = 0; pass < 2; ++pass) {
     int seen = ties_before, gaps = 0, movers = 0;

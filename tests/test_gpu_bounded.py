@@ -285,6 +285,36 @@ def test_evict_context_past_shared_memory():
     assert torch.equal(got[budget:], old[budget:])
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "special", "equal"])
+@pytest.mark.parametrize("budget,recent", [(1, 1), (5, 0), (500, 100), (500, 497), (500, 500),
+                                           (5000, 37)])
+def test_evict_few(kind, budget, recent):
+    """A few entries too many, around the number up to which they are found one by one; protected
+    entries that leave fewer others than must go."""
+    c = Case(11, [budget + d for d in (1, 2, 3, 7, 8, 9, 20)], 2, 2, 64, T=0, fmt="int4")
+    w0, p0 = stats(np.random.default_rng(budget + recent), c.lens, 2, budget + 32, kind)
+    evict(c, Dev(c), w0, p0, budget, recent)
+
+
+def test_evict_few_past_shared_memory():
+    n, budget = 60000, 59995
+    gen = torch.Generator("cuda").manual_seed(1)
+    k = torch.randn((n // 16, 1, 16, 64), generator=gen, device="cuda").bfloat16()
+    tables = torch.randperm(n // 16, generator=gen, device="cuda").int()[None]
+    w = torch.randint(0, 2000, (1, 1, n), generator=gen, device="cuda").float()
+    pos = torch.randperm(n, generator=gen, device="cuda").int().view(1, 1, n)
+    ref = BD.select(w[0, 0].cpu().numpy(), pos[0, 0].cpu().numpy(), budget, 1000)
+    at = torch.arange(n, device="cuda")
+    for a, z in ref:
+        at[z] = a
+    w0, p0, old = w.clone(), pos.clone(), k[tables[0].long()][:, 0].flatten(0, 1).clone()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    assert pa.evict_tokens(k, k.clone(), tables, lens, w, pos, budget, 1000, n).item() == budget
+    assert torch.equal(pos[0, 0, :budget], p0[0, 0][at[:budget]])
+    assert torch.equal(w[0, 0, :budget], w0[0, 0][at[:budget]])
+    assert torch.equal(k[tables[0].long()][:, 0].flatten(0, 1)[:budget], old[at[:budget]])
+
+
 def test_evict_in_order_keeps_the_tail():
     """Equal weights and positions in order: the newest and the lowest indices stay."""
     c = Case(9, [50], 1, 1, 64, T=0, fmt="bf16")
