@@ -112,22 +112,6 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
                : "memory");
 }
 
-// L2 policy of a read: the first to leave the cache, or the default.
-__device__ __forceinline__ uint64_t read_policy(bool once) {
-  uint64_t policy;
-  if (once)
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-  else
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-  return policy;
-}
-
-__device__ __forceinline__ void cp_async_16_hint(uint32_t dst, const void* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "l"(policy)
-               : "memory");
-}
-
 // Arrive on the mbarrier once every cp.async this thread issued so far has
 // landed (the arrival is counted in the barrier's expected count).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
