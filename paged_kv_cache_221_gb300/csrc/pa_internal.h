@@ -135,6 +135,8 @@ struct EvictParams {
   int2* moves;                    // scratch [B, Hkv, max_moves] (from, to)
   int32_t* counts;                // scratch [B, Hkv]
   int mbs, max_ctx, num_seqs, Hkv, num_blocks, weight_entries, budget, num_recent, max_moves;
+  int format, head_dim;           // of the pages
+  bool move_here;                 // few entries to drop: one launch
 };
 
 // The partition size (tokens) a per-sequence call with partition_size 0 uses:

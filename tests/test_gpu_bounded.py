@@ -296,6 +296,18 @@ def test_evict_few(kind, budget, recent):
     evict(c, Dev(c), w0, p0, budget, recent)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("budget,recent,over", [(1, 0, 8), (3, 3, 8), (90, 20, 8), (90, 20, 9),
+                                                (4090, 500, 6), (4090, 500, 7)])
+def test_evict_with_a_close_bound(fmt, D, budget, recent, over):
+    """max_context_len leaves at most 8 entries to drop (one launch), or just more."""
+    c = Case(12 + over, [budget + over, budget + over - 1, budget + 1, budget, 0], 4, 2, D, T=0,
+             fmt=fmt)
+    w0, p0 = stats(np.random.default_rng(over), c.lens, 2, budget + 16, "ties")
+    evict(c, Dev(c), w0, p0, budget, recent)
+
+
 def test_evict_few_past_shared_memory():
     n, budget = 60000, 59995
     gen = torch.Generator("cuda").manual_seed(1)
