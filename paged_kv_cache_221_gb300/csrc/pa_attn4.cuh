@@ -15,12 +15,12 @@
 // ldmatrix.trans delivers as (token 2q, token 2q + 1) pairs of four dims each.
 //
 // Measured (GPU time of a call, bytes of every page once, against a copy's 6780 GB/s): 64
-// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 40.5 us, 161 MB (0.59; the kernel
-// alone 36 us, 0.66); 256 of 128-8192, 64/8 heads, 114 us, 551 MB (0.71); one of 131071 37 us
-// (0.57); five drafts over 32 of 2048-16384 120 us, 324 MB (0.40).  What bounds it: for up to
-// 8 rows memory from the first page to the last (0.68 us per page and warp on 12 warps per
-// SM), 3.5 us to find the work and the first block ids, an uneven end of 5 us and the merge,
-// 5 us; for 24 rows the latency of dependent tensor-core and FP32 steps with the 8 warps
+// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 39.8 us, 161 MB (0.60); 256 of 128-8192,
+// 64/8 heads, 109 us, 551 MB (0.75); one of 131071 35.7 us (0.59); five drafts over 32 of
+// 2048-16384 119 us, 324 MB (0.40).  What bounds it: for up to 8 rows memory and issue slots
+// (DRAM 56 %, issue 50 % of the whole launch) from the first page to the last, 5 us before that
+// (2 to find the work, 3 for block ids and the first page), 3 us of uneven end and the merge, 4
+// us; for 24 rows the latency of dependent tensor-core and FP32 steps with the 8 warps
 // per SM that 255 registers allow (tensor pipe 49 %, issue slots 45 %).
 //
 // Balanced mode (kFlat): runs of pa_runs.cuh.  A job that lies in one run is written out
@@ -34,11 +34,11 @@
 namespace pa {
 
 // NT n-tiles of 8 query rows per warp, NTW row columns (each a worker's job of its own), TP
-// pages per softmax step, STAGES staged steps per warp, MINB CTAs of 4 warps per SM.
-template <int NT_, int NTW_, int TP_, int STAGES_, int MINB_>
+// pages per softmax step, STAGES staged steps per warp, MINB CTAs of WARPS warps per SM.
+template <int NT_, int NTW_, int TP_, int STAGES_, int MINB_, int WARPS_ = 4>
 struct Cfg4 {
   static constexpr int NT = NT_, NTW = NTW_, TP = TP_, STAGES = STAGES_, MINB = MINB_;
-  static constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 8 * NT;
+  static constexpr int kWarps = WARPS_, kThreads = 32 * kWarps, kRows = 8 * NT;
   static constexpr bool kQRegs = NT <= 2;
   static_assert(32 % TP == 0, "a step's pages come from one batch of block ids");
 };
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   uint8_t* smem = smem_all + warp * Sm::kWarpBytes;
   const int G = p.G, T = p.T, nrows = G * T;
   const RunList list = run_list(p, NTW);
-  const int worker = blockIdx.x * C::kWarps + warp;
+  const int worker = warp * gridDim.x + blockIdx.x;
 
   // Per lane: its chunks within a page (chunk `lane` of K and of V, and one of the scale
   // chunks) and their place in a stage.
@@ -496,13 +496,16 @@ template <int D, class C>
 cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
   constexpr int bytes = Smem4<D, C>::kBytes;
   constexpr Attn4Tile tile = attn4_tile(C::kRows * C::NTW);
-  static_assert(tile.nt == C::NT && tile.ntw == C::NTW && tile.ctas == C::MINB, "the host's tile");
+  static_assert(tile.nt == C::NT && tile.ntw == C::NTW && 4 * tile.ctas == C::MINB * C::kWarps,
+                "the host's tile");
   const long long jobs = static_cast<long long>(p.num_seqs) * p.Hkv * C::NTW;
   auto fn = p.flat ? paged_attn4_kernel<D, C, true> : paged_attn4_kernel<D, C, false>;
   const cudaError_t e = p.flat ? allow_smem<paged_attn4_kernel<D, C, true>>(bytes)
                                : allow_smem<paged_attn4_kernel<D, C, false>>(bytes);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>((p.workers + C::kWarps - 1) / C::kWarps);
+  // over the SMs first
+  const unsigned grid = static_cast<unsigned>(std::max(
+      std::min(p.workers, kAttn4Sms * C::MINB), (p.workers + C::kWarps - 1) / C::kWarps));
   const cudaError_t r = launch_behind(fn, dim3(grid), C::kThreads, bytes, s, p.after_store, p);
   if (r != cudaSuccess || !p.flat) return r;
   const int live = std::min(C::kRows, p.G * p.T);   // rows of a tile that are used
@@ -520,12 +523,15 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_attn4(const Attn4Params& p, int rows, cudaStream_t s) {
-  // Pages in flight per warp: with more (a ring of 6 or 8 single pages) the queues in front of
-  // memory grow and every dependent fetch at a job's start waits longer.  64 sequences of
-  // 512-4096 tokens, 4 rows: 41.0 us with rings of 3 double pages, 40.9 / 41.1 / 43.2 / 45.1
-  // with 3 / 4 / 6 / 8 single ones; 256 of 128-8192 tokens, 8 rows: 115.1 and 116.0 / 115.7
-  // / 118.4 / 121.3.  16 warps per SM instead of 12 (128 registers): 43.9 and 123.
-  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 2, 3, 3>>(p, s);
+  // One CTA of all the warps that an SM holds: its warps keep pace, where of three CTAs of four
+  // the oldest was served first and ended at 26 us, the newest at 33 (64 sequences of 512-4096
+  // tokens, 4 rows: 40.4 -> 39.8 us; 256 of 128-8192, 8 rows: 118.0 -> 112.4).  With 16 and 24
+  // rows it loses (56.1 -> 58.3, 119 -> 129 us).
+  // Pages in flight per warp: with more of them the queues in front of memory grow and every
+  // dependent fetch at a job's start waits longer.  Those two batches with rings of 3 / 4 / 6
+  // single pages: 39.8 / 39.8 / 41.1 and 114.3 / 112.4 / 112.9 us; of 3 / 4 double ones:
+  // 39.9 / 41.1 and 113.2 / 115.6.  16 warps per SM instead of 12 (128 registers): 41.8 and 118.
+  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 1, 4, 1, 12>>(p, s);
   if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 1, 4, 2>>(p, s);
   // 20 rows, 32 sequences of 2048-16384 tokens: 120 us, 125 with double pages, 182 with 12 warps
   // (168 registers: the output tile spills)

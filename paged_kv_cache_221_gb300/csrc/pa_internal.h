@@ -79,7 +79,7 @@ struct Attn4Params : AttnParams {
   bool after_store;               // follows the launch that stores the call's new tokens
 };
 // Tile of a warp for `rows` query rows per kv head: n-tiles of 8 rows, row columns, and the
-// CTAs of four warps that an SM holds.
+// groups of four warps that an SM holds.
 struct Attn4Tile {
   int nt, ntw, ctas;
 };
