@@ -451,10 +451,10 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
 // ---------------------------------------------------------------- moves
 // A warp copies kBatch entries at a time, all loads of a batch in flight before its first
 // store: their K and V rows, weights and positions.  16 prompts of 4096-8192 tokens cut to 2048
-// entries: 183 MB of bf16 rows in and out in 33 us (5.5 TB/s; 48 us with one move in flight).
+// entries: 183 MB of bf16 rows in and out in 30 us (6.1 TB/s; 48 us with one move in flight).
 // Gaps lie below `budget` and movers at or
 // above it, so no copy reads what another writes.
-constexpr int kMoveThreads = 256, kBatch = 4;
+constexpr int kMoveThreads = 128, kBatch = 4;
 
 template <int F, int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
@@ -551,8 +551,10 @@ cudaError_t launch_evict(const EvictParams& params, int format, int head_dim, cu
   // few entries per (sequence, kv head): smaller CTAs, more of them at once
   cudaError_t e = p.max_ctx <= 4096 ? launch_select<16>(p, s) : launch_select<32>(p, s);
   if (e != cudaSuccess || p.move_here) return e;
-  // about 8 CTAs per SM in all, at most one batch per warp
-  const int want = std::max(1, 8 * 152 / pairs);
+  // At most one batch per warp, and about 40 CTAs per SM in all: 4 waves, so that rows with more
+  // moves than others leave no tail (evicting from those 16 prompts, the whole call: 58.1 us with
+  // 8 CTAs of 8 warps per SM, 55.0 so).
+  const int want = std::max(1, 40 * kAttn4Sms / pairs);
   const int per_cta = kMoveThreads / 32 * kBatch;
   const int most = (p.max_moves + per_cta - 1) / per_cta;
   const dim3 grid(static_cast<unsigned>(std::min(want, most)), static_cast<unsigned>(pairs));
