@@ -471,6 +471,29 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
   }
 }
 
+// ---------------------------------------------------------------- pairs of fp32 values
+// One instruction for two values, each rounded to nearest.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // ---------------------------------------------------------------- INT4 quantisation
 // A thread's group of 32 dims (bf16 pairs in w): its codes (dim i in bits 4 (i % 8) of word
 // i / 8) and scale byte:
@@ -480,7 +503,10 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
 // The quotient is x * (1 / step) with one correction by its residual, which makes
 // ties come out exact; it is rounded by adding 1.5 * 2^23 + 8 (to nearest even), whose
 // low bits then are the code, and the codes of a word are strung together by multiply-adds
-// on the whole bit patterns, whose constant parts are taken off at the end.
+// on the whole bit patterns, whose constant parts are taken off at the end.  Two values share
+// each of these four steps.  Only a scale that saturated or is subnormal lets a quotient
+// reach 7.5: rounding to nearest takes at most 1/17 off a normal one, so that it is at most
+// 7 * 17 / 16 < 7.46875.
 __device__ __forceinline__ void quantize_int4_32(const uint32_t (&w)[16], float head_scale,
                                                  uint32_t (&codes)[4], uint32_t& scale_byte) {
   uint32_t mb = 0;                            // largest magnitudes as bf16 bits (NaN on top)
@@ -494,20 +520,27 @@ __device__ __forceinline__ void quantize_int4_32(const uint32_t (&w)[16], float 
                      head_scale;
   const bool good = step > 0.f;               // not zero, not NaN
   const float inv = good ? __frcp_rn(step) : 0.f;
-  const float lim = 7.25f * step;             // beyond it the code is +-7
+  const float lim = 7.46875f * step;          // beyond it the code is +-7
   constexpr float kMagic = 12582912.f + 8.f;
   constexpr uint32_t kBase = 0x4B400000u;     // bits of 12582912.f
   constexpr uint32_t kBases = kBase * 0x11111111u;
+  const bool clamp = !(amax <= lim);
+  const uint64_t inv2 = pack_f32x2(inv, inv), minus2 = pack_f32x2(-step, -step);
+  const uint64_t magic2 = pack_f32x2(kMagic, kMagic);
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     uint32_t c = 0;
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      const uint32_t pair = w[4 * v + (i >> 1)];
-      const float x = fminf(fmaxf((i & 1) ? bf16_hi(pair) : bf16_lo(pair), -lim), lim);
-      const float y = x * inv;
-      const float q = fmaf(fmaf(-y, step, x), inv, y);
-      c = c * 16u + __float_as_uint(q + kMagic);
+    for (int i = 3; i >= 0; --i) {
+      float lo = bf16_lo(w[4 * v + i]), hi = bf16_hi(w[4 * v + i]);
+      if (clamp) {
+        lo = fminf(fmaxf(lo, -lim), lim);
+        hi = fminf(fmaxf(hi, -lim), lim);
+      }
+      const uint64_t x = pack_f32x2(lo, hi);
+      const uint64_t y = mul_f32x2(x, inv2);
+      const uint64_t q = add_f32x2(fma_f32x2(fma_f32x2(y, minus2, x), inv2, y), magic2);
+      c = (c * 16u + static_cast<uint32_t>(q >> 32)) * 16u + static_cast<uint32_t>(q);
     }
     codes[v] = good ? c - kBases : 0x88888888u;
   }
