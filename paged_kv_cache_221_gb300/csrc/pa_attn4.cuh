@@ -15,12 +15,12 @@
 // ldmatrix.trans delivers as (token 2q, token 2q + 1) pairs of four dims each.
 //
 // Measured (GPU time of a call, bytes of every page once, against a copy's 6780 GB/s): 64
-// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 39.8 us, 161 MB (0.60); 256 of 128-8192,
-// 64/8 heads, 109 us, 551 MB (0.75); one of 131071 35.7 us (0.59); five drafts over 32 of
+// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 39.2 us, 161 MB (0.61); 256 of 128-8192,
+// 64/8 heads, 107 us, 551 MB (0.76); one of 131071 35.2 us (0.60); five drafts over 32 of
 // 2048-16384 119 us, 324 MB (0.40).  What bounds it: for up to 8 rows memory and issue slots
-// (DRAM 56 %, issue 50 % of the whole launch) from the first page to the last, 5 us before that
-// (2 to find the work, 3 for block ids and the first page), 3 us of uneven end and the merge, 4
-// us; for 24 rows the latency of dependent tensor-core and FP32 steps with the 8 warps
+// (DRAM 58-73 %, issue 56-60 % of the whole launch) from the first page to the last, 5 us
+// before that (2 to find the work, 3 for block ids and the first page), 3 us of uneven end and
+// the merge, 4 us; for 24 rows the latency of dependent tensor-core and FP32 steps with the 8 warps
 // per SM that 255 registers allow (tensor pipe 49 %, issue slots 45 %).
 //
 // Balanced mode (kFlat): runs of pa_runs.cuh.  A job that lies in one run is written out
@@ -228,14 +228,16 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
       // Online softmax: the reference m of a row moves only when a score passes it by
       // 7, so a weight is at most 2^7 and, times a V scale (at most 448), an f16 value.
       bool over = false;
+      float e[TP][NT][4];                    // scores less the reference
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float x = -CUDART_INF_F;
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
           const float* y = t[k][j];
-          x = fmaxf(x, fmaxf(fmaxf(fmaf(y[0], qo.rs0[j], nm0[j]), fmaf(y[2], qo.rs0[j], nm0[j])),
-                             fmaxf(fmaf(y[1], qo.rs1[j], nm1[j]), fmaf(y[3], qo.rs1[j], nm1[j]))));
+          fma_f32x2(e[k][j][0], e[k][j][1], y[0], y[1], qo.rs0[j], qo.rs1[j], nm0[j], nm1[j]);
+          fma_f32x2(e[k][j][2], e[k][j][3], y[2], y[3], qo.rs0[j], qo.rs1[j], nm0[j], nm1[j]);
+          x = fmaxf(x, fmaxf(fmaxf(e[k][j][0], e[k][j][1]), fmaxf(e[k][j][2], e[k][j][3])));
         }
         over |= x > 7.f;
       }
@@ -264,6 +266,13 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
             f1 = nm1[j] == kUnseen ? 0.f : hw_exp2(nm - nm1[j]);
             nm1[j] = nm;
           }
+#pragma unroll
+          for (int k = 0; k < TP; ++k) {
+            e[k][j][0] = fmaf(t[k][j][0], qo.rs0[j], nm0[j]);
+            e[k][j][1] = fmaf(t[k][j][1], qo.rs1[j], nm1[j]);
+            e[k][j][2] = fmaf(t[k][j][2], qo.rs0[j], nm0[j]);
+            e[k][j][3] = fmaf(t[k][j][3], qo.rs1[j], nm1[j]);
+          }
           z[j][0] *= f0;
           z[j][1] *= f1;
           z[j][2] *= f0;
@@ -282,10 +291,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
         uint32_t ph0[NT], ph1[NT];             // P^T: tokens 2q, 2q+1 and 2q+8, 2q+9 of row gid
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const float p0 = hw_exp2(fmaf(t[k][j][0], qo.rs0[j], nm0[j]));
-          const float p1 = hw_exp2(fmaf(t[k][j][1], qo.rs1[j], nm1[j]));
-          const float p2 = hw_exp2(fmaf(t[k][j][2], qo.rs0[j], nm0[j]));
-          const float p3 = hw_exp2(fmaf(t[k][j][3], qo.rs1[j], nm1[j]));
+          const float p0 = hw_exp2(e[k][j][0]);
+          const float p1 = hw_exp2(e[k][j][1]);
+          const float p2 = hw_exp2(e[k][j][2]);
+          const float p3 = hw_exp2(e[k][j][3]);
           ph0[j] = transpose_8x8(half2_bits(__floats2half2_rn(p0, p1)));
           ph1[j] = transpose_8x8(half2_bits(__floats2half2_rn(p2, p3)));
         }
@@ -525,7 +534,8 @@ template <int D>
 cudaError_t launch_attn4(const Attn4Params& p, int rows, cudaStream_t s) {
   // One CTA of all the warps that an SM holds: its warps keep pace, where of three CTAs of four
   // the oldest was served first and ended at 26 us, the newest at 33 (64 sequences of 512-4096
-  // tokens, 4 rows: 40.4 -> 39.8 us; 256 of 128-8192, 8 rows: 118.0 -> 112.4).  With 16 and 24
+  // tokens, 4 rows: 40.4 -> 39.8 us; 256 of 128-8192, 8 rows: 118.0 -> 112.4; before scores and
+  // softmax took two values per instruction, now 39.2 and 110.6).  With 16 and 24
   // rows it loses (56.1 -> 58.3, 119 -> 129 us).
   // Pages in flight per warp: with more of them the queues in front of memory grow and every
   // dependent fetch at a job's start waits longer.  Those two batches with rings of 3 / 4 / 6

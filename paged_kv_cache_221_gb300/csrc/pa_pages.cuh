@@ -330,6 +330,36 @@ __device__ __forceinline__ void make_q_operand(QOperand<F, D, NT, kRegs>& qo,
   if constexpr (!kRegs) qo.base = qt + lane * 8;
 }
 
+// ---------------------------------------------------------------- pairs of fp32 values
+// One instruction for two values, each rounded to nearest.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// (y0, y1) = (a0 b0 + c0, a1 b1 + c1)
+__device__ __forceinline__ void fma_f32x2(float& y0, float& y1, float a0, float a1, float b0,
+                                          float b1, float c0, float c1) {
+  const uint64_t y = fma_f32x2(pack_f32x2(a0, a1), pack_f32x2(b0, b1), pack_f32x2(c0, c1));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(y));
+}
+
 // D = A * B + C and D += A * B on f16 operands; without side effects, so that the compiler
 // may move them.
 __device__ __forceinline__ void mma_f16_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -422,10 +452,9 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          t[j][0] = fmaf(d[h][j][0], s0[g2 + h], t[j][0]);
-          t[j][1] = fmaf(d[h][j][1], s0[g2 + h], t[j][1]);
-          t[j][2] = fmaf(d[h][j][2], s1[g2 + h], t[j][2]);
-          t[j][3] = fmaf(d[h][j][3], s1[g2 + h], t[j][3]);
+          const float a = s0[g2 + h], c = s1[g2 + h];
+          fma_f32x2(t[j][0], t[j][1], d[h][j][0], d[h][j][1], a, a, t[j][0], t[j][1]);
+          fma_f32x2(t[j][2], t[j][3], d[h][j][2], d[h][j][3], c, c, t[j][2], t[j][3]);
         }
     }
   } else {
@@ -469,29 +498,6 @@ __device__ __forceinline__ void page_scores(float (&t)[NT][4], uint32_t page, ui
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[j][e] += u[j][e];
   }
-}
-
-// ---------------------------------------------------------------- pairs of fp32 values
-// One instruction for two values, each rounded to nearest.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // ---------------------------------------------------------------- INT4 quantisation
