@@ -125,19 +125,18 @@ cudaError_t launch_observe_sum(const ObserveParams& p, cudaStream_t s) {
 // order (newest num_recent first, larger weight, lower index).  Either all protected
 // (newest) entries stay and the threshold lies among the others, or it lies among the
 // protected ones; a radix selection over the weights' order-preserving bits finds it
-// in four passes.  Weights and positions are read once: keys and the protected bits
-// stay in shared memory (contexts too long for it are read again at every pass).  Each
-// warp then owns a run of consecutive entries: a ballot per 32 of them and one exchange
-// between the warps settle which ties stay (the lowest indices), a second exchange numbers
-// the dropped entries below `budget` (the gaps) and the kept ones from `budget` on
-// (the movers), and pair i becomes (i-th mover, i-th gap).  Bound by latency: 2.4 us to the
-// newest position, 1 us more to the protected bits, 5 us for the four passes and 5 us for the two
-// exchanges, for 8192 entries with 1024 threads as for 2049 with 512.
+// in four passes.  Weights and positions are read once: a warp owns a run of consecutive
+// entries and keeps them in registers; past 16384 entries keys and protected bits stay in
+// shared memory, and what does not fit there is read again at every pass.  A ballot per 32
+// entries and one exchange between the warps settle which ties stay (the lowest indices), a
+// second exchange numbers the dropped entries below `budget` (the gaps) and the kept ones from
+// `budget` on (the movers), and pair i becomes (i-th mover, i-th gap).  Bound by instructions
+// and barriers: 16 rows x 8 heads of 4096-8192 entries, the whole eviction 55.0 us with the keys
+// in shared memory (8 M instructions, most of them re-deriving what a register holds), 50.0 so.
 
 // Up to this many dropped entries are found one after the other (a decode step drops one per new
-// token).  64 x 8 rows of 2048 + n entries, the whole call: n = 1 / 4 / 8 / 12: 11.1 / 15.2 /
-// 19.7 / 24.2 us, 23.4 / 24.6 / 24.9 / 25.3 by the radix passes; 6000 + n entries: 21.4 / 31.6 /
-// 43.5 / 55.1 and 53.1 / 55.2 / 55.8 / 55.8.
+// token).  64 x 8 rows of 2048 + n entries, the whole call: n = 1 / 4 / 8: 7.4 / 9.7 / 13.2 us,
+// 18.7 by the radix passes (n = 12); 6000 + n entries: 13.2 / 17.1 / 23.0 and 38.4 us.
 constexpr int kFewDropped = 8;
 
 // Larger for larger weights; -0 equals +0; NaN is below every number.
@@ -172,7 +171,7 @@ __device__ __forceinline__ int2 over_warps(int2 mine, int2& total, int2* sh) {
 
 // One entry to its new place, a warp: its K and V rows, weight and position.  For the few moves
 // of a decode step, which the selecting CTA makes itself (the bounded decode step 91.5 -> 89.5 us
-// on the GPU and one launch less on the host).
+// on the GPU and a launch less on the host).
 __device__ __forceinline__ void move_entry(const EvictParams& p, int b, int g, int2 mv, size_t row,
                                            int lane) {
   const int D = p.head_dim;
@@ -204,8 +203,250 @@ __device__ __forceinline__ void move_entry(const EvictParams& p, int b, int g, i
   }
 }
 
-template <int W, bool kStaged>
+// Sequences with nothing to drop, and lengths out of range, which are reported.
+__device__ __forceinline__ bool left_alone(const EvictParams& p, int b, int g, int L) {
+  const bool invalid = L < 0 || L > p.max_ctx;
+  if (!invalid && L > p.budget) return false;
+  if (threadIdx.x == 0) {
+    p.counts[blockIdx.x] = 0;
+    if (g == 0) {
+      p.new_lens[b] = L;
+      if (invalid) atomicOr(&g_pa_err, kErrBounds);
+    }
+  }
+  return true;
+}
+
+// A block outside the pool: the sequence is left as it is (every head sees the same table).
+__device__ __forceinline__ bool bad_block(const EvictParams& p, int b, int L, int threads) {
+  bool bad = false;
+  for (int i = threadIdx.x; i < (L + kBlockSize - 1) / kBlockSize; i += threads)
+    bad |= static_cast<unsigned>(p.block_tables[static_cast<size_t>(b) * p.mbs + i]) >=
+           static_cast<unsigned>(p.num_blocks);
+  return bad;
+}
+
+__device__ __forceinline__ void leave_bad(const EvictParams& p, int b, int g, int L) {
+  if (threadIdx.x != 0) return;
+  p.counts[blockIdx.x] = 0;
+  if (g == 0) {
+    p.new_lens[b] = L;
+    atomicOr(&g_pa_err, kErrBounds);
+  }
+}
+
+// The digit at which a class's keys from the top reach k, and how many of that digit are among
+// the k: from the counts of 256 digits.  A warp.
+__device__ __forceinline__ void find_digit(const int* hist, int k, int lane, int& digit, int& left) {
+  // bins 255 - 8 lane .. 248 - 8 lane
+  int h[8], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = hist[255 - 8 * lane - i];
+    sum += h[i];
+  }
+  int above = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, above, o);
+    if (lane >= o) above += a;
+  }
+  above -= sum;
+  const bool here = above < k && above + sum >= k;
+  int d = -1, l = k - above;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (d < 0 && h[i] >= l) d = 255 - 8 * lane - i;
+    if (d < 0) l -= h[i];
+  }
+  const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  digit = __shfl_sync(0xffffffffu, d, at);
+  left = __shfl_sync(0xffffffffu, l, at);
+}
+
+// The moves of a few dropped entries (lane i holds the i-th, -1 from `drop` on), in rising order
+// of both their ends: the dropped ones below `budget` are the gaps, the kept ones from it on the
+// movers.  Their number.
+__device__ __forceinline__ int pair_few(int gone, int drop, int budget, int2* to, int lane) {
+  const bool gap = gone >= 0 && gone < budget;
+  bool mover = lane < drop;
+  int before = 0;
+  for (int i = 0; i < drop; ++i) {
+    const int x = __shfl_sync(0xffffffffu, gone, i);
+    before += x < gone;                      // all dropped entries below a gap are gaps
+    if (x == budget + lane) mover = false;
+  }
+  const unsigned mb = __ballot_sync(0xffffffffu, mover);
+  if (gap) to[before].y = gone;
+  if (mover) to[__popc(mb & ((1u << lane) - 1u))].x = budget + lane;
+  return __popc(mb);
+}
+
+// Up to E entries per thread, in registers: a warp owns up to 32 E consecutive ones.
+template <int W, int E>
 __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams p) {
+  constexpr int kThreads = 32 * W;
+  static_assert(W >= kFewDropped, "a warp per move");
+  __shared__ int s_hist[4][256];
+  __shared__ int2 s_warp[W];
+  __shared__ long long s_low[2][W];
+  __shared__ int s_newest, s_protected, s_bad, s_count;
+  grid_launch_dependents();
+  const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int L = p.context_lens[b];
+  if (left_alone(p, b, g, L)) return;
+  const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * p.weight_entries;
+  const int per_warp = ((L + 31) / 32 + W - 1) / W;          // words of 32 entries, at most E
+  const int j0 = 32 * warp * per_warp + lane;
+  if (tid == 0) {
+    s_newest = -0x7fffffff - 1;
+    s_protected = s_bad = 0;
+  }
+  for (int i = tid; i < 4 * 256; i += kThreads) s_hist[i >> 8][i & 255] = 0;
+  uint32_t key[E];
+  int pos[E], newest = -0x7fffffff - 1;
+  unsigned live = 0;                         // bit k: entry j0 + 32 k
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    const int j = j0 + 32 * k;
+    const bool mine = k < per_warp && j < L;
+    pos[k] = mine ? p.positions[row + j] : -0x7fffffff - 1;
+    key[k] = mine ? __float_as_uint(p.weights[row + j]) : 0u;
+    live |= mine ? 1u << k : 0u;
+  }
+  const bool bad = bad_block(p, b, L, kThreads);
+  __syncthreads();
+  if (bad) s_bad = 1;
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    newest = max(newest, pos[k]);
+    key[k] = weight_key(__uint_as_float(key[k]));
+  }
+  newest = __reduce_max_sync(0xffffffffu, newest);
+  if (lane == 0) atomicMax(&s_newest, newest);
+  __syncthreads();
+  if (s_bad) {
+    leave_bad(p, b, g, L);
+    return;
+  }
+  const long long bar = static_cast<long long>(s_newest) - p.num_recent;   // protected: pos > bar
+  unsigned prot = 0;
+#pragma unroll
+  for (int k = 0; k < E; ++k) prot |= pos[k] > bar ? 1u << k : 0u;
+  prot &= live;
+  int2* moves = p.moves + static_cast<size_t>(blockIdx.x) * p.max_moves;
+
+  const int drop = L - p.budget;
+  if (drop <= kFewDropped) {
+    // entry j as a number: the smallest ones go, an unprotected one before a protected one, then
+    // the smaller weight, then the higher index
+    long long low;                           // this thread's smallest one
+    auto scan = [&]() {
+      low = 0x7fffffffffffffffll;
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const long long x = static_cast<long long>(
+            (static_cast<unsigned long long>((prot >> k) & 1u) << 62) |
+            (static_cast<unsigned long long>(key[k]) << 30) |
+            static_cast<unsigned>(0x3fffffff - j0 - 32 * k));
+        if ((live >> k) & 1u) low = min(low, x);
+      }
+    };
+    int gone = -1;                           // lane i: the i-th dropped entry
+    scan();
+    for (int i = 0; i < drop; ++i) {
+      long long all = low;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all = min(all, __shfl_xor_sync(0xffffffffu, all, o));
+      if (lane == 0) s_low[i & 1][warp] = all;
+      __syncthreads();
+      all = s_low[i & 1][lane % W];
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) all = min(all, __shfl_xor_sync(0xffffffffu, all, o));
+      const int j = 0x3fffffff - static_cast<int>(all & 0x3fffffff);
+      if (low == all && i + 1 < drop) {
+        live &= ~(1u << ((j - j0) / 32));
+        scan();
+      }
+      if (lane == i) gone = j;
+    }
+    if (warp == 0) {
+      const int n = pair_few(gone, drop, p.budget, p.move_here ? s_warp : moves, lane);
+      if (lane == 0) {
+        p.counts[blockIdx.x] = s_count = n;
+        if (g == 0) p.new_lens[b] = p.budget;
+      }
+    }
+    if (!p.move_here) return;
+    __syncthreads();
+    if (warp < s_count) move_entry(p, b, g, s_warp[warp], row, lane);
+    return;
+  }
+
+  const int protects = __reduce_add_sync(0xffffffffu, __popc(prot));
+  if (lane == 0 && protects > 0) atomicAdd(&s_protected, protects);
+  __syncthreads();
+  const bool among = s_protected >= p.budget;      // the threshold lies among the protected
+  int left = among ? p.budget : p.budget - s_protected;   // entries of that class to keep
+  const unsigned same = among ? prot : live & ~prot;      // the class
+  unsigned tie = left == 0 ? 0u : same;      // of the class, equal to the threshold so far
+  uint32_t threshold = 0;
+  for (int pass = 0; pass < 4 && left > 0; ++pass) {
+    const int shift = 24 - 8 * pass;
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if ((tie >> k) & 1u) atomicAdd(&s_hist[pass][(key[k] >> shift) & 255u], 1);
+    __syncthreads();
+    int digit;
+    find_digit(s_hist[pass], left, lane, digit, left);
+    threshold |= static_cast<uint32_t>(digit) << shift;
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (((key[k] >> shift) & 255u) != static_cast<uint32_t>(digit)) tie &= ~(1u << k);
+  }
+  // protected entries stay unless they are the class; of the class every key above the threshold
+  // stays, and the first `left` that equal it
+  unsigned keep = prot & ~same;
+  if (left > 0) {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (key[k] > threshold) keep |= same & (1u << k);
+  }
+  int2 total;
+  int seen = over_warps<W>(make_int2(__reduce_add_sync(0xffffffffu, __popc(tie)), 0), total, s_warp).x;
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    const unsigned tb = __ballot_sync(0xffffffffu, (tie >> k) & 1u);
+    if (((tie >> k) & 1u) && seen + __popc(tb & below) < left) keep |= 1u << k;
+    seen += __popc(tb);
+  }
+  unsigned low = 0;                          // entries below `budget`
+#pragma unroll
+  for (int k = 0; k < E; ++k) low |= j0 + 32 * k < p.budget ? 1u << k : 0u;
+  const unsigned gap = live & ~keep & low, mover = keep & ~low;
+  int2 at = over_warps<W>(make_int2(__reduce_add_sync(0xffffffffu, __popc(gap)),
+                                    __reduce_add_sync(0xffffffffu, __popc(mover))),
+                          total, s_warp);
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    const bool is_gap = (gap >> k) & 1u, is_mover = (mover >> k) & 1u;
+    const unsigned gb = __ballot_sync(0xffffffffu, is_gap), mb = __ballot_sync(0xffffffffu, is_mover);
+    if (is_gap) moves[at.x + __popc(gb & below)].y = j0 + 32 * k;
+    if (is_mover) moves[at.y + __popc(mb & below)].x = j0 + 32 * k;
+    at.x += __popc(gb);
+    at.y += __popc(mb);
+  }
+  if (tid == 0) {
+    p.counts[blockIdx.x] = total.y;
+    if (g == 0) p.new_lens[b] = p.budget;
+  }
+}
+
+// Longer contexts.  kStaged: keys and protected bits in shared memory.
+template <int W, bool kStaged>
+__global__ void __launch_bounds__(32 * W) evict_select_long_kernel(const EvictParams p) {
   constexpr int kThreads = 32 * W;
   extern __shared__ uint32_t s_dyn[];        // staged: protected bits, then keys
   __shared__ int s_hist[256];
@@ -217,23 +458,7 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = p.context_lens[b];
   int* count = p.counts + blockIdx.x;
-  if (L < 0 || L > p.max_ctx) {
-    if (tid == 0) {
-      *count = 0;
-      if (g == 0) {
-        p.new_lens[b] = L;
-        atomicOr(&g_pa_err, kErrBounds);
-      }
-    }
-    return;
-  }
-  if (L <= p.budget) {
-    if (tid == 0) {
-      *count = 0;
-      if (g == 0) p.new_lens[b] = L;
-    }
-    return;
-  }
+  if (left_alone(p, b, g, L)) return;
   const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * p.weight_entries;
   const float* w = p.weights + row;
   const int* pos = p.positions + row;
@@ -246,12 +471,7 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
     s_bad = 0;
   }
   __syncthreads();
-  // a block outside the pool: the sequence is left as it is (every head sees the same table)
-  const int nblk = (L + kBlockSize - 1) / kBlockSize;
-  for (int i = tid; i < nblk; i += kThreads)
-    if (static_cast<unsigned>(p.block_tables[static_cast<size_t>(b) * p.mbs + i]) >=
-        static_cast<unsigned>(p.num_blocks))
-      s_bad = 1;
+  if (bad_block(p, b, L, kThreads)) s_bad = 1;
   int newest = -0x7fffffff - 1;
 #pragma unroll 4
   for (int j = tid; j < L; j += kThreads) {
@@ -262,13 +482,7 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
   if (lane == 0) atomicMax(&s_newest, newest);
   __syncthreads();
   if (s_bad) {
-    if (tid == 0) {
-      *count = 0;
-      if (g == 0) {
-        p.new_lens[b] = L;
-        atomicOr(&g_pa_err, kErrBounds);
-      }
-    }
+    leave_bad(p, b, g, L);
     return;
   }
   const long long bar = static_cast<long long>(s_newest) - p.num_recent;   // protected: pos > bar
@@ -326,23 +540,10 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
       if (low == last && i + 1 < drop) scan();
       if (lane == i) gone = 0x3fffffff - static_cast<int>(last & 0x3fffffff);
     }
-    // the dropped ones below `budget` are the gaps, the kept ones from it on the movers; both
-    // in rising order
     if (warp == 0) {
-      const bool gap = gone >= 0 && gone < p.budget;
-      bool mover = lane < drop;
-      int before = 0;
-      for (int i = 0; i < drop; ++i) {
-        const int x = __shfl_sync(0xffffffffu, gone, i);
-        before += x < gone;                  // all dropped entries below a gap are gaps
-        if (x == p.budget + lane) mover = false;
-      }
-      const unsigned mb = __ballot_sync(0xffffffffu, mover);
-      int2* to = p.move_here ? s_warp : moves;
-      if (gap) to[before].y = gone;
-      if (mover) to[__popc(mb & ((1u << lane) - 1u))].x = p.budget + lane;
+      const int n = pair_few(gone, drop, p.budget, p.move_here ? s_warp : moves, lane);
       if (lane == 0) {
-        *count = s_left = __popc(mb);
+        *count = s_left = n;
         if (g == 0) p.new_lens[b] = p.budget;
       }
     }
@@ -368,24 +569,10 @@ __global__ void __launch_bounds__(32 * W) evict_select_kernel(const EvictParams 
     }
     __syncthreads();
     if (warp == 0) {
-      // bins 255 - 8 lane .. 248 - 8 lane: find where the count from the top passes k
-      int h[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[i] = s_hist[255 - 8 * lane - i];
-        sum += h[i];
-      }
-      int above = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, above, o);
-        if (lane >= o) above += a;
-      }
-      above -= sum;
-      if (above < k && above + sum >= k) {
-        int left = k - above, i = 0;
-        while (h[i] < left) left -= h[i++];
-        s_digit = 255 - 8 * lane - i;
+      int digit, left;
+      find_digit(s_hist, k, lane, digit, left);
+      if (lane == 0) {
+        s_digit = digit;
         s_left = left;
       }
     }
@@ -527,17 +714,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 namespace {
 
-template <int W>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(p.num_seqs * p.Hkv);
+  auto go = [&](auto fn, int warps, size_t bytes) {
+    return launch_behind(fn, dim3(grid), 32 * warps, bytes, s, false, p);
+  };
+  // 16 entries per thread rather than 8 (twice the CTAs of half the warps per SM): 64 x 8 rows of
+  // 2049 entries 9.3 -> 7.4 us, of 6001 18.5 -> 13.2; 32 entries gain no more
+  if (p.max_ctx <= 4096) return go(evict_select_kernel<8, 16>, 8, 0);
+  if (p.max_ctx <= 8192) return go(evict_select_kernel<16, 16>, 16, 0);
+  if (p.max_ctx <= 16384) return go(evict_select_kernel<32, 16>, 32, 0);
   // keys and protected bits of the longest context, if they fit
   const size_t bytes = (static_cast<size_t>(p.max_ctx) + (p.max_ctx + 31) / 32) * 4;
-  const unsigned grid = static_cast<unsigned>(p.num_seqs * p.Hkv);
-  if (bytes <= 200 * 1024) {
-    const cudaError_t e = allow_smem<evict_select_kernel<W, true>>(200 * 1024);
-    if (e != cudaSuccess) return e;
-    return launch_behind(evict_select_kernel<W, true>, dim3(grid), 32 * W, bytes, s, false, p);
-  }
-  return launch_behind(evict_select_kernel<W, false>, dim3(grid), 32 * W, 0, s, false, p);
+  if (bytes > 200 * 1024) return go(evict_select_long_kernel<32, false>, 32, 0);
+  const cudaError_t e = allow_smem<evict_select_long_kernel<32, true>>(200 * 1024);
+  if (e != cudaSuccess) return e;
+  return go(evict_select_long_kernel<32, true>, 32, bytes);
 }
 
 }  // namespace
@@ -548,8 +740,7 @@ cudaError_t launch_evict(const EvictParams& params, int format, int head_dim, cu
   p.head_dim = head_dim;
   p.move_here = p.max_ctx - p.budget <= kFewDropped && p.max_ctx < (1 << 30);
   const int pairs = p.num_seqs * p.Hkv;
-  // few entries per (sequence, kv head): smaller CTAs, more of them at once
-  cudaError_t e = p.max_ctx <= 4096 ? launch_select<16>(p, s) : launch_select<32>(p, s);
+  const cudaError_t e = launch_select(p, s);
   if (e != cudaSuccess || p.move_here) return e;
   // At most one batch per warp, and about 40 CTAs per SM in all: 4 waves, so that rows with more
   // moves than others leave no tail (evicting from those 16 prompts, the whole call: 58.1 us with

@@ -260,6 +260,19 @@ def test_evict_long(kind, budget, recent):
     evict(c, Dev(c), w0, p0, budget, recent)
 
 
+@pytest.mark.parametrize("kind", ["ties", "special"])
+@pytest.mark.parametrize("top", [4096, 4097, 8192, 8193, 16384, 16385, 20000])
+def test_evict_around_the_sizes_of_the_kernels(kind, top):
+    """Rows up to and past what 8, 16 and 32 warps hold in registers, and from shared memory, with
+    shorter rows beside them; a row one entry too long."""
+    budget = top - 600
+    c = Case(top, [top, budget + 1, budget + 300, 33], 1, 1, 64, T=0, fmt="int4")
+    w0, p0 = stats(np.random.default_rng(top), c.lens, 1, top + 16, kind)
+    evict(c, Dev(c), w0, p0, budget, 250)
+    c = Case(top + 1, [top, 700], 1, 1, 64, T=0, fmt="int4")
+    evict(c, Dev(c), w0[:2], p0[:2], 512, 100)
+
+
 def test_evict_context_past_shared_memory():
     """A row whose keys do not fit in shared memory: read again at every pass."""
     n, budget = 60000, 20000
