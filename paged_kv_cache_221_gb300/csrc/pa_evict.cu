@@ -13,7 +13,7 @@ namespace pa {
 // once, and sums over them.  Twice as many CTAs as are resident at once: the jobs' lengths
 // differ, and what a CTA does before its first tile costs (a call with 1 / 2 / 4 times as many:
 // 121.6 / 118.4 / 123.1 us; equal runs of tiles per CTA: 121.1).  Bound by the scores' bytes on
-// their way out of L2 and back: 189 MB of 20 rows (32 sequences of 2048-16384 tokens) take 43
+// their way out of L2 and back: 189 MB of 20 rows (32 sequences of 2048-16384 tokens) take 37
 // us; a second buffer per CTA (half the CTAs) took 8 us more, refilling each quarter of the
 // rows as it is read 6.
 constexpr int kSumThreads = 128, kSumEntries = 4 * kSumThreads;
@@ -41,12 +41,12 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
   const float* scores = p.scores + bg * nrows * p.max_entries + 4 * threadIdx.x;
   const uint32_t mine_at = smem_u32(s_scores) + 16 * threadIdx.x;
   const int stride = gridDim.x * kSumEntries;
+  const uint64_t policy = read_policy(true);
   auto fetch = [&](int e0) {
     const bool mine = e0 + 4 * static_cast<int>(threadIdx.x) < L;
-    for (int r = 0; r < nrows; ++r)
-      cp_async_16(mine_at + r * kSumRowBytes,
-                  mine ? scores + static_cast<size_t>(r) * p.max_entries + e0 : p.scores,
-                  mine ? 16u : 0u);
+    for (int r = 0; mine && r < nrows; ++r)
+      cp_async_16_hint(mine_at + r * kSumRowBytes,
+                       scores + static_cast<size_t>(r) * p.max_entries + e0, policy);
     cp_async_commit();
   };
   int e0 = blockIdx.x * kSumEntries;

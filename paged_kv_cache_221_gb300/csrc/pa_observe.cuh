@@ -10,9 +10,9 @@
 // and repeats the part that binds the first launch.
 //
 // Measured (GPU time of a call): 64 sequences of 512-4096 tokens, 32/8 heads of 128 dims, bf16
-// pages, 59 us (302 MB of K; the first launch alone 53 us, 5.7 TB/s: bound by memory); five
-// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 119 us: 76 us of scores (160
-// MB of K, 189 MB written; 69 us with the stores left out: bound by the score tiles), 43
+// pages, 58 us (302 MB of K; the first launch alone 53 us, 5.7 TB/s: bound by memory); five
+// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 112 us: 75 us of scores (160
+// MB of K, 189 MB written; 69 us with the stores left out: bound by the score tiles), 37
 // us of sums.  The sequences in 2, 3 or 4 parts through one smaller scratch, so that the scores
 // stay in L2: 130, 146, 160 us.
 #pragma once
@@ -59,10 +59,11 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB)
   const uint32_t swz = page_swizzle<F, D>(lane / P::kChunks, lane % P::kChunks);
   const uint32_t koff = ldsm_offset<F, D>(lane);
 
-  // The scores are read again by the second launch.  Where they are the smaller stream, and one
-  // column reads the pages, those leave the L2 cache first (64 sequences of 512-4096 tokens,
-  // bf16: 61.8 -> 58.8 us); where they are the larger one that loses (121.8 -> 124.4 us).
-  const uint64_t policy = read_policy(NTW == 1 && 4 * nrows * kBlockSize < P::kBytes);
+  // The scores are read again by the second launch, the pages (of a single column) not, so the
+  // pages leave the L2 cache first, as the scores do once they have been summed.  64 sequences
+  // of 512-4096 tokens, bf16: 61.8 -> 58.2 us; five verified tokens over 4-bit pages: 117.1 ->
+  // 112.5.
+  const uint64_t policy = read_policy(NTW == 1);
   Cursor<kFlat> cur;
   Segment seg;
   bool invalid = false;
