@@ -455,7 +455,8 @@ ObservePlan observe_plan(int num_seqs, int hq, int hkv, int T, int max_ctx) {
   if (pl.flat) {
     pl.workers = static_cast<int>(std::min<long long>(kAttn4Sms * tile.ctas * 4,
                                                       (all + kInt4MinShare - 1) / kInt4MinShare));
-    slots = static_cast<size_t>(pl.workers) * 2;
+    // two pieces of cut jobs for each worker, then the jobs that lie whole in a run
+    slots = static_cast<size_t>(pl.workers) * 2 + jobs;
   } else {
     pl.workers = static_cast<int>(std::min<long long>(jobs * pl.max_parts, 1 << 30));
     slots = static_cast<size_t>(jobs) * pl.max_parts;

@@ -55,10 +55,14 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
   for (int r = warp; r < nrows; r += kSumThreads / 32) {
     const int c = r / p.tile_rows, rl = r % p.tile_rows;
     const Pieces y = pc[c];
-    const size_t unit0 = (static_cast<size_t>(b) * list.heads + g * p.ntw + c) * p.max_parts;
+    const size_t job_slot = static_cast<size_t>(b) * list.heads + g * p.ntw + c;
+    const bool whole = y.count == 1;
     float M = -CUDART_INF_F, l = 0.f;
     for (int i = lane; i < y.count; i += 32) {
-      const float2 ml = p.ml[(p.flat ? y.slot(i) : unit0 + i) * p.tile_rows + rl];
+      const size_t at = !p.flat ? job_slot * p.max_parts + i
+                        : whole ? static_cast<size_t>(p.workers) * 2 + job_slot
+                                : y.slot(i);
+      const float2 ml = p.ml[at * p.tile_rows + rl];
       const float m = fmaxf(M, ml.x), u = m == -CUDART_INF_F ? 0.f : m;
       l = l * hw_exp2(M - u) + ml.y * hw_exp2(ml.x - u);
       M = m;

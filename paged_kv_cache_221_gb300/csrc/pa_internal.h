@@ -113,7 +113,9 @@ struct ObserveParams {
   float* weights_out;             // may be `weights`
   int32_t* positions;             // [B, Hkv, weight_entries] or nullptr
   float* scores;                  // scratch [B, Hkv, G * T, max_entries]
-  float2* ml;                     // scratch [slot][rows of a tile]: (m, l) of every piece
+  // scratch [slot][rows of a tile]: (m, l) of every piece.  Balanced runs: two slots per worker
+  // for pieces of cut jobs, then one per job that lies whole in a run; otherwise a slot per unit
+  float2* ml;
   int mbs, max_ctx, num_seqs, T, Hq, Hkv, G, num_blocks;
   int max_entries;                // max_ctx in whole blocks
   int weight_entries;

@@ -227,9 +227,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB)
     }
     cp_async_wait<0>();
     __syncwarp();
-    const size_t slot = kFlat ? static_cast<size_t>(worker) * 2 + seg.second
-                              : (static_cast<size_t>(b) * list.heads + seg.job) * p.max_parts +
-                                    seg.part;
+    const size_t job_slot = static_cast<size_t>(b) * list.heads + seg.job;
+    const size_t slot = !kFlat      ? job_slot * p.max_parts + seg.part
+                        : seg.whole ? static_cast<size_t>(p.workers) * 2 + job_slot
+                                    : static_cast<size_t>(worker) * 2 + seg.second;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float m0 = thr0[j] == -CUDART_INF_F ? -CUDART_INF_F : -nm0[j];

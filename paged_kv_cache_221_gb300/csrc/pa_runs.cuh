@@ -5,7 +5,8 @@
 // warp) that is resident at once, so that ragged contexts neither leave a tail nor a second
 // wave.  Each job counts kSetup entries more than it has pages, for what starting on it
 // costs.  Every worker finds its own run from the lengths.  A job whose pages lie in one run
-// is whole there; of the others a worker holds at most two pieces, its run's first and last.
+// is whole there, and a run may hold many of them; of the cut jobs a worker holds at most two
+// pieces, its run's first and last.  A piece slot of a worker is therefore for cut jobs only.
 // Units: a worker takes whole (partition, sequence, job) units of ppb pages, partition-major.
 #pragma once
 
@@ -165,7 +166,8 @@ __device__ __forceinline__ RunList observe_list(const ObserveParams& p, int ntw)
 }
 
 // The pieces of job `job` of sequence b, in page order: piece i is held by worker w0 + i, as its
-// second piece if `second` and i = 0, otherwise as its first.  A warp.
+// second piece if `second` and i = 0, otherwise as its first.  One piece: the job is whole and
+// has no slot here.  A warp.
 struct Pieces {
   int w0, count;
   bool second;
