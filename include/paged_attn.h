@@ -445,7 +445,8 @@ size_t pa_accumulate_workspace_size(int num_seqs, int num_q_heads, int num_kv_he
  *   weights_out[b, g, j] = sum_{t, h} p[t, h, j]                       L - T <= j < L
  *   positions[b, g, j]   = seq_lens[b] - L + j                         L - T <= j < L
  * The T newest entries start afresh whatever the arrays held; entries from L on are
- * left as they were.  weights_out may be weights itself, and otherwise does not overlap
+ * left as they were.  Where a query row's softmax is NaN (it sees a score of NaN or +inf, or
+ * none above -inf), every entry that the row sees becomes NaN.  weights_out may be weights itself, and otherwise does not overlap
  * it.  positions may be NULL (not written); seq_lens[b], the number of tokens the
  * sequence has seen (NULL: L, nothing evicted so far), gives them.  Only K pages are
  * read: kv_format PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_INT4, k_scale ignored for bf16.

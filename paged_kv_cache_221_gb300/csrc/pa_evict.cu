@@ -21,6 +21,7 @@ constexpr int kSumRowBytes = kSumEntries * 4;
 
 __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveParams p) {
   __shared__ float s_m[kMaxRows], s_f[kMaxRows];
+  __shared__ int s_undefined;                // a row's softmax is NaN
   extern __shared__ __align__(16) float s_scores[];   // [row][thread][4]
   const int b = blockIdx.y / p.Hkv, g = blockIdx.y % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
   };
   int e0 = blockIdx.x * kSumEntries;
   fetch(e0);
+  if (threadIdx.x == 0) s_undefined = 0;
   __syncthreads();
   for (int r = warp; r < nrows; r += kSumThreads / 32) {
     const int c = r / p.tile_rows, rl = r % p.tile_rows;
@@ -75,8 +77,10 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
       M = m;
     }
     if (lane == 0) {
+      // l is NaN behind a score of NaN or +inf, and 0 without a finite one
       s_m[r] = M == -CUDART_INF_F ? 0.f : M;
-      s_f[r] = l > 0.f ? 1.f / l : 0.f;
+      s_f[r] = l > 0.f ? 1.f / l : CUDART_NAN_F;
+      if (!(l > 0.f)) s_undefined = 1;
     }
   }
   __syncthreads();
@@ -89,14 +93,28 @@ __global__ void __launch_bounds__(kSumThreads) observe_sum_kernel(const ObserveP
     cp_async_wait<0>();
     float w[4] = {0.f, 0.f, 0.f, 0.f};
     const float4* x4 = reinterpret_cast<const float4*>(s_scores);   // this thread's own copies
+    if (!s_undefined) {
 #pragma unroll 4
-    for (int r = 0; r < nrows; ++r) {
-      const float4 x = x4[r * kSumThreads + threadIdx.x];
-      const float m = s_m[r], f = s_f[r];
-      w[0] = fmaf(hw_exp2(x.x - m), f, w[0]);
-      w[1] = fmaf(hw_exp2(x.y - m), f, w[1]);
-      w[2] = fmaf(hw_exp2(x.z - m), f, w[2]);
-      w[3] = fmaf(hw_exp2(x.w - m), f, w[3]);
+      for (int r = 0; r < nrows; ++r) {
+        const float4 x = x4[r * kSumThreads + threadIdx.x];
+        const float m = s_m[r], f = s_f[r];
+        w[0] = fmaf(hw_exp2(x.x - m), f, w[0]);
+        w[1] = fmaf(hw_exp2(x.y - m), f, w[1]);
+        w[2] = fmaf(hw_exp2(x.z - m), f, w[2]);
+        w[3] = fmaf(hw_exp2(x.w - m), f, w[3]);
+      }
+    } else if (j0 < L && static_cast<unsigned>(
+                             p.block_tables[static_cast<size_t>(b) * p.mbs + j0 / kBlockSize]) <
+                             static_cast<unsigned>(p.num_blocks)) {
+      // a row adds to the entries that it sees alone (a NaN factor would reach the others): not to
+      // later drafts, nor to entries of a block outside the pool
+      for (int r = 0; r < nrows; ++r) {
+        const float4 x = x4[r * kSumThreads + threadIdx.x];
+        const float m = s_m[r], f = s_f[r], t[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j0 + e <= L - T + r / p.G) w[e] = fmaf(hw_exp2(t[e] - m), f, w[e]);
+      }
     }
     if (e0 + stride < L) fetch(e0 + stride);
 #pragma unroll
