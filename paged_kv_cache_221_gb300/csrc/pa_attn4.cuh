@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
         if (edge) {
           // entries that no query token sees may hold any scale, even NaN
           const int nv = end_of(k) - (tok0 + k * kBlockSize);
-          const int from = p.window > 0 ? L - T - p.window + 1 - (tok0 + k * kBlockSize) : 0;
+          const int first_seen = p.window > 0 ? max(0, L - T - p.window + 1) : 0;
+          const int from = first_seen - (tok0 + k * kBlockSize);
           w0 = 2 * q4 < nv && 2 * q4 >= from ? w0 : 0u;
           w1 = 2 * q4 + 1 < nv && 2 * q4 + 1 >= from ? w1 : 0u;
           w2 = 2 * q4 + 8 < nv && 2 * q4 + 8 >= from ? w2 : 0u;
