@@ -385,8 +385,11 @@ size_t pa_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
  * before they are read.  k_cache / v_cache are written only then.
  *
  * The products run on f16 operands with fp32 accumulation: query rows are scaled by a
- * power of two, softmax weights are rounded to f16, multiplied by the E4M3 scales and
- * rounded to f16 again, and the codes are exact.  Scores scale * q . K stay below 10^29 in
+ * power of two, softmax weights are rounded to f16 (and their sum is that of the rounded
+ * ones), multiplied by the E4M3 scales and rounded to f16 again, and the codes are exact.
+ * Either rounding is at most 2^-11 of the weight or product, or 2^-28 of the row's sum where
+ * that is more: fainter weights, and fainter products of weight and scale, may count as
+ * nothing.  Scores scale * q . K stay below 10^29 in
  * magnitude.
  *
  * Work: with partition_size = 0 and a workspace of pa_int4_workspace_size bytes, the pages

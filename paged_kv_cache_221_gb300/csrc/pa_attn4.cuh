@@ -12,7 +12,12 @@
 // O^T[D x 8] += V^T . P^T, so that a page is one step.  Scores: two k steps per group of
 // 32 dims, times the tokens' scales in fp32.  P.V: the weights, f16, are transposed by
 // movmatrix, multiplied by the group's scales of their tokens, and meet V codes that
-// ldmatrix.trans delivers as (token 2q, token 2q + 1) pairs of four dims each.
+// ldmatrix.trans delivers as (token 2q, token 2q + 1) pairs of four dims each.  A weight is
+// rounded to f16 twice, by itself (its row's sum is that of the rounded ones) and times the scale,
+// 2^-11 each.  Taking the codes' offset off the output afterwards instead of off the codes is
+// faster (39.2 against 41.2 us for the 64 sequences below, 111 against 116, 123 against 125), but a
+// rounding then counts with a code of up to 15 instead of 7, one-sidedly where values are small;
+// taken off as a sum of the rounded products it costs 40.5, 115 and 142 us.
 //
 // Measured (GPU time of a call, bytes of every page once, against a copy's 6780 GB/s): 64
 // sequences of 512-4096 tokens, 32/8 heads of 128 dims, 39.2 us, 161 MB (0.61); 256 of 128-8192,
@@ -164,22 +169,19 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
 
     // Softmax state of rows 2q4, 2q4 + 1 of each n-tile: minus the reference m (log2
     // domain; kUnseen until a score was seen).
-    // z: rows 0 .. NG - 1 hold the groups' sums of weight * scale (what the codes' offset
-    // adds to the output), rows 8 .. 15 the sum of the weights.
-    constexpr float kUnseen = 1e30f;
-    float acc[NT][D / 16][4], z[NT][4], nm0[NT], nm1[NT];
+    // sum: the sum of the rounded weights, in every row of a tile.
+    constexpr float kUnseen = 1e30f, kTop = 3.f;
+    float acc[NT][D / 16][4], sum[NT][4], nm0[NT], nm1[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       nm0[j] = nm1[j] = kUnseen;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) sum[j][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][k][e] = 0.f;
     }
-    // byte pair (token 2q, token 2q+1) of group gid % NG from two words of scales
-    const uint32_t zsel = (gid & (NG - 1)) | ((gid & (NG - 1)) + 4) << 4;
     constexpr uint32_t kOnes = 0x3C003C00u;
 
     // Pages wholly visible to every row: first entry in [lo, hi]
@@ -225,8 +227,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
         }
       }
 
-      // Online softmax: the reference m of a row moves only when a score passes it by
-      // 7, so a weight is at most 2^7 and, times a V scale (at most 448), an f16 value.
+      // Online softmax: the reference m of a row moves, to kTop below the new maximum, only when a
+      // score passes it by 7: a weight is at most 2^7 and, times a V scale (at most 448), an f16
+      // value, and the largest weight at least 2^kTop, for f16's sake: what a weight or a product
+      // loses below 2^-14 is at most 2^-25, so 2^-28 of the sum.
       bool over = false;
       float e[TP][NT][4];                    // scores less the reference
 #pragma unroll
@@ -257,12 +261,12 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           }
           float f0 = 1.f, f1 = 1.f;
           if (fmaf(x0, qo.rs0[j], nm0[j]) > 7.f) {
-            const float nm = -x0 * qo.rs0[j];
+            const float nm = kTop - x0 * qo.rs0[j];
             f0 = nm0[j] == kUnseen ? 0.f : hw_exp2(nm - nm0[j]);
             nm0[j] = nm;
           }
           if (fmaf(x1, qo.rs1[j], nm1[j]) > 7.f) {
-            const float nm = -x1 * qo.rs1[j];
+            const float nm = kTop - x1 * qo.rs1[j];
             f1 = nm1[j] == kUnseen ? 0.f : hw_exp2(nm - nm1[j]);
             nm1[j] = nm;
           }
@@ -273,10 +277,10 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
             e[k][j][2] = fmaf(t[k][j][2], qo.rs0[j], nm0[j]);
             e[k][j][3] = fmaf(t[k][j][3], qo.rs1[j], nm1[j]);
           }
-          z[j][0] *= f0;
-          z[j][1] *= f1;
-          z[j][2] *= f0;
-          z[j][3] *= f1;
+          sum[j][0] *= f0;
+          sum[j][1] *= f1;
+          sum[j][2] *= f0;
+          sum[j][3] *= f1;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             acc[j][k][0] *= f0;
@@ -327,13 +331,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           w2 = 2 * q4 + 8 < nv && 2 * q4 + 8 >= from ? w2 : 0u;
           w3 = 2 * q4 + 9 < nv && 2 * q4 + 9 >= from ? w3 : 0u;
         }
-        {
-          uint32_t za, zb, none;
-          e4m3x4_to_f16x4(__byte_perm(w0, w1, zsel), za, none);
-          e4m3x4_to_f16x4(__byte_perm(w2, w3, zsel), zb, none);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma_f16(z[j], za, kOnes, zb, kOnes, ph0[j], ph1[j]);
-        }
+        for (int j = 0; j < NT; ++j) mma_f16(sum[j], kOnes, kOnes, kOnes, kOnes, ph0[j], ph1[j]);
 #pragma unroll
         for (int g2 = 0; g2 < NG; g2 += 2) {
           // byte pairs (token 2q, token 2q+1) of groups g2 and g2 + 1
@@ -350,14 +349,20 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
             const uint32_t fa = fs[h], fb = fs[2 + h];
             const uint32_t y0 = w[2 * h], y1 = w[2 * h + 1];
             const uint32_t u0 = y0 >> 8, u1 = y1 >> 8;
+            // codes less 8 as f16 subnormals, exact: dims 32 gr + 4 gid + 0 and 2, then + 1 and 3
+            // (times 16)
+            const uint32_t x[4] = {y0, u0, y1, u1};
+            uint32_t a[4], c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = f16x2_add(x[i] & kNibLo, kMinus8Lo);
+              c[i] = f16x2_add(x[i] & kNibHi, kMinus8Hi);
+            }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
               const uint32_t b0 = f16x2_mul(ph0[j], fa), b1 = f16x2_mul(ph1[j], fb);
-              // dims 32 gr + 4 gid + 0 and 2, then + 1 and 3 (times 16)
-              mma_f16(acc[j][2 * gr], y0 & kNibLo, u0 & kNibLo, y1 & kNibLo, u1 & kNibLo, b0,
-                            b1);
-              mma_f16(acc[j][2 * gr + 1], y0 & kNibHi, u0 & kNibHi, y1 & kNibHi, u1 & kNibHi,
-                            b0, b1);
+              mma_f16(acc[j][2 * gr], a[0], a[1], a[2], a[3], b0, b1);
+              mma_f16(acc[j][2 * gr + 1], c[0], c[1], c[2], c[3], b0, b1);
             }
           }
         }
@@ -373,17 +378,11 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     const size_t slot = kFlat ? static_cast<size_t>(worker) * 2 + seg.second : 0;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      float zz[2][NG];
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        zz[0][gr] = 8.f * __shfl_sync(0xffffffffu, z[j][0], gr * 4 + q4);
-        zz[1][gr] = 8.f * __shfl_sync(0xffffffffu, z[j][1], gr * 4 + q4);
-      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {          // rows 2q4 and 2q4 + 1
         const int r = row0 + 8 * j + 2 * q4 + h;
         if (r >= nrows) continue;
-        const float l = z[j][2 + h];
+        const float l = sum[j][h];
         const bool none = (h ? nm1[j] : nm0[j]) == kUnseen;
         const float inv = l > 0.f ? out_scale / l : 0.f;
         const size_t orow = (static_cast<size_t>(b) * T + r / G) * p.Hq + g * G + r % G;
@@ -399,9 +398,7 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           constexpr float A = 16777216.f, B = 1048576.f;   // 2^24, 2^20
           const float* a = acc[j][2 * gr] + h;
           const float* c = acc[j][2 * gr + 1] + h;
-          const float z8 = zz[h][gr];
-          const float4 o = make_float4(fmaf(a[0], A, -z8) * inv, fmaf(c[0], B, -z8) * inv,
-                                       fmaf(a[2], A, -z8) * inv, fmaf(c[2], B, -z8) * inv);
+          const float4 o = make_float4(a[0] * A * inv, c[0] * B * inv, a[2] * A * inv, c[2] * B * inv);
           const int d = 32 * gr + 4 * gid;
           if (seg.whole)
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + d) =

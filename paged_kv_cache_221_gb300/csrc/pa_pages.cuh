@@ -14,9 +14,11 @@
 // both are exact, and mma.sync multiplies subnormal f16 operands exactly.  A 32-bit word
 // of eight nibbles therefore gives its four operand registers with one shift and
 // four masks; the factors 2^24 and 16 are powers of two folded elsewhere (the even
-// and odd dims of Q, the output), and the offset 8 leaves the contraction as 8 * (sum
-// over the group of scale * the other operand), one more small tile.  E2M1 codes would need a conversion for
-// every pair of values, and have a larger error on normally distributed values.
+// and odd dims of Q, the output).  The offset 8: for K it leaves the contraction as 8 * (sum
+// over the group of scale * the query's operand), one more small tile; the V codes take one f16
+// addition more, also exact, so that a rounding of a softmax weight counts with the value
+// itself.  E2M1 codes would need a conversion for every pair of values, and have a
+// larger error on normally distributed values.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -127,7 +129,14 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
                             *reinterpret_cast<const __half2*>(&b)));
 }
 
+__device__ __forceinline__ uint32_t f16x2_add(uint32_t a, uint32_t b) {
+  return half2_bits(__hadd2(*reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&b)));
+}
+
+// Nibbles 0 (and 1) of both halves of a word of codes, and -8 on the same scales.
 constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
+constexpr uint32_t kMinus8Lo = 0x80088008u, kMinus8Hi = 0x80808080u;
 
 // Query rows as B operands of the score tiles.  Lane (gid = lane/4, q = lane%4) of a warp
 // holds, for row gid of an n-tile of 8 rows, the head dims that the K format puts

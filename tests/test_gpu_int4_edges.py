@@ -1,4 +1,7 @@
 """Attention over INT4 pages where roundings, masks and integer ranges meet their ends."""
+import ctypes
+
+import numpy as np
 import pytest
 import torch
 
@@ -14,6 +17,8 @@ __graft_entry__.build()
 import paged_kv_cache_221_gb300 as pa  # noqa: E402
 from bounded_cases import Case  # noqa: E402
 from gpu_util import to_dev  # noqa: E402
+from oracle import fp8 as F  # noqa: E402
+from oracle import int4 as Q4  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -28,6 +33,27 @@ def attend(c, **kw):
                              int(c.lens.max()), c.scale, **kw)
 
 
+def check(out, c, window=0):
+    """Against the oracle; NaN exactly where it has NaN.  The bound: the output is rounded to
+    bf16 (2^-8 of it); a weight is rounded to f16, which moves it against its row's sum (2^-11 of
+    it times |v| + |out|), and times its scale rounded again (2^-11), each of them at least
+    by 2^-25 where the row's largest weight is 2^3 or more (so 2^-28 of the sum), times codes of
+    at most 7; scores err by 2^-20 of sum |q k|."""
+    with np.errstate(invalid="ignore"):
+        ref, mag = Q4.attention(c.q, c.k, c.v, c.k_scale, c.v_scale, c.tables, c.lens, c.scale,
+                                window)
+    got = out.float().cpu().double().numpy()
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(ref))
+    keys = [[c.rows(c.k, b, g, int(n), "k") for g in range(c.Hkv)] for b, n in enumerate(c.lens)]
+    score = 2.0 ** -20 * c.score_size(keys)
+    s_max = np.nanmax(F.decode(Q4.unpack(c.v, c.D)[1]))
+    small = int(c.lens.max()) * 2.0 ** -28 * 7 * (2 * s_max + 1) * float(c.v_scale.max())
+    tol = (2.0 ** -8 + 2.0 ** -11) * np.abs(ref) + (2.0 ** -10 + 2.0 ** -16 + score) * mag + small
+    ok = ~np.isnan(ref)
+    assert (np.abs(got - ref)[ok] <= tol[ok]).all(), f"by {(np.abs(got - ref) - tol)[ok].max():.3e}"
+    return ref
+
+
 # ------------------------------------------------------------------------------- windows
 @pytest.mark.parametrize("T", [1, 2, 5, 16])
 @pytest.mark.parametrize("psize", [0, 32])
@@ -38,3 +64,48 @@ def test_window_up_to_the_largest(window, psize, T):
     plain = attend(c, partition_size=psize)
     assert torch.isfinite(plain.float()).all()
     assert torch.equal(attend(c, window_size=window, partition_size=psize), plain)
+
+
+# ------------------------------------------------------------------------------- faint weights
+@pytest.mark.parametrize("octaves", [12.0, 17.3, 20.0, 21.6])
+@pytest.mark.parametrize("scale_code", [0x08, 0x10, 0x38, 0x7E])     # 2^-6, 2^-5, 1, 448
+@pytest.mark.parametrize("codes", ["zero", "mixed"])
+@pytest.mark.parametrize("D,T", [(64, 1), (128, 5)])
+def test_one_dominant_entry_and_a_faint_tail(octaves, scale_code, codes, D, T):
+    """A sequence taken whole: one entry holds nearly all the weight, 16384 others 2^-octaves of
+    it each.  What little they add must not be lost one-sidedly."""
+    L = 16384 + T
+    rng = np.random.default_rng(7)
+    c = Case(44, [L], 1, 1, D, T=T, power_of_two=True)
+    q = np.zeros((1, T, 1, D))
+    q[..., 0] = 1.0
+    c.q = (np.float32(q).view(np.uint32) >> 16).astype(np.uint16)
+    kc = np.full((c.NB, 1, 16, D), 8, dtype=np.uint8)
+    ks = np.full((c.NB, 1, 16, D // 32), 0x38, dtype=np.uint8)
+    c.k_scale[:] = octaves * np.log(2.0) * np.sqrt(D) / 7          # score octaves ln 2
+    kc[c.tables[0, 0], 0, 3, 0] = 15
+    c.k = Q4.pack(kc, ks)
+    vc = np.full((c.NB, 1, 16, D), 8, dtype=np.uint8) if codes == "zero" else \
+        rng.integers(1, 16, (c.NB, 1, 16, D), dtype=np.uint8)
+    vc[c.tables[0, 0], 0, 3] = rng.choice([1, 15], D)
+    c.v = Q4.pack(vc, np.full((c.NB, 1, 16, D // 32), scale_code, dtype=np.uint8))
+    t = {n: to_dev(getattr(c, n)) for n in ("q", "k", "v", "k_scale", "v_scale", "tables",
+                                            "lens")}
+    out = torch.empty_like(t["q"])
+    p = {n: ctypes.c_void_p(x.data_ptr()) for n, x in t.items()}
+    st = pa.library().pa_attention_int4(
+        ctypes.c_void_p(out.data_ptr()), p["q"], None, None, p["k"], p["v"], p["k_scale"],
+        p["v_scale"], 0, p["tables"], c.mbs, p["lens"], L, 1, T, c.NB, 1, 1, D, 16,
+        float(c.scale), 0, None, 0, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0
+    ref, mag = Q4.attention(c.q, c.k, c.v, c.k_scale, c.v_scale, c.tables, c.lens, c.scale)
+    got = out.float().cpu().double().numpy()
+    hs, s = float(c.v_scale[0]), float(F.decode(np.array([scale_code], dtype=np.uint8))[0])
+    # as check(): scores of at most `octaves` octaves; weights and products below
+    # 2^-14 lose at most 2^-25 each, of a sum that is at least 2^3, times 7
+    tail = L * 2.0 ** -octaves * 7 * s * hs
+    small = L * 2.0 ** -28 * 7 * hs * (2 * s + 1)
+    tol = ((2.0 ** -8 + 2.0 ** -11) * np.abs(ref) + (2.0 ** -10 + 2.0 ** -16) * mag +
+           2.0 ** -20 * octaves * (mag + tail) + small)
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), f"{(err / tol).max():.2f} of the bound"
