@@ -330,6 +330,37 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           w1 = 2 * q4 + 1 < nv && 2 * q4 + 1 >= from ? w1 : 0u;
           w2 = 2 * q4 + 8 < nv && 2 * q4 + 8 >= from ? w2 : 0u;
           w3 = 2 * q4 + 9 < nv && 2 * q4 + 9 >= from ? w3 : 0u;
+          // A NaN scale makes the rows that see its token NaN and no others, whose weight of zero
+          // would not hold it off: it goes into the output tiles of those rows by hand.
+          const uint32_t n0 = e4m3_nan_bytes(w0), n1 = e4m3_nan_bytes(w1);
+          const uint32_t n2 = e4m3_nan_bytes(w2), n3 = e4m3_nan_bytes(w3);
+          if (__any_sync(0xffffffffu, (n0 | n1 | n2 | n3) != 0u)) {
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              auto bit = [&](uint32_t x) { return (x >> (8 * gr)) & 1u; };
+              unsigned at = (bit(n0) | bit(n1) << 1 | bit(n2) << 8 | bit(n3) << 9) << (2 * q4);
+              at |= __shfl_xor_sync(0xffffffffu, at, 1);
+              at |= __shfl_xor_sync(0xffffffffu, at, 2);
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int r = row0 + 8 * j + 2 * q4 + h;
+                  const int last = r < nrows ? L - T + r / G : L - 1;
+                  const int first = p.window > 0 ? max(0, last - p.window + 1) : 0;
+                  const int t0 = tok0 + k * kBlockSize;
+                  const int lo_bit = max(0, first - t0), hi_bit = last - t0;
+                  const unsigned upto = hi_bit < 0 ? 0u : hi_bit > 15 ? 0xffffu : (2u << hi_bit) - 1u;
+                  if ((at & upto) >> min(lo_bit, 16) != 0u)
+                    acc[j][2 * gr][h] = acc[j][2 * gr][2 + h] = acc[j][2 * gr + 1][h] =
+                        acc[j][2 * gr + 1][2 + h] = CUDART_NAN_F;
+                }
+            }
+            w0 &= ~(n0 * 0xffu);
+            w1 &= ~(n1 * 0xffu);
+            w2 &= ~(n2 * 0xffu);
+            w3 &= ~(n3 * 0xffu);
+          }
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) mma_f16(sum[j], kOnes, kOnes, kOnes, kOnes, ph0[j], ph1[j]);

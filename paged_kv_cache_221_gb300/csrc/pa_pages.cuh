@@ -115,6 +115,11 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
       : "r"(w));
 }
 
+// 1 in each byte of w that is an E4M3 NaN (0x7F, 0xFF).
+__device__ __forceinline__ uint32_t e4m3_nan_bytes(uint32_t w) {
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
+}
+
 __device__ __forceinline__ void f16x4_to_f32(const uint32_t (&h)[2], float (&s)[4]) {
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));

@@ -66,6 +66,52 @@ def test_window_up_to_the_largest(window, psize, T):
     assert torch.equal(attend(c, window_size=window, partition_size=psize), plain)
 
 
+# ------------------------------------------------------------------------------- NaN in V
+def spoil_value(c, b, j, g, group):
+    codes, sc = Q4.unpack(c.v, c.D)
+    sc = np.array(sc, copy=True)
+    sc[c.tables[b, j // 16], g, j % 16, group] = 0x7F
+    c.v = Q4.pack(codes, sc)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(4, 2, 64, 2), (6, 2, 128, 3), (8, 2, 128, 5),
+                                        (4, 1, 64, 7), (8, 1, 128, 5), (2, 1, 128, 20)])
+@pytest.mark.parametrize("psize", [0, 32])
+def test_nan_value_of_the_newest_draft(Hq, Hkv, D, T, psize):
+    """A draft's NaN reaches the rows that see it, in the dims of its scale, and no others."""
+    c = Case(41, [300, 33, T], Hq, Hkv, D, T=T)
+    for b in range(3):
+        spoil_value(c, b, int(c.lens[b]) - 1, 0, b % 2)
+    ref = check(attend(c, partition_size=psize), c)
+    G = Hq // Hkv
+    assert np.isnan(ref[0, T - 1, :G, :32]).all() and np.isfinite(ref[0, :T - 1]).all()
+    assert np.isfinite(ref[0, T - 1, :, 32:]).all()
+
+
+@pytest.mark.parametrize("psize", [0, 16])
+@pytest.mark.parametrize("T", [2, 5])
+def test_nan_value_behind_a_window(T, psize):
+    """Seen by the first query token alone, and by all of them in a page that is an edge."""
+    c = Case(42, [300, 70], 4, 2, 64, T=T)
+    spoil_value(c, 0, 300 - T - 20 + 1, 1, 0)
+    spoil_value(c, 1, 70 - 20, 0, 1)
+    ref = check(attend(c, window_size=20, partition_size=psize), c, window=20)
+    assert np.isnan(ref[0, 0, 2:, :32]).all() and np.isfinite(ref[0, 1:]).all()
+    assert np.isnan(ref[1, :, :2, 32:]).all()
+
+
+@pytest.mark.parametrize("j", [0, 100, 299])
+def test_nan_key(j):
+    """A row that sees a NaN score is NaN in every dim."""
+    c = Case(43, [300, 50], 4, 2, 64, T=3)
+    codes, sc = Q4.unpack(c.k, 64)
+    sc = np.array(sc, copy=True)
+    sc[c.tables[0, j // 16], 1, j % 16, 0] = 0x7F
+    c.k = Q4.pack(codes, sc)
+    ref = check(attend(c), c)
+    assert np.isnan(ref[0, 2, 2:]).all() and np.isfinite(ref[0, :, :2]).all()
+
+
 # ------------------------------------------------------------------------------- faint weights
 @pytest.mark.parametrize("octaves", [12.0, 17.3, 20.0, 21.6])
 @pytest.mark.parametrize("scale_code", [0x08, 0x10, 0x38, 0x7E])     # 2^-6, 2^-5, 1, 448
