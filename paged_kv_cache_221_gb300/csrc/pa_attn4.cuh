@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
       // Online softmax: the reference m of a row moves, to kTop below the new maximum, only when a
       // score passes it by 7: a weight is at most 2^7 and, times a V scale (at most 448), an f16
       // value, and the largest weight at least 2^kTop, for f16's sake: what a weight or a product
-      // loses below 2^-14 is at most 2^-25, so 2^-28 of the sum.
+      // loses below 2^-14 is at most 2^-25, so 2^-28 of the sum.  The reference is rounded so that
+      // the maximum's own exponent is never below kTop, however large the scores.
       bool over = false;
       float e[TP][NT][4];                    // scores less the reference
 #pragma unroll
@@ -261,12 +262,12 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           }
           float f0 = 1.f, f1 = 1.f;
           if (fmaf(x0, qo.rs0[j], nm0[j]) > 7.f) {
-            const float nm = kTop - x0 * qo.rs0[j];
+            const float nm = __fadd_ru(kTop, -__fmul_rd(x0, qo.rs0[j]));
             f0 = nm0[j] == kUnseen ? 0.f : hw_exp2(nm - nm0[j]);
             nm0[j] = nm;
           }
           if (fmaf(x1, qo.rs1[j], nm1[j]) > 7.f) {
-            const float nm = kTop - x1 * qo.rs1[j];
+            const float nm = __fadd_ru(kTop, -__fmul_rd(x1, qo.rs1[j]));
             f1 = nm1[j] == kUnseen ? 0.f : hw_exp2(nm - nm1[j]);
             nm1[j] = nm;
           }
@@ -276,6 +277,9 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
             e[k][j][1] = fmaf(t[k][j][1], qo.rs1[j], nm1[j]);
             e[k][j][2] = fmaf(t[k][j][2], qo.rs0[j], nm0[j]);
             e[k][j][3] = fmaf(t[k][j][3], qo.rs1[j], nm1[j]);
+            // past 2^26 the product is rounded by more than the room above kTop (NaN stays NaN)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[k][j][i] = e[k][j][i] > 7.f ? 7.f : e[k][j][i];
           }
           sum[j][0] *= f0;
           sum[j][1] *= f1;

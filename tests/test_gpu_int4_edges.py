@@ -15,10 +15,12 @@ import __graft_entry__  # noqa: E402
 __graft_entry__.build()
 
 import paged_kv_cache_221_gb300 as pa  # noqa: E402
+import workloads as W  # noqa: E402
 from bounded_cases import Case  # noqa: E402
 from gpu_util import to_dev  # noqa: E402
 from oracle import fp8 as F  # noqa: E402
 from oracle import int4 as Q4  # noqa: E402
+from oracle import oracle as O  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -155,3 +157,34 @@ def test_one_dominant_entry_and_a_faint_tail(octaves, scale_code, codes, D, T):
            2.0 ** -20 * octaves * (mag + tail) + small)
     err = np.abs(got - ref)
     assert (err <= tol).all(), f"{(err / tol).max():.2f} of the bound"
+
+
+# ------------------------------------------------------------------------------- large scores
+@pytest.mark.parametrize("octaves", [24, 26, 30, 60, 90])
+@pytest.mark.parametrize("psize,D,T", [(0, 64, 2), (32, 128, 1), (0, 128, 6)])
+def test_scores_past_what_fp32_resolves(octaves, psize, D, T):
+    """Scores so large that their rounding is octaves: the largest one takes all the weight."""
+    c = Case(51, [T, 17 + T, 40, 300, 2000], 4, 2, D, T=T)
+    c.q = W.f32_to_bf16_bits((O.bf16_bits_to_f64(c.q) * 2.0 ** octaves).astype(np.float32))
+    got = attend(c, partition_size=psize).float().cpu().double().numpy()
+    assert np.isfinite(got).all()
+    checked = 0
+    for b, n in enumerate(c.lens):
+        for h in range(4):
+            K, V = (c.rows(p, b, h // 2, int(n), name) for p, name in ((c.k, "k"), (c.v, "v")))
+            for t in range(T):
+                x = O.bf16_bits_to_f64(c.q[b, t, h])
+                s = K[:n - T + t + 1] @ x
+                size = (np.abs(K[:n - T + t + 1]) @ np.abs(x)).max()
+                top = np.sort(s)[-2:]
+                # A score errs by 2^-20 of sum |q k|: rows whose two largest are within four times
+                # that do not count.  Of the others the second one is more than 100 octaves down
+                # (2^-18 * 2^24 * 20 / 8, less the error), so that its weight is nothing.
+                if len(s) > 1 and top[1] - top[0] < 2.0 ** -18 * size:
+                    continue
+                assert size > 20 * 2.0 ** octaves
+                checked += 1
+                ref = V[int(np.argmax(s))]
+                # rounded to bf16, and times its scale to f16
+                assert (np.abs(got[b, t, h] - ref) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(ref)).all()
+    assert checked > 8 * T
