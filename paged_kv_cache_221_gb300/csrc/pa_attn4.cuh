@@ -38,21 +38,19 @@
 
 namespace pa {
 
-// NT n-tiles of 8 query rows per warp, NTW row columns (each a worker's job of its own), TP
-// pages per softmax step, STAGES staged steps per warp, MINB CTAs of WARPS warps per SM.
-template <int NT_, int NTW_, int TP_, int STAGES_, int MINB_, int WARPS_ = 4>
+// NT n-tiles of 8 query rows per warp, NTW row columns (each a worker's job of its own), STAGES
+// staged pages per warp, MINB CTAs of WARPS warps per SM.
+template <int NT_, int NTW_, int STAGES_, int MINB_, int WARPS_ = 4>
 struct Cfg4 {
-  static constexpr int NT = NT_, NTW = NTW_, TP = TP_, STAGES = STAGES_, MINB = MINB_;
+  static constexpr int NT = NT_, NTW = NTW_, STAGES = STAGES_, MINB = MINB_;
   static constexpr int kWarps = WARPS_, kThreads = 32 * kWarps, kRows = 8 * NT;
   static constexpr bool kQRegs = NT <= 2;
-  static_assert(32 % TP == 0, "a step's pages come from one batch of block ids");
 };
 
 template <int D, class C>
 struct Smem4 {
   using P = Page<kPageInt4, D>;
-  static constexpr int kPairBytes = 2 * P::kBytes;          // a K page, then its V page
-  static constexpr int kStageBytes = C::TP * kPairBytes;
+  static constexpr int kStageBytes = 2 * P::kBytes;         // a K page, then its V page
   static constexpr int kRingBytes = C::STAGES * kStageBytes;
   static constexpr int kQBytes = C::kQRegs ? 0 : C::NT * QTileSmem<kPageInt4, D>::kBytes;
   static constexpr int kWarpBytes = kRingBytes + kQBytes;
@@ -69,7 +67,7 @@ template <int D, class C, bool kFlat>
 __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const Attn4Params p) {
   using P = Page<kPageInt4, D>;
   using Sm = Smem4<D, C>;
-  constexpr int NT = C::NT, NTW = C::NTW, TP = C::TP, S = C::STAGES;
+  constexpr int NT = C::NT, NTW = C::NTW, S = C::STAGES;
   constexpr int NG = P::kGroups;
   extern __shared__ __align__(128) uint8_t smem_all[];
   grid_launch_dependents();
@@ -142,21 +140,16 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     auto issue = [&]() {
       if (it < n) {
         if ((it & 31) == 0 && it > 0) load_ids(it);
+        const uint32_t phys = __shfl_sync(0xffffffffu, ids, it & 31);
+        const uint8_t* kp = at_page(ksrc, phys, page_stride);
+        const uint8_t* vp = at_page(vsrc, phys, page_stride);
 #pragma unroll
-        for (int k = 0; k < TP; ++k) {
-          // a step past the last page stages page 0 of the pool, masked below
-          const uint32_t phys = __shfl_sync(0xffffffffu, ids, (it + k) & 31);
-          const uint8_t* kp = at_page(ksrc, phys, page_stride);
-          const uint8_t* vp = at_page(vsrc, phys, page_stride);
-          const uint32_t to = st_in + k * Sm::kPairBytes;
-#pragma unroll
-          for (int c = 0; c < P::kCodes / 512; ++c) {   // 8 (16) rows on: the same swizzle
-            cp_async_16(to + swz + 512 * c, kp + 512 * c, 16);
-            cp_async_16_hint(to + swz + P::kBytes + 512 * c, vp + 512 * c, v_policy);
-          }
-          if (lane < 2 * SC) cp_async_16(to + sdst, at_page(ssrc, phys, page_stride), 16);
+        for (int c = 0; c < P::kCodes / 512; ++c) {   // 8 (16) rows on: the same swizzle
+          cp_async_16(st_in + swz + 512 * c, kp + 512 * c, 16);
+          cp_async_16_hint(st_in + swz + P::kBytes + 512 * c, vp + 512 * c, v_policy);
         }
-        it += TP;
+        if (lane < 2 * SC) cp_async_16(st_in + sdst, at_page(ssrc, phys, page_stride), 16);
+        ++it;
         st_in = st_in + Sm::kStageBytes == ring + Sm::kRingBytes ? ring : st_in + Sm::kStageBytes;
       }
       cp_async_commit();
@@ -191,39 +184,33 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
     int tok0 = pg0 * kBlockSize;
     uint32_t st = ring;
 
-    for (int i = 0; i * TP < n; ++i) {
+    for (int i = 0; i < n; ++i) {
       cp_async_wait<S - 2>();
       __syncwarp();
       issue();                               // into the stage consumed last
-      float t[TP][NT][4];
-#pragma unroll
-      for (int k = 0; k < TP; ++k)
-        page_scores<kPageInt4, D>(t[k], st + k * Sm::kPairBytes, koff, qo, lane);
+      float t[NT][4];
+      page_scores<kPageInt4, D>(t, st, koff, qo, lane);
 
-      const bool edge = tok0 < lo || tok0 + (TP - 1) * kBlockSize > hi || (bad | bad_before) != 0;
-      // The end of page k's entries: none of a page that was not in the pool.  The batch of
-      // ids that page i0 came from is the newest one unless `it` has passed on.
-      auto end_of = [&](int k) {
-        const int i0 = i * TP + k;
-        const unsigned bits = (it - 1) >> 5 == i0 >> 5 ? bad : bad_before;
-        return (bits >> (i0 & 31)) & 1u ? 0 : part_end;
+      const bool edge = tok0 < lo || tok0 > hi || (bad | bad_before) != 0;
+      // The end of the page's entries: none of a page that was not in the pool.  The batch of ids
+      // that page i came from is the newest one unless `it` has passed on.
+      auto end_of_page = [&]() {
+        const unsigned bits = (it - 1) >> 5 == i >> 5 ? bad : bad_before;
+        return (bits >> (i & 31)) & 1u ? 0 : part_end;
       };
       if (edge) {
+        const int end = end_of_page();
+        const int j0 = tok0 + gid, j1 = j0 + 8;
 #pragma unroll
-        for (int k = 0; k < TP; ++k) {
-          const int end = end_of(k);
-          const int j0 = tok0 + k * kBlockSize + gid, j1 = j0 + 8;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const int r = row0 + 8 * j + 2 * q4;
-            const int a = r < nrows ? L - T + r / G : L - 1;
-            const int c = r + 1 < nrows ? L - T + (r + 1) / G : L - 1;
-            const unsigned w = p.wcap;
-            if (j0 >= end || static_cast<unsigned>(a - j0) >= w) t[k][j][0] = -CUDART_INF_F;
-            if (j0 >= end || static_cast<unsigned>(c - j0) >= w) t[k][j][1] = -CUDART_INF_F;
-            if (j1 >= end || static_cast<unsigned>(a - j1) >= w) t[k][j][2] = -CUDART_INF_F;
-            if (j1 >= end || static_cast<unsigned>(c - j1) >= w) t[k][j][3] = -CUDART_INF_F;
-          }
+        for (int j = 0; j < NT; ++j) {
+          const int r = row0 + 8 * j + 2 * q4;
+          const int a = r < nrows ? L - T + r / G : L - 1;
+          const int c = r + 1 < nrows ? L - T + (r + 1) / G : L - 1;
+          const unsigned w = p.wcap;
+          if (j0 >= end || static_cast<unsigned>(a - j0) >= w) t[j][0] = -CUDART_INF_F;
+          if (j0 >= end || static_cast<unsigned>(c - j0) >= w) t[j][1] = -CUDART_INF_F;
+          if (j1 >= end || static_cast<unsigned>(a - j1) >= w) t[j][2] = -CUDART_INF_F;
+          if (j1 >= end || static_cast<unsigned>(c - j1) >= w) t[j][3] = -CUDART_INF_F;
         }
       }
 
@@ -233,28 +220,18 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
       // loses below 2^-14 is at most 2^-25, so 2^-28 of the sum.  The reference is rounded so that
       // the maximum's own exponent is never below kTop, however large the scores.
       bool over = false;
-      float e[TP][NT][4];                    // scores less the reference
+      float e[NT][4];                        // scores less the reference
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        float x = -CUDART_INF_F;
-#pragma unroll
-        for (int k = 0; k < TP; ++k) {
-          const float* y = t[k][j];
-          fma_f32x2(e[k][j][0], e[k][j][1], y[0], y[1], qo.rs0[j], qo.rs1[j], nm0[j], nm1[j]);
-          fma_f32x2(e[k][j][2], e[k][j][3], y[2], y[3], qo.rs0[j], qo.rs1[j], nm0[j], nm1[j]);
-          x = fmaxf(x, fmaxf(fmaxf(e[k][j][0], e[k][j][1]), fmaxf(e[k][j][2], e[k][j][3])));
-        }
-        over |= x > 7.f;
+        const float* y = t[j];
+        fma_f32x2(e[j][0], e[j][1], y[0], y[1], qo.rs0[j], qo.rs1[j], nm0[j], nm1[j]);
+        fma_f32x2(e[j][2], e[j][3], y[2], y[3], qo.rs0[j], qo.rs1[j], nm0[j], nm1[j]);
+        over |= fmaxf(fmaxf(e[j][0], e[j][1]), fmaxf(e[j][2], e[j][3])) > 7.f;
       }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
-#pragma unroll
-          for (int k = 0; k < TP; ++k) {
-            x0 = fmaxf(x0, fmaxf(t[k][j][0], t[k][j][2]));
-            x1 = fmaxf(x1, fmaxf(t[k][j][1], t[k][j][3]));
-          }
+          float x0 = fmaxf(t[j][0], t[j][2]), x1 = fmaxf(t[j][1], t[j][3]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
@@ -271,16 +248,13 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
             f1 = nm1[j] == kUnseen ? 0.f : hw_exp2(nm - nm1[j]);
             nm1[j] = nm;
           }
+          e[j][0] = fmaf(t[j][0], qo.rs0[j], nm0[j]);
+          e[j][1] = fmaf(t[j][1], qo.rs1[j], nm1[j]);
+          e[j][2] = fmaf(t[j][2], qo.rs0[j], nm0[j]);
+          e[j][3] = fmaf(t[j][3], qo.rs1[j], nm1[j]);
+          // past 2^26 the product is rounded by more than the room above kTop (NaN stays NaN)
 #pragma unroll
-          for (int k = 0; k < TP; ++k) {
-            e[k][j][0] = fmaf(t[k][j][0], qo.rs0[j], nm0[j]);
-            e[k][j][1] = fmaf(t[k][j][1], qo.rs1[j], nm1[j]);
-            e[k][j][2] = fmaf(t[k][j][2], qo.rs0[j], nm0[j]);
-            e[k][j][3] = fmaf(t[k][j][3], qo.rs1[j], nm1[j]);
-            // past 2^26 the product is rounded by more than the room above kTop (NaN stays NaN)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[k][j][i] = e[k][j][i] > 7.f ? 7.f : e[k][j][i];
-          }
+          for (int i = 0; i < 4; ++i) e[j][i] = e[j][i] > 7.f ? 7.f : e[j][i];
           sum[j][0] *= f0;
           sum[j][1] *= f1;
           sum[j][2] *= f0;
@@ -294,115 +268,111 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           }
         }
       }
+      uint32_t ph0[NT], ph1[NT];             // P^T: tokens 2q, 2q+1 and 2q+8, 2q+9 of row gid
 #pragma unroll
-      for (int k = 0; k < TP; ++k) {
-        uint32_t ph0[NT], ph1[NT];             // P^T: tokens 2q, 2q+1 and 2q+8, 2q+9 of row gid
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float p0 = hw_exp2(e[k][j][0]);
-          const float p1 = hw_exp2(e[k][j][1]);
-          const float p2 = hw_exp2(e[k][j][2]);
-          const float p3 = hw_exp2(e[k][j][3]);
-          ph0[j] = transpose_8x8(half2_bits(__floats2half2_rn(p0, p1)));
-          ph1[j] = transpose_8x8(half2_bits(__floats2half2_rn(p2, p3)));
-        }
+      for (int j = 0; j < NT; ++j) {
+        const float p0 = hw_exp2(e[j][0]);
+        const float p1 = hw_exp2(e[j][1]);
+        const float p2 = hw_exp2(e[j][2]);
+        const float p3 = hw_exp2(e[j][3]);
+        ph0[j] = transpose_8x8(half2_bits(__floats2half2_rn(p0, p1)));
+        ph1[j] = transpose_8x8(half2_bits(__floats2half2_rn(p2, p3)));
+      }
 
-        // V scales of tokens 2q, 2q+1 (w0, w1) and 2q+8, 2q+9 (w2, w3), a byte per group
-        const uint32_t vp = st + k * Sm::kPairBytes + P::kBytes;
-        uint32_t w0, w1, w2, w3;
-        {
-          const uint32_t a = vp + P::kCodes + 2 * q4 * NG;
-          if constexpr (NG == 4) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(a));
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w2), "=r"(w3) : "r"(a + 32));
-          } else {
-            uint32_t x, y;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a));
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(y) : "r"(a + 16));
-            w0 = x & 0xffffu;
-            w1 = x >> 16;
-            w2 = y & 0xffffu;
-            w3 = y >> 16;
-          }
+      // V scales of tokens 2q, 2q+1 (w0, w1) and 2q+8, 2q+9 (w2, w3), a byte per group
+      const uint32_t vp = st + P::kBytes;
+      uint32_t w0, w1, w2, w3;
+      {
+        const uint32_t a = vp + P::kCodes + 2 * q4 * NG;
+        if constexpr (NG == 4) {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(a));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w2), "=r"(w3) : "r"(a + 32));
+        } else {
+          uint32_t x, y;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(y) : "r"(a + 16));
+          w0 = x & 0xffffu;
+          w1 = x >> 16;
+          w2 = y & 0xffffu;
+          w3 = y >> 16;
         }
-        if (edge) {
-          // entries that no query token sees may hold any scale, even NaN
-          const int nv = end_of(k) - (tok0 + k * kBlockSize);
-          const int first_seen = p.window > 0 ? max(0, L - T - p.window + 1) : 0;
-          const int from = first_seen - (tok0 + k * kBlockSize);
-          w0 = 2 * q4 < nv && 2 * q4 >= from ? w0 : 0u;
-          w1 = 2 * q4 + 1 < nv && 2 * q4 + 1 >= from ? w1 : 0u;
-          w2 = 2 * q4 + 8 < nv && 2 * q4 + 8 >= from ? w2 : 0u;
-          w3 = 2 * q4 + 9 < nv && 2 * q4 + 9 >= from ? w3 : 0u;
-          // A NaN scale makes the rows that see its token NaN and no others, whose weight of zero
-          // would not hold it off: it goes into the output tiles of those rows by hand.
-          const uint32_t n0 = e4m3_nan_bytes(w0), n1 = e4m3_nan_bytes(w1);
-          const uint32_t n2 = e4m3_nan_bytes(w2), n3 = e4m3_nan_bytes(w3);
-          if (__any_sync(0xffffffffu, (n0 | n1 | n2 | n3) != 0u)) {
+      }
+      if (edge) {
+        // entries that no query token sees may hold any scale, even NaN
+        const int nv = end_of_page() - tok0;
+        const int first_seen = p.window > 0 ? max(0, L - T - p.window + 1) : 0;
+        const int from = first_seen - tok0;
+        w0 = 2 * q4 < nv && 2 * q4 >= from ? w0 : 0u;
+        w1 = 2 * q4 + 1 < nv && 2 * q4 + 1 >= from ? w1 : 0u;
+        w2 = 2 * q4 + 8 < nv && 2 * q4 + 8 >= from ? w2 : 0u;
+        w3 = 2 * q4 + 9 < nv && 2 * q4 + 9 >= from ? w3 : 0u;
+        // A NaN scale makes the rows that see its token NaN and no others, whose weight of zero
+        // would not hold it off: it goes into the output tiles of those rows by hand.
+        const uint32_t n0 = e4m3_nan_bytes(w0), n1 = e4m3_nan_bytes(w1);
+        const uint32_t n2 = e4m3_nan_bytes(w2), n3 = e4m3_nan_bytes(w3);
+        if (__any_sync(0xffffffffu, (n0 | n1 | n2 | n3) != 0u)) {
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              auto bit = [&](uint32_t x) { return (x >> (8 * gr)) & 1u; };
-              unsigned at = (bit(n0) | bit(n1) << 1 | bit(n2) << 8 | bit(n3) << 9) << (2 * q4);
-              at |= __shfl_xor_sync(0xffffffffu, at, 1);
-              at |= __shfl_xor_sync(0xffffffffu, at, 2);
+          for (int gr = 0; gr < NG; ++gr) {
+            auto bit = [&](uint32_t x) { return (x >> (8 * gr)) & 1u; };
+            unsigned at = (bit(n0) | bit(n1) << 1 | bit(n2) << 8 | bit(n3) << 9) << (2 * q4);
+            at |= __shfl_xor_sync(0xffffffffu, at, 1);
+            at |= __shfl_xor_sync(0xffffffffu, at, 2);
 #pragma unroll
-              for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int r = row0 + 8 * j + 2 * q4 + h;
-                  const int last = r < nrows ? L - T + r / G : L - 1;
-                  const int first = p.window > 0 ? max(0, last - p.window + 1) : 0;
-                  const int t0 = tok0 + k * kBlockSize;
-                  const int lo_bit = max(0, first - t0), hi_bit = last - t0;
-                  const unsigned upto = hi_bit < 0 ? 0u : hi_bit > 15 ? 0xffffu : (2u << hi_bit) - 1u;
-                  if ((at & upto) >> min(lo_bit, 16) != 0u)
-                    acc[j][2 * gr][h] = acc[j][2 * gr][2 + h] = acc[j][2 * gr + 1][h] =
-                        acc[j][2 * gr + 1][2 + h] = CUDART_NAN_F;
-                }
-            }
-            w0 &= ~(n0 * 0xffu);
-            w1 &= ~(n1 * 0xffu);
-            w2 &= ~(n2 * 0xffu);
-            w3 &= ~(n3 * 0xffu);
+              for (int h = 0; h < 2; ++h) {
+                const int r = row0 + 8 * j + 2 * q4 + h;
+                const int last = r < nrows ? L - T + r / G : L - 1;
+                const int first = p.window > 0 ? max(0, last - p.window + 1) : 0;
+                const int lo_bit = max(0, first - tok0), hi_bit = last - tok0;
+                const unsigned upto = hi_bit < 0 ? 0u : hi_bit > 15 ? 0xffffu : (2u << hi_bit) - 1u;
+                if ((at & upto) >> min(lo_bit, 16) != 0u)
+                  acc[j][2 * gr][h] = acc[j][2 * gr][2 + h] = acc[j][2 * gr + 1][h] =
+                      acc[j][2 * gr + 1][2 + h] = CUDART_NAN_F;
+              }
           }
+          w0 &= ~(n0 * 0xffu);
+          w1 &= ~(n1 * 0xffu);
+          w2 &= ~(n2 * 0xffu);
+          w3 &= ~(n3 * 0xffu);
         }
+      }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_f16(sum[j], kOnes, kOnes, kOnes, kOnes, ph0[j], ph1[j]);
+      for (int j = 0; j < NT; ++j) mma_f16(sum[j], kOnes, kOnes, kOnes, kOnes, ph0[j], ph1[j]);
 #pragma unroll
-        for (int g2 = 0; g2 < NG; g2 += 2) {
-          // byte pairs (token 2q, token 2q+1) of groups g2 and g2 + 1
-          const uint32_t sel = g2 == 0 ? 0x5140u : 0x7362u;
-          const uint32_t sa = __byte_perm(w0, w1, sel), sb = __byte_perm(w2, w3, sel);
-          uint32_t fs[4];
-          e4m3x4_to_f16x4(sa, fs[0], fs[1]);
-          e4m3x4_to_f16x4(sb, fs[2], fs[3]);
-          uint32_t w[4];
-          ldsm_x4_trans(w[0], w[1], w[2], w[3], vp + (koff ^ (g2 << 4)));
+      for (int g2 = 0; g2 < NG; g2 += 2) {
+        // byte pairs (token 2q, token 2q+1) of groups g2 and g2 + 1
+        const uint32_t sel = g2 == 0 ? 0x5140u : 0x7362u;
+        const uint32_t sa = __byte_perm(w0, w1, sel), sb = __byte_perm(w2, w3, sel);
+        uint32_t fs[4];
+        e4m3x4_to_f16x4(sa, fs[0], fs[1]);
+        e4m3x4_to_f16x4(sb, fs[2], fs[3]);
+        uint32_t w[4];
+        ldsm_x4_trans(w[0], w[1], w[2], w[3], vp + (koff ^ (g2 << 4)));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int gr = g2 + h;
-            const uint32_t fa = fs[h], fb = fs[2 + h];
-            const uint32_t y0 = w[2 * h], y1 = w[2 * h + 1];
-            const uint32_t u0 = y0 >> 8, u1 = y1 >> 8;
-            // codes less 8 as f16 subnormals, exact: dims 32 gr + 4 gid + 0 and 2, then + 1 and 3
-            // (times 16)
-            const uint32_t x[4] = {y0, u0, y1, u1};
-            uint32_t a[4], c[4];
+        for (int h = 0; h < 2; ++h) {
+          const int gr = g2 + h;
+          const uint32_t fa = fs[h], fb = fs[2 + h];
+          const uint32_t y0 = w[2 * h], y1 = w[2 * h + 1];
+          const uint32_t u0 = y0 >> 8, u1 = y1 >> 8;
+          // codes less 8 as f16 subnormals, exact: dims 32 gr + 4 gid + 0 and 2, then + 1 and 3
+          // (times 16)
+          const uint32_t x[4] = {y0, u0, y1, u1};
+          uint32_t a[4], c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[i] = f16x2_add(x[i] & kNibLo, kMinus8Lo);
-              c[i] = f16x2_add(x[i] & kNibHi, kMinus8Hi);
-            }
+          for (int i = 0; i < 4; ++i) {
+            a[i] = f16x2_add(x[i] & kNibLo, kMinus8Lo);
+            c[i] = f16x2_add(x[i] & kNibHi, kMinus8Hi);
+          }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const uint32_t b0 = f16x2_mul(ph0[j], fa), b1 = f16x2_mul(ph1[j], fb);
-              mma_f16(acc[j][2 * gr], a[0], a[1], a[2], a[3], b0, b1);
-              mma_f16(acc[j][2 * gr + 1], c[0], c[1], c[2], c[3], b0, b1);
-            }
+          for (int j = 0; j < NT; ++j) {
+            const uint32_t b0 = f16x2_mul(ph0[j], fa), b1 = f16x2_mul(ph1[j], fb);
+            mma_f16(acc[j][2 * gr], a[0], a[1], a[2], a[3], b0, b1);
+            mma_f16(acc[j][2 * gr + 1], c[0], c[1], c[2], c[3], b0, b1);
           }
         }
       }
-      tok0 += TP * kBlockSize;
+      tok0 += kBlockSize;
       st = st + Sm::kStageBytes == ring + Sm::kRingBytes ? ring : st + Sm::kStageBytes;
     }
     cp_async_wait<0>();
@@ -433,7 +403,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
           constexpr float A = 16777216.f, B = 1048576.f;   // 2^24, 2^20
           const float* a = acc[j][2 * gr] + h;
           const float* c = acc[j][2 * gr + 1] + h;
-          const float4 o = make_float4(a[0] * A * inv, c[0] * B * inv, a[2] * A * inv, c[2] * B * inv);
+          const float4 o =
+              make_float4(a[0] * A * inv, c[0] * B * inv, a[2] * A * inv, c[2] * B * inv);
           const int d = 32 * gr + 4 * gid;
           if (seg.whole)
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + d) =
@@ -574,13 +545,13 @@ cudaError_t launch_attn4(const Attn4Params& p, int rows, cudaStream_t s) {
   // dependent fetch at a job's start waits longer.  Those two batches with rings of 3 / 4 / 6
   // single pages: 39.8 / 39.8 / 41.1 and 114.3 / 112.4 / 112.9 us; of 3 / 4 double ones:
   // 39.9 / 41.1 and 113.2 / 115.6.  16 warps per SM instead of 12 (128 registers): 41.8 and 118.
-  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 1, 4, 1, 12>>(p, s);
-  if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 1, 4, 2>>(p, s);
+  if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 4, 1, 12>>(p, s);
+  if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 4, 2>>(p, s);
   // 20 rows, 32 sequences of 2048-16384 tokens: 120 us, 125 with double pages, 182 with 12 warps
   // (168 registers: the output tile spills)
-  if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 1, 3, 2>>(p, s);
-  if (rows <= 32) return launch_cfg4<D, Cfg4<4, 1, 1, 3, 2>>(p, s);
-  return launch_cfg4<D, Cfg4<4, 2, 1, 3, 2>>(p, s);
+  if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 3, 2>>(p, s);
+  if (rows <= 32) return launch_cfg4<D, Cfg4<4, 1, 3, 2>>(p, s);
+  return launch_cfg4<D, Cfg4<4, 2, 3, 2>>(p, s);
 }
 
 }  // namespace pa
