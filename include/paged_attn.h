@@ -342,7 +342,8 @@ pa_status pa_decode_append(void* out, const void* q, const void* new_key, const 
  * octaves, so a head scale need only be of the order of the head's largest
  * magnitude / 1000 (between its largest magnitude / 3136, below which values saturate,
  * and a few thousandths of it); it lies in [2^-100, 2^100].  A NaN makes its 32 dims
- * NaN; infinities saturate.
+ * NaN; infinities saturate.  pa_copy_blocks does not take these pages: copy-on-write copies
+ * the num_kv_heads * page bytes of a block in each pool (cudaMemcpyAsync).
  */
 
 /*
@@ -454,6 +455,11 @@ size_t pa_accumulate_workspace_size(int num_seqs, int num_q_heads, int num_kv_he
  * sequence has seen (NULL: L, nothing evicted so far), gives them.  Only K pages are
  * read: kv_format PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_INT4, k_scale ignored for bf16.
  * q is bf16 [num_seqs, T, num_q_heads, head_dim].
+ * Every one of the T tokens counts, in every sequence.  Verified drafts: call it after
+ * acceptance, once for the sequences that kept the same number n of tokens, with T = n and
+ * the lengths that remain, or rejected drafts stay in the sums.  A prompt: successive calls of
+ * up to 64 query rows per kv head, context_lens at the end of each call's tokens, or its
+ * last tokens alone.
  * Requirements: head_dim 64 or 128, block_size 16, num_q_heads a multiple of
  * num_kv_heads, (num_q_heads/num_kv_heads) * T <= 64, num_seqs * num_kv_heads <= 65535,
  * max_context_len <= max_entries and <= max_blocks_per_seq * 16, q / k_cache 16-byte

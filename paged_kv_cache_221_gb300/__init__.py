@@ -657,7 +657,8 @@ def accumulate_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: tor
     each entry receives, in place or in ``out``; the T newest entries start afresh, and their
     ``positions`` are set from ``seq_lens`` (tokens seen by each sequence; default
     ``context_lens``).  The K pool may hold bf16, FP8 (with ``k_scale``) or INT4 pages (3-dim,
-    with ``k_scale``)."""
+    with ``k_scale``).  All T tokens of every sequence count: of verified drafts, pass those
+    that were accepted (one call for the sequences that kept the same number)."""
     fmt = _kv_format(k_cache)[0]
     dev = k_cache.device
     pool = k_cache.shape
