@@ -523,10 +523,12 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
   if (r != cudaSuccess || !p.flat) return r;
   const int live = std::min(C::kRows, p.G * p.T);   // rows of a tile that are used
   const unsigned rows = static_cast<unsigned>(jobs * live);
-  // more warps per row when a job has many runs
+  // More warps per row when a job has many runs.  32 warps or 8: one sequence of 16000 tokens (126
+  // runs per job) 13.8 and 15.9 us, 8 of 1000-2000 (16) 15.8 and 13.7.  8 warps or 1: 8 of
+  // 8000-16000 (28) 29.9 and 38.3, 16 of 1000-8000 with 32 query rows (9) 64.1 and 56.6.
   if (p.workers >= 64 * jobs)
-    return launch_behind(attn4_merge_kernel<D, 32>, dim3(rows), 1024, 0, s, true, p, C::NTW, C::kRows,
-                         live);
+    return launch_behind(attn4_merge_kernel<D, 32>, dim3(rows), 1024, 0, s, true, p, C::NTW,
+                         C::kRows, live);
   if (p.workers >= 12 * jobs)
     return launch_behind(attn4_merge_kernel<D, 8>, dim3(rows), 256, 0, s, true, p, C::NTW, C::kRows,
                          live);
