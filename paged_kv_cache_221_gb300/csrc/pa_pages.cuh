@@ -240,7 +240,7 @@ __device__ __forceinline__ void make_q_tile(QTile<F, D>& t, const QTileRaw<F, D>
     mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
     // its exponent, kept where 2^(13 - e) and its inverse are normal
     int e = static_cast<int>(mb >> 7) - 127;
-    e = max(-100, min(e, 100));
+    e = max(-100, min(e, 127));
     const float up = sign * __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
     rs *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
     if constexpr (F == kPageFp8) {

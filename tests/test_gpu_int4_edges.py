@@ -188,3 +188,14 @@ def test_scores_past_what_fp32_resolves(octaves, psize, D, T):
                 # rounded to bf16, and times its scale to f16
                 assert (np.abs(got[b, t, h] - ref) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(ref)).all()
     assert checked > 8 * T
+
+
+@pytest.mark.parametrize("octaves", [98, 105, 118])
+@pytest.mark.parametrize("T,D", [(1, 128), (5, 64)])
+def test_queries_near_the_largest_bf16(octaves, T, D):
+    """Query rows up to 2^120 against keys as small: ordinary scores."""
+    c = Case(52, [T, 40, 300], 4, 2, D, T=T, power_of_two=True)
+    c.q = W.f32_to_bf16_bits((O.bf16_bits_to_f64(c.q) * 2.0 ** octaves).astype(np.float32))
+    c.k_scale = (c.k_scale * 2.0 ** -95).astype(np.float32)
+    c.scale *= 2.0 ** (95 - octaves)
+    check(attend(c), c)

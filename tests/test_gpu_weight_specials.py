@@ -118,3 +118,14 @@ def test_bad_block_beside_a_nan_key(fmt):
     x = w[0, 0].cpu()
     assert (x[32:48] == 1).all() and (x[100:] == 1).all()
     assert torch.isnan(x[:32]).all() and torch.isnan(x[48:100]).all()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int4"])
+@pytest.mark.parametrize("octaves", [98, 118])
+def test_queries_near_the_largest_bf16(fmt, octaves):
+    """Query rows up to 2^120 against keys as small: ordinary scores."""
+    c = Case(36, [300, 40, 3], 6, 2, 64, T=3, fmt=fmt, power_of_two=True)
+    c.q = W.f32_to_bf16_bits((O.bf16_bits_to_f64(c.q) * 2.0 ** octaves).astype(np.float32))
+    c.k_scale = (c.k_scale * 2.0 ** -95).astype(np.float32)
+    c.scale *= 2.0 ** (95 - octaves)
+    assert np.isfinite(check(c)).all()
