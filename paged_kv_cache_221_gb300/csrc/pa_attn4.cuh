@@ -15,18 +15,18 @@
 // ldmatrix.trans delivers as (token 2q, token 2q + 1) pairs of four dims each.  A weight is
 // rounded to f16 twice, by itself (its row's sum is that of the rounded ones) and times the scale,
 // 2^-11 each.  Taking the codes' offset off the output afterwards instead of off the codes is
-// faster (39.2 against 41.2 us for the 64 sequences below, 111 against 116, 123 against 125), but a
+// faster (39.2 against 40.2 us for the 64 sequences below, 107 against 109, 119 against 122), but a
 // rounding then counts with a code of up to 15 instead of 7, one-sidedly where values are small;
-// taken off as a sum of the rounded products it costs 40.5, 115 and 142 us.
+// taken off as a sum of the rounded products it costs 40.5, 111 and 139 us.
 //
 // Measured (GPU time of a call, bytes of every page once, against a copy's 6780 GB/s): 64
-// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 39.2 us, 161 MB (0.61); 256 of 128-8192,
-// 64/8 heads, 107 us, 551 MB (0.76); one of 131071 35.2 us (0.60); five drafts over 32 of
-// 2048-16384 119 us, 324 MB (0.40).  What bounds it: for up to 8 rows memory and issue slots
-// (DRAM 58-73 %, issue 56-60 % of the whole launch) from the first page to the last, 5 us
+// sequences of 512-4096 tokens, 32/8 heads of 128 dims, 40.2 us, 161 MB (0.59); 256 of 128-8192,
+// 64/8 heads, 109 us, 551 MB (0.74); one of 131071 36.0 us (0.58); five drafts over 32 of
+// 2048-16384 122 us, 324 MB (0.39).  What bounds it: for up to 8 rows memory and issue slots
+// (DRAM 58-73 %, issue 58-62 % of the whole launch) from the first page to the last, 5 us
 // before that (2 to find the work, 3 for block ids and the first page), 3 us of uneven end and
 // the merge, 4 us; for 24 rows the latency of dependent tensor-core and FP32 steps with the 8 warps
-// per SM that 255 registers allow (tensor pipe 49 %, issue slots 45 %).
+// per SM that 255 registers allow (tensor pipe 48 %, issue slots 46 %).
 //
 // Balanced mode (kFlat): runs of pa_runs.cuh.  A job that lies in one run is written out
 // directly; the others leave (m, l, O) partials, which attn4_merge_kernel joins.
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB) paged_attn4_kernel(const
   const uint32_t koff = ldsm_offset<kPageInt4, D>(lane);
 
   // One column of rows reads a page once, so V pages leave the L2 cache first: the partial sums
-  // stay for the merge and the K pages for a call that sums up weights (32 sequences of 2048-16384
-  // tokens, 20 rows: 124.4 -> 123.5 us; the bounded decode step 93.7 -> 91.7 us).
+  // stay for the merge and the K pages for a call that sums up weights (the bounded decode step over
+  // 4-bit pages 87.0 -> 84.7 us; 256 sequences of 128-8192 tokens 113.6 -> 113.2).
   const uint64_t v_policy = read_policy(NTW == 1);
   Cursor<kFlat> cur;
   Segment seg;
@@ -538,19 +538,18 @@ cudaError_t launch_cfg4(const Attn4Params& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_attn4(const Attn4Params& p, int rows, cudaStream_t s) {
-  // One CTA of all the warps that an SM holds: its warps keep pace, where of three CTAs of four
-  // the oldest was served first and ended at 26 us, the newest at 33 (64 sequences of 512-4096
-  // tokens, 4 rows: 40.4 -> 39.8 us; 256 of 128-8192, 8 rows: 118.0 -> 112.4; before scores and
-  // softmax took two values per instruction, now 39.2 and 110.6).  With 16 and 24
-  // rows it loses (56.1 -> 58.3, 119 -> 129 us).
-  // Pages in flight per warp: with more of them the queues in front of memory grow and every
-  // dependent fetch at a job's start waits longer.  Those two batches with rings of 3 / 4 / 6
-  // single pages: 39.8 / 39.8 / 41.1 and 114.3 / 112.4 / 112.9 us; of 3 / 4 double ones:
-  // 39.9 / 41.1 and 113.2 / 115.6.  16 warps per SM instead of 12 (128 registers): 41.8 and 118.
+  // Measured on 64 sequences of 512-4096 tokens (4 rows), 256 of 128-8192 (8 rows, with an
+  // append) and one of 131071 (4 rows); other forms behind the committed one's 40.2 / 113.2 / 35.9
+  // us.  One CTA of all the warps that an SM holds, so that its warps keep pace: three of four
+  // warps each 40.4 / 118.1 / 37.0.  Pages in flight per warp, since with more of them the
+  // queues in front of memory grow and every dependent fetch at a job's start waits longer: rings of
+  // 3 pages 40.2 / 115.0 / 35.6, of 6 41.6 / 114.3 / 37.0.  16 warps (128 registers) 43.1 / 120.4 /
+  // 38.8.
   if (rows <= 8) return launch_cfg4<D, Cfg4<1, 1, 4, 1, 12>>(p, s);
+  // Two CTAs of four warps rather than one of eight: 16 rows (64 sequences of 512-4096 tokens) 59.4
+  // and 60.3 us, 20 rows (32 of 2048-16384, with an append) 125.4 and 132.7; with 12 warps per SM
+  // (168 registers: the output tile spills) 152.
   if (rows <= 16) return launch_cfg4<D, Cfg4<2, 1, 4, 2>>(p, s);
-  // 20 rows, 32 sequences of 2048-16384 tokens: 120 us, 125 with double pages, 182 with 12 warps
-  // (168 registers: the output tile spills)
   if (rows <= 24) return launch_cfg4<D, Cfg4<3, 1, 3, 2>>(p, s);
   if (rows <= 32) return launch_cfg4<D, Cfg4<4, 1, 3, 2>>(p, s);
   return launch_cfg4<D, Cfg4<4, 2, 3, 2>>(p, s);

@@ -12,7 +12,7 @@ namespace pa {
 // thread copies its 16 bytes of every row's scores to shared memory, all rows in flight at
 // once, and sums over them.  Twice as many CTAs as are resident at once: the jobs' lengths
 // differ, and what a CTA does before its first tile costs (a call with 1 / 2 / 4 times as many:
-// 121.6 / 118.4 / 123.1 us; equal runs of tiles per CTA: 121.1).  Bound by the scores' bytes on
+// 115.2 / 113.3 / 117.4 us).  Bound by the scores' bytes on
 // their way out of L2 and back: 189 MB of 20 rows (32 sequences of 2048-16384 tokens) take 37
 // us; a second buffer per CTA (half the CTAs) took 8 us more, refilling each quarter of the
 // rows as it is read 6.
@@ -192,7 +192,7 @@ __device__ __forceinline__ int2 over_warps(int2 mine, int2& total, int2* sh) {
 }
 
 // One entry to its new place, a warp: its K and V rows, weight and position.  For the few moves
-// of a decode step, which the selecting CTA makes itself (the bounded decode step 91.5 -> 89.5 us
+// of a decode step, which the selecting CTA makes itself (the bounded decode step 87.2 -> 85.9 us
 // on the GPU and a launch less on the host).
 __device__ __forceinline__ void move_entry(const EvictParams& p, int b, int g, int2 mv, size_t row,
                                            int lane) {

@@ -11,7 +11,7 @@
 //
 // Measured (GPU time of a call): 64 sequences of 512-4096 tokens, 32/8 heads of 128 dims, bf16
 // pages, 58 us (302 MB of K; the first launch alone 53 us, 5.7 TB/s: bound by memory); five
-// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 112 us: 75 us of scores (160
+// verified tokens over 4-bit pages, 32 sequences of 2048-16384, 113 us: 75 us of scores (160
 // MB of K, 189 MB written; 69 us with the stores left out: bound by the score tiles), 37
 // us of sums.  The sequences in 2, 3 or 4 parts through one smaller scratch, so that the scores
 // stay in L2: 130, 146, 160 us.
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(C::kThreads, C::MINB)
 
   // The scores are read again by the second launch, the pages (of a single column) not, so the
   // pages leave the L2 cache first, as the scores do once they have been summed.  64 sequences
-  // of 512-4096 tokens, bf16: 61.8 -> 58.2 us; five verified tokens over 4-bit pages: 117.1 ->
-  // 112.5.
+  // of 512-4096 tokens, bf16: 61.9 -> 58.5 us; five verified tokens over 4-bit pages, whose pages
+  // are fewer bytes than their scores: 111.6 -> 113.3.
   const uint64_t policy = read_policy(NTW == 1);
   Cursor<kFlat> cur;
   Segment seg;

@@ -24,7 +24,7 @@ struct RunList {
 
 // Block ids and the first pages are fetched one after the other: about the time of five pages
 // on a busy GPU.  256 sequences of 128-8192 tokens, whose short ones fall several to a run:
-// 126.6 / 118.4 / 117.2 us with 1 / 3 / 6.
+// 125.7 / 116.5 / 113.5 / 114.9 us with 1 / 3 / 5 / 7.
 constexpr int kSetup = kRunSetup;
 
 // Pages that a sequence's query tokens can see, from page `first` on (0 if its length is out of
