@@ -129,3 +129,28 @@ def test_queries_near_the_largest_bf16(fmt, octaves):
     c.k_scale = (c.k_scale * 2.0 ** -95).astype(np.float32)
     c.scale *= 2.0 ** (95 - octaves)
     assert np.isfinite(check(c)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("octaves", [26, 60, 80])
+def test_scores_past_what_fp32_resolves(fmt, octaves):
+    """Scores so large that their rounding is octaves: the largest one takes all the weight."""
+    c = Case(37, [300, 40, 2000], 4, 2, 64, fmt=fmt)
+    c.q = W.f32_to_bf16_bits((O.bf16_bits_to_f64(c.q) * 2.0 ** octaves).astype(np.float32))
+    w = torch.zeros((3, 2, 2000), device="cuda")
+    pa.accumulate_weights(to_dev(c.q), to_dev(c.k), to_dev(c.tables), to_dev(c.lens), w,
+                          max_context_len=2000, scale=c.scale,
+                          k_scale=None if fmt == "bf16" else to_dev(c.k_scale))
+    assert pa.get_device_error() == 0
+    for b, n in enumerate(c.lens):
+        for g in range(2):
+            K = c.rows(c.k, b, g, int(n), "k")
+            ref = np.zeros(2000)
+            for h in (2 * g, 2 * g + 1):
+                x = O.bf16_bits_to_f64(c.q[b, 0, h])
+                s, size = K @ x, (np.abs(K) @ np.abs(x)).max()
+                top = np.sort(s)[-2:]
+                # a score errs by 2^-20 of sum |q k|; the second one is over 100 octaves down
+                assert top[1] - top[0] > 2.0 ** -18 * size and size > 20 * 2.0 ** octaves
+                ref[np.argmax(s)] += 1.0
+            np.testing.assert_array_equal(w[b, g].cpu().numpy(), ref)
