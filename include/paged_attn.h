@@ -608,6 +608,52 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
                          int block_size, pa_stream_t stream);
 
 /*
+ * pa_prompt_attention — causal attention of whole prompts, or of any number of
+ * new tokens per sequence, over their pages.  Query tokens are packed: those of
+ * sequence b are rows query_starts[b] .. query_starts[b + 1] - 1 of q, the
+ * newest positions of its context (context_lens[b] counts them; their K/V have
+ * been stored before, as have those of a cached prefix).  With T_b of them,
+ * query token t sits at position i = context_lens[b] - T_b + t and sees the
+ * positions j <= i, with window_size W > 0 only i - W < j <= i.
+ *
+ *   q, out        [num_tokens, num_q_heads, head_dim]   bf16
+ *   query_starts  [num_seqs + 1]                         int32, ascending; T_b may
+ *                 be 0 (also with an empty context).  Rows of out before
+ *                 query_starts[0] and from query_starts[num_seqs] on are left
+ *                 as they are
+ *   k_cache, v_cache, k_scale, v_scale, kv_dtype: bf16 or FP8 pages as for
+ *                 pa_attention (scales are read for FP8 pages only)
+ *
+ * The keys of a query tile are cut into partitions of partition_size tokens (a
+ * multiple of 128; 0 = chosen for the sizes: none unless there are few query
+ * tiles), whose results a second kernel joins through the workspace
+ * (pa_prompt_workspace_size bytes, 256-byte aligned; without one and with
+ * partition_size 0 nothing is cut).  Softmax statistics and accumulation are
+ * fp32; the weights are rounded to bf16 where they meet the values.  A slot
+ * that a query token must not see does not reach it, whatever it holds; a NaN
+ * or infinity that it sees does.
+ * Requirements: pointers 16-byte aligned, head_dim 64 or 128, block_size 16,
+ * num_q_heads / num_kv_heads at most 128, num_blocks * num_kv_heads * 16 below
+ * 2^31.  A sequence with context_lens[b] < T_b or > max_context_len, or with
+ * starts out of order or outside [0, num_tokens], sets PA_ERR_BOUNDS on the
+ * device and its rows are skipped; a block id outside the pool sets it too and
+ * leaves that sequence's rows unspecified.
+ */
+pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale, int kv_dtype,
+                              int window_size, const int32_t* block_tables,
+                              int max_blocks_per_seq, const int32_t* context_lens,
+                              int max_context_len, const int32_t* query_starts, int num_tokens,
+                              int num_seqs, int num_blocks, int num_q_heads, int num_kv_heads,
+                              int head_dim, int block_size, float scale, int partition_size,
+                              void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/* Scratch bytes pa_prompt_attention needs with these sizes (0 if none). */
+size_t pa_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                int max_context_len, int head_dim, int block_size,
+                                int partition_size, int window_size);
+
+/*
  * pa_spec_accept — speculative decoding, after pa_verify: which of the K draft
  * tokens of each sequence the target keeps, and the one token the target then
  * emits ("ranksignal" post, Spéculer : plusieurs tokens par passe: drafts are

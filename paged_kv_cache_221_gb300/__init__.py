@@ -51,7 +51,7 @@ __all__ = ["reshape_and_cache", "decode", "verify", "decode_shared_prefix", "wor
            "attention", "spec_accept", "GraphRunner", "reshape_and_cache_int4",
            "gather_cache_int4", "attention_int4", "int4_workspace_size", "int4_page_bytes",
            "accumulate_weights", "accumulate_workspace_size", "evict_tokens",
-           "evict_workspace_size",
+           "evict_workspace_size", "prompt_attention", "prompt_workspace_size",
            "PagedAttnError", "STATUS_NAMES"]
 
 
@@ -757,6 +757,65 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
           positions.data_ptr(), entries[2], int(budget), int(num_recent), B, NB, Hkv, D, BS, ws,
           wsb)
     return new_lens
+
+
+@functools.lru_cache(maxsize=1024)
+def prompt_workspace_size(num_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                          max_context_len: int, head_dim: int, partition_size: int = 0,
+                          window_size: int = 0) -> int:
+    """Scratch bytes ``prompt_attention`` needs with these sizes (0 if none)."""
+    return int(library().pa_prompt_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads,
+                                                  max_context_len, head_dim, 16, partition_size,
+                                                  window_size))
+
+
+def prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     query_starts: torch.Tensor, max_context_len: Optional[int] = None,
+                     scale: Optional[float] = None, window_size: int = 0,
+                     partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of packed prompts over their pages: q [N, Hq, D], of which rows
+    ``query_starts[b] .. query_starts[b + 1] - 1`` (int32 [B + 1]) are the newest positions of
+    sequence b's context, already stored in the cache (with a cached prefix in front of them, or
+    none).  Any number of query tokens per sequence, 0 among them; rows of ``out`` that belong
+    to no sequence are left as they are.  bf16 pools, or FP8 pools with ``k_scale`` /
+    ``v_scale``; ``window_size`` > 0 limits each query token to its last ``window_size``
+    positions."""
+    fp8 = k_scale is not None or v_scale is not None
+    if fp8:
+        dev, NB, Hkv, BS, D = _fp8_pools(k_cache, v_cache, k_scale, v_scale)
+    else:
+        _need("k_cache", k_cache, _bf16, 4)
+        dev = k_cache.device
+        _want("v_cache", v_cache, _bf16, 4, dev)
+        NB, Hkv, BS, D = k_cache.shape
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("inconsistent shapes")
+    _want("q", q, _bf16, 3, dev)
+    _want("block_tables", block_tables, _i32, 2, dev)
+    _want("context_lens", context_lens, _i32, 1, dev)
+    _want("query_starts", query_starts, _i32, 1, dev)
+    N, Hq, Dq = q.shape
+    B, mbs = block_tables.shape
+    if Dq != D or context_lens.numel() != B or query_starts.numel() != B + 1:
+        raise ValueError("inconsistent shapes")
+    mcl = max(1, _max_len(max_context_len, context_lens, 1))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want("out", out, _bf16, 3, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    need = prompt_workspace_size(N, B, Hq, Hkv, mcl, D, partition_size, window_size)
+    ws, wsb, keep = _scratch(dev, workspace, need)
+    _call("pa_prompt_attention", dev, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scale.data_ptr() if fp8 else None,
+          v_scale.data_ptr() if fp8 else None, _KV_FP8 if fp8 else _KV_BF16, int(window_size),
+          block_tables.data_ptr(), mbs, context_lens.data_ptr(), mcl, query_starts.data_ptr(), N, B,
+          NB, Hq, Hkv, D, BS, D ** -0.5 if scale is None else float(scale), partition_size, ws, wsb)
+    return out
 
 
 def get_device_error(device=None) -> int:

@@ -85,6 +85,9 @@ SIGNATURES = {
     "pa_evict_workspace_size": (_sz, [_i, _i, _i, _i]),
     "pa_evict_tokens": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                              _i, _i, _i, _vp, _sz, _vp]),
+    "pa_prompt_attention": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i,
+                                 _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "pa_prompt_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "pa_bm_truncate": (_i, [_vp, _i, _i]),
     "pa_bm_create": (_i, [_i, _i, ctypes.POINTER(_vp)]),
     "pa_bm_destroy": (None, [_vp]),

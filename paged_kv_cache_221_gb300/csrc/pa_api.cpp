@@ -72,6 +72,23 @@ bool encode_fp8_maps(CUtensorMap* tk, CUtensorMap* tv, const void* k_base, const
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query rows [num_tokens, Hkv, G, D] bf16; a box is 64 dims of the G heads of one kv head for
+// `box_tokens` tokens, so that row (token, head of the group) lands 128 bytes behind the last.
+bool encode_query_map(CUtensorMap* map, const void* q, int num_tokens, int hkv, int G, int head_dim,
+                      int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(G),
+                        static_cast<cuuint64_t>(hkv), static_cast<cuuint64_t>(num_tokens)};
+  cuuint64_t strides[3] = {row, row * G, row * G * hkv};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The kernel of this host thread's last per-sequence attention launch
@@ -153,6 +170,45 @@ Plan make_plan(int num_seqs, int hq, int T, int max_ctx, int head_dim, int parti
   pl.off_ml = po;
   pl.off_counter = po + pm;
   pl.ws_bytes = po + pm + 256;
+  return pl;
+}
+
+// Prompt attention: how the keys of a pair of query tiles are cut.
+struct PromptPlan {
+  int sub_tokens = 1;     // query tokens of a tile
+  int num_slots = 1;      // pairs of tiles at most
+  int split = 1;          // K/V tiles per partition
+  int max_parts = 1;
+  long long units = 0;    // (pair, kv head, partition) at most
+  size_t bytes = 0, off_ml = 0;
+};
+
+PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int max_ctx,
+                       int head_dim, int partition_size, int window, bool scratch) {
+  PromptPlan pl;
+  pl.sub_tokens = kPromptTile / (hq / hkv);
+  const int pair = 2 * pl.sub_tokens;
+  const long long slots = num_tokens / pair + num_seqs;
+  pl.num_slots = static_cast<int>(std::min<long long>(slots, 1ll << 30));
+  long long keys = max_ctx;
+  if (window > 0) keys = std::min<long long>(keys, static_cast<long long>(window) + pair - 1 +
+                                                       kPromptTile);
+  const int tiles = ceil_div(keys, kPromptTile);
+  pl.split = tiles;
+  if (partition_size > 0) {
+    pl.split = std::min(tiles, partition_size / kPromptTile);
+  } else if (scratch) {
+    const long long pairs = slots * hkv;
+    if (pairs < 152) pl.split = std::max(4, ceil_div(tiles * pairs, 304));
+  }
+  pl.split = std::min(pl.split, tiles);
+  pl.max_parts = ceil_div(tiles, pl.split);
+  pl.units = slots * hkv * pl.max_parts;
+  if (pl.max_parts > 1) {
+    const size_t rows = static_cast<size_t>(num_tokens) * hq * pl.max_parts;
+    pl.off_ml = round256(rows * head_dim * sizeof(float));
+    pl.bytes = pl.off_ml + round256(rows * sizeof(float2));
+  }
   return pl;
 }
 
@@ -739,6 +795,105 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
   return run_attention(a);
 }
 
+size_t pa_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                int max_context_len, int head_dim, int block_size,
+                                int partition_size, int window_size) {
+  if (num_tokens <= 0 || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      max_context_len <= 0 || head_dim <= 0 || block_size != kBlockSize || partition_size < 0 ||
+      partition_size % kPromptTile != 0 || window_size < 0 || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > kPromptTile)
+    return 0;
+  return prompt_plan(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_context_len, head_dim,
+                     partition_size, window_size >= max_context_len ? 0 : window_size, true)
+      .bytes;
+}
+
+pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale, int kv_dtype,
+                              int window_size, const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int max_context_len,
+                              const int32_t* query_starts, int num_tokens, int num_seqs,
+                              int num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
+                              int block_size, float scale, int partition_size, void* workspace,
+                              size_t workspace_bytes, pa_stream_t stream) {
+  if (num_tokens < 0 || num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 1 || partition_size < 0 || window_size < 0 ||
+      (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3))
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_starts)
+    return PA_ERR_INVALID_ARG;
+  const bool kv8 = kv_dtype == PA_KV_FP8_E4M3;
+  if (kv8 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+  const int G = num_q_heads / num_kv_heads;
+  if (G > kPromptTile) return PA_ERR_UNSUPPORTED;
+  if (max_context_len < 1 || static_cast<long long>(max_context_len) >
+                                 static_cast<long long>(max_blocks_per_seq) * kBlockSize)
+    return PA_ERR_INVALID_ARG;
+  if (partition_size % kPromptTile != 0) return PA_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(num_blocks) * num_kv_heads * kBlockSize;
+  if (rows >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (max_context_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  // a window that covers every context is none
+  const int window = window_size >= max_context_len ? 0 : window_size;
+  const PromptPlan plan =
+      prompt_plan(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_context_len, head_dim,
+                  partition_size, window, workspace != nullptr);
+  // the units of work are counted in 32 bits, and one row of the merge's grid in 16
+  if (plan.units >= (1ll << 31) - 65536 || plan.max_parts > 65535) return PA_ERR_UNSUPPORTED;
+  if (plan.bytes > 0) {
+    if (!workspace || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  }
+  CUtensorMap tq, tk, tv;
+  if (!encode_query_map(&tq, q, num_tokens, num_kv_heads, G, head_dim, plan.sub_tokens))
+    return PA_ERR_CUDA;
+  if (kv8) {
+    if (!encode_fp8_maps(&tk, &tv, k_cache, v_cache,
+                         static_cast<long long>(num_blocks) * num_kv_heads, head_dim))
+      return PA_ERR_CUDA;
+  } else if (!encode_pool_map(&tk, k_cache, rows, head_dim) ||
+             !encode_pool_map(&tv, v_cache, rows, head_dim)) {
+    return PA_ERR_CUDA;
+  }
+  PromptParams p{};
+  p.out = out;
+  p.v_pool = v_cache;
+  p.k_scale = kv8 ? k_scale : nullptr;
+  p.v_scale = kv8 ? v_scale : nullptr;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_starts = query_starts;
+  if (plan.bytes > 0) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.off_ml);
+  }
+  p.mbs = max_blocks_per_seq;
+  p.max_ctx = max_context_len;
+  p.num_seqs = num_seqs;
+  p.num_rows = num_tokens;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.G = G;
+  p.num_blocks = num_blocks;
+  p.sub_tokens = plan.sub_tokens;
+  p.num_slots = plan.num_slots;
+  p.split = plan.split;
+  p.max_parts = plan.max_parts;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = window;
+  p.timeout_ns = kDefaultTimeoutNs;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = head_dim == 64 ? launch_prompt_d64(tq, tk, tv, p, kv8, s)
+                                       : launch_prompt_d128(tq, tk, tv, p, kv8, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status pa_spec_accept(const float* target_probs, const float* draft_probs,
                          const int32_t* draft_tokens, const uint32_t* accept_uniforms,
                          const uint32_t* sample_uniforms, int num_seqs, int num_drafts,
@@ -1073,7 +1228,8 @@ pa_status pa_get_device_error(pa_stream_t stream) {
       take_error_attn4_d64(&bits) != cudaSuccess || take_error_attn4_d128(&bits) != cudaSuccess ||
       take_error_cache4(&bits) != cudaSuccess || take_error_observe_bf16(&bits) != cudaSuccess ||
       take_error_observe_fp8(&bits) != cudaSuccess ||
-      take_error_observe_int4(&bits) != cudaSuccess || take_error_evict(&bits) != cudaSuccess)
+      take_error_observe_int4(&bits) != cudaSuccess || take_error_evict(&bits) != cudaSuccess ||
+      take_error_prompt_d64(&bits) != cudaSuccess || take_error_prompt_d128(&bits) != cudaSuccess)
     return PA_ERR_CUDA;
   if (bits & kErrTimeout) return PA_ERR_TIMEOUT;
   if (bits & kErrBounds) return PA_ERR_BOUNDS;

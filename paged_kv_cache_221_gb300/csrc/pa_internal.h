@@ -125,6 +125,28 @@ struct ObserveParams {
   float scale_log2, decay;
 };
 
+// Attention of whole prompts (pa_prompt.cuh).
+struct PromptParams {
+  void* out;                      // bf16 [num_rows, Hq, D]
+  const void* v_pool;
+  const float* k_scale;           // [Hkv], FP8 pages
+  const float* v_scale;
+  const int32_t* block_tables;    // [B, mbs]
+  const int32_t* context_lens;    // [B]
+  const int32_t* query_starts;    // [B + 1]
+  float* part_o;                  // scratch [num_rows, Hq, max_parts, D]
+  float2* part_ml;                // scratch [num_rows, Hq, max_parts]: as for split-KV decoding
+  int mbs, max_ctx, num_seqs, num_rows, Hq, Hkv, G, num_blocks;
+  int sub_tokens;                 // query tokens of a 128-row tile: 128 / G
+  int num_slots;                  // bound on the pairs of tiles: num_rows / (2 sub_tokens) + B
+  int split;                      // K/V tiles per partition
+  int max_parts;                  // partitions of a pair of tiles at most
+  float scale_log2;
+  int window;                     // 0 = none
+  unsigned long long timeout_ns;
+};
+constexpr int kPromptTile = 128;  // rows of a query tile, and keys of a K/V tile
+
 // Eviction: the first launch selects and pairs movers with gaps, the second moves.
 struct EvictParams {
   void* k_pool;
@@ -229,6 +251,12 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* pair
                                cudaStream_t s);
 cudaError_t launch_selftest_wait(unsigned long long timeout_ns, cudaStream_t s);
 
+// Prompt attention: bf16 or FP8 pages; tq maps q as [num_rows, Hkv, G, D].
+cudaError_t launch_prompt_d64(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const PromptParams& p, bool kv8, cudaStream_t s);
+cudaError_t launch_prompt_d128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PromptParams& p, bool kv8, cudaStream_t s);
+
 // Read and clear the device error word of each translation unit (synchronous).
 cudaError_t take_error_attn_d64(unsigned* bits);
 cudaError_t take_error_attn_d128(unsigned* bits);
@@ -250,5 +278,7 @@ cudaError_t take_error_observe_bf16(unsigned* bits);
 cudaError_t take_error_observe_fp8(unsigned* bits);
 cudaError_t take_error_observe_int4(unsigned* bits);
 cudaError_t take_error_evict(unsigned* bits);
+cudaError_t take_error_prompt_d64(unsigned* bits);
+cudaError_t take_error_prompt_d128(unsigned* bits);
 
 }  // namespace pa

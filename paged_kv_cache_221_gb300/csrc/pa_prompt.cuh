@@ -1,0 +1,799 @@
+// Causal attention of whole prompts over the paged cache, on the fifth-generation
+// tensor cores.
+//
+// Query tokens of all sequences are packed; those of sequence b are the newest
+// positions of its context.  With x_j = scale * q . k_j over the visible keys j,
+//   out = sum_j 2^((x_j - m) log2 e) v_j / sum_j 2^((x_j - m) log2 e),
+// m a running reference that follows the row's maximum.
+//
+// Tiles.  The query rows of one kv head are (token, query head of the group) pairs; 128
+// of them (sub_tokens tokens x G heads) are the M dimension of both products:
+//   S[128 rows x 128 keys] = Q . K^T        Q, K in shared memory        (tensor memory)
+//   O[128 rows x D]       += P . V          P in tensor memory, over S   (tensor memory)
+// A unit of work is a pair of such tiles (consecutive tokens) of one kv head, or one
+// partition of its keys, so that each K/V tile that a CTA loads serves 256 rows and one
+// tile's products run while the other tile's weights are computed.
+//
+// Roles of a CTA (persistent, one per SM):
+//   warps 0-3, 4-7  softmax of the first, the second tile: thread = row.  The reference
+//                   moves only when a score passes it by 8 (log2 units); O is then
+//                   rescaled in tensor memory, which no product is using at that time:
+//                   S of the next keys is issued behind P . V of the last ones.
+//   warp 8          finds the units, loads Q and the K/V tiles by TMA, 16 keys per page
+//                   box, through the block table.
+//   warp 9          one thread issues every MMA: per K/V tile P.V then the next S of the
+//                   first tile, the same of the second.
+//   warps 10, 11    tiles at a border of the mask: V rows behind the context become zero,
+//                   and so do infinities and NaN of V rows that some query row must not
+//                   see (0 * inf would reach it); the rows that see those keys get them
+//                   added at the end.
+//
+// Weights are rounded to bf16 (2^-8 of each at most) for the second product, as are the
+// values they meet; statistics and accumulators are fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "pa_pages.cuh"
+#include "pa_ptx.cuh"
+#include "pa_tc.cuh"
+
+namespace pa {
+
+template <int D, bool KV8>
+struct PromptGeo {
+  static constexpr int kSoftmaxWarps = 8;
+  static constexpr int kAux = 2;                         // warps for the borders of the mask
+  static constexpr int kThreads = (kSoftmaxWarps + 2 + kAux) * 32;
+  static constexpr int kHalves = D / 64;                 // 64-dim halves of a row (128 bytes)
+  static constexpr int kHalfBytes = kPromptTile * 128;
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kStages = 5;                      // K and V tiles in flight
+  static constexpr int kPages = kPromptTile / kBlockSize;
+  // shared memory, from a 1024-byte aligned base
+  static constexpr int kRingOff = 2 * kTileBytes;        // behind the two Q tiles
+  static constexpr int kMiscOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kMiscBytes = 1024;
+  static constexpr int kAlloc = kMiscOff + kMiscBytes + 1024;
+  // tensor memory columns
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kO = 2 * kPromptTile;        // S tiles at 0 and 128, then O
+  // registers per thread: launch, softmax warps, others
+  static constexpr int kRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
+  static_assert(kAlloc <= 232448, "shared memory per block");
+  static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs <=
+                    kThreads * kRegs, "the split takes no more than the launch has");
+};
+
+// One unit of work.
+struct PromptUnit {
+  int b;                 // sequence, -1 behind the last unit
+  int head;              // kv head
+  int row0, ntok;        // packed query tokens [row0, row0 + ntok)
+  int pos0;              // position of the first of them
+  int L;                 // context length
+  int t0, t1;            // K/V tiles [t0, t1)
+  int part, parts;
+  int nonfinite;         // infinities or NaN were taken out of V tiles at the mask's border
+};
+
+template <int D, bool KV8>
+struct PromptMisc {
+  using Gm = PromptGeo<D, KV8>;
+  uint64_t full[Gm::kStages];
+  uint64_t empty[Gm::kStages];
+  uint64_t border, checked;            // a V tile at the mask's border is there, is looked at
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
+  uint64_t unit_full[2], unit_empty[2], unit_checked[2]; // by record
+  uint64_t fin;
+  PromptUnit unit[2];
+  uint32_t tmem_base;
+};
+
+// The unit with index u (kv heads fastest, then pairs of tiles, then partitions), found by a
+// whole warp.  Sequence b owns the pairs from query_starts[b] / pair + b on, which leaves every
+// sequence enough of them without a sum over the others; those it has no use for are empty.
+// Its last tokens come first, because they see the most keys.
+__device__ __forceinline__ bool prompt_unit(const PromptParams& p, int u, PromptUnit& un,
+                                            bool* bad) {
+  const int lane = threadIdx.x & 31;
+  const int pair = 2 * p.sub_tokens;
+  *bad = false;
+  un.head = u % p.Hkv;
+  const int slot = u / p.Hkv % p.num_slots;
+  un.part = u / p.Hkv / p.num_slots;
+  int lo = 0, hi = p.num_seqs;
+  do {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    bool below = false;
+    if (at < hi) {
+      const int q = min(max(__ldg(p.query_starts + at), 0), p.num_rows);
+      below = q / pair + at <= slot;
+    }
+    const int n = __popc(__ballot_sync(0xffffffffu, below));
+    if (n == 0) return false;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  } while (hi - lo > 1);
+  const int s0 = __ldg(p.query_starts + lo), s1 = __ldg(p.query_starts + lo + 1);
+  const int L = __ldg(p.context_lens + lo);
+  if (s0 < 0 || s1 < s0 || s1 > p.num_rows || L < s1 - s0 || L > p.max_ctx) {
+    *bad = true;
+    return false;
+  }
+  const int nt = s1 - s0;
+  const int i = slot - (s0 / pair + lo);
+  const int npairs = (nt + pair - 1) / pair;
+  if (i < 0 || i >= npairs) return false;
+  const int at = (npairs - 1 - i) * pair;
+  un.b = lo;
+  un.L = L;
+  un.row0 = s0 + at;
+  un.ntok = min(pair, nt - at);
+  un.pos0 = L - nt + at;
+  const int a = p.window > 0 ? max(0, un.pos0 - p.window + 1) / kPromptTile : 0;
+  const int e = (un.pos0 + un.ntok - 1) / kPromptTile + 1;
+  un.parts = (e - a + p.split - 1) / p.split;
+  if (un.part >= un.parts) return false;
+  un.t0 = a + un.part * p.split;
+  un.t1 = min(e, un.t0 + p.split);
+  un.nonfinite = 0;
+  return true;
+}
+
+// Tokens, first position and K/V tiles [a, e) of tile s of the pair.
+struct PromptSub {
+  int n, first, a, e;
+};
+__device__ __forceinline__ PromptSub prompt_sub(const PromptParams& p, const PromptUnit& un,
+                                                int s) {
+  PromptSub r;
+  r.n = min(p.sub_tokens, un.ntok - s * p.sub_tokens);
+  r.first = un.pos0 + s * p.sub_tokens;
+  r.a = un.t0;
+  if (p.window > 0) r.a = max(r.a, max(0, r.first - p.window + 1) / kPromptTile);
+  r.e = r.n > 0 ? min(un.t1, (r.first + r.n - 1) / kPromptTile + 1) : r.a;
+  r.e = max(r.e, r.a);
+  return r;
+}
+
+// Whether some query token of [first, last] does not see every key of tile t.
+__device__ __forceinline__ bool prompt_masked(const PromptParams& p, int t, int first, int last) {
+  return t * kPromptTile + kPromptTile - 1 > first ||
+         (p.window > 0 && t * kPromptTile <= last - p.window);
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Bits 15 and 31: the low, the high bf16 of the word is infinite or NaN.
+__device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  const uint32_t bad = nonfinite_bf16x2(w);
+  return w & ~((bad >> 15) * 0xFFFFu);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// tcgen05.wait::ld, with the loaded registers tied behind it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_regs(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// A V element for the rows that see it, from the pool.
+template <int D, bool KV8>
+__device__ __forceinline__ float prompt_value(const PromptParams& p, const PromptUnit& un, int j,
+                                              int d) {
+  const int id = __ldg(p.block_tables + static_cast<size_t>(un.b) * p.mbs + j / kBlockSize);
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) return 0.f;
+  const size_t page = static_cast<size_t>(id) * p.Hkv + un.head;
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(
+      p.v_pool)[(page * kBlockSize + j % kBlockSize) * D + d]);
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv, const PromptParams p, int num_units) {
+  using Gm = PromptGeo<D, KV8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  auto& ms = *reinterpret_cast<PromptMisc<D, KV8>*>(smem + Gm::kMiscOff);
+  static_assert(sizeof(PromptMisc<D, KV8>) <= Gm::kMiscBytes, "misc area");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned long long limit = p.timeout_ns;
+
+  // ------------------------------------------------------------------ setup
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Gm::kStages; ++i) {
+      mbar_init(&ms.full[i], 1);
+      mbar_init(&ms.empty[i], 1);
+    }
+    mbar_init(&ms.border, 1);
+    mbar_init(&ms.checked, Gm::kAux);
+    mbar_init(&ms.q_full, 1);
+    mbar_init(&ms.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_full[i], 4);
+      mbar_init(&ms.o_full[i], 1);
+      mbar_init(&ms.o_free[i], 4);
+      mbar_init(&ms.unit_full[i], 1);
+      mbar_init(&ms.unit_empty[i], 1 + Gm::kSoftmaxWarps + Gm::kAux);
+      mbar_init(&ms.unit_checked[i], Gm::kAux);
+    }
+    mbar_init(&ms.fin, 1);
+    fence_barrier_init();
+  }
+  if (warp == Gm::kSoftmaxWarps + 1) tc::tmem_alloc(&ms.tmem_base, Gm::kTmemCols);
+  // rows of the Q tiles that hold no query row stay zero
+  for (int i = threadIdx.x; i < 2 * Gm::kTileBytes / 16; i += Gm::kThreads)
+    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ms.tmem_base;
+  grid_launch_dependents();
+
+  if (warp >= Gm::kSoftmaxWarps) {
+    regs_fewer<Gm::kOtherRegs>();
+    if (warp == Gm::kSoftmaxWarps) {
+      // -------------------------------------------------------------- loads
+      if (lane == 0) {
+        tma_prefetch_map(&tmq);
+        tma_prefetch_map(&tmk);
+        tma_prefetch_map(&tmv);
+      }
+      bool aborted = false;
+      int item = 0, ui = 0, u = blockIdx.x;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!aborted && !mbar_wait(bar, parity, limit)) aborted = true;
+        aborted = __any_sync(0xffffffffu, aborted);
+      };
+      while (true) {
+        PromptUnit un;
+        un.b = -1;
+        for (; u < num_units; u += gridDim.x) {
+          bool bad;
+          if (prompt_unit(p, u, un, &bad)) break;
+          if (bad && lane == 0) atomicOr(&g_pa_err, kErrBounds);
+          un.b = -1;
+        }
+        u += gridDim.x;
+        wait(&ms.unit_empty[ui & 1], (static_cast<uint32_t>(ui >> 1) & 1u) ^ 1u);
+        if (aborted) break;
+        if (lane == 0) {
+          ms.unit[ui & 1] = un;
+          mbar_arrive(&ms.unit_full[ui & 1]);
+        }
+        if (un.b < 0) break;
+        wait(&ms.q_empty, (static_cast<uint32_t>(ui) & 1u) ^ 1u);
+        if (aborted) break;
+        if (lane == 0) {
+          const int subs = un.ntok > p.sub_tokens ? 2 : 1;
+          mbar_arrive_expect_tx(&ms.q_full, static_cast<uint32_t>(subs * Gm::kHalves *
+                                                                  p.sub_tokens * p.G * 128));
+          for (int s = 0; s < subs; ++s)
+            for (int h = 0; h < Gm::kHalves; ++h)
+              tma_load_4d(smem + s * Gm::kTileBytes + h * Gm::kHalfBytes, &tmq, &ms.q_full, h * 64,
+                          0, un.head, un.row0 + s * p.sub_tokens);
+        }
+        // ids of 32 pages (four tiles) in lane order, one batch read ahead; pages behind the
+        // context's end and ids outside the pool become a row past the pool, which TMA fills
+        // with zeros
+        const int32_t* table = p.block_tables + static_cast<size_t>(un.b) * p.mbs;
+        const int npages = (un.L + kBlockSize - 1) / kBlockSize;
+        const int first = un.t0 * Gm::kPages;
+        auto page_id = [&](int i) {
+          int id = p.num_blocks;
+          if (i < npages) {
+            id = __ldg(table + i);
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
+              if (i < un.t1 * Gm::kPages) atomicOr(&g_pa_err, kErrBounds);
+              id = p.num_blocks;
+            }
+          }
+          return id;
+        };
+        int ids = page_id(first + lane), ids_next = page_id(first + 32 + lane);
+        for (int t = un.t0; t < un.t1 && !aborted; ++t) {
+          const int at = (t - un.t0) * Gm::kPages & 31;
+          if (t > un.t0 && at == 0) {
+            ids = ids_next;
+            ids_next = page_id(t * Gm::kPages + 32 + lane);
+          }
+          const int box = lane & (Gm::kPages * Gm::kHalves - 1);
+          const int pg = box / Gm::kHalves, h = box % Gm::kHalves;
+          const int id = __shfl_sync(0xffffffffu, ids, at + pg);
+          const int row = id == p.num_blocks ? p.num_blocks * p.Hkv * kBlockSize
+                                             : (id * p.Hkv + un.head) * kBlockSize;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++item) {
+            const int st = item % Gm::kStages;
+            wait(&ms.empty[st], (static_cast<uint32_t>(item / Gm::kStages) & 1u) ^ 1u);
+            if (aborted) break;
+            if (lane == 0) mbar_arrive_expect_tx(&ms.full[st], Gm::kTileBytes);
+            __syncwarp();
+            if (lane < Gm::kPages * Gm::kHalves)
+              tma_load_2d(smem + Gm::kRingOff + st * Gm::kTileBytes + h * Gm::kHalfBytes +
+                              pg * kBlockSize * 128,
+                          kv ? &tmv : &tmk, &ms.full[st], h * 64, row);
+          }
+        }
+        ++ui;
+        if (aborted) break;
+      }
+      // no copy may still be landing when the CTA ends
+      if (lane == 0)
+        for (int i = max(0, item - Gm::kStages); i < item; ++i)
+          mbar_wait(&ms.full[i % Gm::kStages], static_cast<uint32_t>(i / Gm::kStages) & 1u, limit);
+      if (lane == 0 && ui > 0)
+        mbar_wait(&ms.q_full, static_cast<uint32_t>(ui - 1) & 1u, limit);
+      __syncwarp();
+    } else if (warp == Gm::kSoftmaxWarps + 1) {
+      // -------------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, true>();
+        constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, true, true>();
+        const uint32_t ring = smem_u32(smem + Gm::kRingOff), qsm = smem_u32(smem);
+        bool ok = true;
+        int item0 = 0;
+        uint32_t n_p[2] = {0, 0}, n_u[2] = {0, 0};     // P tiles taken, units of each tile begun
+        uint32_t n_checked = 0;                        // tiles at the mask's border
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, limit)) ok = false;
+        };
+        for (int ui = 0; ok; ++ui) {
+          wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+          if (!ok) break;
+          const PromptUnit un = ms.unit[ui & 1];
+          mbar_arrive(&ms.unit_empty[ui & 1]);
+          if (un.b < 0) break;
+          const PromptSub sub[2] = {prompt_sub(p, un, 0), prompt_sub(p, un, 1)};
+          const int last = un.pos0 + un.ntok - 1;
+          auto scores = [&](int s, int st) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * Gm::kHalfBytes + (k & 3) * 32;
+              tc::mma_f16_ss(tmem + s * kPromptTile,
+                             tc::smem_desc(qsm + s * Gm::kTileBytes + off, 16, 1024),
+                             tc::smem_desc(ring + st * Gm::kTileBytes + off, 16, 1024), kIdS,
+                             k > 0 ? 1u : 0u);
+            }
+            tc::commit(&ms.s_full[s]);
+          };
+          wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
+          {
+            const int st = item0 % Gm::kStages;
+            wait(&ms.full[st], static_cast<uint32_t>(item0 / Gm::kStages) & 1u);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              if (sub[s].a <= un.t0 && un.t0 < sub[s].e) scores(s, st);
+            tc::commit(&ms.empty[st]);
+            if (un.t0 + 1 == un.t1) tc::commit(&ms.q_empty);
+          }
+          for (int t = un.t0; t < un.t1 && ok; ++t) {
+            const int vi = item0 + 2 * (t - un.t0) + 1, ki = vi + 1;
+            const int vst = vi % Gm::kStages, kst = ki % Gm::kStages;
+            const bool border = prompt_masked(p, t, un.pos0, last);
+            bool v_here = false, k_here = false;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (sub[s].a <= t && t < sub[s].e) {
+                if (!v_here) {
+                  wait(&ms.full[vst], static_cast<uint32_t>(vi / Gm::kStages) & 1u);
+                  if (border) mbar_arrive(&ms.border);
+                }
+                if (t == sub[s].a) wait(&ms.o_free[s], (n_u[s]++ & 1u) ^ 1u);
+                wait(&ms.p_full[s], n_p[s]++ & 1u);
+                if (border && !v_here) wait(&ms.checked, n_checked++ & 1u);
+                v_here = true;
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < kPromptTile / 16; ++k)
+                  tc::mma_f16_ts(tmem + Gm::kO + s * D, tmem + s * kPromptTile + k * 8,
+                                 tc::smem_desc(ring + vst * Gm::kTileBytes + k * 2048,
+                                               Gm::kHalfBytes, 1024),
+                                 kIdO, t > sub[s].a || k > 0 ? 1u : 0u);
+                if (t + 1 == sub[s].e) tc::commit(&ms.o_full[s]);
+              }
+              if (sub[s].a <= t + 1 && t + 1 < sub[s].e) {
+                if (!k_here) {
+                  wait(&ms.full[kst], static_cast<uint32_t>(ki / Gm::kStages) & 1u);
+                  k_here = true;
+                }
+                if (!ok) break;
+                tc::fence_after_sync();
+                scores(s, kst);
+              }
+            }
+            if (!ok) break;
+            tc::commit(&ms.empty[vst]);
+            if (t + 1 < un.t1) tc::commit(&ms.empty[kst]);
+            if (t + 2 == un.t1) tc::commit(&ms.q_empty);
+          }
+          item0 += 2 * (un.t1 - un.t0);
+        }
+        // every MMA has completed before the CTA gives its tensor memory back
+        tc::commit(&ms.fin);
+        mbar_wait(&ms.fin, 0, limit);
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- borders of the mask
+      const int aux = warp - Gm::kSoftmaxWarps - 2;
+      bool ok = true;
+      int item0 = 0;
+      uint32_t n_border = 0;
+      for (int ui = 0; ok; ++ui) {
+        ok = mbar_wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u, limit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const PromptUnit un = ms.unit[ui & 1];
+        if (un.b < 0) break;
+        const int last = un.pos0 + un.ntok - 1;
+        for (int t = un.t0; t < un.t1; ++t) {
+          if (!prompt_masked(p, t, un.pos0, last)) continue;
+          const int vi = item0 + 2 * (t - un.t0) + 1, st = vi % Gm::kStages;
+          ok = mbar_wait(&ms.border, n_border++ & 1u, limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // four keys' halves of 128 bytes at a time; the two warps take every other four
+          uint8_t* tile = smem + Gm::kRingOff + st * Gm::kTileBytes;
+          bool found = false;
+#pragma unroll 2
+          for (int k4 = aux; k4 < kPromptTile / 4; k4 += Gm::kAux) {
+            const int key = t * kPromptTile + k4 * 4 + (lane >> 3);
+            const bool dead = key >= un.L;
+            if (!__any_sync(0xffffffffu, key > un.pos0 ||
+                                             (p.window > 0 && key <= last - p.window)))
+              continue;
+#pragma unroll
+            for (int h = 0; h < Gm::kHalves; ++h) {
+              uint4* at = reinterpret_cast<uint4*>(tile + h * Gm::kHalfBytes + k4 * 512) + lane;
+              const uint4 w = *at;
+              if (dead) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
+                         nonfinite_bf16x2(w.w)) {
+                found = true;
+                *at = make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y), finite_bf16x2(w.z),
+                                 finite_bf16x2(w.w));
+              }
+            }
+          }
+          if (found) *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.checked);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ms.unit_checked[ui & 1]);
+          mbar_arrive(&ms.unit_empty[ui & 1]);
+        }
+        item0 += 2 * (un.t1 - un.t0);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    regs_more<Gm::kSoftmaxRegs>();
+    const int s = warp >> 2;
+    const int r = threadIdx.x & 127;                    // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + s * kPromptTile, to = tmem + lanes + Gm::kO + s * D;
+    const int tok = r / p.G, g = r - tok * p.G;         // of this row
+    bool ok = true;
+    uint32_t n_s = 0, n_o = 0;                          // S and O tiles taken
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !mbar_wait(bar, parity, limit)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    for (int ui = 0; ok; ++ui) {
+      wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+      if (!ok) break;
+      const PromptUnit un = ms.unit[ui & 1];
+      if (un.b < 0) break;
+      const PromptSub sub = prompt_sub(p, un, s);
+      const bool live = tok < sub.n;                    // rows past the tile's end repeat the last
+      const int pos = sub.first + min(tok, max(sub.n, 1) - 1);
+      float c = p.scale_log2;
+      if constexpr (KV8) c *= __ldg(p.k_scale + un.head);
+      float ref = -CUDART_INF_F;                        // reference, log2 units
+      float sum = 0.f;
+      for (int t = sub.a; t < sub.e; ++t) {
+        wait(&ms.s_full[s], n_s++ & 1u);
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::tmem_ld32(ts + i * 32, x[i]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait_regs(x[i]);
+        // a score's factor is applied with the reference's subtraction, in one rounding; with
+        // a factor that is not positive, or references that leave no bits behind the point,
+        // it comes first
+        float cc = c;
+        if (!(c > 0.f)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * c);
+          cc = 1.f;
+        }
+        if (prompt_masked(p, t, sub.first, sub.first + sub.n - 1)) {
+          const int hi = pos - t * kPromptTile;         // columns lo < i <= hi are visible
+          const int lo = p.window > 0 ? hi - p.window : -1;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > hi || i <= lo) x[i / 32][i % 32] = __float_as_uint(-CUDART_INF_F);
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = __uint_as_float(x[i][0]);
+#pragma unroll
+          for (int k = 1; k < 32; ++k) mx[i] = fmaxf(mx[i], __uint_as_float(x[i][k]));
+        }
+        float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cc;
+        if (__any_sync(0xffffffffu, fabsf(m) > 67108864.f && fabsf(m) < CUDART_INF_F) &&
+            cc != 1.f) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * cc);
+          cc = 1.f;
+        }
+        const bool move = m > ref + 8.f;                // the first finite score always moves it
+        if (__any_sync(0xffffffffu, move)) {
+          const float to_ref = move ? m : ref;
+          const float f = move ? hw_exp2(ref - m) : 1.f;
+          ref = to_ref;
+          sum *= f;
+          if (t > sub.a) {
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tc::tmem_ld16(to + i * 16, o);
+              tc::tmem_wait_ld();
+              tmem_wait_regs(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tc::tmem_st16(to + i * 16, o);
+            }
+          }
+        }
+        const float off = ref == -CUDART_INF_F ? 0.f : -ref;
+        const uint64_t cc2 = pack_f32x2(cc, cc), off2 = pack_f32x2(off, off);
+        uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(x[i][2 * k]),
+                                                    __uint_as_float(x[i][2 * k + 1])),
+                                         cc2, off2);
+            const float e0 = hw_exp2(__uint_as_float(static_cast<uint32_t>(y)));
+            const float e1 = hw_exp2(__uint_as_float(static_cast<uint32_t>(y >> 32)));
+            part[k & 1] = add_f32x2(part[k & 1], pack_f32x2(e0, e1));
+            w[k] = pack_bf16x2_rn(e0, e1);
+          }
+          tc::tmem_st16(ts + i * 16, w);
+        }
+        part[0] = add_f32x2(part[0], part[1]);
+        sum += __uint_as_float(static_cast<uint32_t>(part[0])) +
+               __uint_as_float(static_cast<uint32_t>(part[0] >> 32));
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_full[s]);
+      }
+      if (!ok) break;
+
+      // -------------------------------------------------------------- unit output
+      wait(&ms.unit_checked[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+      const bool special = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
+      const bool any = sub.e > sub.a;
+      if (any) wait(&ms.o_full[s], n_o++ & 1u);
+      if (!ok) break;
+      tc::fence_after_sync();
+      float vs = 1.f;
+      if constexpr (KV8) vs = __ldg(p.v_scale + un.head);
+      const float inv = any ? __frcp_rn(sum) : 0.f;
+      const size_t row =
+          static_cast<size_t>(un.row0 + s * p.sub_tokens + tok) * p.Hq + un.head * p.G + g;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        if (any) {
+          tc::tmem_ld32(to + i * 32, o);
+          tc::tmem_wait_ld();
+          tmem_wait_regs(o);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k] = any ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+        if (special && live) {
+          for (int t = sub.a; t < sub.e; ++t) {
+            if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
+            const int from = p.window > 0 ? max(t * kPromptTile, pos - p.window + 1)
+                                          : t * kPromptTile;
+            for (int j = from; j <= min(pos, t * kPromptTile + kPromptTile - 1); ++j) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float v = prompt_value<D, KV8>(p, un, j, i * 32 + k);
+                if (!(fabsf(v) < CUDART_INF_F))
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) + v);
+              }
+            }
+          }
+        }
+        if constexpr (KV8) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * vs);
+        }
+        if (live) {
+          if (un.parts == 1) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D) +
+                         i * 4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(
+                  pack_bf16x2_rn(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                  pack_bf16x2_rn(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                  pack_bf16x2_rn(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                  pack_bf16x2_rn(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+          } else {
+            const size_t at = row * p.max_parts + un.part;
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D) + i * 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            if (i == 0) p.part_ml[at] = make_float2(ref, sum);
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (any && lane == 0) mbar_arrive(&ms.o_free[s]);
+    }
+  }
+
+  // ------------------------------------------------------------------ teardown
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == Gm::kSoftmaxWarps + 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, Gm::kTmemCols);
+    tc::tmem_relinquish();
+  }
+}
+
+// ---------------------------------------------------------------- merge of partitions
+// One warp per query row of a pair of tiles whose keys were cut: partition i holds O_i
+// (normalised), the reference m_i (log2 units) and the sum l_i, and counts w_i = l_i 2^(m_i - M).
+constexpr int kPromptMergeWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kPromptMergeWarps * 32)
+    prompt_merge_kernel(const PromptParams p, int rows_per_cta) {
+  constexpr int DL = D / 32;
+  grid_dependency_wait();
+  PromptUnit un;
+  bool bad;
+  if (!prompt_unit(p, blockIdx.x, un, &bad) || un.parts == 1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = un.ntok * p.G;
+  const int end = min(rows, static_cast<int>(blockIdx.y + 1) * rows_per_cta);
+  for (int r = blockIdx.y * rows_per_cta + warp; r < end; r += kPromptMergeWarps) {
+    const size_t row =
+        static_cast<size_t>(un.row0 + r / p.G) * p.Hq + un.head * p.G + r % p.G;
+    const float2* ml = p.part_ml + row * p.max_parts;
+    float M = -CUDART_INF_F;
+    for (int i = lane; i < un.parts; i += 32) {
+      const float2 x = __ldcg(ml + i);
+      M = fmaxf(M, x.y == 0.f ? -CUDART_INF_F : x.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[DL] = {}, total = 0.f;
+    for (int i = 0; i < un.parts; ++i) {
+      const float2 x = __ldcg(ml + i);
+      if (x.y == 0.f) continue;                   // saw no key, or only scores of -inf
+      const float w = x.y * hw_exp2(x.x - M);
+      total += w;
+      const float* src = p.part_o + (row * p.max_parts + i) * D + lane * DL;
+#pragma unroll
+      for (int k = 0; k < DL; ++k) acc[k] += w * __ldcg(src + k);
+    }
+    const float inv = __frcp_rn(total);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + lane * DL;
+#pragma unroll
+    for (int k = 0; k < DL; k += 2)
+      *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2_rn(acc[k] * inv, acc[k + 1] * inv);
+  }
+}
+
+template <int D, bool KV8>
+cudaError_t launch_prompt_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PromptParams& p, cudaStream_t s) {
+  using Gm = PromptGeo<D, KV8>;
+  auto kern = prompt_kernel<D, KV8>;
+  static std::atomic<unsigned long long> configured{0ull};
+  static std::atomic<int> sm_count[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  int sms = bit ? sm_count[dev].load(std::memory_order_relaxed) : 0;
+  if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0 || sms == 0) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    // the softmax warps take their registers from what the launch holds
+    if (at.numRegs < Gm::kRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::kAlloc);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (bit) {
+      sm_count[dev].store(sms, std::memory_order_relaxed);
+      configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+  }
+  const int pairs = p.num_slots * p.Hkv, units = pairs * p.max_parts;
+  kern<<<static_cast<unsigned>(std::min(units, sms)), Gm::kThreads, Gm::kAlloc, s>>>(tq, tk, tv, p,
+                                                                                  units);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.max_parts == 1) return e;
+  const int rows_per_cta = 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs),
+                     static_cast<unsigned>((2 * p.sub_tokens * p.G + rows_per_cta - 1) /
+                                           rows_per_cta), 1);
+  cfg.blockDim = dim3(kPromptMergeWarps * 32, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_merge_kernel<D>, p, rows_per_cta);
+}
+
+}  // namespace pa
