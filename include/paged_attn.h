@@ -78,7 +78,8 @@ typedef enum {
   PA_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed                */
   PA_ERR_BOUNDS = 5,        /* device saw a block id / slot / length out of range  */
   PA_ERR_TIMEOUT = 6,       /* device pipeline wait exceeded its limit             */
-  PA_ERR_OUT_OF_BLOCKS = 7  /* block manager: no free physical block left          */
+  PA_ERR_OUT_OF_BLOCKS = 7  /* no free physical block left (block manager, or seen on
+                               the device by pa_extend_sequences)                  */
 } pa_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -652,6 +653,80 @@ pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, con
 size_t pa_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
                                 int max_context_len, int head_dim, int block_size,
                                 int partition_size, int window_size);
+
+/*
+ * pa_extend_sequences — block tables and slots on the device: every sequence of
+ * the batch takes in new_lens[b] >= 0 tokens.  State, all of it updated in place
+ * and all device memory, as the block manager (pa_bm_*) keeps it on the host:
+ *
+ *   block_tables  [num_seqs, max_blocks_per_seq] int32  entries behind a
+ *                 sequence's blocks are neither read nor changed
+ *   context_lens  [num_seqs]                     int32  tokens so far; then with
+ *                 the new ones
+ *   ref_counts    [num_blocks]                   int32  tables that list a block;
+ *                 0 = free
+ *
+ * A new block is the lowest-numbered free one; the sequences are served in batch
+ * order, each as by pa_bm_append_slot once per token: a partly filled last block
+ * that another sequence still lists is replaced by a fresh one, and the copy to
+ * make before anything is written is reported.  Outputs:
+ *
+ *   query_starts  [num_seqs + 1] int32  prefix sums of new_lens: the packed rows of
+ *                 every sequence's new tokens (pa_prompt_attention)
+ *   slot_mapping  [num_tokens]   int64  slot of each packed row, -1 behind the last
+ *                 (pa_reshape_and_cache skips those)
+ *   positions     [num_tokens]   int32  its position in its sequence, or -1
+ *   block_copies  [num_seqs, 2]  int32  (source, destination) for pa_copy_blocks,
+ *                 (0, 0) for a sequence without a copy, which copies nothing
+ *
+ * num_tokens is the host's bound on the sum of new_lens.  A call that cannot be
+ * met (too few free blocks: PA_ERR_OUT_OF_BLOCKS on the device; more tokens than
+ * num_tokens or than a table holds, a negative length, a last block outside the
+ * pool: PA_ERR_BOUNDS) changes no state, and its outputs are those of an empty
+ * batch: starts 0, slots and positions -1, copies (0, 0).  num_seqs is at most
+ * 16384; a sequence may be listed once.
+ */
+pa_status pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                              int32_t* ref_counts, const int32_t* new_lens, int num_seqs,
+                              int num_tokens, int num_blocks, int block_size,
+                              int32_t* query_starts, int64_t* slot_mapping, int32_t* positions,
+                              int32_t* block_copies, pa_stream_t stream);
+
+/*
+ * pa_truncate_sequences — sequences cut back to new_context_lens[b] tokens on the
+ * device (rejected drafts, entries evicted, 0 for a finished sequence): the
+ * blocks behind them lose one owner each (free at 0) and their table entries
+ * become -1, as by pa_bm_truncate.  A length below 0 or above context_lens[b]
+ * sets PA_ERR_BOUNDS on the device and leaves that sequence as it is; so does an
+ * entry outside the pool or without an owner, for that entry.
+ */
+pa_status pa_truncate_sequences(int32_t* block_tables, int max_blocks_per_seq,
+                                int32_t* context_lens, int32_t* ref_counts,
+                                const int32_t* new_context_lens, int num_seqs, int num_blocks,
+                                int block_size, pa_stream_t stream);
+
+/*
+ * pa_token_logprobs — for every row of logits: the log probability of a given
+ * token, the entropy of the row's distribution, and the num_top most probable
+ * tokens (ties: the lower index first) with their log probabilities.  With p the
+ * softmax of the row, logprob = ln p[token], entropy = - sum p ln p in nats.
+ *
+ *   logits        [num_rows, row_stride]  float32, bf16 or fp16 (PA_LOGITS_*); the
+ *                 first vocab_size of each row count; rows need no alignment
+ *   tokens        [num_rows]  int32; a negative one stands for none (logprob 0), one
+ *                 >= vocab_size sets PA_ERR_BOUNDS on the device (logprob NaN)
+ *   logprobs, entropy             [num_rows]           float32
+ *   top_logprobs, top_tokens      [num_rows, num_top]  float32, int32
+ *
+ * Logits of -inf have probability 0.  A row with a NaN or +inf, or of nothing but
+ * -inf, has NaN results, and any of its tokens as alternatives.  Sums are fp32.
+ * Requirements: vocab_size <= 2^19, num_top <= 32 and <= vocab_size.
+ */
+enum { PA_LOGITS_FP32 = 0, PA_LOGITS_BF16 = 1, PA_LOGITS_FP16 = 2 };
+pa_status pa_token_logprobs(float* logprobs, float* entropy, float* top_logprobs,
+                            int32_t* top_tokens, const void* logits, long long row_stride,
+                            int dtype, const int32_t* tokens, int num_rows, int vocab_size,
+                            int num_top, pa_stream_t stream);
 
 /*
  * pa_spec_accept — speculative decoding, after pa_verify: which of the K draft

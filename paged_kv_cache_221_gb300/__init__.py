@@ -52,6 +52,7 @@ __all__ = ["reshape_and_cache", "decode", "verify", "decode_shared_prefix", "wor
            "gather_cache_int4", "attention_int4", "int4_workspace_size", "int4_page_bytes",
            "accumulate_weights", "accumulate_workspace_size", "evict_tokens",
            "evict_workspace_size", "prompt_attention", "prompt_workspace_size",
+           "extend_sequences", "truncate_sequences", "token_logprobs",
            "PagedAttnError", "STATUS_NAMES"]
 
 
@@ -816,6 +817,99 @@ def prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
           block_tables.data_ptr(), mbs, context_lens.data_ptr(), mcl, query_starts.data_ptr(), N, B,
           NB, Hq, Hkv, D, BS, D ** -0.5 if scale is None else float(scale), partition_size, ws, wsb)
     return out
+
+
+def _batch_state(block_tables, context_lens, ref_counts):
+    if not isinstance(block_tables, _Tensor) or not block_tables.is_cuda:
+        _need("block_tables", block_tables, _i32, 2)
+    dev = block_tables.device
+    _want("block_tables", block_tables, _i32, 2, dev)
+    _want("context_lens", context_lens, _i32, 1, dev)
+    _want("ref_counts", ref_counts, _i32, 1, dev)
+    B, mbs = block_tables.shape
+    if context_lens.numel() != B:
+        raise ValueError("inconsistent shapes")
+    return dev, B, mbs, ref_counts.numel()
+
+
+def extend_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     ref_counts: torch.Tensor, new_lens: torch.Tensor, num_tokens: int):
+    """Take ``new_lens`` new tokens (int32 [B]) into every sequence, on the device.
+
+    ``block_tables`` [B, max_blocks], ``context_lens`` [B] and ``ref_counts`` [num_blocks] (all
+    int32; a block of count 0 is free) are updated in place, in the block manager's order: the
+    lowest free block each time, a shared and partly filled last block replaced by a copy.
+    Returns ``(query_starts [B + 1] int32, slot_mapping [num_tokens] int64, positions
+    [num_tokens] int32, block_copies [B, 2] int32)``: the inputs of ``prompt_attention``,
+    ``reshape_and_cache`` (rows behind the last token have slot -1) and ``copy_blocks`` ((0, 0)
+    where there is nothing to copy).  ``num_tokens`` is a bound on the sum of ``new_lens``.  A
+    call that cannot be met changes nothing, returns an empty batch and sets the device error."""
+    dev, B, mbs, NB = _batch_state(block_tables, context_lens, ref_counts)
+    _want("new_lens", new_lens, _i32, 1, dev)
+    if new_lens.numel() != B:
+        raise ValueError("inconsistent shapes")
+    num_tokens = int(num_tokens)
+    if num_tokens < 0:
+        raise ValueError("num_tokens must not be negative")
+    starts = torch.empty(B + 1, dtype=_i32, device=dev)
+    slots = torch.empty(num_tokens, dtype=_i64, device=dev)
+    positions = torch.empty(num_tokens, dtype=_i32, device=dev)
+    copies = torch.empty((B, 2), dtype=_i32, device=dev)
+    _call("pa_extend_sequences", dev, block_tables.data_ptr(), mbs, context_lens.data_ptr(),
+          ref_counts.data_ptr(), new_lens.data_ptr(), B, num_tokens, NB, 16, starts.data_ptr(),
+          slots.data_ptr(), positions.data_ptr(), copies.data_ptr())
+    return starts, slots, positions, copies
+
+
+def truncate_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor,
+                       ref_counts: torch.Tensor, new_context_lens: torch.Tensor) -> None:
+    """Cut every sequence back to ``new_context_lens`` tokens (int32 [B], at most its length; 0
+    frees it) in the state of ``extend_sequences``: blocks behind them lose an owner, their table
+    entries become -1."""
+    dev, B, mbs, NB = _batch_state(block_tables, context_lens, ref_counts)
+    _want("new_context_lens", new_context_lens, _i32, 1, dev)
+    if new_context_lens.numel() != B:
+        raise ValueError("inconsistent shapes")
+    _call("pa_truncate_sequences", dev, block_tables.data_ptr(), mbs, context_lens.data_ptr(),
+          ref_counts.data_ptr(), new_context_lens.data_ptr(), B, NB, 16)
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, num_top: int = 0):
+    """``(logprobs [N], entropy [N], top_logprobs [N, num_top], top_tokens [N, num_top])`` of
+    logits [N, V] (float32, bf16 or fp16; rows may be strided) for the given tokens (int32 [N];
+    negative: none).  Results are float32 in nats, the tokens int32; of equally probable
+    alternatives the lower index comes first; ``num_top`` is at most 32."""
+    if not isinstance(logits, _Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    dtype = _LOGITS.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have 2 dims, got shape {tuple(logits.shape)}")
+    N, V = logits.shape
+    stride = logits.stride(0) if N > 1 else V
+    if V > 1 and logits.stride(1) != 1 or stride < V:
+        raise ValueError("the logits of a row must be contiguous, and rows must not overlap")
+    dev = logits.device
+    _want("tokens", tokens, _i32, 1, dev)
+    if tokens.numel() != N:
+        raise ValueError("inconsistent shapes")
+    num_top = int(num_top)
+    if not 0 <= num_top <= min(32, V):
+        raise ValueError("num_top must be between 0 and 32 and at most the vocabulary")
+    logprobs = torch.empty(N, dtype=_f32, device=dev)
+    entropy = torch.empty(N, dtype=_f32, device=dev)
+    top_logprobs = torch.empty((N, num_top), dtype=_f32, device=dev)
+    top_tokens = torch.empty((N, num_top), dtype=_i32, device=dev)
+    _call("pa_token_logprobs", dev, logprobs.data_ptr(), entropy.data_ptr(),
+          top_logprobs.data_ptr(), top_tokens.data_ptr(), logits.data_ptr(), stride, dtype,
+          tokens.data_ptr(), N, V, num_top)
+    return logprobs, entropy, top_logprobs, top_tokens
 
 
 def get_device_error(device=None) -> int:

@@ -88,6 +88,10 @@ SIGNATURES = {
     "pa_prompt_attention": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i,
                                  _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "pa_prompt_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "pa_extend_sequences": (_i, [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "pa_truncate_sequences": (_i, [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "pa_token_logprobs": (_i, [_vp, _vp, _vp, _vp, _vp, ctypes.c_longlong, _i, _vp, _i, _i, _i,
+                               _vp]),
     "pa_bm_truncate": (_i, [_vp, _i, _i]),
     "pa_bm_create": (_i, [_i, _i, ctypes.POINTER(_vp)]),
     "pa_bm_destroy": (None, [_vp]),

@@ -31,7 +31,8 @@ SOURCES = ["pa_api.cpp", "pa_misc.cu", "attn_d64.cu", "attn_d128.cu", "group_d64
            "pa_spec.cu", "pa_no_alloc.cu", "attn_tc_d128.cu", "stream_d64.cu", "stream_d128.cu",
            "pa_runner.cpp", "pa_block_manager.cpp", "attn4_d64.cu", "attn4_d128.cu",
            "pa_cache4.cu", "observe_bf16.cu", "observe_fp8.cu", "observe_int4.cu",
-           "pa_evict.cu", "prompt_d64.cu", "prompt_d128.cu"]
+           "pa_evict.cu", "prompt_d64.cu", "prompt_d128.cu", "pa_step.cu",
+           "pa_score.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
          "-I" + CSRC]

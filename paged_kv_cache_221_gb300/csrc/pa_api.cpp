@@ -894,6 +894,86 @@ pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, con
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+pa_status pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                              int32_t* ref_counts, const int32_t* new_lens, int num_seqs,
+                              int num_tokens, int num_blocks, int block_size,
+                              int32_t* query_starts, int64_t* slot_mapping, int32_t* positions,
+                              int32_t* block_copies, pa_stream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      !query_starts)
+    return PA_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || num_seqs > kMaxStepSeqs) return PA_ERR_UNSUPPORTED;
+  // positions and counts of blocks are 32-bit
+  if (max_blocks_per_seq > (1 << 26) || num_blocks > (1 << 30) || num_tokens > (1 << 30))
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 0 && (!block_tables || !context_lens || !ref_counts || !new_lens ||
+                       !block_copies))
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID_ARG;
+  StepParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.ref_counts = ref_counts;
+  p.new_lens = new_lens;
+  p.query_starts = query_starts;
+  p.slots = slot_mapping;
+  p.positions = positions;
+  p.copies = block_copies;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_blocks = num_seqs > 0 ? num_blocks : 0;   // without sequences nothing is looked at
+  p.mbs = max_blocks_per_seq;
+  return launch_extend(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                 : PA_ERR_CUDA;
+}
+
+pa_status pa_truncate_sequences(int32_t* block_tables, int max_blocks_per_seq,
+                                int32_t* context_lens, int32_t* ref_counts,
+                                const int32_t* new_context_lens, int num_seqs, int num_blocks,
+                                int block_size, pa_stream_t stream) {
+  if (num_seqs < 0 || num_blocks < 1 || max_blocks_per_seq < 1) return PA_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || max_blocks_per_seq > (1 << 26)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!block_tables || !context_lens || !ref_counts || !new_context_lens ||
+      new_context_lens == context_lens)
+    return PA_ERR_INVALID_ARG;
+  return launch_truncate(block_tables, context_lens, ref_counts, new_context_lens, num_seqs,
+                         max_blocks_per_seq, num_blocks,
+                         reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_token_logprobs(float* logprobs, float* entropy, float* top_logprobs,
+                            int32_t* top_tokens, const void* logits, long long row_stride,
+                            int dtype, const int32_t* tokens, int num_rows, int vocab_size,
+                            int num_top, pa_stream_t stream) {
+  if (num_rows < 0 || vocab_size < 1 || num_top < 0 || num_top > vocab_size ||
+      row_stride < vocab_size || dtype < PA_LOGITS_FP32 || dtype > PA_LOGITS_FP16)
+    return PA_ERR_INVALID_ARG;
+  if (vocab_size > kMaxSpecVocab || num_top > kMaxScoreTop || num_rows > (1 << 27))
+    return PA_ERR_UNSUPPORTED;
+  if (num_rows == 0) return PA_OK;
+  if (!logprobs || !entropy || !logits || !tokens || (num_top > 0 && (!top_logprobs || !top_tokens)))
+    return PA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) & (dtype == PA_LOGITS_FP32 ? 3u : 1u))
+    return PA_ERR_INVALID_ARG;
+  ScoreParams p{};
+  p.logits = logits;
+  p.tokens = tokens;
+  p.logprobs = logprobs;
+  p.entropy = entropy;
+  p.top_logprobs = top_logprobs;
+  p.top_tokens = top_tokens;
+  p.stride = row_stride;
+  p.num_rows = num_rows;
+  p.vocab = vocab_size;
+  p.top = num_top;
+  return launch_score(p, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 pa_status pa_spec_accept(const float* target_probs, const float* draft_probs,
                          const int32_t* draft_tokens, const uint32_t* accept_uniforms,
                          const uint32_t* sample_uniforms, int num_seqs, int num_drafts,
@@ -1229,10 +1309,12 @@ pa_status pa_get_device_error(pa_stream_t stream) {
       take_error_cache4(&bits) != cudaSuccess || take_error_observe_bf16(&bits) != cudaSuccess ||
       take_error_observe_fp8(&bits) != cudaSuccess ||
       take_error_observe_int4(&bits) != cudaSuccess || take_error_evict(&bits) != cudaSuccess ||
-      take_error_prompt_d64(&bits) != cudaSuccess || take_error_prompt_d128(&bits) != cudaSuccess)
+      take_error_prompt_d64(&bits) != cudaSuccess || take_error_prompt_d128(&bits) != cudaSuccess ||
+      take_error_step(&bits) != cudaSuccess || take_error_score(&bits) != cudaSuccess)
     return PA_ERR_CUDA;
   if (bits & kErrTimeout) return PA_ERR_TIMEOUT;
   if (bits & kErrBounds) return PA_ERR_BOUNDS;
+  if (bits & kErrBlocks) return PA_ERR_OUT_OF_BLOCKS;
   return PA_OK;
 }
 

@@ -147,6 +147,35 @@ struct PromptParams {
 };
 constexpr int kPromptTile = 128;  // rows of a query tile, and keys of a K/V tile
 
+// Block tables of a batch extended on the device (pa_step.cu).
+enum : unsigned { kErrBlocks = 4u };  // of the error word: too few free blocks
+struct StepParams {
+  int32_t* block_tables;          // [B, mbs]
+  int32_t* context_lens;          // [B]
+  int32_t* ref_counts;            // [num_blocks]
+  const int32_t* new_lens;        // [B]
+  int32_t* query_starts;          // [B + 1]
+  int64_t* slots;                 // [num_tokens]
+  int32_t* positions;             // [num_tokens]
+  int32_t* copies;                // [B, 2]
+  int num_seqs, num_tokens, num_blocks, mbs;
+  bool slots_here;                // in the same launch
+};
+constexpr int kMaxStepSeqs = 16384;  // three integers of each in shared memory
+
+// Log probabilities (pa_score.cu).
+struct ScoreParams {
+  const void* logits;             // [num_rows, stride], vocab of them used
+  const int32_t* tokens;          // [num_rows]
+  float* logprobs;                // [num_rows]
+  float* entropy;                 // [num_rows]
+  float* top_logprobs;            // [num_rows, top]
+  int32_t* top_tokens;            // [num_rows, top]
+  long long stride;
+  int num_rows, vocab, top;
+};
+constexpr int kMaxScoreTop = 32;
+
 // Eviction: the first launch selects and pairs movers with gaps, the second moves.
 struct EvictParams {
   void* k_pool;
@@ -257,6 +286,12 @@ cudaError_t launch_prompt_d64(const CUtensorMap& tq, const CUtensorMap& tk, cons
 cudaError_t launch_prompt_d128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PromptParams& p, bool kv8, cudaStream_t s);
 
+cudaError_t launch_extend(const StepParams& p, cudaStream_t s);
+cudaError_t launch_truncate(int32_t* tables, int32_t* lens, int32_t* refs, const int32_t* keep,
+                            int num_seqs, int mbs, int num_blocks, cudaStream_t s);
+// dtype: 0 float32, 1 bf16, 2 fp16.
+cudaError_t launch_score(const ScoreParams& p, int dtype, cudaStream_t s);
+
 // Read and clear the device error word of each translation unit (synchronous).
 cudaError_t take_error_attn_d64(unsigned* bits);
 cudaError_t take_error_attn_d128(unsigned* bits);
@@ -280,5 +315,7 @@ cudaError_t take_error_observe_int4(unsigned* bits);
 cudaError_t take_error_evict(unsigned* bits);
 cudaError_t take_error_prompt_d64(unsigned* bits);
 cudaError_t take_error_prompt_d128(unsigned* bits);
+cudaError_t take_error_step(unsigned* bits);
+cudaError_t take_error_score(unsigned* bits);
 
 }  // namespace pa
