@@ -844,8 +844,8 @@ pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, con
   const PromptPlan plan =
       prompt_plan(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_context_len, head_dim,
                   partition_size, window, workspace != nullptr);
-  // the units of work are counted in 32 bits, and one row of the merge's grid in 16
-  if (plan.units >= (1ll << 31) - 65536 || plan.max_parts > 65535) return PA_ERR_UNSUPPORTED;
+  // the units of work are counted in 32 bits
+  if (plan.units > (1ll << 30)) return PA_ERR_UNSUPPORTED;
   if (plan.bytes > 0) {
     if (!workspace || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;

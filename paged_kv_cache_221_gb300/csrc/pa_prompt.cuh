@@ -28,8 +28,15 @@
 //                   see (0 * inf would reach it); the rows that see those keys get them
 //                   added at the end.
 //
+// FP8 pages.  The products take f16, of which every E4M3 value is one: warps 10 and 11 widen
+// each tile from where TMA left it into the ring that the MMAs read (K rows as they are; V
+// pages are stored by head dim, so that tile becomes a K-major operand), and the query rows in
+// place, each times a power of two that puts its largest element at 2^7 .. 2^8 (a bf16 value
+// may lie outside f16's range) and that the row's scores take back.  Weights become f16, times
+// 2^7, which moves what f16 cannot hold from 2^-25 to 2^-32 of the row's largest weight.
+//
 // Weights are rounded to bf16 (2^-8 of each at most) for the second product, as are the
-// values they meet; statistics and accumulators are fp32.
+// values they meet (f16 for FP8 pages: 2^-11); statistics and accumulators are fp32.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -52,12 +59,16 @@ struct PromptGeo {
   static constexpr int kHalves = D / 64;                 // 64-dim halves of a row (128 bytes)
   static constexpr int kHalfBytes = kPromptTile * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
-  static constexpr int kStages = 5;                      // K and V tiles in flight
+  static constexpr int kStages = KV8 ? 3 : 5;            // K and V tiles ready or in flight
+  static constexpr int kRawStages = KV8 ? 4 : 0;         // FP8 tiles in flight
+  static constexpr int kRawBytes = kPromptTile * D;
+  static constexpr int kShift = KV8 ? 7 : 0;             // weights carry 2^kShift
   static constexpr int kPages = kPromptTile / kBlockSize;
   // shared memory, from a 1024-byte aligned base
   static constexpr int kRingOff = 2 * kTileBytes;        // behind the two Q tiles
-  static constexpr int kMiscOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kMiscBytes = 1024;
+  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kMiscOff = kRawOff + kRawStages * kRawBytes;
+  static constexpr int kMiscBytes = KV8 ? 1024 : 512;
   static constexpr int kAlloc = kMiscOff + kMiscBytes + 1024;
   // tensor memory columns
   static constexpr uint32_t kTmemCols = 512;
@@ -86,13 +97,17 @@ struct PromptMisc {
   using Gm = PromptGeo<D, KV8>;
   uint64_t full[Gm::kStages];
   uint64_t empty[Gm::kStages];
+  uint64_t raw_full[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
+  uint64_t raw_empty[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
   uint64_t border, checked;            // a V tile at the mask's border is there, is looked at
   uint64_t q_full, q_empty;
+  uint64_t q_wide[2];                  // by record: the query rows are f16
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
   uint64_t unit_full[2], unit_empty[2], unit_checked[2]; // by record
   uint64_t fin;
   PromptUnit unit[2];
   uint32_t tmem_base;
+  int8_t q_exp[KV8 ? 2 : 1][2][KV8 ? kPromptTile : 1];   // by record, tile, row: of the factor
 };
 
 // The unit with index u (kv heads fastest, then pairs of tiles, then partitions), found by a
@@ -216,8 +231,116 @@ __device__ __forceinline__ float prompt_value(const PromptParams& p, const Promp
   const int id = __ldg(p.block_tables + static_cast<size_t>(un.b) * p.mbs + j / kBlockSize);
   if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) return 0.f;
   const size_t page = static_cast<size_t>(id) * p.Hkv + un.head;
+  if constexpr (KV8) {
+    const uint32_t c = static_cast<const uint8_t*>(p.v_pool)[(page * D + d) * kBlockSize +
+                                                             j % kBlockSize];
+    const uint32_t h = e4m3x2_to_f16x2(c);
+    return __half2float(__low2half(*reinterpret_cast<const __half2*>(&h)));
+  }
   return __bfloat162float(static_cast<const __nv_bfloat16*>(
       p.v_pool)[(page * kBlockSize + j % kBlockSize) * D + d]);
+}
+
+// 16 E4M3 codes as 16 f16.
+__device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
+                  e4m3x2_to_f16x2(w.y >> 16));
+  hi = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w),
+                  e4m3x2_to_f16x2(w.w >> 16));
+}
+
+// The byte mask of the codes 0x7F and 0xFF (NaN) in a word.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x01010101u & 0x80808080u) >> 7) * 0xFFu;
+}
+
+// A K tile: keys x D codes, as TMA left them, to [half][key][64 dims] f16 with the 128-byte
+// swizzle.  Consecutive lanes take what lies in different banks on both sides.
+template <int D>
+__device__ __forceinline__ void widen_keys(uint8_t* dst, const uint8_t* raw, int lane, int worker,
+                                           int workers) {
+  constexpr int C = D / 16;                    // 16-dim pieces of a row
+#pragma unroll 4
+  for (int i = worker; i < kPromptTile * C / 32; i += workers) {
+    int key, c;
+    if constexpr (C == 8) {                    // 8 rows of one piece, four pieces
+      key = (i >> 1) * 8 + (lane & 7);
+      c = (i & 1) * 4 + (lane >> 3);
+    } else {                                   // 8 rows of four pieces
+      key = i * 8 + (lane >> 2);
+      c = lane & 3;
+    }
+    const int at = C == 8 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + c * 16;
+    uint4 lo, hi;
+    widen16(*reinterpret_cast<const uint4*>(raw + at), lo, hi);
+    uint8_t* row = dst + (c >> 2) * (kPromptTile * 128) + key * 128;
+    const int ch = (c & 3) * 2;
+    *reinterpret_cast<uint4*>(row + ((ch ^ (key & 7)) << 4)) = lo;
+    *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (key & 7)) << 4)) = hi;
+  }
+}
+
+// A V tile: pages of D rows of 16 keys, to [half of 64 keys][dim][64 keys] f16.  At a border of
+// the mask the codes from key `end` of the tile on and NaN become 0; whether there was a NaN.
+template <int D>
+__device__ __forceinline__ bool widen_values(uint8_t* dst, const uint8_t* raw, int lane, int worker,
+                                             int workers, bool border, int end) {
+  bool found = false;
+#pragma unroll 4
+  for (int i = worker; i < kPromptTile / kBlockSize * D / 32; i += workers) {
+    const int pg = i / (D / 32), d = i % (D / 32) * 32 + lane;
+    uint4 w = *reinterpret_cast<const uint4*>(raw + (pg * D + d) * 16);
+    if (border) {
+      uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int left = end - pg * kBlockSize - 4 * k;      // codes of this word that count
+        if (left < 4) x[k] &= left <= 0 ? 0u : (1u << 8 * left) - 1u;
+        const uint32_t bad = nan_codes(x[k]);
+        found |= bad != 0;
+        x[k] &= ~bad;
+      }
+    }
+    uint4 lo, hi;
+    widen16(w, lo, hi);
+    uint8_t* row = dst + (pg >> 2) * (D * 128) + d * 128;
+    const int ch = (pg & 3) * 2;
+    *reinterpret_cast<uint4*>(row + ((ch ^ (d & 7)) << 4)) = lo;
+    *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (d & 7)) << 4)) = hi;
+  }
+  return found;
+}
+
+// A query row, D bf16 in halves of 128 swizzled bytes, to f16 times 2^-e; returns e.
+template <int D>
+__device__ __forceinline__ int widen_query(uint8_t* tile, int row) {
+  float most = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(
+        tile + (c >> 3) * (kPromptTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      most = fmaxf(most, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+  }
+  // the exponent of the largest element, and 7 less, while 2^e and 2^-e are normal numbers
+  int e = most > 0.f && most < CUDART_INF_F
+              ? static_cast<int>(__float_as_uint(most) >> 23) - 127 - 7 : 0;
+  e = max(-126, e);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(
+        tile + (c >> 3) * (kPromptTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    uint4 w = *at;
+    uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = half2_bits(__floats2half2_rn(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up));
+    *at = w;
+  }
+  return e;
 }
 
 template <int D, bool KV8>
@@ -236,8 +359,12 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
   // ------------------------------------------------------------------ setup
   if (threadIdx.x == 0) {
     for (int i = 0; i < Gm::kStages; ++i) {
-      mbar_init(&ms.full[i], 1);
+      mbar_init(&ms.full[i], KV8 ? Gm::kAux : 1);
       mbar_init(&ms.empty[i], 1);
+    }
+    for (int i = 0; i < Gm::kRawStages; ++i) {
+      mbar_init(&ms.raw_full[i], 1);
+      mbar_init(&ms.raw_empty[i], Gm::kAux);
     }
     mbar_init(&ms.border, 1);
     mbar_init(&ms.checked, Gm::kAux);
@@ -251,6 +378,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       mbar_init(&ms.unit_full[i], 1);
       mbar_init(&ms.unit_empty[i], 1 + Gm::kSoftmaxWarps + Gm::kAux);
       mbar_init(&ms.unit_checked[i], Gm::kAux);
+      mbar_init(&ms.q_wide[i], Gm::kAux);
     }
     mbar_init(&ms.fin, 1);
     fence_barrier_init();
@@ -333,39 +461,55 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             ids = ids_next;
             ids_next = page_id(t * Gm::kPages + 32 + lane);
           }
-          const int box = lane & (Gm::kPages * Gm::kHalves - 1);
-          const int pg = box / Gm::kHalves, h = box % Gm::kHalves;
+          // a bf16 page is one box of 16 keys per half, an FP8 page one box
+          constexpr int kBoxes = KV8 ? 1 : Gm::kHalves;
+          const int box = lane & (Gm::kPages * kBoxes - 1);
+          const int pg = box / kBoxes, h = box % kBoxes;
           const int id = __shfl_sync(0xffffffffu, ids, at + pg);
-          const int row = id == p.num_blocks ? p.num_blocks * p.Hkv * kBlockSize
-                                             : (id * p.Hkv + un.head) * kBlockSize;
+          const int page = id * p.Hkv + (id == p.num_blocks ? 0 : un.head);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++item) {
+            if constexpr (KV8) {
+              const int st = item % Gm::kRawStages;
+              wait(&ms.raw_empty[st], (static_cast<uint32_t>(item / Gm::kRawStages) & 1u) ^ 1u);
+              if (aborted) break;
+              if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], Gm::kRawBytes);
+              __syncwarp();
+              if (lane < Gm::kPages)
+                tma_load_2d(smem + Gm::kRawOff + st * Gm::kRawBytes + pg * kBlockSize * D,
+                            kv ? &tmv : &tmk, &ms.raw_full[st], 0,
+                            page * (kv ? D / 8 : kBlockSize));
+              continue;
+            }
             const int st = item % Gm::kStages;
             wait(&ms.empty[st], (static_cast<uint32_t>(item / Gm::kStages) & 1u) ^ 1u);
             if (aborted) break;
             if (lane == 0) mbar_arrive_expect_tx(&ms.full[st], Gm::kTileBytes);
             __syncwarp();
-            if (lane < Gm::kPages * Gm::kHalves)
+            if (lane < Gm::kPages * kBoxes)
               tma_load_2d(smem + Gm::kRingOff + st * Gm::kTileBytes + h * Gm::kHalfBytes +
                               pg * kBlockSize * 128,
-                          kv ? &tmv : &tmk, &ms.full[st], h * 64, row);
+                          kv ? &tmv : &tmk, &ms.full[st], h * 64, page * kBlockSize);
           }
         }
         ++ui;
         if (aborted) break;
       }
       // no copy may still be landing when the CTA ends
-      if (lane == 0)
-        for (int i = max(0, item - Gm::kStages); i < item; ++i)
-          mbar_wait(&ms.full[i % Gm::kStages], static_cast<uint32_t>(i / Gm::kStages) & 1u, limit);
+      if (lane == 0) {
+        constexpr int kRing = KV8 ? Gm::kRawStages : Gm::kStages;
+        uint64_t* landed = KV8 ? ms.raw_full : ms.full;
+        for (int i = max(0, item - kRing); i < item; ++i)
+          mbar_wait(&landed[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, limit);
+      }
       if (lane == 0 && ui > 0)
         mbar_wait(&ms.q_full, static_cast<uint32_t>(ui - 1) & 1u, limit);
       __syncwarp();
     } else if (warp == Gm::kSoftmaxWarps + 1) {
       // -------------------------------------------------------------- MMA issue
       if (lane == 0) {
-        constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, true>();
-        constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, true, true>();
+        constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, !KV8>();
+        constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, !KV8>();
         const uint32_t ring = smem_u32(smem + Gm::kRingOff), qsm = smem_u32(smem);
         bool ok = true;
         int item0 = 0;
@@ -393,7 +537,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             }
             tc::commit(&ms.s_full[s]);
           };
-          wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
+          if constexpr (KV8)
+            wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+          else
+            wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
           {
             const int st = item0 % Gm::kStages;
             wait(&ms.full[st], static_cast<uint32_t>(item0 / Gm::kStages) & 1u);
@@ -407,7 +554,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           for (int t = un.t0; t < un.t1 && ok; ++t) {
             const int vi = item0 + 2 * (t - un.t0) + 1, ki = vi + 1;
             const int vst = vi % Gm::kStages, kst = ki % Gm::kStages;
-            const bool border = prompt_masked(p, t, un.pos0, last);
+            const bool border = !KV8 && prompt_masked(p, t, un.pos0, last);
             bool v_here = false, k_here = false;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -423,11 +570,14 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 if (!ok) break;
                 tc::fence_after_sync();
 #pragma unroll
-                for (int k = 0; k < kPromptTile / 16; ++k)
-                  tc::mma_f16_ts(tmem + Gm::kO + s * D, tmem + s * kPromptTile + k * 8,
-                                 tc::smem_desc(ring + vst * Gm::kTileBytes + k * 2048,
-                                               Gm::kHalfBytes, 1024),
-                                 kIdO, t > sub[s].a || k > 0 ? 1u : 0u);
+                for (int k = 0; k < kPromptTile / 16; ++k) {
+                  const uint32_t tile = ring + vst * Gm::kTileBytes;
+                  const uint64_t desc =
+                      KV8 ? tc::smem_desc(tile + (k >> 2) * (D * 128) + (k & 3) * 32, 16, 1024)
+                          : tc::smem_desc(tile + k * 2048, Gm::kHalfBytes, 1024);
+                  tc::mma_f16_ts(tmem + Gm::kO + s * D, tmem + s * kPromptTile + k * 8, desc, kIdO,
+                                 t > sub[s].a || k > 0 ? 1u : 0u);
+                }
                 if (t + 1 == sub[s].e) tc::commit(&ms.o_full[s]);
               }
               if (sub[s].a <= t + 1 && t + 1 < sub[s].e) {
@@ -465,7 +615,47 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         const PromptUnit un = ms.unit[ui & 1];
         if (un.b < 0) break;
         const int last = un.pos0 + un.ntok - 1;
-        for (int t = un.t0; t < un.t1; ++t) {
+        if constexpr (KV8) {
+          ok = mbar_wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u, limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int rows = p.sub_tokens * p.G;
+          for (int i = aux * 32 + lane; i < 2 * kPromptTile; i += Gm::kAux * 32) {
+            const int s = i / kPromptTile, r = i % kPromptTile;
+            if (r < rows && (s == 0 || un.ntok > p.sub_tokens))
+              ms.q_exp[ui & 1][s][r] =
+                  static_cast<int8_t>(widen_query<D>(smem + s * Gm::kTileBytes, r));
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.q_wide[ui & 1]);
+          for (int i = 0; i < 2 * (un.t1 - un.t0); ++i) {
+            const int t = un.t0 + i / 2, item = item0 + i;
+            const int rs = item % Gm::kRawStages, st = item % Gm::kStages;
+            ok = mbar_wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u,
+                           limit) &&
+                 mbar_wait(&ms.empty[st],
+                           (static_cast<uint32_t>(item / Gm::kStages) & 1u) ^ 1u, limit);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t* raw = smem + Gm::kRawOff + rs * Gm::kRawBytes;
+            uint8_t* dst = smem + Gm::kRingOff + st * Gm::kTileBytes;
+            if ((i & 1) == 0) {
+              widen_keys<D>(dst, raw, lane, aux, Gm::kAux);
+            } else if (widen_values<D>(dst, raw, lane, aux, Gm::kAux,
+                                       prompt_masked(p, t, un.pos0, last),
+                                       un.L - t * kPromptTile)) {
+              *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ms.full[st]);
+              mbar_arrive(&ms.raw_empty[rs]);
+            }
+          }
+        }
+        for (int t = un.t0; t < un.t1 && !KV8; ++t) {
           if (!prompt_masked(p, t, un.pos0, last)) continue;
           const int vi = item0 + 2 * (t - un.t0) + 1, st = vi % Gm::kStages;
           ok = mbar_wait(&ms.border, n_border++ & 1u, limit);
@@ -531,7 +721,13 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       const bool live = tok < sub.n;                    // rows past the tile's end repeat the last
       const int pos = sub.first + min(tok, max(sub.n, 1) - 1);
       float c = p.scale_log2;
-      if constexpr (KV8) c *= __ldg(p.k_scale + un.head);
+      if constexpr (KV8) {
+        wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+        if (!ok) break;
+        const int e = ms.q_exp[ui & 1][s][live ? r : 0];
+        c *= __ldg(p.k_scale + un.head) *
+             __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      }
       float ref = -CUDART_INF_F;                        // reference, log2 units
       float sum = 0.f;
       for (int t = sub.a; t < sub.e; ++t) {
@@ -595,7 +791,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             }
           }
         }
-        const float off = ref == -CUDART_INF_F ? 0.f : -ref;
+        const float off = ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref;
         const uint64_t cc2 = pack_f32x2(cc, cc), off2 = pack_f32x2(off, off);
         uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
@@ -609,7 +805,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             const float e0 = hw_exp2(__uint_as_float(static_cast<uint32_t>(y)));
             const float e1 = hw_exp2(__uint_as_float(static_cast<uint32_t>(y >> 32)));
             part[k & 1] = add_f32x2(part[k & 1], pack_f32x2(e0, e1));
-            w[k] = pack_bf16x2_rn(e0, e1);
+            if constexpr (KV8)
+              w[k] = half2_bits(__floats2half2_rn(e0, e1));
+            else
+              w[k] = pack_bf16x2_rn(e0, e1);
           }
           tc::tmem_st16(ts + i * 16, w);
         }
@@ -684,7 +883,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            if (i == 0) p.part_ml[at] = make_float2(ref, sum);
+            if (i == 0) p.part_ml[at] = make_float2(ref - Gm::kShift, sum);
           }
         }
       }

@@ -5,7 +5,8 @@ namespace pa {
 
 cudaError_t launch_prompt_d64(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PromptParams& p, bool kv8, cudaStream_t s) {
-  return kv8 ? cudaErrorNotSupported : launch_prompt_as<64, false>(tq, tk, tv, p, s);
+  return kv8 ? launch_prompt_as<64, true>(tq, tk, tv, p, s)
+             : launch_prompt_as<64, false>(tq, tk, tv, p, s);
 }
 
 cudaError_t take_error_prompt_d64(unsigned* bits) { return read_error_word(bits); }
