@@ -102,7 +102,7 @@ struct PromptMisc {
   uint64_t border, checked;            // a V tile at the mask's border is there, is looked at
   uint64_t q_full, q_empty;
   uint64_t q_wide[2];                  // by record: the query rows are f16
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
   uint64_t unit_full[2], unit_empty[2], unit_checked[2]; // by record
   uint64_t fin;
   PromptUnit unit[2];
@@ -193,6 +193,29 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// One lane of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+// The two words of a shared-memory operand's descriptor (128-byte swizzle, 8-row groups 1024
+// bytes apart): the low one takes byte offsets / 16 by addition.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return static_cast<uint32_t>(tc::smem_desc(saddr, lbo_bytes, 1024));
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (tc::kSwizzle128B << 29);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+
 // Bits 15 and 31: the low, the high bf16 of the word is infinite or NaN.
 __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
@@ -206,6 +229,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // tcgen05.wait::ld, with the loaded registers tied behind it.
@@ -372,6 +401,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
     mbar_init(&ms.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_half[i], 4);
       mbar_init(&ms.p_full[i], 4);
       mbar_init(&ms.o_full[i], 1);
       mbar_init(&ms.o_free[i], 4);
@@ -507,100 +537,137 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       __syncwarp();
     } else if (warp == Gm::kSoftmaxWarps + 1) {
       // -------------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, !KV8>();
-        constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, !KV8>();
-        const uint32_t ring = smem_u32(smem + Gm::kRingOff), qsm = smem_u32(smem);
-        bool ok = true;
-        int item0 = 0;
-        uint32_t n_p[2] = {0, 0}, n_u[2] = {0, 0};     // P tiles taken, units of each tile begun
-        uint32_t n_checked = 0;                        // tiles at the mask's border
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity, limit)) ok = false;
-        };
-        for (int ui = 0; ok; ++ui) {
-          wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-          if (!ok) break;
-          const PromptUnit un = ms.unit[ui & 1];
-          mbar_arrive(&ms.unit_empty[ui & 1]);
-          if (un.b < 0) break;
-          const PromptSub sub[2] = {prompt_sub(p, un, 0), prompt_sub(p, un, 1)};
-          const int last = un.pos0 + un.ntok - 1;
-          auto scores = [&](int s, int st) {
+      // The whole warp goes through the steps, so that stages and descriptors are uniform
+      // values, and one elected lane issues.
+      constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, !KV8>();
+      constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, !KV8>();
+      const uint32_t ring = smem_u32(smem + Gm::kRingOff), qsm = smem_u32(smem);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      bool ok = true;
+      int stage = 0;                                   // of the next item (K, V, K, V, ..)
+      uint32_t phase = 0;
+      auto next = [&]() {
+        if (++stage == Gm::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      uint32_t n_p[2] = {0, 0}, n_u[2] = {0, 0};       // P tiles taken, units of each tile begun
+      uint32_t n_checked = 0;                          // tiles at the mask's border
+      // Lanes agree on `ok` once per tile; a wait that ran out in between leaves wrong products
+      // behind an error that is already reported.
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, limit);
+      };
+      // S of tile s from the K tile at `lo`
+      auto scores = [&](int s, uint32_t lo) {
+        const uint32_t a = desc_lo(qsm + s * Gm::kTileBytes, 16);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * Gm::kHalfBytes + (k & 3) * 32;
-              tc::mma_f16_ss(tmem + s * kPromptTile,
-                             tc::smem_desc(qsm + s * Gm::kTileBytes + off, 16, 1024),
-                             tc::smem_desc(ring + st * Gm::kTileBytes + off, 16, 1024), kIdS,
-                             k > 0 ? 1u : 0u);
-            }
-            tc::commit(&ms.s_full[s]);
-          };
-          if constexpr (KV8)
-            wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-          else
-            wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
-          {
-            const int st = item0 % Gm::kStages;
-            wait(&ms.full[st], static_cast<uint32_t>(item0 / Gm::kStages) & 1u);
-            tc::fence_after_sync();
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * Gm::kHalfBytes + (k & 3) * 32) >> 4;
+          tc::mma_f16_ss(tm + s * kPromptTile, desc_of(a + off), desc_of(lo + off), kIdS,
+                         k > 0 ? 1u : 0u);
+        }
+        tc::commit(&ms.s_full[s]);
+      };
+      for (int ui = 0; ok; ++ui) {
+        wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        PromptUnit un = ms.unit[ui & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
+        un.b = __shfl_sync(0xffffffffu, un.b, 0);
+        if (un.b < 0) break;
+        un.t0 = __shfl_sync(0xffffffffu, un.t0, 0);
+        un.t1 = __shfl_sync(0xffffffffu, un.t1, 0);
+        un.pos0 = __shfl_sync(0xffffffffu, un.pos0, 0);
+        un.ntok = __shfl_sync(0xffffffffu, un.ntok, 0);
+        const PromptSub sub[2] = {prompt_sub(p, un, 0), prompt_sub(p, un, 1)};
+        const int last = un.pos0 + un.ntok - 1;
+        if constexpr (KV8)
+          wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+        else
+          wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
+        wait(&ms.full[stage], phase);
+        __syncwarp();
+        tc::fence_after_sync();
+        {
+          const uint32_t lo = desc_lo(ring + stage * Gm::kTileBytes, 16);
+          if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-              if (sub[s].a <= un.t0 && un.t0 < sub[s].e) scores(s, st);
-            tc::commit(&ms.empty[st]);
+              if (sub[s].a <= un.t0 && un.t0 < sub[s].e) scores(s, lo);
+            tc::commit(&ms.empty[stage]);
             if (un.t0 + 1 == un.t1) tc::commit(&ms.q_empty);
           }
-          for (int t = un.t0; t < un.t1 && ok; ++t) {
-            const int vi = item0 + 2 * (t - un.t0) + 1, ki = vi + 1;
-            const int vst = vi % Gm::kStages, kst = ki % Gm::kStages;
-            const bool border = !KV8 && prompt_masked(p, t, un.pos0, last);
-            bool v_here = false, k_here = false;
+          __syncwarp();
+          next();
+        }
+        for (int t = un.t0; t < un.t1; ++t) {
+          const bool border = !KV8 && prompt_masked(p, t, un.pos0, last);
+          const bool more = t + 1 < un.t1;
+          const int vst = stage;
+          const uint32_t vph = phase;
+          next();
+          const int kst = stage;
+          const uint32_t kph = phase;
+          if (more) next();
+          const uint32_t vlo = desc_lo(ring + vst * Gm::kTileBytes, KV8 ? 16 : Gm::kHalfBytes);
+          const uint32_t klo = desc_lo(ring + kst * Gm::kTileBytes, 16);
+          wait(&ms.full[vst], vph);
+          if (border && lane == 0) mbar_arrive(&ms.border);
+          bool k_here = false;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (sub[s].a <= t && t < sub[s].e) {
-                if (!v_here) {
-                  wait(&ms.full[vst], static_cast<uint32_t>(vi / Gm::kStages) & 1u);
-                  if (border) mbar_arrive(&ms.border);
-                }
-                if (t == sub[s].a) wait(&ms.o_free[s], (n_u[s]++ & 1u) ^ 1u);
-                wait(&ms.p_full[s], n_p[s]++ & 1u);
-                if (border && !v_here) wait(&ms.checked, n_checked++ & 1u);
-                v_here = true;
-                if (!ok) break;
-                tc::fence_after_sync();
+          for (int s = 0; s < 2; ++s) {
+            const bool now = sub[s].a <= t && t < sub[s].e;
+            const bool then = sub[s].a <= t + 1 && t + 1 < sub[s].e;
+            if (now) {
+              if (border && (s == 0 || !(sub[0].a <= t && t < sub[0].e)))
+                wait(&ms.checked, n_checked++ & 1u);
+              if (t == sub[s].a) wait(&ms.o_free[s], (n_u[s]++ & 1u) ^ 1u);
 #pragma unroll
-                for (int k = 0; k < kPromptTile / 16; ++k) {
-                  const uint32_t tile = ring + vst * Gm::kTileBytes;
-                  const uint64_t desc =
-                      KV8 ? tc::smem_desc(tile + (k >> 2) * (D * 128) + (k & 3) * 32, 16, 1024)
-                          : tc::smem_desc(tile + k * 2048, Gm::kHalfBytes, 1024);
-                  tc::mma_f16_ts(tmem + Gm::kO + s * D, tmem + s * kPromptTile + k * 8, desc, kIdO,
-                                 t > sub[s].a || k > 0 ? 1u : 0u);
-                }
-                if (t + 1 == sub[s].e) tc::commit(&ms.o_full[s]);
-              }
-              if (sub[s].a <= t + 1 && t + 1 < sub[s].e) {
-                if (!k_here) {
-                  wait(&ms.full[kst], static_cast<uint32_t>(ki / Gm::kStages) & 1u);
-                  k_here = true;
-                }
-                if (!ok) break;
+              for (int half = 0; half < 2; ++half) {   // of the keys
+                wait(half ? &ms.p_full[s] : &ms.p_half[s], n_p[s] & 1u);
+                __syncwarp();
                 tc::fence_after_sync();
-                scores(s, kst);
+                if (elect_one()) {
+#pragma unroll
+                  for (int i = 0; i < kPromptTile / 32; ++i) {
+                    const int k = half * (kPromptTile / 32) + i;
+                    const uint32_t off =
+                        (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
+                    tc::mma_f16_ts(tm + Gm::kO + s * D, tm + s * kPromptTile + k * 8,
+                                   desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
+                  }
+                  if (half && t + 1 == sub[s].e) tc::commit(&ms.o_full[s]);
+                }
+                __syncwarp();
               }
+              ++n_p[s];
             }
-            if (!ok) break;
+            if (then) {
+              if (!k_here) wait(&ms.full[kst], kph);
+              k_here = true;
+              __syncwarp();
+              tc::fence_after_sync();
+              if (elect_one()) scores(s, klo);
+              __syncwarp();
+            }
+          }
+          if (elect_one()) {
             tc::commit(&ms.empty[vst]);
-            if (t + 1 < un.t1) tc::commit(&ms.empty[kst]);
+            if (more) tc::commit(&ms.empty[kst]);
             if (t + 2 == un.t1) tc::commit(&ms.q_empty);
           }
-          item0 += 2 * (un.t1 - un.t0);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
-        // every MMA has completed before the CTA gives its tensor memory back
-        tc::commit(&ms.fin);
-        mbar_wait(&ms.fin, 0, limit);
       }
+      // every MMA has completed before the CTA gives its tensor memory back
+      __syncwarp();
+      if (elect_one()) tc::commit(&ms.fin);
+      __syncwarp();
+      mbar_wait(&ms.fin, 0, limit);
       __syncwarp();
     } else {
       // -------------------------------------------------------------- borders of the mask
@@ -708,13 +775,13 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
     const int tok = r / p.G, g = r - tok * p.G;         // of this row
     bool ok = true;
     uint32_t n_s = 0, n_o = 0;                          // S and O tiles taken
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !mbar_wait(bar, parity, limit)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // lanes agree on `ok` where they vote
+      if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, limit);
+      __syncwarp();
     };
     for (int ui = 0; ok; ++ui) {
       wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, ok)) break;
       const PromptUnit un = ms.unit[ui & 1];
       if (un.b < 0) break;
       const PromptSub sub = prompt_sub(p, un, s);
@@ -723,7 +790,6 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       float c = p.scale_log2;
       if constexpr (KV8) {
         wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-        if (!ok) break;
         const int e = ms.q_exp[ui & 1][s][live ? r : 0];
         c *= __ldg(p.k_scale + un.head) *
              __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
@@ -732,7 +798,6 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       float sum = 0.f;
       for (int t = sub.a; t < sub.e; ++t) {
         wait(&ms.s_full[s], n_s++ & 1u);
-        if (!ok) break;
         tc::fence_after_sync();
         uint32_t x[4][32];
 #pragma unroll
@@ -760,11 +825,12 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(x[i][0]);
+          mx[i] = fmaxf(__uint_as_float(x[i][0]), __uint_as_float(x[i][1]));
 #pragma unroll
-          for (int k = 1; k < 32; ++k) mx[i] = fmaxf(mx[i], __uint_as_float(x[i][k]));
+          for (int k = 2; k < 32; k += 2)
+            mx[i] = max3(mx[i], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
         }
-        float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cc;
+        float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * cc;
         if (__any_sync(0xffffffffu, fabsf(m) > 67108864.f && fabsf(m) < CUDART_INF_F) &&
             cc != 1.f) {
 #pragma unroll
@@ -810,6 +876,12 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             else
               w[k] = pack_bf16x2_rn(e0, e1);
           }
+          if (i == 2) {                                 // by now the first two have arrived
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.p_half[s]);
+          }
           tc::tmem_st16(ts + i * 16, w);
         }
         part[0] = add_f32x2(part[0], part[1]);
@@ -819,8 +891,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full[s]);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, ok)) break;
 
       // -------------------------------------------------------------- unit output
       wait(&ms.unit_checked[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
@@ -829,7 +903,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
       const bool any = sub.e > sub.a;
       if (any) wait(&ms.o_full[s], n_o++ & 1u);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after_sync();
       float vs = 1.f;
       if constexpr (KV8) vs = __ldg(p.v_scale + un.head);
