@@ -204,6 +204,36 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
+// MMAs and commits of the lane with `leader` set, in code that the whole warp runs.
+__device__ __forceinline__ void lead_mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void lead_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void lead_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
+}
+
 // The two words of a shared-memory operand's descriptor (128-byte swizzle, 8-row groups 1024
 // bytes apart): the low one takes byte offsets / 16 by addition.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
@@ -559,16 +589,17 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, limit);
       };
+      const uint32_t leader = elect_one() ? 1u : 0u;
       // S of tile s from the K tile at `lo`
       auto scores = [&](int s, uint32_t lo) {
         const uint32_t a = desc_lo(qsm + s * Gm::kTileBytes, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * Gm::kHalfBytes + (k & 3) * 32) >> 4;
-          tc::mma_f16_ss(tm + s * kPromptTile, desc_of(a + off), desc_of(lo + off), kIdS,
-                         k > 0 ? 1u : 0u);
+          lead_mma_ss(leader, tm + s * kPromptTile, desc_of(a + off), desc_of(lo + off), kIdS,
+                      k > 0 ? 1u : 0u);
         }
-        tc::commit(&ms.s_full[s]);
+        lead_commit(leader, &ms.s_full[s]);
       };
       for (int ui = 0; ok; ++ui) {
         wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
@@ -593,14 +624,11 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         tc::fence_after_sync();
         {
           const uint32_t lo = desc_lo(ring + stage * Gm::kTileBytes, 16);
-          if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-              if (sub[s].a <= un.t0 && un.t0 < sub[s].e) scores(s, lo);
-            tc::commit(&ms.empty[stage]);
-            if (un.t0 + 1 == un.t1) tc::commit(&ms.q_empty);
-          }
-          __syncwarp();
+          for (int s = 0; s < 2; ++s)
+            if (sub[s].a <= un.t0 && un.t0 < sub[s].e) scores(s, lo);
+          lead_commit(leader, &ms.empty[stage]);
+          if (un.t0 + 1 == un.t1) lead_commit(leader, &ms.q_empty);
           next();
         }
         for (int t = un.t0; t < un.t1; ++t) {
@@ -630,18 +658,15 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 wait(half ? &ms.p_full[s] : &ms.p_half[s], n_p[s] & 1u);
                 __syncwarp();
                 tc::fence_after_sync();
-                if (elect_one()) {
 #pragma unroll
-                  for (int i = 0; i < kPromptTile / 32; ++i) {
-                    const int k = half * (kPromptTile / 32) + i;
-                    const uint32_t off =
-                        (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
-                    tc::mma_f16_ts(tm + Gm::kO + s * D, tm + s * kPromptTile + k * 8,
-                                   desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
-                  }
-                  if (half && t + 1 == sub[s].e) tc::commit(&ms.o_full[s]);
+                for (int i = 0; i < kPromptTile / 32; ++i) {
+                  const int k = half * (kPromptTile / 32) + i;
+                  const uint32_t off =
+                      (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
+                  lead_mma_ts(leader, tm + Gm::kO + s * D, tm + s * kPromptTile + k * 8,
+                              desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
                 }
-                __syncwarp();
+                if (half && t + 1 == sub[s].e) lead_commit(leader, &ms.o_full[s]);
               }
               ++n_p[s];
             }
@@ -650,23 +675,19 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               k_here = true;
               __syncwarp();
               tc::fence_after_sync();
-              if (elect_one()) scores(s, klo);
-              __syncwarp();
+              scores(s, klo);
             }
           }
-          if (elect_one()) {
-            tc::commit(&ms.empty[vst]);
-            if (more) tc::commit(&ms.empty[kst]);
-            if (t + 2 == un.t1) tc::commit(&ms.q_empty);
-          }
+          lead_commit(leader, &ms.empty[vst]);
+          if (more) lead_commit(leader, &ms.empty[kst]);
+          if (t + 2 == un.t1) lead_commit(leader, &ms.q_empty);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
       }
       // every MMA has completed before the CTA gives its tensor memory back
       __syncwarp();
-      if (elect_one()) tc::commit(&ms.fin);
-      __syncwarp();
+      lead_commit(leader, &ms.fin);
       mbar_wait(&ms.fin, 0, limit);
       __syncwarp();
     } else {
