@@ -15,18 +15,21 @@
 // tile's products run while the other tile's weights are computed.
 //
 // Roles of a CTA (persistent, one per SM):
-//   warps 0-3, 4-7  softmax of the first, the second tile: thread = row.  The reference
-//                   moves only when a score passes it by 8 (log2 units); O is then
-//                   rescaled in tensor memory, which no product is using at that time:
-//                   S of the next keys is issued behind P . V of the last ones.
-//   warp 8          finds the units, loads Q and the K/V tiles by TMA, 16 keys per page
-//                   box, through the block table.
-//   warp 9          one thread issues every MMA: per K/V tile P.V then the next S of the
-//                   first tile, the same of the second.
-//   warps 10, 11    tiles at a border of the mask: V rows behind the context become zero,
-//                   and so do infinities and NaN of V rows that some query row must not
-//                   see (0 * inf would reach it); the rows that see those keys get them
-//                   added at the end.
+//   warps 0-3, 4-7  softmax of the first, the second tile: thread = row.  A tile's weights are
+//                   taken with the reference of the last ones at once; only where their sum
+//                   shows one past 2^15, at the mask's border and at a unit's start is the
+//                   row's maximum looked for, which then becomes the reference.  O is rescaled
+//                   in tensor memory, which no product is using at that time: S of the next
+//                   keys is issued behind P . V of the last ones.
+//   warp 8          finds the units, loads Q and the K tiles by TMA, 16 keys per page box,
+//                   through the block table.
+//   warp 9          issues the MMAs: per K/V tile P.V (in two halves, the first while the last
+//                   quarter of the weights is computed) then the next S of the first tile, the
+//                   same of the second.
+//   warps 10, 11    copy the V tiles, rows behind the context as zeros.  At the mask's border
+//                   infinities and NaN of V rows that some query row must not see are taken
+//                   out (0 * inf would reach it); the rows that see those keys get them added
+//                   at the end.
 //
 // FP8 pages.  The products take f16, of which every E4M3 value is one: warps 10 and 11 widen
 // each tile from where TMA left it into the ring that the MMAs read (K rows as they are; V
@@ -54,19 +57,21 @@ namespace pa {
 template <int D, bool KV8>
 struct PromptGeo {
   static constexpr int kSoftmaxWarps = 8;
-  static constexpr int kAux = 2;                         // warps for the borders of the mask
+  static constexpr int kAux = 2;                         // warps that bring V, or widen K and V
   static constexpr int kThreads = (kSoftmaxWarps + 2 + kAux) * 32;
   static constexpr int kHalves = D / 64;                 // 64-dim halves of a row (128 bytes)
   static constexpr int kHalfBytes = kPromptTile * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
-  static constexpr int kStages = KV8 ? 3 : 5;            // K and V tiles ready or in flight
-  static constexpr int kRawStages = KV8 ? 4 : 0;         // FP8 tiles in flight
+  static constexpr int kKStages = KV8 ? 2 : 3;           // K tiles ready or in flight
+  static constexpr int kVStages = 2;
+  static constexpr int kRawStages = KV8 ? 2 : 0;         // FP8 tiles in flight
   static constexpr int kRawBytes = kPromptTile * D;
   static constexpr int kShift = KV8 ? 7 : 0;             // weights carry 2^kShift
   static constexpr int kPages = kPromptTile / kBlockSize;
   // shared memory, from a 1024-byte aligned base
-  static constexpr int kRingOff = 2 * kTileBytes;        // behind the two Q tiles
-  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kKOff = 2 * kTileBytes;           // behind the two Q tiles
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr int kRawOff = kVOff + kVStages * kTileBytes;
   static constexpr int kMiscOff = kRawOff + kRawStages * kRawBytes;
   static constexpr int kMiscBytes = KV8 ? 1024 : 512;
   static constexpr int kAlloc = kMiscOff + kMiscBytes + 1024;
@@ -79,6 +84,14 @@ struct PromptGeo {
   static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs <=
                     kThreads * kRegs, "the split takes no more than the launch has");
 };
+
+// Weights are taken with the present reference while none of them passes 2^15 (and their sum
+// does not either), which an f16 holds; a reference is one of rounded products up to 2^26.
+constexpr float kPromptLimit = 32768.f, kPromptExact = 67108864.f;
+
+// Columns of S that the weights of keys 32 i .. 32 i + 31 take: the first two quarters those of
+// the last scores, so that the first three quarters of S can be read again.
+__host__ __device__ constexpr int prompt_weight_col(int i) { return i < 2 ? 96 + 16 * i : 32 + 16 * i; }
 
 // One unit of work.
 struct PromptUnit {
@@ -95,11 +108,10 @@ struct PromptUnit {
 template <int D, bool KV8>
 struct PromptMisc {
   using Gm = PromptGeo<D, KV8>;
-  uint64_t full[Gm::kStages];
-  uint64_t empty[Gm::kStages];
+  uint64_t k_full[Gm::kKStages], k_empty[Gm::kKStages];
+  uint64_t v_full[Gm::kVStages], v_empty[Gm::kVStages];
   uint64_t raw_full[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
   uint64_t raw_empty[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
-  uint64_t border, checked;            // a V tile at the mask's border is there, is looked at
   uint64_t q_full, q_empty;
   uint64_t q_wide[2];                  // by record: the query rows are f16
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
@@ -177,6 +189,43 @@ __device__ __forceinline__ PromptSub prompt_sub(const PromptParams& p, const Pro
   r.e = max(r.e, r.a);
   return r;
 }
+
+// Block ids of a unit's pages for one warp: a batch of 32 (four tiles) in lane order, the next
+// one read ahead.  Pages behind the context's end and ids outside the pool (an error) become
+// num_blocks.
+struct PromptPages {
+  const int32_t* table;
+  int first, npages, end, ids, next;
+
+  __device__ __forceinline__ int id(const PromptParams& p, int i) const {
+    int x = p.num_blocks;
+    if (i < npages) {
+      x = __ldg(table + i);
+      if (static_cast<unsigned>(x) >= static_cast<unsigned>(p.num_blocks)) {
+        if (i < end) atomicOr(&g_pa_err, kErrBounds);
+        x = p.num_blocks;
+      }
+    }
+    return x;
+  }
+  __device__ __forceinline__ void begin(const PromptParams& p, const PromptUnit& un, int lane) {
+    table = p.block_tables + static_cast<size_t>(un.b) * p.mbs;
+    npages = (un.L + kBlockSize - 1) / kBlockSize;
+    first = un.t0 * (kPromptTile / kBlockSize);
+    end = un.t1 * (kPromptTile / kBlockSize);
+    ids = id(p, first + lane);
+    next = id(p, first + 32 + lane);
+  }
+  // The lane that holds the first page of tile t; tiles come in order.
+  __device__ __forceinline__ int lane_of(const PromptParams& p, int t, int lane) {
+    const int i = t * (kPromptTile / kBlockSize) - first;
+    if (i > 0 && (i & 31) == 0) {
+      ids = next;
+      next = id(p, first + i + 32 + lane);
+    }
+    return i & 31;
+  }
+};
 
 // Whether some query token of [first, last] does not see every key of tile t.
 __device__ __forceinline__ bool prompt_masked(const PromptParams& p, int t, int first, int last) {
@@ -417,16 +466,18 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 
   // ------------------------------------------------------------------ setup
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Gm::kStages; ++i) {
-      mbar_init(&ms.full[i], KV8 ? Gm::kAux : 1);
-      mbar_init(&ms.empty[i], 1);
+    for (int i = 0; i < Gm::kKStages; ++i) {
+      mbar_init(&ms.k_full[i], KV8 ? Gm::kAux : 1);
+      mbar_init(&ms.k_empty[i], 1);
+    }
+    for (int i = 0; i < Gm::kVStages; ++i) {
+      mbar_init(&ms.v_full[i], Gm::kAux);
+      mbar_init(&ms.v_empty[i], 1);
     }
     for (int i = 0; i < Gm::kRawStages; ++i) {
       mbar_init(&ms.raw_full[i], 1);
       mbar_init(&ms.raw_empty[i], Gm::kAux);
     }
-    mbar_init(&ms.border, 1);
-    mbar_init(&ms.checked, Gm::kAux);
     mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -463,6 +514,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         tma_prefetch_map(&tmk);
         tma_prefetch_map(&tmv);
       }
+      // K tiles (K and V tiles of FP8 pages) into their ring
+      constexpr int kRing = KV8 ? Gm::kRawStages : Gm::kKStages;
+      uint64_t* full = KV8 ? ms.raw_full : ms.k_full;
+      uint64_t* empty = KV8 ? ms.raw_empty : ms.k_empty;
       bool aborted = false;
       int item = 0, ui = 0, u = blockIdx.x;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -486,110 +541,85 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           mbar_arrive(&ms.unit_full[ui & 1]);
         }
         if (un.b < 0) break;
-        wait(&ms.q_empty, (static_cast<uint32_t>(ui) & 1u) ^ 1u);
-        if (aborted) break;
-        if (lane == 0) {
-          const int subs = un.ntok > p.sub_tokens ? 2 : 1;
-          mbar_arrive_expect_tx(&ms.q_full, static_cast<uint32_t>(subs * Gm::kHalves *
-                                                                  p.sub_tokens * p.G * 128));
-          for (int s = 0; s < subs; ++s)
-            for (int h = 0; h < Gm::kHalves; ++h)
-              tma_load_4d(smem + s * Gm::kTileBytes + h * Gm::kHalfBytes, &tmq, &ms.q_full, h * 64,
-                          0, un.head, un.row0 + s * p.sub_tokens);
-        }
-        // ids of 32 pages (four tiles) in lane order, one batch read ahead; pages behind the
-        // context's end and ids outside the pool become a row past the pool, which TMA fills
-        // with zeros
-        const int32_t* table = p.block_tables + static_cast<size_t>(un.b) * p.mbs;
-        const int npages = (un.L + kBlockSize - 1) / kBlockSize;
-        const int first = un.t0 * Gm::kPages;
-        auto page_id = [&](int i) {
-          int id = p.num_blocks;
-          if (i < npages) {
-            id = __ldg(table + i);
-            if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
-              if (i < un.t1 * Gm::kPages) atomicOr(&g_pa_err, kErrBounds);
-              id = p.num_blocks;
-            }
-          }
-          return id;
-        };
-        int ids = page_id(first + lane), ids_next = page_id(first + 32 + lane);
+        PromptPages pages;
+        pages.begin(p, un, lane);
         for (int t = un.t0; t < un.t1 && !aborted; ++t) {
-          const int at = (t - un.t0) * Gm::kPages & 31;
-          if (t > un.t0 && at == 0) {
-            ids = ids_next;
-            ids_next = page_id(t * Gm::kPages + 32 + lane);
-          }
-          // a bf16 page is one box of 16 keys per half, an FP8 page one box
+          // a bf16 page is one box of 16 keys per half, an FP8 page one box; a row past the pool
+          // is filled with zeros
           constexpr int kBoxes = KV8 ? 1 : Gm::kHalves;
           const int box = lane & (Gm::kPages * kBoxes - 1);
           const int pg = box / kBoxes, h = box % kBoxes;
-          const int id = __shfl_sync(0xffffffffu, ids, at + pg);
+          const int at = pages.lane_of(p, t, lane);
+          const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
           const int page = id * p.Hkv + (id == p.num_blocks ? 0 : un.head);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++item) {
-            if constexpr (KV8) {
-              const int st = item % Gm::kRawStages;
-              wait(&ms.raw_empty[st], (static_cast<uint32_t>(item / Gm::kRawStages) & 1u) ^ 1u);
-              if (aborted) break;
-              if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], Gm::kRawBytes);
-              __syncwarp();
-              if (lane < Gm::kPages)
-                tma_load_2d(smem + Gm::kRawOff + st * Gm::kRawBytes + pg * kBlockSize * D,
-                            kv ? &tmv : &tmk, &ms.raw_full[st], 0,
-                            page * (kv ? D / 8 : kBlockSize));
-              continue;
-            }
-            const int st = item % Gm::kStages;
-            wait(&ms.empty[st], (static_cast<uint32_t>(item / Gm::kStages) & 1u) ^ 1u);
+          for (int kv = 0; kv < (KV8 ? 2 : 1); ++kv, ++item) {
+            const int st = item % kRing;
+            wait(&empty[st], (static_cast<uint32_t>(item / kRing) & 1u) ^ 1u);
             if (aborted) break;
-            if (lane == 0) mbar_arrive_expect_tx(&ms.full[st], Gm::kTileBytes);
+            if (lane == 0)
+              mbar_arrive_expect_tx(&full[st], KV8 ? Gm::kRawBytes : Gm::kTileBytes);
             __syncwarp();
-            if (lane < Gm::kPages * kBoxes)
-              tma_load_2d(smem + Gm::kRingOff + st * Gm::kTileBytes + h * Gm::kHalfBytes +
-                              pg * kBlockSize * 128,
-                          kv ? &tmv : &tmk, &ms.full[st], h * 64, page * kBlockSize);
+            if (lane < Gm::kPages * kBoxes) {
+              if constexpr (KV8)
+                tma_load_2d(smem + Gm::kRawOff + st * Gm::kRawBytes + pg * kBlockSize * D,
+                            kv ? &tmv : &tmk, &full[st], 0, page * (kv ? D / 8 : kBlockSize));
+              else
+                tma_load_2d(smem + Gm::kKOff + st * Gm::kTileBytes + h * Gm::kHalfBytes +
+                                pg * kBlockSize * 128,
+                            &tmk, &full[st], h * 64, page * kBlockSize);
+            }
+          }
+          if (t == un.t0 && !aborted) {
+            // the query rows, once the last unit's scores no longer need theirs
+            wait(&ms.q_empty, (static_cast<uint32_t>(ui) & 1u) ^ 1u);
+            if (aborted) break;
+            ++ui;
+            if (lane == 0) {
+              const int subs = un.ntok > p.sub_tokens ? 2 : 1;
+              mbar_arrive_expect_tx(&ms.q_full, static_cast<uint32_t>(subs * Gm::kHalves *
+                                                                      p.sub_tokens * p.G * 128));
+              for (int s = 0; s < subs; ++s)
+                for (int hh = 0; hh < Gm::kHalves; ++hh)
+                  tma_load_4d(smem + s * Gm::kTileBytes + hh * Gm::kHalfBytes, &tmq, &ms.q_full,
+                              hh * 64, 0, un.head, un.row0 + s * p.sub_tokens);
+            }
           }
         }
-        ++ui;
         if (aborted) break;
       }
       // no copy may still be landing when the CTA ends
       if (lane == 0) {
-        constexpr int kRing = KV8 ? Gm::kRawStages : Gm::kStages;
-        uint64_t* landed = KV8 ? ms.raw_full : ms.full;
         for (int i = max(0, item - kRing); i < item; ++i)
-          mbar_wait(&landed[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, limit);
+          mbar_wait(&full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, limit);
+        if (ui > 0) mbar_wait(&ms.q_full, static_cast<uint32_t>(ui - 1) & 1u, limit);
       }
-      if (lane == 0 && ui > 0)
-        mbar_wait(&ms.q_full, static_cast<uint32_t>(ui - 1) & 1u, limit);
       __syncwarp();
     } else if (warp == Gm::kSoftmaxWarps + 1) {
       // -------------------------------------------------------------- MMA issue
+      const uint32_t leader = elect_one() ? 1u : 0u;
       // The whole warp goes through the steps, so that stages and descriptors are uniform
       // values, and one elected lane issues.
       constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, !KV8>();
       constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, !KV8>();
-      const uint32_t ring = smem_u32(smem + Gm::kRingOff), qsm = smem_u32(smem);
+      const uint32_t kring = smem_u32(smem + Gm::kKOff), vring = smem_u32(smem + Gm::kVOff);
+      const uint32_t qsm = smem_u32(smem);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       bool ok = true;
-      int stage = 0;                                   // of the next item (K, V, K, V, ..)
-      uint32_t phase = 0;
-      auto next = [&]() {
-        if (++stage == Gm::kStages) {
-          stage = 0;
-          phase ^= 1u;
+      int kst = 0, vst = 0;                            // stage and phase of the next K, V tile
+      uint32_t kph = 0, vph = 0;
+      auto k_done = [&]() {
+        lead_commit(leader, &ms.k_empty[kst]);
+        if (++kst == Gm::kKStages) {
+          kst = 0;
+          kph ^= 1u;
         }
       };
       uint32_t n_p[2] = {0, 0}, n_u[2] = {0, 0};       // P tiles taken, units of each tile begun
-      uint32_t n_checked = 0;                          // tiles at the mask's border
       // Lanes agree on `ok` once per tile; a wait that ran out in between leaves wrong products
       // behind an error that is already reported.
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, limit);
       };
-      const uint32_t leader = elect_one() ? 1u : 0u;
       // S of tile s from the K tile at `lo`
       auto scores = [&](int s, uint32_t lo) {
         const uint32_t a = desc_lo(qsm + s * Gm::kTileBytes, 16);
@@ -614,44 +644,28 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         un.pos0 = __shfl_sync(0xffffffffu, un.pos0, 0);
         un.ntok = __shfl_sync(0xffffffffu, un.ntok, 0);
         const PromptSub sub[2] = {prompt_sub(p, un, 0), prompt_sub(p, un, 1)};
-        const int last = un.pos0 + un.ntok - 1;
         if constexpr (KV8)
           wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
         else
           wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
-        wait(&ms.full[stage], phase);
+        wait(&ms.k_full[kst], kph);
         __syncwarp();
         tc::fence_after_sync();
-        {
-          const uint32_t lo = desc_lo(ring + stage * Gm::kTileBytes, 16);
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
-            if (sub[s].a <= un.t0 && un.t0 < sub[s].e) scores(s, lo);
-          lead_commit(leader, &ms.empty[stage]);
-          if (un.t0 + 1 == un.t1) lead_commit(leader, &ms.q_empty);
-          next();
-        }
+        for (int s = 0; s < 2; ++s)
+          if (sub[s].a <= un.t0 && un.t0 < sub[s].e)
+            scores(s, desc_lo(kring + kst * Gm::kTileBytes, 16));
+        k_done();
+        if (un.t0 + 1 == un.t1) lead_commit(leader, &ms.q_empty);
         for (int t = un.t0; t < un.t1; ++t) {
-          const bool border = !KV8 && prompt_masked(p, t, un.pos0, last);
           const bool more = t + 1 < un.t1;
-          const int vst = stage;
-          const uint32_t vph = phase;
-          next();
-          const int kst = stage;
-          const uint32_t kph = phase;
-          if (more) next();
-          const uint32_t vlo = desc_lo(ring + vst * Gm::kTileBytes, KV8 ? 16 : Gm::kHalfBytes);
-          const uint32_t klo = desc_lo(ring + kst * Gm::kTileBytes, 16);
-          wait(&ms.full[vst], vph);
-          if (border && lane == 0) mbar_arrive(&ms.border);
+          const uint32_t vlo = desc_lo(vring + vst * Gm::kTileBytes, KV8 ? 16 : Gm::kHalfBytes);
+          const uint32_t klo = desc_lo(kring + kst * Gm::kTileBytes, 16);
+          wait(&ms.v_full[vst], vph);
           bool k_here = false;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const bool now = sub[s].a <= t && t < sub[s].e;
-            const bool then = sub[s].a <= t + 1 && t + 1 < sub[s].e;
-            if (now) {
-              if (border && (s == 0 || !(sub[0].a <= t && t < sub[0].e)))
-                wait(&ms.checked, n_checked++ & 1u);
+            if (sub[s].a <= t && t < sub[s].e) {
               if (t == sub[s].a) wait(&ms.o_free[s], (n_u[s]++ & 1u) ^ 1u);
 #pragma unroll
               for (int half = 0; half < 2; ++half) {   // of the keys
@@ -663,23 +677,28 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                   const int k = half * (kPromptTile / 32) + i;
                   const uint32_t off =
                       (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
-                  lead_mma_ts(leader, tm + Gm::kO + s * D, tm + s * kPromptTile + k * 8,
+                  lead_mma_ts(leader, tm + Gm::kO + s * D,
+                              tm + s * kPromptTile + prompt_weight_col(k / 2) + k % 2 * 8,
                               desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
                 }
                 if (half && t + 1 == sub[s].e) lead_commit(leader, &ms.o_full[s]);
               }
               ++n_p[s];
             }
-            if (then) {
-              if (!k_here) wait(&ms.full[kst], kph);
+            if (sub[s].a <= t + 1 && t + 1 < sub[s].e) {
+              if (!k_here) wait(&ms.k_full[kst], kph);
               k_here = true;
               __syncwarp();
               tc::fence_after_sync();
               scores(s, klo);
             }
           }
-          lead_commit(leader, &ms.empty[vst]);
-          if (more) lead_commit(leader, &ms.empty[kst]);
+          lead_commit(leader, &ms.v_empty[vst]);
+          if (++vst == Gm::kVStages) {
+            vst = 0;
+            vph ^= 1u;
+          }
+          if (more) k_done();
           if (t + 2 == un.t1) lead_commit(leader, &ms.q_empty);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -691,21 +710,23 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       mbar_wait(&ms.fin, 0, limit);
       __syncwarp();
     } else {
-      // -------------------------------------------------------------- borders of the mask
+      // -------------------------------------------------------------- V, or FP8 tiles widened
       const int aux = warp - Gm::kSoftmaxWarps - 2;
       bool ok = true;
-      int item0 = 0;
-      uint32_t n_border = 0;
-      for (int ui = 0; ok; ++ui) {
-        ok = mbar_wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u, limit);
+      int item = 0, tiles = 0;                         // FP8 tiles, V tiles so far
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, limit)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
+      };
+      for (int ui = 0; ok; ++ui) {
+        wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
         if (!ok) break;
         const PromptUnit un = ms.unit[ui & 1];
         if (un.b < 0) break;
         const int last = un.pos0 + un.ntok - 1;
+        bool found = false;
         if constexpr (KV8) {
-          ok = mbar_wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u, limit);
-          ok = __all_sync(0xffffffffu, ok);
+          wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
           if (!ok) break;
           const int rows = p.sub_tokens * p.G;
           for (int i = aux * 32 + lane; i < 2 * kPromptTile; i += Gm::kAux * 32) {
@@ -717,73 +738,111 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms.q_wide[ui & 1]);
-          for (int i = 0; i < 2 * (un.t1 - un.t0); ++i) {
-            const int t = un.t0 + i / 2, item = item0 + i;
-            const int rs = item % Gm::kRawStages, st = item % Gm::kStages;
-            ok = mbar_wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u,
-                           limit) &&
-                 mbar_wait(&ms.empty[st],
-                           (static_cast<uint32_t>(item / Gm::kStages) & 1u) ^ 1u, limit);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint8_t* raw = smem + Gm::kRawOff + rs * Gm::kRawBytes;
-            uint8_t* dst = smem + Gm::kRingOff + st * Gm::kTileBytes;
-            if ((i & 1) == 0) {
-              widen_keys<D>(dst, raw, lane, aux, Gm::kAux);
-            } else if (widen_values<D>(dst, raw, lane, aux, Gm::kAux,
-                                       prompt_masked(p, t, un.pos0, last),
-                                       un.L - t * kPromptTile)) {
-              *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&ms.full[st]);
-              mbar_arrive(&ms.raw_empty[rs]);
-            }
-          }
-        }
-        for (int t = un.t0; t < un.t1 && !KV8; ++t) {
-          if (!prompt_masked(p, t, un.pos0, last)) continue;
-          const int vi = item0 + 2 * (t - un.t0) + 1, st = vi % Gm::kStages;
-          ok = mbar_wait(&ms.border, n_border++ & 1u, limit);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          // four keys' halves of 128 bytes at a time; the two warps take every other four
-          uint8_t* tile = smem + Gm::kRingOff + st * Gm::kTileBytes;
-          bool found = false;
-#pragma unroll 2
-          for (int k4 = aux; k4 < kPromptTile / 4; k4 += Gm::kAux) {
-            const int key = t * kPromptTile + k4 * 4 + (lane >> 3);
-            const bool dead = key >= un.L;
-            if (!__any_sync(0xffffffffu, key > un.pos0 ||
-                                             (p.window > 0 && key <= last - p.window)))
-              continue;
+          for (int t = un.t0; t < un.t1 && ok; ++t, ++tiles) {
 #pragma unroll
-            for (int h = 0; h < Gm::kHalves; ++h) {
-              uint4* at = reinterpret_cast<uint4*>(tile + h * Gm::kHalfBytes + k4 * 512) + lane;
-              const uint4 w = *at;
-              if (dead) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
-                         nonfinite_bf16x2(w.w)) {
-                found = true;
-                *at = make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y), finite_bf16x2(w.z),
-                                 finite_bf16x2(w.w));
+            for (int kv = 0; kv < 2; ++kv, ++item) {
+              const int rs = item % Gm::kRawStages;
+              const int st = tiles % (kv ? Gm::kVStages : Gm::kKStages);
+              const uint32_t use = static_cast<uint32_t>(tiles / (kv ? Gm::kVStages
+                                                                     : Gm::kKStages));
+              wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u);
+              wait(kv ? &ms.v_empty[st] : &ms.k_empty[st], (use & 1u) ^ 1u);
+              if (!ok) break;
+              const uint8_t* raw = smem + Gm::kRawOff + rs * Gm::kRawBytes;
+              if (kv)
+                found |= widen_values<D>(smem + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux,
+                                         Gm::kAux, prompt_masked(p, t, un.pos0, last),
+                                         un.L - t * kPromptTile);
+              else
+                widen_keys<D>(smem + Gm::kKOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux);
+              tc::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(kv ? &ms.v_full[st] : &ms.k_full[st]);
+                mbar_arrive(&ms.raw_empty[rs]);
               }
             }
           }
-          if (found) *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.checked);
+        } else {
+          // A TMA box of 16 keys costs its unit about 70 cycles, whatever the bytes, and K's are
+          // as many as it can take; V comes by 16-byte copies, rows behind the context as zeros.
+          constexpr int kRowChunks = D / 8;            // 16-byte chunks of a row
+          constexpr int kRows = 32 / kRowChunks;       // rows of one warp-wide copy
+          const int c = lane % kRowChunks, r = lane / kRowChunks;
+          PromptPages pages;
+          pages.begin(p, un, lane);
+          // a tile's copies have landed: what some query row must not see, made finite
+          auto finish = [&](int t, int st) {
+            if (prompt_masked(p, t, un.pos0, last)) {
+              uint8_t* tile = smem + Gm::kVOff + st * Gm::kTileBytes;
+              for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
+#pragma unroll 4
+                for (int i = 0; i < kBlockSize / kRows; ++i) {
+                  const int key = pg * kBlockSize + i * kRows + r;
+                  uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * Gm::kHalfBytes +
+                                                       key * 128 + (((c & 7) ^ (key & 7)) << 4));
+                  const uint4 w = *at;
+                  if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
+                      nonfinite_bf16x2(w.w)) {
+                    found = true;
+                    *at = make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y), finite_bf16x2(w.z),
+                                     finite_bf16x2(w.w));
+                  }
+                }
+              }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.v_full[st]);
+          };
+          bool pending = false;
+          for (int t = un.t0; t < un.t1; ++t, ++tiles) {
+            const int st = tiles % Gm::kVStages, before = (tiles + Gm::kVStages - 1) % Gm::kVStages;
+            const uint32_t parity = (static_cast<uint32_t>(tiles / Gm::kVStages) & 1u) ^ 1u;
+            if (!__all_sync(0xffffffffu, tc::mbar_test(&ms.v_empty[st], parity))) {
+              if (pending) {                           // nothing to issue: the last tile first
+                cp_async_wait<0>();
+                finish(t - 1, before);
+                pending = false;
+              }
+              wait(&ms.v_empty[st], parity);
+              if (!ok) break;
+            }
+            const int at = pages.lane_of(p, t, lane);
+            const uint32_t tile = smem_u32(smem + Gm::kVOff + st * Gm::kTileBytes) +
+                                  (c >> 3) * Gm::kHalfBytes;
+#pragma unroll
+            for (int j = 0; j < Gm::kPages / Gm::kAux; ++j) {
+              const int pg = j * Gm::kAux + aux;
+              const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
+              const bool there = id != p.num_blocks;
+              const uint8_t* src = static_cast<const uint8_t*>(p.v_pool) +
+                                   (static_cast<size_t>(there ? id : 0) * p.Hkv + un.head) *
+                                       (kBlockSize * D * 2) + lane * 16;
+#pragma unroll
+              for (int i = 0; i < kBlockSize / kRows; ++i) {
+                const int key = pg * kBlockSize + i * kRows + r;
+                cp_async_16(tile + key * 128 + (((c & 7) ^ (key & 7)) << 4), src + i * 512,
+                            there && t * kPromptTile + key < un.L ? 16u : 0u);
+              }
+            }
+            cp_async_commit();
+            if (pending) {
+              cp_async_wait<1>();
+              finish(t - 1, before);
+            }
+            pending = true;
+          }
+          cp_async_wait<0>();
+          if (pending && ok) finish(un.t1 - 1, (tiles + Gm::kVStages - 1) % Gm::kVStages);
         }
+        if (!ok) break;
+        if (found) *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&ms.unit_checked[ui & 1]);
           mbar_arrive(&ms.unit_empty[ui & 1]);
         }
-        item0 += 2 * (un.t1 - un.t0);
       }
     }
   } else {
@@ -817,97 +876,136 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       }
       float ref = -CUDART_INF_F;                        // reference, log2 units
       float sum = 0.f;
+      bool steady = false;                              // a reference that may stay
       for (int t = sub.a; t < sub.e; ++t) {
         wait(&ms.s_full[s], n_s++ & 1u);
         tc::fence_after_sync();
         uint32_t x[4][32];
+        auto load = [&](int n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tc::tmem_ld32(ts + i * 32, x[i]);
-        tc::tmem_wait_ld();
+          for (int i = 0; i < 4; ++i)
+            if (i < n) tc::tmem_ld32(ts + i * 32, x[i]);
+          tc::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait_regs(x[i]);
-        // a score's factor is applied with the reference's subtraction, in one rounding; with
-        // a factor that is not positive, or references that leave no bits behind the point,
-        // it comes first
+          for (int i = 0; i < 4; ++i)
+            if (i < n) tmem_wait_regs(x[i]);
+        };
+        load(4);
+        // A score's factor is applied with the reference's subtraction, in one rounding; with a
+        // factor that is not positive, or references that leave no bits behind the point, it
+        // comes first.
         float cc = c;
-        if (!(c > 0.f)) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * c);
-          cc = 1.f;
-        }
-        if (prompt_masked(p, t, sub.first, sub.first + sub.n - 1)) {
-          const int hi = pos - t * kPromptTile;         // columns lo < i <= hi are visible
-          const int lo = p.window > 0 ? hi - p.window : -1;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > hi || i <= lo) x[i / 32][i % 32] = __float_as_uint(-CUDART_INF_F);
-        }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = fmaxf(__uint_as_float(x[i][0]), __uint_as_float(x[i][1]));
-#pragma unroll
-          for (int k = 2; k < 32; k += 2)
-            mx[i] = max3(mx[i], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
-        }
-        float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * cc;
-        if (__any_sync(0xffffffffu, fabsf(m) > 67108864.f && fabsf(m) < CUDART_INF_F) &&
-            cc != 1.f) {
+        auto multiply = [&]() {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * cc);
           cc = 1.f;
-        }
-        const bool move = m > ref + 8.f;                // the first finite score always moves it
-        if (__any_sync(0xffffffffu, move)) {
-          const float to_ref = move ? m : ref;
-          const float f = move ? hw_exp2(ref - m) : 1.f;
-          ref = to_ref;
-          sum *= f;
-          if (t > sub.a) {
-#pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t o[16];
-              tc::tmem_ld16(to + i * 16, o);
-              tc::tmem_wait_ld();
-              tmem_wait_regs(o);
+        };
+        const bool masked = prompt_masked(p, t, sub.first, sub.first + sub.n - 1);
+        bool look = masked || !steady;                  // for the maximum
+        if (look) {
+          if (!(c > 0.f)) multiply();
+          if (masked) {
+            const int hi = pos - t * kPromptTile;       // columns lo < i <= hi are visible
+            const int lo = p.window > 0 ? hi - p.window : -1;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tc::tmem_st16(to + i * 16, o);
-            }
+            for (int i = 0; i < 128; ++i)
+              if (i > hi || i <= lo) x[i / 32][i % 32] = __float_as_uint(-CUDART_INF_F);
           }
         }
-        const float off = ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref;
-        const uint64_t cc2 = pack_f32x2(cc, cc), off2 = pack_f32x2(off, off);
-        uint64_t part[2] = {0ull, 0ull};
+        uint64_t part[4], cc2, off2;
+        // of keys 32 i .. 32 i + 31, in place of their scores: one kind of instruction at a time,
+        // which leaves each result time to arrive
+        auto weights = [&](int i, uint32_t (&w)[16]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[16];
+          for (int k = 0; k < 32; k += 2) {
+            const uint64_t y = fma_f32x2(
+                pack_f32x2(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1])), cc2, off2);
+            x[i][k] = static_cast<uint32_t>(y);
+            x[i][k + 1] = static_cast<uint32_t>(y >> 32);
+          }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(x[i][2 * k]),
-                                                    __uint_as_float(x[i][2 * k + 1])),
-                                         cc2, off2);
-            const float e0 = hw_exp2(__uint_as_float(static_cast<uint32_t>(y)));
-            const float e1 = hw_exp2(__uint_as_float(static_cast<uint32_t>(y >> 32)));
-            part[k & 1] = add_f32x2(part[k & 1], pack_f32x2(e0, e1));
+          for (int k = 0; k < 32; ++k)
+            x[i][k] = __float_as_uint(hw_exp2(__uint_as_float(x[i][k])));
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float e0 = __uint_as_float(x[i][k]), e1 = __uint_as_float(x[i][k + 1]);
+            part[k / 2 & 3] = add_f32x2(part[k / 2 & 3], pack_f32x2(e0, e1));
             if constexpr (KV8)
-              w[k] = half2_bits(__floats2half2_rn(e0, e1));
+              w[k / 2] = half2_bits(__floats2half2_rn(e0, e1));
             else
-              w[k] = pack_bf16x2_rn(e0, e1);
+              w[k / 2] = pack_bf16x2_rn(e0, e1);
           }
-          if (i == 2) {                                 // by now the first two have arrived
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.p_half[s]);
+        };
+        auto largest = [&](int i) {
+          float m[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            m[k] = fmaxf(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 4]));
+#pragma unroll
+          for (int k = 8; k < 32; k += 8)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+              m[a] = max3(m[a], __uint_as_float(x[i][k + a]), __uint_as_float(x[i][k + a + 4]));
+          return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+        };
+        auto total = [&]() {
+          const uint64_t y = add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3]));
+          return __uint_as_float(static_cast<uint32_t>(y)) +
+                 __uint_as_float(static_cast<uint32_t>(y >> 32));
+        };
+        uint32_t w[16];
+        while (true) {
+          if (look) {
+            float m = fmaxf(max3(largest(0), largest(1), largest(2)), largest(3)) * cc;
+            if (__any_sync(0xffffffffu, fabsf(m) > kPromptExact && fabsf(m) < CUDART_INF_F)) {
+              if (cc != 1.f) multiply();
+              m = fmaxf(max3(largest(0), largest(1), largest(2)), largest(3));
+            }
+            const bool move = m > ref;                  // the first finite score always moves it
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? hw_exp2(ref - m) : 1.f;
+              ref = move ? m : ref;
+              sum *= f;
+              if (t > sub.a) {
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                  uint32_t o[16];
+                  tc::tmem_ld16(to + i * 16, o);
+                  tc::tmem_wait_ld();
+                  tmem_wait_regs(o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tc::tmem_st16(to + i * 16, o);
+                }
+              }
+            }
+            steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
           }
-          tc::tmem_st16(ts + i * 16, w);
+          const float off = ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref;
+          cc2 = pack_f32x2(cc, cc);
+          off2 = pack_f32x2(off, off);
+          part[0] = part[1] = part[2] = part[3] = 0ull;
+          weights(0, w);
+          tc::tmem_st16(ts + prompt_weight_col(0), w);
+          // the last keys' largest, so that nothing is left to look at behind the test
+          const float behind = fmaf(largest(3), cc, off);
+          weights(1, w);
+          tc::tmem_st16(ts + prompt_weight_col(1), w);
+          weights(2, w);
+          if (look || __all_sync(0xffffffffu, total() <= kPromptLimit && behind <= 15.f)) break;
+          look = true;
+          load(3);
         }
-        part[0] = add_f32x2(part[0], part[1]);
-        sum += __uint_as_float(static_cast<uint32_t>(part[0])) +
-               __uint_as_float(static_cast<uint32_t>(part[0] >> 32));
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_half[s]);
+        tc::tmem_st16(ts + prompt_weight_col(2), w);
+        weights(3, w);
+        tc::tmem_st16(ts + prompt_weight_col(3), w);
+        sum += total();
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
