@@ -89,10 +89,6 @@ struct PromptGeo {
 // does not either), which an f16 holds; a reference is one of rounded products up to 2^26.
 constexpr float kPromptLimit = 32768.f, kPromptExact = 67108864.f;
 
-// Columns of S that the weights of keys 32 i .. 32 i + 31 take: the first two quarters those of
-// the last scores, so that the first three quarters of S can be read again.
-__host__ __device__ constexpr int prompt_weight_col(int i) { return i < 2 ? 96 + 16 * i : 32 + 16 * i; }
-
 // One unit of work.
 struct PromptUnit {
   int b;                 // sequence, -1 behind the last unit
@@ -331,6 +327,98 @@ template <int kRegs>
 __device__ __forceinline__ void regs_fewer() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
+
+// A row's 128 scores of a K/V tile in one thread, and the weights that take their place.
+template <bool KV8>
+struct PromptScores {
+  uint32_t x[4][32];
+  uint32_t w[4][16];
+  uint64_t part[4], factor, offset;
+
+  __device__ __forceinline__ float score(int i) const { return __uint_as_float(x[i / 32][i % 32]); }
+  __device__ __forceinline__ void load(uint32_t taddr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tc::tmem_ld32(taddr + i * 32, x[i]);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_wait_regs(x[i]);
+  }
+  __device__ __forceinline__ void multiply(float c) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) x[i / 32][i % 32] = __float_as_uint(score(i) * c);
+  }
+  __device__ __forceinline__ void mask(int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i)
+      if (i > hi || i <= lo) x[i / 32][i % 32] = __float_as_uint(-CUDART_INF_F);
+  }
+  __device__ __forceinline__ float largest() const {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(score(2 * k), score(2 * k + 1));
+#pragma unroll
+    for (int k = 8; k < 128; k += 8)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) m[a] = max3(m[a], score(k + 2 * a), score(k + 2 * a + 1));
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+  }
+  __device__ __forceinline__ void begin(float c, float off) {
+    factor = pack_f32x2(c, c);
+    offset = pack_f32x2(off, off);
+    part[0] = part[1] = part[2] = part[3] = 0ull;
+  }
+  // Weights 2^(factor x + offset) of the pairs of keys [FROM, TO), packed into w.  Each step
+  // takes one pair through each of three stages, so that the exponentials (four cycles each)
+  // run beside the rest; also(k) is an instruction or two more for step k.
+  template <int FROM, int TO, typename Also>
+  __device__ __forceinline__ void weights(Also also) {
+    constexpr int kExp = 3, kPack = 8;                  // steps behind the argument
+#pragma unroll
+    for (int k = FROM; k < TO + kPack; ++k) {
+      if (k < TO) {
+        uint32_t* v = &x[k / 16][k % 16 * 2];
+        const uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                     factor, offset);
+        v[0] = static_cast<uint32_t>(y);
+        v[1] = static_cast<uint32_t>(y >> 32);
+        also(k);
+      }
+      if (k - kExp >= FROM && k - kExp < TO) {
+        const int j = k - kExp;
+        uint32_t* v = &x[j / 16][j % 16 * 2];
+        v[0] = __float_as_uint(hw_exp2(__uint_as_float(v[0])));
+        v[1] = __float_as_uint(hw_exp2(__uint_as_float(v[1])));
+      }
+      if (k - kPack >= FROM) {
+        const int j = k - kPack;
+        const float e0 = score(2 * j), e1 = score(2 * j + 1);
+        part[j & 3] = add_f32x2(part[j & 3], pack_f32x2(e0, e1));
+        if constexpr (KV8)
+          w[j / 16][j % 16] = half2_bits(__floats2half2_rn(e0, e1));
+        else
+          w[j / 16][j % 16] = pack_bf16x2_rn(e0, e1);
+      }
+    }
+  }
+  __device__ __forceinline__ float total() const {
+    const uint64_t y = add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3]));
+    return __uint_as_float(static_cast<uint32_t>(y)) + __uint_as_float(static_cast<uint32_t>(y >> 32));
+  }
+  // The weights over the scores, the first half of the keys announced once the third quarter is
+  // computed; the second half is stored, not yet complete.
+  __device__ __forceinline__ void finish(uint32_t taddr, uint64_t* half, int lane) {
+    tc::tmem_st16(taddr, w[0]);
+    tc::tmem_st16(taddr + 16, w[1]);
+    weights<32, 48>([](int) {});
+    tc::tmem_wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(half);
+    tc::tmem_st16(taddr + 32, w[2]);
+    weights<48, 64>([](int) {});
+    tc::tmem_st16(taddr + 48, w[3]);
+  }
+};
 
 // A V element for the rows that see it, from the pool.
 template <int D, bool KV8>
@@ -678,7 +766,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                   const uint32_t off =
                       (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
                   lead_mma_ts(leader, tm + Gm::kO + s * D,
-                              tm + s * kPromptTile + prompt_weight_col(k / 2) + k % 2 * 8,
+                              tm + s * kPromptTile + k * 8,
                               desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
                 }
                 if (half && t + 1 == sub[s].e) lead_commit(leader, &ms.o_full[s]);
@@ -880,132 +968,71 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       for (int t = sub.a; t < sub.e; ++t) {
         wait(&ms.s_full[s], n_s++ & 1u);
         tc::fence_after_sync();
-        uint32_t x[4][32];
-        auto load = [&](int n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < n) tc::tmem_ld32(ts + i * 32, x[i]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < n) tmem_wait_regs(x[i]);
-        };
-        load(4);
-        // A score's factor is applied with the reference's subtraction, in one rounding; with a
-        // factor that is not positive, or references that leave no bits behind the point, it
-        // comes first.
-        float cc = c;
-        auto multiply = [&]() {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * cc);
-          cc = 1.f;
-        };
         const bool masked = prompt_masked(p, t, sub.first, sub.first + sub.n - 1);
-        bool look = masked || !steady;                  // for the maximum
-        if (look) {
-          if (!(c > 0.f)) multiply();
+        bool done = false;
+        if (steady && !masked) {
+          PromptScores<KV8> sc;
+          sc.load(ts);
+          sc.begin(c, Gm::kShift - ref);
+          // beside the first half of the weights the largest of the other half's scores, so that
+          // nothing is left to look at behind the test
+          float most[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+          sc.template weights<0, 32>([&](int k) {
+            most[k & 3] = max3(most[k & 3], sc.score(64 + 2 * k), sc.score(65 + 2 * k));
+          });
+          const float m = fmaxf(max3(most[0], most[1], most[2]), most[3]);
+          const bool fine = sc.total() <= kPromptLimit && fmaf(m, c, Gm::kShift - ref) <= 15.f;
+          if (__all_sync(0xffffffffu, fine)) {
+            sc.finish(ts, &ms.p_half[s], lane);
+            sum += sc.total();
+            done = true;
+          }
+        }
+        if (!done) {
+          PromptScores<KV8> sc;
+          sc.load(ts);
+          // A score's factor is applied with the reference's subtraction, in one rounding; with
+          // a factor that is not positive, or references that leave no bits behind the point, it
+          // comes first.
+          float cc = c;
+          if (!(c > 0.f)) {
+            sc.multiply(c);
+            cc = 1.f;
+          }
           if (masked) {
             const int hi = pos - t * kPromptTile;       // columns lo < i <= hi are visible
-            const int lo = p.window > 0 ? hi - p.window : -1;
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > hi || i <= lo) x[i / 32][i % 32] = __float_as_uint(-CUDART_INF_F);
+            sc.mask(p.window > 0 ? hi - p.window : -1, hi);
           }
-        }
-        uint64_t part[4], cc2, off2;
-        // of keys 32 i .. 32 i + 31, in place of their scores: one kind of instruction at a time,
-        // which leaves each result time to arrive
-        auto weights = [&](int i, uint32_t (&w)[16]) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const uint64_t y = fma_f32x2(
-                pack_f32x2(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1])), cc2, off2);
-            x[i][k] = static_cast<uint32_t>(y);
-            x[i][k + 1] = static_cast<uint32_t>(y >> 32);
+          float m = sc.largest() * cc;
+          if (__any_sync(0xffffffffu, fabsf(m) > kPromptExact && fabsf(m) < CUDART_INF_F)) {
+            sc.multiply(cc);
+            cc = 1.f;
+            m = sc.largest();
           }
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            x[i][k] = __float_as_uint(hw_exp2(__uint_as_float(x[i][k])));
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float e0 = __uint_as_float(x[i][k]), e1 = __uint_as_float(x[i][k + 1]);
-            part[k / 2 & 3] = add_f32x2(part[k / 2 & 3], pack_f32x2(e0, e1));
-            if constexpr (KV8)
-              w[k / 2] = half2_bits(__floats2half2_rn(e0, e1));
-            else
-              w[k / 2] = pack_bf16x2_rn(e0, e1);
-          }
-        };
-        auto largest = [&](int i) {
-          float m[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            m[k] = fmaxf(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 4]));
-#pragma unroll
-          for (int k = 8; k < 32; k += 8)
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-              m[a] = max3(m[a], __uint_as_float(x[i][k + a]), __uint_as_float(x[i][k + a + 4]));
-          return fmaxf(max3(m[0], m[1], m[2]), m[3]);
-        };
-        auto total = [&]() {
-          const uint64_t y = add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3]));
-          return __uint_as_float(static_cast<uint32_t>(y)) +
-                 __uint_as_float(static_cast<uint32_t>(y >> 32));
-        };
-        uint32_t w[16];
-        while (true) {
-          if (look) {
-            float m = fmaxf(max3(largest(0), largest(1), largest(2)), largest(3)) * cc;
-            if (__any_sync(0xffffffffu, fabsf(m) > kPromptExact && fabsf(m) < CUDART_INF_F)) {
-              if (cc != 1.f) multiply();
-              m = fmaxf(max3(largest(0), largest(1), largest(2)), largest(3));
-            }
-            const bool move = m > ref;                  // the first finite score always moves it
-            if (__any_sync(0xffffffffu, move)) {
-              const float f = move ? hw_exp2(ref - m) : 1.f;
-              ref = move ? m : ref;
-              sum *= f;
-              if (t > sub.a) {
+          const bool move = m > ref;                    // the first finite score always moves it
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? hw_exp2(ref - m) : 1.f;
+            ref = move ? m : ref;
+            sum *= f;
+            if (t > sub.a) {
 #pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
-                  uint32_t o[16];
-                  tc::tmem_ld16(to + i * 16, o);
-                  tc::tmem_wait_ld();
-                  tmem_wait_regs(o);
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t o[16];
+                tc::tmem_ld16(to + i * 16, o);
+                tc::tmem_wait_ld();
+                tmem_wait_regs(o);
 #pragma unroll
-                  for (int k = 0; k < 16; ++k)
-                    o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                  tc::tmem_st16(to + i * 16, o);
-                }
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tc::tmem_st16(to + i * 16, o);
               }
             }
-            steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
           }
-          const float off = ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref;
-          cc2 = pack_f32x2(cc, cc);
-          off2 = pack_f32x2(off, off);
-          part[0] = part[1] = part[2] = part[3] = 0ull;
-          weights(0, w);
-          tc::tmem_st16(ts + prompt_weight_col(0), w);
-          // the last keys' largest, so that nothing is left to look at behind the test
-          const float behind = fmaf(largest(3), cc, off);
-          weights(1, w);
-          tc::tmem_st16(ts + prompt_weight_col(1), w);
-          weights(2, w);
-          if (look || __all_sync(0xffffffffu, total() <= kPromptLimit && behind <= 15.f)) break;
-          look = true;
-          load(3);
+          steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
+          sc.begin(cc, ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref);
+          sc.template weights<0, 32>([](int) {});
+          sc.finish(ts, &ms.p_half[s], lane);
+          sum += sc.total();
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.p_half[s]);
-        tc::tmem_st16(ts + prompt_weight_col(2), w);
-        weights(3, w);
-        tc::tmem_st16(ts + prompt_weight_col(3), w);
-        sum += total();
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
