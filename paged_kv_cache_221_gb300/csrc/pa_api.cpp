@@ -180,7 +180,8 @@ struct PromptPlan {
   int split = 1;          // K/V tiles per partition
   int max_parts = 1;
   long long units = 0;    // (pair, kv head, partition) at most
-  size_t bytes = 0, off_ml = 0;
+  bool counted = false;   // CTAs take units as they come free
+  size_t bytes = 0, off_ml = 0, off_counter = 0;
 };
 
 PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int max_ctx,
@@ -199,7 +200,7 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
     pl.split = std::min(tiles, partition_size / kPromptTile);
   } else if (scratch) {
     const long long pairs = slots * hkv;
-    if (pairs < 152) pl.split = std::max(4, ceil_div(tiles * pairs, 304));
+    if (pairs < 152) pl.split = std::max(4, ceil_div(tiles, std::max<long long>(1, 152 / pairs)));
   }
   pl.split = std::min(pl.split, tiles);
   pl.max_parts = ceil_div(tiles, pl.split);
@@ -207,7 +208,11 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
   if (pl.max_parts > 1) {
     const size_t rows = static_cast<size_t>(num_tokens) * hq * pl.max_parts;
     pl.off_ml = round256(rows * head_dim * sizeof(float));
-    pl.bytes = pl.off_ml + round256(rows * sizeof(float2));
+    pl.bytes = pl.off_counter = pl.off_ml + round256(rows * sizeof(float2));
+  }
+  if (scratch && pl.units > 304) {
+    pl.counted = true;
+    pl.bytes += 256;
   }
   return pl;
 }
@@ -869,10 +874,13 @@ pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, con
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.query_starts = query_starts;
-  if (plan.bytes > 0) {
+  if (plan.max_parts > 1) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.off_ml);
   }
+  if (plan.counted)
+    p.counter = reinterpret_cast<int*>(static_cast<char*>(workspace) + plan.off_counter);
+  p.num_units = static_cast<int>(plan.units);
   p.mbs = max_blocks_per_seq;
   p.max_ctx = max_context_len;
   p.num_seqs = num_seqs;

@@ -141,6 +141,9 @@ struct PromptParams {
   int num_slots;                  // bound on the pairs of tiles: num_rows / (2 sub_tokens) + B
   int split;                      // K/V tiles per partition
   int max_parts;                  // partitions of a pair of tiles at most
+  int num_units;                  // units of work at most
+  int* counter;                   // scratch: units that CTAs went on to, or nullptr (every
+                                  //   gridDim.x-th unit)
   float scale_log2;
   int window;                     // 0 = none
   unsigned long long timeout_ns;

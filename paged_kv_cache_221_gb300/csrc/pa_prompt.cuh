@@ -14,13 +14,13 @@
 // partition of its keys, so that each K/V tile that a CTA loads serves 256 rows and one
 // tile's products run while the other tile's weights are computed.
 //
-// Roles of a CTA (persistent, one per SM):
+// Roles of a CTA (one per SM, which goes on to further units):
 //   warps 0-3, 4-7  softmax of the first, the second tile: thread = row.  A tile's weights are
 //                   taken with the reference of the last ones at once; only where their sum
 //                   shows one past 2^15, at the mask's border and at a unit's start is the
-//                   row's maximum looked for, which then becomes the reference.  O is rescaled
-//                   in tensor memory, which no product is using at that time: S of the next
-//                   keys is issued behind P . V of the last ones.
+//                   row's maximum looked for, which then becomes the reference if it is far
+//                   above it.  O is then rescaled in tensor memory, which no product is using
+//                   at that time: S of the next keys is issued behind P . V of the last ones.
 //   warp 8          finds the units, loads Q and the K tiles by TMA, 16 keys per page box,
 //                   through the block table.
 //   warp 9          issues the MMAs: per K/V tile P.V (in two halves, the first while the last
@@ -47,6 +47,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "pa_pages.cuh"
 #include "pa_ptx.cuh"
@@ -79,7 +80,7 @@ struct PromptGeo {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 2 * kPromptTile;        // S tiles at 0 and 128, then O
   // registers per thread: launch, softmax warps, others
-  static constexpr int kRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
+  static constexpr int kRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
   static_assert(kAlloc <= 232448, "shared memory per block");
   static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs <=
                     kThreads * kRegs, "the split takes no more than the launch has");
@@ -88,6 +89,8 @@ struct PromptGeo {
 // Weights are taken with the present reference while none of them passes 2^15 (and their sum
 // does not either), which an f16 holds; a reference is one of rounded products up to 2^26.
 constexpr float kPromptLimit = 32768.f, kPromptExact = 67108864.f;
+
+constexpr int kPromptTries = 1 << 23;
 
 // One unit of work.
 struct PromptUnit {
@@ -108,7 +111,7 @@ struct PromptMisc {
   uint64_t v_full[Gm::kVStages], v_empty[Gm::kVStages];
   uint64_t raw_full[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
   uint64_t raw_empty[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];      // by tile of the pair
   uint64_t q_wide[2];                  // by record: the query rows are f16
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
   uint64_t unit_full[2], unit_empty[2], unit_checked[2]; // by record
@@ -186,40 +189,32 @@ __device__ __forceinline__ PromptSub prompt_sub(const PromptParams& p, const Pro
   return r;
 }
 
-// Block ids of a unit's pages for one warp: a batch of 32 (four tiles) in lane order, the next
-// one read ahead.  Pages behind the context's end and ids outside the pool (an error) become
-// num_blocks.
+// Block ids of a unit's pages for one warp: 32 (four tiles) in lane order, and the 32 behind
+// them.  Pages behind the context's end and ids outside the pool (an error) become num_blocks.
 struct PromptPages {
-  const int32_t* table;
-  int first, npages, end, ids, next;
+  int ids, next;
 
-  __device__ __forceinline__ int id(const PromptParams& p, int i) const {
-    int x = p.num_blocks;
-    if (i < npages) {
-      x = __ldg(table + i);
-      if (static_cast<unsigned>(x) >= static_cast<unsigned>(p.num_blocks)) {
-        if (i < end) atomicOr(&g_pa_err, kErrBounds);
-        x = p.num_blocks;
+  // The lane that holds the first page of tile t; tiles come in order.
+  __device__ __forceinline__ int lane_of(const PromptParams& p, const PromptUnit& un, int t,
+                                         int lane) {
+    constexpr int kPages = kPromptTile / kBlockSize;
+    const int at = (t - un.t0) * kPages & 31;
+    if (at == 0) {
+#pragma unroll 1
+      for (int read = t == un.t0 ? 0 : 32; read <= 32; read += 32) {
+        const int i = t * kPages + read + lane;
+        ids = next;
+        next = p.num_blocks;
+        if (i * kBlockSize < un.L && i < un.t1 * kPages) {
+          const int id = __ldg(p.block_tables + static_cast<size_t>(un.b) * p.mbs + i);
+          if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks))
+            next = id;
+          else
+            atomicOr(&g_pa_err, kErrBounds);
+        }
       }
     }
-    return x;
-  }
-  __device__ __forceinline__ void begin(const PromptParams& p, const PromptUnit& un, int lane) {
-    table = p.block_tables + static_cast<size_t>(un.b) * p.mbs;
-    npages = (un.L + kBlockSize - 1) / kBlockSize;
-    first = un.t0 * (kPromptTile / kBlockSize);
-    end = un.t1 * (kPromptTile / kBlockSize);
-    ids = id(p, first + lane);
-    next = id(p, first + 32 + lane);
-  }
-  // The lane that holds the first page of tile t; tiles come in order.
-  __device__ __forceinline__ int lane_of(const PromptParams& p, int t, int lane) {
-    const int i = t * (kPromptTile / kBlockSize) - first;
-    if (i > 0 && (i & 31) == 0) {
-      ids = next;
-      next = id(p, first + i + 32 + lane);
-    }
-    return i & 31;
+    return at;
   }
 };
 
@@ -238,6 +233,32 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Waits a limited number of tries, each of which sleeps a while.  There are many in the code of
+// a CTA's roles, which shares one instruction cache; so a role reports the timeout at its end.
+struct PromptWaits {
+  int tries = kPromptTries;             // 0 behind a wait that ran out
+
+  __device__ __forceinline__ bool ok() const { return tries != 0; }
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    int i = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+      if (++i > tries) {
+        tries = 0;
+        break;
+      }
+    }
+  }
+  // All lanes of the warp go on, or none.
+  __device__ __forceinline__ bool all_ok() {
+    tries = __all_sync(0xffffffffu, tries != 0) ? tries : 0;
+    return tries != 0;
+  }
+  __device__ __forceinline__ void report() const {
+    if (tries == 0 && (threadIdx.x & 31) == 0) atomicOr(&g_pa_err, kErrTimeout);
+  }
+};
+
 // One lane of the warp, the same at every call.
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
@@ -247,6 +268,11 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(yes));
   return yes != 0;
+}
+
+// A value that all lanes hold, in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+  return __reduce_max_sync(0xffffffffu, x);
 }
 
 // MMAs and commits of the lane with `leader` set, in code that the whole warp runs.
@@ -347,10 +373,19 @@ struct PromptScores {
 #pragma unroll
     for (int i = 0; i < 128; ++i) x[i / 32][i % 32] = __float_as_uint(score(i) * c);
   }
+  // Scores outside (lo, hi] to -inf, but for quarters that lie wholly inside for the warp.
   __device__ __forceinline__ void mask(int lo, int hi) {
 #pragma unroll
-    for (int i = 0; i < 128; ++i)
-      if (i > hi || i <= lo) x[i / 32][i % 32] = __float_as_uint(-CUDART_INF_F);
+    for (int i = 0; i < 4; ++i) {
+      const int a = max(0, lo + 1 - 32 * i), b = hi + 1 - 32 * i;     // columns [a, b) of it
+      const uint32_t in = (b <= 0 ? 0u : b >= 32 ? ~0u : (1u << b) - 1u) &
+                          (a >= 32 ? 0u : ~0u << a);
+      if (!__all_sync(0xffffffffu, in == ~0u)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (!(in >> k & 1u)) x[i][k] = __float_as_uint(-CUDART_INF_F);
+      }
+    }
   }
   __device__ __forceinline__ float largest() const {
     float m[4];
@@ -542,7 +577,7 @@ __device__ __forceinline__ int widen_query(uint8_t* tile, int row) {
 template <int D, bool KV8>
 __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                  const __grid_constant__ CUtensorMap tmv, const PromptParams p, int num_units) {
+                  const __grid_constant__ CUtensorMap tmv, const PromptParams p) {
   using Gm = PromptGeo<D, KV8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -550,7 +585,6 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
   auto& ms = *reinterpret_cast<PromptMisc<D, KV8>*>(smem + Gm::kMiscOff);
   static_assert(sizeof(PromptMisc<D, KV8>) <= Gm::kMiscBytes, "misc area");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned long long limit = p.timeout_ns;
 
   // ------------------------------------------------------------------ setup
   if (threadIdx.x == 0) {
@@ -566,9 +600,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       mbar_init(&ms.raw_full[i], 1);
       mbar_init(&ms.raw_empty[i], Gm::kAux);
     }
-    mbar_init(&ms.q_full, 1);
-    mbar_init(&ms.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.q_full[i], 1);
+      mbar_init(&ms.q_empty[i], 1);
       mbar_init(&ms.s_full[i], 1);
       mbar_init(&ms.p_half[i], 4);
       mbar_init(&ms.p_full[i], 4);
@@ -606,44 +640,50 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       constexpr int kRing = KV8 ? Gm::kRawStages : Gm::kKStages;
       uint64_t* full = KV8 ? ms.raw_full : ms.k_full;
       uint64_t* empty = KV8 ? ms.raw_empty : ms.k_empty;
-      bool aborted = false;
+      PromptWaits wait;
       int item = 0, ui = 0, u = blockIdx.x;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!aborted && !mbar_wait(bar, parity, limit)) aborted = true;
-        aborted = __any_sync(0xffffffffu, aborted);
+      uint32_t n_q[2] = {0, 0};                        // loads of each tile's query rows
+      // the unit behind the present one: the next that no CTA has begun, or every gridDim.x-th
+      auto claim = [&]() {
+        return p.counter == nullptr ? u + static_cast<int>(gridDim.x)
+               : lane == 0          ? atomicAdd(p.counter, 1) + static_cast<int>(gridDim.x)
+                                    : 0;
       };
+      int next = claim();
       while (true) {
         PromptUnit un;
         un.b = -1;
-        for (; u < num_units; u += gridDim.x) {
+        while (u < p.num_units) {
           bool bad;
-          if (prompt_unit(p, u, un, &bad)) break;
+          const bool found = prompt_unit(p, u, un, &bad);
+          u = __shfl_sync(0xffffffffu, next, 0);
+          if (u < p.num_units) next = claim();
+          if (found) break;
           if (bad && lane == 0) atomicOr(&g_pa_err, kErrBounds);
           un.b = -1;
         }
-        u += gridDim.x;
         wait(&ms.unit_empty[ui & 1], (static_cast<uint32_t>(ui >> 1) & 1u) ^ 1u);
-        if (aborted) break;
+        if (!wait.all_ok()) break;
         if (lane == 0) {
           ms.unit[ui & 1] = un;
           mbar_arrive(&ms.unit_full[ui & 1]);
         }
+        ++ui;
         if (un.b < 0) break;
         PromptPages pages;
-        pages.begin(p, un, lane);
-        for (int t = un.t0; t < un.t1 && !aborted; ++t) {
+        for (int t = un.t0; t < un.t1 && wait.ok(); ++t) {
           // a bf16 page is one box of 16 keys per half, an FP8 page one box; a row past the pool
           // is filled with zeros
           constexpr int kBoxes = KV8 ? 1 : Gm::kHalves;
           const int box = lane & (Gm::kPages * kBoxes - 1);
           const int pg = box / kBoxes, h = box % kBoxes;
-          const int at = pages.lane_of(p, t, lane);
+          const int at = pages.lane_of(p, un, t, lane);
           const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
           const int page = id * p.Hkv + (id == p.num_blocks ? 0 : un.head);
           for (int kv = 0; kv < (KV8 ? 2 : 1); ++kv, ++item) {
             const int st = item % kRing;
             wait(&empty[st], (static_cast<uint32_t>(item / kRing) & 1u) ^ 1u);
-            if (aborted) break;
+            if (!wait.all_ok()) break;
             if (lane == 0)
               mbar_arrive_expect_tx(&full[st], KV8 ? Gm::kRawBytes : Gm::kTileBytes);
             __syncwarp();
@@ -657,29 +697,34 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                             &tmk, &full[st], h * 64, page * kBlockSize);
             }
           }
-          if (t == un.t0 && !aborted) {
-            // the query rows, once the last unit's scores no longer need theirs
-            wait(&ms.q_empty, (static_cast<uint32_t>(ui) & 1u) ^ 1u);
-            if (aborted) break;
-            ++ui;
-            if (lane == 0) {
-              const int subs = un.ntok > p.sub_tokens ? 2 : 1;
-              mbar_arrive_expect_tx(&ms.q_full, static_cast<uint32_t>(subs * Gm::kHalves *
-                                                                      p.sub_tokens * p.G * 128));
-              for (int s = 0; s < subs; ++s)
+          if (t == un.t0) {
+            // the query rows, each tile's once its last unit's scores no longer need theirs
+            for (int s = 0; s < 2 && wait.ok(); ++s) {
+              const PromptSub sub = prompt_sub(p, un, s);
+              if (sub.a == sub.e) continue;
+              wait(&ms.q_empty[s], (n_q[s] & 1u) ^ 1u);
+              if (!wait.all_ok()) break;
+              ++n_q[s];
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&ms.q_full[s], static_cast<uint32_t>(
+                                                         Gm::kHalves * p.sub_tokens * p.G * 128));
                 for (int hh = 0; hh < Gm::kHalves; ++hh)
-                  tma_load_4d(smem + s * Gm::kTileBytes + hh * Gm::kHalfBytes, &tmq, &ms.q_full,
-                              hh * 64, 0, un.head, un.row0 + s * p.sub_tokens);
+                  tma_load_4d(smem + s * Gm::kTileBytes + hh * Gm::kHalfBytes, &tmq,
+                              &ms.q_full[s], hh * 64, 0, un.head, un.row0 + s * p.sub_tokens);
+              }
             }
           }
         }
-        if (aborted) break;
+        if (!wait.ok()) break;
       }
+      wait.report();
       // no copy may still be landing when the CTA ends
       if (lane == 0) {
+        wait.tries = kPromptTries;
         for (int i = max(0, item - kRing); i < item; ++i)
-          mbar_wait(&full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, limit);
-        if (ui > 0) mbar_wait(&ms.q_full, static_cast<uint32_t>(ui - 1) & 1u, limit);
+          wait(&full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u);
+        for (int s = 0; s < 2; ++s)
+          if (n_q[s] > 0) wait(&ms.q_full[s], (n_q[s] - 1) & 1u);
       }
       __syncwarp();
     } else if (warp == Gm::kSoftmaxWarps + 1) {
@@ -691,8 +736,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, !KV8>();
       const uint32_t kring = smem_u32(smem + Gm::kKOff), vring = smem_u32(smem + Gm::kVOff);
       const uint32_t qsm = smem_u32(smem);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      bool ok = true;
+      const uint32_t tm = uniform(tmem);
+      // Lanes agree to go on once per tile; a wait that ran out in between leaves wrong products
+      // behind an error that is reported.
+      PromptWaits wait;
       int kst = 0, vst = 0;                            // stage and phase of the next K, V tile
       uint32_t kph = 0, vph = 0;
       auto k_done = [&]() {
@@ -703,11 +750,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         }
       };
       uint32_t n_p[2] = {0, 0}, n_u[2] = {0, 0};       // P tiles taken, units of each tile begun
-      // Lanes agree on `ok` once per tile; a wait that ran out in between leaves wrong products
-      // behind an error that is already reported.
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, limit);
-      };
+      uint32_t n_q[2] = {0, 0};                        // query rows of each tile taken
       // S of tile s from the K tile at `lo`
       auto scores = [&](int s, uint32_t lo) {
         const uint32_t a = desc_lo(qsm + s * Gm::kTileBytes, 16);
@@ -719,9 +762,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         }
         lead_commit(leader, &ms.s_full[s]);
       };
-      for (int ui = 0; ok; ++ui) {
+      for (int ui = 0; wait.ok(); ++ui) {
         wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!wait.all_ok()) break;
         PromptUnit un = ms.unit[ui & 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
@@ -732,24 +775,14 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         un.pos0 = __shfl_sync(0xffffffffu, un.pos0, 0);
         un.ntok = __shfl_sync(0xffffffffu, un.ntok, 0);
         const PromptSub sub[2] = {prompt_sub(p, un, 0), prompt_sub(p, un, 1)};
-        if constexpr (KV8)
-          wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-        else
-          wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
-        wait(&ms.k_full[kst], kph);
-        __syncwarp();
-        tc::fence_after_sync();
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (sub[s].a <= un.t0 && un.t0 < sub[s].e)
-            scores(s, desc_lo(kring + kst * Gm::kTileBytes, 16));
-        k_done();
-        if (un.t0 + 1 == un.t1) lead_commit(leader, &ms.q_empty);
-        for (int t = un.t0; t < un.t1; ++t) {
+        if constexpr (KV8) wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+        // P.V of K/V tile t, then S of the next
+        for (int t = un.t0 - 1; t < un.t1; ++t) {
           const bool more = t + 1 < un.t1;
-          const uint32_t vlo = desc_lo(vring + vst * Gm::kTileBytes, KV8 ? 16 : Gm::kHalfBytes);
-          const uint32_t klo = desc_lo(kring + kst * Gm::kTileBytes, 16);
-          wait(&ms.v_full[vst], vph);
+          const uint32_t vlo =
+              uniform(desc_lo(vring + vst * Gm::kTileBytes, KV8 ? 16 : Gm::kHalfBytes));
+          const uint32_t klo = uniform(desc_lo(kring + kst * Gm::kTileBytes, 16));
+          if (t >= un.t0) wait(&ms.v_full[vst], vph);
           bool k_here = false;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
@@ -765,57 +798,61 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                   const int k = half * (kPromptTile / 32) + i;
                   const uint32_t off =
                       (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
-                  lead_mma_ts(leader, tm + Gm::kO + s * D,
-                              tm + s * kPromptTile + k * 8,
+                  lead_mma_ts(leader, tm + Gm::kO + s * D, tm + s * kPromptTile + k * 8,
                               desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
                 }
-                if (half && t + 1 == sub[s].e) lead_commit(leader, &ms.o_full[s]);
               }
+              if (t + 1 == sub[s].e) lead_commit(leader, &ms.o_full[s]);
               ++n_p[s];
             }
             if (sub[s].a <= t + 1 && t + 1 < sub[s].e) {
               if (!k_here) wait(&ms.k_full[kst], kph);
               k_here = true;
+              if (!KV8 && t + 1 == sub[s].a) wait(&ms.q_full[s], n_q[s]++ & 1u);
               __syncwarp();
               tc::fence_after_sync();
               scores(s, klo);
+              if (t + 2 == sub[s].e) lead_commit(leader, &ms.q_empty[s]);
             }
           }
-          lead_commit(leader, &ms.v_empty[vst]);
-          if (++vst == Gm::kVStages) {
-            vst = 0;
-            vph ^= 1u;
+          if (t >= un.t0) {
+            lead_commit(leader, &ms.v_empty[vst]);
+            if (++vst == Gm::kVStages) {
+              vst = 0;
+              vph ^= 1u;
+            }
           }
           if (more) k_done();
-          if (t + 2 == un.t1) lead_commit(leader, &ms.q_empty);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (!wait.all_ok()) break;
         }
       }
       // every MMA has completed before the CTA gives its tensor memory back
       __syncwarp();
       lead_commit(leader, &ms.fin);
-      mbar_wait(&ms.fin, 0, limit);
+      wait.report();
+      wait.tries = kPromptTries;
+      wait(&ms.fin, 0);
       __syncwarp();
     } else {
       // -------------------------------------------------------------- V, or FP8 tiles widened
       const int aux = warp - Gm::kSoftmaxWarps - 2;
-      bool ok = true;
+      PromptWaits wait;
       int item = 0, tiles = 0;                         // FP8 tiles, V tiles so far
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, limit)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-      };
-      for (int ui = 0; ok; ++ui) {
+      uint32_t n_q[2] = {0, 0};
+      for (int ui = 0; wait.ok(); ++ui) {
         wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-        if (!ok) break;
+        if (!wait.all_ok()) break;
         const PromptUnit un = ms.unit[ui & 1];
         if (un.b < 0) break;
         const int last = un.pos0 + un.ntok - 1;
         bool found = false;
         if constexpr (KV8) {
-          wait(&ms.q_full, static_cast<uint32_t>(ui) & 1u);
-          if (!ok) break;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const PromptSub sub = prompt_sub(p, un, s);
+            if (sub.a < sub.e) wait(&ms.q_full[s], n_q[s]++ & 1u);
+          }
+          if (!wait.all_ok()) break;
           const int rows = p.sub_tokens * p.G;
           for (int i = aux * 32 + lane; i < 2 * kPromptTile; i += Gm::kAux * 32) {
             const int s = i / kPromptTile, r = i % kPromptTile;
@@ -826,7 +863,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms.q_wide[ui & 1]);
-          for (int t = un.t0; t < un.t1 && ok; ++t, ++tiles) {
+          for (int t = un.t0; t < un.t1 && wait.ok(); ++t, ++tiles) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int rs = item % Gm::kRawStages;
@@ -835,7 +872,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                                                                      : Gm::kKStages));
               wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u);
               wait(kv ? &ms.v_empty[st] : &ms.k_empty[st], (use & 1u) ^ 1u);
-              if (!ok) break;
+              if (!wait.all_ok()) break;
               const uint8_t* raw = smem + Gm::kRawOff + rs * Gm::kRawBytes;
               if (kv)
                 found |= widen_values<D>(smem + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux,
@@ -858,11 +895,11 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           constexpr int kRows = 32 / kRowChunks;       // rows of one warp-wide copy
           const int c = lane % kRowChunks, r = lane / kRowChunks;
           PromptPages pages;
-          pages.begin(p, un, lane);
           // a tile's copies have landed: what some query row must not see, made finite
           auto finish = [&](int t, int st) {
             if (prompt_masked(p, t, un.pos0, last)) {
               uint8_t* tile = smem + Gm::kVOff + st * Gm::kTileBytes;
+#pragma unroll 1
               for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
 #pragma unroll 4
                 for (int i = 0; i < kBlockSize / kRows; ++i) {
@@ -883,48 +920,52 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.v_full[st]);
           };
-          bool pending = false;
-          for (int t = un.t0; t < un.t1; ++t, ++tiles) {
-            const int st = tiles % Gm::kVStages, before = (tiles + Gm::kVStages - 1) % Gm::kVStages;
-            const uint32_t parity = (static_cast<uint32_t>(tiles / Gm::kVStages) & 1u) ^ 1u;
-            if (!__all_sync(0xffffffffu, tc::mbar_test(&ms.v_empty[st], parity))) {
-              if (pending) {                           // nothing to issue: the last tile first
-                cp_async_wait<0>();
-                finish(t - 1, before);
-                pending = false;
+          int issued = un.t0;
+          for (int done = un.t0; done < un.t1;) {
+            // a tile ahead of the one to finish where its stage is free, or there is none
+            if (issued < un.t1 && issued - done < Gm::kVStages) {
+              const int st = tiles % Gm::kVStages;
+              const uint32_t parity = (static_cast<uint32_t>(tiles / Gm::kVStages) & 1u) ^ 1u;
+              bool free = __all_sync(0xffffffffu, tc::mbar_test(&ms.v_empty[st], parity));
+              if (!free && issued == done) {
+                wait(&ms.v_empty[st], parity);
+                if (!wait.all_ok()) break;
+                free = true;
               }
-              wait(&ms.v_empty[st], parity);
-              if (!ok) break;
-            }
-            const int at = pages.lane_of(p, t, lane);
-            const uint32_t tile = smem_u32(smem + Gm::kVOff + st * Gm::kTileBytes) +
-                                  (c >> 3) * Gm::kHalfBytes;
+              if (free) {
+                const int at = pages.lane_of(p, un, issued, lane);
+                const uint32_t tile = smem_u32(smem + Gm::kVOff + st * Gm::kTileBytes) +
+                                      (c >> 3) * Gm::kHalfBytes;
+#pragma unroll 1
+                for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
+                  const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
+                  const int end = id == p.num_blocks ? 0 : un.L - issued * kPromptTile;
+                  const uint8_t* src = static_cast<const uint8_t*>(p.v_pool) +
+                                       (static_cast<size_t>(id == p.num_blocks ? 0 : id) * p.Hkv +
+                                        un.head) * (kBlockSize * D * 2) + lane * 16;
 #pragma unroll
-            for (int j = 0; j < Gm::kPages / Gm::kAux; ++j) {
-              const int pg = j * Gm::kAux + aux;
-              const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
-              const bool there = id != p.num_blocks;
-              const uint8_t* src = static_cast<const uint8_t*>(p.v_pool) +
-                                   (static_cast<size_t>(there ? id : 0) * p.Hkv + un.head) *
-                                       (kBlockSize * D * 2) + lane * 16;
-#pragma unroll
-              for (int i = 0; i < kBlockSize / kRows; ++i) {
-                const int key = pg * kBlockSize + i * kRows + r;
-                cp_async_16(tile + key * 128 + (((c & 7) ^ (key & 7)) << 4), src + i * 512,
-                            there && t * kPromptTile + key < un.L ? 16u : 0u);
+                  for (int i = 0; i < kBlockSize / kRows; ++i) {
+                    const int key = pg * kBlockSize + i * kRows + r;
+                    cp_async_16(tile + key * 128 + (((c & 7) ^ (key & 7)) << 4), src + i * 512,
+                                key < end ? 16u : 0u);
+                  }
+                }
+                cp_async_commit();
+                ++issued;
+                ++tiles;
+                if (issued - done < Gm::kVStages && issued < un.t1) continue;
               }
             }
-            cp_async_commit();
-            if (pending) {
+            if (issued - done > 1)
               cp_async_wait<1>();
-              finish(t - 1, before);
-            }
-            pending = true;
+            else
+              cp_async_wait<0>();
+            finish(done, (tiles - (issued - done)) % Gm::kVStages);
+            ++done;
           }
           cp_async_wait<0>();
-          if (pending && ok) finish(un.t1 - 1, (tiles + Gm::kVStages - 1) % Gm::kVStages);
         }
-        if (!ok) break;
+        if (!wait.ok()) break;
         if (found) *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
         __syncwarp();
         if (lane == 0) {
@@ -932,6 +973,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           mbar_arrive(&ms.unit_empty[ui & 1]);
         }
       }
+      wait.report();
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -941,15 +983,11 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kPromptTile, to = tmem + lanes + Gm::kO + s * D;
     const int tok = r / p.G, g = r - tok * p.G;         // of this row
-    bool ok = true;
+    PromptWaits wait;                                   // lanes agree to go on where they vote
     uint32_t n_s = 0, n_o = 0;                          // S and O tiles taken
-    auto wait = [&](uint64_t* bar, uint32_t parity) {  // lanes agree on `ok` where they vote
-      if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, limit);
-      __syncwarp();
-    };
-    for (int ui = 0; ok; ++ui) {
+    for (int ui = 0; wait.ok(); ++ui) {
       wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!wait.all_ok()) break;
       const PromptUnit un = ms.unit[ui & 1];
       if (un.b < 0) break;
       const PromptSub sub = prompt_sub(p, un, s);
@@ -967,13 +1005,60 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       bool steady = false;                              // a reference that may stay
       for (int t = sub.a; t < sub.e; ++t) {
         wait(&ms.s_full[s], n_s++ & 1u);
+        __syncwarp();
         tc::fence_after_sync();
         const bool masked = prompt_masked(p, t, sub.first, sub.first + sub.n - 1);
-        bool done = false;
-        if (steady && !masked) {
-          PromptScores<KV8> sc;
+        bool look = masked || !steady;                  // for the maximum
+        PromptScores<KV8> sc;
+        while (true) {
           sc.load(ts);
-          sc.begin(c, Gm::kShift - ref);
+          // A score's factor is applied with the reference's subtraction, in one rounding; with
+          // a factor that is not positive, or references that leave no bits behind the point, it
+          // comes first.
+          float cc = c;
+          if (look) {
+            float m;
+            bool first = !(c > 0.f), border = masked;
+            while (true) {
+              if (first) {
+                sc.multiply(cc);
+                cc = 1.f;
+              }
+              if (border) {
+                const int hi = pos - t * kPromptTile;   // columns lo < i <= hi are visible
+                sc.mask(p.window > 0 ? hi - p.window : -1, hi);
+                border = false;
+              }
+              m = sc.largest() * cc;
+              if (first || !__any_sync(0xffffffffu, fabsf(m) > kPromptExact &&
+                                                        fabsf(m) < CUDART_INF_F))
+                break;
+              first = true;
+            }
+            // by 8 at least, unless weights went past their limit; the first finite score always
+            const bool move = m > ref + (steady && !masked ? 0.f : 8.f);
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? hw_exp2(ref - m) : 1.f;
+              ref = move ? m : ref;
+              sum *= f;
+              if (t > sub.a) {
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                  uint32_t o[16];
+                  tc::tmem_ld16(to + i * 16, o);
+                  tc::tmem_wait_ld();
+                  tmem_wait_regs(o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tc::tmem_st16(to + i * 16, o);
+                }
+              }
+            }
+            steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
+          }
+          const float off = ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref;
+          sc.begin(cc, off);
           // beside the first half of the weights the largest of the other half's scores, so that
           // nothing is left to look at behind the test
           float most[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -981,66 +1066,19 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             most[k & 3] = max3(most[k & 3], sc.score(64 + 2 * k), sc.score(65 + 2 * k));
           });
           const float m = fmaxf(max3(most[0], most[1], most[2]), most[3]);
-          const bool fine = sc.total() <= kPromptLimit && fmaf(m, c, Gm::kShift - ref) <= 15.f;
-          if (__all_sync(0xffffffffu, fine)) {
-            sc.finish(ts, &ms.p_half[s], lane);
-            sum += sc.total();
-            done = true;
-          }
+          const bool fine = sc.total() <= kPromptLimit && fmaf(m, cc, off) <= 15.f;
+          if (look || __all_sync(0xffffffffu, fine)) break;
+          look = true;
         }
-        if (!done) {
-          PromptScores<KV8> sc;
-          sc.load(ts);
-          // A score's factor is applied with the reference's subtraction, in one rounding; with
-          // a factor that is not positive, or references that leave no bits behind the point, it
-          // comes first.
-          float cc = c;
-          if (!(c > 0.f)) {
-            sc.multiply(c);
-            cc = 1.f;
-          }
-          if (masked) {
-            const int hi = pos - t * kPromptTile;       // columns lo < i <= hi are visible
-            sc.mask(p.window > 0 ? hi - p.window : -1, hi);
-          }
-          float m = sc.largest() * cc;
-          if (__any_sync(0xffffffffu, fabsf(m) > kPromptExact && fabsf(m) < CUDART_INF_F)) {
-            sc.multiply(cc);
-            cc = 1.f;
-            m = sc.largest();
-          }
-          const bool move = m > ref;                    // the first finite score always moves it
-          if (__any_sync(0xffffffffu, move)) {
-            const float f = move ? hw_exp2(ref - m) : 1.f;
-            ref = move ? m : ref;
-            sum *= f;
-            if (t > sub.a) {
-#pragma unroll 1
-              for (int i = 0; i < D / 16; ++i) {
-                uint32_t o[16];
-                tc::tmem_ld16(to + i * 16, o);
-                tc::tmem_wait_ld();
-                tmem_wait_regs(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tc::tmem_st16(to + i * 16, o);
-              }
-            }
-          }
-          steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
-          sc.begin(cc, ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref);
-          sc.template weights<0, 32>([](int) {});
-          sc.finish(ts, &ms.p_half[s], lane);
-          sum += sc.total();
-        }
+        sc.finish(ts, &ms.p_half[s], lane);
+        sum += sc.total();
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full[s]);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!wait.all_ok()) break;
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!wait.all_ok()) break;
 
       // -------------------------------------------------------------- unit output
       wait(&ms.unit_checked[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
@@ -1049,68 +1087,74 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
       const bool any = sub.e > sub.a;
       if (any) wait(&ms.o_full[s], n_o++ & 1u);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!wait.all_ok()) break;
       tc::fence_after_sync();
       float vs = 1.f;
       if constexpr (KV8) vs = __ldg(p.v_scale + un.head);
       const float inv = any ? __frcp_rn(sum) : 0.f;
       const size_t row =
           static_cast<size_t>(un.row0 + s * p.sub_tokens + tok) * p.Hq + un.head * p.G + g;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
         uint32_t o[32];
         if (any) {
           tc::tmem_ld32(to + i * 32, o);
           tc::tmem_wait_ld();
           tmem_wait_regs(o);
+          if (i + 1 == D / 32) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.o_free[s]);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           o[k] = any ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
-        if (special && live) {
-          for (int t = sub.a; t < sub.e; ++t) {
-            if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
-            const int from = p.window > 0 ? max(t * kPromptTile, pos - p.window + 1)
-                                          : t * kPromptTile;
-            for (int j = from; j <= min(pos, t * kPromptTile + kPromptTile - 1); ++j) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float v = prompt_value<D, KV8>(p, un, j, i * 32 + k);
-                if (!(fabsf(v) < CUDART_INF_F))
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) + v);
-              }
-            }
-          }
-        }
         if constexpr (KV8) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * vs);
         }
-        if (live) {
-          if (un.parts == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D) +
-                         i * 4;
+        if (live && un.parts == 1) {
+          uint32_t y[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[k] = make_uint4(
-                  pack_bf16x2_rn(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
-                  pack_bf16x2_rn(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
-                  pack_bf16x2_rn(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
-                  pack_bf16x2_rn(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
-          } else {
-            const size_t at = row * p.max_parts + un.part;
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D) + i * 8;
+          for (int k = 0; k < 16; ++k)
+            y[k] = pack_bf16x2_rn(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D) + i * 4;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            if (i == 0) p.part_ml[at] = make_float2(ref - Gm::kShift, sum);
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        } else if (live) {
+          const size_t at = row * p.max_parts + un.part;
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D) + i * 8;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (i == 0) p.part_ml[at] = make_float2(ref - Gm::kShift, sum);
+        }
+      }
+      // the infinities and NaN that were taken out of V, for the rows that see them
+      if (special && live && any) {
+        for (int t = sub.a; t < sub.e; ++t) {
+          if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
+          const int from = p.window > 0 ? max(t * kPromptTile, pos - p.window + 1)
+                                        : t * kPromptTile;
+          for (int j = from; j <= min(pos, t * kPromptTile + kPromptTile - 1); ++j) {
+#pragma unroll 1
+            for (int d = 0; d < D; ++d) {
+              const float v = prompt_value<D, KV8>(p, un, j, d);
+              if (fabsf(v) < CUDART_INF_F) continue;
+              if (un.parts == 1) {
+                __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.out) + row * D + d;
+                *at = __float2bfloat16_rn(__bfloat162float(*at) + v);
+              } else {
+                p.part_o[(row * p.max_parts + un.part) * D + d] += v;
+              }
+            }
           }
         }
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (any && lane == 0) mbar_arrive(&ms.o_free[s]);
     }
+    wait.report();
   }
 
   // ------------------------------------------------------------------ teardown
@@ -1126,46 +1170,60 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 // ---------------------------------------------------------------- merge of partitions
 // One warp per query row of a pair of tiles whose keys were cut: partition i holds O_i
 // (normalised), the reference m_i (log2 units) and the sum l_i, and counts w_i = l_i 2^(m_i - M).
+// Eight partitions' values are on their way at once.
 constexpr int kPromptMergeWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kPromptMergeWarps * 32)
-    prompt_merge_kernel(const PromptParams p, int rows_per_cta) {
+__global__ void __launch_bounds__(kPromptMergeWarps * 32) prompt_merge_kernel(const PromptParams p) {
   constexpr int DL = D / 32;
+  using Vec = std::conditional_t<DL == 4, float4, float2>;
   grid_dependency_wait();
   PromptUnit un;
   bool bad;
   if (!prompt_unit(p, blockIdx.x, un, &bad) || un.parts == 1) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = un.ntok * p.G;
-  const int end = min(rows, static_cast<int>(blockIdx.y + 1) * rows_per_cta);
-  for (int r = blockIdx.y * rows_per_cta + warp; r < end; r += kPromptMergeWarps) {
-    const size_t row =
-        static_cast<size_t>(un.row0 + r / p.G) * p.Hq + un.head * p.G + r % p.G;
-    const float2* ml = p.part_ml + row * p.max_parts;
-    float M = -CUDART_INF_F;
-    for (int i = lane; i < un.parts; i += 32) {
-      const float2 x = __ldcg(ml + i);
-      M = fmaxf(M, x.y == 0.f ? -CUDART_INF_F : x.x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float acc[DL] = {}, total = 0.f;
-    for (int i = 0; i < un.parts; ++i) {
-      const float2 x = __ldcg(ml + i);
-      if (x.y == 0.f) continue;                   // saw no key, or only scores of -inf
-      const float w = x.y * hw_exp2(x.x - M);
-      total += w;
-      const float* src = p.part_o + (row * p.max_parts + i) * D + lane * DL;
-#pragma unroll
-      for (int k = 0; k < DL; ++k) acc[k] += w * __ldcg(src + k);
-    }
-    const float inv = __frcp_rn(total);
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + lane * DL;
-#pragma unroll
-    for (int k = 0; k < DL; k += 2)
-      *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2_rn(acc[k] * inv, acc[k + 1] * inv);
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kPromptMergeWarps + (threadIdx.x >> 5);
+  if (r >= un.ntok * p.G) return;
+  const size_t row = static_cast<size_t>(un.row0 + r / p.G) * p.Hq + un.head * p.G + r % p.G;
+  const float2* ml = p.part_ml + row * p.max_parts;
+  const Vec* src = reinterpret_cast<const Vec*>(p.part_o + row * p.max_parts * D) + lane;
+  float M = -CUDART_INF_F;
+  for (int i = lane; i < un.parts; i += 32) {
+    const float2 x = __ldcg(ml + i);
+    M = fmaxf(M, x.y == 0.f ? -CUDART_INF_F : x.x);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[DL] = {}, total = 0.f;
+  for (int i0 = 0; i0 < un.parts; i0 += 8) {
+    Vec v[8];
+    float w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k;
+      w[k] = 0.f;
+      v[k] = Vec{};
+      if (i < un.parts) {
+        const float2 x = __ldcg(ml + i);
+        v[k] = __ldcg(src + static_cast<size_t>(i) * 32);
+        // a partition without a key of this row, or with scores of -inf alone, counts nothing
+        if (x.y != 0.f) w[k] = x.y * hw_exp2(x.x - M);
+        else v[k] = Vec{};
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      total += w[k];
+      const float* f = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+      for (int d = 0; d < DL; ++d) acc[d] += w[k] * f[d];
+    }
+  }
+  const float inv = __frcp_rn(total);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + lane * DL;
+#pragma unroll
+  for (int k = 0; k < DL; k += 2)
+    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2_rn(acc[k] * inv, acc[k + 1] * inv);
 }
 
 template <int D, bool KV8>
@@ -1195,16 +1253,19 @@ cudaError_t launch_prompt_as(const CUtensorMap& tq, const CUtensorMap& tk, const
       configured.fetch_or(bit, std::memory_order_acq_rel);
     }
   }
-  const int pairs = p.num_slots * p.Hkv, units = pairs * p.max_parts;
-  kern<<<static_cast<unsigned>(std::min(units, sms)), Gm::kThreads, Gm::kAlloc, s>>>(tq, tk, tv, p,
-                                                                                  units);
+  const int pairs = p.num_slots * p.Hkv;
+  if (p.counter != nullptr) {
+    e = cudaMemsetAsync(p.counter, 0, sizeof(int), s);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<static_cast<unsigned>(std::min(p.num_units, sms)), Gm::kThreads, Gm::kAlloc, s>>>(tq, tk, tv,
+                                                                                        p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.max_parts == 1) return e;
-  const int rows_per_cta = 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs),
-                     static_cast<unsigned>((2 * p.sub_tokens * p.G + rows_per_cta - 1) /
-                                           rows_per_cta), 1);
+                     static_cast<unsigned>((2 * p.sub_tokens * p.G + kPromptMergeWarps - 1) /
+                                           kPromptMergeWarps), 1);
   cfg.blockDim = dim3(kPromptMergeWarps * 32, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1212,7 +1273,7 @@ cudaError_t launch_prompt_as(const CUtensorMap& tq, const CUtensorMap& tk, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_merge_kernel<D>, p, rows_per_cta);
+  return cudaLaunchKernelEx(&cfg, prompt_merge_kernel<D>, p);
 }
 
 }  // namespace pa
