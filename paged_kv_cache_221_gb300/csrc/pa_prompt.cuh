@@ -58,7 +58,7 @@ namespace pa {
 template <int D, bool KV8>
 struct PromptGeo {
   static constexpr int kSoftmaxWarps = 8;
-  static constexpr int kAux = 2;                         // warps that bring V, or widen K and V
+  static constexpr int kAux = KV8 ? 6 : 2;               // warps that bring V, or widen K and V
   static constexpr int kThreads = (kSoftmaxWarps + 2 + kAux) * 32;
   static constexpr int kHalves = D / 64;                 // 64-dim halves of a row (128 bytes)
   static constexpr int kHalfBytes = kPromptTile * 128;
@@ -80,7 +80,8 @@ struct PromptGeo {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 2 * kPromptTile;        // S tiles at 0 and 128, then O
   // registers per thread: launch, softmax warps, others
-  static constexpr int kRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+  static constexpr int kRegs = KV8 ? 128 : 168, kSoftmaxRegs = KV8 ? 192 : 208;
+  static constexpr int kOtherRegs = KV8 ? 64 : 88;
   static_assert(kAlloc <= 232448, "shared memory per block");
   static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs <=
                     kThreads * kRegs, "the split takes no more than the launch has");
@@ -491,7 +492,7 @@ template <int D>
 __device__ __forceinline__ void widen_keys(uint8_t* dst, const uint8_t* raw, int lane, int worker,
                                            int workers) {
   constexpr int C = D / 16;                    // 16-dim pieces of a row
-#pragma unroll 4
+#pragma unroll 1
   for (int i = worker; i < kPromptTile * C / 32; i += workers) {
     int key, c;
     if constexpr (C == 8) {                    // 8 rows of one piece, four pieces
@@ -517,7 +518,7 @@ template <int D>
 __device__ __forceinline__ bool widen_values(uint8_t* dst, const uint8_t* raw, int lane, int worker,
                                              int workers, bool border, int end) {
   bool found = false;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = worker; i < kPromptTile / kBlockSize * D / 32; i += workers) {
     const int pg = i / (D / 32), d = i % (D / 32) * 32 + lane;
     uint4 w = *reinterpret_cast<const uint4*>(raw + (pg * D + d) * 16);
@@ -643,24 +644,23 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       PromptWaits wait;
       int item = 0, ui = 0, u = blockIdx.x;
       uint32_t n_q[2] = {0, 0};                        // loads of each tile's query rows
-      // the unit behind the present one: the next that no CTA has begun, or every gridDim.x-th
+      // the unit behind the present one: the next that no CTA has taken (asked for a few tiles
+      // before it is needed, so that none is held for long), or every gridDim.x-th
       auto claim = [&]() {
         return p.counter == nullptr ? u + static_cast<int>(gridDim.x)
                : lane == 0          ? atomicAdd(p.counter, 1) + static_cast<int>(gridDim.x)
                                     : 0;
       };
-      int next = claim();
+      int next = 0;
       while (true) {
         PromptUnit un;
         un.b = -1;
         while (u < p.num_units) {
           bool bad;
-          const bool found = prompt_unit(p, u, un, &bad);
-          u = __shfl_sync(0xffffffffu, next, 0);
-          if (u < p.num_units) next = claim();
-          if (found) break;
+          if (prompt_unit(p, u, un, &bad)) break;
           if (bad && lane == 0) atomicOr(&g_pa_err, kErrBounds);
           un.b = -1;
+          u = __shfl_sync(0xffffffffu, claim(), 0);
         }
         wait(&ms.unit_empty[ui & 1], (static_cast<uint32_t>(ui >> 1) & 1u) ^ 1u);
         if (!wait.all_ok()) break;
@@ -671,7 +671,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         ++ui;
         if (un.b < 0) break;
         PromptPages pages;
+        const int ask = max(un.t0, un.t1 - 4);
         for (int t = un.t0; t < un.t1 && wait.ok(); ++t) {
+          if (t == ask) next = claim();
           // a bf16 page is one box of 16 keys per half, an FP8 page one box; a row past the pool
           // is filled with zeros
           constexpr int kBoxes = KV8 ? 1 : Gm::kHalves;
@@ -716,6 +718,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           }
         }
         if (!wait.ok()) break;
+        u = __shfl_sync(0xffffffffu, next, 0);
       }
       wait.report();
       // no copy may still be landing when the CTA ends
