@@ -113,7 +113,7 @@ struct PromptMisc {
   uint64_t raw_full[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
   uint64_t raw_empty[Gm::kRawStages > 0 ? Gm::kRawStages : 1];
   uint64_t q_full[2], q_empty[2];      // by tile of the pair
-  uint64_t q_wide[2];                  // by record: the query rows are f16
+  uint64_t q_wide[2][2];               // by record and tile: the query rows are f16
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];   // by tile of the pair
   uint64_t unit_full[2], unit_empty[2], unit_checked[2]; // by record
   uint64_t fin;
@@ -612,7 +612,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       mbar_init(&ms.unit_full[i], 1);
       mbar_init(&ms.unit_empty[i], 1 + Gm::kSoftmaxWarps + Gm::kAux);
       mbar_init(&ms.unit_checked[i], Gm::kAux);
-      mbar_init(&ms.q_wide[i], Gm::kAux);
+      mbar_init(&ms.q_wide[i][0], Gm::kAux);
+      mbar_init(&ms.q_wide[i][1], Gm::kAux);
     }
     mbar_init(&ms.fin, 1);
     fence_barrier_init();
@@ -778,7 +779,6 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         un.pos0 = __shfl_sync(0xffffffffu, un.pos0, 0);
         un.ntok = __shfl_sync(0xffffffffu, un.ntok, 0);
         const PromptSub sub[2] = {prompt_sub(p, un, 0), prompt_sub(p, un, 1)};
-        if constexpr (KV8) wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
         // P.V of K/V tile t, then S of the next
         for (int t = un.t0 - 1; t < un.t1; ++t) {
           const bool more = t + 1 < un.t1;
@@ -811,7 +811,12 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             if (sub[s].a <= t + 1 && t + 1 < sub[s].e) {
               if (!k_here) wait(&ms.k_full[kst], kph);
               k_here = true;
-              if (!KV8 && t + 1 == sub[s].a) wait(&ms.q_full[s], n_q[s]++ & 1u);
+              if (t + 1 == sub[s].a) {
+                if constexpr (KV8)
+                  wait(&ms.q_wide[ui & 1][s], static_cast<uint32_t>(ui >> 1) & 1u);
+                else
+                  wait(&ms.q_full[s], n_q[s]++ & 1u);
+              }
               __syncwarp();
               tc::fence_after_sync();
               scores(s, klo);
@@ -850,24 +855,22 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         const int last = un.pos0 + un.ntok - 1;
         bool found = false;
         if constexpr (KV8) {
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < 2; ++s) {
             const PromptSub sub = prompt_sub(p, un, s);
-            if (sub.a < sub.e) wait(&ms.q_full[s], n_q[s]++ & 1u);
+            if (sub.a < sub.e) {
+              wait(&ms.q_full[s], (s ? n_q[1]++ : n_q[0]++) & 1u);
+              if (!wait.all_ok()) break;
+              for (int r = aux * 32 + lane; r < p.sub_tokens * p.G; r += Gm::kAux * 32)
+                ms.q_exp[ui & 1][s][r] =
+                    static_cast<int8_t>(widen_query<D>(smem + s * Gm::kTileBytes, r));
+              tc::fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_wide[ui & 1][s]);
           }
-          if (!wait.all_ok()) break;
-          const int rows = p.sub_tokens * p.G;
-          for (int i = aux * 32 + lane; i < 2 * kPromptTile; i += Gm::kAux * 32) {
-            const int s = i / kPromptTile, r = i % kPromptTile;
-            if (r < rows && (s == 0 || un.ntok > p.sub_tokens))
-              ms.q_exp[ui & 1][s][r] =
-                  static_cast<int8_t>(widen_query<D>(smem + s * Gm::kTileBytes, r));
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.q_wide[ui & 1]);
           for (int t = un.t0; t < un.t1 && wait.ok(); ++t, ++tiles) {
-#pragma unroll
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int rs = item % Gm::kRawStages;
               const int st = tiles % (kv ? Gm::kVStages : Gm::kKStages);
@@ -998,7 +1001,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       const int pos = sub.first + min(tok, max(sub.n, 1) - 1);
       float c = p.scale_log2;
       if constexpr (KV8) {
-        wait(&ms.q_wide[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
+        wait(&ms.q_wide[ui & 1][s], static_cast<uint32_t>(ui >> 1) & 1u);
         const int e = ms.q_exp[ui & 1][s][live ? r : 0];
         c *= __ldg(p.k_scale + un.head) *
              __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
