@@ -11,12 +11,14 @@
 //
 // Alternatives.  The pass also keeps each thread's largest element.  If every one of the
 // W warps has J threads at or above a value t, at least W J elements of the row are, so with
-// W J >= k only elements >= t can be among the k largest.  t is the least of the warps' J-th
-// largest thread maxima; the few threads that hold such elements are read again (from L2)
-// by their whole warps, and what is >= t goes to a list in shared memory, of which the
-// k largest by (value, lower index) are found exactly.  A list that overflows (ties without
-// end, as in rows that are masked to -inf) is made again from the elements above t and, in
-// the order of the row, as many equal ones as are missing.
+// W J >= k only elements >= t can be among the k largest; t is the least of the warps' J-th
+// largest thread maxima, and then the k-th largest of the maxima that reach it.  A thread also
+// remembers where its maximum came from (a step of four vectors) and the largest of its other
+// steps: nearly always that one step, of the few threads that matter, is all that is read again.
+// What is >= t goes to a list in shared memory, of which the k largest by (value, lower index)
+// are found exactly.  A list that overflows (ties without end, as in rows that are masked to
+// -inf) is made again from the elements above t and, in the order of the row, as many equal
+// ones as are missing.
 //
 // The kernel is bound by reading the logits.  A cluster of CTAs shares a row when there are
 // few rows.
@@ -33,12 +35,12 @@ namespace cg = cooperative_groups;
 
 namespace pa {
 
-constexpr int kScoreThreads = 512;
+constexpr int kScoreThreads = 256;          // four CTAs per SM, so that rows are in different stages
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreList = 4096;            // candidates a CTA holds
+constexpr int kScoreList = 2304;            // candidates a CTA holds; a row that leaves a thread
+                                            // without an element has fewer in all
 constexpr int kScoreSplit = 8;              // CTAs that share a row
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-static_assert(2 * kScoreWarps >= kMaxScoreTop, "J is 1 or 2");
 
 // Order of values as unsigned integers; NaN above everything, the zeros equal, 0 = no value.
 __device__ __forceinline__ uint32_t value_key(float x) {
@@ -72,6 +74,11 @@ __device__ __forceinline__ ScoreSums join(ScoreSums a, ScoreSums b) {
   return ScoreSums{r, za + zb, wa + wb};
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -119,13 +126,16 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
-// The N elements x into the sums; elements of -inf add nothing.
+// The N elements x into the sums, and their maximum; elements of -inf add nothing.
 template <int N>
-__device__ __forceinline__ void add_elements(ScoreSums& s, const float (&x)[N], float& most) {
-  float m = x[0];
+__device__ __forceinline__ float add_elements(ScoreSums& s, const float (&x)[N]) {
+  float m = fmaxf(x[0], x[1]), m2 = m;
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
-  most = fmaxf(most, m);
+  for (int i = 2; i + 1 < N; i += 4) {
+    m = max3(m, x[i], x[i + 1]);
+    if (i + 3 < N) m2 = max3(m2, x[i + 2], x[i + 3]);
+  }
+  m = fmaxf(m, m2);
   if (m > s.r + 5.5f) {                       // the first finite element always
     if (s.r != -CUDART_INF_F) {
       const float d = fminf((m - s.r) * kLog2e, 1000.f), f = hw_exp2(-d);
@@ -150,6 +160,7 @@ __device__ __forceinline__ void add_elements(ScoreSums& s, const float (&x)[N], 
   }
   s.z = __uint_as_float(static_cast<uint32_t>(z2)) + __uint_as_float(static_cast<uint32_t>(z2 >> 32));
   s.w = __uint_as_float(static_cast<uint32_t>(w2)) + __uint_as_float(static_cast<uint32_t>(w2 >> 32));
+  return m;
 }
 
 struct ScoreShared {
@@ -159,6 +170,10 @@ struct ScoreShared {
   ScoreSums sums[kScoreWarps];
   ScoreSums cta[kScoreSplit];                            // in CTA 0
   uint32_t warp_key[kScoreWarps];
+  uint32_t maxima[kScoreThreads];
+  int steps[kScoreWarps][32];
+  uint32_t bound;
+  int num_maxima;
   int count[kScoreWarps];
   int n;
 };
@@ -211,7 +226,7 @@ __device__ __forceinline__ void cluster_wait() {
 
 // kSplit CTAs (a cluster) share a row.
 template <typename T, int kSplit>
-__global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const ScoreParams p) {
   constexpr int N = Vec<T>::kN;
   __shared__ ScoreShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -225,7 +240,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
   const int nv = (V - head) / N, tail = head + nv * N;
   const uint4* vec = reinterpret_cast<const uint4*>(x + head);
   const int per = (nv + kSplit - 1) / kSplit, v0 = min(nv, part * per), v1 = min(nv, v0 + per);
-  if (tid == 0) sh.n = 0;
+  if (tid == 0) sh.n = sh.num_maxima = 0;
   if constexpr (kSplit > 1) cluster_arrive();
 
   float given = 0.f;
@@ -242,9 +257,15 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
 
   // ------------------------------------------------------------------ the pass
   ScoreSums s{-CUDART_INF_F, 0.f, 0.f};
-  float most = -CUDART_INF_F;
+  float most = -CUDART_INF_F, second = -CUDART_INF_F;   // maxima of the best and the other steps
+  int best_at = v0;                                     // where the best step begins
   int v = v0 + tid;
-  constexpr int U = 4;                        // loads in flight
+  constexpr int U = 4;                                  // vectors of a step
+  auto keep = [&](float m) {
+    second = fmaxf(second, fminf(m, most));
+    best_at = m > most ? v : best_at;
+    most = fmaxf(most, m);
+  };
   for (; v + (U - 1) * kScoreThreads < v1; v += U * kScoreThreads) {
     uint4 w[U];
 #pragma unroll
@@ -253,12 +274,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
 #pragma unroll
     for (int i = 0; i < U; ++i)
       Vec<T>::get(w[i], *reinterpret_cast<float(*)[N]>(f + i * N));
-    add_elements(s, f, most);
+    keep(add_elements(s, f));
   }
   for (; v < v1; v += kScoreThreads) {
     float f[N];
     Vec<T>::get(__ldg(vec + v), f);
-    add_elements(s, f, most);
+    keep(add_elements(s, f));
   }
   // one element in front of or behind the vectors
   int extra = -1;
@@ -268,11 +289,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
     else if (tid - head < V - tail)
       extra = tail + tid - head;
   }
-  float one = 0.f;
+  float one = -CUDART_INF_F;
   if (extra >= 0) {
     one = to_float(x[extra]);
     const float f[2] = {one, -CUDART_INF_F};
-    add_elements(s, f, most);
+    add_elements(s, f);
   }
 
   // ------------------------------------------------------------------ sums of the row
@@ -285,19 +306,36 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
   // ------------------------------------------------------------------ candidates
   if (K > 0) {
     const bool any = v0 + tid < v1 || extra >= 0;
-    const uint32_t key = any ? value_key(most) : 0u;
-    const uint32_t k1 = __reduce_max_sync(0xffffffffu, key);
-    uint32_t kj = k1;
-    if (K > kScoreWarps) {                    // the second largest
-      const unsigned who = __ballot_sync(0xffffffffu, key == k1);
-      kj = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : key);
+    const uint32_t key = any ? value_key(fmaxf(most, one)) : 0u;
+    // the J-th largest of the warp, W J >= K
+    uint32_t kj = __reduce_max_sync(0xffffffffu, key), left = key;
+    for (int j = kScoreWarps; j < K; j += kScoreWarps) {
+      const unsigned who = __ballot_sync(0xffffffffu, left == kj);
+      if (lane == __ffs(who) - 1) left = 0u;
+      kj = __reduce_max_sync(0xffffffffu, left);
     }
     if (lane == 0) sh.warp_key[warp] = kj;
     __syncthreads();
     uint32_t least = sh.warp_key[0];
 #pragma unroll
     for (int i = 1; i < kScoreWarps; ++i) least = min(least, sh.warp_key[i]);
+    if (key >= least) sh.maxima[atomicAdd(&sh.num_maxima, 1)] = key;
+    __syncthreads();
+    const int maxima = sh.num_maxima;
+    if (tid < maxima) {
+      const uint32_t mine = sh.maxima[tid];
+      int above = 0, equal = 0;
+      for (int i = 0; i < maxima; ++i) {
+        above += sh.maxima[i] > mine;
+        equal += sh.maxima[i] == mine;
+      }
+      if (above < K && above + equal >= K) sh.bound = mine;
+    }
+    __syncthreads();
+    least = sh.bound;
+    const float bound = key_value(least);       // NaN where there is none
     auto offer = [&](float f, int index, bool above) {
+      if (above ? f <= bound : f < bound) return;
       const uint32_t k = value_key(f);
       if (above ? k > least : k >= least) {
         const int at = atomicAdd(&sh.n, 1);
@@ -306,7 +344,22 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
     };
     // NaN passes through maxima, so rows with one look at everything
     auto collect = [&](bool above) {
-      unsigned who = __ballot_sync(0xffffffffu, above ? key > least : key >= least);
+      const bool mine = v0 + tid < v1 && !(above ? most <= bound : most < bound);
+      const bool all = mine && !(above ? second <= bound : second < bound);
+      const unsigned step = __ballot_sync(0xffffffffu, mine && !all);
+      if (mine && !all) sh.steps[warp][__popc(step & ((1u << lane) - 1))] = best_at;
+      __syncwarp();
+      for (int g = lane / U; g - lane / U < __popc(step); g += 32 / U) {
+        if (g >= __popc(step)) continue;
+        const int i = sh.steps[warp][g] + lane % U * kScoreThreads;
+        if (i < v1) {
+          float f[N];
+          Vec<T>::get(__ldg(vec + i), f);
+#pragma unroll
+          for (int k = 0; k < N; ++k) offer(f[k], head + i * N + k, above);
+        }
+      }
+      unsigned who = __ballot_sync(0xffffffffu, all);
       while (who) {
         const int t = (warp << 5) + __ffs(who) - 1;
         who &= who - 1;
@@ -317,6 +370,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const ScorePara
           for (int k = 0; k < N; ++k) offer(f[k], head + i * N + k, above);
         }
       }
+      __syncwarp();
       if (extra >= 0) offer(one, extra, above);
     };
     collect(false);
