@@ -684,7 +684,7 @@ size_t pa_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, i
  * num_tokens or than a table holds, a negative length, a last block outside the
  * pool: PA_ERR_BOUNDS) changes no state, and its outputs are those of an empty
  * batch: starts 0, slots and positions -1, copies (0, 0).  num_seqs is at most
- * 16384; a sequence may be listed once.
+ * 12288; a sequence may be listed once.
  */
 pa_status pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
                               int32_t* ref_counts, const int32_t* new_lens, int num_seqs,

@@ -146,7 +146,6 @@ struct PromptParams {
                                   //   gridDim.x-th unit)
   float scale_log2;
   int window;                     // 0 = none
-  unsigned long long timeout_ns;
 };
 constexpr int kPromptTile = 128;  // rows of a query tile, and keys of a K/V tile
 
@@ -164,7 +163,7 @@ struct StepParams {
   int num_seqs, num_tokens, num_blocks, mbs;
   bool slots_here;                // in the same launch
 };
-constexpr int kMaxStepSeqs = 16384;  // three integers of each in shared memory
+constexpr int kMaxStepSeqs = 12288;  // four integers of each in shared memory
 
 // Log probabilities (pa_score.cu).
 struct ScoreParams {

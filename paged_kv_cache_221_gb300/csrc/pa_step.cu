@@ -13,8 +13,9 @@
 // One cluster of CTAs does it all in one launch, because the work is a few dependent
 // steps on little data: every CTA keeps the whole batch's prefix sums in shared memory,
 // computed by itself, so that the only thing the CTAs exchange is the number of free
-// blocks in each one's slice of the reference counts.  A call that cannot be met
-// changes nothing.
+// blocks in each one's slice of the reference counts.  A thread counts the free blocks of a
+// short run of the pool and, with the sums before it, hands out the same ones.  A call that
+// cannot be met changes nothing.
 #include <cooperative_groups.h>
 #include <stdint.h>
 
@@ -33,36 +34,34 @@ constexpr int kStepThreads = 1024;
 constexpr int kStepWarps = kStepThreads / 32;
 
 struct StepShared {
-  int warp_sum[kStepWarps];
-  int carry;
+  unsigned long long warp_sum[kStepWarps];
+  unsigned long long many;              // new tokens of the sequences that take in over 2^21
   int free_blocks;                      // in this CTA's slice; read by the others
   unsigned fail;                        // error bits
+  int num_shared;
 };
 
-// Inclusive sum over the CTA's threads; `total` gets the sum of all.
-__device__ __forceinline__ int block_scan(int v, StepShared& sh, int* total) {
+// Inclusive sums over the CTA's threads of two 32-bit counts at once; `total` gets those of all.
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, StepShared& sh,
+                                                         unsigned long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
   if (lane == 31) sh.warp_sum[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int w = sh.warp_sum[lane];
+  unsigned long long before = 0, all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    sh.warp_sum[lane] = w;
+  for (int w = 0; w < kStepWarps; ++w) {
+    const unsigned long long x = sh.warp_sum[w];
+    before += w < warp ? x : 0;
+    all += x;
   }
+  *total = all;
   __syncthreads();
-  if (warp > 0) v += sh.warp_sum[warp - 1];
-  *total = sh.warp_sum[kStepWarps - 1];
-  __syncthreads();
-  return v;
+  return before + v;
 }
 
 // Largest b in [0, n) with start[b] <= x (start ascending, start[0] <= x).
@@ -86,6 +85,24 @@ __device__ __forceinline__ void put_slot(const StepParams& p, int i, int b, int 
   p.positions[i] = pos;
 }
 
+// Bit k: block first + k is free; for up to 32 blocks before `end`.
+__device__ __forceinline__ uint32_t free_mask(const StepParams& p, int first, int end, bool wide) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 32; k += 4) {
+    const int i = first + k;
+    if (wide && i + 4 <= end) {
+      const int4 r = *reinterpret_cast<const int4*>(p.ref_counts + i);
+      m |= static_cast<uint32_t>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3)
+           << k;
+    } else {
+      for (int j = i; j < min(i + 4, end); ++j)
+        m |= static_cast<uint32_t>(p.ref_counts[j] == 0) << (j - first);
+    }
+  }
+  return m;
+}
+
 __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThreads, 1)
     extend_kernel(const StepParams p) {
   __shared__ StepShared sh;
@@ -94,15 +111,30 @@ __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThre
   int* at = dyn;                        // [B] blocks before this sequence's; bit 31: copied
   int* start = at + B;                  // [B] tokens before this sequence's
   int* last = start + B;                // [B] partly filled last block that it appends to, or -1
+  int* len = last + B;                  // [B] tokens so far; bit 31 meanwhile: copied
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31;
+  const int gid = rank * kStepThreads + tid, gsize = kStepCluster * kStepThreads;
   if (tid == 0) {
     sh.fail = 0;
-    sh.free_blocks = 0;
+    sh.many = 0;
+    sh.num_shared = 0;
   }
   grid_launch_dependents();
   __syncthreads();
+
+  // ------------------------------------------------- free blocks of this thread's run of the pool
+  // (a multiple of 4 blocks, or of 32 where that is not enough)
+  int run = (p.num_blocks + 4 * gsize - 1) / (4 * gsize) * 4;
+  if (run > 32) run = (run + 31) / 32 * 32;
+  const int first = static_cast<int>(min(static_cast<long long>(p.num_blocks),
+                                         static_cast<long long>(gid) * run));
+  const int end = min(p.num_blocks, first + run);
+  const bool wide = (reinterpret_cast<uintptr_t>(p.ref_counts) & 15u) == 0;
+  const uint32_t mask = first < end ? free_mask(p, first, min(end, first + 32), wide) : 0u;
+  int mine = __popc(mask);
+  for (int i = first + 32; i < end; i += 32) mine += __popc(free_mask(p, i, min(end, i + 32), wide));
 
   // ------------------------------------------------- what every sequence appends to
   for (int b = tid; b < B; b += kStepThreads) {
@@ -118,69 +150,58 @@ __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThre
         id = -1;
       }
     }
+    if (n >> 21) atomicAdd(&sh.many, static_cast<unsigned long long>(n));
     last[b] = id;
+    len[b] = L;
+    start[b] = n;
+    if (id >= 0 && p.ref_counts[id] > 1) at[atomicAdd(&sh.num_shared, 1)] = b;
   }
-  // free blocks of this CTA's slice (a multiple of 4 blocks, so that slices start aligned)
-  const int slice = (p.num_blocks + 4 * kStepCluster - 1) / (4 * kStepCluster) * 4;
-  const int first = min(p.num_blocks, rank * slice), end = min(p.num_blocks, first + slice);
-  const bool wide = (reinterpret_cast<uintptr_t>(p.ref_counts) & 15u) == 0;
-  int mine = 0;
-  for (int i = first + 4 * tid; i < end; i += 4 * kStepThreads) {
-    if (wide && i + 4 <= end) {
-      const int4 r = *reinterpret_cast<const int4*>(p.ref_counts + i);
-      mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    } else {
-      for (int k = i; k < min(i + 4, end); ++k) mine += p.ref_counts[k] == 0;
-    }
+  __syncthreads();
+  // Below, 1024 counts at a time are summed in 32 bits: those up to 2^21 cannot carry, and the
+  // larger ones may not pass the call's limit, 2^30 at most, together.
+  bool met = sh.fail == 0 && sh.many <= static_cast<unsigned long long>(p.num_tokens);
+  // The shared last blocks, a warp for each: the batch's earlier sequences that append into the
+  // same one have left it by then.
+  for (int i = tid >> 5; i < sh.num_shared && met; i += kStepWarps) {
+    const int b = at[i], block = last[b];
+    int same = 0;
+    for (int a = lane; a < b; a += 32) same += last[a] == block;
+    same = __reduce_add_sync(0xffffffffu, same);
+    if (lane == 0 && p.ref_counts[block] - same > 1) len[b] |= static_cast<int>(0x80000000u);
   }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) atomicAdd(&sh.free_blocks, mine);
   __syncthreads();
 
   // ------------------------------------------------- copies, and the sums over the batch
-  int need_sum = 0;
-  unsigned long long new_sum = 0;
-  for (int b0 = 0; b0 < B; b0 += kStepThreads) {
+  unsigned long long sums = 0;          // blocks needed (high), tokens (low) so far
+  for (int b0 = 0; b0 < B && met; b0 += kStepThreads) {
     const int b = b0 + tid;
-    int n = 0, need = 0;
-    bool copied = false;
-    const bool here = b < B && sh.fail == 0;
+    const bool here = b < B;
+    const bool copied = here && len[b] < 0;
+    const int n = here ? start[b] : 0, L = here ? len[b] & 0x7FFFFFFF : 0;
+    const int need = (L + n + kBlockSize - 1) / kBlockSize - (L + kBlockSize - 1) / kBlockSize +
+                     copied;
+    unsigned long long total;
+    const unsigned long long upto =
+        sums + block_scan(static_cast<unsigned long long>(need) << 32 | static_cast<unsigned>(n),
+                          sh, &total);
     if (here) {
-      const int L = p.context_lens[b];
-      n = p.new_lens[b];
-      need = (L + n + kBlockSize - 1) / kBlockSize - (L + kBlockSize - 1) / kBlockSize;
+      at[b] = (static_cast<int>(upto >> 32) - need) | (copied ? static_cast<int>(0x80000000u) : 0);
+      start[b] = static_cast<int>(upto & 0xFFFFFFFFu) - n;
+      len[b] = L;
     }
-    const int id = here ? last[b] : -1;
-    const int owners = id >= 0 ? p.ref_counts[id] : 0;
-    // the batch's earlier sequences that append into the same block have left it by then
-    unsigned shared = __ballot_sync(0xffffffffu, owners > 1);
-    while (shared) {
-      const int src = __ffs(shared) - 1;
-      shared &= shared - 1;
-      const int block = __shfl_sync(0xffffffffu, id, src), before = b - lane + src;
-      int same = 0;
-      for (int a = lane; a < before; a += 32) same += last[a] == block;
-      same = __reduce_add_sync(0xffffffffu, same);
-      if (lane == src) copied = owners - same > 1;
-    }
-    need += copied;
-    int total;
-    const int upto = block_scan(need, sh, &total);
-    int total_new;
-    const int tokens = block_scan(n, sh, &total_new);
-    if (b < B) {
-      at[b] = (need_sum + upto - need) | (copied ? static_cast<int>(0x80000000u) : 0);
-      start[b] = static_cast<int>(new_sum) + tokens - n;
-    }
-    need_sum += total;
-    new_sum += static_cast<unsigned>(total_new);
-    if (new_sum > static_cast<unsigned long long>(p.num_tokens)) break;   // uniform
+    sums += total;
+    met = (sums & 0xFFFFFFFFu) <= static_cast<unsigned>(p.num_tokens);
   }
-  if (new_sum > static_cast<unsigned long long>(p.num_tokens) && tid == 0) sh.fail = kErrBounds;
+  if (!met && tid == 0 && sh.fail == 0) sh.fail = kErrBounds;
+  unsigned long long here_free;
+  const int upto_mine =
+      static_cast<int>(block_scan(static_cast<unsigned long long>(mine), sh, &here_free));
+  if (tid == 0) sh.free_blocks = static_cast<int>(here_free);
   cluster.sync();                       // nobody writes before everybody has read
 
   // ------------------------------------------------- can it be met
   unsigned fail = sh.fail;
+  const int need_sum = static_cast<int>(sums >> 32), used = static_cast<int>(sums & 0xFFFFFFFFu);
   int before = 0, all = 0;
 #pragma unroll
   for (int r = 0; r < kStepCluster; ++r) {
@@ -189,7 +210,6 @@ __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThre
     all += f;
   }
   if (fail == 0 && need_sum > all) fail = kErrBlocks;
-  const int gid = rank * kStepThreads + tid, gsize = kStepCluster * kStepThreads;
   if (gid == 0) {
     if (fail) atomicOr(&g_pa_err, fail);
     p.query_starts[0] = 0;
@@ -208,67 +228,57 @@ __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThre
   }
 
   // ------------------------------------------------- free blocks to the sequences that need them
-  for (int i0 = first; i0 < end && before < need_sum; i0 += 4 * kStepThreads) {
-    const int i = i0 + 4 * tid;
-    int r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = i + k < end ? p.ref_counts[i + k] : 1;
-    const int own = (r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0);
-    int total;
-    int at_rank = before + block_scan(own, sh, &total) - own;
-    before += total;
-    if (own == 0 || at_rank >= need_sum) continue;
-    // the sequences of this thread's ranks: the last one whose blocks start at or before them
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
+  int at_rank = before + upto_mine - mine;
+  if (mine > 0 && at_rank < need_sum) {
+    // the sequence of this thread's first rank: the last one whose blocks start at or before it
+    int b = 0, hi = B;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
       if ((at[mid] & 0x7FFFFFFF) <= at_rank)
-        lo = mid;
+        b = mid;
       else
         hi = mid;
     }
-    int b = lo;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (r[k] != 0 || at_rank >= need_sum) continue;
-      while (b + 1 < B && (at[b + 1] & 0x7FFFFFFF) <= at_rank) ++b;
-      const int j = at_rank - (at[b] & 0x7FFFFFFF);
-      const bool copied = at[b] < 0;
-      const int have = (p.context_lens[b] + kBlockSize - 1) / kBlockSize;
-      int32_t* row = p.block_tables + static_cast<size_t>(b) * p.mbs;
-      p.ref_counts[i + k] = 1;
-      if (copied && j == 0) {
-        row[have - 1] = i + k;
-        atomicSub(p.ref_counts + last[b], 1);
-        p.copies[2 * b] = last[b];
-        p.copies[2 * b + 1] = i + k;
-      } else {
-        row[have + j - copied] = i + k;
+    for (int i0 = first; i0 < end && at_rank < need_sum; i0 += 32) {
+      uint32_t m = i0 == first ? mask : free_mask(p, i0, min(end, i0 + 32), wide);
+      for (; m != 0 && at_rank < need_sum; m &= m - 1, ++at_rank) {
+        const int i = i0 + __ffs(m) - 1;
+        while (b + 1 < B && (at[b + 1] & 0x7FFFFFFF) <= at_rank) ++b;
+        const int j = at_rank - (at[b] & 0x7FFFFFFF);
+        const bool copied = at[b] < 0;
+        const int have = (len[b] + kBlockSize - 1) / kBlockSize;
+        int32_t* row = p.block_tables + static_cast<size_t>(b) * p.mbs;
+        p.ref_counts[i] = 1;
+        if (copied && j == 0) {
+          row[have - 1] = i;
+          atomicSub(p.ref_counts + last[b], 1);
+          p.copies[2 * b] = last[b];
+          p.copies[2 * b + 1] = i;
+        } else {
+          row[have + j - copied] = i;
+        }
       }
-      ++at_rank;
     }
   }
   for (int b = gid; b < B; b += gsize) {
-    p.query_starts[b + 1] = start[b] + p.new_lens[b];
+    const int n = (b + 1 < B ? start[b + 1] : used) - start[b];
+    p.query_starts[b + 1] = start[b] + n;
+    p.context_lens[b] = len[b] + n;
     if (at[b] >= 0) p.copies[2 * b] = p.copies[2 * b + 1] = 0;
   }
-  cluster.sync();                       // the tables are written
+  cluster.sync();                       // the tables are written, and nobody reads another's sums
 
-  // ------------------------------------------------- slots, and the new lengths behind them
-  if (p.slots_here) {
-    const int used = static_cast<int>(new_sum);
-    for (int i = gid; i < p.num_tokens; i += gsize) {
-      if (i < used) {
-        const int b = last_at_most(start, B, i);
-        put_slot(p, i, b, start[b], p.context_lens[b]);
-      } else {
-        p.slots[i] = -1;
-        p.positions[i] = -1;
-      }
+  // ------------------------------------------------- slots
+  if (!p.slots_here) return;
+  for (int i = gid; i < p.num_tokens; i += gsize) {
+    if (i < used) {
+      const int b = last_at_most(start, B, i);
+      put_slot(p, i, b, start[b], len[b]);
+    } else {
+      p.slots[i] = -1;
+      p.positions[i] = -1;
     }
-    cluster.sync();
   }
-  for (int b = gid; b < B; b += gsize) p.context_lens[b] += p.new_lens[b];
 }
 
 // Slots of many tokens, behind extend_kernel: one thread per token.
@@ -290,7 +300,7 @@ cudaError_t launch_extend(const StepParams& args, cudaStream_t s) {
   // up to two tokens per thread of the cluster, the launch that would spread them over the
   // GPU costs more than it saves
   p.slots_here = p.num_tokens <= 2 * kStepCluster * kStepThreads;
-  const int smem = 3 * p.num_seqs * static_cast<int>(sizeof(int));
+  const int smem = 4 * p.num_seqs * static_cast<int>(sizeof(int));
   static std::atomic<unsigned long long> configured{0ull};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -298,7 +308,7 @@ cudaError_t launch_extend(const StepParams& args, cudaStream_t s) {
   const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
   if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
     e = cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             3 * kMaxStepSeqs * static_cast<int>(sizeof(int)));
+                             4 * kMaxStepSeqs * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
     if (bit) configured.fetch_or(bit, std::memory_order_acq_rel);
   }

@@ -65,7 +65,8 @@ def test_prompt_workspace(lib):
     assert size(psize=4096) == 0
     assert size(mcl=128) == 0
     assert size(window=4096) == size() and size(window=100) < size()
-    assert size(N=200000, psize=0) == 0                  # many query tiles: nothing is cut
+    assert size(N=12000, psize=0) == 0                   # enough query tiles: nothing is cut
+    assert size(N=200000, psize=0) == 256                # many: a counter to take them by
     assert size(N=1, B=1, psize=0) > 0
     for kw in (dict(N=0), dict(B=0), dict(hq=5), dict(psize=100), dict(psize=-1), dict(BS=8),
                dict(window=-1), dict(mcl=0), dict(hq=129, hkv=1)):
@@ -83,7 +84,7 @@ def test_extend_arguments(lib):
         assert call(**{name: None}) == INVALID, name
     for kw in (dict(B=-1), dict(N=-1), dict(NB=0), dict(mbs=0)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(BS=8), dict(B=16385), dict(mbs=2 ** 26 + 1), dict(NB=2 ** 30 + 1),
+    for kw in (dict(BS=8), dict(B=12289), dict(mbs=2 ** 26 + 1), dict(NB=2 ** 30 + 1),
                dict(N=2 ** 30 + 1)):
         assert call(**kw) == UNSUPPORTED, kw
 

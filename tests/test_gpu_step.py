@@ -222,6 +222,16 @@ def test_refusals():
         pa.truncate_sequences(t, dev([1, 1]), r, new)
     with pytest.raises(pa.PagedAttnError):
         pa.truncate_sequences(t, n, r, n)
-    big = torch.zeros((16385, 1), dtype=torch.int32, device="cuda")
+    big = torch.zeros((12289, 1), dtype=torch.int32, device="cuda")
     with pytest.raises(pa.PagedAttnError):
         pa.extend_sequences(big, big[:, 0].contiguous(), r, big[:, 0].contiguous(), 1)
+
+
+def test_new_lengths_past_32_bits():
+    """Four sequences of 2^30 new tokens: their sum is 0 in 32 bits, the call is not met."""
+    tables = torch.empty(4, 2 ** 26, dtype=torch.int32, device="cuda")
+    lens, refs = dev([0] * 4), dev([0] * 64)
+    starts, slots, pos, copies = pa.extend_sequences(tables, lens, refs, dev([2 ** 30] * 4), 16)
+    assert pa.get_device_error() == 5
+    assert starts.tolist() == [0] * 5 and slots.tolist() == [-1] * 16 and pos.tolist() == [-1] * 16
+    assert not copies.any() and not lens.any() and not refs.any()
