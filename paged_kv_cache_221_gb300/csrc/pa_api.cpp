@@ -862,9 +862,9 @@ pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, con
     if (!encode_fp8_maps(&tk, &tv, k_cache, v_cache,
                          static_cast<long long>(num_blocks) * num_kv_heads, head_dim))
       return PA_ERR_CUDA;
-  } else if (!encode_pool_map(&tk, k_cache, rows, head_dim) ||
-             !encode_pool_map(&tv, v_cache, rows, head_dim)) {
-    return PA_ERR_CUDA;
+  } else {
+    if (!encode_pool_map(&tk, k_cache, rows, head_dim)) return PA_ERR_CUDA;
+    tv = tk;                       // not used: V of bf16 pages does not come by TMA
   }
   PromptParams p{};
   p.out = out;
@@ -895,7 +895,6 @@ pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, con
   p.max_parts = plan.max_parts;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window;
-  p.timeout_ns = kDefaultTimeoutNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = head_dim == 64 ? launch_prompt_d64(tq, tk, tv, p, kv8, s)
                                        : launch_prompt_d128(tq, tk, tv, p, kv8, s);

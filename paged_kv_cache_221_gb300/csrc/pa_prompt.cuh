@@ -287,6 +287,7 @@ __device__ __forceinline__ void lead_mma_ss(uint32_t leader, uint32_t d, uint64_
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
+// (A in tensor memory, K-major: row r in lane r, two 16-bit values per 32-bit column)
 __device__ __forceinline__ void lead_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       if (lane == 0) {
         tma_prefetch_map(&tmq);
         tma_prefetch_map(&tmk);
-        tma_prefetch_map(&tmv);
+        if constexpr (KV8) tma_prefetch_map(&tmv);
       }
       // K tiles (K and V tiles of FP8 pages) into their ring
       constexpr int kRing = KV8 ? Gm::kRawStages : Gm::kKStages;
@@ -1097,7 +1098,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       tc::fence_after_sync();
       float vs = 1.f;
       if constexpr (KV8) vs = __ldg(p.v_scale + un.head);
-      const float inv = any ? __frcp_rn(sum) : 0.f;
+      // (a partition without a key of this row, or with scores of -inf alone, has no weights)
+      const float inv = sum == 0.f && un.parts > 1 ? 1.f : __frcp_rn(sum);
       const size_t row =
           static_cast<size_t>(un.row0 + s * p.sub_tokens + tok) * p.Hq + un.head * p.G + g;
 #pragma unroll 1
@@ -1138,23 +1140,44 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           if (i == 0) p.part_ml[at] = make_float2(ref - Gm::kShift, sum);
         }
       }
-      // the infinities and NaN that were taken out of V, for the rows that see them
-      if (special && live && any) {
-        for (int t = sub.a; t < sub.e; ++t) {
-          if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
-          const int from = p.window > 0 ? max(t * kPromptTile, pos - p.window + 1)
-                                        : t * kPromptTile;
-          for (int j = from; j <= min(pos, t * kPromptTile + kPromptTile - 1); ++j) {
-#pragma unroll 1
-            for (int d = 0; d < D; ++d) {
-              const float v = prompt_value<D, KV8>(p, un, j, d);
-              if (fabsf(v) < CUDART_INF_F) continue;
-              if (un.parts == 1) {
-                __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.out) + row * D + d;
-                *at = __float2bfloat16_rn(__bfloat162float(*at) + v);
-              } else {
-                p.part_o[(row * p.max_parts + un.part) * D + d] += v;
+      // the infinities and NaN that were taken out of V, for the rows that see them: a row at a
+      // time, its dims over the lanes
+      if (special && any) {
+        __syncwarp();
+        float add[D / 32];
+        int seen = -1;                                  // token that they are of
+        for (int rr = (warp & 3) * 32; rr < (warp & 3) * 32 + 32; ++rr) {
+          const int tk = rr / p.G;
+          if (tk >= sub.n) break;
+          if (tk != seen) {
+            seen = tk;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) add[k] = 0.f;
+            const int at = sub.first + tk, begin = p.window > 0 ? at - p.window + 1 : 0;
+            for (int t = sub.a; t < sub.e; ++t) {
+              if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
+              const int last = min(at, t * kPromptTile + kPromptTile - 1);
+#pragma unroll 4
+              for (int j = max(t * kPromptTile, begin); j <= last; ++j) {
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                  const float v = prompt_value<D, KV8>(p, un, j, k * 32 + lane);
+                  add[k] += fabsf(v) < CUDART_INF_F ? 0.f : v;
+                }
               }
+            }
+          }
+          const size_t out_row = row + (static_cast<size_t>(tk) * p.Hq + rr % p.G) -
+                                 (static_cast<size_t>(tok) * p.Hq + g);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const int d = k * 32 + lane;
+            if (fabsf(add[k]) == 0.f) continue;
+            if (un.parts == 1) {
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + out_row * D + d;
+              *dst = __float2bfloat16_rn(__bfloat162float(*dst) + add[k]);
+            } else {
+              p.part_o[(out_row * p.max_parts + un.part) * D + d] += add[k];
             }
           }
         }
@@ -1212,9 +1235,8 @@ __global__ void __launch_bounds__(kPromptMergeWarps * 32) prompt_merge_kernel(co
       if (i < un.parts) {
         const float2 x = __ldcg(ml + i);
         v[k] = __ldcg(src + static_cast<size_t>(i) * 32);
-        // a partition without a key of this row, or with scores of -inf alone, counts nothing
+        // a partition without weights counts nothing, unless a value was infinite or NaN
         if (x.y != 0.f) w[k] = x.y * hw_exp2(x.x - M);
-        else v[k] = Vec{};
       }
     }
 #pragma unroll
