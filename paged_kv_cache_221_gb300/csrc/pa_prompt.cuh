@@ -80,8 +80,8 @@ struct PromptGeo {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 2 * kPromptTile;        // S tiles at 0 and 128, then O
   // registers per thread: launch, softmax warps, others
-  static constexpr int kRegs = KV8 ? 128 : 168, kSoftmaxRegs = KV8 ? 192 : 208;
-  static constexpr int kOtherRegs = KV8 ? 64 : 88;
+  static constexpr int kRegs = KV8 ? 128 : 168, kSoftmaxRegs = KV8 ? 184 : 208;
+  static constexpr int kOtherRegs = KV8 ? 72 : 88;
   static_assert(kAlloc <= 232448, "shared memory per block");
   static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs <=
                     kThreads * kRegs, "the split takes no more than the launch has");
@@ -354,6 +354,24 @@ __device__ __forceinline__ void regs_more() {
 template <int kRegs>
 __device__ __forceinline__ void regs_fewer() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Of two 16-byte pieces, a lane whose bit B is clear keeps the first and gets the first of the
+// lane with that bit set in place of the second, which goes there in place of its first.
+template <int B>
+__device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int lane) {
+  const bool up = (lane & B) != 0;
+  const uint32_t* pa = reinterpret_cast<const uint32_t*>(&a);
+  const uint32_t* pb = reinterpret_cast<const uint32_t*>(&b);
+  uint32_t got[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    got[k] = __shfl_xor_sync(0xffffffffu, up ? pa[k] : pb[k], B);
+  const uint4 x = make_uint4(got[0], got[1], got[2], got[3]);
+  if (up)
+    a = x;
+  else
+    b = x;
 }
 
 // A row's 128 scores of a K/V tile in one thread, and the weights that take their place.
@@ -653,6 +671,25 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                : lane == 0          ? atomicAdd(p.counter, 1) + static_cast<int>(gridDim.x)
                                     : 0;
       };
+      // the query rows, each tile's once its last unit's scores no longer need theirs: behind the
+      // first K tile, but for FP8 pages in front of it, because the rows have to be widened
+      auto load_query = [&](const PromptUnit& un) {
+#pragma unroll 1
+        for (int s = 0; s < 2 && wait.ok(); ++s) {
+          const PromptSub sub = prompt_sub(p, un, s);
+          if (sub.a == sub.e) continue;
+          wait(&ms.q_empty[s], ((s ? n_q[1] : n_q[0]) & 1u) ^ 1u);
+          if (!wait.all_ok()) break;
+          ++(s ? n_q[1] : n_q[0]);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ms.q_full[s], static_cast<uint32_t>(Gm::kHalves * p.sub_tokens *
+                                                                       p.G * 128));
+            for (int hh = 0; hh < Gm::kHalves; ++hh)
+              tma_load_4d(smem + s * Gm::kTileBytes + hh * Gm::kHalfBytes, &tmq, &ms.q_full[s],
+                          hh * 64, 0, un.head, un.row0 + s * p.sub_tokens);
+          }
+        }
+      };
       int next = 0;
       while (true) {
         PromptUnit un;
@@ -672,6 +709,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         }
         ++ui;
         if (un.b < 0) break;
+        if (KV8) load_query(un);
         PromptPages pages;
         const int ask = max(un.t0, un.t1 - 4);
         for (int t = un.t0; t < un.t1 && wait.ok(); ++t) {
@@ -701,23 +739,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                             &tmk, &full[st], h * 64, page * kBlockSize);
             }
           }
-          if (t == un.t0) {
-            // the query rows, each tile's once its last unit's scores no longer need theirs
-            for (int s = 0; s < 2 && wait.ok(); ++s) {
-              const PromptSub sub = prompt_sub(p, un, s);
-              if (sub.a == sub.e) continue;
-              wait(&ms.q_empty[s], (n_q[s] & 1u) ^ 1u);
-              if (!wait.all_ok()) break;
-              ++n_q[s];
-              if (lane == 0) {
-                mbar_arrive_expect_tx(&ms.q_full[s], static_cast<uint32_t>(
-                                                         Gm::kHalves * p.sub_tokens * p.G * 128));
-                for (int hh = 0; hh < Gm::kHalves; ++hh)
-                  tma_load_4d(smem + s * Gm::kTileBytes + hh * Gm::kHalfBytes, &tmq,
-                              &ms.q_full[s], hh * 64, 0, un.head, un.row0 + s * p.sub_tokens);
-              }
-            }
-          }
+          if (!KV8 && t == un.t0) load_query(un);
         }
         if (!wait.ok()) break;
         u = __shfl_sync(0xffffffffu, next, 0);
@@ -902,25 +924,36 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           constexpr int kRows = 32 / kRowChunks;       // rows of one warp-wide copy
           const int c = lane % kRowChunks, r = lane / kRowChunks;
           PromptPages pages;
-          // a tile's copies have landed: what some query row must not see, made finite
+          // a tile's copies have landed: keys that some query rows see and some must not, the
+          // last rows' newest and the first rows' oldest, are made finite
           auto finish = [&](int t, int st) {
-            if (prompt_masked(p, t, un.pos0, last)) {
-              uint8_t* tile = smem + Gm::kVOff + st * Gm::kTileBytes;
+            uint8_t* tile = smem + Gm::kVOff + st * Gm::kTileBytes;
 #pragma unroll 1
-              for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
+            for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
+              const int at = t * kPromptTile + pg * kBlockSize;
+              const int old = p.window > 0 ? at + p.window : at;
+              if ((at + kBlockSize - 1 <= un.pos0 || at > last) &&
+                  (old + kBlockSize - 1 <= un.pos0 || old > last))
+                continue;
+              auto piece = [&](int i) {
+                const int key = pg * kBlockSize + i * kRows + r;
+                return reinterpret_cast<uint4*>(tile + (c >> 3) * Gm::kHalfBytes + key * 128 +
+                                                (((c & 7) ^ (key & 7)) << 4));
+              };
+              uint32_t bad = 0;
 #pragma unroll 4
-                for (int i = 0; i < kBlockSize / kRows; ++i) {
-                  const int key = pg * kBlockSize + i * kRows + r;
-                  uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * Gm::kHalfBytes +
-                                                       key * 128 + (((c & 7) ^ (key & 7)) << 4));
-                  const uint4 w = *at;
-                  if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
-                      nonfinite_bf16x2(w.w)) {
-                    found = true;
-                    *at = make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y), finite_bf16x2(w.z),
-                                     finite_bf16x2(w.w));
-                  }
-                }
+              for (int i = 0; i < kBlockSize / kRows; ++i) {
+                const uint4 w = *piece(i);
+                bad |= nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
+                       nonfinite_bf16x2(w.w);
+              }
+              if (bad == 0) continue;
+              found = true;
+#pragma unroll 1
+              for (int i = 0; i < kBlockSize / kRows; ++i) {
+                const uint4 w = *piece(i);
+                *piece(i) = make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y),
+                                       finite_bf16x2(w.z), finite_bf16x2(w.w));
               }
             }
             tc::fence_proxy_async_smem();
@@ -946,7 +979,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll 1
                 for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
                   const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
-                  const int end = id == p.num_blocks ? 0 : un.L - issued * kPromptTile;
+                  // what no query row of the unit sees comes as zeros
+                  const int end = id == p.num_blocks ? 0 : last + 1 - issued * kPromptTile;
+                  const int begin =
+                      p.window > 0 ? un.pos0 - p.window + 1 - issued * kPromptTile : 0;
                   const uint8_t* src = static_cast<const uint8_t*>(p.v_pool) +
                                        (static_cast<size_t>(id == p.num_blocks ? 0 : id) * p.Hkv +
                                         un.head) * (kBlockSize * D * 2) + lane * 16;
@@ -954,7 +990,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                   for (int i = 0; i < kBlockSize / kRows; ++i) {
                     const int key = pg * kBlockSize + i * kRows + r;
                     cp_async_16(tile + key * 128 + (((c & 7) ^ (key & 7)) << 4), src + i * 512,
-                                key < end ? 16u : 0u);
+                                key >= begin && key < end ? 16u : 0u);
                   }
                 }
                 cp_async_commit();
@@ -1100,44 +1136,75 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       if constexpr (KV8) vs = __ldg(p.v_scale + un.head);
       // (a partition without a key of this row, or with scores of -inf alone, has no weights)
       const float inv = sum == 0.f && un.parts > 1 ? 1.f : __frcp_rn(sum);
-      const size_t row =
-          static_cast<size_t>(un.row0 + s * p.sub_tokens + tok) * p.Hq + un.head * p.G + g;
+      // Four lanes exchange 16-byte pieces of their rows, so that they write 64 bytes of one row
+      // at a time: a store that touches 32 rows takes 32 cycles, and there is nothing beside it.
+      const bool whole = un.parts == 1;
+      const size_t row0 =
+          static_cast<size_t>(un.row0 + s * p.sub_tokens) * p.Hq + un.head * p.G;
+      const size_t stride = whole ? D * 2 : static_cast<size_t>(p.max_parts) * D * 4;
+      uint8_t* const dst = whole ? static_cast<uint8_t*>(p.out) + row0 * stride
+                                 : reinterpret_cast<uint8_t*>(p.part_o) + row0 * stride +
+                                       un.part * (D * 4);
+      int ln = lane, rel = live ? tok * p.Hq + g : -1;  // this row, from row0
+      // (what follows from the two is not to be kept in registers over the tiles)
+      asm volatile("" : "+r"(ln), "+r"(rel));
+      auto put = [&](int piece, const uint32_t* x) {    // 64 bytes of every lane's row
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        swap_pieces<1>(v[0], v[1], ln);
+        swap_pieces<1>(v[2], v[3], ln);
+        swap_pieces<2>(v[0], v[2], ln);
+        swap_pieces<2>(v[1], v[3], ln);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int to_row = __shfl_sync(0xffffffffu, rel, (ln & 28) + k);
+          if (to_row >= 0)
+            *reinterpret_cast<uint4*>(dst + to_row * stride + piece * 64 + (ln & 3) * 16) = v[k];
+        }
+      };
 #pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
+      for (int i = 0; i < D / 64; ++i) {
+        uint32_t o[2][32];
         if (any) {
-          tc::tmem_ld32(to + i * 32, o);
+          tc::tmem_ld32(to + i * 64, o[0]);
+          tc::tmem_ld32(to + i * 64 + 32, o[1]);
           tc::tmem_wait_ld();
-          tmem_wait_regs(o);
-          if (i + 1 == D / 32) {
+          tmem_wait_regs(o[0]);
+          tmem_wait_regs(o[1]);
+          if (i + 1 == D / 64) {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.o_free[s]);
           }
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            uint32_t* x = &o[k / 32][k % 32];
+            uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                   pack_f32x2(inv, inv));
+            if constexpr (KV8) y = mul_f32x2(y, pack_f32x2(vs, vs));
+            x[0] = static_cast<uint32_t>(y);
+            x[1] = static_cast<uint32_t>(y >> 32);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) o[k / 32][k % 32] = 0u;
         }
+        if (whole) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          o[k] = any ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
-        if constexpr (KV8) {
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * vs);
-        }
-        if (live && un.parts == 1) {
-          uint32_t y[16];
+            for (int k = 0; k < 16; ++k)
+              o[h][k] = pack_bf16x2_rn(__uint_as_float(o[h][2 * k]),
+                                       __uint_as_float(o[h][2 * k + 1]));
+            put(2 * i + h, o[h]);
+          }
+        } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            y[k] = pack_bf16x2_rn(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D) + i * 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-        } else if (live) {
-          const size_t at = row * p.max_parts + un.part;
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D) + i * 8;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (i == 0) p.part_ml[at] = make_float2(ref - Gm::kShift, sum);
+          for (int h = 0; h < 4; ++h) put(4 * i + h, o[h / 2] + h % 2 * 16);
+          if (i == 0 && live)
+            p.part_ml[(row0 + rel) * p.max_parts + un.part] = make_float2(ref - Gm::kShift, sum);
         }
       }
       // the infinities and NaN that were taken out of V, for the rows that see them: a row at a
@@ -1167,8 +1234,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               }
             }
           }
-          const size_t out_row = row + (static_cast<size_t>(tk) * p.Hq + rr % p.G) -
-                                 (static_cast<size_t>(tok) * p.Hq + g);
+          const size_t out_row = row0 + static_cast<size_t>(tk) * p.Hq + rr % p.G;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             const int d = k * 32 + lane;
