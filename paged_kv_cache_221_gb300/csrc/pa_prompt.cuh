@@ -17,8 +17,8 @@
 // Roles of a CTA (one per SM, which goes on to further units):
 //   warps 0-3, 4-7  softmax of the first, the second tile: thread = row.  A tile's weights are
 //                   taken with the reference of the last ones at once; only where their sum
-//                   shows one past 2^15, at the mask's border and at a unit's start is the
-//                   row's maximum looked for, which then becomes the reference if it is far
+//                   shows one past 2^15 and at a unit's start is the row's
+//                   maximum looked for, which then becomes the reference if it is far
 //                   above it.  O is then rescaled in tensor memory, which no product is using
 //                   at that time: S of the next keys is issued behind P . V of the last ones.
 //   warp 8          finds the units, loads Q and the K tiles by TMA, 16 keys per page box,
@@ -63,8 +63,8 @@ struct PromptGeo {
   static constexpr int kHalves = D / 64;                 // 64-dim halves of a row (128 bytes)
   static constexpr int kHalfBytes = kPromptTile * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
-  static constexpr int kKStages = KV8 ? 2 : 3;           // K tiles ready or in flight
-  static constexpr int kVStages = 2;
+  static constexpr int kKStages = 2;                     // K tiles ready or in flight
+  static constexpr int kVStages = KV8 ? 2 : 3;
   static constexpr int kRawStages = KV8 ? 2 : 0;         // FP8 tiles in flight
   static constexpr int kRawBytes = kPromptTile * D;
   static constexpr int kShift = KV8 ? 7 : 0;             // weights carry 2^kShift
@@ -999,7 +999,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 if (issued - done < Gm::kVStages && issued < un.t1) continue;
               }
             }
-            if (issued - done > 1)
+            if (issued - done > 2)
+              cp_async_wait<2>();
+            else if (issued - done > 1)
               cp_async_wait<1>();
             else
               cp_async_wait<0>();
@@ -1051,35 +1053,35 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         __syncwarp();
         tc::fence_after_sync();
         const bool masked = prompt_masked(p, t, sub.first, sub.first + sub.n - 1);
-        bool look = masked || !steady;                  // for the maximum
+        bool look = !steady;                            // for the maximum
         PromptScores<KV8> sc;
         while (true) {
           sc.load(ts);
           // A score's factor is applied with the reference's subtraction, in one rounding; with
           // a factor that is not positive, or references that leave no bits behind the point, it
           // comes first.
-          float cc = c;
-          if (look) {
-            float m;
-            bool first = !(c > 0.f), border = masked;
-            while (true) {
-              if (first) {
-                sc.multiply(cc);
-                cc = 1.f;
-              }
-              if (border) {
-                const int hi = pos - t * kPromptTile;   // columns lo < i <= hi are visible
-                sc.mask(p.window > 0 ? hi - p.window : -1, hi);
-                border = false;
-              }
-              m = sc.largest() * cc;
-              if (first || !__any_sync(0xffffffffu, fabsf(m) > kPromptExact &&
-                                                        fabsf(m) < CUDART_INF_F))
-                break;
-              first = true;
+          float cc = c, m = 0.f;
+          bool first = !(c > 0.f), border = masked;
+          while (true) {
+            if (first) {
+              sc.multiply(cc);
+              cc = 1.f;
             }
+            if (border) {
+              const int hi = pos - t * kPromptTile;     // columns lo < i <= hi are visible
+              sc.mask(p.window > 0 ? hi - p.window : -1, hi);
+              border = false;
+            }
+            if (!look) break;
+            m = sc.largest() * cc;
+            if (first || !__any_sync(0xffffffffu, fabsf(m) > kPromptExact &&
+                                                      fabsf(m) < CUDART_INF_F))
+              break;
+            first = true;
+          }
+          if (look) {
             // by 8 at least, unless weights went past their limit; the first finite score always
-            const bool move = m > ref + (steady && !masked ? 0.f : 8.f);
+            const bool move = m > ref + (steady ? 0.f : 8.f);
             if (__any_sync(0xffffffffu, move)) {
               const float f = move ? hw_exp2(ref - m) : 1.f;
               ref = move ? m : ref;
@@ -1108,7 +1110,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           sc.template weights<0, 32>([&](int k) {
             most[k & 3] = max3(most[k & 3], sc.score(64 + 2 * k), sc.score(65 + 2 * k));
           });
-          const float m = fmaxf(max3(most[0], most[1], most[2]), most[3]);
+          m = fmaxf(max3(most[0], most[1], most[2]), most[3]);
           const bool fine = sc.total() <= kPromptLimit && fmaf(m, cc, off) <= 15.f;
           if (look || __all_sync(0xffffffffu, fine)) break;
           look = true;
@@ -1265,52 +1267,52 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 // ---------------------------------------------------------------- merge of partitions
 // One warp per query row of a pair of tiles whose keys were cut: partition i holds O_i
 // (normalised), the reference m_i (log2 units) and the sum l_i, and counts w_i = l_i 2^(m_i - M).
-// Eight partitions' values are on their way at once.
-constexpr int kPromptMergeWarps = 4;
+// It waits for memory three times at least (unit, statistics, values), so the first sixteen
+// partitions' values are asked for with the statistics, before their weights are known.
+constexpr int kPromptMergeWarps = 4, kPromptMergeParts = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kPromptMergeWarps * 32) prompt_merge_kernel(const PromptParams p) {
   constexpr int DL = D / 32;
   using Vec = std::conditional_t<DL == 4, float4, float2>;
-  grid_dependency_wait();
   PromptUnit un;
   bool bad;
-  if (!prompt_unit(p, blockIdx.x, un, &bad) || un.parts == 1) return;
+  const bool some = prompt_unit(p, blockIdx.x, un, &bad) && un.parts > 1;
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * kPromptMergeWarps + (threadIdx.x >> 5);
-  if (r >= un.ntok * p.G) return;
+  if (!some || r >= un.ntok * p.G) return;
   const size_t row = static_cast<size_t>(un.row0 + r / p.G) * p.Hq + un.head * p.G + r % p.G;
   const float2* ml = p.part_ml + row * p.max_parts;
   const Vec* src = reinterpret_cast<const Vec*>(p.part_o + row * p.max_parts * D) + lane;
+  // a partition without weights counts nothing, unless a value was infinite or NaN
   float M = -CUDART_INF_F;
-  for (int i = lane; i < un.parts; i += 32) {
-    const float2 x = __ldcg(ml + i);
-    M = fmaxf(M, x.y == 0.f ? -CUDART_INF_F : x.x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[DL] = {}, total = 0.f;
-  for (int i0 = 0; i0 < un.parts; i0 += 8) {
-    Vec v[8];
-    float w[8];
+  for (int i0 = 0; i0 < un.parts; i0 += kPromptMergeParts) {
+    Vec v[kPromptMergeParts];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = i0 + k;
-      w[k] = 0.f;
-      v[k] = Vec{};
-      if (i < un.parts) {
+    for (int k = 0; k < kPromptMergeParts; ++k)
+      v[k] = i0 + k < un.parts ? __ldcg(src + static_cast<size_t>(i0 + k) * 32) : Vec{};
+    if (i0 == 0) {
+      for (int i = lane; i < un.parts; i += 32) {
         const float2 x = __ldcg(ml + i);
-        v[k] = __ldcg(src + static_cast<size_t>(i) * 32);
-        // a partition without weights counts nothing, unless a value was infinite or NaN
-        if (x.y != 0.f) w[k] = x.y * hw_exp2(x.x - M);
+        M = fmaxf(M, x.y == 0.f ? -CUDART_INF_F : x.x);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    }
+    float w = 0.f;                                      // of partition i0 + lane
+    if (lane < kPromptMergeParts && i0 + lane < un.parts) {
+      const float2 x = __ldcg(ml + i0 + lane);
+      if (x.y != 0.f) w = x.y * hw_exp2(x.x - M);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      total += w[k];
+    for (int k = 0; k < kPromptMergeParts; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      total += wk;
       const float* f = reinterpret_cast<const float*>(&v[k]);
 #pragma unroll
-      for (int d = 0; d < DL; ++d) acc[d] += w[k] * f[d];
+      for (int d = 0; d < DL; ++d) acc[d] += wk * f[d];
     }
   }
   const float inv = __frcp_rn(total);
