@@ -16,11 +16,11 @@
 //
 // Roles of a CTA (one per SM, which goes on to further units):
 //   warps 0-3, 4-7  softmax of the first, the second tile: thread = row.  A tile's weights are
-//                   taken with the reference of the last ones at once; only where their sum
-//                   shows one past 2^15 and at a unit's start is the row's
-//                   maximum looked for, which then becomes the reference if it is far
-//                   above it.  O is then rescaled in tensor memory, which no product is using
-//                   at that time: S of the next keys is issued behind P . V of the last ones.
+//                   taken with the reference of the last ones at once; only where they pass
+//                   2^15 and at a unit's start is the row's maximum looked for, which then
+//                   becomes the reference if it is far above it.  O is then rescaled in tensor
+//                   memory, which no product is using at that time: S of the next keys is
+//                   issued behind P . V of the last ones.
 //   warp 8          finds the units, loads Q and the K tiles by TMA, 16 keys per page box,
 //                   through the block table.
 //   warp 9          issues the MMAs: per K/V tile P.V (in two halves, the first while the last
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 bad |= nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
                        nonfinite_bf16x2(w.w);
               }
-              if (bad == 0) continue;
+              if (__builtin_expect(bad == 0, 1)) continue;
               found = true;
 #pragma unroll 1
               for (int i = 0; i < kBlockSize / kRows; ++i) {
@@ -1061,27 +1061,28 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           // a factor that is not positive, or references that leave no bits behind the point, it
           // comes first.
           float cc = c, m = 0.f;
-          bool first = !(c > 0.f), border = masked;
-          while (true) {
-            if (first) {
-              sc.multiply(cc);
-              cc = 1.f;
+          // (unlikely, so that the code of most tiles is in one piece)
+          if (__builtin_expect(look || masked, 0)) {
+            bool first = !(c > 0.f), border = masked;
+            while (true) {
+              if (first) {
+                sc.multiply(cc);
+                cc = 1.f;
+              }
+              if (border) {
+                const int hi = pos - t * kPromptTile;   // columns lo < i <= hi are visible
+                sc.mask(p.window > 0 ? hi - p.window : -1, hi);
+                border = false;
+              }
+              if (!look) break;
+              m = sc.largest() * cc;
+              if (first || !__any_sync(0xffffffffu, fabsf(m) > kPromptExact &&
+                                                        fabsf(m) < CUDART_INF_F))
+                break;
+              first = true;
             }
-            if (border) {
-              const int hi = pos - t * kPromptTile;     // columns lo < i <= hi are visible
-              sc.mask(p.window > 0 ? hi - p.window : -1, hi);
-              border = false;
-            }
-            if (!look) break;
-            m = sc.largest() * cc;
-            if (first || !__any_sync(0xffffffffu, fabsf(m) > kPromptExact &&
-                                                      fabsf(m) < CUDART_INF_F))
-              break;
-            first = true;
-          }
-          if (look) {
             // by 8 at least, unless weights went past their limit; the first finite score always
-            const bool move = m > ref + (steady ? 0.f : 8.f);
+            const bool move = look && m > ref + (steady ? 0.f : 8.f);
             if (__any_sync(0xffffffffu, move)) {
               const float f = move ? hw_exp2(ref - m) : 1.f;
               ref = move ? m : ref;
@@ -1100,7 +1101,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 }
               }
             }
-            steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
+            if (look) steady = __all_sync(0xffffffffu, c > 0.f && fabsf(ref) <= kPromptExact);
           }
           const float off = ref == -CUDART_INF_F ? 0.f : Gm::kShift - ref;
           sc.begin(cc, off);
@@ -1211,7 +1212,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       }
       // the infinities and NaN that were taken out of V, for the rows that see them: a row at a
       // time, its dims over the lanes
-      if (special && any) {
+      if (__builtin_expect(special && any, 0)) {
         __syncwarp();
         float add[D / 32];
         int seen = -1;                                  // token that they are of
