@@ -500,6 +500,22 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
                   e4m3x2_to_f16x2(w.w >> 16));
 }
 
+// 16 bytes of shared memory (the tiles' addresses are computed, and as generic ones a tile took
+// three times as long to widen).
+__device__ __forceinline__ uint4 load16(uint32_t at) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "r"(at)
+               : "memory");
+  return w;
+}
+__device__ __forceinline__ void store16(uint32_t at, uint4 w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z),
+               "r"(w.w)
+               : "memory");
+}
+
 // The byte mask of the codes 0x7F and 0xFF (NaN) in a word.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x01010101u & 0x80808080u) >> 7) * 0xFFu;
@@ -508,7 +524,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 // A K tile: keys x D codes, as TMA left them, to [half][key][64 dims] f16 with the 128-byte
 // swizzle.  Consecutive lanes take what lies in different banks on both sides.
 template <int D>
-__device__ __forceinline__ void widen_keys(uint8_t* dst, const uint8_t* raw, int lane, int worker,
+__device__ __forceinline__ void widen_keys(uint32_t dst, uint32_t raw, int lane, int worker,
                                            int workers) {
   constexpr int C = D / 16;                    // 16-dim pieces of a row
 #pragma unroll 1
@@ -523,25 +539,25 @@ __device__ __forceinline__ void widen_keys(uint8_t* dst, const uint8_t* raw, int
     }
     const int at = C == 8 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + c * 16;
     uint4 lo, hi;
-    widen16(*reinterpret_cast<const uint4*>(raw + at), lo, hi);
-    uint8_t* row = dst + (c >> 2) * (kPromptTile * 128) + key * 128;
+    widen16(load16(raw + at), lo, hi);
+    const uint32_t row = dst + (c >> 2) * (kPromptTile * 128) + key * 128;
     const int ch = (c & 3) * 2;
-    *reinterpret_cast<uint4*>(row + ((ch ^ (key & 7)) << 4)) = lo;
-    *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (key & 7)) << 4)) = hi;
+    store16(row + ((ch ^ (key & 7)) << 4), lo);
+    store16(row + (((ch + 1) ^ (key & 7)) << 4), hi);
   }
 }
 
 // A V tile: pages of D rows of 16 keys, to [half of 64 keys][dim][64 keys] f16.  At a border of
 // the mask the codes from key `end` of the tile on and NaN become 0; whether there was a NaN.
 template <int D>
-__device__ __forceinline__ bool widen_values(uint8_t* dst, const uint8_t* raw, int lane, int worker,
+__device__ __forceinline__ bool widen_values(uint32_t dst, uint32_t raw, int lane, int worker,
                                              int workers, bool border, int end) {
   bool found = false;
 #pragma unroll 1
   for (int i = worker; i < kPromptTile / kBlockSize * D / 32; i += workers) {
     const int pg = i / (D / 32), d = i % (D / 32) * 32 + lane;
-    uint4 w = *reinterpret_cast<const uint4*>(raw + (pg * D + d) * 16);
-    if (border) {
+    uint4 w = load16(raw + (pg * D + d) * 16);
+    if (__builtin_expect(border, 0)) {
       uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -554,22 +570,22 @@ __device__ __forceinline__ bool widen_values(uint8_t* dst, const uint8_t* raw, i
     }
     uint4 lo, hi;
     widen16(w, lo, hi);
-    uint8_t* row = dst + (pg >> 2) * (D * 128) + d * 128;
+    const uint32_t row = dst + (pg >> 2) * (D * 128) + d * 128;
     const int ch = (pg & 3) * 2;
-    *reinterpret_cast<uint4*>(row + ((ch ^ (d & 7)) << 4)) = lo;
-    *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (d & 7)) << 4)) = hi;
+    store16(row + ((ch ^ (d & 7)) << 4), lo);
+    store16(row + (((ch + 1) ^ (d & 7)) << 4), hi);
   }
   return found;
 }
 
 // A query row, D bf16 in halves of 128 swizzled bytes, to f16 times 2^-e; returns e.
 template <int D>
-__device__ __forceinline__ int widen_query(uint8_t* tile, int row) {
+__device__ __forceinline__ int widen_query(uint32_t tile, int row) {
   float most = 0.f;
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
-    const uint4 w = *reinterpret_cast<const uint4*>(
-        tile + (c >> 3) * (kPromptTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    const uint4 w =
+        load16(tile + (c >> 3) * (kPromptTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -582,14 +598,14 @@ __device__ __forceinline__ int widen_query(uint8_t* tile, int row) {
   const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
-    uint4* at = reinterpret_cast<uint4*>(
-        tile + (c >> 3) * (kPromptTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-    uint4 w = *at;
+    const uint32_t at =
+        tile + (c >> 3) * (kPromptTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    uint4 w = load16(at);
     uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       x[k] = half2_bits(__floats2half2_rn(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up));
-    *at = w;
+    store16(at, w);
   }
   return e;
 }
@@ -886,7 +902,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               if (!wait.all_ok()) break;
               for (int r = aux * 32 + lane; r < p.sub_tokens * p.G; r += Gm::kAux * 32)
                 ms.q_exp[ui & 1][s][r] =
-                    static_cast<int8_t>(widen_query<D>(smem + s * Gm::kTileBytes, r));
+                    static_cast<int8_t>(widen_query<D>(smem_u32(smem) + s * Gm::kTileBytes, r));
               tc::fence_proxy_async_smem();
             }
             __syncwarp();
@@ -902,13 +918,13 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u);
               wait(kv ? &ms.v_empty[st] : &ms.k_empty[st], (use & 1u) ^ 1u);
               if (!wait.all_ok()) break;
-              const uint8_t* raw = smem + Gm::kRawOff + rs * Gm::kRawBytes;
+              const uint32_t base = smem_u32(smem), raw = base + Gm::kRawOff + rs * Gm::kRawBytes;
               if (kv)
-                found |= widen_values<D>(smem + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux,
+                found |= widen_values<D>(base + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux,
                                          Gm::kAux, prompt_masked(p, t, un.pos0, last),
                                          un.L - t * kPromptTile);
               else
-                widen_keys<D>(smem + Gm::kKOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux);
+                widen_keys<D>(base + Gm::kKOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux);
               tc::fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -927,7 +943,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           // a tile's copies have landed: keys that some query rows see and some must not, the
           // last rows' newest and the first rows' oldest, are made finite
           auto finish = [&](int t, int st) {
-            uint8_t* tile = smem + Gm::kVOff + st * Gm::kTileBytes;
+            const uint32_t tile = smem_u32(smem) + Gm::kVOff + st * Gm::kTileBytes;
 #pragma unroll 1
             for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
               const int at = t * kPromptTile + pg * kBlockSize;
@@ -937,13 +953,12 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 continue;
               auto piece = [&](int i) {
                 const int key = pg * kBlockSize + i * kRows + r;
-                return reinterpret_cast<uint4*>(tile + (c >> 3) * Gm::kHalfBytes + key * 128 +
-                                                (((c & 7) ^ (key & 7)) << 4));
+                return tile + (c >> 3) * Gm::kHalfBytes + key * 128 + (((c & 7) ^ (key & 7)) << 4);
               };
               uint32_t bad = 0;
 #pragma unroll 4
               for (int i = 0; i < kBlockSize / kRows; ++i) {
-                const uint4 w = *piece(i);
+                const uint4 w = load16(piece(i));
                 bad |= nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
                        nonfinite_bf16x2(w.w);
               }
@@ -951,9 +966,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               found = true;
 #pragma unroll 1
               for (int i = 0; i < kBlockSize / kRows; ++i) {
-                const uint4 w = *piece(i);
-                *piece(i) = make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y),
-                                       finite_bf16x2(w.z), finite_bf16x2(w.w));
+                const uint4 w = load16(piece(i));
+                store16(piece(i), make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y),
+                                             finite_bf16x2(w.z), finite_bf16x2(w.w)));
               }
             }
             tc::fence_proxy_async_smem();
