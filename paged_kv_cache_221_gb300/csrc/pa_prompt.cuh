@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
   if (warp == Gm::kSoftmaxWarps + 1) tc::tmem_alloc(&ms.tmem_base, Gm::kTmemCols);
   // rows of the Q tiles that hold no query row stay zero
   for (int i = threadIdx.x; i < 2 * Gm::kTileBytes / 16; i += Gm::kThreads)
-    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    store16(smem_u32(smem) + i * 16, make_uint4(0, 0, 0, 0));
   tc::fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.q_wide[ui & 1][s]);
           }
-          for (int t = un.t0; t < un.t1 && wait.ok(); ++t, ++tiles) {
+          for (int t = un.t0; t < un.t1; ++t, ++tiles) {
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int rs = item % Gm::kRawStages;
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                                                                      : Gm::kKStages));
               wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u);
               wait(kv ? &ms.v_empty[st] : &ms.k_empty[st], (use & 1u) ^ 1u);
-              if (!wait.all_ok()) break;
+              __syncwarp();
               const uint32_t base = smem_u32(smem), raw = base + Gm::kRawOff + rs * Gm::kRawBytes;
               if (kv)
                 found |= widen_values<D>(base + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux,
@@ -1025,7 +1025,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           }
           cp_async_wait<0>();
         }
-        if (!wait.ok()) break;
+        if (!wait.all_ok()) break;
         if (found) *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
         __syncwarp();
         if (lane == 0) {
