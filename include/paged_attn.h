@@ -629,7 +629,9 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
  * multiple of 128; 0 = chosen for the sizes: none unless there are few query
  * tiles), whose results a second kernel joins through the workspace
  * (pa_prompt_workspace_size bytes, 256-byte aligned; without one and with
- * partition_size 0 nothing is cut).  Softmax statistics and accumulation are
+ * partition_size 0 nothing is cut).  The workspace also holds the counter by
+ * which the kernel shares many query tiles out, so calls that may overlap on
+ * the GPU need workspaces of their own.  Softmax statistics and accumulation are
  * fp32; the weights are rounded to bf16 where they meet the values.  A slot
  * that a query token must not see does not reach it, whatever it holds; a NaN
  * or infinity that it sees does.

@@ -199,8 +199,13 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
   if (partition_size > 0) {
     pl.split = std::min(tiles, partition_size / kPromptTile);
   } else if (scratch) {
-    const long long pairs = slots * hkv;
-    if (pairs < 152) pl.split = std::max(4, ceil_div(tiles, std::max<long long>(1, 152 / pairs)));
+    // as many partitions, of four K/V tiles at least, as give every SM a unit with the fewest
+    // pairs of tiles that there can be (the device knows them alone).  Measured, 64 tokens behind
+    // 16384 each, 32 query heads over 8, whole / cut: one sequence 201 / 29 us, 4 203 / 80, 8
+    // 205 / 142; but 12 207 / 219, 16 215 / 272, 32 432 / 519
+    const long long pairs = hkv * std::max(std::min<long long>(num_seqs, num_tokens),
+                                           num_tokens / pair);
+    if (pairs < 152) pl.split = std::max(4, ceil_div(tiles, 152 / pairs));
   }
   pl.split = std::min(pl.split, tiles);
   pl.max_parts = ceil_div(tiles, pl.split);
@@ -210,7 +215,12 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
     pl.off_ml = round256(rows * head_dim * sizeof(float));
     pl.bytes = pl.off_counter = pl.off_ml + round256(rows * sizeof(float2));
   }
-  if (scratch && pl.units > 304) {
+  // CTAs take units as they come free instead of every 152nd where the units are few or long, so
+  // that what is left over counts; the counter's reset is a launch of 3 us, and short units do not
+  // hide a claim.  Measured, as they come / every 152nd: 1 prompt of 2048 tokens 37 / 47 us, 4 of
+  // 1280 64 / 75, 12 FP8 ones up to 4096 583 / 604, 1 of 16384 1385 / 1461; but 24 of 512 97 / 87,
+  // 24 of 2048 700 / 684, 4 behind windows of 1000 360 / 350.
+  if (scratch && pl.units > 152 && pl.split > 8 && (pl.units < 8 * 152 || pl.split > 16)) {
     pl.counted = true;
     pl.bytes += 256;
   }

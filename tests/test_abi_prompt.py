@@ -65,7 +65,7 @@ def test_prompt_workspace(lib):
     assert size(psize=4096) == 0
     assert size(mcl=128) == 0
     assert size(window=4096) == size() and size(window=100) < size()
-    assert size(N=12000, psize=0) == 0                   # enough query tiles: nothing is cut
+    assert size(N=12000, mcl=512, psize=0) == 0          # enough query tiles: nothing is cut
     assert size(N=200000, psize=0) == 256                # many: a counter to take them by
     assert size(N=1, B=1, psize=0) > 0
     for kw in (dict(N=0), dict(B=0), dict(hq=5), dict(psize=100), dict(psize=-1), dict(BS=8),
