@@ -26,12 +26,11 @@
 //   warp 9          issues the MMAs: per K/V tile P.V (in two halves, the first while the last
 //                   quarter of the weights is computed) then the next S of the first tile, the
 //                   same of the second.
-//   warps 10, 11    copy the V tiles, rows behind the context as zeros.  At the mask's border
-//                   infinities and NaN of V rows that some query row must not see are taken
-//                   out (0 * inf would reach it); the rows that see those keys get them added
-//                   at the end.
+//   warps 10, 11    copy the V tiles, rows that no query row sees as zeros.  Of those that some
+//                   see and some must not, infinities and NaN are taken out (0 * inf would reach
+//                   the others); the rows that see them get them added at the end.
 //
-// FP8 pages.  The products take f16, of which every E4M3 value is one: warps 10 and 11 widen
+// FP8 pages.  The products take f16, of which every E4M3 value is one: warps 10 to 15 widen
 // each tile from where TMA left it into the ring that the MMAs read (K rows as they are; V
 // pages are stored by head dim, so that tile becomes a K-major operand), and the query rows in
 // place, each times a power of two that puts its largest element at 2^7 .. 2^8 (a bf16 value
@@ -40,6 +39,23 @@
 //
 // Weights are rounded to bf16 (2^-8 of each at most) for the second product, as are the
 // values they meet (f16 for FP8 pages: 2^-11); statistics and accumulators are fp32.
+//
+// What bounds it.  A K/V tile of a pair is 2048 cycles of products.  A tile's weights take 1350
+// (an exponential is 4 cycles per warp instruction and scheduler; the rest beside it), its P . V
+// and next S with their hand-overs as much again, and the two tiles of a pair alternate: about
+// 2700 in all (3500 for FP8 pages, whose tiles take two thirds of that to widen).  A unit's start
+// and end are 10000 more: outputs written, 3500, and the first maximum, while no product runs.
+// 32 query heads over 8 of 128 dims: 16384 tokens 1385 to 1510 us by the clock that the power
+// limit leaves (1.59 to 1.46 PFLOP/s; a library matrix product in a loop 1.69), 24 prompts of
+// 128 to 2048 tokens 304 us (0.98), 12 of 512 to 4096 over FP8 pages 582 us (1.11), 33 tokens
+// behind 65519 65 us (4.1 TB/s).
+//
+// Measured on the way, 16384 tokens or as said: V by TMA boxes like K, 2300 cycles of
+// the TMA unit for a K/V tile by themselves (a box of 16 keys is about 70 whatever its bytes); three K and two V stages 1460
+// against 1417 us; two threads per row (16 softmax warps) 1466; the rare code between that of most
+// tiles 1430 against 1397, since the roles share one instruction cache; generic instead of
+// shared-memory instructions in widening 653 against 590 (FP8); three lanes' pieces at a time
+// there 766, since registers spill.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -1284,7 +1300,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 // One warp per query row of a pair of tiles whose keys were cut: partition i holds O_i
 // (normalised), the reference m_i (log2 units) and the sum l_i, and counts w_i = l_i 2^(m_i - M).
 // It waits for memory three times at least (unit, statistics, values), so the first sixteen
-// partitions' values are asked for with the statistics, before their weights are known.
+// partitions' values are asked for with the statistics, before their weights are known: 19
+// partitions of 1056 rows 8.5 us out of DRAM, against 12.3 with eight after the weights.
 constexpr int kPromptMergeWarps = 4, kPromptMergeParts = 16;
 
 template <int D>

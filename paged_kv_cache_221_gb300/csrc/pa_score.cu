@@ -20,8 +20,11 @@
 // -inf) is made again from the elements above t and, in the order of the row, as many equal
 // ones as are missing.
 //
-// The kernel is bound by reading the logits.  A cluster of CTAs shares a row when there are
-// few rows.
+// The kernel is bound by reading the logits.  A cluster of CTAs shares a row when there are few
+// and long ones.  2048 rows of 128256 bf16 with 20 alternatives 108 us (4.9 TB/s; 97 without
+// alternatives); 64 of 128256 fp32 with 5 12.4 us, a launch and seven barriers on top of 5 us of
+// reading; 1000 of 32003 fp16 18.5 us.  CTAs of 512 threads 157 us for the first (with 256 others
+// stream while one joins its row), of 128 threads 161, five or six CTAs per SM as four.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
