@@ -639,7 +639,8 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
  * num_q_heads / num_kv_heads at most 128, num_blocks * num_kv_heads * 16 below
  * 2^31.  A sequence with context_lens[b] < T_b or > max_context_len, or with
  * starts out of order or outside [0, num_tokens], sets PA_ERR_BOUNDS on the
- * device and its rows are skipped; a block id outside the pool sets it too and
+ * device and its rows are skipped (with starts out of order, those of sequences
+ * behind it may be too); a block id outside the pool sets it too and
  * leaves that sequence's rows unspecified.
  */
 pa_status pa_prompt_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -683,8 +684,8 @@ size_t pa_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, i
  *
  * num_tokens is the host's bound on the sum of new_lens.  A call that cannot be
  * met (too few free blocks: PA_ERR_OUT_OF_BLOCKS on the device; more tokens than
- * num_tokens or than a table holds, a negative length, a last block outside the
- * pool: PA_ERR_BOUNDS) changes no state, and its outputs are those of an empty
+ * num_tokens or than a table holds, a negative length, a partly filled last
+ * block outside the pool or without an owner: PA_ERR_BOUNDS) changes no state, and its outputs are those of an empty
  * batch: starts 0, slots and positions -1, copies (0, 0).  num_seqs is at most
  * 12288; a sequence may be listed once.
  */

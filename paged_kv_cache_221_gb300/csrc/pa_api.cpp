@@ -924,7 +924,7 @@ pa_status pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int
   if (max_blocks_per_seq > (1 << 26) || num_blocks > (1 << 30) || num_tokens > (1 << 30))
     return PA_ERR_UNSUPPORTED;
   if (num_seqs > 0 && (!block_tables || !context_lens || !ref_counts || !new_lens ||
-                       !block_copies))
+                       !block_copies || new_lens == context_lens))
     return PA_ERR_INVALID_ARG;
   if (num_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID_ARG;
   StepParams p{};

@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = ms.tmem_base;
-  grid_launch_dependents();
+  if (p.max_parts > 1) grid_launch_dependents();       // the merge
 
   if (warp >= Gm::kSoftmaxWarps) {
     regs_fewer<Gm::kOtherRegs>();
@@ -1060,6 +1060,13 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
     const uint32_t ts = tmem + lanes + s * kPromptTile, to = tmem + lanes + Gm::kO + s * D;
     const int tok = r / p.G, g = r - tok * p.G;         // of this row
     PromptWaits wait;                                   // lanes agree to go on where they vote
+    // with starts out of order a search may miss sequences without meeting the wrong ones
+    if (blockIdx.x == 0) {
+      for (int b = threadIdx.x; b < p.num_seqs; b += Gm::kSoftmaxWarps * 32)
+        if (__ldg(p.query_starts + b) > __ldg(p.query_starts + b + 1))
+          atomicOr(&g_pa_err, kErrBounds);
+      __syncwarp();
+    }
     uint32_t n_s = 0, n_o = 0;                          // S and O tiles taken
     for (int ui = 0; wait.ok(); ++ui) {
       wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);

@@ -126,7 +126,7 @@ __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThre
     sh.many = 0;
     sh.num_shared = 0;
   }
-  grid_launch_dependents();
+  if (!p.slots_here) grid_launch_dependents();          // the slots' launch
   __syncthreads();
 
   // ------------------------------------------------- free blocks of this thread's run of the pool
@@ -159,7 +159,9 @@ __global__ void __cluster_dims__(kStepCluster, 1, 1) __launch_bounds__(kStepThre
     last[b] = id;
     len[b] = L;
     start[b] = n;
-    if (id >= 0 && p.ref_counts[id] > 1) at[atomicAdd(&sh.num_shared, 1)] = b;
+    const int owners = id >= 0 ? p.ref_counts[id] : 1;
+    if (owners < 1) sh.fail = kErrBounds;               // it would be handed out as free
+    if (owners > 1) at[atomicAdd(&sh.num_shared, 1)] = b;
   }
   __syncthreads();
   // Below, 1024 counts at a time are summed in 32 bits: those up to 2^21 cannot carry, and the

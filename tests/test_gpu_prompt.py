@@ -249,6 +249,10 @@ def test_sequences_out_of_bounds_are_skipped():
         s = torch.tensor(starts, dtype=torch.int32, device="cuda")
         pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, s, 90)
         assert pa.get_device_error() == BOUNDS, starts
+    c = Prompts(41, [1000, 20, 30], [0, 0, 2000], 4, 2, 64)
+    s = torch.tensor([0, 1000, 50, 1050], dtype=torch.int32, device="cuda")
+    pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, s, c.most)
+    assert pa.get_device_error() == BOUNDS
     for fp8 in (False, True):
         c = Prompts(42, [40, 50, 60], [10, 20, 30], 4, 2, 64, fp8=fp8)
         want = attend(c)
@@ -367,3 +371,37 @@ def test_refusals():
                dict(q=c.q[:, :3].contiguous())):
         with pytest.raises(pa.PagedAttnError):
             call(**kw)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_units_taken_as_ctas_come_free(fp8):
+    """More query tiles than SMs: a counter in the workspace, whatever it held, on two streams at
+    once with workspaces of their own, and by two graphs in turn on one."""
+    c = Prompts(50, [1400, 0, 1300], [0, 3, 200], 16, 16, 64, fp8=fp8, behind=5)
+    d = Prompts(51, [900, 2000], [600, 0], 16, 16, 64, fp8=fp8)
+    want = [run(x)[:sum(x.new)] for x in (c, d)]
+    sizes = [pa.prompt_workspace_size(x.N, len(x.new), 16, 16, x.most, 64) for x in (c, d)]
+    assert sizes == [256, 256]
+    outs = []
+    for x in (c, d):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(attend(x))
+    torch.cuda.synchronize()
+    for x, w, o in zip((c, d), want, outs):
+        assert torch.equal(o[:sum(x.new)], w)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for x in (c, d):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = attend(x, workspace=ws, out=torch.zeros_like(x.q))
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, _out in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for x, w, (_, o) in zip((c, d), want, graphs):
+        assert torch.equal(o[:sum(x.new)], w)
+    assert pa.get_device_error() == 0

@@ -209,3 +209,32 @@ def test_refusals():
         pa.token_logprobs(x[:1].expand(4, 100), t)
     with pytest.raises(ValueError):
         pa.token_logprobs(x.cpu(), t)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_that_a_cluster_shares(dtype):
+    """Few and long rows: ties over all parts, masks, odd places, rows without results."""
+    V, N = 50001, 3
+    x, t = logits(20, N, V, dtype)
+    run((x * 2).round() / 2, t, 20)
+    for v in (0.0, torch.finfo(dtype).min):
+        run(torch.full_like(x, v), t, 32)
+    y = torch.full_like(x, -math.inf)
+    y[:, [0, 6250, 6251, 25000, 49999, 50000]] = x[:, :6]
+    run(y, t, 20)
+    run(x[:, 1:], t.clamp(max=V - 2), 20)
+    run(x[::2, 3:], t[::2].clamp(max=V - 4).contiguous(), 0)
+    for bad in (math.nan, math.inf):
+        z = x.clone()
+        z[1, 31000] = bad
+        lp, h, top, tok = pa.token_logprobs(z, t, 4)
+        assert torch.isnan(lp[1]) and torch.isnan(h[1]) and torch.isnan(top[1]).all()
+        assert ((tok >= 0) & (tok < V)).all()
+        assert torch.isfinite(lp[::2]).all() and torch.isfinite(top[::2]).all()
+    z[2] = -math.inf
+    lp, h, top, tok = pa.token_logprobs(z, t, 4)
+    assert torch.isnan(lp[2]) and torch.isnan(h[2]) and torch.isnan(top[2]).all()
+    t[0] = V
+    lp = pa.token_logprobs(x, t)[0]
+    assert torch.isnan(lp[0]) and torch.isfinite(lp[1:]).all()
+    assert pa.get_device_error() == 5

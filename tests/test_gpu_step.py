@@ -235,3 +235,18 @@ def test_new_lengths_past_32_bits():
     assert pa.get_device_error() == 5
     assert starts.tolist() == [0] * 5 and slots.tolist() == [-1] * 16 and pos.tolist() == [-1] * 16
     assert not copies.any() and not lens.any() and not refs.any()
+
+
+def test_last_block_without_an_owner():
+    """It counts as free and would be handed out to two sequences."""
+    b = Batch(8, 4)
+    b.add(20)
+    b.add(5)
+    st = b.upload()
+    st[2][st[0][0, 1].long()] = 0
+    before = [x.clone() for x in st]
+    got = pa.extend_sequences(*st, dev([1, 20]), 21)
+    assert pa.get_device_error() == 5 and int(got[1].max()) == -1
+    assert all(torch.equal(x, y) for x, y in zip(before, st))
+    with pytest.raises(pa.PagedAttnError):
+        pa.extend_sequences(*st, st[1], 25)
