@@ -107,7 +107,8 @@ struct PromptGeo {
 // does not either), which an f16 holds; a reference is one of rounded products up to 2^26.
 constexpr float kPromptLimit = 32768.f, kPromptExact = 67108864.f;
 
-constexpr int kPromptTries = 1 << 23;
+// A wait's limit: a try gives up after 4 us, so two seconds.
+constexpr int kPromptTries = 1 << 19;
 
 // One unit of work.
 struct PromptUnit {

@@ -405,3 +405,30 @@ def test_units_taken_as_ctas_come_free(fp8):
     for x, w, (_, o) in zip((c, d), want, graphs):
         assert torch.equal(o[:sum(x.new)], w)
     assert pa.get_device_error() == 0
+
+
+def test_rows_past_32_bits():
+    """2^31 elements of q and out, and pages past 4 GB, at their ends."""
+    B, Hq, Hkv, D = 66000, 128, 8, 128
+    g = torch.Generator(device="cuda").manual_seed(52)
+    NB = 140000                                           # 4.6 GB each for K and V
+    k = torch.zeros((NB, Hkv, 16, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    for x in (k, v):
+        x[:4] = torch.randn((4, Hkv, 16, D), generator=g, device="cuda").bfloat16()
+        x[-4:] = torch.randn((4, Hkv, 16, D), generator=g, device="cuda").bfloat16()
+    q = torch.empty((2 * B, Hq, D), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    assert q.numel() > 2 ** 31
+    tables = torch.arange(B, device="cuda").int()[:, None] % 4
+    tables[1::2] += NB - 4
+    lens = torch.full((B,), 5, dtype=torch.int32, device="cuda")
+    starts = torch.arange(B + 1, device="cuda").int() * 2
+    out = pa.prompt_attention(q, k, v, tables, lens, starts, 16)
+    assert pa.get_device_error() == 0
+    for b in (0, 1, 65535, 65998, 65999):
+        kk, vv = (x[tables[b, 0], :, :5].double().repeat_interleave(Hq // Hkv, 0) for x in (k, v))
+        s = torch.einsum("nhd,hld->hnl", q[2 * b:2 * b + 2].double(), kk) * D ** -0.5
+        s[:, 0, 4] = -float("inf")
+        w = s.softmax(-1)
+        check(out[2 * b:2 * b + 2], torch.einsum("hnl,hld->nhd", w, vv),
+              torch.einsum("hnl,hld->nhd", w, vv.abs()))

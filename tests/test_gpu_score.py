@@ -238,3 +238,12 @@ def test_rows_that_a_cluster_shares(dtype):
     lp = pa.token_logprobs(x, t)[0]
     assert torch.isnan(lp[0]) and torch.isfinite(lp[1:]).all()
     assert pa.get_device_error() == 5
+
+
+def test_rows_past_32_bits():
+    x = torch.empty((17000, 128256), dtype=torch.bfloat16, device="cuda").normal_()
+    assert x.numel() > 2 ** 31
+    t = torch.full((17000,), 128255, dtype=torch.int32, device="cuda")
+    got = pa.token_logprobs(x, t, 3)
+    for a, b in zip(got, run(x[-200:], t[-200:], 3)):
+        assert torch.equal(a[-200:], b)
