@@ -111,7 +111,7 @@ constexpr float kPromptLimit = 32768.f, kPromptExact = 67108864.f;
 constexpr int kPromptTries = 1 << 19;
 
 // One unit of work.
-struct PromptUnit {
+struct alignas(16) PromptUnit {
   int b;                 // sequence, -1 behind the last unit
   int head;              // kv head
   int row0, ntok;        // packed query tokens [row0, row0 + ntok)
@@ -533,6 +533,17 @@ __device__ __forceinline__ void store16(uint32_t at, uint4 w) {
                : "memory");
 }
 
+__device__ __forceinline__ PromptUnit load_unit(const PromptUnit& from) {
+  union {
+    uint4 w[3];
+    PromptUnit un;
+  } u;
+  static_assert(sizeof(PromptUnit) == sizeof(u.w), "three pieces");
+#pragma unroll
+  for (int i = 0; i < 3; ++i) u.w[i] = load16(smem_u32(&from) + 16 * i);
+  return u.un;
+}
+
 // The byte mask of the codes 0x7F and 0xFF (NaN) in a word.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x01010101u & 0x80808080u) >> 7) * 0xFFu;
@@ -825,7 +836,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       for (int ui = 0; wait.ok(); ++ui) {
         wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
         if (!wait.all_ok()) break;
-        PromptUnit un = ms.unit[ui & 1];
+        PromptUnit un = load_unit(ms.unit[ui & 1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
         un.b = __shfl_sync(0xffffffffu, un.b, 0);
@@ -906,7 +917,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       for (int ui = 0; wait.ok(); ++ui) {
         wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
         if (!wait.all_ok()) break;
-        const PromptUnit un = ms.unit[ui & 1];
+        const PromptUnit un = load_unit(ms.unit[ui & 1]);
         if (un.b < 0) break;
         const int last = un.pos0 + un.ntok - 1;
         bool found = false;
@@ -932,8 +943,14 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               const int st = tiles % (kv ? Gm::kVStages : Gm::kKStages);
               const uint32_t use = static_cast<uint32_t>(tiles / (kv ? Gm::kVStages
                                                                      : Gm::kKStages));
-              wait(&ms.raw_full[rs], static_cast<uint32_t>(item / Gm::kRawStages) & 1u);
-              wait(kv ? &ms.v_empty[st] : &ms.k_empty[st], (use & 1u) ^ 1u);
+              // (both asked for at once: each answer takes a while)
+              uint64_t* in = &ms.raw_full[rs];
+              uint64_t* to = kv ? &ms.v_empty[st] : &ms.k_empty[st];
+              const uint32_t in_phase = static_cast<uint32_t>(item / Gm::kRawStages) & 1u;
+              const uint32_t to_phase = (use & 1u) ^ 1u;
+              const bool here = tc::mbar_test(in, in_phase), free = tc::mbar_test(to, to_phase);
+              if (!here) wait(in, in_phase);
+              if (!free) wait(to, to_phase);
               __syncwarp();
               const uint32_t base = smem_u32(smem), raw = base + Gm::kRawOff + rs * Gm::kRawBytes;
               if (kv)
@@ -1072,7 +1089,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
     for (int ui = 0; wait.ok(); ++ui) {
       wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
       if (!wait.all_ok()) break;
-      const PromptUnit un = ms.unit[ui & 1];
+      const PromptUnit un = load_unit(ms.unit[ui & 1]);
       if (un.b < 0) break;
       const PromptSub sub = prompt_sub(p, un, s);
       const bool live = tok < sub.n;                    // rows past the tile's end repeat the last
