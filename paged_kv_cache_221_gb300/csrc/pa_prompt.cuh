@@ -47,15 +47,16 @@
 // and end are 10000 more: outputs written, 3500, and the first maximum, while no product runs.
 // 32 query heads over 8 of 128 dims: 16384 tokens 1385 to 1510 us by the clock that the power
 // limit leaves (1.59 to 1.46 PFLOP/s; a library matrix product in a loop 1.69), 24 prompts of
-// 128 to 2048 tokens 304 us (0.98), 12 of 512 to 4096 over FP8 pages 582 us (1.11), 33 tokens
+// 128 to 2048 tokens 301 us (0.99), 12 of 512 to 4096 over FP8 pages 572 us (1.13), 33 tokens
 // behind 65519 65 us (4.1 TB/s).
 //
 // Measured on the way, 16384 tokens or as said: V by TMA boxes like K, 2300 cycles of
 // the TMA unit for a K/V tile by themselves (a box of 16 keys is about 70 whatever its bytes); three K and two V stages 1460
 // against 1417 us; two threads per row (16 softmax warps) 1466; the rare code between that of most
 // tiles 1430 against 1397, since the roles share one instruction cache; generic instead of
-// shared-memory instructions in widening 653 against 590 (FP8); three lanes' pieces at a time
-// there 766, since registers spill.
+// shared-memory instructions in widening 653 against 590 (FP8); three pieces of a lane at a time
+// there 766, since registers spill; three warps for K and three for V instead of six for each in
+// turn 628 against 582.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -21,10 +21,10 @@
 // ones as are missing.
 //
 // The kernel is bound by reading the logits.  A cluster of CTAs shares a row when there are few
-// and long ones.  2048 rows of 128256 bf16 with 20 alternatives 108 us (4.9 TB/s; 97 without
-// alternatives); 64 of 128256 fp32 with 5 12.4 us, a launch and seven barriers on top of 5 us of
-// reading; 1000 of 32003 fp16 18.5 us.  CTAs of 512 threads 157 us for the first (with 256 others
-// stream while one joins its row), of 128 threads 161, five or six CTAs per SM as four.
+// and long ones.  2048 rows of 128256 bf16 with 20 alternatives 97 us (5.4 TB/s); 64 of 128256 fp32 with 5 12.4 us, a launch and seven barriers on top of 5 us of
+// reading; 1000 of 32003 fp16 18.5 us.  With CTAs of 512 threads the first took 157 us (with
+// 256 others stream while one joins its row), of 128 threads 161, then 108 with 256; five or six
+// CTAs per SM as four.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -168,8 +168,15 @@ __device__ __forceinline__ float add_elements(ScoreSums& s, const float (&x)[N])
   return m;
 }
 
+constexpr int kScoreStep = 2;               // vectors of a thread's step
+constexpr int kScoreRing = 4;               // steps on their way in a long row
+constexpr int kScoreLong = 24 * kScoreThreads;  // vectors of a long row (of a CTA's part of it)
+
 struct ScoreShared {
-  unsigned long long list[kScoreList];
+  union {
+    uint4 ring[kScoreRing][kScoreStep * kScoreThreads];  // of every thread, in the pass
+    unsigned long long list[kScoreList];                 // behind it
+  };
   unsigned long long best[kScoreSplit * kMaxScoreTop];   // of every CTA of the row, in CTA 0
   unsigned long long red[kScoreWarps];
   ScoreSums sums[kScoreWarps];
@@ -265,26 +272,58 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const ScorePara
   float most = -CUDART_INF_F, second = -CUDART_INF_F;   // maxima of the best and the other steps
   int best_at = v0;                                     // where the best step begins
   int v = v0 + tid;
-  constexpr int U = 4;                                  // vectors of a step
-  auto keep = [&](float m) {
-    second = fmaxf(second, fminf(m, most));
-    best_at = m > most ? v : best_at;
-    most = fmaxf(most, m);
-  };
-  for (; v + (U - 1) * kScoreThreads < v1; v += U * kScoreThreads) {
-    uint4 w[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) w[i] = __ldg(vec + v + i * kScoreThreads);
+  constexpr int U = kScoreStep;
+  auto step = [&](const uint4 (&w)[U], int at) {
     float f[U * N];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      Vec<T>::get(w[i], *reinterpret_cast<float(*)[N]>(f + i * N));
-    keep(add_elements(s, f));
+    for (int i = 0; i < U; ++i) Vec<T>::get(w[i], *reinterpret_cast<float(*)[N]>(f + i * N));
+    const float m = add_elements(s, f);
+    second = fmaxf(second, fminf(m, most));
+    best_at = m > most ? at : best_at;
+    most = fmaxf(most, m);
+  };
+  if (v1 - v0 >= kScoreLong) {
+    // Through shared memory, some steps ahead: the registers of four CTAs per SM hold too little
+    // for memory to go on while a step is added up.  Measured, ahead / not, 1000 rows: 128256
+    // bf16 49.4 / 53.5 us, 64000 29.5 / 31.0, 48000 22.7 / 22.3, 32003 18.5 / 17.0 (fp32 28.4 /
+    // 28.8); two steps of four vectors ahead 102 against 97 us for the 2048 rows above.
+    auto ask = [&](int stage, int from) {
+      if (from + (U - 1) * kScoreThreads < v1) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          cp_async_16(smem_u32(&sh.ring[stage][i * kScoreThreads + tid]),
+                      vec + from + i * kScoreThreads, 16u);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kScoreRing; ++i) ask(i, v + i * U * kScoreThreads);
+    for (int stage = 0; v + (U - 1) * kScoreThreads < v1; v += U * kScoreThreads) {
+      cp_async_wait<kScoreRing - 1>();
+      uint4 w[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) w[i] = sh.ring[stage][i * kScoreThreads + tid];
+      step(w, v);
+      ask(stage, v + kScoreRing * U * kScoreThreads);
+      stage = stage + 1 == kScoreRing ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+  } else {
+    for (; v + (2 * U - 1) * kScoreThreads < v1; v += 2 * U * kScoreThreads) {
+      uint4 w[2][U];
+#pragma unroll
+      for (int i = 0; i < 2 * U; ++i) w[i / U][i % U] = __ldg(vec + v + i * kScoreThreads);
+      step(w[0], v);
+      step(w[1], v + U * kScoreThreads);
+    }
   }
   for (; v < v1; v += kScoreThreads) {
     float f[N];
     Vec<T>::get(__ldg(vec + v), f);
-    keep(add_elements(s, f));
+    const float m = add_elements(s, f);
+    second = fmaxf(second, fminf(m, most));
+    best_at = m > most ? v : best_at;
+    most = fmaxf(most, m);
   }
   // one element in front of or behind the vectors
   int extra = -1;
