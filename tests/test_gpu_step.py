@@ -250,3 +250,14 @@ def test_last_block_without_an_owner():
     assert all(torch.equal(x, y) for x, y in zip(before, st))
     with pytest.raises(pa.PagedAttnError):
         pa.extend_sequences(*st, st[1], 25)
+
+
+def test_largest_batch():
+    b = Batch(20000, 3)
+    for i in range(12288):
+        b.add((0, 3, 16)[i % 3])
+    state = b.upload()
+    extend(b, state, [i % 2 for i in range(12288)])
+    with pytest.raises(pa.PagedAttnError):
+        pa.extend_sequences(torch.zeros((12289, 1), dtype=torch.int32, device="cuda"),
+                            dev([0] * 12289), state[2], dev([0] * 12289), 1)
