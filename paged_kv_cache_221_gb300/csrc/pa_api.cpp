@@ -199,13 +199,16 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
   if (partition_size > 0) {
     pl.split = std::min(tiles, partition_size / kPromptTile);
   } else if (scratch) {
-    // as many partitions, of four K/V tiles at least, as give every SM a unit with the fewest
-    // pairs of tiles that there can be (the device knows them alone).  Measured, 64 tokens behind
-    // 16384 each, 32 query heads over 8, whole / cut: one sequence 201 / 29 us, 4 203 / 80, 8
-    // 205 / 142; but 12 207 / 219, 16 215 / 272, 32 432 / 519
+    // with the fewest pairs of tiles that there can be (the device knows them alone), as many
+    // partitions, of four K/V tiles at least, as give every SM a unit, or 1.75 where there are
+    // several sequences, whose lengths mostly differ.  Measured, 64 tokens of 32 query heads over 8
+    // behind 4000 to 32000, one unit per SM / 1.75: 8 sequences 219 / 186 us, 4 119 / 84, 2 68 / 54
+    // (behind 16384 each: 8 142 / 149, 4 80 / 88); whole / cut: one 201 / 27, 4 203 / 88, 8 205 /
+    // 149, but 12 207 / 219, 16 215 / 272, 32 432 / 519
     const long long pairs = hkv * std::max(std::min<long long>(num_seqs, num_tokens),
                                            num_tokens / pair);
-    if (pairs < 152) pl.split = std::max(4, ceil_div(tiles, 152 / pairs));
+    if (pairs <= 76)
+      pl.split = std::max(4, ceil_div(tiles, (num_seqs > 1 ? 266 : 152) / pairs));
   }
   pl.split = std::min(pl.split, tiles);
   pl.max_parts = ceil_div(tiles, pl.split);
