@@ -1138,8 +1138,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 break;
               first = true;
             }
-            // by 8 at least, unless weights went past their limit; the first finite score always
-            const bool move = look && m > ref + (steady ? 0.f : 8.f);
+            // by 8 at least, unless weights went past their limit, or 2^(8 + kShift) would be
+            // rounded past it; the first finite score always
+            const bool exact = fabsf(ref) <= kPromptExact;
+            const bool move = look && m > ref + (steady || !exact ? 0.f : 8.f);
             if (__any_sync(0xffffffffu, move)) {
               const float f = move ? hw_exp2(ref - m) : 1.f;
               ref = move ? m : ref;

@@ -1,0 +1,53 @@
+"""Prompt attention where its arithmetic has its borders, against values worked out by hand."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_221_gb300 as pa
+from prompt_cases import Prompts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("step", [8, 16, 64])
+@pytest.mark.parametrize("start", [2 ** 26 - 64, 2 ** 26, 2 ** 26 + 64])
+def test_scores_that_a_few_bits_tell_apart(start, step, fp8):
+    """Scores past 2^26 are multiples of 8 in fp32: each tile's best one is `step` above the last
+    tile's, in powers of two, and the weights 2^0, 2^step, .. 2^(3 step) hold to the end."""
+    c = Prompts(1, [600], [0], 2, 2, 128, fp8=fp8)
+    kind = torch.uint8 if fp8 else torch.bfloat16
+    # k = (2^13, n, 0 ..) and q = (2^13, 8, 0 ..): 2^26 + 8 n; FP8 codes of 2^8 and n / 32 with
+    # scales of 2^5, where n / 32 is an E4M3 value for the n below
+    first, top, scale = (2.0 ** 8, 2.0 ** 5, 2.0 ** 5) if fp8 else (2.0 ** 13, 1.0, 1.0)
+    k = torch.zeros((c.NB, 2, 16, 128), device="cuda")
+    want_n = {0: (start - 2 ** 26) // 8}
+    for t in range(1, 4):
+        want_n[128 * t + 5] = want_n[0] + t * step // 8
+    for j, n in want_n.items():
+        blk, at = int(c.tables[0, j // 16]), j % 16
+        k[blk, :, at, 0] = first
+        k[blk, :, at, 1] = n / top
+    if fp8:
+        code = k.to(torch.float8_e4m3fn)
+        assert torch.equal(code.float(), k)
+        c.k, c.k_scale = code.view(torch.uint8), torch.full_like(c.k_scale, scale)
+        assert c.k.dtype == kind
+    else:
+        c.k = k.to(kind)
+        assert torch.equal(c.k.float(), k)
+    c.q = torch.zeros_like(c.q)
+    c.q[:, :, 0], c.q[:, :, 1] = 2.0 ** 13, 8.0
+    got = pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, c.starts, c.most,
+                              scale=math.log(2.0), k_scale=c.k_scale, v_scale=c.v_scale)
+    assert pa.get_device_error() == 0
+    _, v = c.kv(0)
+    s = torch.full((600, 600), -math.inf, dtype=torch.float64, device="cuda")
+    for j, n in want_n.items():
+        s[j:, j] = 8.0 * (n - want_n[0])
+    w = torch.softmax(s * math.log(2.0), -1)
+    want = torch.einsum("nj,hjd->nhd", w, v)
+    size = torch.einsum("nj,hjd->nhd", w, v.abs())
+    assert torch.isfinite(got).all()
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * (want.abs() + size) * (1 + 2.0 ** -4)).all()
