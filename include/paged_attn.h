@@ -632,9 +632,11 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
  * partition_size 0 nothing is cut).  The workspace also holds the counter by
  * which the kernel shares many query tiles out, so calls that may overlap on
  * the GPU need workspaces of their own.  Softmax statistics and accumulation are
- * fp32; the weights are rounded to bf16 where they meet the values.  A slot
- * that a query token must not see does not reach it, whatever it holds; a NaN
- * or infinity that it sees does.
+ * fp32; where they meet the values the weights have 11 bits (2^-11 of each at
+ * most, and 2^-32 of the row's largest), so that outputs keep the relative L2
+ * error of pa_attention, 2e-3 with normal inputs.  Sums of weight times value
+ * past 2^112 overflow.  A slot that a query token must not see does not reach
+ * it, whatever it holds; a NaN or infinity that it sees does.
  * Requirements: pointers 16-byte aligned, head_dim 64 or 128, block_size 16,
  * num_q_heads / num_kv_heads at most 128, num_blocks * num_kv_heads * 16 below
  * 2^31.  A sequence with context_lens[b] < T_b or > max_context_len, or with

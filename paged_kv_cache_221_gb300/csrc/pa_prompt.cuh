@@ -26,37 +26,52 @@
 //   warp 9          issues the MMAs: per K/V tile P.V (in two halves, the first while the last
 //                   quarter of the weights is computed) then the next S of the first tile, the
 //                   same of the second.
-//   warps 10, 11    copy the V tiles, rows that no query row sees as zeros.  Of those that some
-//                   see and some must not, infinities and NaN are taken out (0 * inf would reach
-//                   the others); the rows that see them get them added at the end.
+//   warps 10 to 15  bring the V tiles, a 16-key page at a time, as f16.
 //
-// FP8 pages.  The products take f16, of which every E4M3 value is one: warps 10 to 15 widen
+// Rounding.  The weights meet V as f16, times 2^7: 2^-11 of each at most, and 2^-32 of the row's
+// largest (which is what f16 cannot hold then); statistics and accumulators are fp32.  As one bf16
+// each they would add 1.1e-3 to 1.7e-3 of relative error to the outputs' own rounding, and both
+// together pass the 2e-3 that the other attention kernels keep.
+//
+// V of bf16 pages.  The product takes two operands of one type, so the pages come through
+// registers and become f16 there, times 2^9.  That is exact or not done: a page with an element
+// that f16 does not have (2^7 and more, below 2^-26) stays bf16, and so do its weights, each in
+// two parts that hold the f16, with a product for both; 16 keys are one step of the product, so
+// that pages of both kinds stand in one tile.  The byte v_split tells the others which.  O carries
+// 2^16 in all, so that sums of weight times value past 2^112 are infinite.  Infinities and NaN are
+// taken out of such a page, since 0 * inf would reach rows that must not see them, and added at the
+// end to the rows that do.
+//
+// FP8 pages.  Every E4M3 value is an f16: warps 10 to 15 widen
 // each tile from where TMA left it into the ring that the MMAs read (K rows as they are; V
 // pages are stored by head dim, so that tile becomes a K-major operand), and the query rows in
 // place, each times a power of two that puts its largest element at 2^7 .. 2^8 (a bf16 value
-// may lie outside f16's range) and that the row's scores take back.  Weights become f16, times
-// 2^7, which moves what f16 cannot hold from 2^-25 to 2^-32 of the row's largest weight.
-//
-// Weights are rounded to bf16 (2^-8 of each at most) for the second product, as are the
-// values they meet (f16 for FP8 pages: 2^-11); statistics and accumulators are fp32.
+// may lie outside f16's range) and that the row's scores take back.  NaN are taken out of V at the
+// mask's border.
 //
 // What bounds it.  A K/V tile of a pair is 2048 cycles of products.  A tile's weights take 1350
-// (an exponential is 4 cycles per warp instruction and scheduler; the rest beside it), its P . V
-// and next S with their hand-overs as much again, and the two tiles of a pair alternate: about
-// 2700 in all (3500 for FP8 pages, whose tiles take two thirds of that to widen).  A unit's start
-// and end are 10000 more: outputs written, 3500, and the first maximum, while no product runs.
-// 32 query heads over 8 of 128 dims: 16384 tokens 1385 to 1510 us by the clock that the power
-// limit leaves (1.59 to 1.46 PFLOP/s; a library matrix product in a loop 1.69), 24 prompts of
-// 128 to 2048 tokens 301 us (0.99), 12 of 512 to 4096 over FP8 pages 572 us (1.13), 33 tokens
-// behind 65519 65 us (4.1 TB/s).
+// alone (an exponential is 4 cycles per warp instruction and scheduler; the rest beside it), its
+// P . V and next S with their hand-overs as much again, and the two tiles of a pair alternate: 2700
+// at least.  The warps that bring V issue 40 instructions for 512 bytes of it from the same four
+// schedulers: about 3100 in all (3500 for FP8 pages, whose K and V take two thirds of that to
+// widen).  A unit's start and end are 10000 more: outputs written, 3500, and the first maximum,
+// while no product runs.  32 query heads over 8 of 128 dims: 16384 tokens 1700 us (1.29 PFLOP/s; a
+// library matrix product in a loop 1.69), 24 prompts of 128 to 2048 tokens 363 us (0.82), 12 of 512
+// to 4096 over FP8 pages 572 us (1.13), 33 tokens behind 65519 71 us (3.8 TB/s).
 //
-// Measured on the way, 16384 tokens or as said: V by TMA boxes like K, 2300 cycles of
-// the TMA unit for a K/V tile by themselves (a box of 16 keys is about 70 whatever its bytes); three K and two V stages 1460
-// against 1417 us; two threads per row (16 softmax warps) 1466; the rare code between that of most
-// tiles 1430 against 1397, since the roles share one instruction cache; generic instead of
-// shared-memory instructions in widening 653 against 590 (FP8); three pieces of a lane at a time
-// there 766, since registers spill; three warps for K and three for V instead of six for each in
-// turn 628 against 582.
+// Measured on the way, 16384 tokens or as said.  The weights of bf16 pages in 8 bits, V as it is:
+// 1470 us (24 prompts 305), the precision above.  In two bf16 parts for all pages: 2118 (448).  V
+// made f16 where asynchronous copies left it: 1820 to 2010 (354 to 420), since shared memory is
+// read and written once more.  Through registers that spill: 2180 (515).  Without the prefetch to
+// L2 33 tokens behind 65519 76 us.  A sum of 64 weights as their limit, where sums of eight are now:
+// four windows of 1000 446 us against 419.
+// V by TMA boxes like K, 2300 cycles of the TMA unit for a K/V tile by themselves (a box of 16 keys
+// is about 70 whatever its bytes); three K and two V stages 1460 against 1417 us; two threads per
+// row (16 softmax warps) 1466; the rare code between that of most tiles 1430 against 1397, since
+// the roles share one instruction cache (these with V as it is); generic instead of shared-memory
+// instructions in widening 653 against 590 (FP8); three pieces of a lane at a time there 766, since
+// registers spill; three warps for K and three for V instead of six for each in turn 628 against
+// 582.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -72,10 +87,12 @@
 
 namespace pa {
 
+constexpr int kPromptVShift = 9;
+
 template <int D, bool KV8>
 struct PromptGeo {
   static constexpr int kSoftmaxWarps = 8;
-  static constexpr int kAux = KV8 ? 6 : 2;               // warps that bring V, or widen K and V
+  static constexpr int kAux = 6;                         // warps that bring V, or widen K and V
   static constexpr int kThreads = (kSoftmaxWarps + 2 + kAux) * 32;
   static constexpr int kHalves = D / 64;                 // 64-dim halves of a row (128 bytes)
   static constexpr int kHalfBytes = kPromptTile * 128;
@@ -84,7 +101,8 @@ struct PromptGeo {
   static constexpr int kVStages = KV8 ? 2 : 3;
   static constexpr int kRawStages = KV8 ? 2 : 0;         // FP8 tiles in flight
   static constexpr int kRawBytes = kPromptTile * D;
-  static constexpr int kShift = KV8 ? 7 : 0;             // weights carry 2^kShift
+  static constexpr int kShift = 7;                       // weights carry 2^kShift
+  static constexpr int kVShift = KV8 ? 0 : kPromptVShift;  // and V, as f16, 2^kVShift
   static constexpr int kPages = kPromptTile / kBlockSize;
   // shared memory, from a 1024-byte aligned base
   static constexpr int kKOff = 2 * kTileBytes;           // behind the two Q tiles
@@ -97,16 +115,15 @@ struct PromptGeo {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 2 * kPromptTile;        // S tiles at 0 and 128, then O
   // registers per thread: launch, softmax warps, others
-  static constexpr int kRegs = KV8 ? 128 : 168, kSoftmaxRegs = KV8 ? 184 : 208;
-  static constexpr int kOtherRegs = KV8 ? 72 : 88;
+  static constexpr int kRegs = 128, kSoftmaxRegs = 184, kOtherRegs = 72;
   static_assert(kAlloc <= 232448, "shared memory per block");
   static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs <=
                     kThreads * kRegs, "the split takes no more than the launch has");
 };
 
-// Weights are taken with the present reference while none of them passes 2^15 (and their sum
-// does not either), which an f16 holds; a reference is one of rounded products up to 2^26.
-constexpr float kPromptLimit = 32768.f, kPromptExact = 67108864.f;
+// Weights are taken with the present reference while none of them passes what f16 holds (for half
+// of them by sums of eight); a reference is one of rounded products up to 2^26.
+constexpr float kPromptLimit = 65504.f, kPromptExact = 67108864.f;
 
 // A wait's limit: a try gives up after 4 us, so two seconds.
 constexpr int kPromptTries = 1 << 19;
@@ -120,7 +137,7 @@ struct alignas(16) PromptUnit {
   int L;                 // context length
   int t0, t1;            // K/V tiles [t0, t1)
   int part, parts;
-  int nonfinite;         // infinities or NaN were taken out of V tiles at the mask's border
+  int odd0, odd1;        // infinities or NaN were taken out of V tiles in [odd0, odd1)
 };
 
 template <int D, bool KV8>
@@ -137,6 +154,7 @@ struct PromptMisc {
   uint64_t fin;
   PromptUnit unit[2];
   uint32_t tmem_base;
+  alignas(8) uint8_t v_split[Gm::kVStages][Gm::kPages];  // 1: the page of V stays bf16
   int8_t q_exp[KV8 ? 2 : 1][2][KV8 ? kPromptTile : 1];   // by record, tile, row: of the factor
 };
 
@@ -188,7 +206,8 @@ __device__ __forceinline__ bool prompt_unit(const PromptParams& p, int u, Prompt
   if (un.part >= un.parts) return false;
   un.t0 = a + un.part * p.split;
   un.t1 = min(e, un.t0 + p.split);
-  un.nonfinite = 0;
+  un.odd0 = un.t1;
+  un.odd1 = un.t0;
   return true;
 }
 
@@ -213,27 +232,23 @@ __device__ __forceinline__ PromptSub prompt_sub(const PromptParams& p, const Pro
 struct PromptPages {
   int ids, next;
 
-  // The lane that holds the first page of tile t; tiles come in order.
-  __device__ __forceinline__ int lane_of(const PromptParams& p, const PromptUnit& un, int t,
-                                         int lane) {
+  // Those from the i-th of the unit on, a multiple of 32; called for each such i in turn.
+  __device__ __forceinline__ void take(const PromptParams& p, const PromptUnit& un, int i,
+                                       int lane) {
     constexpr int kPages = kPromptTile / kBlockSize;
-    const int at = (t - un.t0) * kPages & 31;
-    if (at == 0) {
 #pragma unroll 1
-      for (int read = t == un.t0 ? 0 : 32; read <= 32; read += 32) {
-        const int i = t * kPages + read + lane;
-        ids = next;
-        next = p.num_blocks;
-        if (i * kBlockSize < un.L && i < un.t1 * kPages) {
-          const int id = __ldg(p.block_tables + static_cast<size_t>(un.b) * p.mbs + i);
-          if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks))
-            next = id;
-          else
-            atomicOr(&g_pa_err, kErrBounds);
-        }
+    for (int read = i == 0 ? 0 : 32; read <= 32; read += 32) {
+      const int pg = un.t0 * kPages + i + read + lane;
+      ids = next;
+      next = p.num_blocks;
+      if (pg * kBlockSize < un.L && pg < un.t1 * kPages) {
+        const int id = __ldg(p.block_tables + static_cast<size_t>(un.b) * p.mbs + pg);
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks))
+          next = id;
+        else
+          atomicOr(&g_pa_err, kErrBounds);
       }
     }
-    return at;
   }
 };
 
@@ -337,6 +352,30 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
   return d;
 }
 
+__device__ __forceinline__ void prefetch_l2(const uint8_t* at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t add_u16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("add.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
+// 16 bytes of a page, which nothing else on this SM reads.
+__device__ __forceinline__ uint4 load_once(const uint8_t* from) {
+  uint4 w;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(from));
+  return w;
+}
+
 // Bits 15 and 31: the low, the high bf16 of the word is infinite or NaN.
 __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
@@ -392,8 +431,16 @@ __device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int lane) {
     b = x;
 }
 
+// A tile's pages of V that stay bf16, as bits; kSplitUnknown: not looked up.
+constexpr uint32_t kSplitUnknown = 1u << 31;
+__host__ __device__ constexpr uint32_t page_bit(int pg) { return 1u << (pg % 4 * 8 + pg / 4 * 4); }
+__device__ __forceinline__ uint32_t split_pages(uint32_t bytes) {
+  uint2 w;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(bytes) : "memory");
+  return w.x | w.y << 4;
+}
+
 // A row's 128 scores of a K/V tile in one thread, and the weights that take their place.
-template <bool KV8>
 struct PromptScores {
   uint32_t x[4][32];
   uint32_t w[4][16];
@@ -466,20 +513,51 @@ struct PromptScores {
         const int j = k - kPack;
         const float e0 = score(2 * j), e1 = score(2 * j + 1);
         part[j & 3] = add_f32x2(part[j & 3], pack_f32x2(e0, e1));
-        if constexpr (KV8)
-          w[j / 16][j % 16] = half2_bits(__floats2half2_rn(e0, e1));
-        else
-          w[j / 16][j % 16] = pack_bf16x2_rn(e0, e1);
+        w[j / 16][j % 16] = half2_bits(__floats2half2_rn(e0, e1));
       }
+    }
+  }
+  // A quarter's weights for the V pages of `split` that stay bf16: times 2^kPromptVShift and in two
+  // bf16 parts, which hold the f16 exactly; the second lies 64 columns behind the first.
+  __device__ __forceinline__ void split_quarter(int q, uint32_t taddr, uint32_t split) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!(split & page_bit(2 * q + h))) continue;
+      uint32_t rest[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t& x = w[q][8 * h + k];
+        float2 e = __half22float2(*reinterpret_cast<const __half2*>(&x));
+        e.x *= static_cast<float>(1 << kPromptVShift);
+        e.y *= static_cast<float>(1 << kPromptVShift);
+        x = pack_bf16x2_rn(e.x, e.y);
+        rest[k] = pack_bf16x2_rn(e.x - bf16_lo(x), e.y - bf16_hi(x));
+      }
+      tc::tmem_st8(taddr + kPromptTile / 2 + q * 16 + h * 8, rest);
     }
   }
   __device__ __forceinline__ float total() const {
     const uint64_t y = add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3]));
     return __uint_as_float(static_cast<uint32_t>(y)) + __uint_as_float(static_cast<uint32_t>(y >> 32));
   }
+  // The largest sum of eight weights of the first half: no less than any of them.
+  __device__ __forceinline__ float most_of_eight() const {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = __uint_as_float(static_cast<uint32_t>(part[i]));
+      y[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(part[i] >> 32));
+    }
+    return fmaxf(max3(max3(y[0], y[1], y[2]), y[3], y[4]), max3(y[5], y[6], y[7]));
+  }
   // The weights over the scores, the first half of the keys announced once the third quarter is
   // computed; the second half is stored, not yet complete.
-  __device__ __forceinline__ void finish(uint32_t taddr, uint64_t* half, int lane) {
+  __device__ __forceinline__ void finish(uint32_t taddr, uint64_t* half, int lane,
+                                         uint32_t split) {
+    if (__builtin_expect(split != 0u, 0)) {
+      split_quarter(0, taddr, split);
+      split_quarter(1, taddr, split);
+    }
     tc::tmem_st16(taddr, w[0]);
     tc::tmem_st16(taddr + 16, w[1]);
     weights<32, 48>([](int) {});
@@ -487,8 +565,10 @@ struct PromptScores {
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(half);
+    if (__builtin_expect(split != 0u, 0)) split_quarter(2, taddr, split);
     tc::tmem_st16(taddr + 32, w[2]);
     weights<48, 64>([](int) {});
+    if (__builtin_expect(split != 0u, 0)) split_quarter(3, taddr, split);
     tc::tmem_st16(taddr + 48, w[3]);
   }
 };
@@ -516,6 +596,41 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
                   e4m3x2_to_f16x2(w.y >> 16));
   hi = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w),
                   e4m3x2_to_f16x2(w.w >> 16));
+}
+
+// bf16 values as f16 times 2^kPromptVShift.  Magnitudes from 2^-23 to below 2^7 become normal
+// numbers: their bits move by three and their exponents by a constant.
+constexpr uint32_t kPromptBias = (127 - kPromptVShift - 15) << 7;
+// Whether all of the warp's words w hold such: how far their magnitudes lie above the least (those
+// below it wrap round).
+template <int N>
+__device__ __forceinline__ bool plain_in_f16(const uint4 (&w)[N]) {
+  constexpr uint32_t kBelow = 0x10000u - kPromptBias - (1 << 7), kSpan = 30 << 7;
+  uint32_t most[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      most[k & 1] = max_u16x2(most[k & 1], add_u16x2(x[k] & 0x7FFF7FFFu, kBelow << 16 | kBelow));
+  }
+  most[0] = max_u16x2(most[0], most[1]);
+  return __all_sync(0xffffffffu, max(most[0] & 0xFFFFu, most[0] >> 16) < kSpan);
+}
+__device__ __forceinline__ uint32_t plain_f16x2(uint32_t w) {
+  return ((w & 0x7FFF7FFFu) * 8u - (kPromptBias << 16 | kPromptBias) * 8u) | (w & 0x80008000u);
+}
+// Whether f16 has the word's two values at all: as that, or 0, or down to 2^-26, whose last bit is
+// f16's smallest number then.
+__device__ __forceinline__ bool exact_in_f16(uint32_t w) {
+  constexpr uint32_t kMost = (127 - kPromptVShift + 16) << 7;
+  constexpr uint32_t kLeast = (127 - kPromptVShift - 17) << 7;
+  const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
+  return max(lo, hi) < kMost && (lo == 0u || lo >= kLeast) && (hi == 0u || hi >= kLeast);
+}
+__device__ __forceinline__ uint32_t exact_f16x2(uint32_t w) {      // a 0 becomes one by rounding
+  w += (kPromptVShift << 7) * 0x00010001u;
+  return half2_bits(__floats2half2_rn(bf16_lo(w), bf16_hi(w)));
 }
 
 // 16 bytes of shared memory (the tiles' addresses are computed, and as generic ones a tile took
@@ -658,7 +773,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       mbar_init(&ms.k_empty[i], 1);
     }
     for (int i = 0; i < Gm::kVStages; ++i) {
-      mbar_init(&ms.v_full[i], Gm::kAux);
+      mbar_init(&ms.v_full[i], KV8 ? Gm::kAux : Gm::kPages);
       mbar_init(&ms.v_empty[i], 1);
     }
     for (int i = 0; i < Gm::kRawStages; ++i) {
@@ -764,8 +879,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           constexpr int kBoxes = KV8 ? 1 : Gm::kHalves;
           const int box = lane & (Gm::kPages * kBoxes - 1);
           const int pg = box / kBoxes, h = box % kBoxes;
-          const int at = pages.lane_of(p, un, t, lane);
-          const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
+          const int first = (t - un.t0) * Gm::kPages;
+          if (first % 32 == 0) pages.take(p, un, first, lane);
+          const int id = __shfl_sync(0xffffffffu, pages.ids, (first & 31) + pg);
           const int page = id * p.Hkv + (id == p.num_blocks ? 0 : un.head);
           for (int kv = 0; kv < (KV8 ? 2 : 1); ++kv, ++item) {
             const int st = item % kRing;
@@ -805,7 +921,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       // The whole warp goes through the steps, so that stages and descriptors are uniform
       // values, and one elected lane issues.
       constexpr uint32_t kIdS = tc::idesc_f16<128, kPromptTile, false, false, !KV8>();
-      constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, !KV8>();
+      constexpr uint32_t kIdO = tc::idesc_f16<128, D, false, !KV8, false>();
+      constexpr uint32_t kIdSplit = tc::idesc_f16<128, D, false, true, true>();
       const uint32_t kring = smem_u32(smem + Gm::kKOff), vring = smem_u32(smem + Gm::kVOff);
       const uint32_t qsm = smem_u32(smem);
       const uint32_t tm = uniform(tmem);
@@ -853,7 +970,11 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           const uint32_t vlo =
               uniform(desc_lo(vring + vst * Gm::kTileBytes, KV8 ? 16 : Gm::kHalfBytes));
           const uint32_t klo = uniform(desc_lo(kring + kst * Gm::kTileBytes, 16));
-          if (t >= un.t0) wait(&ms.v_full[vst], vph);
+          uint32_t split = 0u;
+          if (t >= un.t0) {
+            wait(&ms.v_full[vst], vph);
+            if constexpr (!KV8) split = split_pages(smem_u32(ms.v_split[vst]));
+          }
           bool k_here = false;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
@@ -864,13 +985,27 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 wait(half ? &ms.p_full[s] : &ms.p_half[s], n_p[s] & 1u);
                 __syncwarp();
                 tc::fence_after_sync();
+                const uint32_t o = tm + Gm::kO + s * D, w = tm + s * kPromptTile;
+                if (KV8 || __all_sync(0xffffffffu, split == 0u)) {
 #pragma unroll
-                for (int i = 0; i < kPromptTile / 32; ++i) {
-                  const int k = half * (kPromptTile / 32) + i;
-                  const uint32_t off =
-                      (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
-                  lead_mma_ts(leader, tm + Gm::kO + s * D, tm + s * kPromptTile + k * 8,
-                              desc_of(vlo + off), kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
+                  for (int i = 0; i < kPromptTile / 32; ++i) {
+                    const int k = half * (kPromptTile / 32) + i;
+                    const uint32_t off =
+                        (KV8 ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048) >> 4;
+                    lead_mma_ts(leader, o, w + k * 8, desc_of(vlo + off), kIdO,
+                                k > 0 || t > sub[s].a ? 1u : 0u);
+                  }
+                } else {
+#pragma unroll 1
+                  for (int i = 0; i < kPromptTile / 32; ++i) {
+                    const int k = half * (kPromptTile / 32) + i;
+                    const bool two = (split & page_bit(k)) != 0u;
+                    lead_mma_ts(leader, o, w + k * 8, desc_of(vlo + (k * 2048 >> 4)),
+                                two ? kIdSplit : kIdO, k > 0 || t > sub[s].a ? 1u : 0u);
+                    if (two)
+                      lead_mma_ts(leader, o, w + kPromptTile / 2 + k * 8,
+                                  desc_of(vlo + (k * 2048 >> 4)), kIdSplit, 1u);
+                  }
                 }
               }
               if (t + 1 == sub[s].e) lead_commit(leader, &ms.o_full[s]);
@@ -913,7 +1048,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       // -------------------------------------------------------------- V, or FP8 tiles widened
       const int aux = warp - Gm::kSoftmaxWarps - 2;
       PromptWaits wait;
-      int item = 0, tiles = 0;                         // FP8 tiles, V tiles so far
+      int item = 0, tiles = 0, turn = 0;               // FP8 tiles, V tiles so far; whose the next
+                                                       //   page is
       uint32_t n_q[2] = {0, 0};
       for (int ui = 0; wait.ok(); ++ui) {
         wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
@@ -921,7 +1057,12 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         const PromptUnit un = load_unit(ms.unit[ui & 1]);
         if (un.b < 0) break;
         const int last = un.pos0 + un.ntok - 1;
-        bool found = false;
+        auto odd = [&](int t) {
+          if (lane == 0) {
+            atomicMin(&ms.unit[ui & 1].odd0, t);
+            atomicMax(&ms.unit[ui & 1].odd1, t + 1);
+          }
+        };
         if constexpr (KV8) {
 #pragma unroll 1
           for (int s = 0; s < 2; ++s) {
@@ -954,12 +1095,14 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               if (!free) wait(to, to_phase);
               __syncwarp();
               const uint32_t base = smem_u32(smem), raw = base + Gm::kRawOff + rs * Gm::kRawBytes;
-              if (kv)
-                found |= widen_values<D>(base + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux,
-                                         Gm::kAux, prompt_masked(p, t, un.pos0, last),
-                                         un.L - t * kPromptTile);
-              else
+              if (kv) {
+                const bool found = widen_values<D>(
+                    base + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux,
+                    prompt_masked(p, t, un.pos0, last), un.L - t * kPromptTile);
+                if (__any_sync(0xffffffffu, found)) odd(t);
+              } else {
                 widen_keys<D>(base + Gm::kKOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux);
+              }
               tc::fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -970,98 +1113,114 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           }
         } else {
           // A TMA box of 16 keys costs its unit about 70 cycles, whatever the bytes, and K's are
-          // as many as it can take; V comes by 16-byte copies, rows behind the context as zeros.
+          // as many as it can take; and shared memory has no time to be read and written once more
+          // beside the products.  So V comes through registers and becomes f16 there, page by page
+          // round the warps; a piece of a warp's next page is asked for as soon as one of the
+          // present page is stored.
           constexpr int kRowChunks = D / 8;            // 16-byte chunks of a row
           constexpr int kRows = 32 / kRowChunks;       // rows of one warp-wide copy
+          constexpr int kPieces = kBlockSize / kRows;
           const int c = lane % kRowChunks, r = lane / kRowChunks;
+          constexpr int kPageBytes = kBlockSize * D * 2;
+          constexpr uint32_t kOnes = 0x3F803F80u;
+          const int count = (un.t1 - un.t0) * Gm::kPages;
+          // keys of the unit that some query row sees; what nobody sees has weights of 0, so that
+          // any finite number does for it
+          const int begin = (p.window > 0 ? un.pos0 - p.window + 1 : 0) - un.t0 * kPromptTile;
+          const int end = last + 1 - un.t0 * kPromptTile;
+          auto sees = [&](int i, int id, int k) {
+            const int key = i * kBlockSize + k * kRows + r;
+            return id != p.num_blocks && key >= begin && key < end;
+          };
+          const uint8_t* const pool = static_cast<const uint8_t*>(p.v_pool) +
+                                      static_cast<size_t>(un.head) * kPageBytes + lane * 16;
+          auto page_at = [&](int id) {
+            return pool + static_cast<size_t>(id == p.num_blocks ? 0 : id) * p.Hkv * kPageBytes;
+          };
           PromptPages pages;
-          // a tile's copies have landed: keys that some query rows see and some must not, the
-          // last rows' newest and the first rows' oldest, are made finite
-          auto finish = [&](int t, int st) {
-            const uint32_t tile = smem_u32(smem) + Gm::kVOff + st * Gm::kTileBytes;
+          auto id_of = [&](int i) {
+            if (i < Gm::kAux || ((i ^ (i - Gm::kAux)) & 32) != 0)
+              pages.take(p, load_unit(ms.unit[ui & 1]), i & ~31, lane);
+            return __shfl_sync(0xffffffffu, pages.ids, i & 31);
+          };
+          const uint32_t mine = smem_u32(smem) + Gm::kVOff + (c >> 3) * Gm::kHalfBytes + r * 128 +
+                                (((c ^ r) & 7) << 4);
+          int i = (aux + Gm::kAux - turn) % Gm::kAux;  // this warp's first page
+          turn = (turn + count) % Gm::kAux;
+          int next = id_of(i);
+          uint4 w[kPieces];
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) w[k] = load_once(page_at(next) + k * 512);
 #pragma unroll 1
-            for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
-              const int at = t * kPromptTile + pg * kBlockSize;
-              const int old = p.window > 0 ? at + p.window : at;
-              if ((at + kBlockSize - 1 <= un.pos0 || at > last) &&
-                  (old + kBlockSize - 1 <= un.pos0 || old > last))
-                continue;
-              auto piece = [&](int i) {
-                const int key = pg * kBlockSize + i * kRows + r;
-                return tile + (c >> 3) * Gm::kHalfBytes + key * 128 + (((c & 7) ^ (key & 7)) << 4);
-              };
-              uint32_t bad = 0;
-#pragma unroll 4
-              for (int i = 0; i < kBlockSize / kRows; ++i) {
-                const uint4 w = load16(piece(i));
-                bad |= nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) |
-                       nonfinite_bf16x2(w.w);
-              }
-              if (__builtin_expect(bad == 0, 1)) continue;
-              found = true;
+          for (; i < count; i += Gm::kAux) {
+            const int nth = tiles + i / Gm::kPages, st = nth % Gm::kVStages;
+            const int id = next;
+            bool plain, exact = true;
 #pragma unroll 1
-              for (int i = 0; i < kBlockSize / kRows; ++i) {
-                const uint4 w = load16(piece(i));
-                store16(piece(i), make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y),
-                                             finite_bf16x2(w.z), finite_bf16x2(w.w)));
+            for (bool again = true; !(plain = plain_in_f16(w)) && again; again = false) {
+#pragma unroll
+              for (int k = 0; k < kPieces; ++k)
+                if (!sees(i, id, k)) w[k] = make_uint4(kOnes, kOnes, kOnes, kOnes);
+            }
+            if (__builtin_expect(plain, 1)) {
+#pragma unroll
+              for (int k = 0; k < kPieces; ++k)
+                w[k] = make_uint4(plain_f16x2(w[k].x), plain_f16x2(w[k].y), plain_f16x2(w[k].z),
+                                  plain_f16x2(w[k].w));
+            } else {
+#pragma unroll
+              for (int k = 0; k < kPieces; ++k)
+                exact = exact && exact_in_f16(w[k].x) && exact_in_f16(w[k].y) &&
+                        exact_in_f16(w[k].z) && exact_in_f16(w[k].w);
+              exact = __all_sync(0xffffffffu, exact);
+              if (exact) {
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k)
+                  w[k] = make_uint4(exact_f16x2(w[k].x), exact_f16x2(w[k].y), exact_f16x2(w[k].z),
+                                    exact_f16x2(w[k].w));
+              } else {
+                // the page stays bf16: infinities and NaN come out; the rows that see them get
+                // them at the end
+                uint32_t bad = 0u;
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                  bad |= nonfinite_bf16x2(w[k].x) | nonfinite_bf16x2(w[k].y) |
+                         nonfinite_bf16x2(w[k].z) | nonfinite_bf16x2(w[k].w);
+                  w[k] = make_uint4(finite_bf16x2(w[k].x), finite_bf16x2(w[k].y),
+                                    finite_bf16x2(w[k].z), finite_bf16x2(w[k].w));
+                }
+                if (__any_sync(0xffffffffu, bad != 0u))
+                  odd(load_unit(ms.unit[ui & 1]).t0 + i / Gm::kPages);
               }
             }
+            if (i + Gm::kAux < count) next = id_of(i + Gm::kAux);
+            // (and the page behind it to L2, for contexts that come out of memory)
+            const int ahead = i + 2 * Gm::kAux;
+            if (ahead < count) {
+              const bool later = ((ahead ^ (ahead - Gm::kAux)) & 32) != 0;
+              const int far = __shfl_sync(0xffffffffu, later ? pages.next : pages.ids, ahead & 31);
+              prefetch_l2(page_at(far) + lane * (kPageBytes / 32 - 16));
+            }
+            wait(&ms.v_empty[st], (static_cast<uint32_t>(nth / Gm::kVStages) & 1u) ^ 1u);
+            if (!wait.all_ok()) break;
+            const uint32_t to = mine + st * Gm::kTileBytes + i % Gm::kPages * (kBlockSize * 128);
+            auto place = [&](int k) {
+              return (to ^ ((k * kRows & 7) << 4)) + k * kRows * 128;
+            };
+            const uint8_t* const from = page_at(next);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              store16(place(k), w[k]);
+              w[k] = load_once(from + k * 512);
+            }
+            if (lane == 0) ms.v_split[st][i % Gm::kPages] = exact ? 0 : 1;
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.v_full[st]);
-          };
-          int issued = un.t0;
-          for (int done = un.t0; done < un.t1;) {
-            // a tile ahead of the one to finish where its stage is free, or there is none
-            if (issued < un.t1 && issued - done < Gm::kVStages) {
-              const int st = tiles % Gm::kVStages;
-              const uint32_t parity = (static_cast<uint32_t>(tiles / Gm::kVStages) & 1u) ^ 1u;
-              bool free = __all_sync(0xffffffffu, tc::mbar_test(&ms.v_empty[st], parity));
-              if (!free && issued == done) {
-                wait(&ms.v_empty[st], parity);
-                if (!wait.all_ok()) break;
-                free = true;
-              }
-              if (free) {
-                const int at = pages.lane_of(p, un, issued, lane);
-                const uint32_t tile = smem_u32(smem + Gm::kVOff + st * Gm::kTileBytes) +
-                                      (c >> 3) * Gm::kHalfBytes;
-#pragma unroll 1
-                for (int pg = aux; pg < Gm::kPages; pg += Gm::kAux) {
-                  const int id = __shfl_sync(0xffffffffu, pages.ids, at + pg);
-                  // what no query row of the unit sees comes as zeros
-                  const int end = id == p.num_blocks ? 0 : last + 1 - issued * kPromptTile;
-                  const int begin =
-                      p.window > 0 ? un.pos0 - p.window + 1 - issued * kPromptTile : 0;
-                  const uint8_t* src = static_cast<const uint8_t*>(p.v_pool) +
-                                       (static_cast<size_t>(id == p.num_blocks ? 0 : id) * p.Hkv +
-                                        un.head) * (kBlockSize * D * 2) + lane * 16;
-#pragma unroll
-                  for (int i = 0; i < kBlockSize / kRows; ++i) {
-                    const int key = pg * kBlockSize + i * kRows + r;
-                    cp_async_16(tile + key * 128 + (((c & 7) ^ (key & 7)) << 4), src + i * 512,
-                                key >= begin && key < end ? 16u : 0u);
-                  }
-                }
-                cp_async_commit();
-                ++issued;
-                ++tiles;
-                if (issued - done < Gm::kVStages && issued < un.t1) continue;
-              }
-            }
-            if (issued - done > 2)
-              cp_async_wait<2>();
-            else if (issued - done > 1)
-              cp_async_wait<1>();
-            else
-              cp_async_wait<0>();
-            finish(done, (tiles - (issued - done)) % Gm::kVStages);
-            ++done;
           }
-          cp_async_wait<0>();
+          tiles += count / Gm::kPages;
         }
         if (!wait.all_ok()) break;
-        if (found) *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) = 1;
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&ms.unit_checked[ui & 1]);
@@ -1087,6 +1246,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       __syncwarp();
     }
     uint32_t n_s = 0, n_o = 0;                          // S and O tiles taken
+    int v_first = 0;                                    // place of the unit's first V tile: stage,
+                                                        //   kVStages more in odd phases
     for (int ui = 0; wait.ok(); ++ui) {
       wait(&ms.unit_full[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
       if (!wait.all_ok()) break;
@@ -1102,6 +1263,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         c *= __ldg(p.k_scale + un.head) *
              __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       }
+      int v_at = (v_first + sub.a - un.t0) % (2 * Gm::kVStages);
+      v_first = (v_first + un.t1 - un.t0) % (2 * Gm::kVStages);
       float ref = -CUDART_INF_F;                        // reference, log2 units
       float sum = 0.f;
       bool steady = false;                              // a reference that may stay
@@ -1111,7 +1274,13 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         tc::fence_after_sync();
         const bool masked = prompt_masked(p, t, sub.first, sub.first + sub.n - 1);
         bool look = !steady;                            // for the maximum
-        PromptScores<KV8> sc;
+        PromptScores sc;
+        // whether V has pages that stay bf16, nearly always known by now
+        uint32_t split = 0u;
+        const int st = v_at < Gm::kVStages ? v_at : v_at - Gm::kVStages;
+        if constexpr (!KV8)
+          split = tc::mbar_test(&ms.v_full[st], v_at >= Gm::kVStages)
+                      ? split_pages(smem_u32(ms.v_split[st])) : kSplitUnknown;
         while (true) {
           sc.load(ts);
           // A score's factor is applied with the reference's subtraction, in one rounding; with
@@ -1171,11 +1340,19 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             most[k & 3] = max3(most[k & 3], sc.score(64 + 2 * k), sc.score(65 + 2 * k));
           });
           m = fmaxf(max3(most[0], most[1], most[2]), most[3]);
-          const bool fine = sc.total() <= kPromptLimit && fmaf(m, cc, off) <= 15.f;
+          const bool fine = sc.most_of_eight() <= kPromptLimit && fmaf(m, cc, off) <= 15.f;
           if (look || __all_sync(0xffffffffu, fine)) break;
           look = true;
         }
-        sc.finish(ts, &ms.p_half[s], lane);
+        if (!KV8 && __builtin_expect(__any_sync(0xffffffffu, split != 0u), 0)) {
+          if (split == kSplitUnknown) {
+            wait(&ms.v_full[st], v_at >= Gm::kVStages);
+            split = split_pages(smem_u32(ms.v_split[st]));
+          }
+          split = uniform(split);
+        }
+        v_at = v_at + 1 == 2 * Gm::kVStages ? 0 : v_at + 1;
+        sc.finish(ts, &ms.p_half[s], lane, split);
         sum += sc.total();
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -1187,7 +1364,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 
       // -------------------------------------------------------------- unit output
       wait(&ms.unit_checked[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-      const bool special = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) != 0;
+      const int odd0 = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].odd0);
+      const int odd1 = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].odd1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
       const bool any = sub.e > sub.a;
@@ -1197,7 +1375,8 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       float vs = 1.f;
       if constexpr (KV8) vs = __ldg(p.v_scale + un.head);
       // (a partition without a key of this row, or with scores of -inf alone, has no weights)
-      const float inv = sum == 0.f && un.parts > 1 ? 1.f : __frcp_rn(sum);
+      const float inv = (sum == 0.f && un.parts > 1 ? 1.f : __frcp_rn(sum)) *
+                        (1.f / (1 << Gm::kVShift));
       // Four lanes exchange 16-byte pieces of their rows, so that they write 64 bytes of one row
       // at a time: a store that touches 32 rows takes 32 cycles, and there is nothing beside it.
       const bool whole = un.parts == 1;
@@ -1271,7 +1450,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       }
       // the infinities and NaN that were taken out of V, for the rows that see them: a row at a
       // time, its dims over the lanes
-      if (__builtin_expect(special && any, 0)) {
+      if (__builtin_expect(odd0 < odd1 && any, 0)) {
         __syncwarp();
         float add[D / 32];
         int seen = -1;                                  // token that they are of
@@ -1283,16 +1462,13 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) add[k] = 0.f;
             const int at = sub.first + tk, begin = p.window > 0 ? at - p.window + 1 : 0;
-            for (int t = sub.a; t < sub.e; ++t) {
-              if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
-              const int last = min(at, t * kPromptTile + kPromptTile - 1);
+            const int stop = min(at + 1, min(sub.e, odd1) * kPromptTile);
 #pragma unroll 4
-              for (int j = max(t * kPromptTile, begin); j <= last; ++j) {
+            for (int j = max(max(sub.a, odd0) * kPromptTile, begin); j < stop; ++j) {
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                  const float v = prompt_value<D, KV8>(p, un, j, k * 32 + lane);
-                  add[k] += fabsf(v) < CUDART_INF_F ? 0.f : v;
-                }
+              for (int k = 0; k < D / 32; ++k) {
+                const float v = prompt_value<D, KV8>(p, un, j, k * 32 + lane);
+                add[k] += fabsf(v) < CUDART_INF_F ? 0.f : v;
               }
             }
           }
