@@ -615,7 +615,8 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
  * newest positions of its context (context_lens[b] counts them; their K/V have
  * been stored before, as have those of a cached prefix).  With T_b of them,
  * query token t sits at position i = context_lens[b] - T_b + t and sees the
- * positions j <= i, with window_size W > 0 only i - W < j <= i.
+ * positions j <= i, with window_size W > 0 only i - W < j <= i; blocks wholly
+ * before the first query token's window, and their table entries, are not read.
  *
  *   q, out        [num_tokens, num_q_heads, head_dim]   bf16
  *   query_starts  [num_seqs + 1]                         int32, ascending; T_b may

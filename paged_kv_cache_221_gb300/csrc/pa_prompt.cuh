@@ -228,7 +228,8 @@ __device__ __forceinline__ PromptSub prompt_sub(const PromptParams& p, const Pro
 }
 
 // Block ids of a unit's pages for one warp: 32 (four tiles) in lane order, and the 32 behind
-// them.  Pages behind the context's end and ids outside the pool (an error) become num_blocks.
+// them.  Pages behind the context's end, pages in front of every query token's window, whose table
+// entries are not read, and ids outside the pool (an error) become num_blocks.
 struct PromptPages {
   int ids, next;
 
@@ -236,12 +237,13 @@ struct PromptPages {
   __device__ __forceinline__ void take(const PromptParams& p, const PromptUnit& un, int i,
                                        int lane) {
     constexpr int kPages = kPromptTile / kBlockSize;
+    const int first = p.window > 0 ? max(0, un.pos0 - p.window + 1) / kBlockSize : 0;
 #pragma unroll 1
     for (int read = i == 0 ? 0 : 32; read <= 32; read += 32) {
       const int pg = un.t0 * kPages + i + read + lane;
       ids = next;
       next = p.num_blocks;
-      if (pg * kBlockSize < un.L && pg < un.t1 * kPages) {
+      if (pg >= first && pg * kBlockSize < un.L && pg < un.t1 * kPages) {
         const int id = __ldg(p.block_tables + static_cast<size_t>(un.b) * p.mbs + pg);
         if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks))
           next = id;

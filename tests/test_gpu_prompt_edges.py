@@ -51,3 +51,38 @@ def test_scores_that_a_few_bits_tell_apart(start, step, fp8):
     size = torch.einsum("nj,hjd->nhd", w, v.abs())
     assert torch.isfinite(got).all()
     assert ((got.double() - want).abs() <= 2.0 ** -8 * (want.abs() + size) * (1 + 2.0 ** -4)).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("mark", [-1, 2 ** 31 - 1])
+@pytest.mark.parametrize("window", [1, 16, 17, 100, 128, 300])
+def test_blocks_in_front_of_the_window_may_be_gone(window, mark, fp8):
+    """Table entries of blocks wholly before the first query token's window are not looked at, and
+    neither is what the blocks hold, as for single-token attention."""
+    kind = dict(fp8=fp8, extra_blocks=2)
+    for new, cached in (([300, 1, 130], [0, 400, 777]), ([1] * 9, [61 * i for i in range(9)])):
+        c = Prompts(2, new, cached, 8, 2, 128, **kind)
+        most = dict(window_size=window, k_scale=c.k_scale, v_scale=c.v_scale)
+
+        def attend(tables, **kw):
+            return pa.prompt_attention(c.q, c.k, c.v, tables, c.ctx, c.starts, c.most, **most, **kw)
+        want = attend(c.tables), attend(c.tables, partition_size=128)
+        assert pa.get_device_error() == 0
+        gone, held = c.tables.clone(), c.tables
+        for b, n in enumerate(cached):
+            first = max(0, n - window + 1) // 16
+            for blk in held[b, :first].tolist():
+                c.k[blk] = c.v[blk] = 0x7F if fp8 else float("nan")
+            gone[b, :first] = mark
+        got = attend(gone), attend(gone, partition_size=128)
+        assert pa.get_device_error() == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        if len(set(new)) == 1:                            # the same call of single-token attention
+            pa.attention(c.q[:, None], c.k, c.v, gone, c.ctx, c.most, **most)
+            assert pa.get_device_error() == 0
+        # the first block that the window reaches is looked at
+        b = max(range(len(cached)), key=cached.__getitem__)
+        gone[b, max(0, cached[b] - window + 1) // 16] = mark
+        attend(gone)
+        assert pa.get_device_error() == 5
