@@ -343,8 +343,8 @@ pa_status pa_decode_append(void* out, const void* q, const void* new_key, const 
  * octaves, so a head scale need only be of the order of the head's largest
  * magnitude / 1000 (between its largest magnitude / 3136, below which values saturate,
  * and a few thousandths of it); it lies in [2^-100, 2^100].  A NaN makes its 32 dims
- * NaN; infinities saturate.  pa_copy_blocks does not take these pages: copy-on-write copies
- * the num_kv_heads * page bytes of a block in each pool (cudaMemcpyAsync).
+ * NaN; infinities saturate.  Copy-on-write: pa_copy_block_bytes with the num_kv_heads * page
+ * bytes of a block.
  */
 
 /*
@@ -609,6 +609,15 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
                          int block_size, pa_stream_t stream);
 
 /*
+ * pa_copy_block_bytes — pa_copy_blocks for pages of any format: block b of a pool is its
+ * block_bytes bytes from b * block_bytes on, a multiple of 16 (FP8 pages: num_kv_heads *
+ * head_dim * 16; INT4 pages: num_kv_heads * 16 * (head_dim/2 + head_dim/32)).
+ */
+pa_status pa_copy_block_bytes(void* k_cache, void* v_cache, const int32_t* block_pairs,
+                              int num_pairs, int num_blocks, long long block_bytes,
+                              pa_stream_t stream);
+
+/*
  * pa_prompt_attention — causal attention of whole prompts, or of any number of
  * new tokens per sequence, over their pages.  Query tokens are packed: those of
  * sequence b are rows query_starts[b] .. query_starts[b + 1] - 1 of q, the
@@ -682,8 +691,9 @@ size_t pa_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, i
  *   slot_mapping  [num_tokens]   int64  slot of each packed row, -1 behind the last
  *                 (pa_reshape_and_cache skips those)
  *   positions     [num_tokens]   int32  its position in its sequence, or -1
- *   block_copies  [num_seqs, 2]  int32  (source, destination) for pa_copy_blocks,
- *                 (0, 0) for a sequence without a copy, which copies nothing
+ *   block_copies  [num_seqs, 2]  int32  (source, destination) for pa_copy_blocks or
+ *                 pa_copy_block_bytes, (0, 0) for a sequence without a copy, which
+ *                 copies nothing
  *
  * num_tokens is the host's bound on the sum of new_lens.  A call that cannot be
  * met (too few free blocks: PA_ERR_OUT_OF_BLOCKS on the device; more tokens than

@@ -937,20 +937,34 @@ def selftest_wait_timeout(timeout_ns: int, device=None) -> None:
 
 
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs) -> None:
-    """Copy whole physical blocks src -> dst in both pools (copy-on-write), bit-exact.
+    """Copy whole physical blocks src -> dst in both pools (copy-on-write), bit-exact: bf16, FP8
+    or INT4 pools.
 
-    ``pairs``: sequence of (src, dst) ids or an int32 tensor [n, 2] (host or device).
+    ``pairs``: sequence of (src, dst) ids or an int32 tensor [n, 2] (host or device), such as
+    ``extend_sequences`` returns; a pair with src == dst copies nothing.
     """
-    _need("k_cache", k_cache, torch.bfloat16, 4)
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    codes = k_cache.dtype == torch.uint8
+    kind = (torch.uint8, 3 if k_cache.dim() == 3 else 4) if codes else (torch.bfloat16, 4)
+    _need("k_cache", k_cache, *kind)
     dev = k_cache.device
-    _need("v_cache", v_cache, torch.bfloat16, 4, dev)
-    if v_cache.shape != k_cache.shape:
+    _need("v_cache", v_cache, *kind, dev)
+    shape = tuple(k_cache.shape)
+    if codes and len(shape) == 4:
+        shape = (shape[0], shape[1], shape[3], shape[2])     # V pages lie by head dim
+    if tuple(v_cache.shape) != shape:
         raise ValueError("inconsistent shapes")
     t = pairs if isinstance(pairs, torch.Tensor) else torch.tensor(list(pairs), dtype=torch.int32)
     t = t.to(device=dev, dtype=torch.int32).reshape(-1, 2).contiguous()
     if t.shape[0] == 0:
         return
-    NB, Hkv, BS, D = k_cache.shape
+    NB = shape[0]
+    if codes:
+        _call("pa_copy_block_bytes", dev, k_cache.data_ptr(), v_cache.data_ptr(), t.data_ptr(),
+              t.shape[0], NB, k_cache[0].numel() if NB else 0)
+        return
+    _, Hkv, BS, D = shape
     st = library().pa_copy_blocks(_vp(k_cache), _vp(v_cache), _vp(t), t.shape[0], NB, Hkv, D, BS,
                                   _stream(dev))
     _lib.check("pa_copy_blocks", st)

@@ -92,6 +92,7 @@ SIGNATURES = {
     "pa_truncate_sequences": (_i, [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]),
     "pa_token_logprobs": (_i, [_vp, _vp, _vp, _vp, _vp, ctypes.c_longlong, _i, _vp, _i, _i, _i,
                                _vp]),
+    "pa_copy_block_bytes": (_i, [_vp, _vp, _vp, _i, _i, ctypes.c_longlong, _vp]),
     "pa_bm_truncate": (_i, [_vp, _i, _i]),
     "pa_bm_create": (_i, [_i, _i, ctypes.POINTER(_vp)]),
     "pa_bm_destroy": (None, [_vp]),

@@ -651,13 +651,21 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
   if (num_pairs < 0 || num_blocks < 1 || num_kv_heads < 1 || head_dim < 8 || head_dim % 8 != 0)
     return PA_ERR_INVALID_ARG;
   if (block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+  return pa_copy_block_bytes(k_cache, v_cache, block_pairs, num_pairs, num_blocks,
+                             2ll * num_kv_heads * head_dim * block_size, stream);
+}
+
+pa_status pa_copy_block_bytes(void* k_cache, void* v_cache, const int32_t* block_pairs,
+                              int num_pairs, int num_blocks, long long block_bytes,
+                              pa_stream_t stream) {
+  if (num_pairs < 0 || num_blocks < 1 || block_bytes < 16 || block_bytes % 16 != 0)
+    return PA_ERR_INVALID_ARG;
   if (num_pairs == 0) return PA_OK;
   if (num_pairs > 65535) return PA_ERR_UNSUPPORTED;
   if (!k_cache || !v_cache || !block_pairs || !aligned16(k_cache) || !aligned16(v_cache))
     return PA_ERR_INVALID_ARG;
-  return launch_copy_blocks(k_cache, v_cache, block_pairs, num_pairs, num_blocks, num_kv_heads,
-                            head_dim, block_size, reinterpret_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
+  return launch_copy_blocks(k_cache, v_cache, block_pairs, num_pairs, num_blocks, block_bytes,
+                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

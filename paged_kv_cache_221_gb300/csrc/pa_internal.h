@@ -278,8 +278,7 @@ cudaError_t launch_reshape(const void* key, const void* value, void* k_cache, vo
                            const int64_t* slots, int num_tokens, int num_blocks, int hkv,
                            int head_dim, int block_size, cudaStream_t s);
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int num_pairs,
-                               int num_blocks, int hkv, int head_dim, int block_size,
-                               cudaStream_t s);
+                               int num_blocks, long long block_bytes, cudaStream_t s);
 cudaError_t launch_selftest_wait(unsigned long long timeout_ns, cudaStream_t s);
 
 // Prompt attention: bf16 or FP8 pages; tq maps q as [num_rows, Hkv, G, D].

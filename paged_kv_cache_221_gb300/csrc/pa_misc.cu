@@ -141,10 +141,9 @@ __global__ void __launch_bounds__(256)
 }
 
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int num_pairs,
-                               int num_blocks, int hkv, int head_dim, int block_size,
-                               cudaStream_t s) {
+                               int num_blocks, long long block_bytes, cudaStream_t s) {
   if (num_pairs == 0) return cudaSuccess;
-  const long long vecs = static_cast<long long>(hkv) * block_size * head_dim / 8;
+  const long long vecs = block_bytes / 16;
   const long long chunks = (vecs + 255) / 256;
   dim3 grid(static_cast<unsigned>(chunks < 64 ? chunks : 64), static_cast<unsigned>(num_pairs), 1);
   copy_blocks_kernel<<<grid, 256, 0, s>>>(static_cast<uint4*>(k_cache),
