@@ -76,6 +76,7 @@
 
 #include <cuda_bf16.h>
 #include <math_constants.h>
+#include <stddef.h>
 
 #include <algorithm>
 #include <atomic>
@@ -651,6 +652,12 @@ __device__ __forceinline__ void store16(uint32_t at, uint4 w) {
                : "memory");
 }
 
+__device__ __forceinline__ int load4(uint32_t at) {
+  int x;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
 __device__ __forceinline__ PromptUnit load_unit(const PromptUnit& from) {
   union {
     uint4 w[3];
@@ -1126,23 +1133,28 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           constexpr int kPageBytes = kBlockSize * D * 2;
           constexpr uint32_t kOnes = 0x3F803F80u;
           const int count = (un.t1 - un.t0) * Gm::kPages;
-          // keys of the unit that some query row sees; what nobody sees has weights of 0, so that
-          // any finite number does for it
-          const int begin = (p.window > 0 ? un.pos0 - p.window + 1 : 0) - un.t0 * kPromptTile;
-          const int end = last + 1 - un.t0 * kPromptTile;
-          auto sees = [&](int i, int id, int k) {
-            const int key = i * kBlockSize + k * kRows + r;
-            return id != p.num_blocks && key >= begin && key < end;
-          };
           const uint8_t* const pool = static_cast<const uint8_t*>(p.v_pool) +
                                       static_cast<size_t>(un.head) * kPageBytes + lane * 16;
           auto page_at = [&](int id) {
-            return pool + static_cast<size_t>(id == p.num_blocks ? 0 : id) * p.Hkv * kPageBytes;
+            // (pages of the pool: below 2^27)
+            return pool + static_cast<size_t>((id == p.num_blocks ? 0 : id) * p.Hkv) * kPageBytes;
           };
           PromptPages pages;
+          // what is seldom needed of the unit, not kept in registers over the pages
+          auto reload = [&]() {
+            const uint32_t at = smem_u32(&ms.unit[ui & 1]);
+            PromptUnit u;
+            u.b = load4(at + offsetof(PromptUnit, b));
+            u.ntok = load4(at + offsetof(PromptUnit, ntok));
+            u.pos0 = load4(at + offsetof(PromptUnit, pos0));
+            u.L = load4(at + offsetof(PromptUnit, L));
+            u.t0 = load4(at + offsetof(PromptUnit, t0));
+            u.t1 = load4(at + offsetof(PromptUnit, t1));
+            return u;
+          };
           auto id_of = [&](int i) {
             if (i < Gm::kAux || ((i ^ (i - Gm::kAux)) & 32) != 0)
-              pages.take(p, load_unit(ms.unit[ui & 1]), i & ~31, lane);
+              pages.take(p, reload(), i & ~31, lane);
             return __shfl_sync(0xffffffffu, pages.ids, i & 31);
           };
           const uint32_t mine = smem_u32(smem) + Gm::kVOff + (c >> 3) * Gm::kHalfBytes + r * 128 +
@@ -1155,14 +1167,18 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           for (int k = 0; k < kPieces; ++k) w[k] = load_once(page_at(next) + k * 512);
 #pragma unroll 1
           for (; i < count; i += Gm::kAux) {
-            const int nth = tiles + i / Gm::kPages, st = nth % Gm::kVStages;
             const int id = next;
             bool plain, exact = true;
 #pragma unroll 1
             for (bool again = true; !(plain = plain_in_f16(w)) && again; again = false) {
+              // what no query row sees has weights of 0, so that any finite number does for it
+              const PromptUnit u = reload();
+              const int key = u.t0 * kPromptTile + i * kBlockSize + r;
+              const int begin = p.window > 0 ? u.pos0 - p.window + 1 : 0, end = u.pos0 + u.ntok;
 #pragma unroll
               for (int k = 0; k < kPieces; ++k)
-                if (!sees(i, id, k)) w[k] = make_uint4(kOnes, kOnes, kOnes, kOnes);
+                if (id == p.num_blocks || key + k * kRows < begin || key + k * kRows >= end)
+                  w[k] = make_uint4(kOnes, kOnes, kOnes, kOnes);
             }
             if (__builtin_expect(plain, 1)) {
 #pragma unroll
@@ -1192,7 +1208,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                                     finite_bf16x2(w[k].z), finite_bf16x2(w[k].w));
                 }
                 if (__any_sync(0xffffffffu, bad != 0u))
-                  odd(load_unit(ms.unit[ui & 1]).t0 + i / Gm::kPages);
+                  odd(load4(smem_u32(&ms.unit[ui & 1].t0)) + i / Gm::kPages);
               }
             }
             if (i + Gm::kAux < count) next = id_of(i + Gm::kAux);
@@ -1203,6 +1219,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               const int far = __shfl_sync(0xffffffffu, later ? pages.next : pages.ids, ahead & 31);
               prefetch_l2(page_at(far) + lane * (kPageBytes / 32 - 16));
             }
+            const int nth = tiles + i / Gm::kPages, st = nth % Gm::kVStages;
             wait(&ms.v_empty[st], (static_cast<uint32_t>(nth / Gm::kVStages) & 1u) ^ 1u);
             if (!wait.all_ok()) break;
             const uint32_t to = mine + st * Gm::kTileBytes + i % Gm::kPages * (kBlockSize * 128);
