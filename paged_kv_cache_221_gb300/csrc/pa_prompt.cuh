@@ -126,7 +126,10 @@ struct PromptGeo {
 // of them by sums of eight); a reference is one of rounded products up to 2^26.
 constexpr float kPromptLimit = 65504.f, kPromptExact = 67108864.f;
 
-// A wait's limit: a try gives up after 4 us, so two seconds.
+// A wait's limit in tries.  One that fails takes 4.0 us on GB300 (measured with 1, 32 and 512
+// threads that wait, with and without a time hint, which changes nothing), so this is two seconds;
+// PTX gives no bound.  The clock instead of the count costs two registers that the roles do not
+// have: 24 prompts 409 us against 368.
 constexpr int kPromptTries = 1 << 19;
 
 // One unit of work.
