@@ -760,14 +760,19 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
     return new_lens
 
 
+def _int(x):
+    """x for a 32-bit argument: ctypes would take a larger one modulo 2^32."""
+    return max(-2 ** 31, min(2 ** 31 - 1, int(x)))
+
+
 @functools.lru_cache(maxsize=1024)
 def prompt_workspace_size(num_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int,
                           max_context_len: int, head_dim: int, partition_size: int = 0,
                           window_size: int = 0) -> int:
     """Scratch bytes ``prompt_attention`` needs with these sizes (0 if none)."""
-    return int(library().pa_prompt_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads,
-                                                  max_context_len, head_dim, 16, partition_size,
-                                                  window_size))
+    return int(library().pa_prompt_workspace_size(
+        _int(num_tokens), _int(num_seqs), _int(num_q_heads), _int(num_kv_heads),
+        _int(max_context_len), _int(head_dim), 16, _int(partition_size), _int(window_size)))
 
 
 def prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -802,7 +807,8 @@ def prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     B, mbs = block_tables.shape
     if Dq != D or context_lens.numel() != B or query_starts.numel() != B + 1:
         raise ValueError("inconsistent shapes")
-    mcl = max(1, _max_len(max_context_len, context_lens, 1))
+    mcl = _int(max(1, _max_len(max_context_len, context_lens, 1)))
+    window_size, partition_size = _int(window_size), _int(partition_size)
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -813,7 +819,7 @@ def prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     ws, wsb, keep = _scratch(dev, workspace, need)
     _call("pa_prompt_attention", dev, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr() if fp8 else None,
-          v_scale.data_ptr() if fp8 else None, _KV_FP8 if fp8 else _KV_BF16, int(window_size),
+          v_scale.data_ptr() if fp8 else None, _KV_FP8 if fp8 else _KV_BF16, window_size,
           block_tables.data_ptr(), mbs, context_lens.data_ptr(), mcl, query_starts.data_ptr(), N, B,
           NB, Hq, Hkv, D, BS, D ** -0.5 if scale is None else float(scale), partition_size, ws, wsb)
     return out
@@ -849,8 +855,8 @@ def extend_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor,
     if new_lens.numel() != B:
         raise ValueError("inconsistent shapes")
     num_tokens = int(num_tokens)
-    if num_tokens < 0:
-        raise ValueError("num_tokens must not be negative")
+    if not 0 <= num_tokens <= 2 ** 30:
+        raise ValueError("num_tokens must be between 0 and 2^30")
     starts = torch.empty(B + 1, dtype=_i32, device=dev)
     slots = torch.empty(num_tokens, dtype=_i64, device=dev)
     positions = torch.empty(num_tokens, dtype=_i32, device=dev)
@@ -908,7 +914,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, num_top: int = 0)
     top_tokens = torch.empty((N, num_top), dtype=_i32, device=dev)
     _call("pa_token_logprobs", dev, logprobs.data_ptr(), entropy.data_ptr(),
           top_logprobs.data_ptr(), top_tokens.data_ptr(), logits.data_ptr(), stride, dtype,
-          tokens.data_ptr(), N, V, num_top)
+          tokens.data_ptr(), _int(N), _int(V), num_top)
     return logprobs, entropy, top_logprobs, top_tokens
 
 
