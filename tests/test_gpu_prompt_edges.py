@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import paged_kv_cache_221_gb300 as pa
-from prompt_cases import Prompts
+from gpu_util import MAX_REL_L2
+from prompt_cases import Prompts, check
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,40 @@ def test_blocks_in_front_of_the_window_may_be_gone(window, mark, fp8):
         gone[b, max(0, cached[b] - window + 1) // 16] = mark
         attend(gone)
         assert pa.get_device_error() == 5
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B", [2, 4, 8])
+def test_cut_keys_shared_out_by_a_counter(B, fp8):
+    """Several short questions behind long contexts: their keys are cut and the partitions taken as
+    CTAs come free, whatever the workspace held, twice, and from a graph with other lengths."""
+    Hq, Hkv, D = 32, 8, 128
+    cached = [31999 - 3001 * b % 9000 for b in range(B)]
+    c = Prompts(3 + B, [64] * B, cached, Hq, Hkv, D, fp8=fp8)
+    size = pa.prompt_workspace_size(c.N, B, Hq, Hkv, c.most, D)
+    # partial results of every row, their statistics, and the counter
+    parts = (size - 256) // (c.N * Hq * (4 * D + 8))
+    assert parts > 1 and size == c.N * Hq * parts * (4 * D + 8) + 256
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+
+    def attend(**kw):
+        return pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, c.starts, c.most,
+                                   k_scale=c.k_scale, v_scale=c.v_scale, **kw)
+    got = attend(workspace=ws)
+    assert pa.get_device_error() == 0
+    want, size = c.exact()
+    check(got, want, size)
+    off = (got.double() - want).norm(dim=(0, 2)) / want.norm(dim=(0, 2))
+    assert off.max() <= MAX_REL_L2
+    assert torch.equal(attend(workspace=ws), got) and torch.equal(attend(), got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = attend(workspace=ws)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
+    c.ctx -= torch.arange(B, device="cuda").int() * 2000
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, attend()) and pa.get_device_error() == 0
