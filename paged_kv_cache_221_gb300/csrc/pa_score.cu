@@ -13,7 +13,7 @@
 // W warps has J threads at or above a value t, at least W J elements of the row are, so with
 // W J >= k only elements >= t can be among the k largest; t is the least of the warps' J-th
 // largest thread maxima, and then the k-th largest of the maxima that reach it.  A thread also
-// remembers where its maximum came from (a step of four vectors) and the largest of its other
+// remembers where its maximum came from (a step of two vectors) and the largest of its other
 // steps: nearly always that one step, of the few threads that matter, is all that is read again.
 // What is >= t goes to a list in shared memory, of which the k largest by (value, lower index)
 // are found exactly.  A list that overflows (ties without end, as in rows that are masked to
@@ -21,10 +21,10 @@
 // ones as are missing.
 //
 // The kernel is bound by reading the logits.  A cluster of CTAs shares a row when there are few
-// and long ones.  2048 rows of 128256 bf16 with 20 alternatives 97 us (5.4 TB/s); 64 of 128256 fp32 with 5 12.4 us, a launch and seven barriers on top of 5 us of
-// reading; 1000 of 32003 fp16 18.5 us.  With CTAs of 512 threads the first took 157 us (with
-// 256 others stream while one joins its row), of 128 threads 161, then 108 with 256; five or six
-// CTAs per SM as four.
+// and long ones.  2048 rows of 128256 bf16 with 20 alternatives 97 us (5.4 TB/s); 64 of 128256
+// fp32 with 5 12.4 us, a launch and seven barriers on top of 5 us of reading; 1000 of 32003 fp16
+// 18.5 us.  With CTAs of 512 threads the first took 157 us (with 256 others stream while one joins
+// its row), of 128 threads 161, then 108 with 256; five or six CTAs per SM as four.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const ScorePara
         if (at < kScoreList) sh.list[at] = entry_key(k, static_cast<uint32_t>(index));
       }
     };
-    // NaN passes through maxima, so rows with one look at everything
+    // (maxima pass over NaN, so a NaN may not be looked at; a row with one has NaN results, and
+    // any of its tokens as alternatives)
     auto collect = [&](bool above) {
       const bool mine = v0 + tid < v1 && !(above ? most <= bound : most < bound);
       const bool all = mine && !(above ? second <= bound : second < bound);
