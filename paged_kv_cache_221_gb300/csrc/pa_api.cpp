@@ -173,6 +173,10 @@ Plan make_plan(int num_seqs, int hq, int T, int max_ctx, int head_dim, int parti
   return pl;
 }
 
+// SMs of a GB300.  Plans and the workspaces that follow from them are made without asking a device;
+// launches ask it.
+constexpr int kPlanSms = 152;
+
 // Prompt attention: how the keys of a pair of query tiles are cut.
 struct PromptPlan {
   int sub_tokens = 1;     // query tokens of a tile
@@ -202,13 +206,13 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
     // with the fewest pairs of tiles that there can be (the device knows them alone), as many
     // partitions, of four K/V tiles at least, as give every SM a unit, or 1.75 where there are
     // several sequences, whose lengths mostly differ.  Measured, 64 tokens of 32 query heads over 8
-    // behind 4000 to 32000, one unit per SM / 1.75: 8 sequences 219 / 186 us, 4 119 / 84, 2 68 / 54
-    // (behind 16384 each: 8 142 / 149, 4 80 / 88); whole / cut: one 201 / 27, 4 203 / 88, 8 205 /
-    // 149, but 12 207 / 219, 16 215 / 272, 32 432 / 519
+    // behind 4000 to 32000, one unit per SM / 1.75: 8 sequences 257 / 212 us, 4 138 / 93, 2 79 / 58
+    // (behind 16384 each: 8 155 / 164, 4 88 / 99, 2 52 / 64); whole / cut, behind 16384: one
+    // 235 / 30, 4 238 / 99, 8 240 / 164, but 12 247 / 285, 16 253 / 302, 32 495 / 588
     const long long pairs = hkv * std::max(std::min<long long>(num_seqs, num_tokens),
                                            num_tokens / pair);
-    if (pairs <= 76)
-      pl.split = std::max(4, ceil_div(tiles, (num_seqs > 1 ? 266 : 152) / pairs));
+    if (pairs <= kPlanSms / 2)
+      pl.split = std::max(4, ceil_div(tiles, (num_seqs > 1 ? kPlanSms * 7 / 4 : kPlanSms) / pairs));
   }
   pl.split = std::min(pl.split, tiles);
   pl.max_parts = ceil_div(tiles, pl.split);
@@ -220,10 +224,11 @@ PromptPlan prompt_plan(long long num_tokens, int num_seqs, int hq, int hkv, int 
   }
   // CTAs take units as they come free instead of every 152nd where the units are few or long, so
   // that what is left over counts; the counter's reset is a launch of 3 us, and short units do not
-  // hide a claim.  Measured, as they come / every 152nd: 1 prompt of 2048 tokens 37 / 47 us, 4 of
-  // 1280 64 / 75, 12 FP8 ones up to 4096 583 / 604, 1 of 16384 1385 / 1461; but 24 of 512 97 / 87,
-  // 24 of 2048 700 / 684, 4 behind windows of 1000 360 / 350.
-  if (scratch && pl.units > 152 && pl.split > 8 && (pl.units < 8 * 152 || pl.split > 16)) {
+  // hide a claim.  Measured, as they come / every 152nd: 1 prompt of 2048 tokens 44 / 55 us, 4 of
+  // 1280 78 / 88, 12 FP8 ones up to 4096 575 / 598, 1 of 16384 1615 / 1750; but 24 of 512 125 / 104,
+  // 24 of 2048 865 / 785, 4 behind windows of 1000 438 / 411.
+  if (scratch && pl.units > kPlanSms && pl.split > 8 &&
+      (pl.units < 8 * kPlanSms || pl.split > 16)) {
     pl.counted = true;
     pl.bytes += 256;
   }
