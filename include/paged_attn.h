@@ -644,9 +644,10 @@ pa_status pa_copy_block_bytes(void* k_cache, void* v_cache, const int32_t* block
  * the GPU need workspaces of their own.  Softmax statistics and accumulation are
  * fp32; where they meet the values the weights have 11 bits (2^-11 of each at
  * most, and 2^-32 of the row's largest), so that outputs keep the relative L2
- * error of pa_attention, 2e-3 with normal inputs.  Sums of weight times value
- * past 2^112 overflow.  A slot that a query token must not see does not reach
- * it, whatever it holds; a NaN or infinity that it sees does.
+ * error of pa_attention, 2e-3 with normal inputs.  The sums carry 2^16 and have
+ * room for values of magnitude up to 2^74 in any context; larger ones (bf16
+ * pages) may overflow to infinity.  A slot that a query token must not see does
+ * not reach it, whatever it holds; a NaN or infinity that it sees does.
  * Requirements: pointers 16-byte aligned, head_dim 64 or 128, block_size 16,
  * num_q_heads / num_kv_heads at most 128, num_blocks * num_kv_heads * 16 below
  * 2^31.  A sequence with context_lens[b] < T_b or > max_context_len, or with

@@ -38,9 +38,9 @@
 // that f16 does not have (2^7 and more, below 2^-26) stays bf16, and so do its weights, each in
 // two parts that hold the f16, with a product for both; 16 keys are one step of the product, so
 // that pages of both kinds stand in one tile.  The byte v_split tells the others which.  O carries
-// 2^16 in all, so that sums of weight times value past 2^112 are infinite.  Infinities and NaN are
-// taken out of such a page, since 0 * inf would reach rows that must not see them, and added at the
-// end to the rows that do.
+// 2^16 in all, weights up to 2^8 above the reference and 2^30 keys at most: values up to 2^74 never
+// overflow it.  Infinities and NaN are taken out of such a page, since 0 * inf would reach rows that
+// must not see them, and added at the end to the rows that do.
 //
 // FP8 pages.  Every E4M3 value is an f16: warps 10 to 15 widen
 // each tile from where TMA left it into the ring that the MMAs read (K rows as they are; V

@@ -124,3 +124,27 @@ def test_cut_keys_shared_out_by_a_counter(B, fp8):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, attend()) and pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["codes", "mixed"])
+def test_every_value_by_itself(order, D):
+    """Rows that see one key return its values, bit for bit: every bf16 from 2^-126 to below 2^100
+    and 0, page by page alike and page by page of all sizes."""
+    codes = torch.arange(128, (127 + 100) << 7, device="cuda").int()
+    codes = torch.cat([codes, codes + 0x8000, torch.zeros(64, device="cuda").int()])
+    N = -(-codes.numel() // D)
+    codes = torch.cat([codes, codes[:N * D - codes.numel()]])
+    if order == "mixed":
+        g = torch.Generator(device="cuda").manual_seed(D)
+        codes = codes[torch.randperm(N * D, generator=g, device="cuda")]
+    rows = codes.to(torch.int16).view(torch.bfloat16).view(N, D)
+    c = Prompts(4, [N], [0], 4, 2, D)
+    j = torch.arange(N, device="cuda")
+    for head in range(2):
+        c.v[c.tables[0, j // 16].long(), head, j % 16] = rows
+    for kw in (dict(), dict(partition_size=128)):
+        got = pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, c.starts, c.most, window_size=1,
+                                  **kw)
+        assert pa.get_device_error() == 0
+        assert torch.equal(got, rows[:, None].expand(-1, 4, -1))
