@@ -644,7 +644,7 @@ pa_status pa_copy_block_bytes(void* k_cache, void* v_cache, const int32_t* block
  * the GPU need workspaces of their own.  Softmax statistics and accumulation are
  * fp32; where they meet the values the weights have 11 bits (2^-11 of each at
  * most, and 2^-32 of the row's largest), so that outputs keep the relative L2
- * error of pa_attention, 2e-3 with normal inputs.  The sums carry 2^16 and have
+ * error of pa_attention, 2e-3 with normal inputs.  The sums carry 2^15 and have
  * room for values of magnitude up to 2^74 in any context; larger ones (bf16
  * pages) may overflow to infinity.  A slot that a query token must not see does
  * not reach it, whatever it holds; a NaN or infinity that it sees does.

@@ -34,11 +34,11 @@
 // together pass the 2e-3 that the other attention kernels keep.
 //
 // V of bf16 pages.  The product takes two operands of one type, so the pages come through
-// registers and become f16 there, times 2^9.  That is exact or not done: a page with an element
-// that f16 does not have (2^7 and more, below 2^-26) stays bf16, and so do its weights, each in
+// registers and become f16 there, times 2^8.  That is exact or not done: a page with an element
+// that f16 does not have (2^8 and more, below 2^-25) stays bf16, and so do its weights, each in
 // two parts that hold the f16, with a product for both; 16 keys are one step of the product, so
 // that pages of both kinds stand in one tile.  The byte v_split tells the others which.  O carries
-// 2^16 in all, weights up to 2^8 above the reference and 2^30 keys at most: values up to 2^74 never
+// 2^15 in all, weights up to 2^8 above the reference and 2^30 keys at most: values up to 2^74 never
 // overflow it.  Infinities and NaN are taken out of such a page, since 0 * inf would reach rows that
 // must not see them, and added at the end to the rows that do.
 //
@@ -52,19 +52,23 @@
 // What bounds it.  A K/V tile of a pair is 2048 cycles of products.  A tile's weights take 1350
 // alone (an exponential is 4 cycles per warp instruction and scheduler; the rest beside it), its
 // P . V and next S with their hand-overs as much again, and the two tiles of a pair alternate: 2700
-// at least.  The warps that bring V issue 40 instructions for 512 bytes of it from the same four
-// schedulers: about 3100 in all (3500 for FP8 pages, whose K and V take two thirds of that to
+// at least.  The warps that bring V issue 45 instructions for 512 bytes of it from the same four
+// schedulers: about 3150 in all (3500 for FP8 pages, whose K and V take two thirds of that to
 // widen).  A unit's start and end are 10000 more: outputs written, 3500, and the first maximum,
-// while no product runs.  32 query heads over 8 of 128 dims: 16384 tokens 1700 us (1.29 PFLOP/s; a
-// library matrix product in a loop 1.69), 24 prompts of 128 to 2048 tokens 363 us (0.82), 12 of 512
+// while no product runs.  32 query heads over 8 of 128 dims: 16384 tokens 1730 us (1.27 PFLOP/s; a
+// library matrix product in a loop 1.69), 24 prompts of 128 to 2048 tokens 374 us (0.80), 12 of 512
 // to 4096 over FP8 pages 572 us (1.13), 33 tokens behind 65519 71 us (3.8 TB/s).
+//
+// By values, 24 prompts: normal ones, or with half of the dims zero, 369 us; times 0.02 377, times
+// 1e-3 (a third of the tiles have a page with an element below 2^-25) 544; all pages split 657.
 //
 // Measured on the way, 16384 tokens or as said.  The weights of bf16 pages in 8 bits, V as it is:
 // 1470 us (24 prompts 305), the precision above.  In two bf16 parts for all pages: 2118 (448).  V
 // made f16 where asynchronous copies left it: 1820 to 2010 (354 to 420), since shared memory is
-// read and written once more.  Through registers that spill: 2180 (515).  Without the prefetch to
-// L2 33 tokens behind 65519 76 us.  A sum of 64 weights as their limit, where sums of eight are now:
-// four windows of 1000 446 us against 419.
+// read and written once more.  Through registers that spill: 2180 (515).  Bits moved instead of a
+// conversion, in a path for pages without zeros: 1700 (361), but 605 for 24 prompts with half of
+// the dims zero.  Without the prefetch to L2 33 tokens behind 65519 76 us against 71.  A sum of 64
+// weights as their limit, where sums of eight are now: four windows of 1000 446 us against 419.
 // V by TMA boxes like K, 2300 cycles of the TMA unit for a K/V tile by themselves (a box of 16 keys
 // is about 70 whatever its bytes); three K and two V stages 1460 against 1417 us; two threads per
 // row (16 softmax warps) 1466; the rare code between that of most tiles 1430 against 1397, since
@@ -88,7 +92,7 @@
 
 namespace pa {
 
-constexpr int kPromptVShift = 9;
+constexpr int kPromptVShift = 8;
 
 template <int D, bool KV8>
 struct PromptGeo {
@@ -143,6 +147,7 @@ struct alignas(16) PromptUnit {
   int part, parts;
   int odd0, odd1;        // infinities or NaN were taken out of V tiles in [odd0, odd1)
 };
+static_assert(offsetof(PromptUnit, odd1) == offsetof(PromptUnit, odd0) + 4, "one address");
 
 template <int D, bool KV8>
 struct PromptMisc {
@@ -365,6 +370,11 @@ __device__ __forceinline__ void prefetch_l2(const uint8_t* at) {
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t y;
   asm("max.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
 __device__ __forceinline__ uint32_t add_u16x2(uint32_t a, uint32_t b) {
@@ -604,37 +614,29 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
                   e4m3x2_to_f16x2(w.w >> 16));
 }
 
-// bf16 values as f16 times 2^kPromptVShift.  Magnitudes from 2^-23 to below 2^7 become normal
-// numbers: their bits move by three and their exponents by a constant.
-constexpr uint32_t kPromptBias = (127 - kPromptVShift - 15) << 7;
-// Whether all of the warp's words w hold such: how far their magnitudes lie above the least (those
-// below it wrap round).
+// bf16 values as f16 times 2^kPromptVShift: whether all of the warp's words w hold magnitudes from
+// 2^-25, whose last bit is f16's smallest number then, to below 2^8, or 0.
 template <int N>
-__device__ __forceinline__ bool plain_in_f16(const uint4 (&w)[N]) {
-  constexpr uint32_t kBelow = 0x10000u - kPromptBias - (1 << 7), kSpan = 30 << 7;
-  uint32_t most[2] = {0u, 0u};
+__device__ __forceinline__ bool fits_f16(const uint4 (&w)[N]) {
+  constexpr uint32_t kMost = (127 - kPromptVShift + 16) << 7;
+  constexpr uint32_t kLeast = (127 - kPromptVShift - 17) << 7;
+  uint32_t most[2] = {0u, 0u}, least[2] = {~0u, ~0u};     // less 1, so that 0 is the largest
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      most[k & 1] = max_u16x2(most[k & 1], add_u16x2(x[k] & 0x7FFF7FFFu, kBelow << 16 | kBelow));
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t mag = x[k] & 0x7FFF7FFFu;
+      most[k & 1] = max_u16x2(most[k & 1], mag);
+      least[k & 1] = min_u16x2(least[k & 1], add_u16x2(mag, ~0u));
+    }
   }
   most[0] = max_u16x2(most[0], most[1]);
-  return __all_sync(0xffffffffu, max(most[0] & 0xFFFFu, most[0] >> 16) < kSpan);
+  least[0] = min_u16x2(least[0], least[1]);
+  return __all_sync(0xffffffffu, max(most[0] & 0xFFFFu, most[0] >> 16) < kMost &&
+                                     min(least[0] & 0xFFFFu, least[0] >> 16) >= kLeast - 1u);
 }
-__device__ __forceinline__ uint32_t plain_f16x2(uint32_t w) {
-  return ((w & 0x7FFF7FFFu) * 8u - (kPromptBias << 16 | kPromptBias) * 8u) | (w & 0x80008000u);
-}
-// Whether f16 has the word's two values at all: as that, or 0, or down to 2^-26, whose last bit is
-// f16's smallest number then.
-__device__ __forceinline__ bool exact_in_f16(uint32_t w) {
-  constexpr uint32_t kMost = (127 - kPromptVShift + 16) << 7;
-  constexpr uint32_t kLeast = (127 - kPromptVShift - 17) << 7;
-  const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
-  return max(lo, hi) < kMost && (lo == 0u || lo >= kLeast) && (hi == 0u || hi >= kLeast);
-}
-__device__ __forceinline__ uint32_t exact_f16x2(uint32_t w) {      // a 0 becomes one by rounding
+__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t w) {     // a 0 becomes one by rounding
   w += (kPromptVShift << 7) * 0x00010001u;
   return half2_bits(__floats2half2_rn(bf16_lo(w), bf16_hi(w)));
 }
@@ -1071,8 +1073,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         const int last = un.pos0 + un.ntok - 1;
         auto odd = [&](int t) {
           if (lane == 0) {
-            atomicMin(&ms.unit[ui & 1].odd0, t);
-            atomicMax(&ms.unit[ui & 1].odd1, t + 1);
+            const uint32_t at = smem_u32(&ms.unit[ui & 1].odd0);      // and odd1
+            asm volatile("red.shared.min.s32 [%0], %1;\n\tred.shared.max.s32 [%0 + 4], %2;" ::"r"(at),
+                         "r"(t), "r"(t + 1) : "memory");
           }
         };
         if constexpr (KV8) {
@@ -1134,7 +1137,6 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           constexpr int kPieces = kBlockSize / kRows;
           const int c = lane % kRowChunks, r = lane / kRowChunks;
           constexpr int kPageBytes = kBlockSize * D * 2;
-          constexpr uint32_t kOnes = 0x3F803F80u;
           const int count = (un.t1 - un.t0) * Gm::kPages;
           const uint8_t* const pool = static_cast<const uint8_t*>(p.v_pool) +
                                       static_cast<size_t>(un.head) * kPageBytes + lane * 16;
@@ -1171,9 +1173,9 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll 1
           for (; i < count; i += Gm::kAux) {
             const int id = next;
-            bool plain, exact = true;
+            bool fits;
 #pragma unroll 1
-            for (bool again = true; !(plain = plain_in_f16(w)) && again; again = false) {
+            for (bool again = true; !(fits = fits_f16(w)) && again; again = false) {
               // what no query row sees has weights of 0, so that any finite number does for it
               const PromptUnit u = reload();
               const int key = u.t0 * kPromptTile + i * kBlockSize + r;
@@ -1181,38 +1183,26 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < kPieces; ++k)
                 if (id == p.num_blocks || key + k * kRows < begin || key + k * kRows >= end)
-                  w[k] = make_uint4(kOnes, kOnes, kOnes, kOnes);
+                  w[k] = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (__builtin_expect(plain, 1)) {
+            if (__builtin_expect(fits, 1)) {
 #pragma unroll
               for (int k = 0; k < kPieces; ++k)
-                w[k] = make_uint4(plain_f16x2(w[k].x), plain_f16x2(w[k].y), plain_f16x2(w[k].z),
-                                  plain_f16x2(w[k].w));
+                w[k] = make_uint4(scaled_f16x2(w[k].x), scaled_f16x2(w[k].y), scaled_f16x2(w[k].z),
+                                  scaled_f16x2(w[k].w));
             } else {
+              // the page stays bf16: infinities and NaN come out; the rows that see them get them at
+              // the end
+              uint32_t bad = 0u;
 #pragma unroll
-              for (int k = 0; k < kPieces; ++k)
-                exact = exact && exact_in_f16(w[k].x) && exact_in_f16(w[k].y) &&
-                        exact_in_f16(w[k].z) && exact_in_f16(w[k].w);
-              exact = __all_sync(0xffffffffu, exact);
-              if (exact) {
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k)
-                  w[k] = make_uint4(exact_f16x2(w[k].x), exact_f16x2(w[k].y), exact_f16x2(w[k].z),
-                                    exact_f16x2(w[k].w));
-              } else {
-                // the page stays bf16: infinities and NaN come out; the rows that see them get
-                // them at the end
-                uint32_t bad = 0u;
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                  bad |= nonfinite_bf16x2(w[k].x) | nonfinite_bf16x2(w[k].y) |
-                         nonfinite_bf16x2(w[k].z) | nonfinite_bf16x2(w[k].w);
-                  w[k] = make_uint4(finite_bf16x2(w[k].x), finite_bf16x2(w[k].y),
-                                    finite_bf16x2(w[k].z), finite_bf16x2(w[k].w));
-                }
-                if (__any_sync(0xffffffffu, bad != 0u))
-                  odd(load4(smem_u32(&ms.unit[ui & 1].t0)) + i / Gm::kPages);
+              for (int k = 0; k < kPieces; ++k) {
+                bad |= nonfinite_bf16x2(w[k].x) | nonfinite_bf16x2(w[k].y) |
+                       nonfinite_bf16x2(w[k].z) | nonfinite_bf16x2(w[k].w);
+                w[k] = make_uint4(finite_bf16x2(w[k].x), finite_bf16x2(w[k].y),
+                                  finite_bf16x2(w[k].z), finite_bf16x2(w[k].w));
               }
+              if (__any_sync(0xffffffffu, bad != 0u))
+                odd(load4(smem_u32(&ms.unit[ui & 1].t0)) + i / Gm::kPages);
             }
             if (i + Gm::kAux < count) next = id_of(i + Gm::kAux);
             // (and the page behind it to L2, for contexts that come out of memory)
@@ -1235,7 +1225,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               store16(place(k), w[k]);
               w[k] = load_once(from + k * 512);
             }
-            if (lane == 0) ms.v_split[st][i % Gm::kPages] = exact ? 0 : 1;
+            if (lane == 0) ms.v_split[st][i % Gm::kPages] = fits ? 0 : 1;
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.v_full[st]);

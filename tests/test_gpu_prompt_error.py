@@ -105,3 +105,15 @@ def test_weights_of_every_size():
             c.k[blk, :, 0, 0] = gap / 16.0 * 128 ** 0.5
             c.v[blk, :, 0] = 0
         run(c)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_with_zeros(D):
+    """Head dims, keys and pages of zeros, of both signs."""
+    c = Prompts(11, [300, 60], [0, 1000], 8, 2, D)
+    c.v[..., D // 2:] = 0
+    c.v[:, :, 3] = -0.0
+    c.v[int(c.tables[0, 2])] = 0
+    run(c)
+    run(c, partition_size=256)
+    run(c, window=150)
