@@ -921,8 +921,9 @@ int pa_bm_num_tokens(const pa_block_manager* bm, int seq_id);
 /*
  * pa_get_device_error — synchronise `stream`, then return and clear the sticky
  * device error word: PA_ERR_TIMEOUT if any pipeline wait gave up, else
- * PA_ERR_BOUNDS if any out-of-range id, slot or length was seen, else PA_OK
- * (PA_ERR_CUDA if the synchronisation itself failed).
+ * PA_ERR_BOUNDS if any out-of-range id, slot or length was seen, else
+ * PA_ERR_OUT_OF_BLOCKS if pa_extend_sequences had too few free blocks, else
+ * PA_OK (PA_ERR_CUDA if the synchronisation itself failed).
  */
 pa_status pa_get_device_error(pa_stream_t stream);
 
