@@ -38,9 +38,10 @@
 // that f16 does not have (2^8 and more, below 2^-25) stays bf16, and so do its weights, each in
 // two parts that hold the f16, with a product for both; 16 keys are one step of the product, so
 // that pages of both kinds stand in one tile.  The byte v_split tells the others which.  O carries
-// 2^15 in all, weights up to 2^8 above the reference and 2^30 keys at most: values up to 2^74 never
-// overflow it.  Infinities and NaN are taken out of such a page, since 0 * inf would reach rows that
-// must not see them, and added at the end to the rows that do.
+// 2^15 in all, weights up to 2^8 above the reference and 2^30 keys at most: values up to 2^74
+// never overflow it.  Infinities and NaN stay in a page that every row sees; from others they are
+// taken out, since 0 * inf would reach rows that must not see them, and added at the end to the
+// rows that do.
 //
 // FP8 pages.  Every E4M3 value is an f16: warps 10 to 15 widen
 // each tile from where TMA left it into the ring that the MMAs read (K rows as they are; V
@@ -145,9 +146,8 @@ struct alignas(16) PromptUnit {
   int L;                 // context length
   int t0, t1;            // K/V tiles [t0, t1)
   int part, parts;
-  int odd0, odd1;        // infinities or NaN were taken out of V tiles in [odd0, odd1)
+  int nonfinite;         // infinities or NaN were taken out of V pages at the mask's border
 };
-static_assert(offsetof(PromptUnit, odd1) == offsetof(PromptUnit, odd0) + 4, "one address");
 
 template <int D, bool KV8>
 struct PromptMisc {
@@ -163,7 +163,7 @@ struct PromptMisc {
   uint64_t fin;
   PromptUnit unit[2];
   uint32_t tmem_base;
-  alignas(8) uint8_t v_split[Gm::kVStages][Gm::kPages];  // 1: the page of V stays bf16
+  alignas(8) uint8_t v_split[Gm::kVStages][Gm::kPages];  // 0, kSplitPage or kOddPage
   int8_t q_exp[KV8 ? 2 : 1][2][KV8 ? kPromptTile : 1];   // by record, tile, row: of the factor
 };
 
@@ -215,8 +215,7 @@ __device__ __forceinline__ bool prompt_unit(const PromptParams& p, int u, Prompt
   if (un.part >= un.parts) return false;
   un.t0 = a + un.part * p.split;
   un.t1 = min(e, un.t0 + p.split);
-  un.odd0 = un.t1;
-  un.odd1 = un.t0;
+  un.nonfinite = 0;
   return true;
 }
 
@@ -396,9 +395,9 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* from) {
 __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
-__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
-  const uint32_t bad = nonfinite_bf16x2(w);
-  return w & ~((bad >> 15) * 0xFFFFu);
+// (mask: 0xFFFF, or 0 to leave them)
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, uint32_t mask) {
+  return w & ~((nonfinite_bf16x2(w) >> 15) * mask);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
@@ -447,8 +446,9 @@ __device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int lane) {
     b = x;
 }
 
-// A tile's pages of V that stay bf16, as bits; kSplitUnknown: not looked up.
-constexpr uint32_t kSplitUnknown = 1u << 31;
+// A page of V that stays bf16, and one of them that holds infinities or NaN; a tile's as bits
+// (page_bit, and the one above it).  kSplitUnknown: not looked up.
+constexpr uint32_t kSplitPage = 1u, kOddPage = 3u, kSplitUnknown = 1u << 31;
 __host__ __device__ constexpr uint32_t page_bit(int pg) { return 1u << (pg % 4 * 8 + pg / 4 * 4); }
 __device__ __forceinline__ uint32_t split_pages(uint32_t bytes) {
   uint2 w;
@@ -534,20 +534,25 @@ struct PromptScores {
     }
   }
   // A quarter's weights for the V pages of `split` that stay bf16: times 2^kPromptVShift and in two
-  // bf16 parts, which hold the f16 exactly; the second lies 64 columns behind the first.
+  // bf16 parts, which hold the f16 exactly; the second lies 64 columns behind the first.  Where they
+  // meet infinities, which every row sees, neither part is 0: weights are f16's smallest at least,
+  // and a second part of 2^-20 stands for none.
   __device__ __forceinline__ void split_quarter(int q, uint32_t taddr, uint32_t split) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!(split & page_bit(2 * q + h))) continue;
+      const bool odd = (split & page_bit(2 * q + h) << 1) != 0u;
+      const float least = odd ? 0x1p-24f : 0.f, none = odd ? 0x1p-20f : 0.f;
       uint32_t rest[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         uint32_t& x = w[q][8 * h + k];
         float2 e = __half22float2(*reinterpret_cast<const __half2*>(&x));
-        e.x *= static_cast<float>(1 << kPromptVShift);
-        e.y *= static_cast<float>(1 << kPromptVShift);
-        x = pack_bf16x2_rn(e.x, e.y);
-        rest[k] = pack_bf16x2_rn(e.x - bf16_lo(x), e.y - bf16_hi(x));
+        e.x = fmaxf(e.x, least) * static_cast<float>(1 << kPromptVShift);
+        e.y = fmaxf(e.y, least) * static_cast<float>(1 << kPromptVShift);
+        x = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);     // towards 0
+        const float r0 = e.x - bf16_lo(x), r1 = e.y - bf16_hi(x);
+        rest[k] = pack_bf16x2_rn(r0 == 0.f ? e.x * none : r0, r1 == 0.f ? e.y * none : r1);
       }
       tc::tmem_st8(taddr + kPromptTile / 2 + q * 16 + h * 8, rest);
     }
@@ -1071,12 +1076,10 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
         const PromptUnit un = load_unit(ms.unit[ui & 1]);
         if (un.b < 0) break;
         const int last = un.pos0 + un.ntok - 1;
-        auto odd = [&](int t) {
-          if (lane == 0) {
-            const uint32_t at = smem_u32(&ms.unit[ui & 1].odd0);      // and odd1
-            asm volatile("red.shared.min.s32 [%0], %1;\n\tred.shared.max.s32 [%0 + 4], %2;" ::"r"(at),
-                         "r"(t), "r"(t + 1) : "memory");
-          }
+        auto taken_out = [&]() {
+          if (lane == 0)
+            asm volatile("st.shared.b32 [%0], 1;" ::"r"(smem_u32(&ms.unit[ui & 1].nonfinite))
+                         : "memory");
         };
         if constexpr (KV8) {
 #pragma unroll 1
@@ -1114,7 +1117,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 const bool found = widen_values<D>(
                     base + Gm::kVOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux,
                     prompt_masked(p, t, un.pos0, last), un.L - t * kPromptTile);
-                if (__any_sync(0xffffffffu, found)) odd(t);
+                if (__any_sync(0xffffffffu, found)) taken_out();
               } else {
                 widen_keys<D>(base + Gm::kKOff + st * Gm::kTileBytes, raw, lane, aux, Gm::kAux);
               }
@@ -1157,6 +1160,14 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             u.t1 = load4(at + offsetof(PromptUnit, t1));
             return u;
           };
+          // whether some query row must not see all of page i
+          auto border = [&](int i) {
+            const uint32_t at = smem_u32(&ms.unit[ui & 1]);
+            const int first = load4(at + offsetof(PromptUnit, pos0)) -
+                              load4(at + offsetof(PromptUnit, t0)) * kPromptTile - i * kBlockSize;
+            return first < kBlockSize - 1 ||
+                   (p.window > 0 && first + load4(at + offsetof(PromptUnit, ntok)) > p.window);
+          };
           auto id_of = [&](int i) {
             if (i < Gm::kAux || ((i ^ (i - Gm::kAux)) & 32) != 0)
               pages.take(p, reload(), i & ~31, lane);
@@ -1173,6 +1184,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll 1
           for (; i < count; i += Gm::kAux) {
             const int id = next;
+            uint32_t kind = 0u;
             bool fits;
 #pragma unroll 1
             for (bool again = true; !(fits = fits_f16(w)) && again; again = false) {
@@ -1191,18 +1203,20 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
                 w[k] = make_uint4(scaled_f16x2(w[k].x), scaled_f16x2(w[k].y), scaled_f16x2(w[k].z),
                                   scaled_f16x2(w[k].w));
             } else {
-              // the page stays bf16: infinities and NaN come out; the rows that see them get them at
-              // the end
+              // the page stays bf16; infinities and NaN stay where every query row sees it, else
+              // they come out, and the rows that see them get them at the end
+              const uint32_t mask = border(i) ? 0xFFFFu : 0u;
               uint32_t bad = 0u;
 #pragma unroll
               for (int k = 0; k < kPieces; ++k) {
                 bad |= nonfinite_bf16x2(w[k].x) | nonfinite_bf16x2(w[k].y) |
                        nonfinite_bf16x2(w[k].z) | nonfinite_bf16x2(w[k].w);
-                w[k] = make_uint4(finite_bf16x2(w[k].x), finite_bf16x2(w[k].y),
-                                  finite_bf16x2(w[k].z), finite_bf16x2(w[k].w));
+                w[k] = make_uint4(finite_bf16x2(w[k].x, mask), finite_bf16x2(w[k].y, mask),
+                                  finite_bf16x2(w[k].z, mask), finite_bf16x2(w[k].w, mask));
               }
-              if (__any_sync(0xffffffffu, bad != 0u))
-                odd(load4(smem_u32(&ms.unit[ui & 1].t0)) + i / Gm::kPages);
+              const bool any = __any_sync(0xffffffffu, bad != 0u);
+              kind = any && mask == 0u ? kOddPage : kSplitPage;
+              if (any && mask != 0u) taken_out();
             }
             if (i + Gm::kAux < count) next = id_of(i + Gm::kAux);
             // (and the page behind it to L2, for contexts that come out of memory)
@@ -1225,7 +1239,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
               store16(place(k), w[k]);
               w[k] = load_once(from + k * 512);
             }
-            if (lane == 0) ms.v_split[st][i % Gm::kPages] = fits ? 0 : 1;
+            if (lane == 0) ms.v_split[st][i % Gm::kPages] = static_cast<uint8_t>(kind);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.v_full[st]);
@@ -1376,8 +1390,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 
       // -------------------------------------------------------------- unit output
       wait(&ms.unit_checked[ui & 1], static_cast<uint32_t>(ui >> 1) & 1u);
-      const int odd0 = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].odd0);
-      const int odd1 = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].odd1);
+      const bool special = *reinterpret_cast<volatile int*>(&ms.unit[ui & 1].nonfinite) != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.unit_empty[ui & 1]);
       const bool any = sub.e > sub.a;
@@ -1462,7 +1475,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
       }
       // the infinities and NaN that were taken out of V, for the rows that see them: a row at a
       // time, its dims over the lanes
-      if (__builtin_expect(odd0 < odd1 && any, 0)) {
+      if (__builtin_expect(special && any, 0)) {
         __syncwarp();
         float add[D / 32];
         int seen = -1;                                  // token that they are of
@@ -1474,13 +1487,16 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) add[k] = 0.f;
             const int at = sub.first + tk, begin = p.window > 0 ? at - p.window + 1 : 0;
-            const int stop = min(at + 1, min(sub.e, odd1) * kPromptTile);
+            for (int t = sub.a; t < sub.e; ++t) {
+              if (!prompt_masked(p, t, un.pos0, un.pos0 + un.ntok - 1)) continue;
+              const int stop = min(at, t * kPromptTile + kPromptTile - 1);
 #pragma unroll 4
-            for (int j = max(max(sub.a, odd0) * kPromptTile, begin); j < stop; ++j) {
+              for (int j = max(t * kPromptTile, begin); j <= stop; ++j) {
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k) {
-                const float v = prompt_value<D, KV8>(p, un, j, k * 32 + lane);
-                add[k] += fabsf(v) < CUDART_INF_F ? 0.f : v;
+                for (int k = 0; k < D / 32; ++k) {
+                  const float v = prompt_value<D, KV8>(p, un, j, k * 32 + lane);
+                  add[k] += fabsf(v) < CUDART_INF_F ? 0.f : v;
+                }
               }
             }
           }

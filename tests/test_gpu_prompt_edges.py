@@ -148,3 +148,72 @@ def test_every_value_by_itself(order, D):
                                   **kw)
         assert pa.get_device_error() == 0
         assert torch.equal(got, rows[:, None].expand(-1, 4, -1))
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("gap", [5, 25, 40, 80, 200])
+def test_infinities_of_small_weights(gap, value):
+    """An infinite or NaN value reaches the rows that see it however small its weight is, in pages
+    that all rows see as at the mask's border; other head dims stay as they are."""
+    c = Prompts(5, [200, 3], [400, 40], 4, 2, 128)
+    c.q[:, :, 0] = 16.0
+    c.k[:, :, :, 0] = 0
+    for b, keys in enumerate(((7, 100, 395, 420), (5, 41))):
+        for j in keys:
+            blk = int(c.tables[b, j // 16])
+            c.k[blk, :, j % 16] = 0
+            c.k[blk, :, j % 16, 0] = -gap / 16.0 * 128 ** 0.5
+            c.v[blk, :, j % 16, j % 128] = value
+    for kw in (dict(), dict(partition_size=128), dict(window_size=330)):
+        got = pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, c.starts, c.most, **kw)
+        assert pa.get_device_error() == 0
+        check(got, *c.exact(window=kw.get("window_size", 0)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_values_that_are_not_finite_anywhere(fp8):
+    """Scattered over a long context, of both signs, and nothing else in some head dims."""
+    c = Prompts(6, [300, 64], [3000, 9000], 8, 2, 128, fp8=fp8)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    at = torch.rand(c.v.shape, generator=g, device="cuda")
+    if fp8:
+        c.v[at < 2e-6] = 0x7F
+        c.v[:, :, 17] = 0x7F
+    else:
+        c.v[at < 1e-6] = math.inf
+        c.v[at > 1 - 1e-6] = -math.inf
+        c.v[..., 17] = math.nan
+        c.v[..., 18] = math.inf
+    for kw in (dict(), dict(partition_size=1024), dict(window_size=500)):
+        got = pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, c.starts, c.most,
+                                  k_scale=c.k_scale, v_scale=c.v_scale, **kw)
+        assert pa.get_device_error() == 0
+        out, size = exact_of_parts(c, kw.get("window_size", 0))
+        check(got, out, size)
+
+
+def exact_of_parts(c, window):
+    """As Prompts.exact, the values that are not finite apart: a row that sees some in a head dim
+    has their sum there."""
+    kind = 0x7F if c.fp8 else None
+    odd = c.v == kind if c.fp8 else ~torch.isfinite(c.v)
+    used = c.v.clone()
+    c.v = torch.where(odd, torch.zeros_like(used), used)
+    out, size = c.exact(window=window)
+    c.v = used
+    row, G = 0, c.Hq // c.Hkv
+    for b, (n, L) in enumerate(zip(c.new, c.lens)):
+        _, v = c.kv(b)
+        pos = torch.arange(L - n, L, device="cuda")
+        first = (pos - window + 1).clamp(min=0) if window else torch.zeros_like(pos)
+        v = v.repeat_interleave(G, 0)
+        seen = {}
+        for name, mark in (("nan", torch.isnan(v)), ("inf", v == math.inf), ("-inf", v == -math.inf)):
+            count = torch.cat([torch.zeros_like(v[:, :1]), mark.double().cumsum(1)], 1)
+            seen[name] = (count[:, pos + 1] - count[:, first] > 0).transpose(0, 1)
+        rows = slice(row, row + n)
+        out[rows] = torch.where(seen["inf"], math.inf, out[rows])
+        out[rows] = torch.where(seen["-inf"], torch.where(seen["inf"], math.nan, -math.inf), out[rows])
+        out[rows] = torch.where(seen["nan"], math.nan, out[rows])
+        row += n
+    return out, size
