@@ -131,6 +131,10 @@ struct PromptGeo {
 // of them by sums of eight); a reference is one of rounded products up to 2^26.
 constexpr float kPromptLimit = 65504.f, kPromptExact = 67108864.f;
 
+// What a sum of weights is multiplied by at least when a far larger one joins it: with 0 an infinity
+// in it would become NaN.
+constexpr float kPromptFaint = 0x1p-149f;
+
 // A wait's limit in tries.  One that fails takes 4.0 us on GB300 (measured with 1, 32 and 512
 // threads that wait, with and without a time hint, which changes nothing), so this is two seconds;
 // PTX gives no bound.  The clock instead of the count costs two registers that the roles do not
@@ -1338,7 +1342,7 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
             const bool exact = fabsf(ref) <= kPromptExact;
             const bool move = look && m > ref + (steady || !exact ? 0.f : 8.f);
             if (__any_sync(0xffffffffu, move)) {
-              const float f = move ? hw_exp2(ref - m) : 1.f;
+              const float f = move ? fmaxf(hw_exp2(ref - m), kPromptFaint) : 1.f;
               ref = move ? m : ref;
               sum *= f;
               if (t > sub.a) {
@@ -1569,7 +1573,7 @@ __global__ void __launch_bounds__(kPromptMergeWarps * 32) prompt_merge_kernel(co
     float w = 0.f;                                      // of partition i0 + lane
     if (lane < kPromptMergeParts && i0 + lane < un.parts) {
       const float2 x = __ldcg(ml + i0 + lane);
-      if (x.y != 0.f) w = x.y * hw_exp2(x.x - M);
+      if (x.y != 0.f) w = fmaxf(x.y * hw_exp2(x.x - M), kPromptFaint);
     }
 #pragma unroll
     for (int k = 0; k < kPromptMergeParts; ++k) {

@@ -217,3 +217,22 @@ def exact_of_parts(c, window):
         out[rows] = torch.where(seen["nan"], math.nan, out[rows])
         row += n
     return out, size
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("gap", [60, 100, 300])
+def test_infinities_behind_far_larger_scores(gap, value):
+    """What was summed before a far larger score keeps its infinities, in one pass over the keys and
+    where partitions are joined."""
+    c = Prompts(7, [100], [600], 4, 2, 128)
+    c.q[:, :, 0] = 16.0
+    c.k[:, :, :, 0] = 0
+    for j in range(300):
+        c.k[int(c.tables[0, j // 16]), :, j % 16, 0] = -gap / 16.0 * 128 ** 0.5
+    c.v[int(c.tables[0, 1]), :, 4, 9] = value             # of key 20
+    for kw in (dict(), dict(partition_size=128), dict(partition_size=256)):
+        got = pa.prompt_attention(c.q, c.k, c.v, c.tables, c.ctx, c.starts, c.most, **kw)
+        assert pa.get_device_error() == 0
+        out, size = c.exact()
+        assert (out[:, :, 9] == value).all()
+        check(got, out, size)
