@@ -64,3 +64,31 @@ def test_large_values_of_few_threads(N, dtype):
         y = x.clone()
         y[:, few] += 50.0
         run(y, t, 32)
+
+
+@pytest.mark.parametrize("N,V", [(200, 4096), (4, 60000)])
+def test_signs(N, V):
+    """A log probability is never above 0 and an entropy never below, also where one token has
+    nearly all of the probability and rounding is all that is left."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    for low in (-20.0, -40.0, -80.0):
+        x = torch.randn((N, V), generator=g, device="cuda") + low
+        rows = torch.arange(N, device="cuda")
+        near = 5.4 * torch.rand(N, generator=g, device="cuda")
+        shift = 10 * torch.randn(N, generator=g, device="cuda")
+        x[rows, torch.randint(0, V // 2, (N,), generator=g, device="cuda")] = -near - 20.0
+        at = torch.randint(V // 2, V, (N,), generator=g, device="cuda")
+        x[rows, at] = 0.0
+        x += shift[:, None]
+        lp, h, top, _ = pa.token_logprobs(x, at.int(), 5)
+        run(x, at.int(), 5)
+        assert (lp <= 0).all() and (top <= 0).all() and (h >= 0).all()
+        x[rows, torch.randint(0, V // 2, (N,), generator=g, device="cuda")] = shift - near
+        lp, h, top, _ = pa.token_logprobs(x, at.int(), 5)
+        run(x, at.int(), 5)
+        assert (lp <= 0).all() and (top <= 0).all() and (h >= 0).all()
+    x = torch.full((N, V), -math.inf, device="cuda")
+    x[:, 5] = shift
+    x[:, 5] += 0.1
+    lp, h, top, _ = pa.token_logprobs(x, torch.full((N,), 5, dtype=torch.int32, device="cuda"), 1)
+    assert (lp == 0).all() and (h == 0).all() and (top == 0).all()
