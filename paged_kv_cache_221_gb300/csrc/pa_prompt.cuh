@@ -537,30 +537,6 @@ struct PromptScores {
       }
     }
   }
-  // A quarter's weights for the V pages of `split` that stay bf16: times 2^kPromptVShift and in two
-  // bf16 parts, which hold the f16 exactly; the second lies 64 columns behind the first.  Where they
-  // meet infinities, which every row sees, neither part is 0: weights are f16's smallest at least,
-  // and a second part of 2^-20 stands for none.
-  __device__ __forceinline__ void split_quarter(int q, uint32_t taddr, uint32_t split) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!(split & page_bit(2 * q + h))) continue;
-      const bool odd = (split & page_bit(2 * q + h) << 1) != 0u;
-      const float least = odd ? 0x1p-24f : 0.f, none = odd ? 0x1p-20f : 0.f;
-      uint32_t rest[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint32_t& x = w[q][8 * h + k];
-        float2 e = __half22float2(*reinterpret_cast<const __half2*>(&x));
-        e.x = fmaxf(e.x, least) * static_cast<float>(1 << kPromptVShift);
-        e.y = fmaxf(e.y, least) * static_cast<float>(1 << kPromptVShift);
-        x = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);     // towards 0
-        const float r0 = e.x - bf16_lo(x), r1 = e.y - bf16_hi(x);
-        rest[k] = pack_bf16x2_rn(r0 == 0.f ? e.x * none : r0, r1 == 0.f ? e.y * none : r1);
-      }
-      tc::tmem_st8(taddr + kPromptTile / 2 + q * 16 + h * 8, rest);
-    }
-  }
   __device__ __forceinline__ float total() const {
     const uint64_t y = add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3]));
     return __uint_as_float(static_cast<uint32_t>(y)) + __uint_as_float(static_cast<uint32_t>(y >> 32));
@@ -576,27 +552,50 @@ struct PromptScores {
     return fmaxf(max3(max3(y[0], y[1], y[2]), y[3], y[4]), max3(y[5], y[6], y[7]));
   }
   // The weights over the scores, the first half of the keys announced once the third quarter is
-  // computed; the second half is stored, not yet complete.
-  __device__ __forceinline__ void finish(uint32_t taddr, uint64_t* half, int lane,
-                                         uint32_t split) {
-    if (__builtin_expect(split != 0u, 0)) {
-      split_quarter(0, taddr, split);
-      split_quarter(1, taddr, split);
-    }
+  // computed (if that is all of them: `announce`); the second half is stored, not yet complete.
+  __device__ __forceinline__ void finish(uint32_t taddr, uint64_t* half, bool announce) {
     tc::tmem_st16(taddr, w[0]);
     tc::tmem_st16(taddr + 16, w[1]);
     weights<32, 48>([](int) {});
     tc::tmem_wait_st();
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(half);
-    if (__builtin_expect(split != 0u, 0)) split_quarter(2, taddr, split);
+    if (announce) mbar_arrive(half);
     tc::tmem_st16(taddr + 32, w[2]);
     weights<48, 64>([](int) {});
-    if (__builtin_expect(split != 0u, 0)) split_quarter(3, taddr, split);
     tc::tmem_st16(taddr + 48, w[3]);
   }
 };
+
+// The weights of a tile, stored as f16, for the V pages of `split` that stay bf16: times
+// 2^kPromptVShift and in two bf16 parts, which hold the f16 exactly; the second lies 64 columns
+// behind the first.  Where they meet infinities, which every row sees, neither part is 0: weights
+// are f16's smallest at least, and a second part of 2^-20 stands for none.  (A loop of little code,
+// which all roles' instructions have to share a cache with.)
+__device__ __forceinline__ void split_weights(uint32_t taddr, uint32_t split) {
+#pragma unroll 1
+  for (int pg = 0; pg < kPromptTile / kBlockSize; ++pg) {
+    if (!(split & page_bit(pg))) continue;
+    const bool odd = (split & page_bit(pg) << 1) != 0u;
+    const float least = odd ? 0x1p-24f : 0.f, none = odd ? 0x1p-20f : 0.f;
+    uint32_t x[8], rest[8];
+    tc::tmem_ld8(taddr + pg * 8, x);
+    tc::tmem_wait_ld();
+    tmem_wait_regs(x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float2 e = __half22float2(*reinterpret_cast<const __half2*>(&x[k]));
+      e.x = fmaxf(e.x, least) * static_cast<float>(1 << kPromptVShift);
+      e.y = fmaxf(e.y, least) * static_cast<float>(1 << kPromptVShift);
+      x[k] = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);    // towards 0
+      const float r0 = e.x - bf16_lo(x[k]), r1 = e.y - bf16_hi(x[k]);
+      rest[k] = pack_bf16x2_rn(r0 == 0.f ? e.x * none : r0, r1 == 0.f ? e.y * none : r1);
+    }
+    tc::tmem_st8(taddr + pg * 8, x);
+    tc::tmem_st8(taddr + kPromptTile / 2 + pg * 8, rest);
+  }
+  tc::tmem_wait_st();
+}
 
 // A V element for the rows that see it, from the pool.
 template <int D, bool KV8>
@@ -1382,9 +1381,15 @@ __global__ void __launch_bounds__(PromptGeo<D, KV8>::kThreads, 1)
           split = uniform(split);
         }
         v_at = v_at + 1 == 2 * Gm::kVStages ? 0 : v_at + 1;
-        sc.finish(ts, &ms.p_half[s], lane, split);
+        sc.finish(ts, &ms.p_half[s], lane == 0 && split == 0u);
         sum += sc.total();
         tc::tmem_wait_st();
+        if (!KV8 && __builtin_expect(split != 0u, 0)) {
+          split_weights(ts, split);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.p_half[s]);
+        }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full[s]);
