@@ -56,19 +56,20 @@
 // at least.  The warps that bring V issue 45 instructions for 512 bytes of it from the same four
 // schedulers: about 3150 in all (3500 for FP8 pages, whose K and V take two thirds of that to
 // widen).  A unit's start and end are 10000 more: outputs written, 3500, and the first maximum,
-// while no product runs.  32 query heads over 8 of 128 dims: 16384 tokens 1730 us (1.27 PFLOP/s; a
-// library matrix product in a loop 1.69), 24 prompts of 128 to 2048 tokens 374 us (0.80), 12 of 512
-// to 4096 over FP8 pages 572 us (1.13), 33 tokens behind 65519 71 us (3.8 TB/s).
+// while no product runs.  32 query heads over 8 of 128 dims: 16384 tokens 1680 to 1740 us (1.31 to
+// 1.26 PFLOP/s; a library matrix product in a loop 1.69), 24 prompts of 128 to 2048 tokens 367 us
+// (0.81), 12 of 512 to 4096 over FP8 pages 572 us (1.13), 33 tokens behind 65519 70 us (3.8 TB/s).
 //
-// By values, 24 prompts: normal ones, or with half of the dims zero, 369 us; times 0.02 377, times
-// 1e-3 (a third of the tiles have a page with an element below 2^-25) 544; all pages split 657.
+// By values, 24 prompts: normal ones, or with half of the dims zero, 360 us; times 0.02 379, times
+// 1e-3 (a third of the tiles have a page with an element below 2^-25) 520; all pages split 670.
 //
 // Measured on the way, 16384 tokens or as said.  The weights of bf16 pages in 8 bits, V as it is:
 // 1470 us (24 prompts 305), the precision above.  In two bf16 parts for all pages: 2118 (448).  V
 // made f16 where asynchronous copies left it: 1820 to 2010 (354 to 420), since shared memory is
 // read and written once more.  Through registers that spill: 2180 (515).  Bits moved instead of a
 // conversion, in a path for pages without zeros: 1700 (361), but 605 for 24 prompts with half of
-// the dims zero.  Without the prefetch to L2 33 tokens behind 65519 76 us against 71.  A sum of 64
+// the dims zero.  Weights split where they are packed, ten times the code: all pages split 771.
+// Without the prefetch to L2 33 tokens behind 65519 76 us against 71.  A sum of 64
 // weights as their limit, where sums of eight are now: four windows of 1000 446 us against 419.
 // V by TMA boxes like K, 2300 cycles of the TMA unit for a K/V tile by themselves (a box of 16 keys
 // is about 70 whatever its bytes); three K and two V stages 1460 against 1417 us; two threads per
@@ -131,8 +132,8 @@ struct PromptGeo {
 // of them by sums of eight); a reference is one of rounded products up to 2^26.
 constexpr float kPromptLimit = 65504.f, kPromptExact = 67108864.f;
 
-// What a sum of weights is multiplied by at least when a far larger one joins it: with 0 an infinity
-// in it would become NaN.
+// What a sum of weights is multiplied by at least when a far larger one joins it: with 0 an
+// infinity in it would become NaN.
 constexpr float kPromptFaint = 0x1p-149f;
 
 // A wait's limit in tries.  One that fails takes 4.0 us on GB300 (measured with 1, 32 and 512
